@@ -443,6 +443,117 @@ int ttm_lmm_layer_fwd(int B, int T, int H, int d, int chunk, int conv_k,
                       void* y, float* W_out, float* S_out,
                       void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Gated linear recurrence: per sequence and channel
+ *     h_t = exp(g_t) h_{t-1} + x_t,   t = 0 .. T-1,  from h_{-1} = h0,
+ * the linear recurrence with a gate that the Titans momentum is ("论文速览 |
+ * Titans" §4.5), as an operator of its own for the layers around the memory.
+ *   x: [N][T][D] in dtype.  h: [N][T][D] in dtype, contiguous, written (the
+ *     state rounded; the recurrence itself runs in fp32).
+ *   g: the logarithm of the retention.  gate TTM_GATE_CHANNEL: [N][T][D] in
+ *     dtype; TTM_GATE_TOKEN: [N][T] fp32, one value for all channels.  0 keeps
+ *     the state, -infinity forgets it (a document boundary); values above 0
+ *     grow it and are taken as given.
+ *   h0: [N][D] fp32 or NULL (zero).  h_last: [N][D] fp32, written.
+ *   x_seq, x_tok (g_seq, g_tok): elements between sequences and between tokens,
+ *     at least D (1 for a token gate) where there is more than one, so that x
+ *     and g may be columns of wider rows; channels are contiguous.  x and g need
+ *     the alignment of their type only, every other pointer 16 bytes.
+ *   workspace: ttm_glr_workspace_size(..., 0) bytes of device scratch (NULL when
+ *     that is 0); its contents on entry are ignored.
+ * Shapes: N, D >= 1, T >= 0, N D < 2^31 (else TTM_ERR_UNSUPPORTED); T = 0 gives
+ * h_last = h0.  No output may overlap an input, another output or the workspace.
+ * Asynchronous on `stream`; TTM_ERR_INVALID_ARG for malformed arguments,
+ * TTM_ERR_CUDA if a launch fails.
+ */
+typedef enum { TTM_GATE_CHANNEL = 0, TTM_GATE_TOKEN = 1 } ttm_gate;
+size_t ttm_glr_workspace_size(int N, int T, int D, int dtype, int gate, int backward);
+int ttm_glr_fwd(int N, int T, int D, int dtype, int gate,
+                const void* x, long long x_seq, long long x_tok,
+                const void* g, long long g_seq, long long g_tok,
+                const float* h0, void* h, float* h_last,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of ttm_glr_fwd for the adjoints dh of h and dh_last of h_last:
+ *     G_t = dh_t + c_{t+1},  c_t = exp(g_t) G_t,  c_T = dh_last,
+ *     dx_t = G_t,  dg_t = c_t h_{t-1},  dh0 = c_0
+ * (for a token gate dg_t is summed over the channels).
+ *   g, h0: those of the forward call; h: [N][T][D], what it wrote.
+ *   dh: [N][T][D] in dtype with strides as x.  dh_last: [N][D] fp32 or NULL (zero).
+ *   dx: [N][T][D] in dtype; dg: [N][T][D] in dtype, or [N][T] fp32 for a token
+ *     gate; dh0: [N][D] fp32 or NULL; all contiguous, written.
+ *   workspace: ttm_glr_workspace_size(..., 1) bytes.
+ * Sums run in a fixed order (equal inputs give equal bits).  Shapes, alignment,
+ * overlap and errors as ttm_glr_fwd. */
+int ttm_glr_bwd(int N, int T, int D, int dtype, int gate,
+                const void* g, long long g_seq, long long g_tok,
+                const void* h, const float* h0,
+                const void* dh, long long dh_seq, long long dh_tok, const float* dh_last,
+                void* dx, void* dg, float* dh0,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Decode step of the recurrence: continues every sequence by n >= 1 tokens from
+ * `state` ([N][D] fp32, updated in place) and writes h ([N][n][D] in dtype).
+ * Otherwise as ttm_glr_fwd; needs no workspace. */
+int ttm_glr_step(int N, int n, int D, int dtype, int gate,
+                 const void* x, long long x_seq, long long x_tok,
+                 const void* g, long long g_seq, long long g_tok,
+                 float* state, void* h, void* stream);
+
+/*
+ * Layer norm of N rows of D values:
+ *     mean = sum x / D,  rstd = 1 / sqrt(sum (x - mean)^2 / D + eps),
+ *     y = (x - mean) rstd w + b
+ * (the norm in f(x) = x + LN(W x) of "Continual Learning: From Attention to
+ * Neural Memory" §4.7, and of every residual block around the memory).
+ *   x: N rows in dtype, x_row >= D elements apart, aligned to its type.
+ *   w, b: [D] fp32 or NULL (1 and 0).  y: [N][D] in dtype, contiguous.
+ *   mean, rstd: [N] fp32, written for the gradient, or NULL.
+ * Statistics and arithmetic are fp32; the variance is taken about the mean.
+ * Shapes: N >= 0, D >= 1.  Every other pointer is 16-byte aligned; no output may
+ * overlap an input or another output.  Asynchronous on `stream`;
+ * TTM_ERR_INVALID_ARG for malformed arguments, TTM_ERR_CUDA if a launch fails.
+ */
+int ttm_layer_norm_fwd(int N, int D, int dtype, const void* x, long long x_row,
+                       const float* w, const float* b, float eps,
+                       void* y, float* mean, float* rstd, void* stream);
+
+/* Gradient of ttm_layer_norm_fwd for the adjoint dy of y (N rows in dtype, dy_row
+ * elements apart): with n = (x - mean) rstd and u = dy w,
+ *     dx = rstd (u - sum u / D - n sum(u n) / D),  dw = sum dy n,  db = sum dy
+ * (dw and db over the rows).  mean, rstd: what the forward call wrote.
+ *   dx: [N][D] in dtype.  dw, db: [D] fp32 or NULL to skip; zero for N = 0.
+ *   workspace: ttm_layer_norm_bwd_workspace_size(N, D) bytes of device scratch for
+ *     the partial sums (may be NULL when dw and db are).
+ * The row sums run in a fixed order (equal inputs give equal bits). */
+size_t ttm_layer_norm_bwd_workspace_size(int N, int D);
+int ttm_layer_norm_bwd(int N, int D, int dtype, const void* dy, long long dy_row,
+                       const void* x, long long x_row, const float* w,
+                       const float* mean, const float* rstd,
+                       void* dx, float* dw, float* db,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Orthogonalised update of `batch` matrices G [m][n] (an outer-loop gradient or
+ * its momentum): Newton-Schulz steps of odd quintic polynomials in the singular
+ * values,
+ *     X_0 = G / max(|G|_F, eps);  A = X X^T,  X <- a X + (b A + c A^2) X
+ * (X^T X on the right for m > n, the same polynomial on the shorter side).
+ *   G: [batch][m][n] in dtype, contiguous.  out: [batch][m][n] bf16, written.
+ *   coeffs: HOST array of steps x (a, b, c), finite; read during the call.
+ *   workspace: ttm_orthogonalize_workspace_size() bytes of device scratch.
+ * |G|_F is summed in fp32 (it must stay below 1e19).  A zero matrix gives zero.
+ * Shapes: batch, m, n >= 1, 0 <= steps <= 32, eps > 0; batch <= 65535 and
+ * m, n <= TTM_ORTHO_MAX_DIM (else TTM_ERR_UNSUPPORTED).  All device pointers are
+ * 16-byte aligned; no overlap.  Asynchronous on `stream`; TTM_ERR_INVALID_ARG
+ * for malformed arguments, TTM_ERR_CUDA if a launch fails.
+ */
+#define TTM_ORTHO_MAX_DIM 65536
+size_t ttm_orthogonalize_workspace_size(int batch, int m, int n);
+int ttm_orthogonalize(int batch, int m, int n, int dtype, const void* G,
+                      const float* coeffs, int steps, float eps, void* out,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
 /* The activation of the 2-layer memory and its derivative, evaluated on the
  * device exactly as the tensor-core 2-layer kernel evaluates them: for the n
  * values x[i], y[i] = GELU(x) = x Phi(x) and, if dy is not NULL,

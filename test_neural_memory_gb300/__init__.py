@@ -8,6 +8,13 @@ fallback: if the library is missing the calls raise.
     z, W = linear_fwd(q, k, v, theta, W0, chunk)
     z, W, S = titans_fwd(q, k, v, theta, W0, chunk, eta=eta, alpha=alpha)
     z, W1, W2, S1, S2 = mlp_fwd(q, k, v, theta, W1_0, W2_0, chunk, eta=eta, alpha=alpha)
+
+The operators around the scan (gated linear recurrence, layer norm, orthogonalised
+update) are in train.py and re-exported here:
+
+    h, h_last = glr_fwd(x, g, h0=h0)
+    y, mean, rstd = layer_norm_fwd(x, w, b)
+    O = orthogonalize(G)
 """
 from __future__ import annotations
 
@@ -69,6 +76,20 @@ def lib() -> ctypes.CDLL:
                                      [p] * 5 + [p, sz, p])
         L.ttm_linear_bwd.argtypes = [i] * 7 + [p] * 4 + [p, i] + [p] * 7 + [p, sz, p]
         L.ttm_mlp_gelu.restype = i
+        ll, fl = ctypes.c_longlong, ctypes.c_float
+        L.ttm_glr_workspace_size.argtypes = [i] * 6
+        L.ttm_glr_fwd.argtypes = [i] * 5 + [p, ll, ll] * 2 + [p, p, p, p, sz, p]
+        L.ttm_glr_bwd.argtypes = ([i] * 5 + [p, ll, ll] + [p, p] + [p, ll, ll] + [p] * 5 +
+                                  [sz, p])
+        L.ttm_glr_step.argtypes = [i] * 5 + [p, ll, ll] * 2 + [p, p, p]
+        L.ttm_layer_norm_fwd.argtypes = [i] * 3 + [p, ll, p, p, fl] + [p] * 4
+        L.ttm_layer_norm_bwd_workspace_size.argtypes = [i] * 2
+        L.ttm_layer_norm_bwd.argtypes = [i] * 3 + [p, ll] * 2 + [p] * 7 + [sz, p]
+        L.ttm_orthogonalize_workspace_size.argtypes = [i] * 3
+        L.ttm_orthogonalize.argtypes = [i] * 4 + [p, p, i, fl, p, p, sz, p]
+        for f in (L.ttm_glr_workspace_size, L.ttm_layer_norm_bwd_workspace_size,
+                  L.ttm_orthogonalize_workspace_size):
+            f.restype = sz
         for f in (L.ttm_linear_fwd, L.ttm_titans_fwd, L.ttm_mlp_fwd):
             f.restype = i
         L.ttm_status_str.argtypes = [i]
@@ -450,3 +471,7 @@ def mlp_gelu(x, *, want_grad=True, stream=None):
     _check(lib().ttm_mlp_gelu(_ptr(x), _ptr(y), _ptr(dy), x.numel(), _stream(x, stream)),
            "ttm_mlp_gelu")
     return y, dy
+
+
+from .train import (glr_bwd, glr_fwd, glr_step, layer_norm_bwd, layer_norm_fwd,  # noqa: E402,F401
+                    orthogonalize)

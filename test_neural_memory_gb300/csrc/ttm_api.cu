@@ -9,6 +9,7 @@
 
 #include "../../include/ttm.h"
 #include "kernels.h"
+#include "train_ops.h"
 
 namespace {
 
@@ -259,6 +260,15 @@ ttm::LinearArgs lmm_scan_args(const ttm::LmmArgs& a) {
 }
 
 }  // namespace
+
+// What the other API translation unit (train_api.cu) needs of this one's state.
+namespace ttm {
+int* api_status_ptr() { return status_ptr(); }
+long long api_wait_cycles() { return g_wait_cycles.load(); }
+void api_note_launches(int kernels) {
+    __atomic_add_fetch(&g_launches, (unsigned long long)kernels, __ATOMIC_RELAXED);
+}
+}  // namespace ttm
 
 extern "C" {
 

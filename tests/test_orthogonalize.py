@@ -1,0 +1,147 @@
+"""Orthogonalised update against the same steps in float64.
+
+Tolerance.  The products take fp16 operands (11 bits) and add in fp32; X itself is kept to
+fp32's accuracy.  How far that takes the result from float64 depends on the spectrum (the steps
+multiply small singular values by up to 3.4 each), so the test rounds the operands of a float64
+run the same way and allows twice what that moves the result, plus the rounding of the result to
+bf16 (2^-8 of a value at most, under 2^-9 in the norm) and 2e-4 for fp32 sums."""
+import pytest
+import torch
+
+import test_neural_memory_gb300 as ttm
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    ttm.build()
+    yield
+    assert ttm.device_status() == ttm.OK
+
+
+def steps64(G, coeffs, eps=1e-7, rounded=False):
+    half = (lambda t: (t * 1024).half().double() / 1024) if rounded else (lambda t: t)
+    X = G.double()
+    tall = X.shape[-2] > X.shape[-1]
+    X = X.mT if tall else X
+    X = X / X.flatten(1).norm(dim=1)[:, None, None].clamp_min(eps)
+    for a, b, c in coeffs:
+        Y = half(X)
+        A = half(Y @ Y.mT)
+        X = a * X + half(b * A + c * (A @ A)) @ Y
+    return X.mT if tall else X
+
+
+def matrices(batch, m, n, kind, seed=0):
+    r = torch.Generator().manual_seed(seed)
+    G = torch.randn((batch, m, n), generator=r)
+    if kind == "low rank":
+        G = 0.1 * G + torch.randn((batch, m, 2), generator=r) @ torch.randn((batch, 2, n), generator=r)
+    if kind == "one column":
+        G *= 1e-3
+        G[..., 0] += torch.randn((batch, m), generator=r)
+    return G
+
+
+def check(G, coeffs, **kw):
+    O = ttm.orthogonalize(G.cuda(), coeffs=coeffs, **kw)
+    assert O.dtype == torch.bfloat16 and O.shape == G.shape
+    flat = G.reshape(-1, *G.shape[-2:])
+    ref = steps64(flat, coeffs, **kw)
+    moved = (steps64(flat, coeffs, rounded=True, **kw) - ref).flatten(1).norm(dim=1)
+    err = (O.double().cpu().reshape(ref.shape) - ref).flatten(1).norm(dim=1)
+    size = ref.flatten(1).norm(dim=1)
+    assert bool((err <= 2 * moved + (2.0 ** -9 + 2e-4) * size).all()), (err / size, moved / size)
+
+
+@pytest.mark.parametrize("batch,m,n", [(1, 1, 1), (2, 1, 9), (2, 9, 1), (3, 8, 8), (2, 33, 65),
+                                       (5, 64, 64), (4, 64, 40), (3, 128, 128), (2, 127, 128),
+                                       (2, 128, 100), (300, 16, 24), (1, 129, 129), (2, 200, 131),
+                                       (1, 96, 700), (1, 700, 96), (2, 256, 256), (1, 257, 1031),
+                                       (1, 768, 777), (3, 640, 300)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["normal", "low rank"])
+def test_against_float64(batch, m, n, dtype, kind):
+    check(matrices(batch, m, n, kind, seed=m + n).to(DT[dtype]), ttm.train.NS_COEFFS)
+
+
+@pytest.mark.parametrize("m,n", [(64, 64), (100, 300), (300, 200)])
+@pytest.mark.parametrize("steps", [0, 1, 2, 3, 9])
+def test_step_counts_and_other_coefficients(m, n, steps):
+    """The cubically convergent quintic (15/8, -10/8, 3/8), another triple in every step."""
+    coeffs = [(1.875 - 0.01 * i, -1.25 + 0.01 * i, 0.375) for i in range(steps)]
+    check(matrices(2, m, n, "normal"), coeffs)
+
+
+@pytest.mark.parametrize("m,n", [(128, 128), (200, 400)])
+def test_one_strong_column_and_scale(m, n):
+    """Entries over a range of 1e4, and the same matrix scaled by powers of two: equal bits."""
+    G = matrices(2, m, n, "one column")
+    check(G, ttm.train.NS_COEFFS)
+    a = ttm.orthogonalize(G.cuda())
+    for s in (2.0 ** -20, 2.0 ** 30):
+        assert torch.equal(a, ttm.orthogonalize((G * s).cuda(), eps=1e-12))
+
+
+@pytest.mark.parametrize("m,n", [(64, 128), (300, 500)])
+def test_zero_and_tiny(m, n):
+    G = torch.zeros(3, m, n)
+    G[1] = matrices(1, m, n, "normal")[0]
+    G[2] = 1e-12 * G[1]
+    check(G, ttm.train.NS_COEFFS)                  # below eps the norm is not divided out
+    assert not ttm.orthogonalize(G.cuda())[0].any()
+
+
+@pytest.mark.parametrize("m,n", [(64, 64), (300, 200)])
+def test_nan_stays_in_its_matrix(m, n):
+    G = matrices(3, m, n, "normal")
+    clean = ttm.orthogonalize(G.cuda())
+    G[1, 3, 4] = float("nan")
+    O = ttm.orthogonalize(G.cuda())
+    assert bool(torch.isnan(O[1].float()).all())
+    assert torch.equal(O[0], clean[0]) and torch.equal(O[2], clean[2])
+
+
+def test_singular_values_come_near_one():
+    G = matrices(2, 128, 384, "normal")
+    s = torch.linalg.svdvals(ttm.orthogonalize(G.cuda()).float())
+    assert float(s.min()) > 0.6 and float(s.max()) < 1.25
+    # the convergent quintic reaches an orthogonal matrix to the accuracy of its operands
+    O = ttm.orthogonalize(G.cuda(), coeffs=[(1.875, -1.25, 0.375)] * 16).double()
+    eye = O @ O.mT - torch.eye(128, device="cuda", dtype=torch.float64)
+    assert float(eye.abs().max()) < 1e-2
+
+
+def test_stream_workspace_and_repeat():
+    G = matrices(2, 300, 200, "normal").cuda()
+    want = ttm.orthogonalize(G)
+    n = ttm.lib().ttm_orthogonalize_workspace_size(2, 300, 200)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.empty_like(want)
+    got = ttm.orthogonalize(G, out=out, workspace=ws, stream=s)
+    s.synchronize()
+    assert got is out and torch.equal(out, want)
+
+
+def test_refusals():
+    G = torch.randn(2, 20, 30, device="cuda")
+    bad = [lambda: ttm.orthogonalize(G[0, 0]), lambda: ttm.orthogonalize(G[:, :, :8]),
+           lambda: ttm.orthogonalize(G, out=torch.empty_like(G)), lambda: ttm.orthogonalize(G, eps=0.0),
+           lambda: ttm.orthogonalize(G, coeffs=[(1.0, 2.0)]), lambda: ttm.orthogonalize(G.cpu()),
+           lambda: ttm.orthogonalize(G, coeffs=[(1.0, 2.0, float("inf"))]),
+           lambda: ttm.orthogonalize(G, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))]
+    for f in bad:
+        with pytest.raises(ttm.TTMError) as e:
+            f()
+        assert e.value.code == ttm.ERR_INVALID_ARG
+    with pytest.raises(ttm.TTMError) as e:
+        ttm.orthogonalize(G, coeffs=[(1.0, 0.0, 0.0)] * 33)
+    assert e.value.code == ttm.ERR_UNSUPPORTED
+    with pytest.raises(TypeError):
+        ttm.orthogonalize(G.half())
