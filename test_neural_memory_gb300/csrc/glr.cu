@@ -15,24 +15,31 @@
 // memory, takes its map (A, H) in a first pass over it, learns the state before the
 // tile from the blocks of the tiles before, and writes the outputs in a second pass.
 //
-// Tile: 256 threads, each 16 bytes of channels (8 bf16 or 4 fp32 values) times R
-// consecutive tokens, CW threads side by side over the channels and 256 / CW over
-// the tokens.  CW is the smallest power of two that covers D, at most 16: rows of
-// 256 bytes keep DRAM pages busy, and a narrower strip gives more, longer tiles
-// to a row.  The map of a tile is joined by shuffles inside a warp and through
-// shared memory between the eight warps.
+// Tile: 256 threads, each 4 channels times R consecutive tokens, CW threads side by
+// side over the channels and 256 / CW over the tokens.  CW is the smallest power of
+// two that covers D, at most 32 (128 channels).  Then a warp holds one run of tokens
+// and only the eight warps' maps are joined, through shared memory; narrower strips
+// join by shuffles inside a warp first.
 //
-// Between tiles (look-back): a block publishes its tile's map as soon as it has it,
-// then its last warp reads the maps of the tiles before it, 32 flags at a time, back
-// to the nearest one whose end state is known, and publishes its own end state.
+// Between tiles (look-back), a lane per channel: a warp publishes its channels' map of
+// the tile as soon as it has it, finds the nearest tile before whose end state is known,
+// takes that state through the maps in between (read 8 at a time) and publishes its own
+// end state.  Every end state is thus the tile's map applied to the one before, however
+// far back a warp had to start: the result does not depend on timing.  A map is one
+// 64-bit word and an end state one 32-bit word per channel, each its own flag (a bit
+// pattern that the values never take marks an empty word), so neither side needs a
+// fence: with flags of their own and release / acquire the two publications took 6600
+// of a tile's 23700 cycles, and the look-back two round trips instead of one.
 // Tiles are handed out in order by a counter, so a block only ever waits for blocks
 // that are already running.  The waits are bounded: one that runs out sets the
 // device status word and the call's outputs are invalid.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <cstdint>
 
 #include "../../include/ttm.h"
+#include "tc_ptx.cuh"
 #include "train_ops.h"
 
 namespace ttm {
@@ -40,45 +47,38 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRun = 8;                       // tokens of one thread in a tile
-constexpr int kTileBytes = kThreads * kRun * 16;
-constexpr unsigned kMapReady = 1, kEndReady = 2;
+constexpr int V = 4;                          // channels of a thread
+constexpr int kMaxLog = 5;                    // at most 32 threads over the channels
+constexpr int kChans = V << kMaxLog;          // channels of a full strip
+constexpr int kBatch = 8;                     // tiles a look-back reads at a time
 constexpr long long kWaitCycles = 4000000000LL;   // default limit, ~2 s at 2 GHz
 
-template <typename E> struct Vec;
-template <> struct Vec<float> { static constexpr int n = 4; };
-template <> struct Vec<__nv_bfloat16> { static constexpr int n = 8; };
+// R, the tokens of one thread in a tile.
+template <typename E> constexpr int kRun = sizeof(E) == 2 ? 16 : 8;
+template <typename E> constexpr int kTileBytes = kThreads * kRun<E> * V * (int)sizeof(E);
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void put(float& o, float v) { o = v; }
 __device__ __forceinline__ void put(__nv_bfloat16& o, float v) { o = __float2bfloat16(v); }
 
-// 16 bytes of channels as fp32 values and back.
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[4], float) {
-    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+// Four channels as fp32 values and back.
+__device__ __forceinline__ void get4(const float* p, float (&f)[V]) {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
 }
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8], __nv_bfloat16) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+__device__ __forceinline__ void get4(const __nv_bfloat16* p, float (&f)[V]) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xffff0000u);
+    f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xffff0000u);
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[4], float) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                      __float_as_uint(f[3]));
+__device__ __forceinline__ void put4(float* p, const float (&f)[V]) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
 }
-__device__ __forceinline__ uint4 pack(const float (&f)[8], __nv_bfloat16) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ void put4(__nv_bfloat16* p, const float (&f)[V]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                              *reinterpret_cast<const uint32_t*>(&b));
 }
 
 // exp through the base-2 unit (2 units in the last place); -infinity gives 0.
@@ -100,7 +100,7 @@ __device__ __forceinline__ float apply(float A, float H, float c) {
 inline int access_width(const void* p, long long seq, long long tok, int es) {
     const unsigned long long m =
         reinterpret_cast<uintptr_t>(p) | (unsigned long long)seq * es | (unsigned long long)tok * es;
-    return m % 16 == 0 ? 16 : (m % 4 == 0 ? 4 : es);
+    return m % 16 == 0 ? 16 : (m % 8 == 0 ? 8 : (m % 4 == 0 ? 4 : es));
 }
 
 // Copies rows [0, rows) of `bytes` bytes at `pitch` bytes from global memory into
@@ -110,7 +110,7 @@ inline int access_width(const void* p, long long seq, long long tok, int es) {
 __device__ __forceinline__ void load_rows(unsigned char* dst, int rows, int srow, const char* src,
                                           long long pitch, int lo, int hi, int bytes, int width,
                                           const void* any) {
-    const int shift = width == 16 ? 4 : (width == 4 ? 2 : 1);
+    const int shift = 31 - __clz(width);
     const int per = srow >> shift;                    // accesses per row, a power of two
     const int log_per = 31 - __clz(per);
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
@@ -120,6 +120,9 @@ __device__ __forceinline__ void load_rows(unsigned char* dst, int rows, int srow
         const char* p = n ? src + r * pitch + o : static_cast<const char*>(any);
         if (width == 16)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + r * srow + o),
+                         "l"(p), "r"(n) : "memory");
+        else if (width == 8)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(base + r * srow + o),
                          "l"(p), "r"(n) : "memory");
         else if (width == 4)
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(base + r * srow + o),
@@ -134,8 +137,8 @@ __device__ __forceinline__ void load_wait() {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Shared rows back to global memory where a row does not start on 16 bytes:
-// neighbouring threads write neighbouring values.
+// Shared rows back to global memory where a row does not start on four values'
+// bytes: neighbouring threads write neighbouring values.
 __device__ __forceinline__ void store_rows(char* dst, long long pitch, const unsigned char* src,
                                            int rows, int srow, int bytes, int width) {
     const int shift = width == 4 ? 2 : 1;
@@ -159,109 +162,149 @@ struct TilePlan {
     int tokens;            // of a tile
     int ntiles, ncols;     // tiles of a sequence, strips of channels
     unsigned* counter;     // hands out tiles in order; NULL when ntiles == 1
-    unsigned* flags;       // [strip][tile] in processing order
-    float* maps;           // [strip][tile][A | H | end][channels of a strip]
-    int width_x, width_g, width_o;   // access widths of x / dh, g, and the contiguous tensors
+    unsigned long long* maps;   // [strip][tile][channel] in processing order: A low, H high word
+    unsigned* ends;        // [strip][tile][channel]: state after the tile
+    size_t words_bytes;    // of the counter, maps and ends, all set to kEmpty before
+    int tma;               // inputs by tensor copies
+    int width_x, width_g, width_o;   // else: access widths of x / dh, g; the contiguous tensors
     float* dg_part;        // token gate over several strips: [ncols][N T] partial sums
 };
 
-__device__ __forceinline__ unsigned load_flag(const unsigned* p) {
+constexpr unsigned kEmpty = 0xffffffffu;   // as a float a NaN that full() never lets through
+
+__device__ __forceinline__ unsigned full(float v) {
+    const unsigned u = __float_as_uint(v);
+    return u == kEmpty ? 0x7fffffffu : u;
+}
+__device__ __forceinline__ unsigned load_word(const unsigned* p) {
     unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void store_flag(unsigned* p, unsigned v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ unsigned long long load_word(const unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
 }
-
-// One warp: the state before processing tile j of a strip.  Lane l holds channels
-// 4l .. 4l+3 (chans <= 128).  `first` is the state before tile 0.
-__device__ __forceinline__ float4 look_back(const unsigned* flags, const float* maps, int chans,
-                                            int j, float4 first, int* status, long long limit) {
-    const int lane = threadIdx.x & 31;
-    const bool mine = 4 * lane < chans;
-    float4 A = make_float4(1.f, 1.f, 1.f, 1.f), H = make_float4(0.f, 0.f, 0.f, 0.f);
-    const long long t0 = clock64();
-    int next = j - 1;                       // nearest tile not joined yet
-    while (true) {
-        // flags of tiles next, next - 1, ..: wait until those down to an end state are set
-        const int at = next - lane;
-        unsigned have, ends;
-        while (true) {
-            const unsigned f = at >= 0 ? load_flag(flags + at) : kMapReady;
-            have = __ballot_sync(0xffffffffu, f != 0);
-            ends = __ballot_sync(0xffffffffu, at >= 0 && f == kEndReady);
-            const unsigned upto = ends ? (ends & (0u - ends)) : 0u;    // lowest end state
-            const unsigned need = ends ? (upto | (upto - 1u)) : 0xffffffffu;
-            if ((have & need) == need) break;
-            if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
-                if (lane == 0) atomicExch(status, TTM_ERR_TIMEOUT);
-                return first;
-            }
-        }
-        __syncwarp();       // the flags' lanes have acquired; now all lanes may read
-        const int stop = ends ? __ffs(ends) - 1 : 32;     // maps of tiles next .. next - stop + 1
-        const int n = min(stop, next + 1);
-        const float* m = maps + (size_t)next * 3 * chans + 4 * lane;
-        for (int i = 0; i < n; i += 4) {
-            float4 a[4], h[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (mine && i + u < n) {
-                    const float* p = m - (size_t)(i + u) * 3 * chans;
-                    a[u] = __ldcg(reinterpret_cast<const float4*>(p));
-                    h[u] = __ldcg(reinterpret_cast<const float4*>(p + chans));
-                } else {
-                    a[u] = make_float4(1.f, 1.f, 1.f, 1.f);
-                    h[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                H.x = apply(A.x, H.x, h[u].x); H.y = apply(A.y, H.y, h[u].y);
-                H.z = apply(A.z, H.z, h[u].z); H.w = apply(A.w, H.w, h[u].w);
-                A.x *= a[u].x; A.y *= a[u].y; A.z *= a[u].z; A.w *= a[u].w;
-            }
-        }
-        if (ends) {
-            if (mine)
-                first = __ldcg(reinterpret_cast<const float4*>(m - (size_t)stop * 3 * chans +
-                                                               2 * chans));
-            break;
-        }
-        next -= n;
-        if (next < 0) break;
-    }
-    return make_float4(apply(A.x, H.x, first.x), apply(A.y, H.y, first.y),
-                       apply(A.z, H.z, first.z), apply(A.w, H.w, first.w));
+__device__ __forceinline__ void publish_end(unsigned* p, float v) {
+    asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(full(v)) : "memory");
+}
+__device__ __forceinline__ void publish_map(unsigned long long* p, float A, float H) {
+    const unsigned long long w =
+        (unsigned long long)full(H) << 32 | (unsigned long long)__float_as_uint(A);
+    asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(w) : "memory");
+}
+__device__ __forceinline__ bool has_map(unsigned long long w) { return (unsigned)(w >> 32) != kEmpty; }
+__device__ __forceinline__ float apply_map(unsigned long long w, float s) {
+    return apply(__uint_as_float((unsigned)w), __uint_as_float((unsigned)(w >> 32)), s);
 }
 
 // Shared memory behind the input tiles.
 struct Joints {
-    float a[kWarps][128], h[kWarps][128];   // map of each warp's tokens, by channel of the strip
-    float carry[128];                       // state before the tile
+    float a[kWarps][kChans], h[kWarps][kChans];   // map of each warp's tokens, by channel
+    float carry[kChans];                          // state before the tile
     unsigned ticket;
+    unsigned long long arrived;                   // mbarrier of the tensor copies
 };
+
+// One warp, a lane per channel (mine: the lane has one): the state before tile j > 0.
+// maps and ends point to this lane's channel of tile j; tiles are `chans` words apart.
+__device__ __forceinline__ float look_back(const unsigned long long* maps, const unsigned* ends,
+                                           int chans, int j, bool mine, int* status,
+                                           long long limit) {
+    const long long t0 = clock64();
+    while (true) {
+        // the nearest kBatch tiles: end states and maps in one round trip
+        unsigned long long m[kBatch];
+        unsigned e[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const bool in = mine && u < j;
+            m[u] = in ? load_word(maps - (long long)(u + 1) * chans) : 0ull;
+            e[u] = in ? load_word(ends - (long long)(u + 1) * chans) : (u < j ? 0u : kEmpty);
+        }
+        int back = 0;                 // nearest end state, if every map nearer is there
+        bool open = true;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (open && !back && __all_sync(0xffffffffu, e[u] != kEmpty)) back = u + 1;
+            open = open && __all_sync(0xffffffffu, has_map(m[u]));
+        }
+        float s = 0.f;
+        if (!back && open && j > kBatch) {
+            // farther: the nearest end state, then forward again through the maps
+            int far = 0;
+            for (int d = kBatch; d < j && !far; d += kBatch) {
+                unsigned f[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    f[u] = mine && d + u < j ? load_word(ends - (long long)(d + u + 1) * chans)
+                                             : (d + u < j ? 0u : kEmpty);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    if (!far && __all_sync(0xffffffffu, f[u] != kEmpty)) {
+                        far = d + u + 1;
+                        s = __uint_as_float(f[u]);
+                    }
+            }
+            bool there = far != 0;
+            for (int d = far - 1; there && d > kBatch; d -= kBatch) {
+                unsigned long long f[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    f[u] = mine && d - u > kBatch ? load_word(maps - (long long)(d - u) * chans) : 0ull;
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    there = there && __all_sync(0xffffffffu, has_map(f[u]));
+                    if (d - u > kBatch) s = apply_map(f[u], s);
+                }
+            }
+            if (there) back = kBatch + 1;
+        } else if (back) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (u + 1 == back) s = __uint_as_float(e[u]);
+        }
+        if (back) {
+#pragma unroll
+            for (int u = kBatch; u-- > 0;)
+                if (u + 1 < back) s = apply_map(m[u], s);
+            return s;
+        }
+        if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
+            if ((threadIdx.x & 31) == 0) atomicExch(status, TTM_ERR_TIMEOUT);
+            return 0.f;
+        }
+    }
+}
 
 // ------------------------------------------------------------------ tile kernel
 
 template <typename E, bool kToken, bool kBack>
-__global__ void __launch_bounds__(kThreads) glr_tile_kernel(GlrArgs a, TilePlan p) {
-    constexpr int V = Vec<E>::n;
-    extern __shared__ __align__(16) unsigned char smem[];
+__global__ void __launch_bounds__(kThreads, 3)
+    glr_tile_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
+                    const __grid_constant__ CUtensorMap mh, GlrArgs a, TilePlan p) {
+    constexpr int R = kRun<E>;
+    extern __shared__ __align__(128) unsigned char smem[];
     constexpr int kTiles = 1 + (kToken ? 0 : 1) + (kBack ? 1 : 0);
-    unsigned char* sx = smem;                                   // x or dh
-    unsigned char* sg = smem + (kToken ? 0 : kTileBytes);       // g (gate per channel)
-    unsigned char* sh = smem + (kTiles - 1) * kTileBytes;       // gradient: h one token earlier
-    Joints& J = *reinterpret_cast<Joints*>(smem + kTiles * kTileBytes);
+    unsigned char* sx = smem;                                        // x or dh
+    unsigned char* sg = smem + (kToken ? 0 : kTileBytes<E>);         // g (gate per channel)
+    unsigned char* sh = smem + (kTiles - 1) * kTileBytes<E>;         // gradient: h one token earlier
+    Joints& J = *reinterpret_cast<Joints*>(smem + kTiles * kTileBytes<E>);
 
     const int tid = threadIdx.x, warp = tid >> 5;
-    // Which tile: in order of the counter, all strips of tile 0 first
+    uint64_t* arrived = reinterpret_cast<uint64_t*>(&J.arrived);
+    // Which tile: in order of the counter (it starts at kEmpty = -1), all strips of tile 0 first
     unsigned ticket = blockIdx.x;
-    if (p.counter) {
-        if (tid == 0) J.ticket = atomicAdd(p.counter, 1u);
-        __syncthreads();
-        ticket = J.ticket;
+    if (tid == 0) {
+        if (p.tma) {
+            tc::mbar_init(arrived, 1);
+            tc::fence_mbar_init();
+        }
+        if (p.counter) J.ticket = atomicAdd(p.counter, 1u) + 1u;
     }
+    __syncthreads();
+    if (p.counter) ticket = J.ticket;
     const unsigned strips = (unsigned)a.N * p.ncols;
     const int j = ticket / strips;                    // place in processing order
     const unsigned strip = ticket % strips;
@@ -270,54 +313,71 @@ __global__ void __launch_bounds__(kThreads) glr_tile_kernel(GlrArgs a, TilePlan 
     const int tile = kBack ? p.ntiles - 1 - j : j;
     const int t0 = tile * p.tokens;
     const int ntok = min(p.tokens, a.T - t0);
-    const int srow = 16 << p.cw_log;                  // bytes of a shared row
+    const int srow = chans * (int)sizeof(E);          // bytes of a shared row
     const int bytes = min(chans, a.D - c0) * (int)sizeof(E);
 
-    load_rows(sx, p.tokens, srow,
-              reinterpret_cast<const char*>(static_cast<const E*>(a.x) + n * a.x_seq +
-                                            (long long)t0 * a.x_tok + c0),
-              a.x_tok * (long long)sizeof(E), 0, ntok, bytes, p.width_x, a.x);
-    if (!kToken)
-        load_rows(sg, p.tokens, srow,
-                  reinterpret_cast<const char*>(static_cast<const E*>(a.g) + n * a.g_seq +
-                                                (long long)t0 * a.g_tok + c0),
-                  a.g_tok * (long long)sizeof(E), 0, ntok, bytes, p.width_g, a.g);
     const size_t row0 = n * a.T + t0;                 // row of the contiguous tensors
-    if (kBack)   // row r holds h of token t0 + r - 1; token -1 is h0, taken below
-        load_rows(sh, p.tokens, srow,
-                  reinterpret_cast<const char*>(static_cast<const E*>(a.h) + c0) +
-                      ((long long)row0 - 1) * a.D * (long long)sizeof(E),
-                  (long long)a.D * sizeof(E), t0 == 0 ? 1 : 0, ntok, bytes, p.width_o, a.h);
+    if (p.tma) {
+        // gradient: row r of sh holds h of token t0 + r - 1; token -1 is h0, taken below
+        if (tid == 0) {
+            tc::mbar_expect_tx(arrived, kTiles * kTileBytes<E>);
+            const int box = min(p.tokens, 256);
+            for (int r = 0; r < p.tokens; r += box) {
+                tc::tma_load_3d(sx + r * srow, &mx, arrived, c0, t0 + r, (int)n);
+                if (!kToken) tc::tma_load_3d(sg + r * srow, &mg, arrived, c0, t0 + r, (int)n);
+                if (kBack) tc::tma_load_3d(sh + r * srow, &mh, arrived, c0, t0 + r - 1, (int)n);
+            }
+        }
+    } else {
+        load_rows(sx, p.tokens, srow,
+                  reinterpret_cast<const char*>(static_cast<const E*>(a.x) + n * a.x_seq +
+                                                (long long)t0 * a.x_tok + c0),
+                  a.x_tok * (long long)sizeof(E), 0, ntok, bytes, p.width_x, a.x);
+        if (!kToken)
+            load_rows(sg, p.tokens, srow,
+                      reinterpret_cast<const char*>(static_cast<const E*>(a.g) + n * a.g_seq +
+                                                    (long long)t0 * a.g_tok + c0),
+                      a.g_tok * (long long)sizeof(E), 0, ntok, bytes, p.width_g, a.g);
+        if (kBack)
+            load_rows(sh, p.tokens, srow,
+                      reinterpret_cast<const char*>(static_cast<const E*>(a.h) + c0) +
+                          ((long long)row0 - 1) * a.D * (long long)sizeof(E),
+                      (long long)a.D * sizeof(E), t0 == 0 ? 1 : 0, ntok, bytes, p.width_o, a.h);
+    }
 
     // This thread's channels and run of tokens, in processing order
     const int cw = 1 << p.cw_log, ch = (tid & (cw - 1)) * V;
     const int place = tid >> p.cw_log, runs = kThreads >> p.cw_log;
-    const int r0 = (kBack ? runs - 1 - place : place) * kRun;
+    const int r0 = (kBack ? runs - 1 - place : place) * R;
     const bool live = c0 + ch < a.D;
-    float tg[kRun];                                   // retentions of a token gate
-    if (kToken) {
-        const float* g = static_cast<const float*>(a.g) + n * a.g_seq + (long long)t0 * a.g_tok;
-#pragma unroll
-        for (int i = 0; i < kRun; ++i)
-            tg[i] = r0 + i < ntok ? retention(g[(long long)(r0 + i) * a.g_tok]) : 1.f;
+    const float* gt = static_cast<const float*>(a.g) + n * a.g_seq + (long long)t0 * a.g_tok;
+    if (p.tma) {
+        const long long since = clock64();
+        while (!tc::mbar_try_wait(arrived, 0))
+            if (clock64() - since > a.wait_cycles) {
+                atomicExch(a.status, TTM_ERR_TIMEOUT);
+                break;
+            }
+    } else {
+        load_wait();
+        __syncthreads();
     }
-    const float* init = kBack ? a.dh_last : a.h0;
-    load_wait();
-    __syncthreads();
 
-    const int so = r0 * srow + (tid & (cw - 1)) * 16;
+    const int so = r0 * chans + ch;                   // this thread's first value of a tile
+    const E *tx = reinterpret_cast<const E*>(sx) + so, *tg = reinterpret_cast<const E*>(sg) + so;
     float A[V], H[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) { A[v] = 1.f; H[v] = 0.f; }
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-        const int q = kBack ? kRun - 1 - i : i;
+    for (int i = 0; i < R; ++i) {
+        const int q = kBack ? R - 1 - i : i;
         float x[V], g[V];
-        unpack(*reinterpret_cast<const uint4*>(sx + so + q * srow), x, E());
-        if (!kToken) unpack(*reinterpret_cast<const uint4*>(sg + so + q * srow), g, E());
+        get4(tx + q * chans, x);
+        if (!kToken) get4(tg + q * chans, g);
+        const float rt = kToken && r0 + q < ntok ? retention(gt[(long long)(r0 + q) * a.g_tok]) : 1.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float r = kToken ? tg[q] : retention(g[v]);
+            const float r = kToken ? rt : retention(g[v]);
             H[v] = kBack ? r * (H[v] + x[v]) : fmaf(r, H[v], x[v]);
             A[v] *= r;
         }
@@ -336,104 +396,89 @@ __global__ void __launch_bounds__(kThreads) glr_tile_kernel(GlrArgs a, TilePlan 
         }
     }
     if ((tid & 31) >= 32 - cw) {
+        put4(&J.a[warp][ch], A);
+        put4(&J.h[warp][ch], H);
+    }
+    if (cw < 32) {   // exclusive of this thread's own run
 #pragma unroll
-        for (int v = 0; v < V; v += 4) {
-            *reinterpret_cast<float4*>(&J.a[warp][ch + v]) = make_float4(A[v], A[v + 1], A[v + 2], A[v + 3]);
-            *reinterpret_cast<float4*>(&J.h[warp][ch + v]) = make_float4(H[v], H[v + 1], H[v + 2], H[v + 3]);
+        for (int v = 0; v < V; ++v) {
+            A[v] = __shfl_up_sync(0xffffffffu, A[v], cw);
+            H[v] = __shfl_up_sync(0xffffffffu, H[v], cw);
         }
     }
-    // exclusive of this thread's own run
+    if ((tid & 31) < cw) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        A[v] = __shfl_up_sync(0xffffffffu, A[v], cw);
-        H[v] = __shfl_up_sync(0xffffffffu, H[v], cw);
-        if ((tid & 31) < cw) { A[v] = 1.f; H[v] = 0.f; }
+        for (int v = 0; v < V; ++v) { A[v] = 1.f; H[v] = 0.f; }
     }
     __syncthreads();
 
-    // The last warp takes the tile's map and the state before the tile
-    if (warp == kWarps - 1) {
-        const int lane = tid & 31, c = 4 * lane;
-        float4 first = make_float4(0.f, 0.f, 0.f, 0.f), mA = make_float4(1.f, 1.f, 1.f, 1.f),
-               mH = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < chans) {
-            const size_t nd = n * a.D + c0 + c;
-            const int left = a.D - c0 - c;
-            if (j == 0 && init) {
-                if (left > 0) first.x = init[nd];
-                if (left > 1) first.y = init[nd + 1];
-                if (left > 2) first.z = init[nd + 2];
-                if (left > 3) first.w = init[nd + 3];
-            }
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float4 wa = *reinterpret_cast<const float4*>(&J.a[w][c]);
-                const float4 wh = *reinterpret_cast<const float4*>(&J.h[w][c]);
-                mH.x = apply(wa.x, wh.x, mH.x); mH.y = apply(wa.y, wh.y, mH.y);
-                mH.z = apply(wa.z, wh.z, mH.z); mH.w = apply(wa.w, wh.w, mH.w);
-                mA.x *= wa.x; mA.y *= wa.y; mA.z *= wa.z; mA.w *= wa.w;
-            }
+    // A lane per channel: publish the tile's map, look back, publish the state after it.
+    // Every state after a tile is that tile's map applied to the state before, wherever
+    // the look-back started, so equal inputs give equal bits.
+    const int swarps = (chans + 31) / 32;             // warps with a lane per channel
+    if (warp < swarps) {
+        const bool mine = tid < chans;
+        float before = 0.f;
+        if (j == 0) {
+            const float* init = kBack ? a.dh_last : a.h0;
+            if (init && mine && c0 + tid < a.D) before = init[n * a.D + c0 + tid];
         }
-        float4 before = first;
         if (p.counter) {
-            unsigned* flags = p.flags + (size_t)strip * p.ntiles;
-            float* maps = p.maps + (size_t)strip * p.ntiles * 3 * chans;
-            float* own = maps + (size_t)j * 3 * chans + c;
-            if (j > 0) {
-                if (c < chans) {
-                    __stcg(reinterpret_cast<float4*>(own), mA);
-                    __stcg(reinterpret_cast<float4*>(own + chans), mH);
+            const size_t own = ((size_t)strip * p.ntiles + j) * chans + tid;
+            float mA = 1.f, mH = 0.f;
+            if (mine) {
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    mH = apply(J.a[w][tid], J.h[w][tid], mH);
+                    mA *= J.a[w][tid];
                 }
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) store_flag(flags + j, kMapReady);
-                before = look_back(flags, maps, chans, j, first, a.status, a.wait_cycles);
             }
-            if (j + 1 < p.ntiles) {
-                if (c < chans)
-                    __stcg(reinterpret_cast<float4*>(own + 2 * chans),
-                           make_float4(apply(mA.x, mH.x, before.x), apply(mA.y, mH.y, before.y),
-                                       apply(mA.z, mH.z, before.z), apply(mA.w, mH.w, before.w)));
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) store_flag(flags + j, kEndReady);
-            }
+            if (mine && j > 0 && j + 1 < p.ntiles) publish_map(p.maps + own, mA, mH);
+            if (j > 0) before = look_back(p.maps + own, p.ends + own, chans, j, mine, a.status, a.wait_cycles);
+            if (mine && j + 1 < p.ntiles) publish_end(p.ends + own, apply(mA, mH, before));
         }
-        if (c < chans) *reinterpret_cast<float4*>(&J.carry[c]) = before;
+        if (mine) J.carry[tid] = before;
     }
     __syncthreads();
 
     // State before this thread's run: the tile's, through the warps before, then the
     // runs before in this warp
     float s[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = J.carry[ch + v];
+    get4(&J.carry[ch], s);
     for (int w = 0; w < warp; ++w) {
+        float wa[V], wh[V];
+        get4(&J.a[w][ch], wa);
+        get4(&J.h[w][ch], wh);
 #pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = apply(J.a[w][ch + v], J.h[w][ch + v], s[v]);
+        for (int v = 0; v < V; ++v) s[v] = apply(wa[v], wh[v], s[v]);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] = apply(A[v], H[v], s[v]);
 
-    const bool direct = p.width_o == 16;
+    const bool direct = p.width_o == 4 * sizeof(E);   // rows start on a thread's four values
     E* out = static_cast<E*>(kBack ? a.dx : a.h) + row0 * a.D + c0 + ch;
     E* outg = kBack && !kToken ? static_cast<E*>(a.dg) + row0 * a.D + c0 + ch : nullptr;
-    float sum[kRun];                                  // token gate: this thread's share of dg
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-        const int q = kBack ? kRun - 1 - i : i, r = r0 + q;
+    E *wx = reinterpret_cast<E*>(sx) + so, *wh = reinterpret_cast<E*>(sh) + so;
+    float* dg = nullptr;                              // token gate: its gradient, or a strip's share
+    if (kBack && kToken)
+        dg = (p.ncols > 1 ? p.dg_part + (size_t)(strip % p.ncols) * a.N * a.T
+                          : static_cast<float*>(a.dg)) + row0;
+#pragma unroll 4
+    for (int i = 0; i < R; ++i) {
+        const int q = kBack ? R - 1 - i : i, r = r0 + q;
         float x[V], g[V], o[V];
-        unpack(*reinterpret_cast<const uint4*>(sx + so + q * srow), x, E());
-        if (!kToken) unpack(*reinterpret_cast<const uint4*>(sg + so + q * srow), g, E());
+        get4(tx + q * chans, x);
+        if (!kToken) get4(tg + q * chans, g);
+        const float rt = kToken && r < ntok ? retention(gt[(long long)r * a.g_tok]) : 1.f;
         if (!kBack) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                s[v] = fmaf(kToken ? tg[q] : retention(g[v]), s[v], x[v]);
+                s[v] = fmaf(kToken ? rt : retention(g[v]), s[v], x[v]);
                 o[v] = s[v];
             }
         } else {
             float b[V];
-            unpack(*reinterpret_cast<const uint4*>(sh + so + q * srow), b, E());
+            get4(wh + q * chans, b);
             if (t0 + r == 0 && a.h0 && live) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
@@ -443,21 +488,21 @@ __global__ void __launch_bounds__(kThreads) glr_tile_kernel(GlrArgs a, TilePlan 
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 o[v] = x[v] + s[v];
-                s[v] = (kToken ? tg[q] : retention(g[v])) * o[v];
+                s[v] = (kToken ? rt : retention(g[v])) * o[v];
                 b[v] *= s[v];
                 if (kToken) acc += b[v];
             }
-            if (kToken) {
-                sum[q] = acc;
-            } else {
-                const uint4 u = pack(b, E());
-                if (!direct) *reinterpret_cast<uint4*>(sh + so + q * srow) = u;
-                else if (live && r < ntok) *reinterpret_cast<uint4*>(outg + (size_t)r * a.D) = u;
+            if (kToken) {   // over the cw threads of the strip's channels, lanes of one warp
+                for (int d = cw >> 1; d; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
+                if (ch == 0 && r < ntok) dg[r] = acc;
+            } else if (!direct) {
+                put4(wh + q * chans, b);
+            } else if (live && r < ntok) {
+                put4(outg + (size_t)r * a.D, b);
             }
         }
-        const uint4 u = pack(o, E());
-        if (!direct) *reinterpret_cast<uint4*>(sx + so + q * srow) = u;
-        else if (live && r < ntok) *reinterpret_cast<uint4*>(out + (size_t)r * a.D) = u;
+        if (!direct) put4(wx + q * chans, o);
+        else if (live && r < ntok) put4(out + (size_t)r * a.D, o);
     }
 
     // End of the strip: the tokens past T leave the state as it is
@@ -466,17 +511,6 @@ __global__ void __launch_bounds__(kThreads) glr_tile_kernel(GlrArgs a, TilePlan 
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (c0 + ch + v < a.D) end[n * a.D + c0 + ch + v] = s[v];
-    }
-    if (kBack && kToken) {
-        // over the cw threads of the strip's channels; they are lanes of one warp
-#pragma unroll
-        for (int q = 0; q < kRun; ++q)
-            for (int d = cw >> 1; d; d >>= 1) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], d);
-        float* dg = p.ncols > 1 ? p.dg_part + (size_t)(strip % p.ncols) * a.N * a.T
-                                : static_cast<float*>(a.dg);
-#pragma unroll
-        for (int q = 0; q < kRun; ++q)
-            if ((tid & (cw - 1)) == (q & (cw - 1)) && r0 + q < ntok) dg[row0 + r0 + q] = sum[q];
     }
     if (!direct) {
         __syncthreads();
@@ -498,8 +532,8 @@ __global__ void glr_gate_sum_kernel(const float* part, int ncols, size_t n, floa
     dg[i] = s;
 }
 
-// Token by token for calls of few tokens: one thread per 16 bytes of channels (W = 1:
-// per channel, where rows do not start on 16 bytes).  The state stays in registers.
+// Token by token for calls of few tokens: one thread per four channels (W = 1: per
+// channel, where rows do not start on four values' bytes), the state in registers.
 template <typename E, bool kToken, int W>
 __global__ void glr_serial_kernel(GlrArgs a, const float* start) {
     const int per = (a.D + W - 1) / W;
@@ -515,24 +549,24 @@ __global__ void glr_serial_kernel(GlrArgs a, const float* start) {
     const E* gc = static_cast<const E*>(a.g) + n * a.g_seq + d;
     const float* gt = static_cast<const float*>(a.g) + n * a.g_seq;
     E* h = static_cast<E*>(a.h) + n * a.T * a.D + d;
-#pragma unroll 2
+#pragma unroll 4
     for (int t = 0; t < a.T; ++t) {
         float xv[W], gv[W];
         if constexpr (W == 1) {
             xv[0] = to_f(x[(long long)t * a.x_tok]);
             if (!kToken) gv[0] = to_f(gc[(long long)t * a.g_tok]);
         } else {
-            unpack(*reinterpret_cast<const uint4*>(x + (long long)t * a.x_tok), xv, E());
-            if (!kToken) unpack(*reinterpret_cast<const uint4*>(gc + (long long)t * a.g_tok), gv, E());
+            get4(x + (long long)t * a.x_tok, xv);
+            if (!kToken) get4(gc + (long long)t * a.g_tok, gv);
         }
         const float rt = kToken ? retention(gt[(long long)t * a.g_tok]) : 0.f;
 #pragma unroll
         for (int v = 0; v < W; ++v) s[v] = fmaf(kToken ? rt : retention(gv[v]), s[v], xv[v]);
         if constexpr (W == 1) put(h[(size_t)t * a.D], s[0]);
-        else *reinterpret_cast<uint4*>(h + (size_t)t * a.D) = pack(s, E());
+        else put4(h + (size_t)t * a.D, s);
     }
-#pragma unroll
-    for (int v = 0; v < W; ++v) a.h_last[nd + v] = s[v];
+    if constexpr (W == 1) a.h_last[nd] = s[0];
+    else put4(a.h_last + nd, s);
 }
 
 // ------------------------------------------------------------------------- host
@@ -542,10 +576,9 @@ constexpr int kSerialTokens = 8;
 
 TilePlan make_plan(const GlrArgs& a, int backward, size_t* bytes) {
     TilePlan p{};
-    const int es = a.bf16 ? 2 : 4, V = 16 / es;
-    while (p.cw_log < 4 && (V << p.cw_log) < a.D) ++p.cw_log;
+    while (p.cw_log < kMaxLog && (V << p.cw_log) < a.D) ++p.cw_log;
     const int chans = V << p.cw_log;
-    p.tokens = (kThreads >> p.cw_log) * kRun;
+    p.tokens = (kThreads >> p.cw_log) * (a.bf16 ? kRun<__nv_bfloat16> : kRun<float>);
     p.ntiles = (a.T + p.tokens - 1) / p.tokens;
     if (p.ntiles < 1) p.ntiles = 1;
     p.ncols = (a.D + chans - 1) / chans;
@@ -553,11 +586,12 @@ TilePlan make_plan(const GlrArgs& a, int backward, size_t* bytes) {
     size_t off = 0;
     char* w = static_cast<char*>(a.workspace);
     if (p.ntiles > 1) {
+        const size_t words = strips * p.ntiles * chans;
         p.counter = reinterpret_cast<unsigned*>(w);
-        p.flags = reinterpret_cast<unsigned*>(w + 256);
-        off = 256 + (strips * p.ntiles * 4 + 255) / 256 * 256;
-        p.maps = reinterpret_cast<float*>(w + off);
-        off += strips * p.ntiles * 3 * chans * sizeof(float);
+        p.maps = reinterpret_cast<unsigned long long*>(w + 256);
+        p.ends = reinterpret_cast<unsigned*>(w + 256 + words * 8);
+        p.words_bytes = 256 + words * 12;
+        off = (p.words_bytes + 255) / 256 * 256;
     }
     if (backward && a.gate_token && p.ncols > 1) {
         p.dg_part = reinterpret_cast<float*>(w + off);
@@ -567,18 +601,36 @@ TilePlan make_plan(const GlrArgs& a, int backward, size_t* bytes) {
     return p;
 }
 
+// Tensor maps of the inputs where they allow it: 16-byte rows and strides below 2^40.
+template <typename E>
+bool tile_map(CUtensorMap* m, const TilePlan& p, const GlrArgs& a, const void* ptr, long long seq,
+              long long tok) {
+    const unsigned long long es = sizeof(E), D = a.D;
+    unsigned long long ts = a.T > 1 ? tok * es : (D * es + 15) / 16 * 16;
+    unsigned long long ss = a.N > 1 ? seq * es : ts * a.T;
+    if (reinterpret_cast<uintptr_t>(ptr) % 16 || ts % 16 || ss % 16 || ss >= 1ull << 40) return false;
+    return make_tma_map(m, sizeof(E) == 2 ? TmaType::bf16 : TmaType::f32, ptr,
+                        {D, (unsigned long long)a.T, (unsigned long long)a.N}, {ts, ss},
+                        {(unsigned)V << p.cw_log, (unsigned)min(p.tokens, 256), 1u}, false);
+}
+
 template <typename E, bool kToken, bool kBack>
-cudaError_t tile_launch(const GlrArgs& a, const TilePlan& p, cudaStream_t s) {
+cudaError_t tile_launch(const GlrArgs& a, TilePlan p, cudaStream_t s) {
     constexpr int tiles = 1 + (kToken ? 0 : 1) + (kBack ? 1 : 0);
-    constexpr int smem = tiles * kTileBytes + (int)sizeof(Joints);
+    constexpr int smem = tiles * kTileBytes<E> + (int)sizeof(Joints);
     auto kernel = glr_tile_kernel<E, kToken, kBack>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (p.ntiles > 1) {
-        e = cudaMemsetAsync(a.workspace, 0, 256 + (size_t)a.N * p.ncols * p.ntiles * 4, s);
+        e = cudaMemsetAsync(a.workspace, kEmpty & 0xff, p.words_bytes, s);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<(unsigned)((size_t)a.N * p.ncols * p.ntiles), kThreads, smem, s>>>(a, p);
+    CUtensorMap mx{}, mg{}, mh{};
+    p.tma = ((size_t)V << p.cw_log) * sizeof(E) >= 16 &&
+            tile_map<E>(&mx, p, a, a.x, a.x_seq, a.x_tok) &&
+            (kToken || tile_map<E>(&mg, p, a, a.g, a.g_seq, a.g_tok)) &&
+            (!kBack || tile_map<E>(&mh, p, a, a.h, (long long)a.T * a.D, a.D));
+    kernel<<<(unsigned)((size_t)a.N * p.ncols * p.ntiles), kThreads, smem, s>>>(mx, mg, mh, a, p);
     return cudaGetLastError();
 }
 
@@ -589,7 +641,10 @@ cudaError_t tiles(GlrArgs a, bool back, cudaStream_t s, int* launches) {
     const int es = sizeof(E);
     p.width_x = access_width(a.x, a.N > 1 ? a.x_seq : 0, a.T > 1 ? a.x_tok : 0, es);
     p.width_g = a.gate_token ? 4 : access_width(a.g, a.N > 1 ? a.g_seq : 0, a.T > 1 ? a.g_tok : 0, es);
-    p.width_o = access_width(nullptr, 0, a.D, es);
+    p.width_o = min(access_width(nullptr, 0, a.D, es), V * es);
+    const int srow = (V << p.cw_log) * es;
+    p.width_x = min(p.width_x, srow);
+    p.width_g = min(p.width_g, srow);
     if (a.wait_cycles <= 0) a.wait_cycles = kWaitCycles;
     *launches = 1;
     cudaError_t e;
@@ -605,12 +660,11 @@ cudaError_t tiles(GlrArgs a, bool back, cudaStream_t s, int* launches) {
 
 template <typename E>
 cudaError_t serial(const GlrArgs& a, const float* start, cudaStream_t s) {
-    constexpr int V = Vec<E>::n;
     const int es = sizeof(E);
-    bool wide = access_width(a.x, a.N > 1 ? a.x_seq : 0, a.T > 1 ? a.x_tok : 0, es) == 16 &&
-                access_width(nullptr, 0, a.D, es) == 16;
+    bool wide = a.D % V == 0 &&
+                access_width(a.x, a.N > 1 ? a.x_seq : 0, a.T > 1 ? a.x_tok : 0, es) >= V * es;
     if (!a.gate_token)
-        wide = wide && access_width(a.g, a.N > 1 ? a.g_seq : 0, a.T > 1 ? a.g_tok : 0, es) == 16;
+        wide = wide && access_width(a.g, a.N > 1 ? a.g_seq : 0, a.T > 1 ? a.g_tok : 0, es) >= V * es;
     const size_t threads = (size_t)a.N * (wide ? a.D / V : a.D);
     const unsigned blocks = (unsigned)((threads + 127) / 128);
     if (wide && a.gate_token) glr_serial_kernel<E, true, V><<<blocks, 128, 0, s>>>(a, start);

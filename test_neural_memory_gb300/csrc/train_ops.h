@@ -73,6 +73,14 @@ struct OrthoArgs {
 size_t ortho_workspace_bytes(int batch, int m, int n);
 cudaError_t ortho_launch(const OrthoArgs& a, cudaStream_t s, int* launches);
 
+// Tensor map (a CUtensorMap) of a 3-D view: dims from the innermost on, byte strides of
+// the outer two (multiples of 16, below 2^40), a box of at most 256 values a side whose
+// inner extent is a multiple of 16 bytes.  Values outside the view load as zero.
+// tma_map.cu; false when the driver refuses it.
+enum class TmaType { f32, bf16, f16 };
+bool make_tma_map(void* map, TmaType type, const void* ptr, const unsigned long long (&dims)[3],
+                  const unsigned long long (&strides)[2], const unsigned (&box)[3], bool swizzle128);
+
 // Process-wide state of the API layer (ttm_api.cu).
 int* api_status_ptr();              // device status word of the current device; NULL on failure
 long long api_wait_cycles();        // bounded-wait limit in SM cycles (0: default)

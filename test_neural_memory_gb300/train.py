@@ -44,13 +44,20 @@ def _done(code, what):
         raise TTMError(code, what)
 
 
+def _raw(t, stream):
+    """The call's stream as CUDA sees it: `stream`, or the current one of t's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream.cuda_stream
+
+
 def _on(stream):
     """Allocations inside belong to the stream the call runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
-def _raw(t, stream):
-    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+_HERE = contextlib.nullcontext()
+_F32, _BF16 = torch.float32, torch.bfloat16
 
 
 def _p(t):
@@ -59,18 +66,24 @@ def _p(t):
 
 def _f32(t, shape, device, what):
     """Checks a contiguous fp32 tensor (or None) of the given shape on the call's device."""
-    if t is not None and (t.dtype is not torch.float32 or tuple(t.shape) != tuple(shape) or
-                          not t.is_contiguous() or t.device != device):
+    if t is not None and (t.dtype is not _F32 or t.shape != shape or not t.is_contiguous() or
+                          t.device != device):
         _bad(f"{what} must be a contiguous float32 tensor of shape {tuple(shape)}")
 
 
 def _out(t, shape, dtype, device, what):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or \
-            t.device != device:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         _bad(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     return t
+
+
+def _out_like(t, x, what):
+    """An output of the shape and dtype of x, contiguous."""
+    if t is None and x.is_contiguous():
+        return torch.empty_like(x)
+    return _out(t, x.shape, x.dtype, x.device, what)
 
 
 def _scratch(workspace, need, device):
@@ -100,15 +113,12 @@ def _one_stride(shape, st, lead, what):
     return step
 
 
-def _strides(t, lead, what):
+def _strides(t, lead, inner, what):
     """(sequence stride, token stride) in elements of a view whose first `lead` dimensions
-    number the sequences and whose next one the tokens."""
+    number the sequences and whose next one the tokens of `inner` values."""
     shape, st = t.shape, t.stride()
     if lead == 1 and shape[0] > 1 and shape[1] > 1:
         return st[0], st[1]
-    inner = 1
-    for s in shape[lead + 1:]:
-        inner *= s
     tok = st[lead] if shape[lead] > 1 else inner
     seq = _one_stride(shape, st, lead, what)
     return shape[lead] * tok if seq is None else seq, tok
@@ -116,23 +126,33 @@ def _strides(t, lead, what):
 
 def _glr_shapes(x, g, what):
     """Common checks: x [..., T, D], g of the same shape (a gate per channel, x's dtype) or
-    [..., T] (a gate per token, fp32).  Returns (lead, N, T, D, gate code)."""
-    lead = x.dim() - 2
+    [..., T] (a gate per token, fp32).  Returns (shape of the state, N, T, D, dtype code, gate
+    code, x's sequence and token stride, g's sequence and token stride)."""
+    shape = x.shape
+    lead = len(shape) - 2
     if lead < 0:
         _bad(f"{what}: expected [..., T, D]")
-    T, D = x.shape[-2:]
-    if (D > 1 and x.stride(-1) != 1) or x.device != g.device or not x.is_cuda:
+    if lead == 1:
+        N, T, D = shape
+        state = (N, D)
+    else:
+        T, D = shape[-2:]
+        state, N = (*shape[:-2], D), 1
+        for s in shape[:-2]:
+            N *= s
+    dt = _code(x, what)
+    if (D > 1 and x.stride(-1) != 1) or not x.is_cuda or x.device != g.device:
         _bad(f"{what}: channels must be contiguous, all tensors on one CUDA device")
-    N = 1
-    for s in x.shape[:-2]:
-        N *= s
-    if g.dim() == lead + 2:
-        if g.shape != x.shape or g.dtype is not x.dtype or (D > 1 and g.stride(-1) != 1):
+    gshape = g.shape
+    if len(gshape) == lead + 2:
+        if gshape != shape or g.dtype is not x.dtype or (D > 1 and g.stride(-1) != 1):
             _bad(f"{what}: a gate per channel has the shape, dtype and channel order of x")
-        return lead, N, T, D, GATE_CHANNEL
-    if g.shape != x.shape[:-1] or g.dtype is not torch.float32:
-        _bad(f"{what}: a gate per token is float32 of shape {tuple(x.shape[:-1])}")
-    return lead, N, T, D, GATE_TOKEN
+        gate, inner = GATE_CHANNEL, D
+    else:
+        if gshape != shape[:-1] or g.dtype is not _F32:
+            _bad(f"{what}: a gate per token is float32 of shape {tuple(shape[:-1])}")
+        gate, inner = GATE_TOKEN, 1
+    return (state, N, T, D, dt, gate, *_strides(x, lead, D, what), *_strides(g, lead, inner, what))
 
 
 def glr_fwd(x, g, *, h0=None, h=None, h_last=None, workspace=None, stream=None):
@@ -140,17 +160,16 @@ def glr_fwd(x, g, *, h0=None, h=None, h_last=None, workspace=None, stream=None):
     ([..., T, D], fp32 or bf16; may be a column slice).  g: the log of the retention, one
     value per channel (shape and dtype of x) or per token ([..., T] fp32).  h0: [..., D]
     fp32 or None.  Returns (h like x, h_last [..., D] fp32)."""
-    lead, N, T, D, gate = _glr_shapes(x, g, "glr_fwd")
-    dt, dev, L = _code(x, "x"), x.device, lib()
-    state = (*x.shape[:-2], D)
+    state, N, T, D, dt, gate, xs, xt, gs, gt = _glr_shapes(x, g, "glr_fwd")
+    dev, L = x.device, lib()
     _f32(h0, state, dev, "h0")
     with _on(stream):
-        h = _out(h, x.shape, x.dtype, dev, "h")
-        h_last = _out(h_last, state, torch.float32, dev, "h_last")
+        h = _out_like(h, x, "h")
+        h_last = _out(h_last, state, _F32, dev, "h_last")
         workspace = _scratch(workspace, L.ttm_glr_workspace_size(N, T, D, dt, gate, 0), dev)
-    _done(L.ttm_glr_fwd(N, T, D, dt, gate, x.data_ptr(), *_strides(x, lead, "x"), g.data_ptr(),
-                        *_strides(g, lead, "g"), _p(h0), h.data_ptr(), h_last.data_ptr(),
-                        _p(workspace), _nbytes(workspace), _raw(x, stream)), "ttm_glr_fwd")
+    _done(L.ttm_glr_fwd(N, T, D, dt, gate, x.data_ptr(), xs, xt, g.data_ptr(), gs, gt, _p(h0),
+                        h.data_ptr(), h_last.data_ptr(), _p(workspace), _nbytes(workspace),
+                        _raw(x, stream)), "ttm_glr_fwd")
     return h, h_last
 
 
@@ -160,23 +179,22 @@ def glr_bwd(g, h, dh, *, h0=None, dh_last=None, want_dh0=True, workspace=None, o
     ([..., D] fp32 or None) the adjoints of its outputs.  Returns a dict with dx, dg (shaped
     as x and g) and dh0 ([..., D] fp32, None when want_dh0 is False).  `out` may hold
     preallocated tensors for these keys."""
-    lead, N, T, D, gate = _glr_shapes(dh, g, "glr_bwd")
-    dt, dev, L = _code(dh, "dh"), dh.device, lib()
-    state = (*dh.shape[:-2], D)
+    state, N, T, D, dt, gate, ds, dtok, gs, gt = _glr_shapes(dh, g, "glr_bwd")
+    dev, L = dh.device, lib()
     if h.shape != dh.shape or h.dtype is not dh.dtype or not h.is_contiguous() or h.device != dev:
         _bad("glr_bwd: h must be contiguous, of the shape and dtype of dh")
     _f32(h0, state, dev, "h0")
     _f32(dh_last, state, dev, "dh_last")
     out = out or {}
     with _on(stream):
-        dx = _out(out.get("dx"), dh.shape, dh.dtype, dev, "dx")
-        dg = _out(out.get("dg"), g.shape, g.dtype, dev, "dg")
-        dh0 = _out(out.get("dh0"), state, torch.float32, dev, "dh0") if want_dh0 else None
+        dx = _out_like(out.get("dx"), dh, "dx")
+        dg = _out_like(out.get("dg"), g, "dg")
+        dh0 = _out(out.get("dh0"), state, _F32, dev, "dh0") if want_dh0 else None
         workspace = _scratch(workspace, L.ttm_glr_workspace_size(N, T, D, dt, gate, 1), dev)
-    _done(L.ttm_glr_bwd(N, T, D, dt, gate, g.data_ptr(), *_strides(g, lead, "g"), h.data_ptr(),
-                        _p(h0), dh.data_ptr(), *_strides(dh, lead, "dh"), _p(dh_last),
-                        dx.data_ptr(), dg.data_ptr(), _p(dh0), _p(workspace), _nbytes(workspace),
-                        _raw(dh, stream)), "ttm_glr_bwd")
+    _done(L.ttm_glr_bwd(N, T, D, dt, gate, g.data_ptr(), gs, gt, h.data_ptr(), _p(h0),
+                        dh.data_ptr(), ds, dtok, _p(dh_last), dx.data_ptr(), dg.data_ptr(),
+                        _p(dh0), _p(workspace), _nbytes(workspace), _raw(dh, stream)),
+          "ttm_glr_bwd")
     return dict(dx=dx, dg=dg, dh0=dh0)
 
 
@@ -184,16 +202,14 @@ def glr_step(x, g, state, *, h=None, stream=None):
     """Decode step of the recurrence: continues every sequence by the n tokens of x
     ([..., n, D]) from `state` ([..., D] fp32, updated in place).  g as in glr_fwd.
     Returns h like x."""
-    lead, N, n, D, gate = _glr_shapes(x, g, "glr_step")
-    dt, dev = _code(x, "x"), x.device
+    shape, N, n, D, dt, gate, xs, xt, gs, gt = _glr_shapes(x, g, "glr_step")
     if state is None:
         _bad("glr_step: state is required")
-    _f32(state, (*x.shape[:-2], D), dev, "state")
+    _f32(state, shape, x.device, "state")
     with _on(stream):
-        h = _out(h, x.shape, x.dtype, dev, "h")
-    _done(lib().ttm_glr_step(N, n, D, dt, gate, x.data_ptr(), *_strides(x, lead, "x"),
-                             g.data_ptr(), *_strides(g, lead, "g"), state.data_ptr(),
-                             h.data_ptr(), _raw(x, stream)), "ttm_glr_step")
+        h = _out_like(h, x, "h")
+    _done(lib().ttm_glr_step(N, n, D, dt, gate, x.data_ptr(), xs, xt, g.data_ptr(), gs, gt,
+                             state.data_ptr(), h.data_ptr(), _raw(x, stream)), "ttm_glr_step")
     return h
 
 
@@ -220,10 +236,10 @@ def layer_norm_fwd(x, w=None, b=None, *, eps=1e-5, y=None, mean=None, rstd=None,
     _f32(w, (D,), dev, "w")
     _f32(b, (D,), dev, "b")
     with _on(stream):
-        y = _out(y, x.shape, x.dtype, dev, "y")
+        y = _out_like(y, x, "y")
         if want_stats:
-            mean = _out(mean, x.shape[:-1], torch.float32, dev, "mean")
-            rstd = _out(rstd, x.shape[:-1], torch.float32, dev, "rstd")
+            mean = _out(mean, x.shape[:-1], _F32, dev, "mean")
+            rstd = _out(rstd, x.shape[:-1], _F32, dev, "rstd")
         else:
             mean = rstd = None
     _done(lib().ttm_layer_norm_fwd(N, D, dt, x.data_ptr(), row, _p(w), _p(b), eps, y.data_ptr(),
@@ -248,9 +264,9 @@ def layer_norm_bwd(dy, x, mean, rstd, w=None, *, want_dw=True, want_db=True, wor
     _f32(w, (D,), dev, "w")
     out, L = out or {}, lib()
     with _on(stream):
-        dx = _out(out.get("dx"), x.shape, x.dtype, dev, "dx")
-        dw = _out(out.get("dw"), (D,), torch.float32, dev, "dw") if want_dw else None
-        db = _out(out.get("db"), (D,), torch.float32, dev, "db") if want_db else None
+        dx = _out_like(out.get("dx"), x, "dx")
+        dw = _out(out.get("dw"), (D,), _F32, dev, "dw") if want_dw else None
+        db = _out(out.get("db"), (D,), _F32, dev, "db") if want_db else None
         need = L.ttm_layer_norm_bwd_workspace_size(N, D) if want_dw or want_db else 0
         workspace = _scratch(workspace, need, dev)
     _done(L.ttm_layer_norm_bwd(N, D, dt, dy.data_ptr(), dy_row, x.data_ptr(), row, _p(w),
