@@ -1,105 +1,836 @@
 // Orthogonalised update: X_0 = G / max(|G|_F, eps), then per step
-//   A = X X^T,  X <- a X + (b A + c A^2) X       (on the shorter side of G)
+//   A = X X^T,  X <- a X + (b A + c A^2) X
+// on the shorter side of G (X^T X from the right for a tall G), r the shorter side, l the
+// longer.
+//
+// Numbers.  The products take fp16 operands and add in fp32.  bf16 operands are not
+// enough: the steps multiply small singular values by up to a = 3.4 each, and their
+// rounding with them (1 % off for a normal matrix, 6 % for one of low rank plus noise).  With
+// fp16 operands and X itself kept to fp32's accuracy (in registers, or as the sum of two
+// fp16 values) the result is 1.7e-3 to 2.5e-3 off, of which rounding it to bf16 is 1.7e-3; with
+// X rounded to fp16 every step it would be 8e-3 for the matrix of low rank.  Operands are
+// stored times 2^10, so that entries of 1e-4 stay clear of fp16's subnormal range.
+//
+// Both sides at most 128: one block keeps a matrix on chip through all steps
+// (ns_small_kernel).  Larger: three products a step (ns_gemm_kernel).  A and
+// B = b A + c A^2 are symmetric, so only their tiles on and below the diagonal are
+// computed and each is written twice, once transposed.
+#include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/ttm.h"
+#include "tc_ptx.cuh"
 #include "train_ops.h"
 
 namespace ttm {
 namespace {
 
-// X_0 in fp32, one block per matrix.
-__global__ void ns_start_kernel(OrthoArgs a, float* X) {
-    __shared__ float part[256];
-    const size_t mn = (size_t)a.m * a.n, base = blockIdx.x * mn;
-    auto G = [&](size_t i) {
-        return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.G)[base + i])
-                      : static_cast<const float*>(a.G)[base + i];
-    };
+using namespace tc;
+
+constexpr float kScale = 1024.f, kUnscale = 1.f / 1024.f;
+constexpr long long kWaitCycles = 4000000000LL;   // default limit, ~2 s at 2 GHz
+
+// Instruction descriptor of tcgen05.mma .kind::f16 with fp16 A / B and an fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
+    return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) |
+           (uint32_t(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+__device__ __forceinline__ uint32_t bf162_bits(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 1 / max(norm, eps); NaN stays NaN.
+__device__ __forceinline__ float inverse_norm(float sum_of_squares, float eps) {
+    const float norm = sqrtf(sum_of_squares);
+    return norm <= eps ? 1.f / eps : 1.f / norm;
+}
+
+// Bounded wait.  A wait that runs out sets the block's abort flag (every role then
+// stops) and the device status word.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abort, int* status,
+                                       long long limit) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait_sleep(bar, parity, 20000)) {
+        if (*(volatile int*)abort) return false;
+        if (clock64() - t0 > limit) {
+            *(volatile int*)abort = 1;
+            atomicExch(status, TTM_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, int* abort, int* status,
+                                         long long limit) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, status, limit);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort, int* status,
+                                          long long limit) {
+    return __all_sync(0xffffffffu, wait_one(bar, parity, abort, status, limit));
+}
+// After an abort: give copies and products in flight a last bounded chance to land.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, long long limit) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if (clock64() - t0 > limit) return;
+}
+
+// --------------------------------------------------------------- one block a matrix
+
+// X, 128 x 128 zero-padded, as fp16 operands in two halves of 64 columns (rows of 128 bytes,
+// 128-byte swizzle), its fp32 values in registers: thread (row, half) holds 64 of them.
+// A, then B in its place, likewise.  Per step three products into the same 128 columns of
+// tensor memory, each followed by its epilogue; two blocks share an SM, so that one's
+// products run beside the other's epilogue.
+constexpr int kSide = 128, kSmallThreads = 256;
+constexpr uint32_t kHalfBytes = kSide * 128;            // 64 columns of an operand
+constexpr uint32_t kOperandBytes = 2 * kHalfBytes;
+
+struct SmallShared {
+    uint64_t done;
+    uint32_t tmem;
+    int abort;
+    float part[kSmallThreads / 32];
+};
+
+__device__ __forceinline__ uint4* operand_at(unsigned char* base, int row, int chunk) {
+    return reinterpret_cast<uint4*>(base + (chunk >> 3) * kHalfBytes + row * 128 +
+                                    (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+__global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid_constant__ OrthoArgs a) {
+    extern __shared__ unsigned char raw[];
+    unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    unsigned char *sx = base, *sa = base + kOperandBytes;
+    SmallShared& S = *reinterpret_cast<SmallShared*>(base + 2 * kOperandBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool wide = a.m <= a.n;
+    const int r = wide ? a.m : a.n, l = wide ? a.n : a.m;
+    const int rp = r <= 64 ? 64 : 128, lp = l <= 64 ? 64 : 128;
+    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+    const size_t mat = (size_t)blockIdx.x * a.m * a.n;
+
+    if (warp == 0) tmem_alloc(&S.tmem, 128);
+    if (tid == 0) {
+        mbar_init(&S.done, 1);
+        fence_mbar_init();
+        S.abort = 0;
+    }
+
+    // X_0: row of the short side, columns of the long one
+    float X[64];
     float s = 0.f;
-    for (size_t i = threadIdx.x; i < mn; i += blockDim.x) s += G(i) * G(i);
-    part[threadIdx.x] = s;
+#pragma unroll
+    for (int c = 0; c < 64; ++c) {
+        const int col = half * 64 + c;
+        X[c] = 0.f;
+        if (row < r && col < l) {
+            const size_t i = mat + (wide ? (size_t)row * a.n + col : (size_t)col * a.n + row);
+            X[c] = a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.G)[i])
+                          : static_cast<const float*>(a.G)[i];
+        }
+        s = fmaf(X[c], X[c], s);
+    }
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) S.part[warp] = s;
+    tc_fence_before();
     __syncthreads();
-    for (int w = 128; w > 0; w /= 2) {
-        if (threadIdx.x < w) part[threadIdx.x] += part[threadIdx.x + w];
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    s = 0.f;
+    for (int w = 0; w < kSmallThreads / 32; ++w) s += S.part[w];
+    const float inv = inverse_norm(s, a.eps) * kScale;
+#pragma unroll
+    for (int c = 0; c < 64; ++c) X[c] *= inv;
+
+    const uint32_t xb = smem_u32(sx), ab = smem_u32(sa);
+    const uint32_t acc = tmem_addr(tmem, (warp & 3) * 32, half * 64);
+    uint32_t phase = 0;
+    // Every epilogue ends here: operands written, accumulators read, next product issued.
+    auto ready = [&]() {
+        fence_proxy_async_smem();
+        tc_fence_before();
         __syncthreads();
+        tc_fence_after();
+    };
+    auto wait_product = [&]() {
+        const bool ok = wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles);
+        phase ^= 1;
+        tc_fence_after();
+        return ok;
+    };
+    for (int step = 0; step < a.steps; ++step) {
+        const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            *operand_at(sx, row, half * 8 + q) =
+                make_uint4(half2_bits(X[8 * q], X[8 * q + 1]), half2_bits(X[8 * q + 2], X[8 * q + 3]),
+                           half2_bits(X[8 * q + 4], X[8 * q + 5]), half2_bits(X[8 * q + 6], X[8 * q + 7]));
+        ready();
+        if (warp == 0) {                                // A = X X^T
+            if (elect_one()) {
+                const uint32_t id = idesc_f16(128, rp, 0, 0);
+                for (int k = 0; k < lp / 16; ++k) {
+                    const uint64_t d = sdesc(xb + (k >> 2) * kHalfBytes + (k & 3) * 32, 16, 1024, 2);
+                    mma_bf16(tmem, d, d, id, k > 0);
+                }
+                mma_commit(&S.done);
+            }
+            __syncwarp();
+        }
+        if (!wait_product()) break;
+        const bool mine = half * 64 < rp;               // columns of A and B that exist
+        if (mine) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                tmem_ld16(acc + 16 * q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float* f = v + 8 * h;
+                    *operand_at(sa, row, half * 8 + 2 * q + h) =
+                        make_uint4(half2_bits(f[0] * kUnscale, f[1] * kUnscale),
+                                   half2_bits(f[2] * kUnscale, f[3] * kUnscale),
+                                   half2_bits(f[4] * kUnscale, f[5] * kUnscale),
+                                   half2_bits(f[6] * kUnscale, f[7] * kUnscale));
+                }
+            }
+        }
+        ready();
+        if (warp == 0) {                                // A A (A is symmetric)
+            if (elect_one()) {
+                const uint32_t id = idesc_f16(128, rp, 0, 0);
+                for (int k = 0; k < rp / 16; ++k) {
+                    const uint64_t d = sdesc(ab + (k >> 2) * kHalfBytes + (k & 3) * 32, 16, 1024, 2);
+                    mma_bf16(tmem, d, d, id, k > 0);
+                }
+                mma_commit(&S.done);
+            }
+            __syncwarp();
+        }
+        if (!wait_product()) break;
+        if (mine) {                                     // B = b A + c A A over A
+            const float c2 = cc * kUnscale;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                tmem_ld16(acc + 16 * q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint4* at = operand_at(sa, row, half * 8 + 2 * q + h);
+                    uint32_t w[4] = {at->x, at->y, at->z, at->w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 old = half2_floats(w[i]);
+                        w[i] = half2_bits(fmaf(c2, v[8 * h + 2 * i], cb * old.x),
+                                          fmaf(c2, v[8 * h + 2 * i + 1], cb * old.y));
+                    }
+                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        ready();
+        if (warp == 0) {                                // B X, X as [k][n]
+            if (elect_one()) {
+                const uint32_t id = idesc_f16(128, lp, 0, 1);
+                for (int k = 0; k < rp / 16; ++k)
+                    mma_bf16(tmem, sdesc(ab + (k >> 2) * kHalfBytes + (k & 3) * 32, 16, 1024, 2),
+                             sdesc(xb + k * 2048, kHalfBytes, 1024, 2), id, k > 0);
+                mma_commit(&S.done);
+            }
+            __syncwarp();
+        }
+        if (!wait_product()) break;
+        if (half * 64 < lp) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                tmem_ld16(acc + 16 * q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    X[16 * q + i] = fmaf(ca, X[16 * q + i], v[i] * kUnscale);
+            }
+        }
     }
-    const float r = 1.f / fmaxf(sqrtf(part[0]), a.eps);
-    for (size_t i = threadIdx.x; i < mn; i += blockDim.x) X[base + i] = G(i) * r;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + mat;
+    if (wide && a.n % 8 == 0) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int col = half * 64 + 8 * q;
+            const float* f = X + 8 * q;
+            if (row < r && col < l)
+                *reinterpret_cast<uint4*>(out + (size_t)row * a.n + col) =
+                    make_uint4(bf162_bits(f[0] * kUnscale, f[1] * kUnscale),
+                               bf162_bits(f[2] * kUnscale, f[3] * kUnscale),
+                               bf162_bits(f[4] * kUnscale, f[5] * kUnscale),
+                               bf162_bits(f[6] * kUnscale, f[7] * kUnscale));
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+            const int col = half * 64 + c;
+            if (row < r && col < l)
+                out[wide ? (size_t)row * a.n + col : (size_t)col * a.n + row] =
+                    __float2bfloat16(X[c] * kUnscale);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (S.abort && tid == 0) drain(&S.done, phase, a.wait_cycles);
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 128);
 }
 
-// out = alpha P Q + beta C with P [M][K], Q [K][N] given by strides; C and out [M][N].
-__global__ void ns_product_kernel(int M, int N, int K, float alpha, const float* P, int p0, int p1,
-                                  const float* Q, int q0, int q1, float beta, const float* C,
-                                  float* out, size_t sP, size_t sQ, size_t sC,
-                                  __nv_bfloat16* rounded) {
-    __shared__ float p[16][17], q[16][17];
-    const int r = blockIdx.y * 16 + threadIdx.y, c = blockIdx.x * 16 + threadIdx.x;
-    P += blockIdx.z * sP;
-    Q += blockIdx.z * sQ;
+// ------------------------------------------------------------------ norm and X_0
+
+constexpr int kNormBlocks = 256;       // partial sums of a matrix
+
+__device__ __forceinline__ float block_sum(float s) {
+    __shared__ float buf[8];
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0.f;
+    for (int w = 0; w < 8; ++w) s += buf[w];
+    return s;
+}
+
+__device__ __forceinline__ float4 load4(const OrthoArgs& a, size_t i) {
+    if (!a.bf16) return *reinterpret_cast<const float4*>(static_cast<const float*>(a.G) + i);
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.G) + i);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ float load1(const OrthoArgs& a, size_t i) {
+    return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.G)[i])
+                  : static_cast<const float*>(a.G)[i];
+}
+
+__global__ void __launch_bounds__(256) ns_norm_kernel(const __grid_constant__ OrthoArgs a, float* part) {
+    const size_t mn = (size_t)a.m * a.n, base = blockIdx.y * mn;
     float s = 0.f;
-    for (int k = 0; k < K; k += 16) {
-        p[threadIdx.y][threadIdx.x] =
-            r < M && k + threadIdx.x < K ? P[(size_t)r * p0 + (size_t)(k + threadIdx.x) * p1] : 0.f;
-        q[threadIdx.y][threadIdx.x] =
-            c < N && k + threadIdx.y < K ? Q[(size_t)(k + threadIdx.y) * q0 + (size_t)c * q1] : 0.f;
-        __syncthreads();
-        for (int i = 0; i < 16; ++i) s += p[threadIdx.y][i] * q[i][threadIdx.x];
-        __syncthreads();
+    if (mn % 4 == 0) {
+        for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < mn; i += (size_t)gridDim.x * 1024) {
+            const float4 g = load4(a, base + i);
+            s += g.x * g.x + g.y * g.y + (g.z * g.z + g.w * g.w);
+        }
+    } else {
+        for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < mn; i += (size_t)gridDim.x * 256)
+            s = fmaf(load1(a, base + i), load1(a, base + i), s);
     }
-    if (r >= M || c >= N) return;
-    const size_t o = blockIdx.z * sC + (size_t)r * N + c;
-    const float v = alpha * s + (beta != 0.f ? beta * C[o] : 0.f);
-    if (rounded) rounded[o] = __float2bfloat16(v);
-    else out[o] = v;
+    s = block_sum(s);
+    if (threadIdx.x == 0) part[blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
-__global__ void ns_round_kernel(size_t n, const float* X, __nv_bfloat16* out) {
-    const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < n) out[i] = __float2bfloat16(X[i]);
+// X_0 as hi + lo, rows `pitch` values apart.
+__global__ void __launch_bounds__(256) ns_start_kernel(const __grid_constant__ OrthoArgs a, const float* part,
+                                                       int parts, int pitch, __half* hi, __half* lo) {
+    const float s = block_sum(threadIdx.x < parts ? part[blockIdx.y * parts + threadIdx.x] : 0.f);
+    const float inv = inverse_norm(s, a.eps) * kScale;
+    const int V = a.n % 4 == 0 ? 4 : 1, per = a.n / V;
+    const size_t total = (size_t)a.m * per, mat = (size_t)blockIdx.y * a.m;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
+        const size_t row = mat + i / per, src = row * a.n + (i % per) * V, dst = row * pitch + (i % per) * V;
+        if (V == 4) {
+            float4 g = load4(a, src);
+            g.x *= inv; g.y *= inv; g.z *= inv; g.w *= inv;
+            const uint2 h = make_uint2(half2_bits(g.x, g.y), half2_bits(g.z, g.w));
+            const float2 h0 = half2_floats(h.x), h1 = half2_floats(h.y);
+            *reinterpret_cast<uint2*>(hi + dst) = h;
+            *reinterpret_cast<uint2*>(lo + dst) =
+                make_uint2(half2_bits(g.x - h0.x, g.y - h0.y), half2_bits(g.z - h1.x, g.w - h1.y));
+        } else {
+            const float g = load1(a, src) * inv;
+            hi[dst] = __float2half_rn(g);
+            lo[dst] = __float2half_rn(g - __half2float(hi[dst]));
+        }
+    }
+}
+
+// No steps asked for: the normalised matrix itself.
+__global__ void __launch_bounds__(256) ns_round_kernel(int m, int n, int pitch, const __half* hi,
+                                                       const __half* lo, __nv_bfloat16* out) {
+    const size_t total = (size_t)m * n, mat = (size_t)blockIdx.y * m;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (size_t)gridDim.x * 256) {
+        const size_t src = (mat + i / n) * pitch + i % n;
+        out[mat * n + i] = __float2bfloat16((__half2float(hi[src]) + __half2float(lo[src])) * kUnscale);
+    }
+}
+
+// ------------------------------------------------------------------------ products
+
+// One of the three products of a step, tiles of 128 x BN, K in blocks of 64.
+//   kGram:   out = alpha acc                (A; on and below the diagonal, mirrored)
+//   kSquare: out = alpha acc + beta in      (B from A A and A; likewise)
+//   kUpdate: X'  = alpha acc + beta X       (X and X' as hi + lo; the last one to bf16)
+// Roles (192 threads, one block an SM): warp 0 copies operand tiles in (kStages deep), warp 1
+// issues the products into one of two accumulators, warps 2-5 take the other through the
+// epilogue, 32 rows each, 64 columns at a time: the values to add come in by tensor copies one
+// chunk ahead, the results replace them in shared memory and leave by tensor copies, so
+// that every access to global memory is a full row of 128 bytes.
+enum { kGram, kSquare, kUpdate };
+constexpr int kBM = 128, kBK = 64, kGemmThreads = 192;
+constexpr uint32_t kChunkBytes = 32 * 128;              // 32 rows of 64 fp16 values
+constexpr uint32_t kEpiBytes = 4 * 2 * 2 * kChunkBytes; // warps x buffers x (hi, lo)
+
+__host__ __device__ constexpr int stages_of(int BN) { return BN == 256 ? 3 : (BN == 128 ? 5 : 6); }
+__host__ __device__ constexpr uint32_t stage_bytes(int BN) { return (kBM + BN) * 128; }
+
+struct GemmParams {
+    int M, N, K, batch;
+    int tiles_m, tiles_n, per_matrix, tiles;
+    float alpha, beta;
+    __nv_bfloat16* last;        // kUpdate, last step: [batch][M][N]
+    int last_by_copy;           // its rows start on 16 bytes
+    int* status;
+    long long limit;
+};
+
+struct GemmShared {
+    uint64_t full[6], empty[6], acc_full[2], acc_empty[2], in[4][2];
+    uint32_t tmem;
+    int abort;
+};
+
+struct TileAt {
+    int row, col, mat;
+};
+
+// Tile t: all tiles (columns outermost, so that tiles at work share columns of X), or for the
+// symmetric results those with an element on or below the diagonal, row by row.
+template <int EPI, int BN>
+__device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
+    TileAt at;
+    at.mat = t / p.per_matrix;
+    t -= at.mat * p.per_matrix;
+    if (EPI == kUpdate) {
+        at.row = t % p.tiles_m * kBM;
+        at.col = t / p.tiles_m * BN;
+        return at;
+    }
+    int i = 0;
+    while (true) {
+        const int n = min(p.tiles_n, (i * kBM + kBM - 1) / BN + 1);
+        if (t < n) break;
+        t -= n;
+        ++i;
+    }
+    at.row = i * kBM;
+    at.col = t * BN;
+    return at;
+}
+
+template <bool AMN, bool BMN, int EPI, int BN>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    ns_gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                   const __grid_constant__ CUtensorMap in0, const __grid_constant__ CUtensorMap in1,
+                   const __grid_constant__ CUtensorMap out0, const __grid_constant__ CUtensorMap out1,
+                   const __grid_constant__ GemmParams p) {
+    constexpr int kStages = stages_of(BN);
+    extern __shared__ unsigned char raw[];
+    unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    unsigned char* epi = base + kStages * stage_bytes(BN);
+    GemmShared& S = *reinterpret_cast<GemmShared*>(epi + kEpiBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kblocks = (p.K + kBK - 1) / kBK;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&S.full[i], 1);
+            mbar_init(&S.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.acc_full[i], 1);
+            mbar_init(&S.acc_empty[i], 4);
+            for (int w = 0; w < 4; ++w) mbar_init(&S.in[w][i], 1);
+        }
+        fence_mbar_init();
+        S.abort = 0;
+    }
+    if (warp == 1) tmem_alloc(&S.tmem, 2 * BN);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+
+    if (warp == 0 && lane == 0) {
+        int it = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+            const TileAt at = tile_at<EPI, BN>(p, t);
+            for (int k = 0; k < kblocks; ++k, ++it) {
+                const int s = it % kStages;
+                ok = wait_one(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort, p.status, p.limit);
+                if (!ok) break;
+                unsigned char *da = base + s * stage_bytes(BN), *db = da + kBM * 128;
+                mbar_expect_tx(&S.full[s], stage_bytes(BN));
+                if (AMN) {
+                    for (int i = 0; i < kBM / 64; ++i)
+                        tma_load_3d(da + i * 8192, &ma, &S.full[s], at.row + 64 * i, k * kBK, at.mat);
+                } else {
+                    tma_load_3d(da, &ma, &S.full[s], k * kBK, at.row, at.mat);
+                }
+                if (BMN) {
+                    for (int i = 0; i < BN / 64; ++i)
+                        tma_load_3d(db + i * 8192, &mb, &S.full[s], at.col + 64 * i, k * kBK, at.mat);
+                } else {
+                    tma_load_3d(db, &mb, &S.full[s], k * kBK, at.col, at.mat);
+                }
+            }
+        }
+        if (*(volatile int*)&S.abort)                   // copies still in flight
+            for (int i = max(0, it - kStages); i < it; ++i)
+                drain(&S.full[i % kStages], (i / kStages) & 1, p.limit);
+    } else if (warp == 1 && lane == 0) {
+        constexpr uint32_t id = idesc_f16(kBM, BN, AMN, BMN);
+        int it = 0, n = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++n) {
+            const int acc = n & 1;
+            ok = wait_one(&S.acc_empty[acc], ((n >> 1) & 1) ^ 1, &S.abort, p.status, p.limit);
+            if (!ok) break;
+            tc_fence_after();
+            for (int k = 0; k < kblocks; ++k, ++it) {
+                const int s = it % kStages;
+                ok = wait_one(&S.full[s], (it / kStages) & 1, &S.abort, p.status, p.limit);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t da = smem_u32(base + s * stage_bytes(BN)), db = da + kBM * 128;
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk)
+                    mma_bf16(tmem + acc * BN,
+                             AMN ? sdesc(da + kk * 2048, 8192, 1024, 2) : sdesc(da + kk * 32, 16, 1024, 2),
+                             BMN ? sdesc(db + kk * 2048, 8192, 1024, 2) : sdesc(db + kk * 32, 16, 1024, 2),
+                             id, k > 0 || kk > 0);
+                mma_commit(&S.empty[s]);
+            }
+            if (ok) mma_commit(&S.acc_full[acc]);
+        }
+        if (*(volatile int*)&S.abort && it > 0)         // products still in flight
+            drain(&S.empty[(it - 1) % kStages], ((it - 1) / kStages) & 1, p.limit);
+    } else if (warp >= 2) {
+        const int part = warp & 3;                      // this warp's lanes of tensor memory
+        unsigned char* buf = epi + (warp - 2) * 4 * kChunkBytes;
+        uint64_t* in = S.in[warp - 2];
+        int n = 0, cnt = 0;
+        for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++n) {
+            const TileAt at = tile_at<EPI, BN>(p, t);
+            const int acc = n & 1, row0 = at.row + part * 32;
+            // chunks of 64 columns that have an element to write: a prefix
+            int chunks = 0;
+            if (row0 < p.M) chunks = min(BN / 64, (p.N - at.col + 63) / 64);
+            if (EPI != kUpdate && chunks > 0) chunks = min(chunks, max(0, (row0 + 31 - at.col) / 64 + (row0 + 31 >= at.col)));
+            auto fetch = [&](int c, int b) {            // lane 0: chunk c into buffer b
+                bulk_wait_read<0>();
+                mbar_expect_tx(&in[b], (EPI == kUpdate ? 2 : 1) * kChunkBytes);
+                tma_load_3d(buf + b * 2 * kChunkBytes, &in0, &in[b], at.col + 64 * c, row0, at.mat);
+                if (EPI == kUpdate)
+                    tma_load_3d(buf + b * 2 * kChunkBytes + kChunkBytes, &in1, &in[b], at.col + 64 * c,
+                                row0, at.mat);
+            };
+            if (EPI != kGram && chunks > 0 && lane == 0) fetch(0, cnt & 1);
+            if (!wait_warp(&S.acc_full[acc], (n >> 1) & 1, &S.abort, p.status, p.limit)) break;
+            tc_fence_after();
+            bool ok = true;
+            for (int c = 0; c < chunks; ++c, ++cnt) {
+                const int b = cnt & 1, col0 = at.col + 64 * c;
+                unsigned char *hi = buf + b * 2 * kChunkBytes, *lo = hi + kChunkBytes;
+                if (lane == 0) {
+                    if (EPI == kGram) bulk_wait_read<1>();
+                    else if (c + 1 < chunks) fetch(c + 1, b ^ 1);
+                }
+                __syncwarp();
+                if (EPI != kGram) {
+                    ok = wait_warp(&in[b], (cnt >> 1) & 1, &S.abort, p.status, p.limit);
+                    if (!ok) break;
+                }
+                const bool mirror = EPI != kUpdate && row0 > col0 + 63;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float v[16];
+                    tmem_ld16(tmem_addr(tmem, part * 32, acc * BN + 64 * c + 16 * q), v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t o = lane * 128 + (((2 * q + h) ^ (lane & 7)) << 4);
+                        uint4* at_hi = reinterpret_cast<uint4*>(hi + o);
+                        uint4* at_lo = reinterpret_cast<uint4*>(lo + o);
+                        float* f = v + 8 * h;
+                        uint32_t w[4], z[4];
+                        if (EPI == kGram) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) f[i] *= p.alpha;
+                        } else {
+                            const uint4 u = *at_hi;
+                            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+                            if (EPI == kUpdate) {
+                                const uint4 y = *at_lo;
+                                z[0] = y.x; z[1] = y.y; z[2] = y.z; z[3] = y.w;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float2 x = half2_floats(w[i]);
+                                if (EPI == kUpdate) {
+                                    const float2 y = half2_floats(z[i]);
+                                    x.x += y.x;
+                                    x.y += y.y;
+                                }
+                                f[2 * i] = fmaf(p.alpha, f[2 * i], p.beta * x.x);
+                                f[2 * i + 1] = fmaf(p.alpha, f[2 * i + 1], p.beta * x.y);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (EPI == kUpdate && p.last) {
+                                w[i] = bf162_bits(f[2 * i] * kUnscale, f[2 * i + 1] * kUnscale);
+                            } else {
+                                w[i] = half2_bits(f[2 * i], f[2 * i + 1]);
+                                if (EPI == kUpdate) {
+                                    const float2 x = half2_floats(w[i]);
+                                    z[i] = half2_bits(f[2 * i] - x.x, f[2 * i + 1] - x.y);
+                                }
+                            }
+                        }
+                        *at_hi = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (EPI == kUpdate) {
+                            if (!p.last) *at_lo = make_uint4(z[0], z[1], z[2], z[3]);
+                        } else if (mirror) {            // [64 columns][32 rows]
+                            __half* m = reinterpret_cast<__half*>(lo) + (16 * q + 8 * h) * 32 + lane;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) m[i * 32] = __float2half_rn(f[i]);
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (EPI == kUpdate && p.last && !p.last_by_copy) {
+                    __nv_bfloat16* o = p.last + ((size_t)at.mat * p.M + row0) * p.N + col0;
+                    for (int r = 0; r < 32 && row0 + r < p.M; ++r)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int e = lane + 32 * i;
+                            if (col0 + e < p.N)
+                                o[(size_t)r * p.N + e] = *reinterpret_cast<__nv_bfloat16*>(
+                                    hi + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2);
+                        }
+                    fence_proxy_async_smem();           // read before the next copy into it
+                    __syncwarp();
+                } else if (lane == 0) {
+                    tma_store_3d(&out0, hi, col0, row0, at.mat);
+                    if (EPI == kUpdate) {
+                        if (!p.last) tma_store_3d(&out1, lo, col0, row0, at.mat);
+                    } else if (mirror) {
+                        tma_store_3d(&out1, lo, row0, col0, at.mat);
+                    }
+                    bulk_commit();
+                }
+            }
+            if (!ok) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.acc_empty[acc]);
+        }
+        if (lane == 0) {
+            bulk_wait<0>();
+            if (*(volatile int*)&S.abort && EPI != kGram)
+                for (int b = 0; b < 2; ++b) drain(&in[b], 0, p.limit >> 3);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 2 * BN);
+}
+
+// ----------------------------------------------------------------------------- host
+
+int pitch_of(int n) { return (n + 7) / 8 * 8; }
+
+struct Workspace {
+    size_t x[2][2], a, b, part, total;      // X (ping, pong) x (hi, lo), A, B, norm sums
+};
+
+Workspace layout(int batch, int m, int n) {
+    Workspace w{};
+    const size_t xs = (size_t)batch * m * pitch_of(n) * 2;
+    const size_t rs = (size_t)(m < n ? m : n), as = (size_t)batch * rs * pitch_of((int)rs) * 2;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    for (auto& pair : w.x)
+        for (size_t& o : pair) o = take(xs);
+    w.a = take(as);
+    w.b = take(as);
+    w.part = take((size_t)batch * kNormBlocks * sizeof(float));
+    w.total = off;
+    return w;
+}
+
+bool small(int m, int n) { return m <= kSide && n <= kSide; }
+
+// A stored fp16 (or bf16) matrix batch: [batch][rows][pitch].
+struct Mat {
+    const void* p;
+    int rows, cols, pitch, batch;
+    TmaType type = TmaType::f16;
+    bool map(CUtensorMap* m, unsigned bx, unsigned by, bool swizzle) const {
+        const unsigned long long row = (unsigned long long)pitch * 2;
+        return make_tma_map(m, type, p, {(unsigned long long)cols, (unsigned long long)rows, (unsigned long long)batch},
+                            {row, row * rows}, {bx, by, 1u}, swizzle);
+    }
+};
+
+template <bool AMN, bool BMN, int EPI, int BN>
+cudaError_t gemm_bn(const Mat& A, const Mat& B, const Mat& I0, const Mat& I1, const Mat& O0, const Mat& O1,
+                    GemmParams p, cudaStream_t s) {
+    p.tiles_m = (p.M + kBM - 1) / kBM;
+    p.tiles_n = (p.N + BN - 1) / BN;
+    p.per_matrix = 0;
+    if (EPI == kUpdate) {
+        p.per_matrix = p.tiles_m * p.tiles_n;
+    } else {
+        for (int i = 0; i < p.tiles_m; ++i) {
+            const int n = (i * kBM + kBM - 1) / BN + 1;
+            p.per_matrix += n < p.tiles_n ? n : p.tiles_n;
+        }
+    }
+    const long long tiles = (long long)p.per_matrix * p.batch;
+    if (tiles > (1LL << 31) - 1) return cudaErrorInvalidValue;
+    p.tiles = (int)tiles;
+    CUtensorMap ma, mb, in0{}, in1{}, out0{}, out1{};
+    bool ok = A.map(&ma, 64, AMN ? 64 : kBM, true) && B.map(&mb, 64, BMN ? 64 : BN, true);
+    if (EPI != kGram) ok = ok && I0.map(&in0, 64, 32, true);
+    if (EPI == kUpdate) ok = ok && I1.map(&in1, 64, 32, true);
+    if (!p.last || p.last_by_copy) ok = ok && O0.map(&out0, 64, 32, true);
+    if (EPI != kUpdate) ok = ok && O0.map(&out1, 32, 64, false);
+    else if (!p.last) ok = ok && O1.map(&out1, 64, 32, true);
+    if (!ok) return cudaErrorInvalidValue;
+    constexpr int smem = 1024 + stages_of(BN) * stage_bytes(BN) + kEpiBytes + sizeof(GemmShared);
+    auto kernel = ns_gemm_kernel<AMN, BMN, EPI, BN>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<p.tiles < 152 ? p.tiles : 152, kGemmThreads, smem, s>>>(ma, mb, in0, in1, out0, out1, p);
+    return cudaGetLastError();
+}
+
+// The widest tile that still gives most SMs one.
+template <bool AMN, bool BMN, int EPI>
+cudaError_t gemm(const Mat& A, const Mat& B, const Mat& I0, const Mat& I1, const Mat& O0, const Mat& O1,
+                 const GemmParams& p, cudaStream_t s) {
+    auto tiles = [&](int BN) {
+        const double all = (double)((p.M + kBM - 1) / kBM) * ((p.N + BN - 1) / BN) * p.batch;
+        return EPI == kUpdate ? all : all * 0.55;
+    };
+    if (tiles(256) >= 128) return gemm_bn<AMN, BMN, EPI, 256>(A, B, I0, I1, O0, O1, p, s);
+    if (tiles(128) >= 100) return gemm_bn<AMN, BMN, EPI, 128>(A, B, I0, I1, O0, O1, p, s);
+    return gemm_bn<AMN, BMN, EPI, 64>(A, B, I0, I1, O0, O1, p, s);
 }
 
 }  // namespace
 
 size_t ortho_workspace_bytes(int batch, int m, int n) {
-    const size_t r = m < n ? m : n;
-    return (size_t)batch * (2 * (size_t)m * n + 2 * r * r) * sizeof(float);
+    return small(m, n) ? 0 : layout(batch, m, n).total;
 }
 
-cudaError_t ortho_launch(const OrthoArgs& a, cudaStream_t s, int* launches) {
-    const size_t mn = (size_t)a.m * a.n;
-    const int r = a.m < a.n ? a.m : a.n, l = a.m < a.n ? a.n : a.m;
+cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
+    OrthoArgs a = in;
+    if (a.wait_cycles <= 0) a.wait_cycles = kWaitCycles;
+    if (small(a.m, a.n)) {
+        constexpr int smem = 1024 + 2 * kOperandBytes + sizeof(SmallShared);
+        const cudaError_t e =
+            cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ns_small_kernel<<<a.batch, kSmallThreads, smem, s>>>(a);
+        *launches = 1;
+        return cudaGetLastError();
+    }
+    const Workspace w = layout(a.batch, a.m, a.n);
+    char* ws = static_cast<char*>(a.workspace);
     const bool wide = a.m <= a.n;
-    const size_t rr = (size_t)r * r;
-    float* X = static_cast<float*>(a.workspace);
-    float *Y = X + a.batch * mn, *A = Y + a.batch * mn, *B = A + a.batch * rr;
-    ns_start_kernel<<<a.batch, 256, 0, s>>>(a, X);
-    *launches = 1;
-    const dim3 t(16, 16);
-    auto grid = [&](int M, int N) { return dim3((N + 15) / 16, (M + 15) / 16, a.batch); };
+    const int r = wide ? a.m : a.n, l = wide ? a.n : a.m;
+    const int xp = pitch_of(a.n), ap = pitch_of(r);
+    Mat X[2][2];
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j) X[i][j] = Mat{ws + w.x[i][j], a.m, a.n, xp, a.batch};
+    const Mat A{ws + w.a, r, r, ap, a.batch}, B{ws + w.b, r, r, ap, a.batch};
+    const Mat out{a.out, a.m, a.n, a.n, a.batch, TmaType::bf16};
+    float* part = reinterpret_cast<float*>(ws + w.part);
+
+    const size_t mn = (size_t)a.m * a.n;
+    size_t blocks = (mn + 4095) / 4096;
+    if (blocks > kNormBlocks) blocks = kNormBlocks;
+    const dim3 grid((unsigned)blocks, a.batch);
+    ns_norm_kernel<<<grid, 256, 0, s>>>(a, part);
+    size_t fill = (mn + 4095) / 4096;
+    if (fill > 2048) fill = 2048;
+    ns_start_kernel<<<dim3((unsigned)fill, a.batch), 256, 0, s>>>(
+        a, part, (int)blocks, xp, (__half*)X[0][0].p, (__half*)X[0][1].p);
+    *launches = 2;
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (a.steps == 0) {
+        ns_round_kernel<<<dim3((unsigned)fill, a.batch), 256, 0, s>>>(
+            a.m, a.n, xp, (const __half*)X[0][0].p, (const __half*)X[0][1].p, (__nv_bfloat16*)a.out);
+        ++*launches;
+        return cudaGetLastError();
+    }
     for (int i = 0; i < a.steps; ++i) {
-        const float* c = a.coeffs + 3 * i;
-        __nv_bfloat16* last = i + 1 == a.steps ? static_cast<__nv_bfloat16*>(a.out) : nullptr;
-        // A = X X^T (X^T X for a tall matrix); B = b A + c A^2; Y = a X + B X (X B)
-        const int k0 = wide ? 1 : a.n, k1 = wide ? a.n : 1;
-        ns_product_kernel<<<grid(r, r), t, 0, s>>>(r, r, l, 1.f, X, k1, k0, X, k0, k1, 0.f, nullptr,
-                                                   A, mn, mn, rr, nullptr);
-        ns_product_kernel<<<grid(r, r), t, 0, s>>>(r, r, r, c[2], A, r, 1, A, r, 1, c[1], A, B, rr,
-                                                   rr, rr, nullptr);
-        if (wide)
-            ns_product_kernel<<<grid(a.m, a.n), t, 0, s>>>(a.m, a.n, r, 1.f, B, r, 1, X, a.n, 1, c[0],
-                                                           X, Y, rr, mn, mn, last);
-        else
-            ns_product_kernel<<<grid(a.m, a.n), t, 0, s>>>(a.m, a.n, r, 1.f, X, a.n, 1, B, r, 1, c[0],
-                                                           X, Y, mn, rr, mn, last);
-        float* z = X; X = Y; Y = z;
+        const float *c = a.coeffs + 3 * i;
+        const Mat *x = X[i & 1], *y = X[(i & 1) ^ 1];
+        // B is stored times 2^10, less where its coefficients are large
+        float sb = kScale;
+        while (sb > 1.f && (std::fabs(c[1]) + std::fabs(c[2])) * sb > 8.f * kScale) sb *= 0.5f;
+        GemmParams p{};
+        p.batch = a.batch;
+        p.status = a.status;
+        p.limit = a.wait_cycles;
+        p.M = p.N = r;
+        p.K = l;
+        p.alpha = kUnscale;                              // (2^10 X)(2^10 X)^T -> 2^10 A
+        e = wide ? gemm<false, false, kGram>(x[0], x[0], A, A, A, A, p, s)
+                 : gemm<true, true, kGram>(x[0], x[0], A, A, A, A, p, s);
+        if (e != cudaSuccess) return e;
+        p.K = r;
+        p.alpha = c[2] * sb * kUnscale * kUnscale;       // -> sb (b A + c A A)
+        p.beta = c[1] * sb * kUnscale;
+        e = gemm<false, false, kSquare>(A, A, A, A, B, B, p, s);
+        if (e != cudaSuccess) return e;
+        p.M = a.m;
+        p.N = a.n;
+        p.alpha = 1.f / sb;                              // -> 2^10 X'
+        p.beta = c[0];
+        if (i + 1 == a.steps) {
+            p.last = static_cast<__nv_bfloat16*>(a.out);
+            p.last_by_copy = a.n % 8 == 0;
+        }
+        const Mat& o = p.last ? out : y[0];
+        e = wide ? gemm<false, true, kUpdate>(B, x[0], x[0], x[1], o, y[1], p, s)
+                 : gemm<false, false, kUpdate>(x[0], B, x[0], x[1], o, y[1], p, s);
+        if (e != cudaSuccess) return e;
         *launches += 3;
     }
-    if (a.steps == 0) {
-        ns_round_kernel<<<(unsigned)((a.batch * mn + 255) / 256), 256, 0, s>>>(
-            a.batch * mn, X, static_cast<__nv_bfloat16*>(a.out));
-        ++*launches;
-    }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace ttm

@@ -135,7 +135,8 @@ def test_refusals():
            lambda: ttm.orthogonalize(G, out=torch.empty_like(G)), lambda: ttm.orthogonalize(G, eps=0.0),
            lambda: ttm.orthogonalize(G, coeffs=[(1.0, 2.0)]), lambda: ttm.orthogonalize(G.cpu()),
            lambda: ttm.orthogonalize(G, coeffs=[(1.0, 2.0, float("inf"))]),
-           lambda: ttm.orthogonalize(G, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))]
+           lambda: ttm.orthogonalize(torch.randn(200, 300, device="cuda"),
+                                     workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))]
     for f in bad:
         with pytest.raises(ttm.TTMError) as e:
             f()
