@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
 
 // ------------------------------------------------------------------ norm and X_0
 
-constexpr int kNormBlocks = 256;       // partial sums of a matrix
+constexpr int kNormBlocks = 1024;      // partial sums of a matrix
 
 __device__ __forceinline__ float block_sum(float s) {
     __shared__ float buf[8];
@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const __grid_constant__ Or
     const size_t mn = (size_t)a.m * a.n, base = blockIdx.y * mn;
     float s = 0.f;
     if (mn % 4 == 0) {
+#pragma unroll 4
         for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < mn; i += (size_t)gridDim.x * 1024) {
             const float4 g = load4(a, base + i);
             s += g.x * g.x + g.y * g.y + (g.z * g.z + g.w * g.w);
@@ -342,7 +343,9 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const __grid_constant__ Or
 // X_0 as hi + lo, rows `pitch` values apart.
 __global__ void __launch_bounds__(256) ns_start_kernel(const __grid_constant__ OrthoArgs a, const float* part,
                                                        int parts, int pitch, __half* hi, __half* lo) {
-    const float s = block_sum(threadIdx.x < parts ? part[blockIdx.y * parts + threadIdx.x] : 0.f);
+    float s = 0.f;
+    for (int i = threadIdx.x; i < parts; i += 256) s += part[blockIdx.y * parts + i];
+    s = block_sum(s);
     const float inv = inverse_norm(s, a.eps) * kScale;
     const int V = a.n % 4 == 0 ? 4 : 1, per = a.n / V;
     const size_t total = (size_t)a.m * per, mat = (size_t)blockIdx.y * a.m;
@@ -374,9 +377,71 @@ __global__ void __launch_bounds__(256) ns_round_kernel(int m, int n, int pitch, 
     }
 }
 
+// ------------------------------------------------------- two blocks on one tile (PTX)
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of the same shared variable in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// Tensor copy into this block's shared memory, counted on a barrier of either block.
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* tmap, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on `bar` in both blocks once the products issued so far are complete.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)), "h"((uint16_t)3)
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void alloc_columns(uint32_t* dst, uint32_t n) {
+    if (CG == 1) {
+        tmem_alloc(dst, n);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(n)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void free_columns(uint32_t t, uint32_t n) {
+    if (CG == 1) tmem_dealloc(t, n);
+    else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(n) : "memory");
+}
+
 // ------------------------------------------------------------------------ products
 
-// One of the three products of a step, tiles of 128 x BN, K in blocks of 64.
+// One of the three products of a step, tiles of 128 CG x BN, K in blocks of 64.  With CG = 2
+// two blocks (a cluster) share a tile: each copies in its 128 rows of A and half of the BN
+// rows of B, one issues products over both (M = 256), each keeps its rows' accumulators.
+// That halves what a block reads of B, which is what bounds a tile: with CG = 1 the copies
+// reach about 50 bytes a cycle and SM, 983 cycles for the 48 KB of a block of K at BN = 256 whose
+// products take 512.
 //   kGram:   out = alpha acc                (A; on and below the diagonal, mirrored)
 //   kSquare: out = alpha acc + beta in      (B from A A and A; likewise)
 //   kUpdate: X'  = alpha acc + beta X       (X and X' as hi + lo; the last one to bf16)
@@ -390,8 +455,12 @@ constexpr int kBM = 128, kBK = 64, kGemmThreads = 192;
 constexpr uint32_t kChunkBytes = 32 * 128;              // 32 rows of 64 fp16 values
 constexpr uint32_t kEpiBytes = 4 * 2 * 2 * kChunkBytes; // warps x buffers x (hi, lo)
 
-__host__ __device__ constexpr int stages_of(int BN) { return BN == 256 ? 3 : (BN == 128 ? 5 : 6); }
-__host__ __device__ constexpr uint32_t stage_bytes(int BN) { return (kBM + BN) * 128; }
+// As many stages as fit beside the epilogue's buffers in 227 KB, at most 6.
+__host__ __device__ constexpr int stages_of(int CG, int BN) {
+    const int n = (int)((232448 - 1024 - 512 - kEpiBytes) / ((kBM + BN / CG) * 128));
+    return n < 6 ? n : 6;
+}
+__host__ __device__ constexpr uint32_t stage_bytes(int CG, int BN) { return (kBM + BN / CG) * 128; }
 
 struct GemmParams {
     int M, N, K, batch;
@@ -415,40 +484,43 @@ struct TileAt {
 
 // Tile t: all tiles (columns outermost, so that tiles at work share columns of X), or for the
 // symmetric results those with an element on or below the diagonal, row by row.
-template <int EPI, int BN>
+template <int EPI, int TM, int BN>
 __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
     TileAt at;
     at.mat = t / p.per_matrix;
     t -= at.mat * p.per_matrix;
     if (EPI == kUpdate) {
-        at.row = t % p.tiles_m * kBM;
+        at.row = t % p.tiles_m * TM;
         at.col = t / p.tiles_m * BN;
         return at;
     }
     int i = 0;
     while (true) {
-        const int n = min(p.tiles_n, (i * kBM + kBM - 1) / BN + 1);
+        const int n = min(p.tiles_n, (i * TM + TM - 1) / BN + 1);
         if (t < n) break;
         t -= n;
         ++i;
     }
-    at.row = i * kBM;
+    at.row = i * TM;
     at.col = t * BN;
     return at;
 }
 
-template <bool AMN, bool BMN, int EPI, int BN>
+template <bool AMN, bool BMN, int EPI, int CG, int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     ns_gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                    const __grid_constant__ CUtensorMap in0, const __grid_constant__ CUtensorMap in1,
                    const __grid_constant__ CUtensorMap out0, const __grid_constant__ CUtensorMap out1,
                    const __grid_constant__ GemmParams p) {
-    constexpr int kStages = stages_of(BN);
+    constexpr int kStages = stages_of(CG, BN), TM = kBM * CG;
+    constexpr uint32_t kStage = stage_bytes(CG, BN);
     extern __shared__ unsigned char raw[];
     unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    unsigned char* epi = base + kStages * stage_bytes(BN);
+    unsigned char* epi = base + kStages * kStage;
     GemmShared& S = *reinterpret_cast<GemmShared*>(epi + kEpiBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CG == 2 ? (int)cluster_rank() : 0;
+    const int first = blockIdx.x / CG, stride = gridDim.x / CG;
     const int kblocks = (p.K + kBK - 1) / kBK;
 
     if (threadIdx.x == 0) {
@@ -458,51 +530,57 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.acc_full[i], 1);
-            mbar_init(&S.acc_empty[i], 4);
+            mbar_init(&S.acc_empty[i], 4 * CG);
             for (int w = 0; w < 4; ++w) mbar_init(&S.in[w][i], 1);
         }
         fence_mbar_init();
         S.abort = 0;
     }
-    if (warp == 1) tmem_alloc(&S.tmem, 2 * BN);
+    if (warp == 1) alloc_columns<CG>(&S.tmem, 2 * BN);
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();                        // both blocks' barriers are set up
     tc_fence_after();
     const uint32_t tmem = S.tmem;
 
     if (warp == 0 && lane == 0) {
         int it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
-            const TileAt at = tile_at<EPI, BN>(p, t);
+        for (int t = first; t < p.tiles && ok; t += stride) {
+            TileAt at = tile_at<EPI, TM, BN>(p, t);
+            at.row += rank * kBM;
+            at.col += rank * (BN / CG);
             for (int k = 0; k < kblocks; ++k, ++it) {
                 const int s = it % kStages;
                 ok = wait_one(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort, p.status, p.limit);
                 if (!ok) break;
-                unsigned char *da = base + s * stage_bytes(BN), *db = da + kBM * 128;
-                mbar_expect_tx(&S.full[s], stage_bytes(BN));
+                unsigned char *da = base + s * kStage, *db = da + kBM * 128;
+                if (rank == 0) mbar_expect_tx(&S.full[s], CG * kStage);
+                const uint32_t bar = CG == 2 ? peer_addr(&S.full[s], 0) : 0;
+                auto load = [&](unsigned char* dst, const CUtensorMap* m, int x, int y) {
+                    if (CG == 2) tma_load_3d_pair(dst, m, bar, x, y, at.mat);
+                    else tma_load_3d(dst, m, &S.full[s], x, y, at.mat);
+                };
                 if (AMN) {
-                    for (int i = 0; i < kBM / 64; ++i)
-                        tma_load_3d(da + i * 8192, &ma, &S.full[s], at.row + 64 * i, k * kBK, at.mat);
+                    for (int i = 0; i < kBM / 64; ++i) load(da + i * 8192, &ma, at.row + 64 * i, k * kBK);
                 } else {
-                    tma_load_3d(da, &ma, &S.full[s], k * kBK, at.row, at.mat);
+                    load(da, &ma, k * kBK, at.row);
                 }
                 if (BMN) {
-                    for (int i = 0; i < BN / 64; ++i)
-                        tma_load_3d(db + i * 8192, &mb, &S.full[s], at.col + 64 * i, k * kBK, at.mat);
+                    for (int i = 0; i < BN / CG / 64; ++i) load(db + i * 8192, &mb, at.col + 64 * i, k * kBK);
                 } else {
-                    tma_load_3d(db, &mb, &S.full[s], k * kBK, at.col, at.mat);
+                    load(db, &mb, k * kBK, at.col);
                 }
             }
         }
-        if (*(volatile int*)&S.abort)                   // copies still in flight
+        if (*(volatile int*)&S.abort && rank == 0)      // copies still in flight
             for (int i = max(0, it - kStages); i < it; ++i)
                 drain(&S.full[i % kStages], (i / kStages) & 1, p.limit);
-    } else if (warp == 1 && lane == 0) {
-        constexpr uint32_t id = idesc_f16(kBM, BN, AMN, BMN);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        constexpr uint32_t id = idesc_f16(TM, BN, AMN, BMN);
         int it = 0, n = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, ++n) {
+        for (int t = first; t < p.tiles && ok; t += stride, ++n) {
             const int acc = n & 1;
             ok = wait_one(&S.acc_empty[acc], ((n >> 1) & 1) ^ 1, &S.abort, p.status, p.limit);
             if (!ok) break;
@@ -512,16 +590,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 ok = wait_one(&S.full[s], (it / kStages) & 1, &S.abort, p.status, p.limit);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t da = smem_u32(base + s * stage_bytes(BN)), db = da + kBM * 128;
+                const uint32_t da = smem_u32(base + s * kStage), db = da + kBM * 128;
 #pragma unroll
-                for (int kk = 0; kk < kBK / 16; ++kk)
-                    mma_bf16(tmem + acc * BN,
-                             AMN ? sdesc(da + kk * 2048, 8192, 1024, 2) : sdesc(da + kk * 32, 16, 1024, 2),
-                             BMN ? sdesc(db + kk * 2048, 8192, 1024, 2) : sdesc(db + kk * 32, 16, 1024, 2),
-                             id, k > 0 || kk > 0);
-                mma_commit(&S.empty[s]);
+                for (int kk = 0; kk < kBK / 16; ++kk) {
+                    const uint64_t xa = AMN ? sdesc(da + kk * 2048, 8192, 1024, 2) : sdesc(da + kk * 32, 16, 1024, 2);
+                    const uint64_t xb = BMN ? sdesc(db + kk * 2048, 8192, 1024, 2) : sdesc(db + kk * 32, 16, 1024, 2);
+                    if (CG == 2) mma_pair(tmem + acc * BN, xa, xb, id, k > 0 || kk > 0);
+                    else mma_bf16(tmem + acc * BN, xa, xb, id, k > 0 || kk > 0);
+                }
+                if (CG == 2) commit_pair(&S.empty[s]);
+                else mma_commit(&S.empty[s]);
             }
-            if (ok) mma_commit(&S.acc_full[acc]);
+            if (!ok) break;
+            if (CG == 2) commit_pair(&S.acc_full[acc]);
+            else mma_commit(&S.acc_full[acc]);
         }
         if (*(volatile int*)&S.abort && it > 0)         // products still in flight
             drain(&S.empty[(it - 1) % kStages], ((it - 1) / kStages) & 1, p.limit);
@@ -530,9 +612,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         unsigned char* buf = epi + (warp - 2) * 4 * kChunkBytes;
         uint64_t* in = S.in[warp - 2];
         int n = 0, cnt = 0;
-        for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++n) {
-            const TileAt at = tile_at<EPI, BN>(p, t);
-            const int acc = n & 1, row0 = at.row + part * 32;
+        for (int t = first; t < p.tiles; t += stride, ++n) {
+            const TileAt at = tile_at<EPI, TM, BN>(p, t);
+            const int acc = n & 1, row0 = at.row + rank * kBM + part * 32;
             // chunks of 64 columns that have an element to write: a prefix
             int chunks = 0;
             if (row0 < p.M) chunks = min(BN / 64, (p.N - at.col + 63) / 64);
@@ -645,7 +727,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (!ok) break;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S.acc_empty[acc]);
+            if (lane == 0) {
+                if (CG == 2) mbar_arrive_at(peer_addr(&S.acc_empty[acc], 0));
+                else mbar_arrive(&S.acc_empty[acc]);
+            }
         }
         if (lane == 0) {
             bulk_wait<0>();
@@ -656,8 +741,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();                        // no arrival at a block that has left
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 2 * BN);
+    if (warp == 1) free_columns<CG>(tmem, 2 * BN);
 }
 
 // ----------------------------------------------------------------------------- host
@@ -701,50 +787,71 @@ struct Mat {
     }
 };
 
-template <bool AMN, bool BMN, int EPI, int BN>
-cudaError_t gemm_bn(const Mat& A, const Mat& B, const Mat& I0, const Mat& I1, const Mat& O0, const Mat& O1,
-                    GemmParams p, cudaStream_t s) {
-    p.tiles_m = (p.M + kBM - 1) / kBM;
-    p.tiles_n = (p.N + BN - 1) / BN;
-    p.per_matrix = 0;
-    if (EPI == kUpdate) {
-        p.per_matrix = p.tiles_m * p.tiles_n;
-    } else {
-        for (int i = 0; i < p.tiles_m; ++i) {
-            const int n = (i * kBM + kBM - 1) / BN + 1;
-            p.per_matrix += n < p.tiles_n ? n : p.tiles_n;
-        }
+// Tiles of one matrix.
+int tiles_of(int epi, int M, int N, int TM, int BN) {
+    const int tm = (M + TM - 1) / TM, tn = (N + BN - 1) / BN;
+    if (epi == kUpdate) return tm * tn;
+    int all = 0;
+    for (int i = 0; i < tm; ++i) {
+        const int n = (i * TM + TM - 1) / BN + 1;
+        all += n < tn ? n : tn;
     }
+    return all;
+}
+
+template <bool AMN, bool BMN, int EPI, int CG, int BN>
+cudaError_t gemm_tiles(const Mat& A, const Mat& B, const Mat& I0, const Mat& I1, const Mat& O0, const Mat& O1,
+                       GemmParams p, cudaStream_t s) {
+    p.tiles_m = (p.M + kBM * CG - 1) / (kBM * CG);
+    p.tiles_n = (p.N + BN - 1) / BN;
+    p.per_matrix = tiles_of(EPI, p.M, p.N, kBM * CG, BN);
     const long long tiles = (long long)p.per_matrix * p.batch;
     if (tiles > (1LL << 31) - 1) return cudaErrorInvalidValue;
     p.tiles = (int)tiles;
     CUtensorMap ma, mb, in0{}, in1{}, out0{}, out1{};
-    bool ok = A.map(&ma, 64, AMN ? 64 : kBM, true) && B.map(&mb, 64, BMN ? 64 : BN, true);
+    bool ok = A.map(&ma, 64, AMN ? 64 : kBM, true) && B.map(&mb, 64, BMN ? 64 : BN / CG, true);
     if (EPI != kGram) ok = ok && I0.map(&in0, 64, 32, true);
     if (EPI == kUpdate) ok = ok && I1.map(&in1, 64, 32, true);
     if (!p.last || p.last_by_copy) ok = ok && O0.map(&out0, 64, 32, true);
     if (EPI != kUpdate) ok = ok && O0.map(&out1, 32, 64, false);
     else if (!p.last) ok = ok && O1.map(&out1, 64, 32, true);
     if (!ok) return cudaErrorInvalidValue;
-    constexpr int smem = 1024 + stages_of(BN) * stage_bytes(BN) + kEpiBytes + sizeof(GemmShared);
-    auto kernel = ns_gemm_kernel<AMN, BMN, EPI, BN>;
+    constexpr int smem = 1024 + stages_of(CG, BN) * stage_bytes(CG, BN) + kEpiBytes + sizeof(GemmShared);
+    static_assert(smem <= 232448, "shared memory of a block");
+    auto kernel = ns_gemm_kernel<AMN, BMN, EPI, CG, BN>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<p.tiles < 152 ? p.tiles : 152, kGemmThreads, smem, s>>>(ma, mb, in0, in1, out0, out1, p);
-    return cudaGetLastError();
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(CG * (p.tiles < 152 / CG ? p.tiles : 152 / CG));
+    c.blockDim = dim3(kGemmThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, ma, mb, in0, in1, out0, out1, p);
 }
 
-// The widest tile that still gives most SMs one.
+// The tile that takes the least time by this count: rounds of tiles over the SMs times a tile's
+// blocks of K (cycles for its copies or products, whichever is more) and its start and epilogue.
 template <bool AMN, bool BMN, int EPI>
 cudaError_t gemm(const Mat& A, const Mat& B, const Mat& I0, const Mat& I1, const Mat& O0, const Mat& O1,
                  const GemmParams& p, cudaStream_t s) {
-    auto tiles = [&](int BN) {
-        const double all = (double)((p.M + kBM - 1) / kBM) * ((p.N + BN - 1) / BN) * p.batch;
-        return EPI == kUpdate ? all : all * 0.55;
+    auto cost = [&](int CG, int BN, double block) {
+        const long long tiles = (long long)tiles_of(EPI, p.M, p.N, kBM * CG, BN) * p.batch;
+        const long long slots = 152 / CG, rounds = (tiles + slots - 1) / slots;
+        return (double)rounds * ((p.K + kBK - 1) / kBK * block + 20.0 * BN) + 4000;
     };
-    if (tiles(256) >= 128) return gemm_bn<AMN, BMN, EPI, 256>(A, B, I0, I1, O0, O1, p, s);
-    if (tiles(128) >= 100) return gemm_bn<AMN, BMN, EPI, 128>(A, B, I0, I1, O0, O1, p, s);
-    return gemm_bn<AMN, BMN, EPI, 64>(A, B, I0, I1, O0, O1, p, s);
+    const double c64 = cost(1, 64, 490), c128 = cost(1, 128, 650), p128 = cost(2, 128, 490),
+                 p256 = cost(2, 256, 660);
+    if (p256 <= p128 && p256 <= c128 && p256 <= c64)
+        return gemm_tiles<AMN, BMN, EPI, 2, 256>(A, B, I0, I1, O0, O1, p, s);
+    if (p128 <= c128 && p128 <= c64) return gemm_tiles<AMN, BMN, EPI, 2, 128>(A, B, I0, I1, O0, O1, p, s);
+    if (c128 <= c64) return gemm_tiles<AMN, BMN, EPI, 1, 128>(A, B, I0, I1, O0, O1, p, s);
+    return gemm_tiles<AMN, BMN, EPI, 1, 64>(A, B, I0, I1, O0, O1, p, s);
 }
 
 }  // namespace
