@@ -447,9 +447,11 @@ __device__ __forceinline__ void free_columns(uint32_t t, uint32_t n) {
 //   kUpdate: X'  = alpha acc + beta X       (X and X' as hi + lo; the last one to bf16)
 // Roles (192 threads, one block an SM): warp 0 copies operand tiles in (kStages deep), warp 1
 // issues the products into one of two accumulators, warps 2-5 take the other through the
-// epilogue, 32 rows each, 64 columns at a time: the values to add come in by tensor copies one
-// chunk ahead, the results replace them in shared memory and leave by tensor copies, so
-// that every access to global memory is a full row of 128 bytes.
+// epilogue, 32 rows each, 64 columns at a time.  The values to add come in one chunk ahead and
+// the results leave through shared memory, so that accesses to global memory are full
+// rows of 128 bytes; they go by ordinary loads and stores, because tensor copies queue
+// behind the operands' (with those an epilogue of the projection's update took 27000
+// cycles a tile, more than its products' 17000).
 enum { kGram, kSquare, kUpdate };
 constexpr int kBM = 128, kBK = 64, kGemmThreads = 192;
 constexpr uint32_t kChunkBytes = 32 * 128;              // 32 rows of 64 fp16 values
@@ -466,14 +468,16 @@ struct GemmParams {
     int M, N, K, batch;
     int tiles_m, tiles_n, per_matrix, tiles;
     float alpha, beta;
-    __nv_bfloat16* last;        // kUpdate, last step: [batch][M][N]
-    int last_by_copy;           // its rows start on 16 bytes
+    const __half *in_hi, *in_lo;    // values to add, [batch][M][pitch]
+    __half *out_hi, *out_lo;        // results, [batch][M][pitch]
+    int pitch;                      // of all four, a multiple of 8
+    __nv_bfloat16* last;            // kUpdate, last step: the result instead, [batch][M][N]
     int* status;
     long long limit;
 };
 
 struct GemmShared {
-    uint64_t full[6], empty[6], acc_full[2], acc_empty[2], in[4][2];
+    uint64_t full[6], empty[6], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int abort;
 };
@@ -509,8 +513,6 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
 template <bool AMN, bool BMN, int EPI, int CG, int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     ns_gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-                   const __grid_constant__ CUtensorMap in0, const __grid_constant__ CUtensorMap in1,
-                   const __grid_constant__ CUtensorMap out0, const __grid_constant__ CUtensorMap out1,
                    const __grid_constant__ GemmParams p) {
     constexpr int kStages = stages_of(CG, BN), TM = kBM * CG;
     constexpr uint32_t kStage = stage_bytes(CG, BN);
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     unsigned char* epi = base + kStages * kStage;
     GemmShared& S = *reinterpret_cast<GemmShared*>(epi + kEpiBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)cluster_rank() : 0;
     const int first = blockIdx.x / CG, stride = gridDim.x / CG;
     const int kblocks = (p.K + kBK - 1) / kBK;
@@ -531,7 +533,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.acc_full[i], 1);
             mbar_init(&S.acc_empty[i], 4 * CG);
-            for (int w = 0; w < 4; ++w) mbar_init(&S.in[w][i], 1);
         }
         fence_mbar_init();
         S.abort = 0;
@@ -576,82 +577,107 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (*(volatile int*)&S.abort && rank == 0)      // copies still in flight
             for (int i = max(0, it - kStages); i < it; ++i)
                 drain(&S.full[i % kStages], (i / kStages) & 1, p.limit);
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
+        // The whole warp walks the loop, so that descriptors stay in uniform registers, and one
+        // elected lane issues: with a single lane in the loop a product left every 137 cycles
+        // whatever its size.
         constexpr uint32_t id = idesc_f16(TM, BN, AMN, BMN);
-        int it = 0, n = 0;
+        constexpr uint32_t step_a = (AMN ? 2048 : 32) >> 4, step_b = (BMN ? 2048 : 32) >> 4;
+        const uint32_t base_u = __shfl_sync(0xffffffffu, smem_u32(base), 0);
+        const uint64_t a0 = AMN ? sdesc(base_u, 8192, 1024, 2) : sdesc(base_u, 16, 1024, 2);
+        const uint64_t b0 = BMN ? sdesc(base_u + kBM * 128, 8192, 1024, 2) : sdesc(base_u + kBM * 128, 16, 1024, 2);
+        int s = 0, n = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int t = first; t < p.tiles && ok; t += stride, ++n) {
             const int acc = n & 1;
-            ok = wait_one(&S.acc_empty[acc], ((n >> 1) & 1) ^ 1, &S.abort, p.status, p.limit);
+            ok = wait_warp(&S.acc_empty[acc], ((n >> 1) & 1) ^ 1, &S.abort, p.status, p.limit);
             if (!ok) break;
             tc_fence_after();
-            for (int k = 0; k < kblocks; ++k, ++it) {
-                const int s = it % kStages;
-                ok = wait_one(&S.full[s], (it / kStages) & 1, &S.abort, p.status, p.limit);
+            const uint32_t d = tmem + acc * BN;
+            for (int k = 0; k < kblocks; ++k) {
+                ok = wait_warp(&S.full[s], phase, &S.abort, p.status, p.limit);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t da = smem_u32(base + s * kStage), db = da + kBM * 128;
+                const uint64_t da = a0 + s * (kStage >> 4), db = b0 + s * (kStage >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kBK / 16; ++kk) {
-                    const uint64_t xa = AMN ? sdesc(da + kk * 2048, 8192, 1024, 2) : sdesc(da + kk * 32, 16, 1024, 2);
-                    const uint64_t xb = BMN ? sdesc(db + kk * 2048, 8192, 1024, 2) : sdesc(db + kk * 32, 16, 1024, 2);
-                    if (CG == 2) mma_pair(tmem + acc * BN, xa, xb, id, k > 0 || kk > 0);
-                    else mma_bf16(tmem + acc * BN, xa, xb, id, k > 0 || kk > 0);
+                    for (int kk = 0; kk < kBK / 16; ++kk) {
+                        if (CG == 2) mma_pair(d, da + kk * step_a, db + kk * step_b, id, k > 0 || kk > 0);
+                        else mma_bf16(d, da + kk * step_a, db + kk * step_b, id, k > 0 || kk > 0);
+                    }
+                    if (CG == 2) commit_pair(&S.empty[s]);
+                    else mma_commit(&S.empty[s]);
+                    if (k + 1 == kblocks) {
+                        if (CG == 2) commit_pair(&S.acc_full[acc]);
+                        else mma_commit(&S.acc_full[acc]);
+                    }
                 }
-                if (CG == 2) commit_pair(&S.empty[s]);
-                else mma_commit(&S.empty[s]);
+                __syncwarp();
+                if (++s == kStages) { s = 0; phase ^= 1; }
             }
-            if (!ok) break;
-            if (CG == 2) commit_pair(&S.acc_full[acc]);
-            else mma_commit(&S.acc_full[acc]);
         }
-        if (*(volatile int*)&S.abort && it > 0)         // products still in flight
-            drain(&S.empty[(it - 1) % kStages], ((it - 1) / kStages) & 1, p.limit);
+        // after an abort: products still in flight (the commit of the stage before s)
+        if (*(volatile int*)&S.abort && lane == 0 && (s > 0 || phase))
+            drain(&S.empty[s ? s - 1 : kStages - 1], s ? phase : phase ^ 1, p.limit);
     } else if (warp >= 2) {
         const int part = warp & 3;                      // this warp's lanes of tensor memory
         unsigned char* buf = epi + (warp - 2) * 4 * kChunkBytes;
-        uint64_t* in = S.in[warp - 2];
-        int n = 0, cnt = 0;
+        int n = 0;
         for (int t = first; t < p.tiles; t += stride, ++n) {
             const TileAt at = tile_at<EPI, TM, BN>(p, t);
             const int acc = n & 1, row0 = at.row + rank * kBM + part * 32;
+            const size_t mat = (size_t)at.mat * p.M * p.pitch;
             // chunks of 64 columns that have an element to write: a prefix
             int chunks = 0;
             if (row0 < p.M) chunks = min(BN / 64, (p.N - at.col + 63) / 64);
-            if (EPI != kUpdate && chunks > 0) chunks = min(chunks, max(0, (row0 + 31 - at.col) / 64 + (row0 + 31 >= at.col)));
-            auto fetch = [&](int c, int b) {            // lane 0: chunk c into buffer b
-                bulk_wait_read<0>();
-                mbar_expect_tx(&in[b], (EPI == kUpdate ? 2 : 1) * kChunkBytes);
-                tma_load_3d(buf + b * 2 * kChunkBytes, &in0, &in[b], at.col + 64 * c, row0, at.mat);
-                if (EPI == kUpdate)
-                    tma_load_3d(buf + b * 2 * kChunkBytes + kChunkBytes, &in1, &in[b], at.col + 64 * c,
-                                row0, at.mat);
+            if (EPI != kUpdate && chunks > 0)
+                chunks = min(chunks, max(0, (row0 + 31 - at.col) / 64 + (row0 + 31 >= at.col)));
+            // rows of 128 bytes: lane l takes 16 bytes l % 8 of rows l / 8, l / 8 + 4, ..
+            const int piece = lane & 7, prow = lane >> 3;
+            auto fetch = [&](int c) {                   // chunk c into its buffer
+                unsigned char* to = buf + (c & 1) * 2 * kChunkBytes;
+                const int col = at.col + 64 * c + 8 * piece;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = prow + 4 * i;
+                    const size_t o = mat + (size_t)(row0 + r) * p.pitch + col;
+                    const bool in = row0 + r < p.M && col < p.pitch;
+                    const uint32_t d = smem_u32(to) + r * 128 + ((piece ^ (r & 7)) << 4);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
+                                 "l"(in ? p.in_hi + o : p.in_hi), "r"(in ? 16 : 0) : "memory");
+                    if (EPI == kUpdate)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + kChunkBytes),
+                                     "l"(in ? p.in_lo + o : p.in_lo), "r"(in ? 16 : 0) : "memory");
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
             };
-            if (EPI != kGram && chunks > 0 && lane == 0) fetch(0, cnt & 1);
+            if (EPI != kGram && chunks > 0) fetch(0);
             if (!wait_warp(&S.acc_full[acc], (n >> 1) & 1, &S.abort, p.status, p.limit)) break;
             tc_fence_after();
-            bool ok = true;
-            for (int c = 0; c < chunks; ++c, ++cnt) {
-                const int b = cnt & 1, col0 = at.col + 64 * c;
-                unsigned char *hi = buf + b * 2 * kChunkBytes, *lo = hi + kChunkBytes;
-                if (lane == 0) {
-                    if (EPI == kGram) bulk_wait_read<1>();
-                    else if (c + 1 < chunks) fetch(c + 1, b ^ 1);
-                }
-                __syncwarp();
+            for (int c = 0; c < chunks; ++c) {
+                const int col0 = at.col + 64 * c;
+                unsigned char *hi = buf + (c & 1) * 2 * kChunkBytes, *lo = hi + kChunkBytes;
                 if (EPI != kGram) {
-                    ok = wait_warp(&in[b], (cnt >> 1) & 1, &S.abort, p.status, p.limit);
-                    if (!ok) break;
+                    if (c + 1 < chunks) {
+                        fetch(c + 1);
+                        asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    } else {
+                        asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    }
+                    __syncwarp();
                 }
                 const bool mirror = EPI != kUpdate && row0 > col0 + 63;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float v[16];
-                    tmem_ld16(tmem_addr(tmem, part * 32, acc * BN + 64 * c + 16 * q), v);
+                for (int q = 0; q < 2; ++q) {
+                    float v[32];
+                    const uint32_t ta = tmem_addr(tmem, part * 32, acc * BN + 64 * c + 32 * q);
+                    tmem_ld16(ta, *reinterpret_cast<float(*)[16]>(v));
+                    tmem_ld16(ta + 16, *reinterpret_cast<float(*)[16]>(v + 16));
                     tmem_wait_ld();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t o = lane * 128 + (((2 * q + h) ^ (lane & 7)) << 4);
+                    for (int h = 0; h < 4; ++h) {
+                        const uint32_t o = lane * 128 + (((4 * q + h) ^ (lane & 7)) << 4);
                         uint4* at_hi = reinterpret_cast<uint4*>(hi + o);
                         uint4* at_lo = reinterpret_cast<uint4*>(lo + o);
                         float* f = v + 8 * h;
@@ -694,15 +720,32 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         if (EPI == kUpdate) {
                             if (!p.last) *at_lo = make_uint4(z[0], z[1], z[2], z[3]);
                         } else if (mirror) {            // [64 columns][32 rows]
-                            __half* m = reinterpret_cast<__half*>(lo) + (16 * q + 8 * h) * 32 + lane;
+                            __half* m = reinterpret_cast<__half*>(lo) + (32 * q + 8 * h) * 32 + lane;
 #pragma unroll
                             for (int i = 0; i < 8; ++i) m[i * 32] = __float2half_rn(f[i]);
                         }
                     }
                 }
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (EPI == kUpdate && p.last && !p.last_by_copy) {
+                // out again, row by row; the columns between N and the pitch are never read
+                const bool rows16 = EPI != kUpdate || !p.last || p.N % 8 == 0;
+                if (rows16) {
+                    const int col = col0 + 8 * piece, width = EPI == kUpdate && p.last ? p.N : p.pitch;
+                    __half* o_hi = EPI == kUpdate && p.last
+                                       ? reinterpret_cast<__half*>(p.last) + (size_t)at.mat * p.M * p.N
+                                       : p.out_hi + mat;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = prow + 4 * i;
+                        const uint32_t o = r * 128 + ((piece ^ (r & 7)) << 4);
+                        if (row0 + r < p.M && col < width) {
+                            const size_t g = (size_t)(row0 + r) * width + col;
+                            *reinterpret_cast<uint4*>(o_hi + g) = *reinterpret_cast<uint4*>(hi + o);
+                            if (EPI == kUpdate && !p.last)
+                                *reinterpret_cast<uint4*>(p.out_lo + mat + g) = *reinterpret_cast<uint4*>(lo + o);
+                        }
+                    }
+                } else {
                     __nv_bfloat16* o = p.last + ((size_t)at.mat * p.M + row0) * p.N + col0;
                     for (int r = 0; r < 32 && row0 + r < p.M; ++r)
 #pragma unroll
@@ -712,30 +755,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                 o[(size_t)r * p.N + e] = *reinterpret_cast<__nv_bfloat16*>(
                                     hi + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2);
                         }
-                    fence_proxy_async_smem();           // read before the next copy into it
-                    __syncwarp();
-                } else if (lane == 0) {
-                    tma_store_3d(&out0, hi, col0, row0, at.mat);
-                    if (EPI == kUpdate) {
-                        if (!p.last) tma_store_3d(&out1, lo, col0, row0, at.mat);
-                    } else if (mirror) {
-                        tma_store_3d(&out1, lo, row0, col0, at.mat);
-                    }
-                    bulk_commit();
                 }
+                if (mirror) {                           // rows of 64 bytes, 4 lanes each
+                    const int x = row0 + 8 * (lane & 3);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = (lane >> 2) + 8 * i;
+                        if (x < p.pitch)
+                            *reinterpret_cast<uint4*>(p.out_hi + mat + (size_t)(col0 + r) * p.pitch + x) =
+                                *reinterpret_cast<uint4*>(lo + r * 64 + (lane & 3) * 16);
+                    }
+                }
+                __syncwarp();
             }
-            if (!ok) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
                 if (CG == 2) mbar_arrive_at(peer_addr(&S.acc_empty[acc], 0));
                 else mbar_arrive(&S.acc_empty[acc]);
             }
-        }
-        if (lane == 0) {
-            bulk_wait<0>();
-            if (*(volatile int*)&S.abort && EPI != kGram)
-                for (int b = 0; b < 2; ++b) drain(&in[b], 0, p.limit >> 3);
         }
     }
     __syncwarp();
@@ -751,7 +789,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 int pitch_of(int n) { return (n + 7) / 8 * 8; }
 
 struct Workspace {
-    size_t x[2][2], a, b, part, total;      // X (ping, pong) x (hi, lo), A, B, norm sums
+    size_t hi[2], lo, a, b, part, total;    // X as hi (two in turn) + lo (in place), A, B, norm sums
 };
 
 Workspace layout(int batch, int m, int n) {
@@ -764,8 +802,8 @@ Workspace layout(int batch, int m, int n) {
         off += (bytes + 255) / 256 * 256;
         return at;
     };
-    for (auto& pair : w.x)
-        for (size_t& o : pair) o = take(xs);
+    for (size_t& o : w.hi) o = take(xs);
+    w.lo = take(xs);
     w.a = take(as);
     w.b = take(as);
     w.part = take((size_t)batch * kNormBlocks * sizeof(float));
@@ -775,15 +813,15 @@ Workspace layout(int batch, int m, int n) {
 
 bool small(int m, int n) { return m <= kSide && n <= kSide; }
 
-// A stored fp16 (or bf16) matrix batch: [batch][rows][pitch].
+// A stored fp16 matrix batch: [batch][rows][pitch].
 struct Mat {
-    const void* p;
+    __half* p;
     int rows, cols, pitch, batch;
-    TmaType type = TmaType::f16;
-    bool map(CUtensorMap* m, unsigned bx, unsigned by, bool swizzle) const {
+    bool map(CUtensorMap* m, unsigned bx, unsigned by) const {
         const unsigned long long row = (unsigned long long)pitch * 2;
-        return make_tma_map(m, type, p, {(unsigned long long)cols, (unsigned long long)rows, (unsigned long long)batch},
-                            {row, row * rows}, {bx, by, 1u}, swizzle);
+        return make_tma_map(m, TmaType::f16, p,
+                            {(unsigned long long)cols, (unsigned long long)rows, (unsigned long long)batch},
+                            {row, row * rows}, {bx, by, 1u}, true);
     }
 };
 
@@ -800,22 +838,15 @@ int tiles_of(int epi, int M, int N, int TM, int BN) {
 }
 
 template <bool AMN, bool BMN, int EPI, int CG, int BN>
-cudaError_t gemm_tiles(const Mat& A, const Mat& B, const Mat& I0, const Mat& I1, const Mat& O0, const Mat& O1,
-                       GemmParams p, cudaStream_t s) {
+cudaError_t gemm_tiles(const Mat& A, const Mat& B, GemmParams p, cudaStream_t s) {
     p.tiles_m = (p.M + kBM * CG - 1) / (kBM * CG);
     p.tiles_n = (p.N + BN - 1) / BN;
     p.per_matrix = tiles_of(EPI, p.M, p.N, kBM * CG, BN);
     const long long tiles = (long long)p.per_matrix * p.batch;
     if (tiles > (1LL << 31) - 1) return cudaErrorInvalidValue;
     p.tiles = (int)tiles;
-    CUtensorMap ma, mb, in0{}, in1{}, out0{}, out1{};
-    bool ok = A.map(&ma, 64, AMN ? 64 : kBM, true) && B.map(&mb, 64, BMN ? 64 : BN / CG, true);
-    if (EPI != kGram) ok = ok && I0.map(&in0, 64, 32, true);
-    if (EPI == kUpdate) ok = ok && I1.map(&in1, 64, 32, true);
-    if (!p.last || p.last_by_copy) ok = ok && O0.map(&out0, 64, 32, true);
-    if (EPI != kUpdate) ok = ok && O0.map(&out1, 32, 64, false);
-    else if (!p.last) ok = ok && O1.map(&out1, 64, 32, true);
-    if (!ok) return cudaErrorInvalidValue;
+    CUtensorMap ma, mb;
+    if (!A.map(&ma, 64, AMN ? 64 : kBM) || !B.map(&mb, 64, BMN ? 64 : BN / CG)) return cudaErrorInvalidValue;
     constexpr int smem = 1024 + stages_of(CG, BN) * stage_bytes(CG, BN) + kEpiBytes + sizeof(GemmShared);
     static_assert(smem <= 232448, "shared memory of a block");
     auto kernel = ns_gemm_kernel<AMN, BMN, EPI, CG, BN>;
@@ -832,14 +863,13 @@ cudaError_t gemm_tiles(const Mat& A, const Mat& B, const Mat& I0, const Mat& I1,
     c.stream = s;
     c.attrs = at;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kernel, ma, mb, in0, in1, out0, out1, p);
+    return cudaLaunchKernelEx(&c, kernel, ma, mb, p);
 }
 
 // The tile that takes the least time by this count: rounds of tiles over the SMs times a tile's
 // blocks of K (cycles for its copies or products, whichever is more) and its start and epilogue.
 template <bool AMN, bool BMN, int EPI>
-cudaError_t gemm(const Mat& A, const Mat& B, const Mat& I0, const Mat& I1, const Mat& O0, const Mat& O1,
-                 const GemmParams& p, cudaStream_t s) {
+cudaError_t gemm(const Mat& A, const Mat& B, const GemmParams& p, cudaStream_t s) {
     auto cost = [&](int CG, int BN, double block) {
         const long long tiles = (long long)tiles_of(EPI, p.M, p.N, kBM * CG, BN) * p.batch;
         const long long slots = 152 / CG, rounds = (tiles + slots - 1) / slots;
@@ -848,10 +878,10 @@ cudaError_t gemm(const Mat& A, const Mat& B, const Mat& I0, const Mat& I1, const
     const double c64 = cost(1, 64, 490), c128 = cost(1, 128, 650), p128 = cost(2, 128, 490),
                  p256 = cost(2, 256, 660);
     if (p256 <= p128 && p256 <= c128 && p256 <= c64)
-        return gemm_tiles<AMN, BMN, EPI, 2, 256>(A, B, I0, I1, O0, O1, p, s);
-    if (p128 <= c128 && p128 <= c64) return gemm_tiles<AMN, BMN, EPI, 2, 128>(A, B, I0, I1, O0, O1, p, s);
-    if (c128 <= c64) return gemm_tiles<AMN, BMN, EPI, 1, 128>(A, B, I0, I1, O0, O1, p, s);
-    return gemm_tiles<AMN, BMN, EPI, 1, 64>(A, B, I0, I1, O0, O1, p, s);
+        return gemm_tiles<AMN, BMN, EPI, 2, 256>(A, B, p, s);
+    if (p128 <= c128 && p128 <= c64) return gemm_tiles<AMN, BMN, EPI, 2, 128>(A, B, p, s);
+    if (c128 <= c64) return gemm_tiles<AMN, BMN, EPI, 1, 128>(A, B, p, s);
+    return gemm_tiles<AMN, BMN, EPI, 1, 64>(A, B, p, s);
 }
 
 }  // namespace
@@ -877,11 +907,13 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
     const bool wide = a.m <= a.n;
     const int r = wide ? a.m : a.n, l = wide ? a.n : a.m;
     const int xp = pitch_of(a.n), ap = pitch_of(r);
-    Mat X[2][2];
-    for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2; ++j) X[i][j] = Mat{ws + w.x[i][j], a.m, a.n, xp, a.batch};
-    const Mat A{ws + w.a, r, r, ap, a.batch}, B{ws + w.b, r, r, ap, a.batch};
-    const Mat out{a.out, a.m, a.n, a.n, a.batch, TmaType::bf16};
+    // every tile reads all of hi's rows, so the new one goes elsewhere; a value of lo is read and
+    // written by the same warp
+    const Mat hi[2] = {{reinterpret_cast<__half*>(ws + w.hi[0]), a.m, a.n, xp, a.batch},
+                       {reinterpret_cast<__half*>(ws + w.hi[1]), a.m, a.n, xp, a.batch}};
+    __half* lo = reinterpret_cast<__half*>(ws + w.lo);
+    const Mat A{reinterpret_cast<__half*>(ws + w.a), r, r, ap, a.batch};
+    const Mat B{reinterpret_cast<__half*>(ws + w.b), r, r, ap, a.batch};
     float* part = reinterpret_cast<float*>(ws + w.part);
 
     const size_t mn = (size_t)a.m * a.n;
@@ -892,19 +924,19 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
     size_t fill = (mn + 4095) / 4096;
     if (fill > 2048) fill = 2048;
     ns_start_kernel<<<dim3((unsigned)fill, a.batch), 256, 0, s>>>(
-        a, part, (int)blocks, xp, (__half*)X[0][0].p, (__half*)X[0][1].p);
+        a, part, (int)blocks, xp, hi[0].p, lo);
     *launches = 2;
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (a.steps == 0) {
         ns_round_kernel<<<dim3((unsigned)fill, a.batch), 256, 0, s>>>(
-            a.m, a.n, xp, (const __half*)X[0][0].p, (const __half*)X[0][1].p, (__nv_bfloat16*)a.out);
+            a.m, a.n, xp, hi[0].p, lo, (__nv_bfloat16*)a.out);
         ++*launches;
         return cudaGetLastError();
     }
     for (int i = 0; i < a.steps; ++i) {
         const float *c = a.coeffs + 3 * i;
-        const Mat *x = X[i & 1], *y = X[(i & 1) ^ 1];
+        const Mat &x = hi[i & 1], &y = hi[(i & 1) ^ 1];
         // B is stored times 2^10, less where its coefficients are large
         float sb = kScale;
         while (sb > 1.f && (std::fabs(c[1]) + std::fabs(c[2])) * sb > 8.f * kScale) sb *= 0.5f;
@@ -915,25 +947,27 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         p.M = p.N = r;
         p.K = l;
         p.alpha = kUnscale;                              // (2^10 X)(2^10 X)^T -> 2^10 A
-        e = wide ? gemm<false, false, kGram>(x[0], x[0], A, A, A, A, p, s)
-                 : gemm<true, true, kGram>(x[0], x[0], A, A, A, A, p, s);
+        p.pitch = ap;
+        p.out_hi = A.p;
+        e = wide ? gemm<false, false, kGram>(x, x, p, s) : gemm<true, true, kGram>(x, x, p, s);
         if (e != cudaSuccess) return e;
         p.K = r;
         p.alpha = c[2] * sb * kUnscale * kUnscale;       // -> sb (b A + c A A)
         p.beta = c[1] * sb * kUnscale;
-        e = gemm<false, false, kSquare>(A, A, A, A, B, B, p, s);
+        p.in_hi = A.p;
+        p.out_hi = B.p;
+        e = gemm<false, false, kSquare>(A, A, p, s);
         if (e != cudaSuccess) return e;
         p.M = a.m;
         p.N = a.n;
         p.alpha = 1.f / sb;                              // -> 2^10 X'
         p.beta = c[0];
-        if (i + 1 == a.steps) {
-            p.last = static_cast<__nv_bfloat16*>(a.out);
-            p.last_by_copy = a.n % 8 == 0;
-        }
-        const Mat& o = p.last ? out : y[0];
-        e = wide ? gemm<false, true, kUpdate>(B, x[0], x[0], x[1], o, y[1], p, s)
-                 : gemm<false, false, kUpdate>(x[0], B, x[0], x[1], o, y[1], p, s);
+        p.pitch = xp;
+        p.in_hi = x.p;
+        p.in_lo = p.out_lo = lo;
+        p.out_hi = y.p;
+        p.last = i + 1 == a.steps ? static_cast<__nv_bfloat16*>(a.out) : nullptr;
+        e = wide ? gemm<false, true, kUpdate>(B, x, p, s) : gemm<false, false, kUpdate>(x, B, p, s);
         if (e != cudaSuccess) return e;
         *launches += 3;
     }
