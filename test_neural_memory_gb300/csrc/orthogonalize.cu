@@ -298,6 +298,13 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
     if (warp == 0) tmem_dealloc(tmem, 128);
 }
 
+// The kernels of a call are launched so that one may start while the blocks of the one before
+// finish: its set-up runs beside them, and it waits here before it reads what they wrote.
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ norm and X_0
 
 constexpr int kNormBlocks = 1024;      // partial sums of a matrix
@@ -445,17 +452,15 @@ __device__ __forceinline__ void free_columns(uint32_t t, uint32_t n) {
 //   kGram:   out = alpha acc                (A; on and below the diagonal, mirrored)
 //   kSquare: out = alpha acc + beta in      (B from A A and A; likewise)
 //   kUpdate: X'  = alpha acc + beta X       (X and X' as hi + lo; the last one to bf16)
-// Roles (192 threads, one block an SM): warp 0 copies operand tiles in (kStages deep), warp 1
-// issues the products into one of two accumulators, warps 2-5 take the other through the
-// epilogue, 32 rows each, 64 columns at a time.  The values to add come in one chunk ahead and
-// the results leave through shared memory, so that accesses to global memory are full
-// rows of 128 bytes; they go by ordinary loads and stores, because tensor copies queue
-// behind the operands' (with those an epilogue of the projection's update took 27000
-// cycles a tile, more than its products' 17000).
+// Roles (320 threads, one block an SM): warp 0 copies operand tiles in (kStages deep), warp 1
+// issues the products into one of two accumulators, warps 2-9 take the other through the
+// epilogue: 32 rows and every other chunk of 64 columns each.  The values to add and the
+// results go through shared memory, so that accesses to global memory are full rows of
+// 128 bytes.
 enum { kGram, kSquare, kUpdate };
-constexpr int kBM = 128, kBK = 64, kGemmThreads = 192;
+constexpr int kBM = 128, kBK = 64, kEpiWarps = 8, kGemmThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kChunkBytes = 32 * 128;              // 32 rows of 64 fp16 values
-constexpr uint32_t kEpiBytes = 4 * 2 * 2 * kChunkBytes; // warps x buffers x (hi, lo)
+constexpr uint32_t kEpiBytes = kEpiWarps * 2 * kChunkBytes;   // (hi, lo) for each warp
 
 // As many stages as fit beside the epilogue's buffers in 227 KB, at most 6.
 __host__ __device__ constexpr int stages_of(int CG, int BN) {
@@ -532,7 +537,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.acc_full[i], 1);
-            mbar_init(&S.acc_empty[i], 4 * CG);
+            mbar_init(&S.acc_empty[i], kEpiWarps * CG);
         }
         fence_mbar_init();
         S.abort = 0;
@@ -543,6 +548,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (CG == 2) cluster_sync();                        // both blocks' barriers are set up
     tc_fence_after();
     const uint32_t tmem = S.tmem;
+    after_previous();
 
     if (warp == 0 && lane == 0) {
         int it = 0;
@@ -622,7 +628,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             drain(&S.empty[s ? s - 1 : kStages - 1], s ? phase : phase ^ 1, p.limit);
     } else if (warp >= 2) {
         const int part = warp & 3;                      // this warp's lanes of tensor memory
-        unsigned char* buf = epi + (warp - 2) * 4 * kChunkBytes;
+        const int turn = (warp - 2) >> 2;               // of the chunks, this warp's share
+        unsigned char *hi = epi + (warp - 2) * 2 * kChunkBytes, *lo = hi + kChunkBytes;
         int n = 0;
         for (int t = first; t < p.tiles; t += stride, ++n) {
             const TileAt at = tile_at<EPI, TM, BN>(p, t);
@@ -635,36 +642,28 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 chunks = min(chunks, max(0, (row0 + 31 - at.col) / 64 + (row0 + 31 >= at.col)));
             // rows of 128 bytes: lane l takes 16 bytes l % 8 of rows l / 8, l / 8 + 4, ..
             const int piece = lane & 7, prow = lane >> 3;
-            auto fetch = [&](int c) {                   // chunk c into its buffer
-                unsigned char* to = buf + (c & 1) * 2 * kChunkBytes;
+            auto fetch = [&](int c) {                   // the values to add to chunk c
                 const int col = at.col + 64 * c + 8 * piece;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = prow + 4 * i;
                     const size_t o = mat + (size_t)(row0 + r) * p.pitch + col;
                     const bool in = row0 + r < p.M && col < p.pitch;
-                    const uint32_t d = smem_u32(to) + r * 128 + ((piece ^ (r & 7)) << 4);
+                    const uint32_t d = smem_u32(hi) + r * 128 + ((piece ^ (r & 7)) << 4);
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
                                  "l"(in ? p.in_hi + o : p.in_hi), "r"(in ? 16 : 0) : "memory");
                     if (EPI == kUpdate)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + kChunkBytes),
                                      "l"(in ? p.in_lo + o : p.in_lo), "r"(in ? 16 : 0) : "memory");
                 }
-                asm volatile("cp.async.commit_group;" ::: "memory");
             };
-            if (EPI != kGram && chunks > 0) fetch(0);
+            if (EPI != kGram && turn < chunks) fetch(turn);
             if (!wait_warp(&S.acc_full[acc], (n >> 1) & 1, &S.abort, p.status, p.limit)) break;
             tc_fence_after();
-            for (int c = 0; c < chunks; ++c) {
+            for (int c = turn; c < chunks; c += 2) {
                 const int col0 = at.col + 64 * c;
-                unsigned char *hi = buf + (c & 1) * 2 * kChunkBytes, *lo = hi + kChunkBytes;
                 if (EPI != kGram) {
-                    if (c + 1 < chunks) {
-                        fetch(c + 1);
-                        asm volatile("cp.async.wait_group 1;" ::: "memory");
-                    } else {
-                        asm volatile("cp.async.wait_group 0;" ::: "memory");
-                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
                     __syncwarp();
                 }
                 const bool mirror = EPI != kUpdate && row0 > col0 + 63;
@@ -767,6 +766,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                 }
                 __syncwarp();
+                if (EPI != kGram && c + 2 < chunks) fetch(c + 2);
             }
             tc_fence_before();
             __syncwarp();
@@ -852,17 +852,19 @@ cudaError_t gemm_tiles(const Mat& A, const Mat& B, GemmParams p, cudaStream_t s)
     auto kernel = ns_gemm_kernel<AMN, BMN, EPI, CG, BN>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = CG;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(CG * (p.tiles < 152 / CG ? p.tiles : 152 / CG));
     c.blockDim = dim3(kGemmThreads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
     c.attrs = at;
-    c.numAttrs = 1;
+    c.numAttrs = 2;
     return cudaLaunchKernelEx(&c, kernel, ma, mb, p);
 }
 
