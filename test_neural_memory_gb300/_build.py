@@ -1,21 +1,27 @@
-"""Builds libttm.so in-tree with nvcc for sm_103a (no torch involvement).
+"""Builds libttm.so in-tree with nvcc for sm_103a (no torch involvement), and beside it
+ttm_torch.so, the compiled part of the Python binding.
 
 Each translation unit under ``csrc/`` is compiled in parallel, then linked
 into ``_lib/libttm.so`` with the CUDA runtime linked statically, so the
-library loads on machines without a GPU driver.
+library loads on machines without a GPU driver.  ``csrc/bind_train.cpp`` is
+compiled by the host compiler against torch's headers and linked with libttm.so.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libttm.so")
+BIND = os.path.join(LIBDIR, "ttm_torch.so")
+BIND_SRC = os.path.join(CSRC, "bind_train.cpp")
 ROOT = os.path.dirname(HERE)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -34,12 +40,24 @@ def sources() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    deps = sources() + [BIND_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
     deps.append(os.path.join(ROOT, "include", "ttm.h"))
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _bind_flags(nvcc: str) -> tuple[list[str], list[str]]:
+    """Compiler and linker flags of the torch binding (torch is found, not imported)."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")]
+    lib = os.path.join(torch, "lib")
+    cflags = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(f"-I{p}" for p in inc)]
+    ldflags = [f"-L{lib}", f"-L{LIBDIR}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+               "-lc10_cuda", "-lttm", f"-Wl,-rpath,{lib}", "-Wl,-rpath,$ORIGIN"]
+    return cflags, ldflags
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -61,8 +79,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+    cflags, ldflags = _bind_flags(nvcc)
+    bind_obj = os.path.join(objdir, "bind_train.cpp.o")
+
+    def compile_bind() -> None:
+        r = subprocess.run(["g++", *cflags, "-c", BIND_SRC, "-o", bind_obj], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+
+    with cf.ThreadPoolExecutor(max_workers=max(2, min(16, os.cpu_count() or 1))) as ex:
+        bind = ex.submit(compile_bind)
         objs = list(ex.map(compile_one, sources()))
+        bind.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", *objs, "-lcublas",
            "-Xlinker", "-rpath=" + os.path.join(os.path.dirname(os.path.dirname(nvcc)), "lib64"),
@@ -71,6 +99,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = BIND + f".{os.getpid()}.tmp"
+    r = subprocess.run(["g++", "-shared", bind_obj, *ldflags, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the torch binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
     return LIB
 
 
