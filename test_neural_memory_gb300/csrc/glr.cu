@@ -39,6 +39,7 @@
 #include <cstdint>
 
 #include "../../include/ttm.h"
+#include "pairs.cuh"
 #include "tc_ptx.cuh"
 #include "train_ops.h"
 
@@ -53,32 +54,52 @@ constexpr int kChans = V << kMaxLog;          // channels of a full strip
 constexpr int kBatch = 8;                     // tiles a look-back reads at a time
 constexpr long long kWaitCycles = 4000000000LL;   // default limit, ~2 s at 2 GHz
 
-// R, the tokens of one thread in a tile.
-template <typename E> constexpr int kRun = sizeof(E) == 2 ? 16 : 8;
-template <typename E> constexpr int kTileBytes = kThreads * kRun<E> * V * (int)sizeof(E);
+// R, the tokens of one thread in a tile: what it holds of them in registers is 64 of those
+// forward, 48 in the gradient.
+template <typename E, bool kBack> constexpr int kRun = (sizeof(E) == 2 ? 16 : 8) / (kBack ? 2 : 1);
+template <typename E, bool kBack> constexpr int kTileBytes = kThreads * kRun<E, kBack> * V * (int)sizeof(E);
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void put(float& o, float v) { o = v; }
 __device__ __forceinline__ void put(__nv_bfloat16& o, float v) { o = __float2bfloat16(v); }
 
-// Four channels as fp32 values and back.
+// Four channels as they are stored.
+template <typename E> struct Held;
+template <> struct Held<float> {
+    float4 u;
+    __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void get(f2 (&f)[2]) const { f[0] = pair(u.x, u.y); f[1] = pair(u.z, u.w); }
+    __device__ __forceinline__ void set(const f2 (&f)[2]) { split(f[0], u.x, u.y); split(f[1], u.z, u.w); }
+    __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = u; }
+    __device__ __forceinline__ void repack() {}
+};
+template <> struct Held<__nv_bfloat16> {
+    uint2 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void get(f2 (&f)[2]) const { f[0] = pair_of_bf16(u.x); f[1] = pair_of_bf16(u.y); }
+    __device__ __forceinline__ void set(const f2 (&f)[2]) { u = make_uint2(bf16_of_pair(f[0]), bf16_of_pair(f[1])); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = u; }
+    // forgets the unpacked values: cheaper to take again than to keep over the look-back
+    __device__ __forceinline__ void repack() { asm volatile("" : "+r"(u.x), "+r"(u.y)); }
+};
 __device__ __forceinline__ void get4(const float* p, float (&f)[V]) {
     const float4 u = *reinterpret_cast<const float4*>(p);
     f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
 }
 __device__ __forceinline__ void get4(const __nv_bfloat16* p, float (&f)[V]) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xffff0000u);
-    f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xffff0000u);
+    Held<__nv_bfloat16> h;
+    f2 q[2];
+    h.load(p);
+    h.get(q);
+    split(q[0], f[0], f[1]);
+    split(q[1], f[2], f[3]);
 }
 __device__ __forceinline__ void put4(float* p, const float (&f)[V]) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
 }
 __device__ __forceinline__ void put4(__nv_bfloat16* p, const float (&f)[V]) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                              *reinterpret_cast<const uint32_t*>(&b));
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_of_pair(pair(f[0], f[1])), bf16_of_pair(pair(f[2], f[3])));
 }
 
 // exp through the base-2 unit (2 units in the last place); -infinity gives 0.
@@ -86,6 +107,17 @@ __device__ __forceinline__ float retention(float g) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(g * 1.44269504088896341f));
     return r;
+}
+
+__device__ __forceinline__ void retention(const f2 (&g)[2], f2 (&r)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float lo, hi;
+        split(mul(g[i], splat<f2>(1.44269504088896341f)), lo, hi);
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(lo));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(hi));
+        r[i] = pair(lo, hi);
+    }
 }
 
 // A c + H for the map (A, H).  A state of exactly zero stays out of the product: a
@@ -104,55 +136,63 @@ inline int access_width(const void* p, long long seq, long long tok, int es) {
 }
 
 // Copies rows [0, rows) of `bytes` bytes at `pitch` bytes from global memory into
-// shared rows of `srow` bytes, width bytes at a time; rows below `lo` or from `hi` on
-// and bytes past the end read as zero (`any`: an address of the tensor that copies of
-// no bytes name).  Asynchronous except for 2-byte accesses.
+// shared rows of `srow` bytes, sizeof(U) bytes at a time; rows below `lo` or from `hi` on
+// and bytes past the end read as zero.  A thread keeps its column.  (Asynchronous copies
+// of 4 bytes take the SM 32 cycles a warp: 16500 for a tile of 64 x 128 fp32 values twice,
+// against 3000 this way.)
+template <typename E, typename U>
+__device__ __forceinline__ void load_rows_by(unsigned char* dst, int rows, int srow, const char* src,
+                                             long long pitch, int lo, int hi, int bytes) {
+    const int per = srow / (int)sizeof(U);            // accesses per row, a power of two <= kThreads
+    const int o = (threadIdx.x & (per - 1)) * (int)sizeof(U), step = kThreads / per;
+    const int whole = o + (int)sizeof(U) <= bytes;
+    for (int r = threadIdx.x / per; r < rows; r += 8 * step) {
+        U u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int q = r + k * step;
+            u[k] = U{};
+            if (q >= lo && q < hi && o < bytes) {
+                const char* p = src + q * pitch + o;
+                if (whole) {
+                    u[k] = *reinterpret_cast<const U*>(p);
+                } else {                              // the row ends inside
+#pragma unroll
+                    for (int e = 0; e < (int)(sizeof(U) / sizeof(E)); ++e)
+                        if (o + (e + 1) * (int)sizeof(E) <= bytes)
+                            reinterpret_cast<E*>(&u[k])[e] = reinterpret_cast<const E*>(p)[e];
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (r + k * step < rows) *reinterpret_cast<U*>(dst + (r + k * step) * srow + o) = u[k];
+    }
+}
+template <typename E>
 __device__ __forceinline__ void load_rows(unsigned char* dst, int rows, int srow, const char* src,
-                                          long long pitch, int lo, int hi, int bytes, int width,
-                                          const void* any) {
-    const int shift = 31 - __clz(width);
-    const int per = srow >> shift;                    // accesses per row, a power of two
-    const int log_per = 31 - __clz(per);
-    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    for (int i = threadIdx.x; i < rows << log_per; i += kThreads) {
-        const int r = i >> log_per, o = (i & (per - 1)) << shift;
-        const int n = r >= lo && r < hi ? max(0, min(width, bytes - o)) : 0;
-        const char* p = n ? src + r * pitch + o : static_cast<const char*>(any);
-        if (width == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(base + r * srow + o),
-                         "l"(p), "r"(n) : "memory");
-        else if (width == 8)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(base + r * srow + o),
-                         "l"(p), "r"(n) : "memory");
-        else if (width == 4)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(base + r * srow + o),
-                         "l"(p), "r"(n) : "memory");
-        else
-            *reinterpret_cast<unsigned short*>(dst + r * srow + o) =
-                n ? *reinterpret_cast<const unsigned short*>(p) : (unsigned short)0;
-    }
+                                          long long pitch, int lo, int hi, int bytes, int width) {
+    if (width == 8) load_rows_by<E, uint2>(dst, rows, srow, src, pitch, lo, hi, bytes);
+    else if (width == 4) load_rows_by<E, uint32_t>(dst, rows, srow, src, pitch, lo, hi, bytes);
+    else load_rows_by<E, unsigned short>(dst, rows, srow, src, pitch, lo, hi, bytes);
 }
 
-__device__ __forceinline__ void load_wait() {
-    asm volatile("cp.async.wait_all;" ::: "memory");
+// Shared rows back to global memory where a row does not start on 16 bytes:
+// neighbouring threads write neighbouring values.
+template <typename U>
+__device__ __forceinline__ void store_rows_by(char* dst, long long pitch, const unsigned char* src,
+                                              int rows, int srow, int bytes) {
+    const int per = srow / (int)sizeof(U), o = (threadIdx.x & (per - 1)) * (int)sizeof(U);
+    if (o >= bytes) return;
+#pragma unroll 8
+    for (int r = threadIdx.x / per; r < rows; r += kThreads / per)
+        *reinterpret_cast<U*>(dst + r * pitch + o) = *reinterpret_cast<const U*>(src + r * srow + o);
 }
-
-// Shared rows back to global memory where a row does not start on four values'
-// bytes: neighbouring threads write neighbouring values.
-__device__ __forceinline__ void store_rows(char* dst, long long pitch, const unsigned char* src,
-                                           int rows, int srow, int bytes, int width) {
-    const int shift = width == 4 ? 2 : 1;
-    const int per = srow >> shift, log_per = 31 - __clz(per);
-    for (int i = threadIdx.x; i < rows << log_per; i += kThreads) {
-        const int r = i >> log_per, o = (i & (per - 1)) << shift;
-        if (o >= bytes) continue;
-        if (width == 4)
-            *reinterpret_cast<uint32_t*>(dst + r * pitch + o) =
-                *reinterpret_cast<const uint32_t*>(src + r * srow + o);
-        else
-            *reinterpret_cast<unsigned short*>(dst + r * pitch + o) =
-                *reinterpret_cast<const unsigned short*>(src + r * srow + o);
-    }
+__device__ __forceinline__ void store_rows(char* dst, long long pitch, const unsigned char* src, int rows,
+                                           int srow, int bytes, int width) {
+    if (width == 8) store_rows_by<uint2>(dst, pitch, src, rows, srow, bytes);
+    else if (width == 4) store_rows_by<uint32_t>(dst, pitch, src, rows, srow, bytes);
+    else store_rows_by<unsigned short>(dst, pitch, src, rows, srow, bytes);
 }
 
 // ------------------------------------------------------------------- look-back
@@ -165,7 +205,8 @@ struct TilePlan {
     unsigned long long* maps;   // [strip][tile][channel] in processing order: A low, H high word
     unsigned* ends;        // [strip][tile][channel]: state after the tile
     size_t words_bytes;    // of the counter, maps and ends, all set to kEmpty before
-    int tma;               // inputs by tensor copies
+    unsigned tiles;        // of all strips
+    int tma, tma_out;      // inputs, outputs by tensor copies
     int width_x, width_g, width_o;   // else: access widths of x / dh, g; the contiguous tensors
     float* dg_part;        // token gate over several strips: [ncols][N T] partial sums
 };
@@ -280,247 +321,302 @@ __device__ __forceinline__ float look_back(const unsigned long long* maps, const
 
 // ------------------------------------------------------------------ tile kernel
 
+// Persistent, two blocks an SM.  A block takes a tile from shared memory into registers, so
+// that the next tile's copies run while it looks back and writes this one's results.
 template <typename E, bool kToken, bool kBack>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 2)
     glr_tile_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
-                    const __grid_constant__ CUtensorMap mh, GlrArgs a, TilePlan p) {
-    constexpr int R = kRun<E>;
+                    const __grid_constant__ CUtensorMap mh, const __grid_constant__ CUtensorMap mo,
+                    const __grid_constant__ CUtensorMap mog, const __grid_constant__ GlrArgs a,
+                    const __grid_constant__ TilePlan p) {
+    constexpr int R = kRun<E, kBack>;
+    constexpr int kIns = 1 + (kToken ? 0 : 1) + (kBack ? 1 : 0);
+    constexpr uint32_t kBytes = kTileBytes<E, kBack>;
     extern __shared__ __align__(128) unsigned char smem[];
-    constexpr int kTiles = 1 + (kToken ? 0 : 1) + (kBack ? 1 : 0);
     unsigned char* sx = smem;                                        // x or dh
-    unsigned char* sg = smem + (kToken ? 0 : kTileBytes<E>);         // g (gate per channel)
-    unsigned char* sh = smem + (kTiles - 1) * kTileBytes<E>;         // gradient: h one token earlier
-    Joints& J = *reinterpret_cast<Joints*>(smem + kTiles * kTileBytes<E>);
+    unsigned char* sg = smem + (kToken ? 0 : kBytes);                // g (gate per channel)
+    unsigned char* sh = smem + (kIns - 1) * kBytes;                  // gradient: h one token earlier
+    unsigned char* so = smem + kIns * kBytes;                        // h or dx
+    unsigned char* sog = so + kBytes;                                // gradient: dg (gate per channel)
+    Joints& J = *reinterpret_cast<Joints*>(so + (kBack && !kToken ? 2 : 1) * kBytes);
+    uint64_t* arrived = reinterpret_cast<uint64_t*>(&J.arrived);
 
     const int tid = threadIdx.x, warp = tid >> 5;
-    uint64_t* arrived = reinterpret_cast<uint64_t*>(&J.arrived);
-    // Which tile: in order of the counter (it starts at kEmpty = -1), all strips of tile 0 first
-    unsigned ticket = blockIdx.x;
-    if (tid == 0) {
-        if (p.tma) {
-            tc::mbar_init(arrived, 1);
-            tc::fence_mbar_init();
-        }
-        if (p.counter) J.ticket = atomicAdd(p.counter, 1u) + 1u;
-    }
-    __syncthreads();
-    if (p.counter) ticket = J.ticket;
+    const int chans = V << p.cw_log, srow = chans * (int)sizeof(E);  // a strip's channels, their bytes
     const unsigned strips = (unsigned)a.N * p.ncols;
-    const int j = ticket / strips;                    // place in processing order
-    const unsigned strip = ticket % strips;
-    const size_t n = strip / p.ncols;
-    const int chans = V << p.cw_log, c0 = (strip % p.ncols) * chans;
-    const int tile = kBack ? p.ntiles - 1 - j : j;
-    const int t0 = tile * p.tokens;
-    const int ntok = min(p.tokens, a.T - t0);
-    const int srow = chans * (int)sizeof(E);          // bytes of a shared row
-    const int bytes = min(chans, a.D - c0) * (int)sizeof(E);
-
-    const size_t row0 = n * a.T + t0;                 // row of the contiguous tensors
-    if (p.tma) {
-        // gradient: row r of sh holds h of token t0 + r - 1; token -1 is h0, taken below
-        if (tid == 0) {
-            tc::mbar_expect_tx(arrived, kTiles * kTileBytes<E>);
-            const int box = min(p.tokens, 256);
-            for (int r = 0; r < p.tokens; r += box) {
-                tc::tma_load_3d(sx + r * srow, &mx, arrived, c0, t0 + r, (int)n);
-                if (!kToken) tc::tma_load_3d(sg + r * srow, &mg, arrived, c0, t0 + r, (int)n);
-                if (kBack) tc::tma_load_3d(sh + r * srow, &mh, arrived, c0, t0 + r - 1, (int)n);
-            }
-        }
-    } else {
-        load_rows(sx, p.tokens, srow,
-                  reinterpret_cast<const char*>(static_cast<const E*>(a.x) + n * a.x_seq +
-                                                (long long)t0 * a.x_tok + c0),
-                  a.x_tok * (long long)sizeof(E), 0, ntok, bytes, p.width_x, a.x);
-        if (!kToken)
-            load_rows(sg, p.tokens, srow,
-                      reinterpret_cast<const char*>(static_cast<const E*>(a.g) + n * a.g_seq +
-                                                    (long long)t0 * a.g_tok + c0),
-                      a.g_tok * (long long)sizeof(E), 0, ntok, bytes, p.width_g, a.g);
-        if (kBack)
-            load_rows(sh, p.tokens, srow,
-                      reinterpret_cast<const char*>(static_cast<const E*>(a.h) + c0) +
-                          ((long long)row0 - 1) * a.D * (long long)sizeof(E),
-                      (long long)a.D * sizeof(E), t0 == 0 ? 1 : 0, ntok, bytes, p.width_o, a.h);
-    }
-
-    // This thread's channels and run of tokens, in processing order
+    // this thread's channels and run of tokens, in processing order
     const int cw = 1 << p.cw_log, ch = (tid & (cw - 1)) * V;
     const int place = tid >> p.cw_log, runs = kThreads >> p.cw_log;
     const int r0 = (kBack ? runs - 1 - place : place) * R;
-    const bool live = c0 + ch < a.D;
-    const float* gt = static_cast<const float*>(a.g) + n * a.g_seq + (long long)t0 * a.g_tok;
-    if (p.tma) {
-        const long long since = clock64();
-        while (!tc::mbar_try_wait(arrived, 0))
-            if (clock64() - since > a.wait_cycles) {
-                atomicExch(a.status, TTM_ERR_TIMEOUT);
-                break;
-            }
-    } else {
-        load_wait();
-        __syncthreads();
-    }
+    const int own = r0 * chans + ch;                  // its first value of a tile
+    const int swarps = (chans + 31) / 32;             // warps with a lane per channel
 
-    const int so = r0 * chans + ch;                   // this thread's first value of a tile
-    const E *tx = reinterpret_cast<const E*>(sx) + so, *tg = reinterpret_cast<const E*>(sg) + so;
-    float A[V], H[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) { A[v] = 1.f; H[v] = 0.f; }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int q = kBack ? R - 1 - i : i;
-        float x[V], g[V];
-        get4(tx + q * chans, x);
-        if (!kToken) get4(tg + q * chans, g);
-        const float rt = kToken && r0 + q < ntok ? retention(gt[(long long)(r0 + q) * a.g_tok]) : 1.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float r = kToken ? rt : retention(g[v]);
-            H[v] = kBack ? r * (H[v] + x[v]) : fmaf(r, H[v], x[v]);
-            A[v] *= r;
+    // Tiles in order, all strips of the first one first: from the counter (it starts at
+    // kEmpty = -1), or, where no tile waits for another, every gridDim-th
+    auto request = [&](unsigned ticket) {             // thread 0: the tile's tensor copies
+        const unsigned strip = ticket % strips;
+        const int j = ticket / strips, n = strip / p.ncols, c0 = (strip % p.ncols) * chans;
+        const int t0 = (kBack ? p.ntiles - 1 - j : j) * p.tokens;
+        tc::mbar_expect_tx(arrived, kIns * kBytes);
+        const int box = min(p.tokens, 256);
+        for (int r = 0; r < p.tokens; r += box) {
+            tc::tma_load_3d(sx + r * srow, &mx, arrived, c0, t0 + r, n);
+            if (!kToken) tc::tma_load_3d(sg + r * srow, &mg, arrived, c0, t0 + r, n);
+            // row r of sh holds h of token t0 + r - 1; token -1 is h0, taken below
+            if (kBack) tc::tma_load_3d(sh + r * srow, &mh, arrived, c0, t0 + r - 1, n);
         }
-    }
-
-    // Join over the runs of a warp (inclusive), then over the warps
-    for (int d = cw; d < 32; d <<= 1) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float pa = __shfl_up_sync(0xffffffffu, A[v], d);
-            const float ph = __shfl_up_sync(0xffffffffu, H[v], d);
-            if ((tid & 31) >= d) {
-                H[v] = apply(A[v], H[v], ph);
-                A[v] *= pa;
-            }
+    };
+    if (tid == 0) {
+        J.ticket = p.counter ? atomicAdd(p.counter, 1u) + 1u : blockIdx.x;
+        if (p.tma) {
+            tc::mbar_init(arrived, 1);
+            tc::fence_mbar_init();
+            if (J.ticket < p.tiles) request(J.ticket);
         }
-    }
-    if ((tid & 31) >= 32 - cw) {
-        put4(&J.a[warp][ch], A);
-        put4(&J.h[warp][ch], H);
-    }
-    if (cw < 32) {   // exclusive of this thread's own run
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            A[v] = __shfl_up_sync(0xffffffffu, A[v], cw);
-            H[v] = __shfl_up_sync(0xffffffffu, H[v], cw);
-        }
-    }
-    if ((tid & 31) < cw) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) { A[v] = 1.f; H[v] = 0.f; }
     }
     __syncthreads();
 
-    // A lane per channel: publish the tile's map, look back, publish the state after it.
-    // Every state after a tile is that tile's map applied to the state before, wherever
-    // the look-back started, so equal inputs give equal bits.
-    const int swarps = (chans + 31) / 32;             // warps with a lane per channel
-    if (warp < swarps) {
-        const bool mine = tid < chans;
-        float before = 0.f;
-        if (j == 0) {
-            const float* init = kBack ? a.dh_last : a.h0;
-            if (init && mine && c0 + tid < a.D) before = init[n * a.D + c0 + tid];
+    unsigned phase = 0;
+    for (unsigned ticket = J.ticket; ticket < p.tiles; ticket = J.ticket, phase ^= 1u) {
+        const unsigned strip = ticket % strips;
+        const int j = ticket / strips;                // place in processing order
+        const size_t n = strip / p.ncols;
+        const int c0 = (strip % p.ncols) * chans;
+        const int t0 = (kBack ? p.ntiles - 1 - j : j) * p.tokens;
+        const int ntok = min(p.tokens, a.T - t0);
+        const int bytes = min(chans, a.D - c0) * (int)sizeof(E);
+        const size_t row0 = n * a.T + t0;             // row of the contiguous tensors
+        const bool live = c0 + ch < a.D;
+        unsigned next = 0;
+        if (tid == 0) next = p.counter ? atomicAdd(p.counter, 1u) + 1u : ticket + gridDim.x;
+
+        if (p.tma) {
+            const long long since = clock64();
+            while (!tc::mbar_try_wait(arrived, phase))
+                if (clock64() - since > a.wait_cycles) {
+                    atomicExch(a.status, TTM_ERR_TIMEOUT);
+                    break;
+                }
+        } else {
+            load_rows<E>(sx, p.tokens, srow,
+                         reinterpret_cast<const char*>(static_cast<const E*>(a.x) + n * a.x_seq +
+                                                       (long long)t0 * a.x_tok + c0),
+                         a.x_tok * (long long)sizeof(E), 0, ntok, bytes, p.width_x);
+            if (!kToken)
+                load_rows<E>(sg, p.tokens, srow,
+                             reinterpret_cast<const char*>(static_cast<const E*>(a.g) + n * a.g_seq +
+                                                           (long long)t0 * a.g_tok + c0),
+                             a.g_tok * (long long)sizeof(E), 0, ntok, bytes, p.width_g);
+            if (kBack)
+                load_rows<E>(sh, p.tokens, srow,
+                             reinterpret_cast<const char*>(static_cast<const E*>(a.h) + c0) +
+                                 ((long long)row0 - 1) * a.D * (long long)sizeof(E),
+                             (long long)a.D * sizeof(E), t0 == 0 ? 1 : 0, ntok, bytes, p.width_o);
+            __syncthreads();
         }
-        if (p.counter) {
-            const size_t own = ((size_t)strip * p.ntiles + j) * chans + tid;
-            float mA = 1.f, mH = 0.f;
-            if (mine) {
+        Held<E> hx[R], hg[kToken ? 1 : R], hh[kBack ? R : 1];
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    mH = apply(J.a[w][tid], J.h[w][tid], mH);
-                    mA *= J.a[w][tid];
+        for (int q = 0; q < R; ++q) {
+            hx[q].load(reinterpret_cast<const E*>(sx) + own + q * chans);
+            if (!kToken) hg[q].load(reinterpret_cast<const E*>(sg) + own + q * chans);
+            if (kBack) hh[q].load(reinterpret_cast<const E*>(sh) + own + q * chans);
+        }
+        const float* gt = static_cast<const float*>(a.g) + n * a.g_seq + (long long)t0 * a.g_tok;
+        auto retain = [&](int q, f2 (&r)[2]) {        // of token r0 + q
+            if constexpr (kToken) {
+                r[0] = r[1] =
+                    splat<f2>(r0 + q < ntok ? retention(gt[(long long)(r0 + q) * a.g_tok]) : 1.f);
+            } else {
+                f2 g[2];
+                hg[q].get(g);
+                retention(g, r);
+            }
+        };
+
+        // This run's map
+        float A[V], H[V];
+        {
+            f2 mA[2] = {splat<f2>(1.f), splat<f2>(1.f)}, mH[2] = {splat<f2>(0.f), splat<f2>(0.f)};
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int q = kBack ? R - 1 - i : i;
+                f2 x[2], r[2];
+                hx[q].get(x);
+                retain(q, r);
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    mH[v] = kBack ? mul(r[v], add(mH[v], x[v])) : fma(r[v], mH[v], x[v]);
+                    mA[v] = mul(mA[v], r[v]);
                 }
             }
-            if (mine && j > 0 && j + 1 < p.ntiles) publish_map(p.maps + own, mA, mH);
-            if (j > 0) before = look_back(p.maps + own, p.ends + own, chans, j, mine, a.status, a.wait_cycles);
-            if (mine && j + 1 < p.ntiles) publish_end(p.ends + own, apply(mA, mH, before));
+            split(mA[0], A[0], A[1]);
+            split(mA[1], A[2], A[3]);
+            split(mH[0], H[0], H[1]);
+            split(mH[1], H[2], H[3]);
         }
-        if (mine) J.carry[tid] = before;
-    }
-    __syncthreads();
-
-    // State before this thread's run: the tile's, through the warps before, then the
-    // runs before in this warp
-    float s[V];
-    get4(&J.carry[ch], s);
-    for (int w = 0; w < warp; ++w) {
-        float wa[V], wh[V];
-        get4(&J.a[w][ch], wa);
-        get4(&J.h[w][ch], wh);
 #pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = apply(wa[v], wh[v], s[v]);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = apply(A[v], H[v], s[v]);
+        for (int q = 0; q < R; ++q) {
+            hx[q].repack();
+            if (!kToken) hg[q].repack();
+            if (kBack) hh[q].repack();
+        }
 
-    const bool direct = p.width_o == 4 * sizeof(E);   // rows start on a thread's four values
-    E* out = static_cast<E*>(kBack ? a.dx : a.h) + row0 * a.D + c0 + ch;
-    E* outg = kBack && !kToken ? static_cast<E*>(a.dg) + row0 * a.D + c0 + ch : nullptr;
-    E *wx = reinterpret_cast<E*>(sx) + so, *wh = reinterpret_cast<E*>(sh) + so;
-    float* dg = nullptr;                              // token gate: its gradient, or a strip's share
-    if (kBack && kToken)
-        dg = (p.ncols > 1 ? p.dg_part + (size_t)(strip % p.ncols) * a.N * a.T
-                          : static_cast<float*>(a.dg)) + row0;
-#pragma unroll 4
-    for (int i = 0; i < R; ++i) {
-        const int q = kBack ? R - 1 - i : i, r = r0 + q;
-        float x[V], g[V], o[V];
-        get4(tx + q * chans, x);
-        if (!kToken) get4(tg + q * chans, g);
-        const float rt = kToken && r < ntok ? retention(gt[(long long)r * a.g_tok]) : 1.f;
-        if (!kBack) {
+        // Join over the runs of a warp (inclusive), then over the warps
+        for (int d = cw; d < 32; d <<= 1) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                s[v] = fmaf(kToken ? rt : retention(g[v]), s[v], x[v]);
-                o[v] = s[v];
+                const float pa = __shfl_up_sync(0xffffffffu, A[v], d);
+                const float ph = __shfl_up_sync(0xffffffffu, H[v], d);
+                if ((tid & 31) >= d) {
+                    H[v] = apply(A[v], H[v], ph);
+                    A[v] *= pa;
+                }
+            }
+        }
+        if ((tid & 31) >= 32 - cw) {
+            put4(&J.a[warp][ch], A);
+            put4(&J.h[warp][ch], H);
+        }
+        if (cw < 32) {   // exclusive of this thread's own run
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                A[v] = __shfl_up_sync(0xffffffffu, A[v], cw);
+                H[v] = __shfl_up_sync(0xffffffffu, H[v], cw);
+            }
+        }
+        if ((tid & 31) < cw) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) { A[v] = 1.f; H[v] = 0.f; }
+        }
+        __syncthreads();                              // maps written, the tile is in registers
+
+        if (tid == 0) {
+            J.ticket = next;
+            if (p.tma && next < p.tiles) request(next);
+        }
+        // A lane per channel: publish the tile's map, look back, publish the state after it.
+        // Every state after a tile is that tile's map applied to the state before, wherever
+        // the look-back started, so equal inputs give equal bits.
+        if (warp < swarps) {
+            const bool mine = tid < chans;
+            float before = 0.f;
+            if (j == 0) {
+                const float* init = kBack ? a.dh_last : a.h0;
+                if (init && mine && c0 + tid < a.D) before = init[n * a.D + c0 + tid];
+            }
+            if (p.counter) {
+                const size_t word = ((size_t)strip * p.ntiles + j) * chans + tid;
+                float mA = 1.f, mH = 0.f;
+                if (mine) {
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        mH = apply(J.a[w][tid], J.h[w][tid], mH);
+                        mA *= J.a[w][tid];
+                    }
+                }
+                if (mine && j > 0 && j + 1 < p.ntiles) publish_map(p.maps + word, mA, mH);
+                if (j > 0) before = look_back(p.maps + word, p.ends + word, chans, j, mine, a.status, a.wait_cycles);
+                if (mine && j + 1 < p.ntiles) publish_end(p.ends + word, apply(mA, mH, before));
+            }
+            if (mine) J.carry[tid] = before;
+        }
+        if (p.tma_out && tid == 0) tc::bulk_wait_read<0>();   // the results before have left
+        __syncthreads();
+
+        // State before this thread's run: the tile's, through the warps before, then the
+        // runs before in this warp
+        f2 s[2];
+        {
+            float f[V];
+            get4(&J.carry[ch], f);
+            for (int w = 0; w < warp; ++w) {
+                float wa[V], wh[V];
+                get4(&J.a[w][ch], wa);
+                get4(&J.h[w][ch], wh);
+#pragma unroll
+                for (int v = 0; v < V; ++v) f[v] = apply(wa[v], wh[v], f[v]);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = apply(A[v], H[v], f[v]);
+            s[0] = pair(f[0], f[1]);
+            s[1] = pair(f[2], f[3]);
+        }
+        float* dg = nullptr;                          // token gate: its gradient, or a strip's share
+        if (kBack && kToken)
+            dg = (p.ncols > 1 ? p.dg_part + (size_t)(strip % p.ncols) * a.N * a.T
+                              : static_cast<float*>(a.dg)) + row0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int q = kBack ? R - 1 - i : i;
+            f2 x[2], r[2], o[2];
+            hx[q].get(x);
+            retain(q, r);
+            if (!kBack) {
+#pragma unroll
+                for (int v = 0; v < 2; ++v) o[v] = s[v] = fma(r[v], s[v], x[v]);
+            } else {
+                f2 b[2];
+                hh[q].get(b);
+                if (q == 0 && t0 + r0 == 0 && a.h0 && live) {
+                    float f[V];
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        f[v] = c0 + ch + v < a.D ? a.h0[n * a.D + c0 + ch + v] : 0.f;
+                    b[0] = pair(f[0], f[1]);
+                    b[1] = pair(f[2], f[3]);
+                }
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    o[v] = add(x[v], s[v]);
+                    s[v] = mul(r[v], o[v]);
+                    b[v] = mul(b[v], s[v]);
+                }
+                if (kToken) {   // over the cw threads of the strip's channels, lanes of one warp
+                    float acc = total(add(b[0], b[1]));
+                    for (int d = cw >> 1; d; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
+                    if (ch == 0 && r0 + q < ntok) dg[r0 + q] = acc;
+                } else {
+                    Held<E> w;
+                    w.set(b);
+                    w.store(reinterpret_cast<E*>(sog) + own + q * chans);
+                }
+            }
+            Held<E> w;
+            w.set(o);
+            w.store(reinterpret_cast<E*>(so) + own + q * chans);
+        }
+
+        // End of the strip: the tokens past T leave the state as it is
+        float* end = kBack ? a.dh0 : a.h_last;
+        if (j == p.ntiles - 1 && place == runs - 1 && end) {
+            float f[V];
+            split(s[0], f[0], f[1]);
+            split(s[1], f[2], f[3]);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (c0 + ch + v < a.D) end[n * a.D + c0 + ch + v] = f[v];
+        }
+        if (p.tma_out) tc::fence_proxy_async_smem();
+        __syncthreads();
+        if (p.tma_out) {
+            if (tid == 0) {
+                const int box = min(p.tokens, 256);
+                for (int r = 0; r < ntok; r += box) {
+                    tc::tma_store_3d(&mo, so + r * srow, c0, t0 + r, (int)n);
+                    if (kBack && !kToken) tc::tma_store_3d(&mog, sog + r * srow, c0, t0 + r, (int)n);
+                }
+                tc::bulk_commit();
             }
         } else {
-            float b[V];
-            get4(wh + q * chans, b);
-            if (t0 + r == 0 && a.h0 && live) {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    b[v] = c0 + ch + v < a.D ? a.h0[n * a.D + c0 + ch + v] : 0.f;
-            }
-            float acc = 0.f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                o[v] = x[v] + s[v];
-                s[v] = (kToken ? rt : retention(g[v])) * o[v];
-                b[v] *= s[v];
-                if (kToken) acc += b[v];
-            }
-            if (kToken) {   // over the cw threads of the strip's channels, lanes of one warp
-                for (int d = cw >> 1; d; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-                if (ch == 0 && r < ntok) dg[r] = acc;
-            } else if (!direct) {
-                put4(wh + q * chans, b);
-            } else if (live && r < ntok) {
-                put4(outg + (size_t)r * a.D, b);
+            char* o = reinterpret_cast<char*>(static_cast<E*>(kBack ? a.dx : a.h) + row0 * a.D + c0);
+            store_rows(o, (long long)a.D * sizeof(E), so, ntok, srow, bytes, p.width_o);
+            if (kBack && !kToken) {
+                o = reinterpret_cast<char*>(static_cast<E*>(a.dg) + row0 * a.D + c0);
+                store_rows(o, (long long)a.D * sizeof(E), sog, ntok, srow, bytes, p.width_o);
             }
         }
-        if (!direct) put4(wx + q * chans, o);
-        else if (live && r < ntok) put4(out + (size_t)r * a.D, o);
     }
-
-    // End of the strip: the tokens past T leave the state as it is
-    float* end = kBack ? a.dh0 : a.h_last;
-    if (j == p.ntiles - 1 && place == runs - 1 && end) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (c0 + ch + v < a.D) end[n * a.D + c0 + ch + v] = s[v];
-    }
-    if (!direct) {
-        __syncthreads();
-        char* o = reinterpret_cast<char*>(static_cast<E*>(kBack ? a.dx : a.h) + row0 * a.D + c0);
-        store_rows(o, (long long)a.D * sizeof(E), sx, ntok, srow, bytes, p.width_o);
-        if (kBack && !kToken) {
-            o = reinterpret_cast<char*>(static_cast<E*>(a.dg) + row0 * a.D + c0);
-            store_rows(o, (long long)a.D * sizeof(E), sh, ntok, srow, bytes, p.width_o);
-        }
-    }
+    if (p.tma_out && tid == 0) tc::bulk_wait_read<0>();       // the block's shared memory goes with it
 }
 
 // dg of a token gate from the strips' partial sums, in the strips' order.
@@ -578,11 +674,14 @@ TilePlan make_plan(const GlrArgs& a, int backward, size_t* bytes) {
     TilePlan p{};
     while (p.cw_log < kMaxLog && (V << p.cw_log) < a.D) ++p.cw_log;
     const int chans = V << p.cw_log;
-    p.tokens = (kThreads >> p.cw_log) * (a.bf16 ? kRun<__nv_bfloat16> : kRun<float>);
+    const int run = backward ? (a.bf16 ? kRun<__nv_bfloat16, true> : kRun<float, true>)
+                             : (a.bf16 ? kRun<__nv_bfloat16, false> : kRun<float, false>);
+    p.tokens = (kThreads >> p.cw_log) * run;
     p.ntiles = (a.T + p.tokens - 1) / p.tokens;
     if (p.ntiles < 1) p.ntiles = 1;
     p.ncols = (a.D + chans - 1) / chans;
     const size_t strips = (size_t)a.N * p.ncols;
+    p.tiles = (unsigned)(strips * p.ntiles);
     size_t off = 0;
     char* w = static_cast<char*>(a.workspace);
     if (p.ntiles > 1) {
@@ -616,8 +715,8 @@ bool tile_map(CUtensorMap* m, const TilePlan& p, const GlrArgs& a, const void* p
 
 template <typename E, bool kToken, bool kBack>
 cudaError_t tile_launch(const GlrArgs& a, TilePlan p, cudaStream_t s) {
-    constexpr int tiles = 1 + (kToken ? 0 : 1) + (kBack ? 1 : 0);
-    constexpr int smem = tiles * kTileBytes<E> + (int)sizeof(Joints);
+    constexpr int tiles = 1 + (kToken ? 0 : 1) + (kBack ? 1 : 0) + (kBack && !kToken ? 2 : 1);
+    constexpr int smem = tiles * kTileBytes<E, kBack> + (int)sizeof(Joints);
     auto kernel = glr_tile_kernel<E, kToken, kBack>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -625,12 +724,15 @@ cudaError_t tile_launch(const GlrArgs& a, TilePlan p, cudaStream_t s) {
         e = cudaMemsetAsync(a.workspace, kEmpty & 0xff, p.words_bytes, s);
         if (e != cudaSuccess) return e;
     }
-    CUtensorMap mx{}, mg{}, mh{};
+    CUtensorMap mx{}, mg{}, mh{}, mo{}, mog{};
     p.tma = ((size_t)V << p.cw_log) * sizeof(E) >= 16 &&
             tile_map<E>(&mx, p, a, a.x, a.x_seq, a.x_tok) &&
             (kToken || tile_map<E>(&mg, p, a, a.g, a.g_seq, a.g_tok)) &&
             (!kBack || tile_map<E>(&mh, p, a, a.h, (long long)a.T * a.D, a.D));
-    kernel<<<(unsigned)((size_t)a.N * p.ncols * p.ntiles), kThreads, smem, s>>>(mx, mg, mh, a, p);
+    p.tma_out = ((size_t)V << p.cw_log) * sizeof(E) >= 16 &&
+                tile_map<E>(&mo, p, a, kBack ? a.dx : a.h, (long long)a.T * a.D, a.D) &&
+                (!kBack || kToken || tile_map<E>(&mog, p, a, a.dg, (long long)a.T * a.D, a.D));
+    kernel<<<min(p.tiles, 2u * 152u), kThreads, smem, s>>>(mx, mg, mh, mo, mog, a, p);
     return cudaGetLastError();
 }
 
@@ -641,10 +743,10 @@ cudaError_t tiles(GlrArgs a, bool back, cudaStream_t s, int* launches) {
     const int es = sizeof(E);
     p.width_x = access_width(a.x, a.N > 1 ? a.x_seq : 0, a.T > 1 ? a.x_tok : 0, es);
     p.width_g = a.gate_token ? 4 : access_width(a.g, a.N > 1 ? a.g_seq : 0, a.T > 1 ? a.g_tok : 0, es);
-    p.width_o = min(access_width(nullptr, 0, a.D, es), V * es);
     const int srow = (V << p.cw_log) * es;
-    p.width_x = min(p.width_x, srow);
-    p.width_g = min(p.width_g, srow);
+    p.width_x = min(p.width_x, min(srow, 8));
+    p.width_g = min(p.width_g, min(srow, 8));
+    p.width_o = min(access_width(nullptr, 0, a.D, es), min(srow, 8));
     if (a.wait_cycles <= 0) a.wait_cycles = kWaitCycles;
     *launches = 1;
     cudaError_t e;

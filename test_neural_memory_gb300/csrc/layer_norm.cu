@@ -24,7 +24,9 @@
 #include <cuda_bf16.h>
 
 #include <cstdint>
+#include <type_traits>
 
+#include "pairs.cuh"
 #include "train_ops.h"
 
 namespace ttm {
@@ -32,7 +34,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBlocks = 152 * 4;     // gradient: blocks, and partial sums per column
 constexpr int kLongThreads = 512;
 
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -40,209 +41,285 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void put(float& o, float v) { o = v; }
 __device__ __forceinline__ void put(__nv_bfloat16& o, float v) { o = __float2bfloat16(v); }
 
+// W neighbouring values as they are stored: whole 32-bit words, or one bf16 value.  Taken as
+// kN items of type T, pairs for W > 1.
 template <typename E, int W>
-struct alignas(sizeof(E) * W) Pack {
-    E v[W];
+struct Pack {
+    using Word = std::conditional_t<sizeof(E) * W == 2, unsigned short, uint32_t>;
+    using T = std::conditional_t<W == 1, float, f2>;
+    static constexpr int kN = W == 1 ? 1 : W / 2, kWords = sizeof(E) * W / sizeof(Word);
+    struct alignas(sizeof(E) * W) Data {
+        Word w[kWords];
+    } d;
+
+    __device__ __forceinline__ void load(const E* p) { d = *reinterpret_cast<const Data*>(p); }
+    __device__ __forceinline__ void store(E* p) const { *reinterpret_cast<Data*>(p) = d; }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) d.w[i] = 0;
+    }
+    // Forgets the unpacked values: they are cheaper to take again than to keep in registers.
+    __device__ __forceinline__ void repack() {
+        if constexpr (sizeof(Word) == 4) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) asm volatile("" : "+r"(d.w[i]));
+        }
+    }
+    __device__ __forceinline__ T get(int i) const {
+        if constexpr (W == 1) {
+            if constexpr (sizeof(E) == 2) return __uint_as_float((uint32_t)d.w[0] << 16);
+            else return __uint_as_float(d.w[0]);
+        } else if constexpr (sizeof(E) == 2) {
+            return pair_of_bf16(d.w[i]);
+        } else {
+            return pair(__uint_as_float(d.w[2 * i]), __uint_as_float(d.w[2 * i + 1]));
+        }
+    }
+    __device__ __forceinline__ void set(int i, T v) {
+        if constexpr (W == 1) {
+            if constexpr (sizeof(E) == 2) d.w[0] = __bfloat16_as_ushort(__float2bfloat16(v));
+            else d.w[0] = __float_as_uint(v);
+        } else if constexpr (sizeof(E) == 2) {
+            d.w[i] = bf16_of_pair(v);
+        } else {
+            float lo, hi;
+            split(v, lo, hi);
+            d.w[2 * i] = __float_as_uint(lo);
+            d.w[2 * i + 1] = __float_as_uint(hi);
+        }
+    }
 };
 
-template <typename E, int W>
-__device__ __forceinline__ Pack<E, W> load_pack(const E* p) {
-    return *reinterpret_cast<const Pack<E, W>*>(p);
-}
-
-// W fp32 values; their address is a multiple of 4 W bytes, at most 16 taken at a time.
-template <int W>
-__device__ __forceinline__ void load_f(const float* p, float (&f)[W], float absent) {
+// W weights (fp32, or `absent` each), 16 bytes at a time.
+template <int W, typename T, int N>
+__device__ __forceinline__ void load_weights(const float* p, T (&f)[N], float absent) {
+    if (!p) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) f[i] = absent;
-    if (!p) return;
-    constexpr int S = W < 4 ? W : 4;
+        for (int i = 0; i < N; ++i) f[i] = splat<T>(absent);
+        return;
+    }
+    if constexpr (W == 1) {
+        f[0] = p[0];
+    } else if constexpr (W == 2) {
+        const float2 q = *reinterpret_cast<const float2*>(p);
+        f[0] = pair(q.x, q.y);
+    } else {
 #pragma unroll
-    for (int i = 0; i < W; i += S) {
-        const Pack<float, S> q = load_pack<float, S>(p + i);
-#pragma unroll
-        for (int j = 0; j < S; ++j) f[i + j] = q.v[j];
+        for (int i = 0; i < N; i += 2) {
+            const float4 q = *reinterpret_cast<const float4*>(p + 2 * i);
+            f[i] = pair(q.x, q.y);
+            f[i + 1] = pair(q.z, q.w);
+        }
     }
 }
 
-// Sums over the TPR threads of a row; TPR = kThreads goes through `buf` (shared,
-// [kWarps][C]), which the caller may use again after the next reduction's barrier.
+// Sums over the TPR threads of a row; TPR = kThreads goes through `buf` (shared), which
+// the caller may use again after the next reduction's barrier.
 template <int TPR, int C>
-__device__ __forceinline__ void row_sums(float (&s)[C], float (*buf)[C]) {
+__device__ __forceinline__ void row_sums(float (&s)[C], float (*buf)[kWarps]) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int o = (TPR < 32 ? TPR : 32) / 2; o; o >>= 1)
             s[c] += __shfl_xor_sync(0xffffffffu, s[c], o);
     if (TPR > 32) {
-        const int warp = threadIdx.x >> 5;
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
-            for (int c = 0; c < C; ++c) buf[warp][c] = s[c];
+            for (int c = 0; c < C; ++c) buf[c][threadIdx.x >> 5] = s[c];
         __syncthreads();
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            s[c] = 0.f;
-#pragma unroll
-            for (int w = 0; w < TPR / 32; ++w) s[c] += buf[w][c];
+            const float4 a = *reinterpret_cast<const float4*>(&buf[c][0]);
+            const float4 b = *reinterpret_cast<const float4*>(&buf[c][4]);
+            s[c] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
         }
     }
 }
 
 template <typename E, int W, int TPR, int K, int ROWS>
-__global__ void __launch_bounds__(kThreads) ln_fwd_kernel(LayerNormArgs a) {
-    constexpr int kSets = kThreads / TPR;             // rows side by side in a block
-    __shared__ float buf[2][kWarps][ROWS];
+__global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const __grid_constant__ LayerNormArgs a) {
+    using P = Pack<E, W>;
+    using T = typename P::T;
+    constexpr int kSets = kThreads / TPR, N = P::kN;  // rows side by side in a block
+    __shared__ __align__(16) float buf[2][ROWS][kWarps];
     const int lane = threadIdx.x % TPR, set = threadIdx.x / TPR;
     const int packs = a.D / W;
     const float inv = 1.f / a.D;
     const E* x = static_cast<const E*>(a.x);
-    E* y = static_cast<E*>(a.y);
-    for (long long r0 = (long long)blockIdx.x * kSets * ROWS; r0 < a.N;
-         r0 += (long long)gridDim.x * kSets * ROWS) {
-        Pack<E, W> in[ROWS][K];
-        float s[ROWS], mean[ROWS];
+    const long long r0 = (long long)blockIdx.x * kSets * ROWS + set;   // rows r0 + i kSets
+    P in[ROWS][K];
+    float s[ROWS], mean[ROWS], rstd[ROWS];
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const long long r = r0 + i * kSets + set;
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (r < a.N && lane + k * TPR < packs)
-                    in[i][k] = load_pack<E, W>(x + r * a.x_row + (lane + k * TPR) * W);
-        }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            s[i] = 0.f;
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (r0 + i * kSets + set < a.N && lane + k * TPR < packs)
-#pragma unroll
-                    for (int v = 0; v < W; ++v) s[i] += to_f(in[i][k].v[v]);
-        }
-        row_sums<TPR>(s, buf[0]);
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            mean[i] = s[i] * inv;
-            s[i] = 0.f;
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (r0 + i * kSets + set < a.N && lane + k * TPR < packs)
-#pragma unroll
-                    for (int v = 0; v < W; ++v) {
-                        const float d = to_f(in[i][k].v[v]) - mean[i];
-                        s[i] = fmaf(d, d, s[i]);
-                    }
-        }
-        row_sums<TPR>(s, buf[1]);
-        float rstd[ROWS];
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) rstd[i] = 1.f / sqrtf(fmaf(s[i], inv, a.eps));
+    for (int i = 0; i < ROWS; ++i)
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (lane + k * TPR) * W;
-            if (lane + k * TPR >= packs) continue;
-            float w[W], b[W];
-            load_f<W>(a.w ? a.w + c : nullptr, w, 1.f);
-            load_f<W>(a.b ? a.b + c : nullptr, b, 0.f);
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                const long long r = r0 + i * kSets + set;
-                if (r >= a.N) continue;
-                Pack<E, W> out;
-#pragma unroll
-                for (int v = 0; v < W; ++v)
-                    put(out.v[v], fmaf((to_f(in[i][k].v[v]) - mean[i]) * rstd[i], w[v], b[v]));
-                *reinterpret_cast<Pack<E, W>*>(y + r * a.D + c) = out;
-            }
+            in[i][k].zero();
+            if (r0 + i * kSets < a.N && lane + k * TPR < packs)
+                in[i][k].load(x + (r0 + i * kSets) * a.x_row + (lane + k * TPR) * W);
         }
-        if (lane == 0)
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                const long long r = r0 + i * kSets + set;
-                if (r >= a.N) continue;
-                if (a.mean) a.mean[r] = mean[i];
-                if (a.rstd) a.rstd[r] = rstd[i];
-            }
+    for (int i = 0; i < ROWS; ++i) {
+        T t = splat<T>(0.f);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) t = add(t, in[i][k].get(j));
+            in[i][k].repack();
+        }
+        s[i] = total(t);
     }
+    row_sums<TPR>(s, buf[0]);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        mean[i] = s[i] * inv;
+        T t = splat<T>(0.f);
+        const T m = splat<T>(-mean[i]);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (lane + k * TPR < packs)
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const T d = add(in[i][k].get(j), m);
+                    t = fma(d, d, t);
+                }
+            in[i][k].repack();
+        }
+        s[i] = total(t);
+    }
+    row_sums<TPR>(s, buf[1]);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) rstd[i] = 1.f / sqrtf(fmaf(s[i], inv, a.eps));
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = (lane + k * TPR) * W;
+        if (lane + k * TPR >= packs) continue;
+        T w[N], b[N];
+        load_weights<W>(a.w ? a.w + c : nullptr, w, 1.f);
+        load_weights<W>(a.b ? a.b + c : nullptr, b, 0.f);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const long long r = r0 + i * kSets;
+            if (r >= a.N) continue;
+            const T m = splat<T>(-mean[i]), q = splat<T>(rstd[i]);
+            P out;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                out.set(j, fma(mul(add(in[i][k].get(j), m), q), w[j], b[j]));
+            out.store(static_cast<E*>(a.y) + r * a.D + c);
+        }
+    }
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const long long r = r0 + i * kSets;
+            if (r >= a.N) continue;
+            if (a.mean) a.mean[r] = mean[i];
+            if (a.rstd) a.rstd[r] = rstd[i];
+        }
 }
 
-template <typename E, int W, int TPR, int K, int ROWS>
-__global__ void __launch_bounds__(kThreads) ln_bwd_kernel(LayerNormArgs a) {
-    constexpr int kSets = kThreads / TPR;
-    __shared__ float buf[2][kWarps][2 * ROWS];
+template <typename E, int W, int TPR, int K, int ROWS, int BLOCKS>
+__global__ void __launch_bounds__(kThreads, BLOCKS) ln_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
+    using P = Pack<E, W>;
+    using T = typename P::T;
+    constexpr int kSets = kThreads / TPR, N = P::kN;
+    __shared__ __align__(16) float buf[2][2 * ROWS][kWarps];
     const int lane = threadIdx.x % TPR, set = threadIdx.x / TPR;
     const int packs = a.D / W;
     const float inv = 1.f / a.D;
     const E *x = static_cast<const E*>(a.x), *dy = static_cast<const E*>(a.dy);
-    E* dx = static_cast<E*>(a.dx);
-    float dw[K][W], db[K][W];
+    T dw[K][N], db[K][N];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int v = 0; v < W; ++v) dw[k][v] = db[k][v] = 0.f;
-    int turn = 0;
-    for (long long r0 = (long long)blockIdx.x * kSets * ROWS; r0 < a.N;
-         r0 += (long long)gridDim.x * kSets * ROWS, turn ^= 1) {
-        Pack<E, W> px[ROWS][K], pd[ROWS][K];
-        float mean[ROWS], rstd[ROWS], s[2 * ROWS];
+        for (int j = 0; j < N; ++j) dw[k][j] = db[k][j] = splat<T>(0.f);
+    // the next rows are asked for before the reduction of these
+    P nx[ROWS][K], nd[ROWS][K];
+    float nmean[ROWS], nrstd[ROWS];
+    auto fetch = [&](long long r0) {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             const long long r = r0 + i * kSets + set;
             const bool in = r < a.N;
-            mean[i] = in ? a.mean[r] : 0.f;
-            rstd[i] = in ? a.rstd[r] : 0.f;
+            nmean[i] = in ? a.mean[r] : 0.f;
+            nrstd[i] = in ? a.rstd[r] : 0.f;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const int c = (lane + k * TPR) * W;
+                nx[i][k].zero();
+                nd[i][k].zero();
                 if (in && lane + k * TPR < packs) {
-                    px[i][k] = load_pack<E, W>(x + r * a.x_row + c);
-                    pd[i][k] = load_pack<E, W>(dy + r * a.dy_row + c);
-                } else {
-#pragma unroll
-                    for (int v = 0; v < W; ++v) {
-                        put(px[i][k].v[v], 0.f);
-                        put(pd[i][k].v[v], 0.f);
-                    }
+                    nx[i][k].load(x + r * a.x_row + c);
+                    nd[i][k].load(dy + r * a.dy_row + c);
                 }
             }
-            s[2 * i] = s[2 * i + 1] = 0.f;
         }
+    };
+    int turn = 0;
+    const long long stride = (long long)gridDim.x * kSets * ROWS;
+    fetch((long long)blockIdx.x * kSets * ROWS);
+    for (long long r0 = (long long)blockIdx.x * kSets * ROWS; r0 < a.N; r0 += stride, turn ^= 1) {
+        P px[ROWS][K], pd[ROWS][K];
+        float mean[ROWS], rstd[ROWS], s[2 * ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            mean[i] = nmean[i];
+            rstd[i] = nrstd[i];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                px[i][k] = nx[i][k];
+                pd[i][k] = nd[i][k];
+            }
+        }
+        fetch(r0 + stride);
+        T su[ROWS], sn[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) su[i] = sn[i] = splat<T>(0.f);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            float w[W];
-            load_f<W>(a.w && lane + k * TPR < packs ? a.w + (lane + k * TPR) * W : nullptr, w, 1.f);
+            T w[N];
+            load_weights<W>(a.w && lane + k * TPR < packs ? a.w + (lane + k * TPR) * W : nullptr, w, 1.f);
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i)
+            for (int i = 0; i < ROWS; ++i) {
+                const T q = splat<T>(rstd[i]), m = splat<T>(-mean[i] * rstd[i]);
 #pragma unroll
-                for (int v = 0; v < W; ++v) {
-                    const float g = to_f(pd[i][k].v[v]);
-                    const float n = (to_f(px[i][k].v[v]) - mean[i]) * rstd[i];
-                    const float u = g * w[v];
-                    db[k][v] += g;                      // absent rows and columns have g = 0
-                    dw[k][v] = fmaf(g, n, dw[k][v]);
-                    s[2 * i] += u;
-                    s[2 * i + 1] = fmaf(u, n, s[2 * i + 1]);
+                for (int j = 0; j < N; ++j) {           // absent rows and columns have dy = 0
+                    const T g = pd[i][k].get(j), n = fma(px[i][k].get(j), q, m), u = mul(g, w[j]);
+                    db[k][j] = add(db[k][j], g);
+                    dw[k][j] = fma(g, n, dw[k][j]);
+                    su[i] = add(su[i], u);
+                    sn[i] = fma(u, n, sn[i]);
                 }
+                px[i][k].repack();
+                pd[i][k].repack();
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            s[2 * i] = total(su[i]);
+            s[2 * i + 1] = total(sn[i]);
         }
         row_sums<TPR>(s, buf[turn]);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (lane + k * TPR) * W;
             if (lane + k * TPR >= packs) continue;
-            float w[W];
-            load_f<W>(a.w ? a.w + c : nullptr, w, 1.f);
+            T w[N];
+            load_weights<W>(a.w ? a.w + c : nullptr, w, 1.f);
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
                 const long long r = r0 + i * kSets + set;
                 if (r >= a.N) continue;
-                const float su = s[2 * i] * inv, sn = s[2 * i + 1] * inv;
-                Pack<E, W> out;
+                // rstd (u - su - n sn) with n = x rstd - mean rstd, in two products
+                const T q = splat<T>(rstd[i]), m = splat<T>(-mean[i] * rstd[i]);
+                const T c0 = splat<T>(-s[2 * i] * inv), c1 = splat<T>(-s[2 * i + 1] * inv);
+                P out;
 #pragma unroll
-                for (int v = 0; v < W; ++v) {
-                    const float n = (to_f(px[i][k].v[v]) - mean[i]) * rstd[i];
-                    put(out.v[v], rstd[i] * (fmaf(to_f(pd[i][k].v[v]), w[v], -su) - n * sn));
+                for (int j = 0; j < N; ++j) {
+                    const T n = fma(px[i][k].get(j), q, m);
+                    out.set(j, mul(q, fma(n, c1, fma(pd[i][k].get(j), w[j], c0))));
                 }
-                *reinterpret_cast<Pack<E, W>*>(dx + r * a.D + c) = out;
+                out.store(static_cast<E*>(a.dx) + r * a.D + c);
             }
         }
     }
@@ -250,43 +327,44 @@ __global__ void __launch_bounds__(kThreads) ln_bwd_kernel(LayerNormArgs a) {
     // over the rows side by side in the block: sets of a warp by shuffles, warps through shared
     // memory (one warp or more per row: the sets are whole warps)
     float* part = a.partial + (size_t)blockIdx.x * 2 * a.D;
-    if (TPR == kThreads) {
+    extern __shared__ float sums[];                     // TPR < kThreads: [kWarps][2][TPR K W]
+    const int cols = TPR * K * W, warp = threadIdx.x >> 5;
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int v = 0; v < W; ++v) {
-                const int c = (lane + k * TPR) * W + v;
-                if (lane + k * TPR < packs) {
-                    part[c] = dw[k][v];
-                    part[a.D + c] = db[k][v];
+        for (int j = 0; j < N; ++j) {
+            float v[2][2];                              // [dw, db][first, second of the item]
+            if constexpr (W == 1) {
+                v[0][0] = dw[k][j];
+                v[1][0] = db[k][j];
+            } else {
+                split(dw[k][j], v[0][0], v[0][1]);
+                split(db[k][j], v[1][0], v[1][1]);
+            }
+#pragma unroll
+            for (int e = 0; e < (W == 1 ? 1 : 2); ++e) {
+                const int c = (lane + k * TPR) * W + 2 * j + e;
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    if (TPR == kThreads) {
+                        if (lane + k * TPR < packs) part[z * a.D + c] = v[z][e];
+                    } else {
+#pragma unroll
+                        for (int o = TPR; o < 32; o <<= 1)
+                            v[z][e] += __shfl_xor_sync(0xffffffffu, v[z][e], o);
+                        if ((threadIdx.x & 31) < TPR) sums[(warp * 2 + z) * cols + c] = v[z][e];
+                    }
                 }
             }
-    } else {
-        extern __shared__ float sums[];                 // [kWarps][2][TPR K W]
-        const int cols = TPR * K * W, warp = threadIdx.x >> 5;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int v = 0; v < W; ++v) {
-#pragma unroll
-                for (int o = TPR; o < 32; o <<= 1) {
-                    dw[k][v] += __shfl_xor_sync(0xffffffffu, dw[k][v], o);
-                    db[k][v] += __shfl_xor_sync(0xffffffffu, db[k][v], o);
-                }
-                if ((threadIdx.x & 31) < TPR) {
-                    const int c = (lane + k * TPR) * W + v;
-                    sums[(warp * 2 + 0) * cols + c] = dw[k][v];
-                    sums[(warp * 2 + 1) * cols + c] = db[k][v];
-                }
-            }
-        __syncthreads();
-        for (int c = threadIdx.x; c < 2 * a.D; c += kThreads) {
-            const int which = c >= a.D, col = c - which * a.D;
-            float t = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) t += sums[(w * 2 + which) * cols + col];
-            part[c] = t;
         }
+    if (TPR == kThreads) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.D; c += kThreads) {
+        const int which = c >= a.D, col = c - which * a.D;
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) t += sums[(w * 2 + which) * cols + col];
+        part[c] = t;
     }
 }
 
@@ -381,22 +459,28 @@ __global__ void __launch_bounds__(512) ln_join_kernel(const float* part, int blo
 
 // ------------------------------------------------------------------------- host
 
+// Gradient: two blocks an SM with two rows each in flight and two more on the way.  At 131072 x
+// 2048 bf16: 284 us; 300 us with one block of four rows, 314 with three of one row, 420 with
+// four (their registers spill).
+constexpr int kResident = 2;
+constexpr int kMaxBlocks = 152 * kResident;
+
 template <typename E, int W, int TPR, int K>
-cudaError_t run(const LayerNormArgs& a, bool back, int blocks_of_rows, cudaStream_t s) {
-    constexpr int sets = kThreads / TPR;
+cudaError_t run(const LayerNormArgs& a, bool back, int blocks, cudaStream_t s) {
+    constexpr int sets = kThreads / TPR, bytes = W * K * (int)sizeof(E);
     if (!back) {
-        constexpr int rows = W * K * (int)sizeof(E) >= 64 ? 1 : (W * K * (int)sizeof(E) >= 32 ? 2 : 4);
+        constexpr int rows = bytes >= 64 ? 1 : (bytes >= 32 ? 2 : 4);   // 64 bytes in flight a thread
         const long long need = ((long long)a.N + sets * rows - 1) / (sets * rows);
-        ln_fwd_kernel<E, W, TPR, K, rows>
-            <<<(unsigned)(need < 152 * 16 ? need : 152 * 16), kThreads, 0, s>>>(a);
+        ln_fwd_kernel<E, W, TPR, K, rows><<<(unsigned)need, kThreads, 0, s>>>(a);
     } else {
-        constexpr int rows = W * K * (int)sizeof(E) >= 32 ? 1 : 2;
+        constexpr int rows = bytes > 32 ? 1 : 2;
+        constexpr int resident = K * W <= 16 ? kResident : 1;
         const size_t shared = TPR == kThreads || !a.partial ? 0 : (size_t)kWarps * 2 * TPR * K * W * 4;
-        auto kernel = ln_bwd_kernel<E, W, TPR, K, rows>;
+        auto kernel = ln_bwd_kernel<E, W, TPR, K, rows, resident>;
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) return e;
-        kernel<<<blocks_of_rows, kThreads, shared, s>>>(a);
+        kernel<<<blocks, kThreads, shared, s>>>(a);
     }
     return cudaGetLastError();
 }

@@ -58,6 +58,17 @@ __device__ __forceinline__ float inverse_norm(float sum_of_squares, float eps) {
     return norm <= eps ? 1.f / eps : 1.f / norm;
 }
 
+__device__ __forceinline__ float4 load4(const OrthoArgs& a, size_t i) {
+    if (!a.bf16) return *reinterpret_cast<const float4*>(static_cast<const float*>(a.G) + i);
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.G) + i);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ float load1(const OrthoArgs& a, size_t i) {
+    return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.G)[i])
+                  : static_cast<const float*>(a.G)[i];
+}
+
 // Bounded wait.  A wait that runs out sets the block's abort flag (every role then
 // stops) and the device status word.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abort, int* status,
@@ -116,7 +127,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
     unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     unsigned char *sx = base, *sa = base + kOperandBytes;
     SmallShared& S = *reinterpret_cast<SmallShared*>(base + 2 * kOperandBytes);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const bool wide = a.m <= a.n;
     const int r = wide ? a.m : a.n, l = wide ? a.n : a.m;
     const int rp = r <= 64 ? 64 : 128, lp = l <= 64 ? 64 : 128;
@@ -130,20 +141,43 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
         S.abort = 0;
     }
 
-    // X_0: row of the short side, columns of the long one
+    // X_0: row of the short side, columns of the long one.  A wide G is read along its rows
+    // into shared memory (fp32 rows of 512 bytes over both operands, 16-byte groups
+    // permuted by row) and taken from there by row; a tall one's columns are already what
+    // neighbouring lanes want.
     float X[64];
+    if (wide) {
+        auto at = [&](int i, int j) {
+            return reinterpret_cast<float*>(base + i * 512 + (((j >> 2) ^ (i & 7)) << 4) + (j & 3) * 4);
+        };
+        if (a.n % 4 == 0) {
+            const int per = a.n / 4;
+#pragma unroll 4
+            for (int i = tid; i < a.m * per; i += kSmallThreads)
+                *reinterpret_cast<float4*>(at(i / per, i % per * 4)) = load4(a, mat + (size_t)i * 4);
+        } else {
+#pragma unroll 4
+            for (int i = tid; i < a.m * a.n; i += kSmallThreads) *at(i / a.n, i % a.n) = load1(a, mat + i);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(at(row, half * 64 + c));
+            const float f[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) X[c + e] = row < r && half * 64 + c + e < l ? f[e] : 0.f;
+        }
+        __syncthreads();                                // before the operands take its place
+    } else {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+            const int col = half * 64 + c;
+            X[c] = row < r && col < l ? load1(a, mat + (size_t)col * a.n + row) : 0.f;
+        }
+    }
     float s = 0.f;
 #pragma unroll
-    for (int c = 0; c < 64; ++c) {
-        const int col = half * 64 + c;
-        X[c] = 0.f;
-        if (row < r && col < l) {
-            const size_t i = mat + (wide ? (size_t)row * a.n + col : (size_t)col * a.n + row);
-            X[c] = a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.G)[i])
-                          : static_cast<const float*>(a.G)[i];
-        }
-        s = fmaf(X[c], X[c], s);
-    }
+    for (int c = 0; c < 64; ++c) s = fmaf(X[c], X[c], s);
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) S.part[warp] = s;
     tc_fence_before();
@@ -183,9 +217,11 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
         if (warp == 0) {                                // A = X X^T
             if (elect_one()) {
                 const uint32_t id = idesc_f16(128, rp, 0, 0);
-                for (int k = 0; k < lp / 16; ++k) {
-                    const uint64_t d = sdesc(xb + (k >> 2) * kHalfBytes + (k & 3) * 32, 16, 1024, 2);
-                    mma_bf16(tmem, d, d, id, k > 0);
+                const uint64_t d0 = sdesc(xb, 16, 1024, 2);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint64_t d = d0 + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4);
+                    if (k * 16 < lp) mma_bf16(tmem, d, d, id, k > 0);
                 }
                 mma_commit(&S.done);
             }
@@ -214,9 +250,11 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
         if (warp == 0) {                                // A A (A is symmetric)
             if (elect_one()) {
                 const uint32_t id = idesc_f16(128, rp, 0, 0);
-                for (int k = 0; k < rp / 16; ++k) {
-                    const uint64_t d = sdesc(ab + (k >> 2) * kHalfBytes + (k & 3) * 32, 16, 1024, 2);
-                    mma_bf16(tmem, d, d, id, k > 0);
+                const uint64_t d0 = sdesc(ab, 16, 1024, 2);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint64_t d = d0 + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4);
+                    if (k * 16 < rp) mma_bf16(tmem, d, d, id, k > 0);
                 }
                 mma_commit(&S.done);
             }
@@ -248,9 +286,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
         if (warp == 0) {                                // B X, X as [k][n]
             if (elect_one()) {
                 const uint32_t id = idesc_f16(128, lp, 0, 1);
-                for (int k = 0; k < rp / 16; ++k)
-                    mma_bf16(tmem, sdesc(ab + (k >> 2) * kHalfBytes + (k & 3) * 32, 16, 1024, 2),
-                             sdesc(xb + k * 2048, kHalfBytes, 1024, 2), id, k > 0);
+                const uint64_t d0 = sdesc(ab, 16, 1024, 2), e0 = sdesc(xb, kHalfBytes, 1024, 2);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k * 16 < rp)
+                        mma_bf16(tmem, d0 + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4),
+                                 e0 + (k * 2048 >> 4), id, k > 0);
                 mma_commit(&S.done);
             }
             __syncwarp();
@@ -317,17 +358,6 @@ __device__ __forceinline__ float block_sum(float s) {
     s = 0.f;
     for (int w = 0; w < 8; ++w) s += buf[w];
     return s;
-}
-
-__device__ __forceinline__ float4 load4(const OrthoArgs& a, size_t i) {
-    if (!a.bf16) return *reinterpret_cast<const float4*>(static_cast<const float*>(a.G) + i);
-    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.G) + i);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
-__device__ __forceinline__ float load1(const OrthoArgs& a, size_t i) {
-    return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.G)[i])
-                  : static_cast<const float*>(a.G)[i];
 }
 
 __global__ void __launch_bounds__(256) ns_norm_kernel(const __grid_constant__ OrthoArgs a, float* part) {
