@@ -16,10 +16,8 @@
 // tile from the blocks of the tiles before, and writes the outputs in a second pass.
 //
 // Tile: 256 threads, each 4 channels times R consecutive tokens, CW threads side by
-// side over the channels and 256 / CW over the tokens.  CW is the smallest power of
-// two that covers D, at most 32 (128 channels).  Then a warp holds one run of tokens
-// and only the eight warps' maps are joined, through shared memory; narrower strips
-// join by shuffles inside a warp first.
+// side over a strip of channels and 256 / CW over the tokens (make_plan chooses CW).
+// The runs of a warp are joined by shuffles, the eight warps' through shared memory.
 //
 // Between tiles (look-back), a lane per channel: a warp publishes its channels' map of
 // the tile as soon as it has it, finds the nearest tile before whose end state is known,
@@ -28,8 +26,7 @@
 // far back a warp had to start: the result does not depend on timing.  A map is one
 // 64-bit word and an end state one 32-bit word per channel, each its own flag (a bit
 // pattern that the values never take marks an empty word), so neither side needs a
-// fence: with flags of their own and release / acquire the two publications took 6600
-// of a tile's 23700 cycles, and the look-back two round trips instead of one.
+// fence: with release / acquire the two publications took 6600 of a tile's 23700 cycles.
 // Tiles are handed out in order by a counter, so a block only ever waits for blocks
 // that are already running.  The waits are bounded: one that runs out sets the
 // device status word and the call's outputs are invalid.
@@ -49,9 +46,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int V = 4;                          // channels of a thread
-constexpr int kMaxLog = 5;                    // at most 32 threads over the channels
+constexpr int kMaxLog = 4;                        // at most 16 threads over the channels
 constexpr int kChans = V << kMaxLog;          // channels of a full strip
-constexpr int kBatch = 8;                     // tiles a look-back reads at a time
+constexpr int kNear = 4, kBatch = 8;              // tiles a look-back takes with the hints; maps then
 constexpr long long kWaitCycles = 4000000000LL;   // default limit, ~2 s at 2 GHz
 
 // R, the tokens of one thread in a tile: what it holds of them in registers is 64 of those
@@ -204,7 +201,8 @@ struct TilePlan {
     unsigned* counter;     // hands out tiles in order; NULL when ntiles == 1
     unsigned long long* maps;   // [strip][tile][channel] in processing order: A low, H high word
     unsigned* ends;        // [strip][tile][channel]: state after the tile
-    size_t words_bytes;    // of the counter, maps and ends, all set to kEmpty before
+    unsigned* hints;       // [strip][32 channels][tile]: kMapThere, kEndThere
+    size_t words_bytes;    // of the counter, maps, ends and hints, all set to kEmpty before
     unsigned tiles;        // of all strips
     int tma, tma_out;      // inputs, outputs by tensor copies
     int width_x, width_g, width_o;   // else: access widths of x / dh, g; the contiguous tensors
@@ -212,6 +210,7 @@ struct TilePlan {
 };
 
 constexpr unsigned kEmpty = 0xffffffffu;   // as a float a NaN that full() never lets through
+constexpr unsigned kMapThere = 1, kEndThere = 2;
 
 __device__ __forceinline__ unsigned full(float v) {
     const unsigned u = __float_as_uint(v);
@@ -226,6 +225,9 @@ __device__ __forceinline__ unsigned long long load_word(const unsigned long long
     unsigned long long v;
     asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
     return v;
+}
+__device__ __forceinline__ void store_word(unsigned* p, unsigned v) {
+    asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 __device__ __forceinline__ void publish_end(unsigned* p, float v) {
     asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(full(v)) : "memory");
@@ -249,74 +251,79 @@ struct Joints {
 };
 
 // One warp, a lane per channel (mine: the lane has one): the state before tile j > 0.
-// maps and ends point to this lane's channel of tile j; tiles are `chans` words apart.
-__device__ __forceinline__ float look_back(const unsigned long long* maps, const unsigned* ends,
-                                           int chans, int j, bool mine, int* status,
+// maps and ends point to this lane's channel of tile j, `chans` words a tile; hints to
+// the warp's word of tile j.  The words of the nearest four tiles come in the same round
+// trip as the hints, which say in one load where the nearest end state of the 32 tiles
+// before is and that the maps in between are out; they are not ordered with the words
+// themselves, each of which is looked at until it is there.
+__device__ __forceinline__ float look_back(const unsigned* hints, const unsigned long long* maps,
+                                           const unsigned* ends, int chans, int j, bool mine, int* status,
                                            long long limit) {
+    const int lane = threadIdx.x & 31;
     const long long t0 = clock64();
+    auto late = [&]() {
+        if (!__any_sync(0xffffffffu, clock64() - t0 > limit)) return false;
+        if (lane == 0) atomicExch(status, TTM_ERR_TIMEOUT);
+        return true;
+    };
+    int back;                                         // distance of the end state
     while (true) {
-        // the nearest kBatch tiles: end states and maps in one round trip
-        unsigned long long m[kBatch];
-        unsigned e[kBatch];
+        const unsigned f = lane < j ? load_word(hints - 1 - lane) : kMapThere;
+        unsigned ne[kNear];
+        unsigned long long nm[kNear];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
+        for (int u = 0; u < kNear; ++u) {
             const bool in = mine && u < j;
-            m[u] = in ? load_word(maps - (long long)(u + 1) * chans) : 0ull;
-            e[u] = in ? load_word(ends - (long long)(u + 1) * chans) : (u < j ? 0u : kEmpty);
+            ne[u] = in ? load_word(ends - (long long)(u + 1) * chans) : (u < j ? 0u : kEmpty);
+            nm[u] = in ? load_word(maps - (long long)(u + 1) * chans) : 0ull;
         }
-        int back = 0;                 // nearest end state, if every map nearer is there
-        bool open = true;
+        bool open = true;                             // every map nearer than u is there
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (open && !back && __all_sync(0xffffffffu, e[u] != kEmpty)) back = u + 1;
-            open = open && __all_sync(0xffffffffu, has_map(m[u]));
-        }
-        float s = 0.f;
-        if (!back && open && j > kBatch) {
-            // farther: the nearest end state, then forward again through the maps
-            int far = 0;
-            for (int d = kBatch; d < j && !far; d += kBatch) {
-                unsigned f[kBatch];
+        for (int u = 0; u < kNear; ++u) {
+            if (open && __all_sync(0xffffffffu, ne[u] != kEmpty)) {
+                float s = __uint_as_float(ne[u]);
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u)
-                    f[u] = mine && d + u < j ? load_word(ends - (long long)(d + u + 1) * chans)
-                                             : (d + u < j ? 0u : kEmpty);
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u)
-                    if (!far && __all_sync(0xffffffffu, f[u] != kEmpty)) {
-                        far = d + u + 1;
-                        s = __uint_as_float(f[u]);
-                    }
+                for (int w = kNear - 1; w >= 0; --w)
+                    if (w < u) s = apply_map(nm[w], s);
+                return s;
             }
-            bool there = far != 0;
-            for (int d = far - 1; there && d > kBatch; d -= kBatch) {
-                unsigned long long f[kBatch];
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u)
-                    f[u] = mine && d - u > kBatch ? load_word(maps - (long long)(d - u) * chans) : 0ull;
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    there = there && __all_sync(0xffffffffu, has_map(f[u]));
-                    if (d - u > kBatch) s = apply_map(f[u], s);
-                }
-            }
-            if (there) back = kBatch + 1;
-        } else if (back) {
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (u + 1 == back) s = __uint_as_float(e[u]);
+            open = open && __all_sync(0xffffffffu, has_map(nm[u]));
         }
-        if (back) {
-#pragma unroll
-            for (int u = kBatch; u-- > 0;)
-                if (u + 1 < back) s = apply_map(m[u], s);
-            return s;
-        }
-        if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
-            if ((threadIdx.x & 31) == 0) atomicExch(status, TTM_ERR_TIMEOUT);
-            return 0.f;
-        }
+        const unsigned out = __ballot_sync(0xffffffffu, f != kEmpty);
+        const unsigned end = __ballot_sync(0xffffffffu, f == kEndThere);
+        back = __ffs(end);
+        const unsigned nearer = (end & (0u - end)) - 1u;
+        if (end && (out & nearer) == nearer) break;
+        if (late()) return 0.f;
     }
+    unsigned e;
+    unsigned long long m[kBatch];
+    int d = back - 1;                                 // distance of the next map
+    float s = 0.f;
+    bool first = true;
+    do {
+        while (true) {
+            bool there = true;
+            if (first) {
+                e = mine ? load_word(ends - (long long)back * chans) : 0u;
+                there = e != kEmpty;
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                m[u] = mine && d - u > 0 ? load_word(maps - (long long)(d - u) * chans) : 0ull;
+                there = there && has_map(m[u]);
+            }
+            if (__all_sync(0xffffffffu, there)) break;
+            if (late()) return 0.f;
+        }
+        if (first) s = __uint_as_float(e);
+        first = false;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (d - u > 0) s = apply_map(m[u], s);
+        d -= kBatch;
+    } while (d > 0);
+    return s;
 }
 
 // ------------------------------------------------------------------ tile kernel
@@ -514,9 +521,21 @@ __global__ void __launch_bounds__(kThreads, 2)
                         mA *= J.a[w][tid];
                     }
                 }
-                if (mine && j > 0 && j + 1 < p.ntiles) publish_map(p.maps + word, mA, mH);
-                if (j > 0) before = look_back(p.maps + word, p.ends + word, chans, j, mine, a.status, a.wait_cycles);
-                if (mine && j + 1 < p.ntiles) publish_end(p.ends + word, apply(mA, mH, before));
+                unsigned* hint = p.hints + ((size_t)strip * swarps + warp) * p.ntiles + j;
+                const bool tell = j + 1 < p.ntiles;
+                if (tell && j > 0) {
+                    if (mine) publish_map(p.maps + word, mA, mH);
+                    __syncwarp();
+                    if ((tid & 31) == 0) store_word(hint, kMapThere);
+                }
+                if (j > 0)
+                    before = look_back(hint, p.maps + word, p.ends + word, chans, j, mine, a.status,
+                                       a.wait_cycles);
+                if (tell) {
+                    if (mine) publish_end(p.ends + word, apply(mA, mH, before));
+                    __syncwarp();
+                    if ((tid & 31) == 0) store_word(hint, kEndThere);
+                }
             }
             if (mine) J.carry[tid] = before;
         }
@@ -672,11 +691,25 @@ constexpr int kSerialTokens = 8;
 
 TilePlan make_plan(const GlrArgs& a, int backward, size_t* bytes) {
     TilePlan p{};
-    while (p.cw_log < kMaxLog && (V << p.cw_log) < a.D) ++p.cw_log;
-    const int chans = V << p.cw_log;
+    const int es = a.bf16 ? 2 : 4;
     const int run = backward ? (a.bf16 ? kRun<__nv_bfloat16, true> : kRun<float, true>)
                              : (a.bf16 ? kRun<__nv_bfloat16, false> : kRun<float, false>);
-    p.tokens = (kThreads >> p.cw_log) * run;
+    // Strips of 64 channels (or D).  With few of them the blocks at work on one are many, and each
+    // waits longer for the state before its tile, so they are halved, and their tiles twice as
+    // long, down to rows of 64 bytes, until there are 128 of them (128 channels, bf16: 1 x 131072
+    // tokens 155 us with one strip of 128 channels, 86 with two, 54 with four; 64 x 32768 tokens
+    // 245 us with two strips a row, 258 with four).  Down to rows of 32 bytes where all of a
+    // sequence then is one tile and nobody waits (2 x 777 x 768: 6.0 us against 7.7).
+    auto strips_at = [&](int log) { return (long long)a.N * ((a.D + (V << log) - 1) / (V << log)); };
+    auto tokens_at = [&](int log) { return (kThreads >> log) * run; };
+    while (p.cw_log < kMaxLog && (V << p.cw_log) < a.D) ++p.cw_log;
+    while (p.cw_log > 0 && (V << p.cw_log) * es > 64 && a.T > tokens_at(p.cw_log) && strips_at(p.cw_log) < 128)
+        --p.cw_log;
+    if (p.cw_log > 0 && (V << p.cw_log) * es > 32 && a.T > tokens_at(p.cw_log) &&
+        a.T <= tokens_at(p.cw_log - 1) && strips_at(p.cw_log - 1) <= 2 * 152)
+        --p.cw_log;
+    const int chans = V << p.cw_log;
+    p.tokens = tokens_at(p.cw_log);
     p.ntiles = (a.T + p.tokens - 1) / p.tokens;
     if (p.ntiles < 1) p.ntiles = 1;
     p.ncols = (a.D + chans - 1) / chans;
@@ -689,7 +722,8 @@ TilePlan make_plan(const GlrArgs& a, int backward, size_t* bytes) {
         p.counter = reinterpret_cast<unsigned*>(w);
         p.maps = reinterpret_cast<unsigned long long*>(w + 256);
         p.ends = reinterpret_cast<unsigned*>(w + 256 + words * 8);
-        p.words_bytes = 256 + words * 12;
+        p.hints = p.ends + words;
+        p.words_bytes = 256 + words * 12 + strips * ((chans + 31) / 32) * p.ntiles * 4;
         off = (p.words_bytes + 255) / 256 * 256;
     }
     if (backward && a.gate_token && p.ncols > 1) {
