@@ -51,10 +51,12 @@ constexpr int kChans = V << kMaxLog;          // channels of a full strip
 constexpr int kNear = 4, kBatch = 8;              // tiles a look-back takes with the hints; maps then
 constexpr long long kWaitCycles = 4000000000LL;   // default limit, ~2 s at 2 GHz
 
-// R, the tokens of one thread in a tile: what it holds of them in registers is 64 of those
-// forward, 48 in the gradient.
-template <typename E, bool kBack> constexpr int kRun = (sizeof(E) == 2 ? 16 : 8) / (kBack ? 2 : 1);
-template <typename E, bool kBack> constexpr int kTileBytes = kThreads * kRun<E, kBack> * V * (int)sizeof(E);
+// R, the tokens of one thread in a tile: its two tensors (three in the gradient with a gate per
+// channel, which gets half the tokens) take 64 (48) registers.
+template <typename E, bool kToken, bool kBack>
+constexpr int kRun = (sizeof(E) == 2 ? 16 : 8) / (kBack && !kToken ? 2 : 1);
+template <typename E, bool kToken, bool kBack>
+constexpr int kTileBytes = kThreads * kRun<E, kToken, kBack> * V * (int)sizeof(E);
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -143,10 +145,11 @@ __device__ __forceinline__ void load_rows_by(unsigned char* dst, int rows, int s
     const int per = srow / (int)sizeof(U);            // accesses per row, a power of two <= kThreads
     const int o = (threadIdx.x & (per - 1)) * (int)sizeof(U), step = kThreads / per;
     const int whole = o + (int)sizeof(U) <= bytes;
-    for (int r = threadIdx.x / per; r < rows; r += 8 * step) {
-        U u[8];
+    constexpr int kFlight = 64 / (int)sizeof(U);      // loads in flight: 64 bytes a thread
+    for (int r = threadIdx.x / per; r < rows; r += kFlight * step) {
+        U u[kFlight];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kFlight; ++k) {
             const int q = r + k * step;
             u[k] = U{};
             if (q >= lo && q < hi && o < bytes) {
@@ -162,7 +165,7 @@ __device__ __forceinline__ void load_rows_by(unsigned char* dst, int rows, int s
             }
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < kFlight; ++k)
             if (r + k * step < rows) *reinterpret_cast<U*>(dst + (r + k * step) * srow + o) = u[k];
     }
 }
@@ -336,9 +339,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const __grid_constant__ CUtensorMap mh, const __grid_constant__ CUtensorMap mo,
                     const __grid_constant__ CUtensorMap mog, const __grid_constant__ GlrArgs a,
                     const __grid_constant__ TilePlan p) {
-    constexpr int R = kRun<E, kBack>;
+    constexpr int R = kRun<E, kToken, kBack>;
     constexpr int kIns = 1 + (kToken ? 0 : 1) + (kBack ? 1 : 0);
-    constexpr uint32_t kBytes = kTileBytes<E, kBack>;
+    constexpr uint32_t kBytes = kTileBytes<E, kToken, kBack>;
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned char* sx = smem;                                        // x or dh
     unsigned char* sg = smem + (kToken ? 0 : kBytes);                // g (gate per channel)
@@ -647,8 +650,41 @@ __global__ void glr_gate_sum_kernel(const float* part, int ncols, size_t n, floa
     dg[i] = s;
 }
 
-// Token by token for calls of few tokens: one thread per four channels (W = 1: per
-// channel, where rows do not start on four values' bytes), the state in registers.
+// W neighbouring channels, W = 1, 4 or 8, at once (16 bytes at most in one access).
+template <typename E, int W>
+__device__ __forceinline__ void get_wide(const E* p, float (&f)[W]) {
+    if constexpr (W == 1) {
+        f[0] = to_f(*p);
+    } else if constexpr (sizeof(E) == 2 && W == 8) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) get4(p + i, *reinterpret_cast<float(*)[4]>(f + i));
+    }
+}
+template <typename E, int W>
+__device__ __forceinline__ void put_wide(E* p, const float (&f)[W]) {
+    if constexpr (W == 1) {
+        put(*p, f[0]);
+    } else if constexpr (sizeof(E) == 2 && W == 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = bf16_of_pair(pair(f[2 * i], f[2 * i + 1]));
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) put4(p + i, *reinterpret_cast<const float(*)[4]>(f + i));
+    }
+}
+
+// Token by token: one thread per W channels (the widest of 16 bytes, four channels and one
+// that all rows start on), the state in registers.
 template <typename E, bool kToken, int W>
 __global__ void glr_serial_kernel(GlrArgs a, const float* start) {
     const int per = (a.D + W - 1) / W;
@@ -659,7 +695,8 @@ __global__ void glr_serial_kernel(GlrArgs a, const float* start) {
     const size_t nd = n * a.D + d;
     float s[W];
 #pragma unroll
-    for (int v = 0; v < W; ++v) s[v] = start ? start[nd + v] : 0.f;
+    for (int v = 0; v < W; ++v) s[v] = 0.f;
+    if (start) get_wide(start + nd, s);
     const E* x = static_cast<const E*>(a.x) + n * a.x_seq + d;
     const E* gc = static_cast<const E*>(a.g) + n * a.g_seq + d;
     const float* gt = static_cast<const float*>(a.g) + n * a.g_seq;
@@ -667,33 +704,30 @@ __global__ void glr_serial_kernel(GlrArgs a, const float* start) {
 #pragma unroll 4
     for (int t = 0; t < a.T; ++t) {
         float xv[W], gv[W];
-        if constexpr (W == 1) {
-            xv[0] = to_f(x[(long long)t * a.x_tok]);
-            if (!kToken) gv[0] = to_f(gc[(long long)t * a.g_tok]);
-        } else {
-            get4(x + (long long)t * a.x_tok, xv);
-            if (!kToken) get4(gc + (long long)t * a.g_tok, gv);
-        }
+        get_wide(x + (long long)t * a.x_tok, xv);
+        if (!kToken) get_wide(gc + (long long)t * a.g_tok, gv);
         const float rt = kToken ? retention(gt[(long long)t * a.g_tok]) : 0.f;
 #pragma unroll
         for (int v = 0; v < W; ++v) s[v] = fmaf(kToken ? rt : retention(gv[v]), s[v], xv[v]);
-        if constexpr (W == 1) put(h[(size_t)t * a.D], s[0]);
-        else put4(h + (size_t)t * a.D, s);
+        put_wide(h + (size_t)t * a.D, s);
     }
-    if constexpr (W == 1) a.h_last[nd] = s[0];
-    else put4(a.h_last + nd, s);
+    put_wide(a.h_last + nd, s);
 }
 
 // ------------------------------------------------------------------------- host
 
-// A call of at most this many tokens runs token by token: a tile would be mostly empty.
-constexpr int kSerialTokens = 8;
+// Token by token where a tile would be mostly empty, and where the channels alone keep the
+// SMs busy (8 x 152 x 128 threads of four): nothing is joined or waited for then.
+bool by_tokens(const GlrArgs& a) {
+    return a.T <= 8 || (size_t)a.N * a.D >= 4ull * 152 * 1024;
+}
 
 TilePlan make_plan(const GlrArgs& a, int backward, size_t* bytes) {
     TilePlan p{};
     const int es = a.bf16 ? 2 : 4;
-    const int run = backward ? (a.bf16 ? kRun<__nv_bfloat16, true> : kRun<float, true>)
-                             : (a.bf16 ? kRun<__nv_bfloat16, false> : kRun<float, false>);
+    const int run = backward && !a.gate_token
+                        ? (a.bf16 ? kRun<__nv_bfloat16, false, true> : kRun<float, false, true>)
+                        : (a.bf16 ? kRun<__nv_bfloat16, true, true> : kRun<float, true, true>);
     // Strips of 64 channels (or D).  With few of them the blocks at work on one are many, and each
     // waits longer for the state before its tile, so they are halved, and their tiles twice as
     // long, down to rows of 64 bytes, until there are 128 of them (128 channels, bf16: 1 x 131072
@@ -750,7 +784,7 @@ bool tile_map(CUtensorMap* m, const TilePlan& p, const GlrArgs& a, const void* p
 template <typename E, bool kToken, bool kBack>
 cudaError_t tile_launch(const GlrArgs& a, TilePlan p, cudaStream_t s) {
     constexpr int tiles = 1 + (kToken ? 0 : 1) + (kBack ? 1 : 0) + (kBack && !kToken ? 2 : 1);
-    constexpr int smem = tiles * kTileBytes<E, kBack> + (int)sizeof(Joints);
+    constexpr int smem = tiles * kTileBytes<E, kToken, kBack> + (int)sizeof(Joints);
     auto kernel = glr_tile_kernel<E, kToken, kBack>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -794,32 +828,38 @@ cudaError_t tiles(GlrArgs a, bool back, cudaStream_t s, int* launches) {
     return cudaGetLastError();
 }
 
+template <typename E, int W>
+cudaError_t serial_launch(const GlrArgs& a, const float* start, cudaStream_t s) {
+    const size_t threads = (size_t)a.N * (a.D / W);
+    const unsigned blocks = (unsigned)((threads + 127) / 128);
+    if (a.gate_token) glr_serial_kernel<E, true, W><<<blocks, 128, 0, s>>>(a, start);
+    else glr_serial_kernel<E, false, W><<<blocks, 128, 0, s>>>(a, start);
+    return cudaGetLastError();
+}
+
 template <typename E>
 cudaError_t serial(const GlrArgs& a, const float* start, cudaStream_t s) {
     const int es = sizeof(E);
-    bool wide = a.D % V == 0 &&
-                access_width(a.x, a.N > 1 ? a.x_seq : 0, a.T > 1 ? a.x_tok : 0, es) >= V * es;
+    int width = access_width(a.x, a.N > 1 ? a.x_seq : 0, a.T > 1 ? a.x_tok : 0, es);
     if (!a.gate_token)
-        wide = wide && access_width(a.g, a.N > 1 ? a.g_seq : 0, a.T > 1 ? a.g_tok : 0, es) >= V * es;
-    const size_t threads = (size_t)a.N * (wide ? a.D / V : a.D);
-    const unsigned blocks = (unsigned)((threads + 127) / 128);
-    if (wide && a.gate_token) glr_serial_kernel<E, true, V><<<blocks, 128, 0, s>>>(a, start);
-    else if (wide) glr_serial_kernel<E, false, V><<<blocks, 128, 0, s>>>(a, start);
-    else if (a.gate_token) glr_serial_kernel<E, true, 1><<<blocks, 128, 0, s>>>(a, start);
-    else glr_serial_kernel<E, false, 1><<<blocks, 128, 0, s>>>(a, start);
-    return cudaGetLastError();
+        width = min(width, access_width(a.g, a.N > 1 ? a.g_seq : 0, a.T > 1 ? a.g_tok : 0, es));
+    // 16 bytes a thread where that still makes a thread for every lane of the GPU's SMs
+    if (es == 2 && width == 16 && a.D % 8 == 0 && (size_t)a.N * a.D >= 8ull * 152 * 1024)
+        return serial_launch<E, 8>(a, start, s);
+    if (width >= V * es && a.D % V == 0) return serial_launch<E, V>(a, start, s);
+    return serial_launch<E, 1>(a, start, s);
 }
 
 }  // namespace
 
 size_t glr_workspace_bytes(const GlrArgs& a, int backward) {
     size_t bytes = 0;
-    if (backward || a.T > kSerialTokens) make_plan(a, backward, &bytes);
+    if (backward || !by_tokens(a)) make_plan(a, backward, &bytes);
     return bytes;
 }
 
 cudaError_t glr_fwd_launch(const GlrArgs& a, cudaStream_t s, int* launches) {
-    if (a.T > kSerialTokens)
+    if (!by_tokens(a))
         return a.bf16 ? tiles<__nv_bfloat16>(a, false, s, launches) : tiles<float>(a, false, s, launches);
     *launches = 1;
     return a.bf16 ? serial<__nv_bfloat16>(a, a.h0, s) : serial<float>(a, a.h0, s);

@@ -6,10 +6,12 @@
 // Numbers.  The products take fp16 operands and add in fp32.  bf16 operands are not
 // enough: the steps multiply small singular values by up to a = 3.4 each, and their
 // rounding with them (1 % off for a normal matrix, 6 % for one of low rank plus noise).  With
-// fp16 operands and X itself kept to fp32's accuracy (in registers, or as the sum of two
-// fp16 values) the result is 1.7e-3 to 2.5e-3 off, of which rounding it to bf16 is 1.7e-3; with
-// X rounded to fp16 every step it would be 8e-3 for the matrix of low rank.  Operands are
-// stored times 2^10, so that entries of 1e-4 stay clear of fp16's subnormal range.
+// fp16 operands, X itself kept to fp32's accuracy (in registers, or as the sum of two fp16
+// values) and the diagonal of B, its largest entries once X is near orthogonal, in fp32
+// beside the product, the result is 1.7e-3 to 2.0e-3 off, of which rounding it to bf16
+// is 1.7e-3; with B's diagonal in fp16 it would be up to 2.6e-3, with X rounded to
+// fp16 every step 8e-3 for the matrix of low rank.  Operands are stored times 2^10, so
+// that entries of 1e-4 stay clear of fp16's subnormal range.
 //
 // Both sides at most 128: one block keeps a matrix on chip through all steps
 // (ns_small_kernel).  Larger: three products a step (ns_gemm_kernel).  A and
@@ -115,6 +117,7 @@ struct SmallShared {
     uint32_t tmem;
     int abort;
     float part[kSmallThreads / 32];
+    float diag[kSide];
 };
 
 __device__ __forceinline__ uint4* operand_at(unsigned char* base, int row, int chunk) {
@@ -261,7 +264,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
             __syncwarp();
         }
         if (!wait_product()) break;
-        if (mine) {                                     // B = b A + c A A over A
+        float diag = 0.f;                               // of B, this row's
+        if (mine) {                                     // B = b A + c A A over A, without its diagonal
             const float c2 = cc * kUnscale;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -275,14 +279,20 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 old = half2_floats(w[i]);
-                        w[i] = half2_bits(fmaf(c2, v[8 * h + 2 * i], cb * old.x),
-                                          fmaf(c2, v[8 * h + 2 * i + 1], cb * old.y));
+                        float x = fmaf(c2, v[8 * h + 2 * i], cb * old.x);
+                        float y = fmaf(c2, v[8 * h + 2 * i + 1], cb * old.y);
+                        const int col = half * 64 + 16 * q + 8 * h + 2 * i;
+                        if (col == row) { diag = x; x = 0.f; }
+                        if (col + 1 == row) { diag = y; y = 0.f; }
+                        w[i] = half2_bits(x, y);
                     }
                     *at = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
         }
+        if (mine && row < rp && (row >> 6) == half) S.diag[row] = diag;
         ready();
+        const float keep = ca + (row < rp ? S.diag[row] * kUnscale : 0.f);
         if (warp == 0) {                                // B X, X as [k][n]
             if (elect_one()) {
                 const uint32_t id = idesc_f16(128, lp, 0, 1);
@@ -305,7 +315,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    X[16 * q + i] = fmaf(ca, X[16 * q + i], v[i] * kUnscale);
+                    X[16 * q + i] = fmaf(keep, X[16 * q + i], v[i] * kUnscale);
             }
         }
     }
@@ -479,7 +489,8 @@ __device__ __forceinline__ void free_columns(uint32_t t, uint32_t n) {
 // That halves what a block reads of B, which is what bounds a tile: with CG = 1 the copies
 // reach about 50 bytes a cycle and SM, 983 cycles for the 48 KB of a block of K at BN = 256 whose
 // products take 512.
-//   kGram:   out = alpha acc                (A; on and below the diagonal, mirrored)
+//   kGram:   out = alpha acc                (A; on and below the diagonal, mirrored; or, with few
+//            tiles and a long K, fp32 sums over parts of K, which ns_join_kernel adds)
 //   kSquare: out = alpha acc + beta in      (B from A A and A; likewise)
 //   kUpdate: X'  = alpha acc + beta X       (X and X' as hi + lo; the last one to bf16)
 // Roles (320 threads, one block an SM): warp 0 copies operand tiles in (kStages deep), warp 1
@@ -502,7 +513,14 @@ __host__ __device__ constexpr uint32_t stage_bytes(int CG, int BN) { return (kBM
 struct GemmParams {
     int M, N, K, batch;
     int tiles_m, tiles_n, per_matrix, tiles;
+    int splits, split_blocks;       // kGram: parts of K, blocks of K in a part
+    float* parts;                   // splits > 1: [splits][batch][M][part_pitch]
+    int part_pitch;
     float alpha, beta;
+    float* diag;                    // B's diagonal, [batch][short side]: kSquare writes it, kUpdate
+                                    // adds it to beta, by row (or by_column)
+    float diag_scale;
+    int by_column, diag_n;
     const __half *in_hi, *in_lo;    // values to add, [batch][M][pitch]
     __half *out_hi, *out_lo;        // results, [batch][M][pitch]
     int pitch;                      // of all four, a multiple of 8
@@ -519,6 +537,7 @@ struct GemmShared {
 
 struct TileAt {
     int row, col, mat;
+    int k0, k1, split;              // its blocks of K
 };
 
 // Tile t: all tiles (columns outermost, so that tiles at work share columns of X), or for the
@@ -526,6 +545,16 @@ struct TileAt {
 template <int EPI, int TM, int BN>
 __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
     TileAt at;
+    const int kblocks = (p.K + kBK - 1) / kBK;
+    at.split = 0;
+    at.k0 = 0;
+    at.k1 = kblocks;
+    if (EPI == kGram && p.splits > 1) {
+        at.split = t % p.splits;
+        t /= p.splits;
+        at.k0 = at.split * p.split_blocks;
+        at.k1 = min(kblocks, at.k0 + p.split_blocks);
+    }
     at.mat = t / p.per_matrix;
     t -= at.mat * p.per_matrix;
     if (EPI == kUpdate) {
@@ -558,8 +587,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)cluster_rank() : 0;
     const int first = blockIdx.x / CG, stride = gridDim.x / CG;
-    const int kblocks = (p.K + kBK - 1) / kBK;
-
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&S.full[i], 1);
@@ -587,7 +614,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             TileAt at = tile_at<EPI, TM, BN>(p, t);
             at.row += rank * kBM;
             at.col += rank * (BN / CG);
-            for (int k = 0; k < kblocks; ++k, ++it) {
+            for (int k = at.k0; k < at.k1; ++k, ++it) {
                 const int s = it % kStages;
                 ok = wait_one(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort, p.status, p.limit);
                 if (!ok) break;
@@ -631,7 +658,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + acc * BN;
-            for (int k = 0; k < kblocks; ++k) {
+            const TileAt at = tile_at<EPI, TM, BN>(p, t);
+            for (int k = at.k0; k < at.k1; ++k) {
                 ok = wait_warp(&S.full[s], phase, &S.abort, p.status, p.limit);
                 if (!ok) break;
                 tc_fence_after();
@@ -639,12 +667,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk) {
-                        if (CG == 2) mma_pair(d, da + kk * step_a, db + kk * step_b, id, k > 0 || kk > 0);
-                        else mma_bf16(d, da + kk * step_a, db + kk * step_b, id, k > 0 || kk > 0);
+                        if (CG == 2) mma_pair(d, da + kk * step_a, db + kk * step_b, id, k > at.k0 || kk > 0);
+                        else mma_bf16(d, da + kk * step_a, db + kk * step_b, id, k > at.k0 || kk > 0);
                     }
                     if (CG == 2) commit_pair(&S.empty[s]);
                     else mma_commit(&S.empty[s]);
-                    if (k + 1 == kblocks) {
+                    if (k + 1 == at.k1) {
                         if (CG == 2) commit_pair(&S.acc_full[acc]);
                         else mma_commit(&S.acc_full[acc]);
                     }
@@ -697,6 +725,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     __syncwarp();
                 }
                 const bool mirror = EPI != kUpdate && row0 > col0 + 63;
+                const int row = row0 + lane;
+                const float* diag = p.diag + (size_t)at.mat * p.diag_n;
+                float keep = p.beta;
+                if (EPI == kUpdate && !p.by_column && row < p.M) keep = fmaf(p.diag_scale, diag[row], keep);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     float v[32];
@@ -704,6 +736,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     tmem_ld16(ta, *reinterpret_cast<float(*)[16]>(v));
                     tmem_ld16(ta + 16, *reinterpret_cast<float(*)[16]>(v + 16));
                     tmem_wait_ld();
+                    if (EPI == kGram && p.splits > 1) {
+                        float* to = p.parts + (((size_t)at.split * p.batch + at.mat) * p.M + row) * p.part_pitch;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const int col = col0 + 32 * q + i;
+                            if (row < p.M && col < p.part_pitch)
+                                *reinterpret_cast<float4*>(to + col) =
+                                    make_float4(v[i] * p.alpha, v[i + 1] * p.alpha, v[i + 2] * p.alpha,
+                                                v[i + 3] * p.alpha);
+                        }
+                        continue;
+                    }
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         const uint32_t o = lane * 128 + (((4 * q + h) ^ (lane & 7)) << 4);
@@ -729,8 +773,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                     x.x += y.x;
                                     x.y += y.y;
                                 }
-                                f[2 * i] = fmaf(p.alpha, f[2 * i], p.beta * x.x);
-                                f[2 * i + 1] = fmaf(p.alpha, f[2 * i + 1], p.beta * x.y);
+                                float b0 = keep, b1 = keep;
+                                const int col = col0 + 32 * q + 8 * h + 2 * i;
+                                if (EPI == kUpdate && p.by_column) {
+                                    if (col < p.N) b0 = fmaf(p.diag_scale, diag[col], b0);
+                                    if (col + 1 < p.N) b1 = fmaf(p.diag_scale, diag[col + 1], b1);
+                                }
+                                f[2 * i] = fmaf(p.alpha, f[2 * i], b0 * x.x);
+                                f[2 * i + 1] = fmaf(p.alpha, f[2 * i + 1], b1 * x.y);
+                                if (EPI == kSquare && col == row && row < p.M) {
+                                    p.diag[(size_t)at.mat * p.diag_n + row] = f[2 * i];
+                                    f[2 * i] = 0.f;
+                                }
+                                if (EPI == kSquare && col + 1 == row && row < p.M) {
+                                    p.diag[(size_t)at.mat * p.diag_n + row] = f[2 * i + 1];
+                                    f[2 * i + 1] = 0.f;
+                                }
                             }
                         }
 #pragma unroll
@@ -756,6 +814,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                 }
                 __syncwarp();
+                if (EPI == kGram && p.splits > 1) continue;
                 // out again, row by row; the columns between N and the pitch are never read
                 const bool rows16 = EPI != kUpdate || !p.last || p.N % 8 == 0;
                 if (rows16) {
@@ -814,13 +873,65 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (warp == 1) free_columns<CG>(tmem, 2 * BN);
 }
 
+// A from the parts' sums, in the parts' order: a block takes 32 x 32 values on or below the
+// diagonal and writes them and their mirror image.
+__global__ void __launch_bounds__(256) ns_join_kernel(const float* parts, int splits, int batch, int n,
+                                                      int part_pitch, int pitch, __half* A) {
+    __shared__ float tile[32][33];
+    after_previous();
+    const int r0 = blockIdx.y * 32, c0 = blockIdx.x * 32;
+    if (c0 > r0) return;
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const size_t mat = blockIdx.z;
+    A += mat * n * pitch;
+    for (int y = ty; y < 32; y += 8) {
+        const int r = r0 + y, c = c0 + tx;
+        float t = 0.f;
+        if (r < n && c <= r)
+            for (int i = 0; i < splits; ++i) t += parts[(((size_t)i * batch + mat) * n + r) * part_pitch + c];
+        tile[y][tx] = t;
+        if (r < n && c <= r) A[(size_t)r * pitch + c] = __float2half_rn(t);
+    }
+    __syncthreads();
+    for (int y = ty; y < 32; y += 8) {
+        const int r = c0 + y, c = r0 + tx;              // the mirrored element, of row r < c
+        if (c < n && r < c) A[(size_t)r * pitch + c] = __float2half_rn(tile[tx][y]);
+    }
+}
+
 // ----------------------------------------------------------------------------- host
 
 int pitch_of(int n) { return (n + 7) / 8 * 8; }
 
 struct Workspace {
-    size_t hi[2], lo, a, b, part, total;    // X as hi (two in turn) + lo (in place), A, B, norm sums
+    size_t hi[2], lo, a, b, diag, part, parts, total;  // X as hi (two in turn) + lo (in place), A, B and its
+                                                // diagonal, norm sums, A by parts of K
 };
+
+// Tiles of one matrix.
+int tiles_of(int epi, int M, int N, int TM, int BN) {
+    const int tm = (M + TM - 1) / TM, tn = (N + BN - 1) / BN;
+    if (epi == kUpdate) return tm * tn;
+    int all = 0;
+    for (int i = 0; i < tm; ++i) {
+        const int n = (i * TM + TM - 1) / BN + 1;
+        all += n < tn ? n : tn;
+    }
+    return all;
+}
+
+// Parts of K for A = X X^T, r x r from l columns: as many as fill the SMs with tiles of 128 x 64,
+// of four blocks of K at least; 1 where the tiles alone come near that.
+int split_of(int batch, int r, int l) {
+    const long long tiles = (long long)tiles_of(kGram, r, r, kBM, 64) * batch;
+    const int kblocks = (l + kBK - 1) / kBK;
+    if (tiles > 50 || kblocks < 16) return 1;
+    int s = (int)(152 / tiles);
+    if (s > kblocks / 4) s = kblocks / 4;
+    if (s > 16) s = 16;
+    const int each = (kblocks + s - 1) / s;
+    return (kblocks + each - 1) / each;                 // no part is empty
+}
 
 Workspace layout(int batch, int m, int n) {
     Workspace w{};
@@ -836,7 +947,10 @@ Workspace layout(int batch, int m, int n) {
     w.lo = take(xs);
     w.a = take(as);
     w.b = take(as);
+    w.diag = take((size_t)batch * rs * sizeof(float));
     w.part = take((size_t)batch * kNormBlocks * sizeof(float));
+    const int splits = split_of(batch, (int)rs, m < n ? n : m);
+    if (splits > 1) w.parts = take((size_t)splits * batch * rs * ((rs + 3) / 4 * 4) * sizeof(float));
     w.total = off;
     return w;
 }
@@ -855,16 +969,25 @@ struct Mat {
     }
 };
 
-// Tiles of one matrix.
-int tiles_of(int epi, int M, int N, int TM, int BN) {
-    const int tm = (M + TM - 1) / TM, tn = (N + BN - 1) / BN;
-    if (epi == kUpdate) return tm * tn;
-    int all = 0;
-    for (int i = 0; i < tm; ++i) {
-        const int n = (i * TM + TM - 1) / BN + 1;
-        all += n < tn ? n : tn;
-    }
-    return all;
+// Launches a kernel whose set-up may overlap the one before (after_previous), in clusters of
+// `cluster` blocks.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
+                         const A&... args) {
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = block;
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 2;
+    return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
 template <bool AMN, bool BMN, int EPI, int CG, int BN>
@@ -872,7 +995,7 @@ cudaError_t gemm_tiles(const Mat& A, const Mat& B, GemmParams p, cudaStream_t s)
     p.tiles_m = (p.M + kBM * CG - 1) / (kBM * CG);
     p.tiles_n = (p.N + BN - 1) / BN;
     p.per_matrix = tiles_of(EPI, p.M, p.N, kBM * CG, BN);
-    const long long tiles = (long long)p.per_matrix * p.batch;
+    const long long tiles = (long long)p.per_matrix * p.batch * (EPI == kGram && p.splits > 1 ? p.splits : 1);
     if (tiles > (1LL << 31) - 1) return cudaErrorInvalidValue;
     p.tiles = (int)tiles;
     CUtensorMap ma, mb;
@@ -882,26 +1005,15 @@ cudaError_t gemm_tiles(const Mat& A, const Mat& B, GemmParams p, cudaStream_t s)
     auto kernel = ns_gemm_kernel<AMN, BMN, EPI, CG, BN>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CG;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3(CG * (p.tiles < 152 / CG ? p.tiles : 152 / CG));
-    c.blockDim = dim3(kGemmThreads);
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
-    c.attrs = at;
-    c.numAttrs = 2;
-    return cudaLaunchKernelEx(&c, kernel, ma, mb, p);
+    return launch_after(kernel, dim3(CG * (p.tiles < 152 / CG ? p.tiles : 152 / CG)), dim3(kGemmThreads), smem, s, CG,
+                        ma, mb, p);
 }
 
 // The tile that takes the least time by this count: rounds of tiles over the SMs times a tile's
 // blocks of K (cycles for its copies or products, whichever is more) and its start and epilogue.
 template <bool AMN, bool BMN, int EPI>
 cudaError_t gemm(const Mat& A, const Mat& B, const GemmParams& p, cudaStream_t s) {
+    if (EPI == kGram && p.splits > 1) return gemm_tiles<AMN, BMN, EPI, 1, 64>(A, B, p, s);
     auto cost = [&](int CG, int BN, double block) {
         const long long tiles = (long long)tiles_of(EPI, p.M, p.N, kBM * CG, BN) * p.batch;
         const long long slots = 152 / CG, rounds = (tiles + slots - 1) / slots;
@@ -947,6 +1059,7 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
     const Mat A{reinterpret_cast<__half*>(ws + w.a), r, r, ap, a.batch};
     const Mat B{reinterpret_cast<__half*>(ws + w.b), r, r, ap, a.batch};
     float* part = reinterpret_cast<float*>(ws + w.part);
+    const int splits = split_of(a.batch, r, l);
 
     const size_t mn = (size_t)a.m * a.n;
     size_t blocks = (mn + 4095) / 4096;
@@ -981,18 +1094,32 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         p.alpha = kUnscale;                              // (2^10 X)(2^10 X)^T -> 2^10 A
         p.pitch = ap;
         p.out_hi = A.p;
+        p.splits = splits;
+        p.split_blocks = ((l + kBK - 1) / kBK + splits - 1) / splits;
+        p.parts = reinterpret_cast<float*>(ws + w.parts);
+        p.part_pitch = (r + 3) / 4 * 4;
         e = wide ? gemm<false, false, kGram>(x, x, p, s) : gemm<true, true, kGram>(x, x, p, s);
         if (e != cudaSuccess) return e;
+        if (splits > 1) {
+            const unsigned t = (r + 31) / 32;
+            e = launch_after(ns_join_kernel, dim3(t, t, a.batch), dim3(256), 0, s, 1, (const float*)p.parts, splits,
+                             a.batch, r, p.part_pitch, ap, A.p);
+            if (e != cudaSuccess) return e;
+            ++*launches;
+        }
         p.K = r;
         p.alpha = c[2] * sb * kUnscale * kUnscale;       // -> sb (b A + c A A)
         p.beta = c[1] * sb * kUnscale;
         p.in_hi = A.p;
         p.out_hi = B.p;
+        p.diag = reinterpret_cast<float*>(ws + w.diag);
+        p.diag_n = r;
         e = gemm<false, false, kSquare>(A, A, p, s);
         if (e != cudaSuccess) return e;
         p.M = a.m;
         p.N = a.n;
-        p.alpha = 1.f / sb;                              // -> 2^10 X'
+        p.alpha = p.diag_scale = 1.f / sb;               // -> 2^10 X'
+        p.by_column = !wide;
         p.beta = c[0];
         p.pitch = xp;
         p.in_hi = x.p;

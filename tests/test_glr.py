@@ -75,7 +75,7 @@ def on(t):
 
 SHAPES = [(1, 1, 1), (1, 2, 8), (2, 3, 5), (1, 17, 64), (3, 64, 128), (2, 127, 64), (2, 129, 40),
           (1, 1000, 199), (5, 513, 24), (2, 300, 136), (1, 2049, 128), (300, 9, 16), (3, 5, 2048),
-          (1, 4097, 8)]
+          (1, 4097, 8), (1300, 20, 512), (5, 11, 131)]
 
 
 @pytest.mark.parametrize("N,T,D", SHAPES)
