@@ -134,47 +134,51 @@ inline int access_width(const void* p, long long seq, long long tok, int es) {
     return m % 16 == 0 ? 16 : (m % 8 == 0 ? 8 : (m % 4 == 0 ? 4 : es));
 }
 
-// Copies rows [0, rows) of `bytes` bytes at `pitch` bytes from global memory into
-// shared rows of `srow` bytes, sizeof(U) bytes at a time; rows below `lo` or from `hi` on
-// and bytes past the end read as zero.  A thread keeps its column.  (Asynchronous copies
-// of 4 bytes take the SM 32 cycles a warp: 16500 for a tile of 64 x 128 fp32 values twice,
-// against 3000 this way.)
-template <typename E, typename U>
-__device__ __forceinline__ void load_rows_by(unsigned char* dst, int rows, int srow, const char* src,
-                                             long long pitch, int lo, int hi, int bytes) {
-    const int per = srow / (int)sizeof(U);            // accesses per row, a power of two <= kThreads
-    const int o = (threadIdx.x & (per - 1)) * (int)sizeof(U), step = kThreads / per;
-    const int whole = o + (int)sizeof(U) <= bytes;
-    constexpr int kFlight = 64 / (int)sizeof(U);      // loads in flight: 64 bytes a thread
+// Copies rows [0, rows) of `bytes` bytes at `pitch` bytes from global memory, wherever they
+// start, into shared rows of `srow` bytes (a multiple of 8), 16 at a time; rows below `lo` or
+// from `hi` on and bytes past the end read as zero.  Global memory is read in aligned 16-byte
+// words that hold at least one byte of the row, and two of them shifted into place: 436 x
+// 508 x 768 bf16 from rows of 771 values took 300 us in loads of two bytes.
+__device__ __forceinline__ void load_rows(unsigned char* dst, int rows, int srow, const char* src,
+                                          long long pitch, int lo, int hi, int bytes) {
+    constexpr int kFlight = 4;                        // pairs of loads a thread has in flight
+    const int per = max(1, srow / 16);                // threads a row, a power of two
+    const int o = (threadIdx.x & (per - 1)) * 16, step = kThreads / per;
+    const int left = bytes - o;                       // of the row, from this thread's bytes on
     for (int r = threadIdx.x / per; r < rows; r += kFlight * step) {
-        U u[kFlight];
+        uint4 u[kFlight], v[kFlight];
+        int sh[kFlight];
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
             const int q = r + k * step;
-            u[k] = U{};
-            if (q >= lo && q < hi && o < bytes) {
-                const char* p = src + q * pitch + o;
-                if (whole) {
-                    u[k] = *reinterpret_cast<const U*>(p);
-                } else {                              // the row ends inside
-#pragma unroll
-                    for (int e = 0; e < (int)(sizeof(U) / sizeof(E)); ++e)
-                        if (o + (e + 1) * (int)sizeof(E) <= bytes)
-                            reinterpret_cast<E*>(&u[k])[e] = reinterpret_cast<const E*>(p)[e];
-                }
-            }
+            const char* p = src + q * pitch + o;
+            sh[k] = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+            const uint4* w = reinterpret_cast<const uint4*>(p - sh[k]);
+            const bool in = q >= lo && q < hi && left > 0;
+            u[k] = in ? w[0] : make_uint4(0, 0, 0, 0);
+            v[k] = in && sh[k] + left > 16 && sh[k] ? w[1] : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int k = 0; k < kFlight; ++k)
-            if (r + k * step < rows) *reinterpret_cast<U*>(dst + (r + k * step) * srow + o) = u[k];
+        for (int k = 0; k < kFlight; ++k) {
+            uint32_t w[8] = {u[k].x, u[k].y, u[k].z, u[k].w, v[k].x, v[k].y, v[k].z, v[k].w};
+            if (sh[k] & 8)
+#pragma unroll
+                for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+            if (sh[k] & 4)
+#pragma unroll
+                for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = __funnelshift_r(w[i], w[i + 1], (sh[k] & 3) * 8);
+                if (left < 4 * i + 4) w[i] = left == 4 * i + 2 ? w[i] & 0xffffu : 0u;
+            }
+            const int q = r + k * step;
+            if (q >= rows) continue;
+            unsigned char* to = dst + q * srow + o;
+            if (srow >= 16) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+        }
     }
-}
-template <typename E>
-__device__ __forceinline__ void load_rows(unsigned char* dst, int rows, int srow, const char* src,
-                                          long long pitch, int lo, int hi, int bytes, int width) {
-    if (width == 8) load_rows_by<E, uint2>(dst, rows, srow, src, pitch, lo, hi, bytes);
-    else if (width == 4) load_rows_by<E, uint32_t>(dst, rows, srow, src, pitch, lo, hi, bytes);
-    else load_rows_by<E, unsigned short>(dst, rows, srow, src, pitch, lo, hi, bytes);
 }
 
 // Shared rows back to global memory where a row does not start on 16 bytes:
@@ -208,7 +212,7 @@ struct TilePlan {
     size_t words_bytes;    // of the counter, maps, ends and hints, all set to kEmpty before
     unsigned tiles;        // of all strips
     int tma, tma_out;      // inputs, outputs by tensor copies
-    int width_x, width_g, width_o;   // else: access widths of x / dh, g; the contiguous tensors
+    int width_o;           // else: access width of the outputs' rows
     float* dg_part;        // token gate over several strips: [ncols][N T] partial sums
 };
 
@@ -252,6 +256,19 @@ struct Joints {
     unsigned ticket;
     unsigned long long arrived;                   // mbarrier of the tensor copies
 };
+
+// Sums of v[0 .. 2N-1] over groups of 2D lanes by exchanging halves: lane l of a group is left
+// with the sums of the values whose index agrees with it in the bits exchanged, in v[0 ..].
+template <int N, int D>
+__device__ __forceinline__ void scatter_sums(float* v) {
+    const bool up = threadIdx.x & D;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float mine = up ? v[i + N] : v[i], other = up ? v[i] : v[i + N];
+        v[i] = mine + __shfl_xor_sync(0xffffffffu, other, D);
+    }
+    if constexpr (N > 1) scatter_sums<N / 2, D / 2>(v);
+}
 
 // One warp, a lane per channel (mine: the lane has one): the state before tile j > 0.
 // maps and ends point to this lane's channel of tile j, `chans` words a tile; hints to
@@ -331,10 +348,13 @@ __device__ __forceinline__ float look_back(const unsigned* hints, const unsigned
 
 // ------------------------------------------------------------------ tile kernel
 
-// Persistent, two blocks an SM.  A block takes a tile from shared memory into registers, so
-// that the next tile's copies run while it looks back and writes this one's results.
+// Blocks an SM: what registers and shared memory leave room for.
+template <bool kToken, bool kBack> constexpr int kResident = kToken && !kBack ? 3 : 2;
+
+// Persistent.  A block takes a tile from shared memory into registers, so that the next tile's
+// copies run while it looks back and writes this one's results.
 template <typename E, bool kToken, bool kBack>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
     glr_tile_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
                     const __grid_constant__ CUtensorMap mh, const __grid_constant__ CUtensorMap mo,
                     const __grid_constant__ CUtensorMap mog, const __grid_constant__ GlrArgs a,
@@ -349,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     unsigned char* so = smem + kIns * kBytes;                        // h or dx
     unsigned char* sog = so + kBytes;                                // gradient: dg (gate per channel)
     Joints& J = *reinterpret_cast<Joints*>(so + (kBack && !kToken ? 2 : 1) * kBytes);
+    float* sgt = reinterpret_cast<float*>(&J + 1);    // token gate: a tile's, two in turn
     uint64_t* arrived = reinterpret_cast<uint64_t*>(&J.arrived);
 
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -376,6 +397,19 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (kBack) tc::tma_load_3d(sh + r * srow, &mh, arrived, c0, t0 + r - 1, n);
         }
     };
+    // token gate: copies of a tile's gates, waited for before the barrier that ends a tile
+    auto request_gates = [&](unsigned ticket, unsigned turn) {
+        const unsigned strip = ticket % strips;
+        const int j = ticket / strips, t0 = (kBack ? p.ntiles - 1 - j : j) * p.tokens;
+        const float* g = static_cast<const float*>(a.g) + (strip / p.ncols) * a.g_seq + (long long)t0 * a.g_tok;
+        float* to = sgt + turn * p.tokens;
+        for (int i = tid; i < p.tokens; i += kThreads) {
+            const bool in = t0 + i < a.T;             // past the end: 0, which keeps the state
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(to + i)),
+                         "l"(in ? g + (long long)i * a.g_tok : static_cast<const float*>(a.g)), "r"(in ? 4 : 0)
+                         : "memory");
+        }
+    };
     if (tid == 0) {
         J.ticket = p.counter ? atomicAdd(p.counter, 1u) + 1u : blockIdx.x;
         if (p.tma) {
@@ -385,6 +419,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
     __syncthreads();
+    if (kToken) {
+        if (J.ticket < p.tiles) request_gates(J.ticket, 0);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+    }
 
     unsigned phase = 0;
     for (unsigned ticket = J.ticket; ticket < p.tiles; ticket = J.ticket, phase ^= 1u) {
@@ -408,20 +447,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                     break;
                 }
         } else {
-            load_rows<E>(sx, p.tokens, srow,
+            load_rows(sx, p.tokens, srow,
                          reinterpret_cast<const char*>(static_cast<const E*>(a.x) + n * a.x_seq +
                                                        (long long)t0 * a.x_tok + c0),
-                         a.x_tok * (long long)sizeof(E), 0, ntok, bytes, p.width_x);
+                         a.x_tok * (long long)sizeof(E), 0, ntok, bytes);
             if (!kToken)
-                load_rows<E>(sg, p.tokens, srow,
+                load_rows(sg, p.tokens, srow,
                              reinterpret_cast<const char*>(static_cast<const E*>(a.g) + n * a.g_seq +
                                                            (long long)t0 * a.g_tok + c0),
-                             a.g_tok * (long long)sizeof(E), 0, ntok, bytes, p.width_g);
+                             a.g_tok * (long long)sizeof(E), 0, ntok, bytes);
             if (kBack)
-                load_rows<E>(sh, p.tokens, srow,
+                load_rows(sh, p.tokens, srow,
                              reinterpret_cast<const char*>(static_cast<const E*>(a.h) + c0) +
                                  ((long long)row0 - 1) * a.D * (long long)sizeof(E),
-                             (long long)a.D * sizeof(E), t0 == 0 ? 1 : 0, ntok, bytes, p.width_o);
+                             (long long)a.D * sizeof(E), t0 == 0 ? 1 : 0, ntok, bytes);
             __syncthreads();
         }
         Held<E> hx[R], hg[kToken ? 1 : R], hh[kBack ? R : 1];
@@ -431,11 +470,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (!kToken) hg[q].load(reinterpret_cast<const E*>(sg) + own + q * chans);
             if (kBack) hh[q].load(reinterpret_cast<const E*>(sh) + own + q * chans);
         }
-        const float* gt = static_cast<const float*>(a.g) + n * a.g_seq + (long long)t0 * a.g_tok;
+        const float* gt = sgt + phase * p.tokens + r0;
         auto retain = [&](int q, f2 (&r)[2]) {        // of token r0 + q
             if constexpr (kToken) {
-                r[0] = r[1] =
-                    splat<f2>(r0 + q < ntok ? retention(gt[(long long)(r0 + q) * a.g_tok]) : 1.f);
+                r[0] = r[1] = splat<f2>(retention(gt[q]));
             } else {
                 f2 g[2];
                 hg[q].get(g);
@@ -544,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (p.tma_out && tid == 0) tc::bulk_wait_read<0>();   // the results before have left
         __syncthreads();
+        if (kToken && J.ticket < p.tiles) request_gates(J.ticket, phase ^ 1u);
 
         // State before this thread's run: the tile's, through the warps before, then the
         // runs before in this warp
@@ -567,6 +606,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (kBack && kToken)
             dg = (p.ncols > 1 ? p.dg_part + (size_t)(strip % p.ncols) * a.N * a.T
                               : static_cast<float*>(a.dg)) + row0;
+        float share[kBack && kToken ? R : 1];         // token gate: this thread's share of dg
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int q = kBack ? R - 1 - i : i;
@@ -593,10 +633,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     s[v] = mul(r[v], o[v]);
                     b[v] = mul(b[v], s[v]);
                 }
-                if (kToken) {   // over the cw threads of the strip's channels, lanes of one warp
-                    float acc = total(add(b[0], b[1]));
-                    for (int d = cw >> 1; d; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-                    if (ch == 0 && r0 + q < ntok) dg[r0 + q] = acc;
+                if (kToken) {
+                    share[q] = total(add(b[0], b[1]));
                 } else {
                     Held<E> w;
                     w.set(b);
@@ -606,6 +644,25 @@ __global__ void __launch_bounds__(kThreads, 2)
             Held<E> w;
             w.set(o);
             w.store(reinterpret_cast<E*>(so) + own + q * chans);
+        }
+
+        if constexpr (kBack && kToken) {
+            // over the cw threads of the strip's channels, lanes of one warp
+            if (cw == 16) {
+                if (R == 8) {                         // 16 lanes for 8 values: add their halves first
+#pragma unroll
+                    for (int q = 0; q < R; ++q) share[q] += __shfl_xor_sync(0xffffffffu, share[q], 8);
+                }
+                scatter_sums<R / 2, R / 2>(share);
+                const int q = tid & (R - 1);
+                if ((tid & 15) < R && r0 + q < ntok) dg[r0 + q] = share[0];
+            } else {
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    for (int d = cw >> 1; d; d >>= 1) share[q] += __shfl_xor_sync(0xffffffffu, share[q], d);
+                    if (ch == 0 && r0 + q < ntok) dg[r0 + q] = share[q];
+                }
+            }
         }
 
         // End of the strip: the tokens past T leave the state as it is
@@ -619,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (c0 + ch + v < a.D) end[n * a.D + c0 + ch + v] = f[v];
         }
         if (p.tma_out) tc::fence_proxy_async_smem();
+        if (kToken) asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
         if (p.tma_out) {
             if (tid == 0) {
@@ -784,7 +842,8 @@ bool tile_map(CUtensorMap* m, const TilePlan& p, const GlrArgs& a, const void* p
 template <typename E, bool kToken, bool kBack>
 cudaError_t tile_launch(const GlrArgs& a, TilePlan p, cudaStream_t s) {
     constexpr int tiles = 1 + (kToken ? 0 : 1) + (kBack ? 1 : 0) + (kBack && !kToken ? 2 : 1);
-    constexpr int smem = tiles * kTileBytes<E, kToken, kBack> + (int)sizeof(Joints);
+    const int smem = tiles * kTileBytes<E, kToken, kBack> + (int)sizeof(Joints) +
+                     (kToken ? 2 * p.tokens * (int)sizeof(float) : 0);
     auto kernel = glr_tile_kernel<E, kToken, kBack>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -800,7 +859,7 @@ cudaError_t tile_launch(const GlrArgs& a, TilePlan p, cudaStream_t s) {
     p.tma_out = ((size_t)V << p.cw_log) * sizeof(E) >= 16 &&
                 tile_map<E>(&mo, p, a, kBack ? a.dx : a.h, (long long)a.T * a.D, a.D) &&
                 (!kBack || kToken || tile_map<E>(&mog, p, a, a.dg, (long long)a.T * a.D, a.D));
-    kernel<<<min(p.tiles, 2u * 152u), kThreads, smem, s>>>(mx, mg, mh, mo, mog, a, p);
+    kernel<<<min(p.tiles, kResident<kToken, kBack> * 152u), kThreads, smem, s>>>(mx, mg, mh, mo, mog, a, p);
     return cudaGetLastError();
 }
 
@@ -809,11 +868,7 @@ cudaError_t tiles(GlrArgs a, bool back, cudaStream_t s, int* launches) {
     size_t bytes;
     TilePlan p = make_plan(a, back, &bytes);
     const int es = sizeof(E);
-    p.width_x = access_width(a.x, a.N > 1 ? a.x_seq : 0, a.T > 1 ? a.x_tok : 0, es);
-    p.width_g = a.gate_token ? 4 : access_width(a.g, a.N > 1 ? a.g_seq : 0, a.T > 1 ? a.g_tok : 0, es);
     const int srow = (V << p.cw_log) * es;
-    p.width_x = min(p.width_x, min(srow, 8));
-    p.width_g = min(p.width_g, min(srow, 8));
     p.width_o = min(access_width(nullptr, 0, a.D, es), min(srow, 8));
     if (a.wait_cycles <= 0) a.wait_cycles = kWaitCycles;
     *launches = 1;

@@ -7,10 +7,12 @@
 // enough: the steps multiply small singular values by up to a = 3.4 each, and their
 // rounding with them (1 % off for a normal matrix, 6 % for one of low rank plus noise).  With
 // fp16 operands, X itself kept to fp32's accuracy (in registers, or as the sum of two fp16
-// values) and the diagonal of B, its largest entries once X is near orthogonal, in fp32
-// beside the product, the result is 1.7e-3 to 2.0e-3 off, of which rounding it to bf16
+// values, hi + lo) and the diagonal of B, its largest entries once X is near orthogonal, in
+// fp32 beside the product, the result is 1.7e-3 to 2.0e-3 off, of which rounding it to bf16
 // is 1.7e-3; with B's diagonal in fp16 it would be up to 2.6e-3, with X rounded to
-// fp16 every step 8e-3 for the matrix of low rank.  Operands are stored times 2^10, so
+// fp16 every step 8e-3 for the matrix of low rank.  A rounding of X is multiplied by the a
+// of the steps still to come: where their product is below 48 (the last three states of five
+// default steps, 1e-4 in all) lo is not kept, which saves a third of the traffic.  Operands are stored times 2^10, so
 // that entries of 1e-4 stay clear of fp16's subnormal range.
 //
 // Both sides at most 128: one block keeps a matrix on chip through all steps
@@ -279,13 +281,19 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 old = half2_floats(w[i]);
-                        float x = fmaf(c2, v[8 * h + 2 * i], cb * old.x);
-                        float y = fmaf(c2, v[8 * h + 2 * i + 1], cb * old.y);
-                        const int col = half * 64 + 16 * q + 8 * h + 2 * i;
-                        if (col == row) { diag = x; x = 0.f; }
-                        if (col + 1 == row) { diag = y; y = 0.f; }
-                        w[i] = half2_bits(x, y);
+                        v[8 * h + 2 * i] = fmaf(c2, v[8 * h + 2 * i], cb * old.x);
+                        v[8 * h + 2 * i + 1] = fmaf(c2, v[8 * h + 2 * i + 1], cb * old.y);
                     }
+                    if (half * 8 + 2 * q + h == row >> 3) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (i == (row & 7)) {
+                                diag = v[8 * h + i];
+                                v[8 * h + i] = 0.f;
+                            }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = half2_bits(v[8 * h + 2 * i], v[8 * h + 2 * i + 1]);
                     *at = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
@@ -494,10 +502,13 @@ __device__ __forceinline__ void free_columns(uint32_t t, uint32_t n) {
 //   kSquare: out = alpha acc + beta in      (B from A A and A; likewise)
 //   kUpdate: X'  = alpha acc + beta X       (X and X' as hi + lo; the last one to bf16)
 // Roles (320 threads, one block an SM): warp 0 copies operand tiles in (kStages deep), warp 1
-// issues the products into one of two accumulators, warps 2-9 take the other through the
-// epilogue: 32 rows and every other chunk of 64 columns each.  The values to add and the
-// results go through shared memory, so that accesses to global memory are full rows of
-// 128 bytes.
+// issues the products into one of two accumulators, two teams of four warps (2-5, 6-9) take
+// them through the epilogue, 32 rows a warp, 64 columns at a time: every other chunk of a
+// tile each, or, where K is short and a block has several tiles, every other tile (the
+// epilogue's latency is what those would wait for: 612 matrices of 491 x 200 took 1440 us
+// without, 1260 with; the 2048 x 8240 projection, K of 2048 and more, 560 against
+// 590).  The values to add and the results go through shared
+// memory, so that accesses to global memory are full rows of 128 bytes.
 enum { kGram, kSquare, kUpdate };
 constexpr int kBM = 128, kBK = 64, kEpiWarps = 8, kGemmThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kChunkBytes = 32 * 128;              // 32 rows of 64 fp16 values
@@ -505,7 +516,7 @@ constexpr uint32_t kEpiBytes = kEpiWarps * 2 * kChunkBytes;   // (hi, lo) for ea
 
 // As many stages as fit beside the epilogue's buffers in 227 KB, at most 6.
 __host__ __device__ constexpr int stages_of(int CG, int BN) {
-    const int n = (int)((232448 - 1024 - 512 - kEpiBytes) / ((kBM + BN / CG) * 128));
+    const int n = (int)((232448 - 1024 - 3072 - kEpiBytes) / ((kBM + BN / CG) * 128));
     return n < 6 ? n : 6;
 }
 __host__ __device__ constexpr uint32_t stage_bytes(int CG, int BN) { return (kBM + BN / CG) * 128; }
@@ -521,8 +532,8 @@ struct GemmParams {
                                     // adds it to beta, by row (or by_column)
     float diag_scale;
     int by_column, diag_n;
-    const __half *in_hi, *in_lo;    // values to add, [batch][M][pitch]
-    __half *out_hi, *out_lo;        // results, [batch][M][pitch]
+    const __half *in_hi, *in_lo;    // values to add, [batch][M][pitch]; in_lo may be NULL
+    __half *out_hi, *out_lo;        // results, [batch][M][pitch]; out_lo may be NULL
     int pitch;                      // of all four, a multiple of 8
     __nv_bfloat16* last;            // kUpdate, last step: the result instead, [batch][M][N]
     int* status;
@@ -530,6 +541,7 @@ struct GemmParams {
 };
 
 struct GemmShared {
+    float cols[kEpiWarps][64];
     uint64_t full[6], empty[6], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int abort;
@@ -587,6 +599,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)cluster_rank() : 0;
     const int first = blockIdx.x / CG, stride = gridDim.x / CG;
+    const bool by_tile = p.tiles > stride && p.K <= 8 * kBK;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&S.full[i], 1);
@@ -594,7 +607,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.acc_full[i], 1);
-            mbar_init(&S.acc_empty[i], kEpiWarps * CG);
+            mbar_init(&S.acc_empty[i], (by_tile ? 4 : kEpiWarps) * CG);
         }
         fence_mbar_init();
         S.abort = 0;
@@ -686,10 +699,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             drain(&S.empty[s ? s - 1 : kStages - 1], s ? phase : phase ^ 1, p.limit);
     } else if (warp >= 2) {
         const int part = warp & 3;                      // this warp's lanes of tensor memory
-        const int turn = (warp - 2) >> 2;               // of the chunks, this warp's share
+        const int team = (warp - 2) >> 2;
+        const int turn = by_tile ? 0 : team, hop = by_tile ? 1 : 2;   // this warp's chunks
         unsigned char *hi = epi + (warp - 2) * 2 * kChunkBytes, *lo = hi + kChunkBytes;
         int n = 0;
         for (int t = first; t < p.tiles; t += stride, ++n) {
+            if (by_tile && (n & 1) != team) continue;
             const TileAt at = tile_at<EPI, TM, BN>(p, t);
             const int acc = n & 1, row0 = at.row + rank * kBM + part * 32;
             const size_t mat = (size_t)at.mat * p.M * p.pitch;
@@ -710,7 +725,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     const uint32_t d = smem_u32(hi) + r * 128 + ((piece ^ (r & 7)) << 4);
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
                                  "l"(in ? p.in_hi + o : p.in_hi), "r"(in ? 16 : 0) : "memory");
-                    if (EPI == kUpdate)
+                    if (EPI == kUpdate && p.in_lo)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + kChunkBytes),
                                      "l"(in ? p.in_lo + o : p.in_lo), "r"(in ? 16 : 0) : "memory");
                 }
@@ -718,7 +733,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (EPI != kGram && turn < chunks) fetch(turn);
             if (!wait_warp(&S.acc_full[acc], (n >> 1) & 1, &S.abort, p.status, p.limit)) break;
             tc_fence_after();
-            for (int c = turn; c < chunks; c += 2) {
+            for (int c = turn; c < chunks; c += hop) {
                 const int col0 = at.col + 64 * c;
                 if (EPI != kGram) {
                     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -728,7 +743,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const int row = row0 + lane;
                 const float* diag = p.diag + (size_t)at.mat * p.diag_n;
                 float keep = p.beta;
-                if (EPI == kUpdate && !p.by_column && row < p.M) keep = fmaf(p.diag_scale, diag[row], keep);
+                float* cols = S.cols[warp - 2];         // by column: this chunk's 64
+                if (EPI == kUpdate && p.by_column) {
+#pragma unroll
+                    for (int i = 0; i < 64; i += 32)
+                        cols[i + lane] = col0 + i + lane < p.N ? p.diag_scale * diag[col0 + i + lane] : 0.f;
+                    __syncwarp();
+                } else if (EPI == kUpdate && row < p.M) {
+                    keep = fmaf(p.diag_scale, diag[row], keep);
+                }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     float v[32];
@@ -761,34 +784,34 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         } else {
                             const uint4 u = *at_hi;
                             w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-                            if (EPI == kUpdate) {
+                            if (EPI == kUpdate && p.in_lo) {
                                 const uint4 y = *at_lo;
                                 z[0] = y.x; z[1] = y.y; z[2] = y.z; z[3] = y.w;
                             }
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 float2 x = half2_floats(w[i]);
-                                if (EPI == kUpdate) {
+                                if (EPI == kUpdate && p.in_lo) {
                                     const float2 y = half2_floats(z[i]);
                                     x.x += y.x;
                                     x.y += y.y;
                                 }
                                 float b0 = keep, b1 = keep;
-                                const int col = col0 + 32 * q + 8 * h + 2 * i;
                                 if (EPI == kUpdate && p.by_column) {
-                                    if (col < p.N) b0 = fmaf(p.diag_scale, diag[col], b0);
-                                    if (col + 1 < p.N) b1 = fmaf(p.diag_scale, diag[col + 1], b1);
+                                    const float2 e = *reinterpret_cast<const float2*>(cols + 32 * q + 8 * h + 2 * i);
+                                    b0 += e.x;
+                                    b1 += e.y;
                                 }
                                 f[2 * i] = fmaf(p.alpha, f[2 * i], b0 * x.x);
                                 f[2 * i + 1] = fmaf(p.alpha, f[2 * i + 1], b1 * x.y);
-                                if (EPI == kSquare && col == row && row < p.M) {
-                                    p.diag[(size_t)at.mat * p.diag_n + row] = f[2 * i];
-                                    f[2 * i] = 0.f;
-                                }
-                                if (EPI == kSquare && col + 1 == row && row < p.M) {
-                                    p.diag[(size_t)at.mat * p.diag_n + row] = f[2 * i + 1];
-                                    f[2 * i + 1] = 0.f;
-                                }
+                            }
+                            if (EPI == kSquare && col0 + 32 * q + 8 * h == (row & ~7) && row < p.M) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    if (i == (row & 7)) {
+                                        p.diag[(size_t)at.mat * p.diag_n + row] = f[i];
+                                        f[i] = 0.f;
+                                    }
                             }
                         }
 #pragma unroll
@@ -797,7 +820,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                 w[i] = bf162_bits(f[2 * i] * kUnscale, f[2 * i + 1] * kUnscale);
                             } else {
                                 w[i] = half2_bits(f[2 * i], f[2 * i + 1]);
-                                if (EPI == kUpdate) {
+                                if (EPI == kUpdate && p.out_lo) {
                                     const float2 x = half2_floats(w[i]);
                                     z[i] = half2_bits(f[2 * i] - x.x, f[2 * i + 1] - x.y);
                                 }
@@ -805,7 +828,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         }
                         *at_hi = make_uint4(w[0], w[1], w[2], w[3]);
                         if (EPI == kUpdate) {
-                            if (!p.last) *at_lo = make_uint4(z[0], z[1], z[2], z[3]);
+                            if (p.out_lo) *at_lo = make_uint4(z[0], z[1], z[2], z[3]);
                         } else if (mirror) {            // [64 columns][32 rows]
                             __half* m = reinterpret_cast<__half*>(lo) + (32 * q + 8 * h) * 32 + lane;
 #pragma unroll
@@ -829,7 +852,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         if (row0 + r < p.M && col < width) {
                             const size_t g = (size_t)(row0 + r) * width + col;
                             *reinterpret_cast<uint4*>(o_hi + g) = *reinterpret_cast<uint4*>(hi + o);
-                            if (EPI == kUpdate && !p.last)
+                            if (EPI == kUpdate && p.out_lo)
                                 *reinterpret_cast<uint4*>(p.out_lo + mat + g) = *reinterpret_cast<uint4*>(lo + o);
                         }
                     }
@@ -855,7 +878,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                 }
                 __syncwarp();
-                if (EPI != kGram && c + 2 < chunks) fetch(c + 2);
+                if (EPI != kGram && c + hop < chunks) fetch(c + hop);
             }
             tc_fence_before();
             __syncwarp();
@@ -1079,6 +1102,13 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         ++*launches;
         return cudaGetLastError();
     }
+    // what the steps after step i multiply a small singular value by
+    auto grows_after = [&](int i) {
+        float g = 1.f;
+        while (++i < a.steps) g *= std::fabs(a.coeffs[3 * i]);
+        return g;
+    };
+    bool has_lo = true;
     for (int i = 0; i < a.steps; ++i) {
         const float *c = a.coeffs + 3 * i;
         const Mat &x = hi[i & 1], &y = hi[(i & 1) ^ 1];
@@ -1123,7 +1153,9 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         p.beta = c[0];
         p.pitch = xp;
         p.in_hi = x.p;
-        p.in_lo = p.out_lo = lo;
+        p.in_lo = has_lo ? lo : nullptr;
+        has_lo = grows_after(i) >= 48.f;
+        p.out_lo = has_lo ? lo : nullptr;
         p.out_hi = y.p;
         p.last = i + 1 == a.steps ? static_cast<__nv_bfloat16*>(a.out) : nullptr;
         e = wide ? gemm<false, true, kUpdate>(B, x, p, s) : gemm<false, false, kUpdate>(x, B, p, s);
