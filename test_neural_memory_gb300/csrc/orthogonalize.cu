@@ -15,8 +15,8 @@
 // default steps, 1e-4 in all) lo is not kept, which saves a third of the traffic.  Operands are stored times 2^10, so
 // that entries of 1e-4 stay clear of fp16's subnormal range.
 //
-// Both sides at most 128: one block keeps a matrix on chip through all steps
-// (ns_small_kernel).  Larger: three products a step (ns_gemm_kernel).  A and
+// A short side of at most 128 and a long one of at most 1024: one block, or a cluster, keeps
+// a matrix on chip through all steps (ns_small_kernel).  Larger: three products a step (ns_gemm_kernel).  A and
 // B = b A + c A^2 are symmetric, so only their tiles on and below the diagonal are
 // computed and each is written twice, once transposed.
 #include <cuda.h>
@@ -103,14 +103,57 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, long long 
         if (clock64() - t0 > limit) return;
 }
 
-// --------------------------------------------------------------- one block a matrix
+// ------------------------------------------------------------------- clusters (PTX)
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of the same shared variable in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float peer_load(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void peer_store2(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+
+// ------------------------------------------------- one block, or one cluster, a matrix
 
 // X, 128 x 128 zero-padded, as fp16 operands in two halves of 64 columns (rows of 128 bytes,
 // 128-byte swizzle), its fp32 values in registers: thread (row, half) holds 64 of them.
 // A, then B in its place, likewise.  Per step three products into the same 128 columns of
 // tensor memory, each followed by its epilogue; two blocks share an SM, so that one's
 // products run beside the other's epilogue.
-constexpr int kSide = 128, kSmallThreads = 256;
+//
+// kCluster: a long side of up to 1024 is split over the blocks of a cluster, 128 columns each.
+// A is then a sum over the blocks: each leaves its share in shared memory (fp32), adds a
+// range of rows over all blocks in their order and hands the result to all of them;
+// everything else stays a block's own.  (2 x 709 x 37: 88 us as products from global
+// memory.)
+constexpr int kSide = 128, kSmallThreads = 256, kMaxCluster = 8;
 constexpr uint32_t kHalfBytes = kSide * 128;            // 64 columns of an operand
 constexpr uint32_t kOperandBytes = 2 * kHalfBytes;
 
@@ -119,6 +162,7 @@ struct SmallShared {
     uint32_t tmem;
     int abort;
     float part[kSmallThreads / 32];
+    float sum;
     float diag[kSide];
 };
 
@@ -127,17 +171,22 @@ __device__ __forceinline__ uint4* operand_at(unsigned char* base, int row, int c
                                     (((chunk & 7) ^ (row & 7)) << 4));
 }
 
-__global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid_constant__ OrthoArgs a) {
+template <bool kCluster>
+__global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
+    ns_small_kernel(const __grid_constant__ OrthoArgs a) {
     extern __shared__ unsigned char raw[];
     unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     unsigned char *sx = base, *sa = base + kOperandBytes;
-    SmallShared& S = *reinterpret_cast<SmallShared*>(base + 2 * kOperandBytes);
+    unsigned char* shares = base + 2 * kOperandBytes;   // kCluster: this block's share of A
+    SmallShared& S = *reinterpret_cast<SmallShared*>(shares + (kCluster ? kSide * kSide * 4 : 0));
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const bool wide = a.m <= a.n;
-    const int r = wide ? a.m : a.n, l = wide ? a.n : a.m;
+    const int rank = kCluster ? (int)cluster_rank() : 0, ranks = kCluster ? (int)cluster_size() : 1;
+    const int c0 = rank * kSide;                        // of the long side: this block's columns
+    const int r = wide ? a.m : a.n, l = min((wide ? a.n : a.m) - c0, kSide);
     const int rp = r <= 64 ? 64 : 128, lp = l <= 64 ? 64 : 128;
     const int row = (warp & 3) * 32 + lane, half = warp >> 2;
-    const size_t mat = (size_t)blockIdx.x * a.m * a.n;
+    const size_t mat = (size_t)(blockIdx.x / ranks) * a.m * a.n;
 
     if (warp == 0) tmem_alloc(&S.tmem, 128);
     if (tid == 0) {
@@ -156,13 +205,15 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
             return reinterpret_cast<float*>(base + i * 512 + (((j >> 2) ^ (i & 7)) << 4) + (j & 3) * 4);
         };
         if (a.n % 4 == 0) {
-            const int per = a.n / 4;
+            const int per = l / 4;
 #pragma unroll 4
             for (int i = tid; i < a.m * per; i += kSmallThreads)
-                *reinterpret_cast<float4*>(at(i / per, i % per * 4)) = load4(a, mat + (size_t)i * 4);
+                *reinterpret_cast<float4*>(at(i / per, i % per * 4)) =
+                    load4(a, mat + (size_t)(i / per) * a.n + c0 + i % per * 4);
         } else {
 #pragma unroll 4
-            for (int i = tid; i < a.m * a.n; i += kSmallThreads) *at(i / a.n, i % a.n) = load1(a, mat + i);
+            for (int i = tid; i < a.m * l; i += kSmallThreads)
+                *at(i / l, i % l) = load1(a, mat + (size_t)(i / l) * a.n + c0 + i % l);
         }
         __syncthreads();
 #pragma unroll
@@ -177,7 +228,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
 #pragma unroll
         for (int c = 0; c < 64; ++c) {
             const int col = half * 64 + c;
-            X[c] = row < r && col < l ? load1(a, mat + (size_t)col * a.n + row) : 0.f;
+            X[c] = row < r && col < l ? load1(a, mat + (size_t)(c0 + col) * a.n + row) : 0.f;
         }
     }
     float s = 0.f;
@@ -191,6 +242,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
     const uint32_t tmem = S.tmem;
     s = 0.f;
     for (int w = 0; w < kSmallThreads / 32; ++w) s += S.part[w];
+    if (kCluster) {                                     // the norm is that of all blocks' columns
+        if (tid == 0) S.sum = s;
+        cluster_sync();
+        s = 0.f;
+        for (int i = 0; i < ranks; ++i) s += peer_load(peer_addr(&S.sum, i));
+    }
     const float inv = inverse_norm(s, a.eps) * kScale;
 #pragma unroll
     for (int c = 0; c < 64; ++c) X[c] *= inv;
@@ -234,7 +291,44 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
         }
         if (!wait_product()) break;
         const bool mine = half * 64 < rp;               // columns of A and B that exist
-        if (mine) {
+        if (kCluster) {
+            // rows of 512 bytes, 16-byte groups permuted by row
+            auto group = [&](int i, int g) { return shares + i * 512 + ((g ^ (i & 7)) << 4); };
+            if (mine) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float v[16];
+                    tmem_ld16(acc + 16 * q, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        *reinterpret_cast<float4*>(group(row, half * 16 + 4 * q + h)) =
+                            make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+                }
+            }
+            tc_fence_before();
+            cluster_sync();                             // every block's share is written
+            tc_fence_after();
+            const int rows = (rp + ranks - 1) / ranks, groups = rp / 4;
+#pragma unroll 2
+            for (int i = tid; i < rows * groups; i += kSmallThreads) {
+                const int y = rank * rows + i / groups, g = i % groups;
+                if (y >= rp) break;
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f), q[kMaxCluster];
+#pragma unroll
+                for (int k = 0; k < kMaxCluster; ++k)
+                    if (k < ranks) q[k] = peer_load4(peer_addr(group(y, g), k));
+#pragma unroll
+                for (int k = 0; k < kMaxCluster; ++k)
+                    if (k < ranks) { t.x += q[k].x; t.y += q[k].y; t.z += q[k].z; t.w += q[k].w; }
+                const uint32_t lo = half2_bits(t.x * kUnscale, t.y * kUnscale);
+                const uint32_t hi = half2_bits(t.z * kUnscale, t.w * kUnscale);
+                const unsigned char* at = reinterpret_cast<unsigned char*>(operand_at(sa, y, g >> 1)) + (g & 1) * 8;
+                for (int k = 0; k < ranks; ++k) peer_store2(peer_addr(at, k), lo, hi);
+            }
+            asm volatile("fence.proxy.async;" ::: "memory");
+            cluster_sync();                             // A is whole in every block
+        } else if (mine) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float v[16];
@@ -334,7 +428,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
             const int col = half * 64 + 8 * q;
             const float* f = X + 8 * q;
             if (row < r && col < l)
-                *reinterpret_cast<uint4*>(out + (size_t)row * a.n + col) =
+                *reinterpret_cast<uint4*>(out + (size_t)row * a.n + c0 + col) =
                     make_uint4(bf162_bits(f[0] * kUnscale, f[1] * kUnscale),
                                bf162_bits(f[2] * kUnscale, f[3] * kUnscale),
                                bf162_bits(f[4] * kUnscale, f[5] * kUnscale),
@@ -345,7 +439,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
         for (int c = 0; c < 64; ++c) {
             const int col = half * 64 + c;
             if (row < r && col < l)
-                out[wide ? (size_t)row * a.n + col : (size_t)col * a.n + row] =
+                out[wide ? (size_t)row * a.n + c0 + col : (size_t)(c0 + col) * a.n + row] =
                     __float2bfloat16(X[c] * kUnscale);
         }
     }
@@ -353,6 +447,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) ns_small_kernel(const __grid
     __syncthreads();
     if (S.abort && tid == 0) drain(&S.done, phase, a.wait_cycles);
     __syncthreads();
+    if (kCluster) cluster_sync();                       // no access to a block that has left
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 128);
 }
@@ -434,20 +529,6 @@ __global__ void __launch_bounds__(256) ns_round_kernel(int m, int n, int pitch, 
 
 // ------------------------------------------------------- two blocks on one tile (PTX)
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Address of the same shared variable in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
-}
 __device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -978,7 +1059,12 @@ Workspace layout(int batch, int m, int n) {
     return w;
 }
 
-bool small(int m, int n) { return m <= kSide && n <= kSide; }
+// Whether a call stays on chip: blocks of 128 columns, up to two for each SM where a matrix takes
+// several (20 x 128 x 1024: 80 us so, 140 us as products; 300 x 100 x 900: 1075 and 452).
+bool small(int batch, int m, int n) {
+    const int r = m < n ? m : n, ranks = ((m < n ? n : m) + kSide - 1) / kSide;
+    return r <= kSide && (ranks == 1 || (ranks <= kMaxCluster && (long long)batch * ranks <= 2 * 152));
+}
 
 // A stored fp16 matrix batch: [batch][rows][pitch].
 struct Mat {
@@ -992,17 +1078,17 @@ struct Mat {
     }
 };
 
-// Launches a kernel whose set-up may overlap the one before (after_previous), in clusters of
-// `cluster` blocks.
+// Launches a kernel in clusters of `cluster` blocks; `overlap`: its set-up may run beside the
+// kernel before (after_previous).
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
-                         const A&... args) {
+cudaError_t launch_in_clusters(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                               int cluster, bool overlap, const A&... args) {
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
+    at[1].val.programmaticStreamSerializationAllowed = overlap;
     cudaLaunchConfig_t c{};
     c.gridDim = grid;
     c.blockDim = block;
@@ -1028,8 +1114,8 @@ cudaError_t gemm_tiles(const Mat& A, const Mat& B, GemmParams p, cudaStream_t s)
     auto kernel = ns_gemm_kernel<AMN, BMN, EPI, CG, BN>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_after(kernel, dim3(CG * (p.tiles < 152 / CG ? p.tiles : 152 / CG)), dim3(kGemmThreads), smem, s, CG,
-                        ma, mb, p);
+    return launch_in_clusters(kernel, dim3(CG * (p.tiles < 152 / CG ? p.tiles : 152 / CG)), dim3(kGemmThreads), smem, s,
+                              CG, true, ma, mb, p);
 }
 
 // The tile that takes the least time by this count: rounds of tiles over the SMs times a tile's
@@ -1054,20 +1140,27 @@ cudaError_t gemm(const Mat& A, const Mat& B, const GemmParams& p, cudaStream_t s
 }  // namespace
 
 size_t ortho_workspace_bytes(int batch, int m, int n) {
-    return small(m, n) ? 0 : layout(batch, m, n).total;
+    return small(batch, m, n) ? 0 : layout(batch, m, n).total;
 }
 
 cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
     OrthoArgs a = in;
     if (a.wait_cycles <= 0) a.wait_cycles = kWaitCycles;
-    if (small(a.m, a.n)) {
-        constexpr int smem = 1024 + 2 * kOperandBytes + sizeof(SmallShared);
-        const cudaError_t e =
-            cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        ns_small_kernel<<<a.batch, kSmallThreads, smem, s>>>(a);
+    if (small(a.batch, a.m, a.n)) {
+        constexpr int smem = 1024 + 2 * kOperandBytes + sizeof(SmallShared), shares = kSide * kSide * 4;
+        const int ranks = ((a.m > a.n ? a.m : a.n) + kSide - 1) / kSide;
         *launches = 1;
-        return cudaGetLastError();
+        cudaError_t e;
+        if (ranks == 1) {
+            e = cudaFuncSetAttribute(ns_small_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            ns_small_kernel<false><<<a.batch, kSmallThreads, smem, s>>>(a);
+            return cudaGetLastError();
+        }
+        e = cudaFuncSetAttribute(ns_small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem + shares);
+        if (e != cudaSuccess) return e;
+        return launch_in_clusters(ns_small_kernel<true>, dim3(a.batch * ranks), dim3(kSmallThreads), smem + shares, s,
+                                  ranks, false, a);
     }
     const Workspace w = layout(a.batch, a.m, a.n);
     char* ws = static_cast<char*>(a.workspace);
@@ -1132,7 +1225,7 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         if (e != cudaSuccess) return e;
         if (splits > 1) {
             const unsigned t = (r + 31) / 32;
-            e = launch_after(ns_join_kernel, dim3(t, t, a.batch), dim3(256), 0, s, 1, (const float*)p.parts, splits,
+            e = launch_in_clusters(ns_join_kernel, dim3(t, t, a.batch), dim3(256), 0, s, 1, true, (const float*)p.parts, splits,
                              a.batch, r, p.part_pitch, ap, A.p);
             if (e != cudaSuccess) return e;
             ++*launches;

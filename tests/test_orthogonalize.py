@@ -63,7 +63,8 @@ def check(G, coeffs, **kw):
                                        (2, 128, 100), (300, 16, 24), (1, 129, 129), (2, 200, 131),
                                        (1, 96, 700), (1, 700, 96), (2, 256, 256), (1, 257, 1031),
                                        (1, 768, 777), (3, 640, 300), (2, 40, 2000), (1, 1999, 37),
-                                       (1, 130, 3001), (1, 1601, 9), (3, 1300, 70)])
+                                       (1, 130, 3001), (1, 1601, 9), (3, 1300, 70), (3, 128, 1024),
+                                       (2, 5, 130), (2, 1023, 128), (90, 64, 385), (1, 66, 643)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["normal", "low rank"])
 def test_against_float64(batch, m, n, dtype, kind):
