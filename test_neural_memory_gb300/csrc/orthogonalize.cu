@@ -605,6 +605,7 @@ __host__ __device__ constexpr uint32_t stage_bytes(int CG, int BN) { return (kBM
 struct GemmParams {
     int M, N, K, batch;
     int tiles_m, tiles_n, per_matrix, tiles;
+    int whole;                      // kUpdate, BN = 256: tiles before the halved ones
     int splits, split_blocks;       // kGram: parts of K, blocks of K in a part
     float* parts;                   // splits > 1: [splits][batch][M][part_pitch]
     int part_pitch;
@@ -629,12 +630,15 @@ struct GemmShared {
 };
 
 struct TileAt {
-    int row, col, mat;
+    int row, col, mat, width;       // width: BN, or half of it
     int k0, k1, split;              // its blocks of K
 };
 
 // Tile t: all tiles (columns outermost, so that tiles at work share columns of X), or for the
-// symmetric results those with an element on or below the diagonal, row by row.
+// symmetric results those with an element on or below the diagonal, row by row.  Where the last
+// round of tiles 256 wide would leave more than half of the blocks idle, its tiles are halved.
+template <int EPI, int TM, int BN> constexpr bool kHalves = EPI == kUpdate && TM == 256 && BN == 256;
+
 template <int EPI, int TM, int BN>
 __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
     TileAt at;
@@ -648,11 +652,16 @@ __device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
         at.k0 = at.split * p.split_blocks;
         at.k1 = min(kblocks, at.k0 + p.split_blocks);
     }
+    const bool halved = kHalves<EPI, TM, BN> && t >= p.whole;
+    const int part = halved ? (t - p.whole) & 1 : 0;
+    if (halved) t = p.whole + ((t - p.whole) >> 1);
     at.mat = t / p.per_matrix;
     t -= at.mat * p.per_matrix;
+    at.width = BN;
     if (EPI == kUpdate) {
         at.row = t % p.tiles_m * TM;
-        at.col = t / p.tiles_m * BN;
+        at.col = t / p.tiles_m * BN + part * (BN / 2);
+        if (halved) at.width = BN / 2;
         return at;
     }
     int i = 0;
@@ -707,13 +716,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int t = first; t < p.tiles && ok; t += stride) {
             TileAt at = tile_at<EPI, TM, BN>(p, t);
             at.row += rank * kBM;
-            at.col += rank * (BN / CG);
+            at.col += rank * (at.width / CG);
+            // a halved tile's B in rows of K is copied whole all the same
+            const uint32_t stage = kBM * 128 + (BMN ? at.width : BN) / CG * 128;
             for (int k = at.k0; k < at.k1; ++k, ++it) {
                 const int s = it % kStages;
                 ok = wait_one(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort, p.status, p.limit);
                 if (!ok) break;
                 unsigned char *da = base + s * kStage, *db = da + kBM * 128;
-                if (rank == 0) mbar_expect_tx(&S.full[s], CG * kStage);
+                if (rank == 0) mbar_expect_tx(&S.full[s], CG * stage);
                 const uint32_t bar = CG == 2 ? peer_addr(&S.full[s], 0) : 0;
                 auto load = [&](unsigned char* dst, const CUtensorMap* m, int x, int y) {
                     if (CG == 2) tma_load_3d_pair(dst, m, bar, x, y, at.mat);
@@ -725,7 +736,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     load(da, &ma, k * kBK, at.row);
                 }
                 if (BMN) {
-                    for (int i = 0; i < BN / CG / 64; ++i) load(db + i * 8192, &mb, at.col + 64 * i, k * kBK);
+                    for (int i = 0; i < at.width / CG / 64; ++i) load(db + i * 8192, &mb, at.col + 64 * i, k * kBK);
                 } else {
                     load(db, &mb, k * kBK, at.col);
                 }
@@ -738,7 +749,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         // The whole warp walks the loop, so that descriptors stay in uniform registers, and one
         // elected lane issues: with a single lane in the loop a product left every 137 cycles
         // whatever its size.
-        constexpr uint32_t id = idesc_f16(TM, BN, AMN, BMN);
         constexpr uint32_t step_a = (AMN ? 2048 : 32) >> 4, step_b = (BMN ? 2048 : 32) >> 4;
         const uint32_t base_u = __shfl_sync(0xffffffffu, smem_u32(base), 0);
         const uint64_t a0 = AMN ? sdesc(base_u, 8192, 1024, 2) : sdesc(base_u, 16, 1024, 2);
@@ -753,6 +763,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             tc_fence_after();
             const uint32_t d = tmem + acc * BN;
             const TileAt at = tile_at<EPI, TM, BN>(p, t);
+            const uint32_t id = at.width == BN ? idesc_f16(TM, BN, AMN, BMN) : idesc_f16(TM, BN / 2, AMN, BMN);
             for (int k = at.k0; k < at.k1; ++k) {
                 ok = wait_warp(&S.full[s], phase, &S.abort, p.status, p.limit);
                 if (!ok) break;
@@ -791,7 +802,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const size_t mat = (size_t)at.mat * p.M * p.pitch;
             // chunks of 64 columns that have an element to write: a prefix
             int chunks = 0;
-            if (row0 < p.M) chunks = min(BN / 64, (p.N - at.col + 63) / 64);
+            if (row0 < p.M) chunks = max(0, min(at.width / 64, (p.N - at.col + 63) / 64));
             if (EPI != kUpdate && chunks > 0)
                 chunks = min(chunks, max(0, (row0 + 31 - at.col) / 64 + (row0 + 31 >= at.col)));
             // rows of 128 bytes: lane l takes 16 bytes l % 8 of rows l / 8, l / 8 + 4, ..
@@ -1105,8 +1116,15 @@ cudaError_t gemm_tiles(const Mat& A, const Mat& B, GemmParams p, cudaStream_t s)
     p.tiles_n = (p.N + BN - 1) / BN;
     p.per_matrix = tiles_of(EPI, p.M, p.N, kBM * CG, BN);
     const long long tiles = (long long)p.per_matrix * p.batch * (EPI == kGram && p.splits > 1 ? p.splits : 1);
-    if (tiles > (1LL << 31) - 1) return cudaErrorInvalidValue;
-    p.tiles = (int)tiles;
+    if (tiles > (1LL << 30)) return cudaErrorInvalidValue;
+    p.tiles = p.whole = (int)tiles;
+    if (kHalves<EPI, kBM * CG, BN>) {
+        const int rest = p.tiles % (152 / CG);
+        if (rest <= 152 / CG / 2) {
+            p.whole -= rest;
+            p.tiles += rest;
+        }
+    }
     CUtensorMap ma, mb;
     if (!A.map(&ma, 64, AMN ? 64 : kBM) || !B.map(&mb, 64, BMN ? 64 : BN / CG)) return cudaErrorInvalidValue;
     constexpr int smem = 1024 + stages_of(CG, BN) * stage_bytes(CG, BN) + kEpiBytes + sizeof(GemmShared);
@@ -1125,8 +1143,10 @@ cudaError_t gemm(const Mat& A, const Mat& B, const GemmParams& p, cudaStream_t s
     if (EPI == kGram && p.splits > 1) return gemm_tiles<AMN, BMN, EPI, 1, 64>(A, B, p, s);
     auto cost = [&](int CG, int BN, double block) {
         const long long tiles = (long long)tiles_of(EPI, p.M, p.N, kBM * CG, BN) * p.batch;
-        const long long slots = 152 / CG, rounds = (tiles + slots - 1) / slots;
-        return (double)rounds * ((p.K + kBK - 1) / kBK * block + 20.0 * BN) + 4000;
+        const long long slots = 152 / CG, rest = tiles % slots;
+        const bool halves = EPI == kUpdate && CG == 2 && BN == 256 && rest <= slots / 2;
+        const double rounds = (double)(tiles / slots) + (rest == 0 ? 0. : (halves ? 0.6 : 1.));
+        return rounds * ((p.K + kBK - 1) / kBK * block + 20.0 * BN) + 4000;
     };
     const double c64 = cost(1, 64, 490), c128 = cost(1, 128, 650), p128 = cost(2, 128, 490),
                  p256 = cost(2, 256, 660);

@@ -64,7 +64,8 @@ def check(G, coeffs, **kw):
                                        (1, 96, 700), (1, 700, 96), (2, 256, 256), (1, 257, 1031),
                                        (1, 768, 777), (3, 640, 300), (2, 40, 2000), (1, 1999, 37),
                                        (1, 130, 3001), (1, 1601, 9), (3, 1300, 70), (3, 128, 1024),
-                                       (2, 5, 130), (2, 1023, 128), (90, 64, 385), (1, 66, 643)])
+                                       (2, 5, 130), (2, 1023, 128), (90, 64, 385), (1, 66, 643),
+                                       (40, 260, 500), (41, 500, 260)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["normal", "low rank"])
 def test_against_float64(batch, m, n, dtype, kind):
