@@ -741,9 +741,10 @@ __device__ __forceinline__ void put_wide(E* p, const float (&f)[W]) {
     }
 }
 
-// Token by token: one thread per W channels (the widest of 16 bytes, four channels and one
-// that all rows start on), the state in registers.
-template <typename E, bool kToken, int W>
+// Token by token: one thread per W channels, the state in registers.  The outputs overlap no
+// input, so the loads of B tokens go out together, ahead of their stores (1 x 128 x 64, bf16: 10 us
+// against 25 with one token's loads at a time).
+template <typename E, bool kToken, int W, int B>
 __global__ void glr_serial_kernel(GlrArgs a, const float* start) {
     const int per = (a.D + W - 1) / W;
     const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -759,25 +760,96 @@ __global__ void glr_serial_kernel(GlrArgs a, const float* start) {
     const E* gc = static_cast<const E*>(a.g) + n * a.g_seq + d;
     const float* gt = static_cast<const float*>(a.g) + n * a.g_seq;
     E* h = static_cast<E*>(a.h) + n * a.T * a.D + d;
-#pragma unroll 4
-    for (int t = 0; t < a.T; ++t) {
-        float xv[W], gv[W];
-        get_wide(x + (long long)t * a.x_tok, xv);
-        if (!kToken) get_wide(gc + (long long)t * a.g_tok, gv);
-        const float rt = kToken ? retention(gt[(long long)t * a.g_tok]) : 0.f;
+    for (int t0 = 0; t0 < a.T; t0 += B) {
+        float xv[B][W], gv[B][kToken ? 1 : W];
 #pragma unroll
-        for (int v = 0; v < W; ++v) s[v] = fmaf(kToken ? rt : retention(gv[v]), s[v], xv[v]);
-        put_wide(h + (size_t)t * a.D, s);
+        for (int b = 0; b < B; ++b) {
+            const long long t = min(t0 + b, a.T - 1);
+            get_wide(x + t * a.x_tok, xv[b]);
+            if constexpr (kToken) gv[b][0] = gt[t * a.g_tok];
+            else get_wide(gc + t * a.g_tok, gv[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (t0 + b >= a.T) break;
+            const float rt = kToken ? retention(gv[b][0]) : 0.f;
+#pragma unroll
+            for (int v = 0; v < W; ++v) s[v] = fmaf(kToken ? rt : retention(gv[b][v]), s[v], xv[b][v]);
+            put_wide(h + (size_t)(t0 + b) * a.D, s);
+        }
     }
     put_wide(a.h_last + nd, s);
 }
 
+// The gradient likewise, from the last token on (gates per channel: a token gate's sum over the
+// channels is the tiles' work).
+template <typename E, int W, int B>
+__global__ void glr_serial_back_kernel(GlrArgs a) {
+    const int per = (a.D + W - 1) / W;
+    const size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (size_t)a.N * per) return;
+    const size_t n = i / per;
+    const int d = (int)(i % per) * W;
+    const size_t nd = n * a.D + d, at = n * a.T * a.D + d;
+    float c[W], first[W];
+#pragma unroll
+    for (int v = 0; v < W; ++v) c[v] = first[v] = 0.f;
+    if (a.dh_last) get_wide(a.dh_last + nd, c);
+    if (a.h0) get_wide(a.h0 + nd, first);
+    const E* dh = static_cast<const E*>(a.x) + n * a.x_seq + d;
+    const E* g = static_cast<const E*>(a.g) + n * a.g_seq + d;
+    const E* h = static_cast<const E*>(a.h) + at;
+    E *dx = static_cast<E*>(a.dx) + at, *dg = static_cast<E*>(a.dg) + at;
+    for (int t0 = a.T - 1; t0 >= 0; t0 -= B) {
+        float G[B][W], gv[B][W], before[B][W];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const long long t = max(t0 - b, 0);
+            get_wide(dh + t * a.x_tok, G[b]);
+            get_wide(g + t * a.g_tok, gv[b]);
+            get_wide(h + max(t - 1, 0ll) * a.D, before[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int t = t0 - b;
+            if (t < 0) break;
+#pragma unroll
+            for (int v = 0; v < W; ++v) {
+                G[b][v] += c[v];
+                c[v] = retention(gv[b][v]) * G[b][v];
+                before[b][v] = c[v] * (t > 0 ? before[b][v] : first[v]);
+            }
+            put_wide(dx + (size_t)t * a.D, G[b]);
+            put_wide(dg + (size_t)t * a.D, before[b]);
+        }
+    }
+    if (a.dh0) put_wide(a.dh0 + nd, c);
+}
+
 // ------------------------------------------------------------------------- host
 
-// Token by token where a tile would be mostly empty, and where the channels alone keep the
-// SMs busy (8 x 152 x 128 threads of four): nothing is joined or waited for then.
-bool by_tokens(const GlrArgs& a) {
-    return a.T <= 8 || (size_t)a.N * a.D >= 4ull * 152 * 1024;
+// Channels a thread of the token by token kernels takes: 16 bytes where that still makes a thread
+// for every lane of the GPU's SMs, else four, or one where the rows do not allow it.
+int thread_width(const GlrArgs& a) {
+    const int es = a.bf16 ? 2 : 4;
+    int width = access_width(a.x, a.N > 1 ? a.x_seq : 0, a.T > 1 ? a.x_tok : 0, es);
+    if (!a.gate_token)
+        width = min(width, access_width(a.g, a.N > 1 ? a.g_seq : 0, a.T > 1 ? a.g_tok : 0, es));
+    if (es == 2 && width == 16 && a.D % 8 == 0 && (size_t)a.N * a.D >= 8ull * 152 * 1024) return 8;
+    return width >= V * es && a.D % V == 0 ? V : 1;
+}
+
+// Token by token where a sequence is short, where it is short against the number of tiles that
+// sequences make, and where the channels alone keep the SMs busy: nothing is joined or waited for
+// then.  A token takes 0.08 us (0.14 in the gradient), a round of tiles 3.3.  In us, by tokens and
+// by tiles, bf16, forward / gradient: 1 x 16 x 64 2.3 / 3.4 and 3.6 / 3.4, 1 x 32 x 64 3.6 / 5.3 and
+// 3.8 / 3.4; 64 x 48 x 768 5.2 / 7.5 and 10.7 / 9.0, 64 x 96 x 768 8.6 / 13.5 and 10.8 / 9.5;
+// 200 x 128 x 2048 49 / 82 and 67 / 80; 512 x 512 x 2048 gradient 827 and 889.
+bool by_tokens(const GlrArgs& a, bool back) {
+    if (back && a.gate_token) return false;
+    const size_t strips = (size_t)a.N * ((a.D + kChans - 1) / kChans);
+    return a.T <= 16 || (a.T <= 128 && strips >= 16 * (size_t)a.T) ||
+           (size_t)a.N * a.D >= thread_width(a) * (152ull * 1024);
 }
 
 TilePlan make_plan(const GlrArgs& a, int backward, size_t* bytes) {
@@ -883,45 +955,50 @@ cudaError_t tiles(GlrArgs a, bool back, cudaStream_t s, int* launches) {
     return cudaGetLastError();
 }
 
-template <typename E, int W>
-cudaError_t serial_launch(const GlrArgs& a, const float* start, cudaStream_t s) {
+template <typename E, int W, int B>
+cudaError_t serial_launch(const GlrArgs& a, bool back, const float* start, cudaStream_t s) {
     const size_t threads = (size_t)a.N * (a.D / W);
     const unsigned blocks = (unsigned)((threads + 127) / 128);
-    if (a.gate_token) glr_serial_kernel<E, true, W><<<blocks, 128, 0, s>>>(a, start);
-    else glr_serial_kernel<E, false, W><<<blocks, 128, 0, s>>>(a, start);
+    if (back) glr_serial_back_kernel<E, W, W == 1 || B == 1 ? B : B / 2><<<blocks, 128, 0, s>>>(a);
+    else if (a.gate_token) glr_serial_kernel<E, true, W, B><<<blocks, 128, 0, s>>>(a, start);
+    else glr_serial_kernel<E, false, W, B><<<blocks, 128, 0, s>>>(a, start);
     return cudaGetLastError();
 }
 
+// One or two tokens one by one: loads past the end cost more than they hide (1228 tokens of 3371
+// channels, bf16: 39 us by eight, 20 by one).
+template <typename E, int W>
+cudaError_t serial_batches(const GlrArgs& a, bool back, const float* start, cudaStream_t s) {
+    return a.T <= 2 ? serial_launch<E, W, 1>(a, back, start, s)
+                    : serial_launch<E, W, W == 8 ? 4 : 8>(a, back, start, s);
+}
+
 template <typename E>
-cudaError_t serial(const GlrArgs& a, const float* start, cudaStream_t s) {
-    const int es = sizeof(E);
-    int width = access_width(a.x, a.N > 1 ? a.x_seq : 0, a.T > 1 ? a.x_tok : 0, es);
-    if (!a.gate_token)
-        width = min(width, access_width(a.g, a.N > 1 ? a.g_seq : 0, a.T > 1 ? a.g_tok : 0, es));
-    // 16 bytes a thread where that still makes a thread for every lane of the GPU's SMs
-    if (es == 2 && width == 16 && a.D % 8 == 0 && (size_t)a.N * a.D >= 8ull * 152 * 1024)
-        return serial_launch<E, 8>(a, start, s);
-    if (width >= V * es && a.D % V == 0) return serial_launch<E, V>(a, start, s);
-    return serial_launch<E, 1>(a, start, s);
+cudaError_t serial(const GlrArgs& a, bool back, const float* start, cudaStream_t s) {
+    const int width = thread_width(a);
+    if constexpr (sizeof(E) == 2)
+        if (width == 8) return serial_batches<E, 8>(a, back, start, s);
+    if (width == V) return serial_batches<E, V>(a, back, start, s);
+    return serial_batches<E, 1>(a, back, start, s);
 }
 
 }  // namespace
 
 size_t glr_workspace_bytes(const GlrArgs& a, int backward) {
     size_t bytes = 0;
-    if (backward || !by_tokens(a)) make_plan(a, backward, &bytes);
+    if (!by_tokens(a, backward != 0)) make_plan(a, backward, &bytes);
     return bytes;
 }
 
 cudaError_t glr_fwd_launch(const GlrArgs& a, cudaStream_t s, int* launches) {
-    if (!by_tokens(a))
+    if (!by_tokens(a, false))
         return a.bf16 ? tiles<__nv_bfloat16>(a, false, s, launches) : tiles<float>(a, false, s, launches);
     *launches = 1;
-    return a.bf16 ? serial<__nv_bfloat16>(a, a.h0, s) : serial<float>(a, a.h0, s);
+    return a.bf16 ? serial<__nv_bfloat16>(a, false, a.h0, s) : serial<float>(a, false, a.h0, s);
 }
 
 cudaError_t glr_step_launch(const GlrArgs& a, cudaStream_t s) {
-    return a.bf16 ? serial<__nv_bfloat16>(a, a.h_last, s) : serial<float>(a, a.h_last, s);
+    return a.bf16 ? serial<__nv_bfloat16>(a, false, a.h_last, s) : serial<float>(a, false, a.h_last, s);
 }
 
 cudaError_t glr_bwd_launch(const GlrArgs& a, cudaStream_t s, int* launches) {
@@ -932,7 +1009,10 @@ cudaError_t glr_bwd_launch(const GlrArgs& a, cudaStream_t s, int* launches) {
         return a.dh_last ? cudaMemcpyAsync(a.dh0, a.dh_last, bytes, cudaMemcpyDeviceToDevice, s)
                          : cudaMemsetAsync(a.dh0, 0, bytes, s);
     }
-    return a.bf16 ? tiles<__nv_bfloat16>(a, true, s, launches) : tiles<float>(a, true, s, launches);
+    if (!by_tokens(a, true))
+        return a.bf16 ? tiles<__nv_bfloat16>(a, true, s, launches) : tiles<float>(a, true, s, launches);
+    *launches = 1;
+    return a.bf16 ? serial<__nv_bfloat16>(a, true, nullptr, s) : serial<float>(a, true, nullptr, s);
 }
 
 }  // namespace ttm

@@ -300,3 +300,30 @@ def test_refusals():
         assert e.value.code == ttm.ERR_INVALID_ARG
     with pytest.raises(TypeError):
         ttm.glr_fwd(x.half(), g.half())
+
+
+@pytest.mark.parametrize("N,T,D", [(1, 16, 64), (2, 10, 36), (3, 15, 7), (300, 18, 70), (64, 48, 768),
+                                   (160, 21, 1001), (160, 130, 1001), (2500, 3, 512), (2500, 7, 512),
+                                   (3000, 2, 44)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("token,pad", [(False, 0), (False, 3), (True, 0)])
+def test_short_sequences_and_many_channels(N, T, D, dtype, token, pad):
+    x, g, h0 = make(N, T, D, dtype, token, seed=N + T, resets=True)
+    dh = make(N, T, D, dtype, True, seed=N + T + 1)[0]
+
+    def view(t):
+        wide = torch.full(t.shape[:-1] + (t.shape[-1] + pad,), math.nan, dtype=t.dtype, device="cuda")
+        wide[..., :t.shape[-1]] = t.cuda()
+        return wide[..., :t.shape[-1]]
+
+    xc, gc, dhc = view(x), (view(g) if not token else g.cuda()), view(dh)
+    h, last = ttm.glr_fwd(xc, gc, h0=on(h0))
+    rh, th, rl, tl = reference(x, g, h0)
+    close(h, rh, th, x.dtype)
+    close(last, rl, tl, torch.float32)
+    rh = rh.to(x.dtype)
+    out = ttm.glr_bwd(gc, on(rh), dhc, h0=on(h0))
+    dx, tx, dg, tg, c, tc = grad_reference(g, rh, h0, dh, None)
+    close(out["dx"], dx, tx, x.dtype)
+    close(out["dg"], dg, tg, g.dtype)
+    close(out["dh0"], c, tc, torch.float32)
