@@ -14,10 +14,18 @@
 //
 // Layout: TPR threads share a row, each K packs of W values that are TPR packs apart
 // (every access of a warp is contiguous), ROWS rows at a time so that enough loads are
-// in flight and one reduction serves several rows.  TPR is 8 or 32 (shuffles) for
-// short rows and the whole block of 256 (shuffles, then shared memory) for long ones.
-// Rows longer than the registers hold are read again from the cache instead.
-// W is the widest pack that the rows' alignment and D allow.
+// in flight and one reduction serves several rows.  TPR is the rows' packs up to a warp
+// (shuffles), or the whole block of 256 (shuffles, then shared memory) for long rows; a warp
+// takes rows of up to 1024 single values, in which a block of 256 would mostly wait at barriers
+// (697568 x 169 bf16, gradient: 679 us with a row a block, 236 with a row a warp).  Rows longer
+// than the registers hold are read again from the cache instead.  W is the widest pack that the
+// rows' alignment and D allow; rows of x and dy that do not start on 16 bytes are read in 16-byte
+// words all the same and shifted into place (238817 x 768 bf16 from rows of 771, forward: 318 us
+// value by value, 137 so).
+//
+// Measured, bf16, forward and gradient: 131072 x 2048 199 and 264 us (5.4 and 6.1 TB/s of 6.8 that a
+// copy reaches), 786432 x 64 40 and 50 us, 100000 x 512 41 and 54 us, 8000 x 8192 60 and 105 us (its
+// sums of dw and db take the registers of one of the two blocks an SM).
 //
 // The gradient's blocks leave their dw, db sums in the workspace and a second kernel adds
 // them in a fixed order: no atomics, so equal inputs give equal bits.
@@ -90,6 +98,46 @@ struct Pack {
     }
 };
 
+// A pack on its way from global memory; kShift: from a row that does not start on 16 bytes.  That one
+// is read in the aligned 16-byte words that hold a value of it, two as a rule (the second one a
+// neighbour's first, so from L1), and shifted into place when it is taken.
+template <typename E, int W, bool kShift>
+struct Coming {
+    Pack<E, W> p;
+    __device__ __forceinline__ void zero() { p.zero(); }
+    __device__ __forceinline__ void load(const E* at, int) { p.load(at); }
+    __device__ __forceinline__ Pack<E, W> take(int) const { return p; }
+};
+template <typename E, int W>
+struct Coming<E, W, true> {
+    uint4 u, v;
+    __device__ __forceinline__ void zero() { u = v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const E* at, int shift) {   // shift: of `at` past 16 bytes
+        const uint4* w = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(at) - shift);
+        u = w[0];
+        if (shift) v = w[1];
+    }
+    __device__ __forceinline__ Pack<E, W> take(int shift) const {
+        static_assert(sizeof(Pack<E, W>) == 16, "16 bytes");
+        uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        if (shift & 8)
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        if (shift & 4)
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        Pack<E, W> r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.d.w[i] = sizeof(E) == 4 ? w[i] : __funnelshift_r(w[i], w[i + 1], (shift & 3) * 8);
+        return r;
+    }
+};
+template <typename E>
+__device__ __forceinline__ int shift_of(const E* row) {
+    return (int)(reinterpret_cast<uintptr_t>(row) & 15);
+}
+
 // W weights (fp32, or `absent` each), 16 bytes at a time.
 template <int W, typename T, int N>
 __device__ __forceinline__ void load_weights(const float* p, T (&f)[N], float absent) {
@@ -136,7 +184,7 @@ __device__ __forceinline__ void row_sums(float (&s)[C], float (*buf)[kWarps]) {
     }
 }
 
-template <typename E, int W, int TPR, int K, int ROWS>
+template <typename E, int W, bool kShift, int TPR, int K, int ROWS>
 __global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const __grid_constant__ LayerNormArgs a) {
     using P = Pack<E, W>;
     using T = typename P::T;
@@ -147,21 +195,26 @@ __global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const __grid_constant_
     const float inv = 1.f / a.D;
     const E* x = static_cast<const E*>(a.x);
     const long long r0 = (long long)blockIdx.x * kSets * ROWS + set;   // rows r0 + i kSets
+    Coming<E, W, kShift> coming[ROWS][K];
     P in[ROWS][K];
     float s[ROWS], mean[ROWS], rstd[ROWS];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i)
+    for (int i = 0; i < ROWS; ++i) {
+        const E* row = x + (r0 + i * kSets) * a.x_row;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            in[i][k].zero();
+            coming[i][k].zero();
             if (r0 + i * kSets < a.N && lane + k * TPR < packs)
-                in[i][k].load(x + (r0 + i * kSets) * a.x_row + (lane + k * TPR) * W);
+                coming[i][k].load(row + (lane + k * TPR) * W, shift_of(row));
         }
+    }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         T t = splat<T>(0.f);
+        const int shift = shift_of(x + (r0 + i * kSets) * a.x_row);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
+            in[i][k] = coming[i][k].take(shift);
 #pragma unroll
             for (int j = 0; j < N; ++j) t = add(t, in[i][k].get(j));
             in[i][k].repack();
@@ -218,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const __grid_constant_
         }
 }
 
-template <typename E, int W, int TPR, int K, int ROWS, int BLOCKS>
+template <typename E, int W, bool kShift, int TPR, int K, int ROWS, int BLOCKS>
 __global__ void __launch_bounds__(kThreads, BLOCKS) ln_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
     using P = Pack<E, W>;
     using T = typename P::T;
@@ -234,13 +287,14 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) ln_bwd_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j < N; ++j) dw[k][j] = db[k][j] = splat<T>(0.f);
     // the next rows are asked for before the reduction of these
-    P nx[ROWS][K], nd[ROWS][K];
+    Coming<E, W, kShift> nx[ROWS][K], nd[ROWS][K];
     float nmean[ROWS], nrstd[ROWS];
     auto fetch = [&](long long r0) {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             const long long r = r0 + i * kSets + set;
             const bool in = r < a.N;
+            const E *xr = x + r * a.x_row, *dr = dy + r * a.dy_row;
             nmean[i] = in ? a.mean[r] : 0.f;
             nrstd[i] = in ? a.rstd[r] : 0.f;
 #pragma unroll
@@ -249,29 +303,33 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) ln_bwd_kernel(const __grid_c
                 nx[i][k].zero();
                 nd[i][k].zero();
                 if (in && lane + k * TPR < packs) {
-                    nx[i][k].load(x + r * a.x_row + c);
-                    nd[i][k].load(dy + r * a.dy_row + c);
+                    nx[i][k].load(xr + c, shift_of(xr));
+                    nd[i][k].load(dr + c, shift_of(dr));
                 }
             }
         }
     };
+    constexpr bool kAhead = K * W <= 32;                // or the registers are full
     int turn = 0;
     const long long stride = (long long)gridDim.x * kSets * ROWS;
-    fetch((long long)blockIdx.x * kSets * ROWS);
+    if (kAhead) fetch((long long)blockIdx.x * kSets * ROWS);
     for (long long r0 = (long long)blockIdx.x * kSets * ROWS; r0 < a.N; r0 += stride, turn ^= 1) {
+        if (!kAhead) fetch(r0);
         P px[ROWS][K], pd[ROWS][K];
         float mean[ROWS], rstd[ROWS], s[2 * ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
+            const long long r = r0 + i * kSets + set;
+            const int sx = shift_of(x + r * a.x_row), sd = shift_of(dy + r * a.dy_row);
             mean[i] = nmean[i];
             rstd[i] = nrstd[i];
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                px[i][k] = nx[i][k];
-                pd[i][k] = nd[i][k];
+                px[i][k] = nx[i][k].take(sx);
+                pd[i][k] = nd[i][k].take(sd);
             }
         }
-        fetch(r0 + stride);
+        if (kAhead) fetch(r0 + stride);
         T su[ROWS], sn[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) su[i] = sn[i] = splat<T>(0.f);
@@ -465,18 +523,27 @@ __global__ void __launch_bounds__(512) ln_join_kernel(const float* part, int blo
 constexpr int kResident = 2;
 constexpr int kMaxBlocks = 152 * kResident;
 
-template <typename E, int W, int TPR, int K>
+// Whether the gradient shifts rows into place: fp32 rows read value by value, which need half the
+// registers on the way, are faster between these lengths (100000 x 512: 94 us against 122, 16000 x
+// 4096: 132 and 209; but 1000000 x 24: 137 and 93).
+template <typename E>
+constexpr bool shift_pays(int D) {
+    return sizeof(E) == 2 || D <= 32 || D > 4096;
+}
+
+template <typename E, int W, bool kShift, int TPR, int K>
 cudaError_t run(const LayerNormArgs& a, bool back, int blocks, cudaStream_t s) {
-    constexpr int sets = kThreads / TPR, bytes = W * K * (int)sizeof(E);
+    constexpr int sets = kThreads / TPR, word = W * (int)sizeof(E) < 4 ? 4 : W * (int)sizeof(E);
+    constexpr int bytes = K * word;                     // of registers for a row
     if (!back) {
         constexpr int rows = bytes >= 64 ? 1 : (bytes >= 32 ? 2 : 4);   // 64 bytes in flight a thread
         const long long need = ((long long)a.N + sets * rows - 1) / (sets * rows);
-        ln_fwd_kernel<E, W, TPR, K, rows><<<(unsigned)need, kThreads, 0, s>>>(a);
-    } else {
-        constexpr int rows = bytes > 32 ? 1 : 2;
-        constexpr int resident = K * W <= 16 ? kResident : 1;
+        ln_fwd_kernel<E, W, kShift, TPR, K, rows><<<(unsigned)need, kThreads, 0, s>>>(a);
+    } else if constexpr (!kShift || shift_pays<E>(TPR * K * W)) {
+        constexpr int rows = bytes > (kShift ? 16 : 32) || K * W > 8 ? 1 : 2;
+        constexpr int resident = K * W <= (kShift ? 8 : 16) ? kResident : 1;
         const size_t shared = TPR == kThreads || !a.partial ? 0 : (size_t)kWarps * 2 * TPR * K * W * 4;
-        auto kernel = ln_bwd_kernel<E, W, TPR, K, rows, resident>;
+        auto kernel = ln_bwd_kernel<E, W, kShift, TPR, K, rows, resident>;
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) return e;
@@ -485,7 +552,8 @@ cudaError_t run(const LayerNormArgs& a, bool back, int blocks, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// Widest pack the rows allow: 16 bytes, 4 bytes, one value.
+// Widest pack the rows allow: 16 bytes (0: shifted into place, where only the outputs' rows start on
+// 16 bytes), 4 bytes, one value.
 template <typename E>
 int pack_width(const LayerNormArgs& a, bool back) {
     auto fits = [&](int w) {
@@ -495,20 +563,37 @@ int pack_width(const LayerNormArgs& a, bool back) {
         return !back || (reinterpret_cast<uintptr_t>(a.dy) % b == 0 &&
                          (a.N <= 1 || a.dy_row * sizeof(E) % b == 0));
     };
-    if (fits(16 / sizeof(E))) return 16 / sizeof(E);
+    if (a.D % (16 / sizeof(E)) == 0 && fits(16 / sizeof(E))) return 16 / sizeof(E);
+    if (a.D % (16 / sizeof(E)) == 0 && (!back || shift_pays<E>(a.D))) return 0;
     return sizeof(E) == 2 && fits(2) ? 2 : 1;
 }
 
-template <typename E, int W>
+template <typename E, int W, bool kShift = false>
 cudaError_t by_length(const LayerNormArgs& a, bool back, int blocks, cudaStream_t s) {
     const int packs = a.D / W;
-    if (packs <= 8) return run<E, W, 8, 1>(a, back, blocks, s);
-    if (packs <= 32) return run<E, W, 32, 1>(a, back, blocks, s);
-    if (packs <= 64) return run<E, W, 32, 2>(a, back, blocks, s);
-    if (packs <= 128) return run<E, W, 32, 4>(a, back, blocks, s);
-    if (packs <= 256) return run<E, W, 256, 1>(a, back, blocks, s);
-    if (packs <= 512) return run<E, W, 256, 2>(a, back, blocks, s);
-    if (packs <= 1024) return run<E, W, 256, 4>(a, back, blocks, s);
+    if (packs <= 4) return run<E, W, kShift, 4, 1>(a, back, blocks, s);
+    if (packs <= 8) return run<E, W, kShift, 8, 1>(a, back, blocks, s);
+    if (packs <= 16) return run<E, W, kShift, 16, 1>(a, back, blocks, s);
+    if (packs <= 32) return run<E, W, kShift, 32, 1>(a, back, blocks, s);
+    if (packs <= 64) return run<E, W, kShift, 32, 2>(a, back, blocks, s);
+    if constexpr (W > 2)
+        if (packs <= 96) return run<E, W, kShift, 32, 3>(a, back, blocks, s);
+    if (packs <= 128) return run<E, W, kShift, 32, 4>(a, back, blocks, s);
+    if constexpr (W <= 2) {
+        if (packs <= 256) return run<E, W, kShift, 32, 8>(a, back, blocks, s);
+        if (packs <= 512) return run<E, W, kShift, 32, 16>(a, back, blocks, s);
+        if constexpr (W == 1)
+            if (packs <= 1024) return run<E, W, kShift, 32, 32>(a, back, blocks, s);
+        if (packs <= 1024) return run<E, W, kShift, 256, 4>(a, back, blocks, s);
+        if (packs <= 2048) return run<E, W, kShift, 256, 8>(a, back, blocks, s);
+        if (packs <= 4096) return run<E, W, kShift, 256, 16>(a, back, blocks, s);
+    } else {
+        if (packs <= 256) return run<E, W, kShift, 256, 1>(a, back, blocks, s);
+        if (packs <= 512) return run<E, W, kShift, 256, 2>(a, back, blocks, s);
+        if (packs <= 1024) return run<E, W, kShift, 256, 4>(a, back, blocks, s);
+        if constexpr (W == 4 || !kShift)
+            if (packs <= 2048) return run<E, W, kShift, 256, 8>(a, back, blocks, s);
+    }
     if (!back) ln_fwd_long_kernel<E><<<a.N < 152 * 4 ? a.N : 152 * 4, kLongThreads, 0, s>>>(a);
     else ln_bwd_long_kernel<E><<<blocks, kLongThreads, 0, s>>>(a);
     return cudaGetLastError();
@@ -520,6 +605,7 @@ cudaError_t by_width(const LayerNormArgs& a, bool back, int blocks, cudaStream_t
     if (w == 1) return by_length<E, 1>(a, back, blocks, s);
     if constexpr (sizeof(E) == 2)
         if (w == 2) return by_length<E, 2>(a, back, blocks, s);
+    if (w == 0) return by_length<E, 16 / (int)sizeof(E), true>(a, back, blocks, s);
     return by_length<E, 16 / (int)sizeof(E)>(a, back, blocks, s);
 }
 

@@ -174,3 +174,12 @@ def test_refusals():
         assert e.value.code == ttm.ERR_INVALID_ARG
     with pytest.raises(TypeError):
         ttm.layer_norm_fwd(x.half())
+
+
+@pytest.mark.parametrize("N,D", [(70, 3), (70, 12), (300, 16), (70, 24), (70, 32), (70, 96), (70, 131), (70, 300),
+                                 (70, 500), (70, 513), (330, 771), (330, 600), (40, 1026), (40, 1600), (40, 2050),
+                                 (20, 3074), (20, 4098), (700, 6000), (330, 8184), (700, 12000)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pad", [0, 3, 1, 2, 4])
+def test_row_lengths_and_starts(N, D, dtype, pad):
+    test_forward_and_gradient(N, D, dtype, pad != 1, pad)
