@@ -458,13 +458,17 @@ int ttm_lmm_layer_fwd(int B, int T, int H, int d, int chunk, int conv_k,
  *   x_seq, x_tok (g_seq, g_tok): elements between sequences and between tokens,
  *     at least D (1 for a token gate) where there is more than one, so that x
  *     and g may be columns of wider rows; channels are contiguous.  x and g need
- *     the alignment of their type only, every other pointer 16 bytes.
+ *     the alignment of their type only, every other pointer 16 bytes.  Rows that
+ *     start elsewhere are read in the aligned 16-byte words that hold a byte of
+ *     them.
  *   workspace: ttm_glr_workspace_size(..., 0) bytes of device scratch (NULL when
  *     that is 0); its contents on entry are ignored.
  * Shapes: N, D >= 1, T >= 0, N D < 2^31 (else TTM_ERR_UNSUPPORTED); T = 0 gives
  * h_last = h0.  No output may overlap an input, another output or the workspace.
- * Asynchronous on `stream`; TTM_ERR_INVALID_ARG for malformed arguments,
- * TTM_ERR_CUDA if a launch fails.
+ * Long sequences are split over blocks that hand the state on with bounded waits:
+ * ttm_device_status reports TTM_ERR_TIMEOUT, and the outputs are invalid, if one
+ * ran out.  Equal inputs give equal bits.  Asynchronous on `stream`;
+ * TTM_ERR_INVALID_ARG for malformed arguments, TTM_ERR_CUDA if a launch fails.
  */
 typedef enum { TTM_GATE_CHANNEL = 0, TTM_GATE_TOKEN = 1 } ttm_gate;
 size_t ttm_glr_workspace_size(int N, int T, int D, int dtype, int gate, int backward);
@@ -506,7 +510,9 @@ int ttm_glr_step(int N, int n, int D, int dtype, int gate,
  *     y = (x - mean) rstd w + b
  * (the norm in f(x) = x + LN(W x) of "Continual Learning: From Attention to
  * Neural Memory" §4.7, and of every residual block around the memory).
- *   x: N rows in dtype, x_row >= D elements apart, aligned to its type.
+ *   x: N rows in dtype, x_row >= D elements apart, aligned to its type (rows that
+ *     start elsewhere than on 16 bytes may be read in the aligned 16-byte words that
+ *     hold a value of them).
  *   w, b: [D] fp32 or NULL (1 and 0).  y: [N][D] in dtype, contiguous.
  *   mean, rstd: [N] fp32, written for the gradient, or NULL.
  * Statistics and arithmetic are fp32; the variance is taken about the mean.
@@ -543,6 +549,9 @@ int ttm_layer_norm_bwd(int N, int D, int dtype, const void* dy, long long dy_row
  *   coeffs: HOST array of steps x (a, b, c), finite; read during the call.
  *   workspace: ttm_orthogonalize_workspace_size() bytes of device scratch.
  * |G|_F is summed in fp32 (it must stay below 1e19).  A zero matrix gives zero.
+ * The products take fp16 operands and add in fp32, X itself is kept to about fp32's
+ * accuracy: with the usual coefficients the result is 2e-3 of its norm off (bf16
+ * rounding alone: 1.7e-3).  Device waits are bounded: see ttm_device_status.
  * Shapes: batch, m, n >= 1, 0 <= steps <= 32, eps > 0; batch <= 65535 and
  * m, n <= TTM_ORTHO_MAX_DIM (else TTM_ERR_UNSUPPORTED).  All device pointers are
  * 16-byte aligned; no overlap.  Asynchronous on `stream`; TTM_ERR_INVALID_ARG

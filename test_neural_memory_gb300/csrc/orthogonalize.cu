@@ -554,6 +554,451 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
             smem_u32(bar)), "h"((uint16_t)3)
         : "memory");
 }
+// ------------------------------------------------- a short side of at most 128, in A alone
+//
+// A step multiplies X by a polynomial of A = X X^T: X <- P X, P = a I + b A + c A^2, after which
+// A <- P A P, and all of these commute.  So X_n = Q X_0 with Q the product of the steps' P, and the
+// steps need A alone: G is read for |G|_F, for A_0 and for Q X_0, three times in all and not
+// twice a step.  What that costs is accuracy: a rounding of A_0 is not put right by the next step's
+// A.  Every operand here is therefore a sum hi + lo of two fp16 values, and a product takes hi hi +
+// hi lo + lo hi: 1e-4 off for a matrix of low rank plus noise, 1e-5 for a normal one, before
+// the result is rounded to bf16.  Roundings grow as small singular values do, so coefficients that grow these by
+// more than 1024 in all take the other path (tame).
+//
+//   ns_gram_kernel:  A_0 by parts of the long side, 128 of it at a time (fp32 sums)
+//   ns_poly_kernel:  Q from A_0, a block a matrix
+//   ns_apply_kernel: Q X_0, 128 of the long side at a time
+//
+// MARK
+constexpr float kQScale = 32.f;
+constexpr int kGramThreads = 256;
+constexpr uint32_t kTileBytes = 2 * kOperandBytes;      // hi and lo
+
+struct GramShared {
+    uint64_t done;
+    uint32_t tmem;
+    int abort;
+};
+
+// hi and lo of eight values.
+__device__ __forceinline__ void split8(const float* f, uint4& hi, uint4& lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = half2_bits(f[2 * i], f[2 * i + 1]);
+        const float2 x = half2_floats(h[i]);
+        l[i] = half2_bits(f[2 * i] - x.x, f[2 * i + 1] - x.y);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// acc (+)= (hi + lo)(hi + lo) but for lo lo, over `steps` blocks of 16 of K; AMN, BMN: the operand's
+// rows are K.  `lo` of each lies `a_lo`, `b_lo` bytes behind its hi.
+__device__ __forceinline__ void mma_split(uint32_t acc, uint32_t a, uint32_t a_lo, bool amn, uint32_t b,
+                                          uint32_t b_lo, bool bmn, int N, int steps, bool add) {
+    const uint32_t id = idesc_f16(128, N, amn, bmn);
+    const uint64_t a0 = sdesc(a, amn ? kHalfBytes : 16, 1024, 2), b0 = sdesc(b, bmn ? kHalfBytes : 16, 1024, 2);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (k >= steps) break;
+        const uint32_t across = (k >> 2) * kHalfBytes + (k & 3) * 32, down = k * 2048;
+        const uint64_t ah = a0 + ((amn ? down : across) >> 4), bh = b0 + ((bmn ? down : across) >> 4);
+        mma_bf16(acc, ah, bh, id, add || k > 0);
+        mma_bf16(acc, ah, bh + (b_lo >> 4), id, true);
+        mma_bf16(acc, ah + (a_lo >> 4), bh, id, true);
+    }
+}
+
+// rows x cols of G from element `at` on, times scale, as an operand hi and lo; zero up to multiples
+// of 16.  Batches of loads go out together.
+__device__ __forceinline__ void load_tile(const OrthoArgs& a, size_t at, int rows, int cols, float scale,
+                                          unsigned char* hi) {
+    unsigned char* lo = hi + kOperandBytes;
+    const int r16 = (rows + 15) & ~15, c16 = (cols + 15) & ~15;
+    const int tid = threadIdx.x, wide = a.n % 4 == 0 ? 4 : 2;
+    int log = 2;                                        // threads side by side over the columns
+    while ((wide << log) < c16) ++log;
+    const int col = (tid & ((1 << log) - 1)) * wide, step = kGramThreads >> log;
+    if (col >= c16) return;
+    const uint32_t swz = ((col & 63) * 2) & 15;
+    constexpr int B = 8;
+    for (int r0 = tid >> log; r0 < r16; r0 += B * step) {
+        float4 g[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int row = r0 + i * step;
+            g[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row >= rows) continue;
+            const size_t e = at + (size_t)row * a.n + col;
+            if (wide == 4) {
+                if (col < cols) g[i] = load4(a, e);
+            } else {
+                if (col < cols) g[i].x = load1(a, e);
+                if (col + 1 < cols) g[i].y = load1(a, e + 1);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int row = r0 + i * step;
+            if (row >= r16) break;
+            const uint32_t o = (uint32_t)(reinterpret_cast<unsigned char*>(operand_at(hi, row, col >> 3)) - hi) + swz;
+            const float x0 = g[i].x * scale, x1 = g[i].y * scale, x2 = g[i].z * scale, x3 = g[i].w * scale;
+            const uint32_t h0 = half2_bits(x0, x1);
+            const float2 f0 = half2_floats(h0);
+            const uint32_t l0 = half2_bits(x0 - f0.x, x1 - f0.y);
+            if (wide == 4) {
+                const uint32_t h1 = half2_bits(x2, x3);
+                const float2 f1 = half2_floats(h1);
+                *reinterpret_cast<uint2*>(hi + o) = make_uint2(h0, h1);
+                *reinterpret_cast<uint2*>(lo + o) = make_uint2(l0, half2_bits(x2 - f1.x, x3 - f1.y));
+            } else {
+                *reinterpret_cast<uint32_t*>(hi + o) = h0;
+                *reinterpret_cast<uint32_t*>(lo + o) = l0;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float start_scale(const OrthoArgs& a, const float* part, int parts, size_t mat) {
+    float s = 0.f;
+    for (int i = threadIdx.x; i < parts; i += 256) s += part[mat * parts + i];
+    return inverse_norm(block_sum(s), a.eps) * kScale;
+}
+
+// Operands in shared memory, accumulators read: the next product may be issued.
+__device__ __forceinline__ void operands_ready() {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+}
+
+struct GramPlan {
+    int rp;                         // the short side, 64 or 128
+    int chunks;                     // of 128 of the long side
+    int gram_parts, gram_each;      // parts of a matrix in ns_gram_kernel, chunks of a part
+    int apply_parts, apply_each;
+    int norm_parts;
+    float *norm, *sums;             // sums: [matrix][part][column / 4][row][4]
+    unsigned char* q;               // Q as an operand, hi and lo, [matrix]
+};
+
+__global__ void __launch_bounds__(kGramThreads, 3)
+    ns_gram_kernel(const __grid_constant__ OrthoArgs a, const __grid_constant__ GramPlan p) {
+    extern __shared__ unsigned char raw[];
+    unsigned char* tile = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    GramShared& S = *reinterpret_cast<GramShared*>(tile + kTileBytes);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const bool wide = a.m <= a.n;
+    const int r = wide ? a.m : a.n, l = wide ? a.n : a.m;
+    const size_t mat = blockIdx.x / p.gram_parts;
+    const int part = blockIdx.x % p.gram_parts;
+    if (warp == 0) tmem_alloc(&S.tmem, 128);
+    if (tid == 0) {
+        mbar_init(&S.done, 1);
+        fence_mbar_init();
+        S.abort = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    after_previous();
+    const float scale = start_scale(a, p.norm, p.norm_parts, mat);
+    const int c0 = part * p.gram_each, c1 = min(p.chunks, c0 + p.gram_each);
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int c = c0; c < c1; ++c) {
+        const int at = c * kSide, len = min(kSide, l - at);
+        if (c > c0) {
+            ok = wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles);
+            if (__syncthreads_or(!ok)) break;
+            phase ^= 1;
+        }
+        load_tile(a, mat * a.m * a.n + (wide ? (size_t)at : (size_t)at * a.n), wide ? r : len, wide ? len : r, scale,
+                  tile);
+        operands_ready();
+        if (warp == 0) {
+            if (elect_one()) {
+                const uint32_t x = smem_u32(tile);
+                mma_split(tmem, x, kOperandBytes, !wide, x, kOperandBytes, !wide, p.rp, (len + 15) / 16, c > c0);
+                mma_commit(&S.done);
+            }
+            __syncwarp();
+        }
+    }
+    if (ok) ok = wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles);
+    tc_fence_after();
+    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+    if (ok && half * 64 < p.rp && (warp & 3) * 32 < p.rp) {
+        float* to = p.sums + ((size_t)blockIdx.x * p.rp * p.rp) + (size_t)half * 64 * p.rp + row * 4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float v[16];
+            tmem_ld16(tmem_addr(tmem, (warp & 3) * 32, half * 64 + 16 * q), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                *reinterpret_cast<float4*>(to + (size_t)(4 * q + h) * 4 * p.rp) =
+                    make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (S.abort && tid == 0) drain(&S.done, phase, a.wait_cycles);
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 128);
+}
+
+__global__ void __launch_bounds__(kGramThreads)
+    ns_poly_kernel(const __grid_constant__ OrthoArgs a, const __grid_constant__ GramPlan p) {
+    extern __shared__ unsigned char raw[];
+    unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    const uint32_t ob = p.rp / 64 * kHalfBytes;         // an operand; its lo follows its hi
+    unsigned char *sa = base, *sp = base + 2 * ob, *sq = base + 4 * ob;
+    GramShared& S = *reinterpret_cast<GramShared*>(base + 6 * ob);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int r = a.m <= a.n ? a.m : a.n, row = (warp & 3) * 32 + lane, half = warp >> 2;
+    const bool mine = half * 64 < p.rp;                 // columns that exist
+    const size_t mat = blockIdx.x;
+    if (warp == 0) tmem_alloc(&S.tmem, 256);
+    if (tid == 0) {
+        mbar_init(&S.done, 1);
+        fence_mbar_init();
+        S.abort = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem, acc = tmem_addr(tmem, (warp & 3) * 32, half * 64);
+    after_previous();
+
+    auto put = [&](unsigned char* to, int q, const float* f) {   // columns 8 q .. of this thread's 64
+        uint4 hi, lo;
+        split8(f, hi, lo);
+        uint4* at = operand_at(to, row, half * 8 + q);
+        *at = hi;
+        *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(at) + ob) = lo;
+    };
+    // A_0 from the parts, in their order; zero past the short side
+    float A[64];
+#pragma unroll
+    for (int c = 0; c < 64; ++c) A[c] = 0.f;
+    if (mine && row < r) {
+        for (int k = 0; k < p.gram_parts; ++k) {
+            const float* from = p.sums + ((mat * p.gram_parts + k) * p.rp * p.rp) + (size_t)half * 64 * p.rp + row * 4;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const float4 v = *reinterpret_cast<const float4*>(from + (size_t)q * 4 * p.rp);
+                A[4 * q] += v.x; A[4 * q + 1] += v.y; A[4 * q + 2] += v.z; A[4 * q + 3] += v.w;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 64; ++c) A[c] = half * 64 + c < r ? A[c] * (kUnscale * kUnscale) : 0.f;
+    }
+    auto put_A = [&]() {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = A[8 * q + i] * kScale;
+            put(sa, q, f);
+        }
+    };
+    if (mine) put_A();
+    uint32_t phase = 0;
+    const int steps = (r + 15) / 16;
+    auto product = [&](uint32_t column, const unsigned char* x, const unsigned char* y) {
+        mma_split(tmem_addr(tmem, 0, column), smem_u32(x), ob, false, smem_u32(y), ob, false, p.rp, steps, false);
+    };
+    // the same verdict in every warp: all of them meet at the barriers that follow
+    auto finished = [&]() {
+        const bool ok = wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles);
+        if (__syncthreads_or(!ok)) return false;
+        phase ^= 1;
+        tc_fence_after();
+        return true;
+    };
+    bool ok = true;
+    for (int k = 0; k < a.steps; ++k) {
+        const float ca = a.coeffs[3 * k], cb = a.coeffs[3 * k + 1], cc = a.coeffs[3 * k + 2];
+        const bool last = k + 1 == a.steps;
+        operands_ready();
+        if (warp == 0) {
+            if (elect_one()) {
+                product(0, sa, sa);
+                mma_commit(&S.done);
+            }
+            __syncwarp();
+        }
+        if (!(ok = finished())) break;
+        if (mine) {                                     // P; the first is Q too
+            const float c2 = cc * (kUnscale * kUnscale);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                tmem_ld16(acc + 16 * q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int col = half * 64 + 16 * q + i;
+                    v[i] = fmaf(c2, v[i], cb * A[16 * q + i]) + (col == row && row < r ? ca : 0.f);
+                }
+                float f[16];
+                if (k == 0) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) f[i] = v[i] * kQScale;
+                    put(sq, 2 * q, f);
+                    put(sq, 2 * q + 1, f + 8);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] = v[i] * kScale;
+                put(sp, 2 * q, f);
+                put(sp, 2 * q + 1, f + 8);
+            }
+        }
+        if (last && k == 0) break;
+        operands_ready();
+        if (warp == 0) {
+            if (elect_one()) {
+                if (!last) product(0, sp, sa);
+                if (k > 0) product(128, sp, sq);
+                mma_commit(&S.done);
+            }
+            __syncwarp();
+        }
+        if (!(ok = finished())) break;
+        if (mine) {                                     // P A over A, P Q over Q
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                if (!last) {
+                    tmem_ld16(acc + 16 * q, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] *= kUnscale;
+                    put(sa, 2 * q, v);
+                    put(sa, 2 * q + 1, v + 8);
+                }
+                if (k > 0) {
+                    tmem_ld16(acc + 128 + 16 * q, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] *= kUnscale;
+                    put(sq, 2 * q, v);
+                    put(sq, 2 * q + 1, v + 8);
+                }
+            }
+        }
+        if (last) break;
+        operands_ready();
+        if (warp == 0) {
+            if (elect_one()) {
+                product(0, sa, sp);
+                mma_commit(&S.done);
+            }
+            __syncwarp();
+        }
+        if (!(ok = finished())) break;
+        if (mine) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                tmem_ld16(acc + 16 * q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) A[16 * q + i] = v[i] * (kUnscale * kUnscale);
+            }
+            put_A();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (ok) {
+        uint4* to = reinterpret_cast<uint4*>(p.q + mat * 2 * ob);
+        for (uint32_t i = tid; i < 2 * ob / 16; i += kGramThreads) to[i] = reinterpret_cast<const uint4*>(sq)[i];
+    }
+    if (S.abort && tid == 0) drain(&S.done, phase, a.wait_cycles);
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 256);
+}
+
+// A wide G's tile is the first operand, with the long side as its rows, a tall one's the second, with
+// the long side as the accumulators' columns: either way neighbouring lanes write neighbouring
+// elements.
+__global__ void __launch_bounds__(kGramThreads)
+    ns_apply_kernel(const __grid_constant__ OrthoArgs a, const __grid_constant__ GramPlan p) {
+    extern __shared__ unsigned char raw[];
+    unsigned char* tile = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    const uint32_t ob = p.rp / 64 * kHalfBytes;
+    unsigned char* sq = tile + kTileBytes;
+    GramShared& S = *reinterpret_cast<GramShared*>(sq + 2 * ob);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const bool wide = a.m <= a.n;
+    const int r = wide ? a.m : a.n, l = wide ? a.n : a.m;
+    const size_t mat = blockIdx.x / p.apply_parts, mn = (size_t)a.m * a.n;
+    const int part = blockIdx.x % p.apply_parts;
+    if (warp == 0) tmem_alloc(&S.tmem, 128);
+    if (tid == 0) {
+        mbar_init(&S.done, 1);
+        fence_mbar_init();
+        S.abort = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    after_previous();
+    const float scale = start_scale(a, p.norm, p.norm_parts, mat);
+    const uint4* from = reinterpret_cast<const uint4*>(p.q + mat * 2 * ob);
+    for (uint32_t i = tid; i < 2 * ob / 16; i += kGramThreads) reinterpret_cast<uint4*>(sq)[i] = from[i];
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + mat * mn;
+    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+    const int c0 = part * p.apply_each, c1 = min(p.chunks, c0 + p.apply_each);
+    uint32_t phase = 0;
+    for (int c = c0; c < c1; ++c) {
+        const int at = c * kSide, len = min(kSide, l - at);
+        load_tile(a, mat * mn + (wide ? (size_t)at : (size_t)at * a.n), wide ? r : len, wide ? len : r, scale, tile);
+        operands_ready();
+        if (warp == 0) {
+            if (elect_one()) {
+                const uint32_t x = smem_u32(tile), q = smem_u32(sq);
+                if (wide) mma_split(tmem, x, kOperandBytes, true, q, ob, false, p.rp, (r + 15) / 16, false);
+                else mma_split(tmem, q, ob, false, x, kOperandBytes, false, 128, (r + 15) / 16, false);
+                mma_commit(&S.done);
+            }
+            __syncwarp();
+        }
+        const bool ok = wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles);
+        if (__syncthreads_or(!ok)) break;
+        phase ^= 1;
+        tc_fence_after();
+        const int rows = wide ? len : r, cols = wide ? r : len;   // of the accumulators
+        if (half * 64 < cols && (warp & 3) * 32 < rows) {
+            __nv_bfloat16* o = out + (wide ? (size_t)at + row : (size_t)at * a.n + row) + (size_t)half * 64 * a.n;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[16];
+                tmem_ld16(tmem_addr(tmem, (warp & 3) * 32, half * 64 + 16 * q), v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (row < rows && half * 64 + 16 * q + i < cols)
+                        o[(size_t)(16 * q + i) * a.n] = __float2bfloat16(v[i] * (kUnscale / kQScale));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (S.abort && tid == 0) drain(&S.done, phase, a.wait_cycles);
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 128);
+}
+
 template <int CG>
 __device__ __forceinline__ void alloc_columns(uint32_t* dst, uint32_t n) {
     if (CG == 1) {
@@ -575,9 +1020,12 @@ __device__ __forceinline__ void free_columns(uint32_t t, uint32_t n) {
 // One of the three products of a step, tiles of 128 CG x BN, K in blocks of 64.  With CG = 2
 // two blocks (a cluster) share a tile: each copies in its 128 rows of A and half of the BN
 // rows of B, one issues products over both (M = 256), each keeps its rows' accumulators.
-// That halves what a block reads of B, which is what bounds a tile: with CG = 1 the copies
-// reach about 50 bytes a cycle and SM, 983 cycles for the 48 KB of a block of K at BN = 256 whose
-// products take 512.
+// That halves what a block reads of B, and the copies are what bounds a tile: they reach about 50
+// bytes a cycle and SM, so that a block of K takes 490 cycles for the 24 KB of a tile of 256 x 128 and
+// 650 for the 32 KB of 256 x 256, whose products take 256 and 512.  At 2048 x 8240 A takes 36 us
+// (129 blocks of K in one round of tiles), B 16 and the update 52, 58 with lo (37 without its
+// epilogue, whose 100 MB pass through the same L2): 530 us for five steps with norm and start, 1.06
+// PFLOP/s with the symmetric products counted half.
 //   kGram:   out = alpha acc                (A; on and below the diagonal, mirrored; or, with few
 //            tiles and a long K, fp32 sums over parts of K, which ns_join_kernel adds)
 //   kSquare: out = alpha acc + beta in      (B from A A and A; likewise)
@@ -1070,6 +1518,53 @@ Workspace layout(int batch, int m, int n) {
     return w;
 }
 
+// Whether the steps may run on A alone: bounds on the operands (fp16, scaled) and on the growth of
+// a rounding, from the polynomials' values over the range of the singular values.
+bool tame(const float* coeffs, int steps) {
+    float top = 1.f, grown = 1.f;                       // of the singular values, of Q
+    for (int k = 0; k < steps; ++k) {
+        const float *c = coeffs + 3 * k;
+        float most = 0.f, next = 0.f;
+        for (int i = 0; i <= 64; ++i) {
+            const float x = top * i / 64, y = x * x, p = std::fabs(c[0] + (c[1] + c[2] * y) * y);
+            most = p > most ? p : most;
+            next = x * p > next ? x * p : next;
+        }
+        grown *= most;
+        if (!(most <= 48.f && most * top * top <= 48.f && grown <= 1024.f)) return false;
+        top = 1.01f * next;
+    }
+    return steps > 0;
+}
+
+GramPlan gram_plan(int batch, int m, int n, size_t* bytes) {
+    GramPlan p{};
+    const int r = m < n ? m : n, l = m < n ? n : m;
+    p.rp = r <= 64 ? 64 : 128;
+    p.chunks = (l + kSide - 1) / kSide;
+    auto cut = [&](int slots, int* parts, int* each) {  // about as many blocks as run at a time
+        int k = (slots + batch - 1) / batch;
+        if (k > p.chunks) k = p.chunks;
+        *each = (p.chunks + k - 1) / k;
+        *parts = (p.chunks + *each - 1) / *each;
+    };
+    cut(152 * 3, &p.gram_parts, &p.gram_each);
+    cut(152 * (p.rp == 64 ? 2 : 1), &p.apply_parts, &p.apply_each);
+    const size_t mn = (size_t)m * n;
+    p.norm_parts = (int)((mn + 4095) / 4096 < kNormBlocks ? (mn + 4095) / 4096 : kNormBlocks);
+    size_t off = 0;
+    auto take = [&](size_t b) {
+        const size_t at = off;
+        off += (b + 255) / 256 * 256;
+        return at;
+    };
+    p.norm = reinterpret_cast<float*>(take((size_t)batch * p.norm_parts * 4));
+    p.sums = reinterpret_cast<float*>(take((size_t)batch * p.gram_parts * p.rp * p.rp * 4));
+    p.q = reinterpret_cast<unsigned char*>(take((size_t)batch * 2 * (p.rp / 64) * kHalfBytes));
+    *bytes = off;
+    return p;
+}
+
 // Whether a call stays on chip: blocks of 128 columns, up to two for each SM where a matrix takes
 // several (20 x 128 x 1024: 80 us so, 140 us as products; 300 x 100 x 900: 1075 and 452).
 bool small(int batch, int m, int n) {
@@ -1160,7 +1655,11 @@ cudaError_t gemm(const Mat& A, const Mat& B, const GemmParams& p, cudaStream_t s
 }  // namespace
 
 size_t ortho_workspace_bytes(int batch, int m, int n) {
-    return small(batch, m, n) ? 0 : layout(batch, m, n).total;
+    if (small(batch, m, n)) return 0;
+    size_t bytes = 0;
+    if (m <= kSide || n <= kSide) gram_plan(batch, m, n, &bytes);
+    const size_t products = layout(batch, m, n).total;
+    return bytes > products ? bytes : products;
 }
 
 cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
@@ -1181,6 +1680,28 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         if (e != cudaSuccess) return e;
         return launch_in_clusters(ns_small_kernel<true>, dim3(a.batch * ranks), dim3(kSmallThreads), smem + shares, s,
                                   ranks, false, a);
+    }
+    if ((a.m <= kSide || a.n <= kSide) && tame(a.coeffs, a.steps)) {
+        size_t bytes;
+        GramPlan p = gram_plan(a.batch, a.m, a.n, &bytes);
+        char* ws = static_cast<char*>(a.workspace);
+        p.norm = reinterpret_cast<float*>(ws + reinterpret_cast<size_t>(p.norm));
+        p.sums = reinterpret_cast<float*>(ws + reinterpret_cast<size_t>(p.sums));
+        p.q = reinterpret_cast<unsigned char*>(ws + reinterpret_cast<size_t>(p.q));
+        ns_norm_kernel<<<dim3(p.norm_parts, a.batch), 256, 0, s>>>(a, p.norm);
+        const int ob = p.rp / 64 * (int)kHalfBytes, gram = 1024 + kTileBytes + sizeof(GramShared),
+                  poly = 1024 + 6 * ob + sizeof(GramShared), apply = gram + 2 * ob;
+        auto launch = [&](void (*kernel)(OrthoArgs, GramPlan), long long blocks, int smem) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            return launch_in_clusters(kernel, dim3((unsigned)blocks), dim3(kGramThreads), smem, s, 1, true, a, p);
+        };
+        cudaError_t e = cudaGetLastError();
+        if (e == cudaSuccess) e = launch(ns_gram_kernel, (long long)a.batch * p.gram_parts, gram);
+        if (e == cudaSuccess) e = launch(ns_poly_kernel, a.batch, poly);
+        if (e == cudaSuccess) e = launch(ns_apply_kernel, (long long)a.batch * p.apply_parts, apply);
+        *launches = 4;
+        return e;
     }
     const Workspace w = layout(a.batch, a.m, a.n);
     char* ws = static_cast<char*>(a.workspace);
