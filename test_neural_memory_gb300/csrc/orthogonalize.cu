@@ -566,18 +566,40 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 // more than 1024 in all take the other path (tame).
 //
 //   ns_gram_kernel:  A_0 by parts of the long side, 128 of it at a time (fp32 sums)
-//   ns_poly_kernel:  Q from A_0, a block a matrix
+//   ns_sum_kernel:   the parts' sums, in the parts' order, where they are many
+//   ns_poly_kernel:  Q from A_0, a block a matrix: a chain of three products and their epilogues a
+//                    step, 4 us of it
 //   ns_apply_kernel: Q X_0, 128 of the long side at a time
 //
-// MARK
+// RP: the short side, padded to 64 or 128.  4 RP threads, so that each takes 32 of a tile's elements:
+// those of the next tile are on their way while the products of this one run and its results
+// leave.  Operands are RP rows of 64 columns (128 bytes, 128-byte swizzle) next to one another, tiles of
+// a tall G 128 rows; with RP = 64 a product of 128 rows reads 64 more than there are, whose results
+// nobody takes and which lie in the same block's shared memory (kPad).
 constexpr float kQScale = 32.f;
-constexpr int kGramThreads = 256;
-constexpr uint32_t kTileBytes = 2 * kOperandBytes;      // hi and lo
+template <int RP> constexpr int kGramThreads = 4 * RP;
+template <int RP> constexpr uint32_t kTileBytes = RP * 256;           // hi, and lo behind it
+template <int RP> constexpr uint32_t kQBytes = RP * RP * 2;           // likewise
+template <int RP> constexpr uint32_t kPad = RP == 64 ? 16384 : 0;
+template <int RP> constexpr int kGramSmem = 1024 + 2 * kTileBytes<RP> + kPad<RP> + 64;
+template <int RP> constexpr int kPolySmem = 1024 + 6 * kQBytes<RP> + kPad<RP> + 64;
+template <int RP> constexpr int kApplySmem = 1024 + 2 * kTileBytes<RP> + 2 * kQBytes<RP> + kPad<RP> + 64;
 
 struct GramShared {
     uint64_t done;
     uint32_t tmem;
     int abort;
+};
+static_assert(sizeof(GramShared) <= 64, "the room left for it");
+
+struct GramPlan {
+    int rp;
+    int chunks;                     // of 128 of the long side
+    int gram_parts, gram_each;      // parts of a matrix in ns_gram_kernel, chunks of a part
+    int apply_parts, apply_each;
+    int norm_parts;
+    float *norm, *sums;             // sums: [matrix][part][column / 4][row][4]
+    unsigned char* q;               // Q as an operand, hi and lo, [matrix]
 };
 
 // hi and lo of eight values.
@@ -593,77 +615,104 @@ __device__ __forceinline__ void split8(const float* f, uint4& hi, uint4& lo) {
     lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// acc (+)= (hi + lo)(hi + lo) but for lo lo, over `steps` blocks of 16 of K; AMN, BMN: the operand's
-// rows are K.  `lo` of each lies `a_lo`, `b_lo` bytes behind its hi.
-__device__ __forceinline__ void mma_split(uint32_t acc, uint32_t a, uint32_t a_lo, bool amn, uint32_t b,
-                                          uint32_t b_lo, bool bmn, int N, int steps, bool add) {
-    const uint32_t id = idesc_f16(128, N, amn, bmn);
-    const uint64_t a0 = sdesc(a, amn ? kHalfBytes : 16, 1024, 2), b0 = sdesc(b, bmn ? kHalfBytes : 16, 1024, 2);
+// An operand in shared memory: hi, its lo, bytes between 64 columns; mn: its rows are K.
+struct Operand {
+    uint32_t hi, lo, half;
+    bool mn;
+};
+
+// acc (+)= (hi + lo)(hi + lo) but for lo lo, over `steps` blocks of 16 of K.
+__device__ __forceinline__ void mma_split(uint32_t acc, const Operand& x, const Operand& y, int N, int steps,
+                                          bool add) {
+    const uint32_t id = idesc_f16(128, N, x.mn, y.mn);
+    const uint64_t x0 = sdesc(x.hi, x.mn ? x.half : 16, 1024, 2), y0 = sdesc(y.hi, y.mn ? y.half : 16, 1024, 2);
+    const uint32_t xl = (x.lo - x.hi) >> 4, yl = (y.lo - y.hi) >> 4;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         if (k >= steps) break;
-        const uint32_t across = (k >> 2) * kHalfBytes + (k & 3) * 32, down = k * 2048;
-        const uint64_t ah = a0 + ((amn ? down : across) >> 4), bh = b0 + ((bmn ? down : across) >> 4);
-        mma_bf16(acc, ah, bh, id, add || k > 0);
-        mma_bf16(acc, ah, bh + (b_lo >> 4), id, true);
-        mma_bf16(acc, ah + (a_lo >> 4), bh, id, true);
+        const uint32_t inside = (k & 3) * 32, down = k * 2048;
+        const uint64_t xh = x0 + ((x.mn ? down : (k >> 2) * x.half + inside) >> 4);
+        const uint64_t yh = y0 + ((y.mn ? down : (k >> 2) * y.half + inside) >> 4);
+        mma_bf16(acc, xh, yh, id, add || k > 0);
+        mma_bf16(acc, xh, yh + yl, id, true);
+        mma_bf16(acc, xh + xl, yh, id, true);
     }
 }
 
-// rows x cols of G from element `at` on, times scale, as an operand hi and lo; zero up to multiples
-// of 16.  Batches of loads go out together.
-__device__ __forceinline__ void load_tile(const OrthoArgs& a, size_t at, int rows, int cols, float scale,
-                                          unsigned char* hi) {
-    unsigned char* lo = hi + kOperandBytes;
-    const int r16 = (rows + 15) & ~15, c16 = (cols + 15) & ~15;
-    const int tid = threadIdx.x, wide = a.n % 4 == 0 ? 4 : 2;
-    int log = 2;                                        // threads side by side over the columns
-    while ((wide << log) < c16) ++log;
-    const int col = (tid & ((1 << log) - 1)) * wide, step = kGramThreads >> log;
-    if (col >= c16) return;
-    const uint32_t swz = ((col & 63) * 2) & 15;
-    constexpr int B = 8;
-    for (int r0 = tid >> log; r0 < r16; r0 += B * step) {
-        float4 g[B];
+// A tile of G, rows x cols from element `at` on: on its way in registers, then an operand hi and lo,
+// zero up to multiples of 16.
+template <int RP>
+struct Tile {
+    float4 g[8];
+    int rows, cols, col, first, step;
+    bool four;                                          // four neighbours at a time, else two rows' pairs
+
+    __device__ __forceinline__ void fetch(const OrthoArgs& a, size_t at, int rows_, int cols_) {
+        rows = rows_;
+        cols = cols_;
+        four = a.n % 4 == 0;
+        const int v = four ? 4 : 2, c16 = (cols + 15) & ~15;
+        int log = 2;                                    // threads side by side over the columns
+        while ((v << log) < c16) ++log;
+        col = (threadIdx.x & ((1 << log) - 1)) * v;
+        first = threadIdx.x >> log;
+        step = kGramThreads<RP> >> log;
+        at += col;
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int row = r0 + i * step;
+        for (int i = 0; i < 8; ++i) {
             g[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (row >= rows) continue;
-            const size_t e = at + (size_t)row * a.n + col;
-            if (wide == 4) {
-                if (col < cols) g[i] = load4(a, e);
+            if (four) {
+                const int row = first + i * step;
+                if (row < rows && col < cols) g[i] = load4(a, at + (size_t)row * a.n);
             } else {
-                if (col < cols) g[i].x = load1(a, e);
-                if (col + 1 < cols) g[i].y = load1(a, e + 1);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int row = r0 + i * step;
-            if (row >= r16) break;
-            const uint32_t o = (uint32_t)(reinterpret_cast<unsigned char*>(operand_at(hi, row, col >> 3)) - hi) + swz;
-            const float x0 = g[i].x * scale, x1 = g[i].y * scale, x2 = g[i].z * scale, x3 = g[i].w * scale;
-            const uint32_t h0 = half2_bits(x0, x1);
-            const float2 f0 = half2_floats(h0);
-            const uint32_t l0 = half2_bits(x0 - f0.x, x1 - f0.y);
-            if (wide == 4) {
-                const uint32_t h1 = half2_bits(x2, x3);
-                const float2 f1 = half2_floats(h1);
-                *reinterpret_cast<uint2*>(hi + o) = make_uint2(h0, h1);
-                *reinterpret_cast<uint2*>(lo + o) = make_uint2(l0, half2_bits(x2 - f1.x, x3 - f1.y));
-            } else {
-                *reinterpret_cast<uint32_t*>(hi + o) = h0;
-                *reinterpret_cast<uint32_t*>(lo + o) = l0;
+                const int r0 = first + 2 * i * step, r1 = r0 + step;
+                const size_t e0 = at + (size_t)r0 * a.n, e1 = at + (size_t)r1 * a.n;
+                if (r0 < rows && col < cols) g[i].x = load1(a, e0);
+                if (r0 < rows && col + 1 < cols) g[i].y = load1(a, e0 + 1);
+                if (r1 < rows && col < cols) g[i].z = load1(a, e1);
+                if (r1 < rows && col + 1 < cols) g[i].w = load1(a, e1 + 1);
             }
         }
     }
-}
+    __device__ __forceinline__ void put(unsigned char* hi, uint32_t half, float scale) const {
+        const int r16 = (rows + 15) & ~15;
+        if (col >= ((cols + 15) & ~15)) return;
+        auto at = [&](int row) {
+            return hi + (col >> 6) * half + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4) + (col & 7) * 2;
+        };
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 x = make_float4(g[i].x * scale, g[i].y * scale, g[i].z * scale, g[i].w * scale);
+            const uint2 h = make_uint2(half2_bits(x.x, x.y), half2_bits(x.z, x.w));
+            const float2 f0 = half2_floats(h.x), f1 = half2_floats(h.y);
+            const uint2 l = make_uint2(half2_bits(x.x - f0.x, x.y - f0.y), half2_bits(x.z - f1.x, x.w - f1.y));
+            if (four) {
+                const int row = first + i * step;
+                if (row >= r16) continue;
+                *reinterpret_cast<uint2*>(at(row)) = h;
+                *reinterpret_cast<uint2*>(at(row) + kTileBytes<RP>) = l;
+            } else {
+                const int r0 = first + 2 * i * step, r1 = r0 + step;
+                if (r0 < r16) {
+                    *reinterpret_cast<uint32_t*>(at(r0)) = h.x;
+                    *reinterpret_cast<uint32_t*>(at(r0) + kTileBytes<RP>) = l.x;
+                }
+                if (r1 < r16) {
+                    *reinterpret_cast<uint32_t*>(at(r1)) = h.y;
+                    *reinterpret_cast<uint32_t*>(at(r1) + kTileBytes<RP>) = l.y;
+                }
+            }
+        }
+    }
+};
 
-__device__ __forceinline__ float start_scale(const OrthoArgs& a, const float* part, int parts, size_t mat) {
+// 2^10 / max(|G|_F, eps), the same in every warp.
+__device__ __forceinline__ float start_scale(const OrthoArgs& a, const GramPlan& p, size_t mat) {
     float s = 0.f;
-    for (int i = threadIdx.x; i < parts; i += 256) s += part[mat * parts + i];
-    return inverse_norm(block_sum(s), a.eps) * kScale;
+#pragma unroll 8
+    for (int i = threadIdx.x & 31; i < p.norm_parts; i += 32) s += p.norm[mat * p.norm_parts + i];
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return inverse_norm(s, a.eps) * kScale;
 }
 
 // Operands in shared memory, accumulators read: the next product may be issued.
@@ -674,133 +723,151 @@ __device__ __forceinline__ void operands_ready() {
     tc_fence_after();
 }
 
-struct GramPlan {
-    int rp;                         // the short side, 64 or 128
-    int chunks;                     // of 128 of the long side
-    int gram_parts, gram_each;      // parts of a matrix in ns_gram_kernel, chunks of a part
-    int apply_parts, apply_each;
-    int norm_parts;
-    float *norm, *sums;             // sums: [matrix][part][column / 4][row][4]
-    unsigned char* q;               // Q as an operand, hi and lo, [matrix]
-};
+// Waits for the products issued last; the same verdict in every warp, as all meet at the barriers that
+// follow.
+__device__ __forceinline__ bool products_done(GramShared& S, uint32_t& phase, const OrthoArgs& a) {
+    const bool ok = wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles);
+    if (__syncthreads_or(!ok)) return false;
+    phase ^= 1;
+    tc_fence_after();
+    return true;
+}
 
-__global__ void __launch_bounds__(kGramThreads, 3)
+__device__ __forceinline__ uint32_t set_up(GramShared& S, int warp, int columns) {
+    if (warp == 0) tmem_alloc(&S.tmem, columns);
+    if (threadIdx.x == 0) {
+        mbar_init(&S.done, 1);
+        fence_mbar_init();
+        S.abort = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return S.tmem;
+}
+__device__ __forceinline__ void tear_down(GramShared& S, int warp, int columns, uint32_t phase, const OrthoArgs& a) {
+    tc_fence_before();
+    __syncthreads();
+    if (S.abort && threadIdx.x == 0) drain(&S.done, phase, a.wait_cycles);
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(S.tmem, columns);
+}
+
+template <int RP>
+__global__ void __launch_bounds__(kGramThreads<RP>, RP == 64 ? 4 : 1)
     ns_gram_kernel(const __grid_constant__ OrthoArgs a, const __grid_constant__ GramPlan p) {
     extern __shared__ unsigned char raw[];
     unsigned char* tile = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    GramShared& S = *reinterpret_cast<GramShared*>(tile + kTileBytes);
-    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    GramShared& S = *reinterpret_cast<GramShared*>(tile + 2 * kTileBytes<RP> + kPad<RP>);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const bool wide = a.m <= a.n;
     const int r = wide ? a.m : a.n, l = wide ? a.n : a.m;
     const size_t mat = blockIdx.x / p.gram_parts;
     const int part = blockIdx.x % p.gram_parts;
-    if (warp == 0) tmem_alloc(&S.tmem, 128);
-    if (tid == 0) {
-        mbar_init(&S.done, 1);
-        fence_mbar_init();
-        S.abort = 0;
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = S.tmem;
+    const uint32_t tmem = set_up(S, warp, 128);
     after_previous();
-    const float scale = start_scale(a, p.norm, p.norm_parts, mat);
     const int c0 = part * p.gram_each, c1 = min(p.chunks, c0 + p.gram_each);
+    const uint32_t x = smem_u32(tile), half = wide ? RP * 128 : kHalfBytes;
+    const Operand X{x, x + kTileBytes<RP>, half, !wide};
+    Tile<RP> t;
+    auto fetch = [&](int c) {
+        const int at = c * kSide, len = min(kSide, l - at);
+        t.fetch(a, mat * a.m * a.n + (wide ? (size_t)at : (size_t)at * a.n), wide ? r : len, wide ? len : r);
+    };
+    fetch(c0);
+    const float scale = start_scale(a, p, mat);
     uint32_t phase = 0;
     bool ok = true;
     for (int c = c0; c < c1; ++c) {
-        const int at = c * kSide, len = min(kSide, l - at);
-        if (c > c0) {
-            ok = wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles);
-            if (__syncthreads_or(!ok)) break;
-            phase ^= 1;
-        }
-        load_tile(a, mat * a.m * a.n + (wide ? (size_t)at : (size_t)at * a.n), wide ? r : len, wide ? len : r, scale,
-                  tile);
+        if (c > c0 && !(ok = products_done(S, phase, a))) break;
+        t.put(tile, half, scale);
+        const int len = wide ? t.cols : t.rows;
         operands_ready();
         if (warp == 0) {
             if (elect_one()) {
-                const uint32_t x = smem_u32(tile);
-                mma_split(tmem, x, kOperandBytes, !wide, x, kOperandBytes, !wide, p.rp, (len + 15) / 16, c > c0);
+                mma_split(tmem, X, X, RP, (len + 15) / 16, c > c0);
                 mma_commit(&S.done);
             }
             __syncwarp();
         }
+        if (c + 1 < c1) fetch(c + 1);
     }
-    if (ok) ok = wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles);
-    tc_fence_after();
-    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
-    if (ok && half * 64 < p.rp && (warp & 3) * 32 < p.rp) {
-        float* to = p.sums + ((size_t)blockIdx.x * p.rp * p.rp) + (size_t)half * 64 * p.rp + row * 4;
+    if (ok) ok = products_done(S, phase, a);
+    const int row = (warp & 3) * 32 + lane, q0 = (warp >> 2) * 8;   // 32 columns a thread
+    if (ok && row < RP) {
+        float* to = p.sums + (size_t)blockIdx.x * RP * RP + row * 4;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
             float v[16];
-            tmem_ld16(tmem_addr(tmem, (warp & 3) * 32, half * 64 + 16 * q), v);
+            tmem_ld16(tmem_addr(tmem, (warp & 3) * 32, q0 * 4 + 16 * q), v);
             tmem_wait_ld();
 #pragma unroll
             for (int h = 0; h < 4; ++h)
-                *reinterpret_cast<float4*>(to + (size_t)(4 * q + h) * 4 * p.rp) =
+                *reinterpret_cast<float4*>(to + (size_t)(q0 + 4 * q + h) * 4 * RP) =
                     make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (S.abort && tid == 0) drain(&S.done, phase, a.wait_cycles);
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 0) tmem_dealloc(tmem, 128);
+    tear_down(S, warp, 128, phase, a);
 }
 
-__global__ void __launch_bounds__(kGramThreads)
+// The sums of a matrix's parts into its first one.
+__global__ void __launch_bounds__(256) ns_sum_kernel(const __grid_constant__ GramPlan p) {
+    after_previous();
+    const size_t n = (size_t)p.rp * p.rp / 4;
+    float4* at = reinterpret_cast<float4*>(p.sums) + blockIdx.y * p.gram_parts * n + blockIdx.x * 256 + threadIdx.x;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < p.gram_parts; ++k) {
+        const float4 v = at[k * n];
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    at[0] = s;
+}
+constexpr int kFewParts = 4;        // ns_poly_kernel adds as many itself
+
+template <int RP>
+__global__ void __launch_bounds__(kGramThreads<RP>, RP == 64 ? 2 : 1)
     ns_poly_kernel(const __grid_constant__ OrthoArgs a, const __grid_constant__ GramPlan p) {
     extern __shared__ unsigned char raw[];
     unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    const uint32_t ob = p.rp / 64 * kHalfBytes;         // an operand; its lo follows its hi
+    constexpr uint32_t ob = kQBytes<RP>, half = RP * 128;
     unsigned char *sa = base, *sp = base + 2 * ob, *sq = base + 4 * ob;
-    GramShared& S = *reinterpret_cast<GramShared*>(base + 6 * ob);
-    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int r = a.m <= a.n ? a.m : a.n, row = (warp & 3) * 32 + lane, half = warp >> 2;
-    const bool mine = half * 64 < p.rp;                 // columns that exist
+    GramShared& S = *reinterpret_cast<GramShared*>(base + 6 * ob + kPad<RP>);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int r = a.m <= a.n ? a.m : a.n, row = (warp & 3) * 32 + lane, c0 = (warp >> 2) * 32;
+    const bool mine = row < RP;                         // 32 columns from c0 on
     const size_t mat = blockIdx.x;
-    if (warp == 0) tmem_alloc(&S.tmem, 256);
-    if (tid == 0) {
-        mbar_init(&S.done, 1);
-        fence_mbar_init();
-        S.abort = 0;
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = S.tmem, acc = tmem_addr(tmem, (warp & 3) * 32, half * 64);
+    const uint32_t tmem = set_up(S, warp, 2 * RP), acc = tmem_addr(tmem, (warp & 3) * 32, c0);
     after_previous();
 
-    auto put = [&](unsigned char* to, int q, const float* f) {   // columns 8 q .. of this thread's 64
+    auto put = [&](unsigned char* to, int q, const float* f) {   // columns c0 + 8 q ..
         uint4 hi, lo;
         split8(f, hi, lo);
-        uint4* at = operand_at(to, row, half * 8 + q);
-        *at = hi;
-        *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(at) + ob) = lo;
+        unsigned char* at = to + ((c0 + 8 * q) >> 6) * half + row * 128 + (((((c0 >> 3) + q) & 7) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(at) = hi;
+        *reinterpret_cast<uint4*>(at + ob) = lo;
     };
     // A_0 from the parts, in their order; zero past the short side
-    float A[64];
+    float A[32];
 #pragma unroll
-    for (int c = 0; c < 64; ++c) A[c] = 0.f;
-    if (mine && row < r) {
-        for (int k = 0; k < p.gram_parts; ++k) {
-            const float* from = p.sums + ((mat * p.gram_parts + k) * p.rp * p.rp) + (size_t)half * 64 * p.rp + row * 4;
+    for (int c = 0; c < 32; ++c) A[c] = 0.f;
+    if (row < r) {
+        const int parts = p.gram_parts > kFewParts ? 1 : p.gram_parts;
+        const float* from = p.sums + mat * p.gram_parts * RP * RP + (size_t)c0 * RP + row * 4;
+        for (int k = 0; k < parts; ++k, from += RP * RP) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                const float4 v = *reinterpret_cast<const float4*>(from + (size_t)q * 4 * p.rp);
+            for (int q = 0; q < 8; ++q) {
+                const float4 v = *reinterpret_cast<const float4*>(from + q * 4 * RP);
                 A[4 * q] += v.x; A[4 * q + 1] += v.y; A[4 * q + 2] += v.z; A[4 * q + 3] += v.w;
             }
         }
 #pragma unroll
-        for (int c = 0; c < 64; ++c) A[c] = half * 64 + c < r ? A[c] * (kUnscale * kUnscale) : 0.f;
+        for (int c = 0; c < 32; ++c) A[c] = c0 + c < r ? A[c] * (kUnscale * kUnscale) : 0.f;
     }
     auto put_A = [&]() {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
+        for (int q = 0; q < 4; ++q) {
             float f[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = A[8 * q + i] * kScale;
@@ -811,15 +878,9 @@ __global__ void __launch_bounds__(kGramThreads)
     uint32_t phase = 0;
     const int steps = (r + 15) / 16;
     auto product = [&](uint32_t column, const unsigned char* x, const unsigned char* y) {
-        mma_split(tmem_addr(tmem, 0, column), smem_u32(x), ob, false, smem_u32(y), ob, false, p.rp, steps, false);
-    };
-    // the same verdict in every warp: all of them meet at the barriers that follow
-    auto finished = [&]() {
-        const bool ok = wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles);
-        if (__syncthreads_or(!ok)) return false;
-        phase ^= 1;
-        tc_fence_after();
-        return true;
+        const uint32_t u = smem_u32(x), v = smem_u32(y);
+        mma_split(tmem_addr(tmem, 0, column), Operand{u, u + ob, half, false}, Operand{v, v + ob, half, false}, RP,
+                  steps, false);
     };
     bool ok = true;
     for (int k = 0; k < a.steps; ++k) {
@@ -833,20 +894,19 @@ __global__ void __launch_bounds__(kGramThreads)
             }
             __syncwarp();
         }
-        if (!(ok = finished())) break;
+        if (!(ok = products_done(S, phase, a))) break;
         if (mine) {                                     // P; the first is Q too
             const float c2 = cc * (kUnscale * kUnscale);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[16];
+            for (int q = 0; q < 2; ++q) {
+                float v[16], f[16];
                 tmem_ld16(acc + 16 * q, v);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int col = half * 64 + 16 * q + i;
+                    const int col = c0 + 16 * q + i;
                     v[i] = fmaf(c2, v[i], cb * A[16 * q + i]) + (col == row && row < r ? ca : 0.f);
                 }
-                float f[16];
                 if (k == 0) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) f[i] = v[i] * kQScale;
@@ -864,47 +924,51 @@ __global__ void __launch_bounds__(kGramThreads)
         if (warp == 0) {
             if (elect_one()) {
                 if (!last) product(0, sp, sa);
-                if (k > 0) product(128, sp, sq);
+                if (k > 0) product(RP, sp, sq);
                 mma_commit(&S.done);
             }
             __syncwarp();
         }
-        if (!(ok = finished())) break;
-        if (mine) {                                     // P A over A, P Q over Q
+        if (!(ok = products_done(S, phase, a))) break;
+        if (mine && !last) {                            // P A over A
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 float v[16];
-                if (!last) {
-                    tmem_ld16(acc + 16 * q, v);
-                    tmem_wait_ld();
+                tmem_ld16(acc + 16 * q, v);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] *= kUnscale;
-                    put(sa, 2 * q, v);
-                    put(sa, 2 * q + 1, v + 8);
+                for (int i = 0; i < 16; ++i) v[i] *= kUnscale;
+                put(sa, 2 * q, v);
+                put(sa, 2 * q + 1, v + 8);
+            }
+        }
+        if (!last) {
+            operands_ready();
+            if (warp == 0) {
+                if (elect_one()) {
+                    product(0, sa, sp);
+                    mma_commit(&S.done);
                 }
-                if (k > 0) {
-                    tmem_ld16(acc + 128 + 16 * q, v);
-                    tmem_wait_ld();
+                __syncwarp();
+            }
+        }
+        if (mine && k > 0) {                            // P Q over Q, beside the product above
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] *= kUnscale;
-                    put(sq, 2 * q, v);
-                    put(sq, 2 * q + 1, v + 8);
-                }
+            for (int q = 0; q < 2; ++q) {
+                float v[16];
+                tmem_ld16(acc + RP + 16 * q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] *= kUnscale;
+                put(sq, 2 * q, v);
+                put(sq, 2 * q + 1, v + 8);
             }
         }
         if (last) break;
-        operands_ready();
-        if (warp == 0) {
-            if (elect_one()) {
-                product(0, sa, sp);
-                mma_commit(&S.done);
-            }
-            __syncwarp();
-        }
-        if (!(ok = finished())) break;
+        if (!(ok = products_done(S, phase, a))) break;
         if (mine) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 float v[16];
                 tmem_ld16(acc + 16 * q, v);
                 tmem_wait_ld();
@@ -914,89 +978,82 @@ __global__ void __launch_bounds__(kGramThreads)
             put_A();
         }
     }
-    tc_fence_before();
     __syncthreads();
     if (ok) {
         uint4* to = reinterpret_cast<uint4*>(p.q + mat * 2 * ob);
-        for (uint32_t i = tid; i < 2 * ob / 16; i += kGramThreads) to[i] = reinterpret_cast<const uint4*>(sq)[i];
+        for (uint32_t i = threadIdx.x; i < 2 * ob / 16; i += kGramThreads<RP>)
+            to[i] = reinterpret_cast<const uint4*>(sq)[i];
     }
-    if (S.abort && tid == 0) drain(&S.done, phase, a.wait_cycles);
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 0) tmem_dealloc(tmem, 256);
+    tear_down(S, warp, 2 * RP, phase, a);
 }
 
 // A wide G's tile is the first operand, with the long side as its rows, a tall one's the second, with
 // the long side as the accumulators' columns: either way neighbouring lanes write neighbouring
 // elements.
-__global__ void __launch_bounds__(kGramThreads)
+template <int RP>
+__global__ void __launch_bounds__(kGramThreads<RP>, RP == 64 ? 3 : 1)
     ns_apply_kernel(const __grid_constant__ OrthoArgs a, const __grid_constant__ GramPlan p) {
     extern __shared__ unsigned char raw[];
     unsigned char* tile = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    const uint32_t ob = p.rp / 64 * kHalfBytes;
-    unsigned char* sq = tile + kTileBytes;
-    GramShared& S = *reinterpret_cast<GramShared*>(sq + 2 * ob);
-    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    constexpr uint32_t ob = kQBytes<RP>;
+    unsigned char* sq = tile + 2 * kTileBytes<RP>;
+    GramShared& S = *reinterpret_cast<GramShared*>(sq + 2 * ob + kPad<RP>);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const bool wide = a.m <= a.n;
     const int r = wide ? a.m : a.n, l = wide ? a.n : a.m;
     const size_t mat = blockIdx.x / p.apply_parts, mn = (size_t)a.m * a.n;
     const int part = blockIdx.x % p.apply_parts;
-    if (warp == 0) tmem_alloc(&S.tmem, 128);
-    if (tid == 0) {
-        mbar_init(&S.done, 1);
-        fence_mbar_init();
-        S.abort = 0;
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = S.tmem;
+    const int N = wide ? RP : kSide;                    // columns of an accumulator, of two in turn
+    const uint32_t tmem = set_up(S, warp, 2 * N);
     after_previous();
-    const float scale = start_scale(a, p.norm, p.norm_parts, mat);
-    const uint4* from = reinterpret_cast<const uint4*>(p.q + mat * 2 * ob);
-    for (uint32_t i = tid; i < 2 * ob / 16; i += kGramThreads) reinterpret_cast<uint4*>(sq)[i] = from[i];
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + mat * mn;
-    const int row = (warp & 3) * 32 + lane, half = warp >> 2;
     const int c0 = part * p.apply_each, c1 = min(p.chunks, c0 + p.apply_each);
-    uint32_t phase = 0;
-    for (int c = c0; c < c1; ++c) {
+    Tile<RP> t;
+    auto fetch = [&](int c) {
         const int at = c * kSide, len = min(kSide, l - at);
-        load_tile(a, mat * mn + (wide ? (size_t)at : (size_t)at * a.n), wide ? r : len, wide ? len : r, scale, tile);
+        t.fetch(a, mat * mn + (wide ? (size_t)at : (size_t)at * a.n), wide ? r : len, wide ? len : r);
+    };
+    fetch(c0);
+    const float scale = start_scale(a, p, mat);
+    const uint4* from = reinterpret_cast<const uint4*>(p.q + mat * 2 * ob);
+    for (uint32_t i = threadIdx.x; i < 2 * ob / 16; i += kGramThreads<RP>) reinterpret_cast<uint4*>(sq)[i] = from[i];
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + mat * mn;
+    const uint32_t x = smem_u32(tile), q = smem_u32(sq), half = wide ? RP * 128 : kHalfBytes;
+    const Operand X{x, x + kTileBytes<RP>, half, wide}, Q{q, q + ob, RP * 128, false};
+    const int row = (warp & 3) * 32 + lane, each = N / (kGramThreads<RP> / 128), col0 = (warp >> 2) * each;
+    uint32_t phase = 0;
+    auto issue = [&](int c) {
+        t.put(tile, half, scale);
         operands_ready();
         if (warp == 0) {
             if (elect_one()) {
-                const uint32_t x = smem_u32(tile), q = smem_u32(sq);
-                if (wide) mma_split(tmem, x, kOperandBytes, true, q, ob, false, p.rp, (r + 15) / 16, false);
-                else mma_split(tmem, q, ob, false, x, kOperandBytes, false, 128, (r + 15) / 16, false);
+                const uint32_t acc = tmem_addr(tmem, 0, (c & 1) * N);
+                if (wide) mma_split(acc, X, Q, N, (r + 15) / 16, false);
+                else mma_split(acc, Q, X, N, (r + 15) / 16, false);
                 mma_commit(&S.done);
             }
             __syncwarp();
         }
-        const bool ok = wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles);
-        if (__syncthreads_or(!ok)) break;
-        phase ^= 1;
-        tc_fence_after();
+        if (c + 1 < c1) fetch(c + 1);
+    };
+    issue(c0);
+    for (int c = c0; c < c1; ++c) {
+        if (!products_done(S, phase, a)) break;
+        if (c + 1 < c1) issue(c + 1);
+        const int at = c * kSide, len = min(kSide, l - at);
         const int rows = wide ? len : r, cols = wide ? r : len;   // of the accumulators
-        if (half * 64 < cols && (warp & 3) * 32 < rows) {
-            __nv_bfloat16* o = out + (wide ? (size_t)at + row : (size_t)at * a.n + row) + (size_t)half * 64 * a.n;
+        if ((warp & 3) * 32 >= rows) continue;
+        __nv_bfloat16* o = out + (wide ? (size_t)at : (size_t)at * a.n) + row + (size_t)col0 * a.n;
+        for (int i0 = 0; i0 < each && col0 + i0 < cols; i0 += 16, o += (size_t)16 * a.n) {
+            float v[16];
+            tmem_ld16(tmem_addr(tmem, (warp & 3) * 32, (c & 1) * N + col0 + i0), v);
+            tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[16];
-                tmem_ld16(tmem_addr(tmem, (warp & 3) * 32, half * 64 + 16 * q), v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (row < rows && half * 64 + 16 * q + i < cols)
-                        o[(size_t)(16 * q + i) * a.n] = __float2bfloat16(v[i] * (kUnscale / kQScale));
-            }
+            for (int i = 0; i < 16; ++i)
+                if (row < rows && col0 + i0 + i < cols)
+                    o[(size_t)i * a.n] = __float2bfloat16(v[i] * (kUnscale / kQScale));
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (S.abort && tid == 0) drain(&S.done, phase, a.wait_cycles);
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 0) tmem_dealloc(tmem, 128);
+    tear_down(S, warp, 2 * N, phase, a);
 }
 
 template <int CG>
@@ -1548,8 +1605,8 @@ GramPlan gram_plan(int batch, int m, int n, size_t* bytes) {
         *each = (p.chunks + k - 1) / k;
         *parts = (p.chunks + *each - 1) / *each;
     };
-    cut(152 * 3, &p.gram_parts, &p.gram_each);
-    cut(152 * (p.rp == 64 ? 2 : 1), &p.apply_parts, &p.apply_each);
+    cut(152 * (p.rp == 128 ? 1 : 4), &p.gram_parts, &p.gram_each);
+    cut(152 * (p.rp == 128 ? 1 : m <= n ? 3 : 2), &p.apply_parts, &p.apply_each);
     const size_t mn = (size_t)m * n;
     p.norm_parts = (int)((mn + 4095) / 4096 < kNormBlocks ? (mn + 4095) / 4096 : kNormBlocks);
     size_t off = 0;
@@ -1560,16 +1617,17 @@ GramPlan gram_plan(int batch, int m, int n, size_t* bytes) {
     };
     p.norm = reinterpret_cast<float*>(take((size_t)batch * p.norm_parts * 4));
     p.sums = reinterpret_cast<float*>(take((size_t)batch * p.gram_parts * p.rp * p.rp * 4));
-    p.q = reinterpret_cast<unsigned char*>(take((size_t)batch * 2 * (p.rp / 64) * kHalfBytes));
+    p.q = reinterpret_cast<unsigned char*>(take((size_t)batch * p.rp * p.rp * 4));
     *bytes = off;
     return p;
 }
 
-// Whether a call stays on chip: blocks of 128 columns, up to two for each SM where a matrix takes
-// several (20 x 128 x 1024: 80 us so, 140 us as products; 300 x 100 x 900: 1075 and 452).
+// Whether a call stays on chip: one block a matrix, or, with a short side of up to 64, a cluster of
+// blocks of 128 of the long side, up to two blocks for each SM (2 x 709 x 37: 28 us so, 40 by its
+// A alone; 1 x 64 x 256: 25 and 32; but 20 x 128 x 1024: 79 and 65).
 bool small(int batch, int m, int n) {
     const int r = m < n ? m : n, ranks = ((m < n ? n : m) + kSide - 1) / kSide;
-    return r <= kSide && (ranks == 1 || (ranks <= kMaxCluster && (long long)batch * ranks <= 2 * 152));
+    return r <= kSide && (ranks == 1 || (r <= 64 && ranks <= kMaxCluster && (long long)batch * ranks <= 2 * 152));
 }
 
 // A stored fp16 matrix batch: [batch][rows][pitch].
@@ -1652,6 +1710,24 @@ cudaError_t gemm(const Mat& A, const Mat& B, const GemmParams& p, cudaStream_t s
     return gemm_tiles<AMN, BMN, EPI, 1, 64>(A, B, p, s);
 }
 
+template <int RP>
+cudaError_t gram_steps(const OrthoArgs& a, const GramPlan& p, cudaStream_t s, int* launches) {
+    *launches = 4;
+    auto launch = [&](void (*kernel)(OrthoArgs, GramPlan), int blocks, int smem) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        return launch_in_clusters(kernel, dim3(blocks), dim3(kGramThreads<RP>), smem, s, 1, true, a, p);
+    };
+    cudaError_t e = launch(ns_gram_kernel<RP>, a.batch * p.gram_parts, kGramSmem<RP>);
+    if (e == cudaSuccess && p.gram_parts > kFewParts) {
+        ++*launches;
+        e = launch_in_clusters(ns_sum_kernel, dim3(RP * RP / 1024, a.batch), dim3(256), 0, s, 1, true, p);
+    }
+    if (e == cudaSuccess) e = launch(ns_poly_kernel<RP>, a.batch, kPolySmem<RP>);
+    if (e == cudaSuccess) e = launch(ns_apply_kernel<RP>, a.batch * p.apply_parts, kApplySmem<RP>);
+    return e;
+}
+
 }  // namespace
 
 size_t ortho_workspace_bytes(int batch, int m, int n) {
@@ -1689,19 +1765,9 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         p.sums = reinterpret_cast<float*>(ws + reinterpret_cast<size_t>(p.sums));
         p.q = reinterpret_cast<unsigned char*>(ws + reinterpret_cast<size_t>(p.q));
         ns_norm_kernel<<<dim3(p.norm_parts, a.batch), 256, 0, s>>>(a, p.norm);
-        const int ob = p.rp / 64 * (int)kHalfBytes, gram = 1024 + kTileBytes + sizeof(GramShared),
-                  poly = 1024 + 6 * ob + sizeof(GramShared), apply = gram + 2 * ob;
-        auto launch = [&](void (*kernel)(OrthoArgs, GramPlan), long long blocks, int smem) {
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e != cudaSuccess) return e;
-            return launch_in_clusters(kernel, dim3((unsigned)blocks), dim3(kGramThreads), smem, s, 1, true, a, p);
-        };
-        cudaError_t e = cudaGetLastError();
-        if (e == cudaSuccess) e = launch(ns_gram_kernel, (long long)a.batch * p.gram_parts, gram);
-        if (e == cudaSuccess) e = launch(ns_poly_kernel, a.batch, poly);
-        if (e == cudaSuccess) e = launch(ns_apply_kernel, (long long)a.batch * p.apply_parts, apply);
-        *launches = 4;
-        return e;
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        return p.rp == 64 ? gram_steps<64>(a, p, s, launches) : gram_steps<128>(a, p, s, launches);
     }
     const Workspace w = layout(a.batch, a.m, a.n);
     char* ws = static_cast<char*>(a.workspace);
