@@ -15,8 +15,10 @@
 // default steps, 1e-4 in all) lo is not kept, which saves a third of the traffic.  Operands are stored times 2^10, so
 // that entries of 1e-4 stay clear of fp16's subnormal range.
 //
-// A short side of at most 128 and a long one of at most 1024: one block, or a cluster, keeps
-// a matrix on chip through all steps (ns_small_kernel).  Larger: three products a step (ns_gemm_kernel).  A and
+// Three ways, by size.  128 x 128 at most, or 64 x 1024: one block, or a cluster, keeps a matrix on chip through all
+// steps (ns_small_kernel: 192 x 128 x 128 in 26 us on the device).  A longer long side: the steps run on A alone, and
+// G is read three times in all (ns_gram_kernel and those after it: 158 x 39 x 3516 in 137 us, 630 as products of every
+// step).  A longer short side: three products a step (ns_gemm_kernel).  A and
 // B = b A + c A^2 are symmetric, so only their tiles on and below the diagonal are
 // computed and each is written twice, once transposed.
 #include <cuda.h>
@@ -562,14 +564,16 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 // twice a step.  What that costs is accuracy: a rounding of A_0 is not put right by the next step's
 // A.  Every operand here is therefore a sum hi + lo of two fp16 values, and a product takes hi hi +
 // hi lo + lo hi: 1e-4 off for a matrix of low rank plus noise, 1e-5 for a normal one, before
-// the result is rounded to bf16.  Roundings grow as small singular values do, so coefficients that grow these by
+// the result is rounded to bf16 (1.66e-3).  Roundings grow as small singular values do, so coefficients that grow these by
 // more than 1024 in all take the other path (tame).
 //
 //   ns_gram_kernel:  A_0 by parts of the long side, 128 of it at a time (fp32 sums)
 //   ns_sum_kernel:   the parts' sums, in the parts' order, where they are many
 //   ns_poly_kernel:  Q from A_0, a block a matrix: a chain of three products and their epilogues a
-//                    step, 4 us of it
+//                    step, 33 us for five steps (24 for RP = 64) whatever the long side
 //   ns_apply_kernel: Q X_0, 128 of the long side at a time
+// 158 x 39 x 3516 fp32: norm 18, A_0 44, Q 24, Q X_0 54 us, where reading G takes 13: the tiles' conversion to
+// hi and lo, and stores of 64 bytes a warp, bound the two that read it.
 //
 // RP: the short side, padded to 64 or 128.  4 RP threads, so that each takes 32 of a tile's elements:
 // those of the next tile are on their way while the products of this one run and its results

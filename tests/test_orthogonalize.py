@@ -149,3 +149,59 @@ def test_refusals():
     assert e.value.code == ttm.ERR_UNSUPPORTED
     with pytest.raises(TypeError):
         ttm.orthogonalize(G.half())
+
+
+@pytest.mark.parametrize("batch,m,n", [(1, 128, 129), (3, 129, 100), (153, 65, 300), (2, 90, 234), (400, 3, 131),
+                                       (7, 1000, 128), (5, 1001, 77), (2, 5000, 64), (1, 60, 5003), (2, 4998, 33),
+                                       (700, 11, 286), (310, 200, 16), (310, 201, 15), (1, 128, 20011),
+                                       (1, 9973, 127), (160, 1027, 48), (1, 2, 1025), (1, 1, 3001)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["normal", "low rank"])
+def test_short_side_of_up_to_128(batch, m, n, dtype, kind):
+    """Where the steps run on A alone: an operand, a sum of two fp16 values, errs by 2^-22 of itself and A by
+    2^-20 of its norm; the default steps let that grow by 3.4445^5 = 485 at most, 4.7e-4 in all."""
+    G = matrices(batch, m, n, kind, seed=m * n).to(DT[dtype])
+    O = ttm.orthogonalize(G.cuda())
+    ref = steps64(G, ttm.train.NS_COEFFS)
+    err, size = (O.double().cpu() - ref).flatten(1).norm(dim=1), ref.flatten(1).norm(dim=1)
+    # a cluster (64 x 1024 at most) or the products (other coefficients) keep the bound above
+    moved = (steps64(G, ttm.train.NS_COEFFS, rounded=True) - ref).flatten(1).norm(dim=1)
+    alone = min(m, n) > 64 or max(m, n) > 1024 or batch * ((max(m, n) + 127) // 128) > 304
+    slack = 4.7e-4 * size if alone else 2 * moved
+    assert bool((err <= slack + (2.0 ** -9 + 2e-4) * size).all()), float((err / size).max())
+    assert torch.equal(O, ttm.orthogonalize(G.cuda()))
+
+
+@pytest.mark.parametrize("m,n", [(100, 300), (70, 1500), (1500, 40)])
+@pytest.mark.parametrize("steps", [1, 2, 4, 12])
+def test_short_side_step_counts(m, n, steps):
+    """Coefficients in turn; twelve steps let a rounding grow too far for A alone."""
+    coeffs = [((1.875, -1.25, 0.375), ttm.train.NS_COEFFS[0], (1.5, -0.5, 0.0))[i % 3] for i in range(steps)]
+    check(matrices(2, m, n, "normal"), coeffs)
+
+
+def test_short_side_zero_tiny_nan_and_scale():
+    for m, n in ((100, 300), (3000, 50)):
+        G = torch.zeros(4, m, n)
+        G[1:] = matrices(3, m, n, "one column")
+        G[2] *= 1e-12
+        check(G, ttm.train.NS_COEFFS)
+        clean = ttm.orthogonalize(G.cuda())
+        assert not clean[0].any()
+        a = ttm.orthogonalize((G[1:2] * 2.0 ** 30).cuda(), eps=1e-12)
+        assert torch.equal(a, ttm.orthogonalize((G[1:2] * 2.0 ** -20).cuda(), eps=1e-12))
+        G[1, 3, 4] = float("nan")
+        O = ttm.orthogonalize(G.cuda())
+        assert bool(torch.isnan(O[1].float()).all())
+        assert torch.equal(O[0], clean[0]) and torch.equal(O[2:], clean[2:])
+
+
+def test_offsets_past_32_bits():
+    """530 matrices of 64 x 65536, 2.2e9 elements: the last one counts."""
+    G = torch.zeros(530, 64, 65536, dtype=torch.bfloat16, device="cuda")
+    last = matrices(1, 64, 65536, "normal").bfloat16()
+    G[-1] = last[0].cuda()
+    O = ttm.orthogonalize(G)
+    ref = steps64(last, ttm.train.NS_COEFFS)[0]
+    err = float((O[-1].double().cpu() - ref).norm() / ref.norm())
+    assert err < 2.0 ** -9 + 2e-4 + 4.7e-4 and not O[:-1].any()
