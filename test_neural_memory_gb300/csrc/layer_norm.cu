@@ -17,7 +17,7 @@
 // in flight and one reduction serves several rows.  TPR is the rows' packs up to a warp
 // (shuffles), or the whole block of 256 (shuffles, then shared memory) for long rows; a warp
 // takes rows of up to 1024 single values, in which a block of 256 would mostly wait at barriers
-// (697568 x 169 bf16, gradient: 679 us with a row a block, 236 with a row a warp).  Rows longer
+// (697568 x 169 bf16, gradient: 679 us with a row a block, 236 with a row a warp) once there are many.  Rows longer
 // than the registers hold are read again from the cache instead.  W is the widest pack that the
 // rows' alignment and D allow; rows of x and dy that do not start on 16 bytes are read in 16-byte
 // words all the same and shifted into place (238817 x 768 bf16 from rows of 771, forward: 318 us
@@ -539,7 +539,7 @@ cudaError_t run(const LayerNormArgs& a, bool back, int blocks, cudaStream_t s) {
         constexpr int rows = bytes >= 64 ? 1 : (bytes >= 32 ? 2 : 4);   // 64 bytes in flight a thread
         const long long need = ((long long)a.N + sets * rows - 1) / (sets * rows);
         ln_fwd_kernel<E, W, kShift, TPR, K, rows><<<(unsigned)need, kThreads, 0, s>>>(a);
-    } else if constexpr (!kShift || shift_pays<E>(TPR * K * W)) {
+    } else if constexpr (kShift ? shift_pays<E>(TPR * K * W) : W > 2 || TPR > 32 || K * W < 32) {
         constexpr int rows = bytes > (kShift ? 16 : 32) || K * W > 8 ? 1 : 2;
         constexpr int resident = K * W <= (kShift ? 8 : 16) ? kResident : 1;
         const size_t shared = TPR == kThreads || !a.partial ? 0 : (size_t)kWarps * 2 * TPR * K * W * 4;
@@ -568,6 +568,11 @@ int pack_width(const LayerNormArgs& a, bool back) {
     return sizeof(E) == 2 && fits(2) ? 2 : 1;
 }
 
+// Rows of more than 128 values or pairs, a warp each: with enough of them, or a block a row has more
+// loads in flight (1537 x 500 bf16 in odd rows: 4.0 and 7.9 us by blocks, 5.7 and 9.6 by warps; 12000: 13.9
+// and 21.6, 9.8 and 18.1).  In the gradient a warp's registers do not reach for 32 values a thread
+// (48000 x 900: 91 us, 78 by blocks).
+constexpr int kManyRows = 4096;
 template <typename E, int W, bool kShift = false>
 cudaError_t by_length(const LayerNormArgs& a, bool back, int blocks, cudaStream_t s) {
     const int packs = a.D / W;
@@ -580,10 +585,14 @@ cudaError_t by_length(const LayerNormArgs& a, bool back, int blocks, cudaStream_
         if (packs <= 96) return run<E, W, kShift, 32, 3>(a, back, blocks, s);
     if (packs <= 128) return run<E, W, kShift, 32, 4>(a, back, blocks, s);
     if constexpr (W <= 2) {
-        if (packs <= 256) return run<E, W, kShift, 32, 8>(a, back, blocks, s);
-        if (packs <= 512) return run<E, W, kShift, 32, 16>(a, back, blocks, s);
-        if constexpr (W == 1)
-            if (packs <= 1024) return run<E, W, kShift, 32, 32>(a, back, blocks, s);
+        if (a.N >= kManyRows) {
+            if (packs <= 256) return run<E, W, kShift, 32, 8>(a, back, blocks, s);
+            if (packs <= 512 && !(back && W == 2)) return run<E, W, kShift, 32, 16>(a, back, blocks, s);
+            if constexpr (W == 1)
+                if (packs <= 1024 && !back) return run<E, W, kShift, 32, 32>(a, back, blocks, s);
+        }
+        if (packs <= 256) return run<E, W, kShift, 256, 1>(a, back, blocks, s);
+        if (packs <= 512) return run<E, W, kShift, 256, 2>(a, back, blocks, s);
         if (packs <= 1024) return run<E, W, kShift, 256, 4>(a, back, blocks, s);
         if (packs <= 2048) return run<E, W, kShift, 256, 8>(a, back, blocks, s);
         if (packs <= 4096) return run<E, W, kShift, 256, 16>(a, back, blocks, s);

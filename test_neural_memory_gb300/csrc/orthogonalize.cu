@@ -150,10 +150,11 @@ __device__ __forceinline__ void peer_store2(uint32_t addr, uint32_t a, uint32_t 
 // tensor memory, each followed by its epilogue; two blocks share an SM, so that one's
 // products run beside the other's epilogue.
 //
-// kCluster: a long side of up to 1024 is split over the blocks of a cluster, 128 columns each.
+// kCluster: a short side of up to 64 whose long one, of up to 1024, is split over the blocks of a cluster, 128
+// columns each.
 // A is then a sum over the blocks: each leaves its share in shared memory (fp32), adds a
 // range of rows over all blocks in their order and hands the result to all of them;
-// everything else stays a block's own.  (2 x 709 x 37: 88 us as products from global
+// everything else stays a block's own.  (2 x 709 x 37: 28 us, 88 as products from global
 // memory.)
 constexpr int kSide = 128, kSmallThreads = 256, kMaxCluster = 8;
 constexpr uint32_t kHalfBytes = kSide * 128;            // 64 columns of an operand

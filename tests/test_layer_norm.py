@@ -183,3 +183,10 @@ def test_refusals():
 @pytest.mark.parametrize("pad", [0, 3, 1, 2, 4])
 def test_row_lengths_and_starts(N, D, dtype, pad):
     test_forward_and_gradient(N, D, dtype, pad != 1, pad)
+
+
+@pytest.mark.parametrize("D", [131, 300, 500, 513, 771, 900, 1026])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_many_rows(D, dtype, pad):
+    test_forward_and_gradient(4100, D, dtype, True, pad)
