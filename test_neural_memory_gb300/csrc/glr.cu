@@ -19,6 +19,10 @@
 // side over a strip of channels and 256 / CW over the tokens (make_plan chooses CW).
 // The runs of a warp are joined by shuffles, the eight warps' through shared memory.
 //
+// Measured, bf16, a gate per channel: forward 16 x 131072 x 128 256 us (6.3 TB/s, 93 % of what a copy
+// reaches), 256 x 8192 x 128 241 us (6.7 TB/s); gradient 96 x 8192 x 64 83 us (6.1 TB/s); one tile,
+// 2 x 777 x 768, 6.0 us.
+//
 // Between tiles (look-back), a lane per channel: a warp publishes its channels' map of
 // the tile as soon as it has it, finds the nearest tile before whose end state is known,
 // takes that state through the maps in between (read 8 at a time) and publishes its own
