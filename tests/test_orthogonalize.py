@@ -205,3 +205,23 @@ def test_offsets_past_32_bits():
     ref = steps64(last, ttm.train.NS_COEFFS)[0]
     err = float((O[-1].double().cpu() - ref).norm() / ref.norm())
     assert err < 2.0 ** -9 + 2e-4 + 4.7e-4 and not O[:-1].any()
+
+
+@pytest.mark.parametrize("batch,m,n", [(4, 128, 128), (2, 700, 30), (3, 100, 900), (1, 2, 5000), (2, 300, 400)])
+def test_captured_in_a_graph(batch, m, n):
+    G = matrices(batch, m, n, "normal").cuda()
+    out = torch.empty(G.shape, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(max(16, ttm.lib().ttm_orthogonalize_workspace_size(batch, m, n)), dtype=torch.uint8,
+                     device="cuda")
+    ttm.orthogonalize(G, out=out, workspace=ws)
+    want = [out.clone()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ttm.orthogonalize(G, out=out, workspace=ws)
+        ttm.orthogonalize(G, out=out, workspace=ws)
+    G.copy_(matrices(batch, m, n, "low rank", seed=3))
+    want.append(ttm.orthogonalize(G))
+    out.zero_()
+    ws.fill_(255)
+    graph.replay()
+    assert torch.equal(out, want[1]) and not torch.equal(*want)
