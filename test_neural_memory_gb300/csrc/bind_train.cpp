@@ -9,7 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -71,8 +71,9 @@ void check(const Maybe& t, at::IntArrayRef shape, const at::Device& dev, const c
     if (t) check(*t, shape, at::kFloat, dev, what);
 }
 
+// Without the dispatcher, which takes longer than the allocation itself.
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+    return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 at::Tensor output(const Maybe& given, at::IntArrayRef shape, at::ScalarType type, const at::Device& dev,
                   const char* what) {
