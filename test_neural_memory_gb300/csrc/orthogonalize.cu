@@ -7,12 +7,12 @@
 // enough: the steps multiply small singular values by up to a = 3.4 each, and their
 // rounding with them (1 % off for a normal matrix, 6 % for one of low rank plus noise).  With
 // fp16 operands, X itself kept to fp32's accuracy (in registers, or as the sum of two fp16
-// values, hi + lo) and the diagonal of B, its largest entries once X is near orthogonal, in
-// fp32 beside the product, the result is 1.7e-3 to 2.0e-3 off, of which rounding it to bf16
-// is 1.7e-3; with B's diagonal in fp16 it would be up to 2.6e-3, with X rounded to
-// fp16 every step 8e-3 for the matrix of low rank.  A rounding of X is multiplied by the a
-// of the steps still to come: where their product is below 48 (the last three states of five
-// default steps, 1e-4 in all) lo is not kept, which saves a third of the traffic.  Operands are stored times 2^10, so
+// values, hi + lo, in every step) and the diagonal of B, its largest entries once X is near
+// orthogonal, in fp32 beside the product, the result of a normal matrix is 1.7e-3 to 2.0e-3
+// off, of which rounding it to bf16 is 1.7e-3; with B's diagonal in fp16 it would be up to
+// 2.6e-3.  lo is kept to the end because a matrix of few directions has nothing that puts a
+// rounding of X right: with lo dropped from the last three of five states one of rank 1
+// was 1.4e-2 off.  Operands are stored times 2^10, so
 // that entries of 1e-4 stay clear of fp16's subnormal range.
 //
 // Three ways, by size.  128 x 128 at most, or 64 x 1024: one block, or a cluster, keeps a matrix on chip through all
@@ -1136,9 +1136,10 @@ struct GemmParams {
                                     // adds it to beta, by row (or by_column)
     float diag_scale;
     int by_column, diag_n;
-    const __half *in_hi, *in_lo;    // values to add, [batch][M][pitch]; in_lo may be NULL
-    __half *out_hi, *out_lo;        // results, [batch][M][pitch]; out_lo may be NULL
-    int pitch;                      // of all four, a multiple of 8
+    const __half* in_hi;            // values to add, [batch][M][pitch]
+    __half* out_hi;                 // results, likewise
+    __half* lo;                     // kUpdate: lo of X, and of X' in its place
+    int pitch;                      // of all three, a multiple of 8
     __nv_bfloat16* last;            // kUpdate, last step: the result instead, [batch][M][N]
     int* status;
     long long limit;
@@ -1339,9 +1340,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     const uint32_t d = smem_u32(hi) + r * 128 + ((piece ^ (r & 7)) << 4);
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
                                  "l"(in ? p.in_hi + o : p.in_hi), "r"(in ? 16 : 0) : "memory");
-                    if (EPI == kUpdate && p.in_lo)
+                    if (EPI == kUpdate)
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d + kChunkBytes),
-                                     "l"(in ? p.in_lo + o : p.in_lo), "r"(in ? 16 : 0) : "memory");
+                                     "l"(in ? p.lo + o : p.lo), "r"(in ? 16 : 0) : "memory");
                 }
             };
             if (EPI != kGram && turn < chunks) fetch(turn);
@@ -1398,14 +1399,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         } else {
                             const uint4 u = *at_hi;
                             w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-                            if (EPI == kUpdate && p.in_lo) {
+                            if (EPI == kUpdate) {
                                 const uint4 y = *at_lo;
                                 z[0] = y.x; z[1] = y.y; z[2] = y.z; z[3] = y.w;
                             }
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 float2 x = half2_floats(w[i]);
-                                if (EPI == kUpdate && p.in_lo) {
+                                if (EPI == kUpdate) {
                                     const float2 y = half2_floats(z[i]);
                                     x.x += y.x;
                                     x.y += y.y;
@@ -1434,7 +1435,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                 w[i] = bf162_bits(f[2 * i] * kUnscale, f[2 * i + 1] * kUnscale);
                             } else {
                                 w[i] = half2_bits(f[2 * i], f[2 * i + 1]);
-                                if (EPI == kUpdate && p.out_lo) {
+                                if (EPI == kUpdate) {
                                     const float2 x = half2_floats(w[i]);
                                     z[i] = half2_bits(f[2 * i] - x.x, f[2 * i + 1] - x.y);
                                 }
@@ -1442,7 +1443,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         }
                         *at_hi = make_uint4(w[0], w[1], w[2], w[3]);
                         if (EPI == kUpdate) {
-                            if (p.out_lo) *at_lo = make_uint4(z[0], z[1], z[2], z[3]);
+                            if (!p.last) *at_lo = make_uint4(z[0], z[1], z[2], z[3]);
                         } else if (mirror) {            // [64 columns][32 rows]
                             __half* m = reinterpret_cast<__half*>(lo) + (32 * q + 8 * h) * 32 + lane;
 #pragma unroll
@@ -1466,8 +1467,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         if (row0 + r < p.M && col < width) {
                             const size_t g = (size_t)(row0 + r) * width + col;
                             *reinterpret_cast<uint4*>(o_hi + g) = *reinterpret_cast<uint4*>(hi + o);
-                            if (EPI == kUpdate && p.out_lo)
-                                *reinterpret_cast<uint4*>(p.out_lo + mat + g) = *reinterpret_cast<uint4*>(lo + o);
+                            if (EPI == kUpdate && !p.last)
+                                *reinterpret_cast<uint4*>(p.lo + mat + g) = *reinterpret_cast<uint4*>(lo + o);
                         }
                     }
                 } else {
@@ -1827,13 +1828,6 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         ++*launches;
         return cudaGetLastError();
     }
-    // what the steps after step i multiply a small singular value by
-    auto grows_after = [&](int i) {
-        float g = 1.f;
-        while (++i < a.steps) g *= std::fabs(a.coeffs[3 * i]);
-        return g;
-    };
-    bool has_lo = true;
     for (int i = 0; i < a.steps; ++i) {
         const float *c = a.coeffs + 3 * i;
         const Mat &x = hi[i & 1], &y = hi[(i & 1) ^ 1];
@@ -1878,9 +1872,7 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         p.beta = c[0];
         p.pitch = xp;
         p.in_hi = x.p;
-        p.in_lo = has_lo ? lo : nullptr;
-        has_lo = grows_after(i) >= 48.f;
-        p.out_lo = has_lo ? lo : nullptr;
+        p.lo = lo;
         p.out_hi = y.p;
         p.last = i + 1 == a.steps ? static_cast<__nv_bfloat16*>(a.out) : nullptr;
         e = wide ? gemm<false, true, kUpdate>(B, x, p, s) : gemm<false, false, kUpdate>(x, B, p, s);

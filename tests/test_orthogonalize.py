@@ -225,3 +225,28 @@ def test_captured_in_a_graph(batch, m, n):
     ws.fill_(255)
     graph.replay()
     assert torch.equal(out, want[1]) and not torch.equal(*want)
+
+
+def spectrum(batch, m, n, kind, seed=0):
+    """Matrices of few directions, whose small singular values the steps never take to one."""
+    r = torch.Generator().manual_seed(seed)
+    if kind == "rank 1" or kind == "rank 8":
+        k = 1 if kind == "rank 1" else 8
+        return torch.randn((batch, m, k), generator=r) @ torch.randn((batch, k, n), generator=r)
+    if kind == "rank 8 and noise":
+        noise = torch.randn((batch, m, n), generator=r)
+        return 0.01 * noise + torch.randn((batch, m, 8), generator=r) @ torch.randn((batch, 8, n), generator=r)
+    k = min(m, n)                                     # singular values from 1 down to 1e-6
+    u = torch.linalg.qr(torch.randn((batch, m, k), generator=r, dtype=torch.float64))[0]
+    v = torch.linalg.qr(torch.randn((batch, n, k), generator=r, dtype=torch.float64))[0]
+    s = torch.logspace(0, -6, k, dtype=torch.float64) if k > 1 else torch.ones(1, dtype=torch.float64)
+    return ((u * s) @ v.mT).float()
+
+
+@pytest.mark.parametrize("batch,m,n", [(1, 300, 500), (1, 512, 512), (1, 768, 777), (1, 600, 300),
+                                       (1, 100, 900)])
+@pytest.mark.parametrize("kind", ["rank 1", "rank 8", "rank 8 and noise", "1 to 1e-6"])
+def test_few_directions(batch, m, n, kind):
+    """The bound of check(), which lets X be rounded to fp16 as an operand but not as a state: what
+    is lost of a small singular value grows by 3.4 in every later step."""
+    check(spectrum(batch, m, n, kind, seed=m + n), ttm.train.NS_COEFFS)
