@@ -8,11 +8,15 @@
 // rounding with them (1 % off for a normal matrix, 6 % for one of low rank plus noise).  With
 // fp16 operands, X itself kept to fp32's accuracy (in registers, or as the sum of two fp16
 // values, hi + lo, in every step) and the diagonal of B, its largest entries once X is near
-// orthogonal, in fp32 beside the product, the result of a normal matrix is 1.7e-3 to 2.0e-3
-// off, of which rounding it to bf16 is 1.7e-3; with B's diagonal in fp16 it would be up to
+// orthogonal, in fp32 beside the product, the result is 1.7e-3 to 2.1e-3 off (2.4e-3 at 16 x 24), of
+// which rounding it to bf16 is 1.7e-3; with B's diagonal in fp16 it would be up to
 // 2.6e-3.  lo is kept to the end because a matrix of few directions has nothing that puts a
 // rounding of X right: with lo dropped from the last three of five states one of rank 1
-// was 1.4e-2 off.  Operands are stored times 2^10, so
+// was 1.4e-2 off.  For the same reason the diagonal multiplies all of X in the last steps alone, and
+// before them hi, as the rest of B does: B (X - hi) is next to nothing for a matrix of few directions, its
+// diagonal's share by itself is not, and grows with the steps to come (rank 1: 2.6e-2 off at 16 x 24,
+// 4e-3 at 128 x 128).  Near the end that growth is small (kLateGrowth) and a matrix of full rank gains
+// (512 x 512: 1.86e-3 off, 2.06e-3 with hi in every step).  Operands are stored times 2^10, so
 // that entries of 1e-4 stay clear of fp16's subnormal range.
 //
 // Three ways, by size.  128 x 128 at most, or 64 x 1024: one block, or a cluster, keeps a matrix on chip through all
@@ -397,7 +401,8 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
         }
         if (mine && row < rp && (row >> 6) == half) S.diag[row] = diag;
         ready();
-        const float keep = ca + (row < rp ? S.diag[row] * kUnscale : 0.f);
+        const float beside = row < rp ? S.diag[row] * kUnscale : 0.f;
+        const float keep = step < a.late ? 1.f : ca + beside;
         if (warp == 0) {                                // B X, X as [k][n]
             if (elect_one()) {
                 const uint32_t id = idesc_f16(128, lp, 0, 1);
@@ -410,6 +415,14 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
                 mma_commit(&S.done);
             }
             __syncwarp();
+        }
+        if (step < a.late) {                            // the diagonal times hi, the rest of a step a X
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                const float2 h = half2_floats(half2_bits(X[c], X[c + 1]));
+                X[c] = fmaf(ca, X[c], beside * h.x);
+                X[c + 1] = fmaf(ca, X[c + 1], beside * h.y);
+            }
         }
         if (!wait_product()) break;
         if (half * 64 < lp) {
@@ -1133,8 +1146,9 @@ struct GemmParams {
     int part_pitch;
     float alpha, beta;
     float* diag;                    // B's diagonal, [batch][short side]: kSquare writes it, kUpdate
-                                    // adds it to beta, by row (or by_column)
-    float diag_scale;
+                                    // adds it to beta, by row (or by_column): beta + diag times hi,
+                                    // beta + diag_lo / diag_scale of it times lo
+    float diag_scale, diag_lo;      // diag_lo: diag_scale, or 0
     int by_column, diag_n;
     const __half* in_hi;            // values to add, [batch][M][pitch]
     __half* out_hi;                 // results, likewise
@@ -1357,15 +1371,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const bool mirror = EPI != kUpdate && row0 > col0 + 63;
                 const int row = row0 + lane;
                 const float* diag = p.diag + (size_t)at.mat * p.diag_n;
-                float keep = p.beta;
+                float keep = p.beta, keep_lo = p.beta;
                 float* cols = S.cols[warp - 2];         // by column: this chunk's 64
                 if (EPI == kUpdate && p.by_column) {
 #pragma unroll
                     for (int i = 0; i < 64; i += 32)
-                        cols[i + lane] = col0 + i + lane < p.N ? p.diag_scale * diag[col0 + i + lane] : 0.f;
+                        cols[i + lane] = col0 + i + lane < p.N ? diag[col0 + i + lane] : 0.f;
                     __syncwarp();
                 } else if (EPI == kUpdate && row < p.M) {
                     keep = fmaf(p.diag_scale, diag[row], keep);
+                    keep_lo = fmaf(p.diag_lo, diag[row], keep_lo);
                 }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -1405,20 +1420,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             }
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                float2 x = half2_floats(w[i]);
+                                const float2 x = half2_floats(w[i]);
+                                float b0 = keep, b1 = keep;
+                                float2 add = make_float2(0.f, 0.f);
                                 if (EPI == kUpdate) {
                                     const float2 y = half2_floats(z[i]);
-                                    x.x += y.x;
-                                    x.y += y.y;
+                                    float c0 = keep_lo, c1 = keep_lo;
+                                    if (p.by_column) {
+                                        const float2 e =
+                                            *reinterpret_cast<const float2*>(cols + 32 * q + 8 * h + 2 * i);
+                                        b0 = fmaf(p.diag_scale, e.x, b0);
+                                        b1 = fmaf(p.diag_scale, e.y, b1);
+                                        c0 = fmaf(p.diag_lo, e.x, c0);
+                                        c1 = fmaf(p.diag_lo, e.y, c1);
+                                    }
+                                    add = make_float2(c0 * y.x, c1 * y.y);
                                 }
-                                float b0 = keep, b1 = keep;
-                                if (EPI == kUpdate && p.by_column) {
-                                    const float2 e = *reinterpret_cast<const float2*>(cols + 32 * q + 8 * h + 2 * i);
-                                    b0 += e.x;
-                                    b1 += e.y;
-                                }
-                                f[2 * i] = fmaf(p.alpha, f[2 * i], b0 * x.x);
-                                f[2 * i + 1] = fmaf(p.alpha, f[2 * i + 1], b1 * x.y);
+                                f[2 * i] = fmaf(p.alpha, f[2 * i], fmaf(b0, x.x, add.x));
+                                f[2 * i + 1] = fmaf(p.alpha, f[2 * i + 1], fmaf(b1, x.y, add.y));
                             }
                             if (EPI == kSquare && col0 + 32 * q + 8 * h == (row & ~7) && row < p.M) {
 #pragma unroll
@@ -1593,21 +1612,44 @@ Workspace layout(int batch, int m, int n) {
     return w;
 }
 
+// The most that a step multiplies a singular value by, for singular values of 0 to `top`, and the largest
+// that it leaves.
+struct Reach {
+    float most, next;
+};
+Reach reach(const float* c, float top) {
+    Reach r{0.f, 0.f};
+    for (int i = 0; i <= 64; ++i) {
+        const float x = top * i / 64, y = x * x, p = std::fabs(c[0] + (c[1] + c[2] * y) * y);
+        r.most = p > r.most ? p : r.most;
+        r.next = x * p > r.next ? x * p : r.next;
+    }
+    return r;
+}
+
+// The first step after which the steps to come multiply a singular value by less than this.
+constexpr float kLateGrowth = 8.f;
+int late_step(const float* coeffs, int steps) {
+    float most[kNsMaxSteps], top = 1.f, after = 1.f;
+    for (int k = 0; k < steps; ++k) {
+        const Reach r = reach(coeffs + 3 * k, top);
+        most[k] = r.most;
+        top = 1.01f * r.next;
+    }
+    int k = steps;
+    while (k > 0 && after < kLateGrowth) after *= most[--k];
+    return k;
+}
+
 // Whether the steps may run on A alone: bounds on the operands (fp16, scaled) and on the growth of
 // a rounding, from the polynomials' values over the range of the singular values.
 bool tame(const float* coeffs, int steps) {
     float top = 1.f, grown = 1.f;                       // of the singular values, of Q
     for (int k = 0; k < steps; ++k) {
-        const float *c = coeffs + 3 * k;
-        float most = 0.f, next = 0.f;
-        for (int i = 0; i <= 64; ++i) {
-            const float x = top * i / 64, y = x * x, p = std::fabs(c[0] + (c[1] + c[2] * y) * y);
-            most = p > most ? p : most;
-            next = x * p > next ? x * p : next;
-        }
-        grown *= most;
-        if (!(most <= 48.f && most * top * top <= 48.f && grown <= 1024.f)) return false;
-        top = 1.01f * next;
+        const Reach r = reach(coeffs + 3 * k, top);
+        grown *= r.most;
+        if (!(r.most <= 48.f && r.most * top * top <= 48.f && grown <= 1024.f)) return false;
+        top = 1.01f * r.next;
     }
     return steps > 0;
 }
@@ -1767,6 +1809,7 @@ size_t ortho_workspace_bytes(int batch, int m, int n) {
 cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
     OrthoArgs a = in;
     if (a.wait_cycles <= 0) a.wait_cycles = kWaitCycles;
+    a.late = late_step(a.coeffs, a.steps);
     if (small(a.batch, a.m, a.n)) {
         constexpr int smem = 1024 + 2 * kOperandBytes + sizeof(SmallShared), shares = kSide * kSide * 4;
         const int ranks = ((a.m > a.n ? a.m : a.n) + kSide - 1) / kSide;
@@ -1868,6 +1911,7 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         p.M = a.m;
         p.N = a.n;
         p.alpha = p.diag_scale = 1.f / sb;               // -> 2^10 X'
+        p.diag_lo = i < a.late ? 0.f : p.diag_scale;
         p.by_column = !wide;
         p.beta = c[0];
         p.pitch = xp;

@@ -63,6 +63,7 @@ struct OrthoArgs {
     const void* G;                  // [batch][m][n]
     int steps;
     float coeffs[3 * kNsMaxSteps];
+    int late;                       // first step whose B takes its diagonal times all of X
     float eps;
     void* out;                      // [batch][m][n] bf16
     void* workspace;

@@ -250,3 +250,12 @@ def test_few_directions(batch, m, n, kind):
     """The bound of check(), which lets X be rounded to fp16 as an operand but not as a state: what
     is lost of a small singular value grows by 3.4 in every later step."""
     check(spectrum(batch, m, n, kind, seed=m + n), ttm.train.NS_COEFFS)
+
+
+@pytest.mark.parametrize("batch,m,n", [(4, 16, 24), (3, 64, 64), (2, 64, 100), (3, 128, 128), (2, 100, 128),
+                                       (1, 60, 700), (1, 700, 60), (2, 1000, 50), (2, 500, 200), (2, 130, 200)])
+@pytest.mark.parametrize("kind", ["rank 1", "rank 8", "rank 8 and noise", "1 to 1e-6", "normal", "low rank"])
+def test_few_directions_and_short_sides(batch, m, n, kind):
+    """The same bound where B's diagonal is a large part of it although X is far from orthogonal."""
+    G = (matrices if kind in ("normal", "low rank") else spectrum)(batch, m, n, kind, seed=m + n)
+    check(G, ttm.train.NS_COEFFS)
