@@ -6,6 +6,8 @@
 // with u = dy w:
 //   dx = rstd (u - sum u / D - n sum(u n) / D),
 //   dw = sum over rows of dy n,  db = sum over rows of dy.
+// x - mean is taken first in both directions, then times rstd: x rstd - mean rstd would lose what a row
+// far from zero has in n (5e-4 of it at a mean of 1e4 times the spread).
 //
 // What bounds it: HBM, two tensors forward and three in the gradient.  A row is read
 // once and stays in registers: the variance is taken about the mean (no difference of
@@ -339,14 +341,14 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) ln_bwd_kernel(const __grid_c
             load_weights<W>(a.w && lane + k * TPR < packs ? a.w + (lane + k * TPR) * W : nullptr, w, 1.f);
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                const T q = splat<T>(rstd[i]), m = splat<T>(-mean[i] * rstd[i]);
+                const T q = splat<T>(rstd[i]), m = splat<T>(-mean[i]);
 #pragma unroll
                 for (int j = 0; j < N; ++j) {           // absent rows and columns have dy = 0
-                    const T g = pd[i][k].get(j), n = fma(px[i][k].get(j), q, m), u = mul(g, w[j]);
+                    const T g = pd[i][k].get(j), d = add(px[i][k].get(j), m), u = mul(g, w[j]);
                     db[k][j] = add(db[k][j], g);
-                    dw[k][j] = fma(g, n, dw[k][j]);
+                    dw[k][j] = fma(mul(g, q), d, dw[k][j]);
                     su[i] = add(su[i], u);
-                    sn[i] = fma(u, n, sn[i]);
+                    sn[i] = fma(u, d, sn[i]);           // sum(u n) / rstd
                 }
                 px[i][k].repack();
                 pd[i][k].repack();
@@ -368,14 +370,14 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) ln_bwd_kernel(const __grid_c
             for (int i = 0; i < ROWS; ++i) {
                 const long long r = r0 + i * kSets + set;
                 if (r >= a.N) continue;
-                // rstd (u - su - n sn) with n = x rstd - mean rstd, in two products
-                const T q = splat<T>(rstd[i]), m = splat<T>(-mean[i] * rstd[i]);
-                const T c0 = splat<T>(-s[2 * i] * inv), c1 = splat<T>(-s[2 * i + 1] * inv);
+                // rstd (u - su - n sn)
+                const T q = splat<T>(rstd[i]), m = splat<T>(-mean[i]), c0 = splat<T>(-s[2 * i] * inv);
+                const T c1 = splat<T>(-s[2 * i + 1] * rstd[i] * inv * rstd[i]);
                 P out;
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const T n = fma(px[i][k].get(j), q, m);
-                    out.set(j, mul(q, fma(n, c1, fma(pd[i][k].get(j), w[j], c0))));
+                    const T d = add(px[i][k].get(j), m);
+                    out.set(j, mul(q, fma(d, c1, fma(pd[i][k].get(j), w[j], c0))));
                 }
                 out.store(static_cast<E*>(a.dx) + r * a.D + c);
             }

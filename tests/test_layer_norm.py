@@ -190,3 +190,43 @@ def test_row_lengths_and_starts(N, D, dtype, pad):
 @pytest.mark.parametrize("pad", [0, 1])
 def test_many_rows(D, dtype, pad):
     test_forward_and_gradient(4100, D, dtype, True, pad)
+
+
+@pytest.mark.parametrize("N,D", [(40, 64), (70, 131), (33, 768), (9, 1000), (130, 2048), (5, 8192), (5000, 300)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("at", [1e3, 1e4])
+def test_gradient_of_rows_far_from_zero(N, D, dtype, at):
+    """For the given statistics n = (x - mean) rstd errs by two roundings, 2^-23 of itself, however large
+    the mean is against the spread; the other bounds as in test_forward_and_gradient."""
+    wide, w, _, dy = make(N, D, dtype, True, seed=N + D)
+    x = (at + (4.0 if dtype == "f32" else at / 8) * wide.float()).to(DT[dtype])
+    mean, rstd = (t.float() for t in stats(x.double(), 1e-5))
+    out = ttm.layer_norm_bwd(dy.cuda(), x.cuda(), mean.cuda(), rstd.cuda(), w.cuda())
+    m64, r64 = mean.double()[:, None], rstd.double()[:, None]
+    q = (D / 8 + 12) * 2.0 ** -24
+    n, g = (x.double() - m64) * r64, dy.double()
+    u, en = g * w.double(), 2.0 ** -23 * n.abs()
+    s1, s2 = u.mean(-1, keepdim=True), (u * n).mean(-1, keepdim=True)
+    t1 = (q + 2.0 ** -23) * u.abs().mean(-1, keepdim=True)
+    t2 = (q + 2.0 ** -22) * (u * n).abs().mean(-1, keepdim=True) + (u.abs() * en).mean(-1, keepdim=True)
+    tol = r64 * (t1 + n.abs() * t2 + en * s2.abs() + 2.0 ** -21 * (u.abs() + s1.abs() + (n * s2).abs()))
+    close(out["dx"], r64 * (u - s1 - n * s2), tol, DT[dtype])
+    rows = (N + 12) * 2.0 ** -24
+    close(out["dw"], (g * n).sum(0), (rows + 2.0 ** -22) * (g * n).abs().sum(0) + (g.abs() * en).sum(0))
+    close(out["db"], g.sum(0), rows * g.abs().sum(0))
+
+
+@pytest.mark.parametrize("D", [24, 64, 100, 131, 771, 1000, 2048, 3001, 20011])
+@pytest.mark.parametrize("value", [100.0, 1e36, 3e38])
+def test_gradient_of_constant_rows(D, value):
+    """x = mean everywhere, so n = 0: dw = 0 and dx = rstd (u - mean u), also where mean rstd is past fp32."""
+    r = torch.Generator().manual_seed(1)
+    x, dy = torch.full((6, D), value), torch.randn((6, D), generator=r)
+    mean, rstd = torch.full((6,), value), torch.full((6,), 1e-5 ** -0.5)
+    out = ttm.layer_norm_bwd(dy.cuda(), x.cuda(), mean.cuda(), rstd.cuda())
+    assert not out["dw"].any()
+    u, r64 = dy.double(), rstd.double()[:, None]
+    q = (D / 8 + 12) * 2.0 ** -24
+    s1 = u.mean(-1, keepdim=True)
+    tol = r64 * ((q + 2.0 ** -23) * u.abs().mean(-1, keepdim=True) + 2.0 ** -21 * (u.abs() + s1.abs()))
+    close(out["dx"], r64 * (u - s1), tol)
