@@ -230,3 +230,14 @@ def test_gradient_of_constant_rows(D, value):
     s1 = u.mean(-1, keepdim=True)
     tol = r64 * ((q + 2.0 ** -23) * u.abs().mean(-1, keepdim=True) + 2.0 ** -21 * (u.abs() + s1.abs()))
     close(out["dx"], r64 * (u - s1), tol)
+
+@pytest.mark.parametrize("D", [3, 5, 7, 24, 49, 60, 100, 131, 300, 513, 768, 771, 1000, 1600, 3001, 6000, 20011])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_constant_rows_have_their_value_as_mean(D, dtype):
+    """Whole numbers whose sum is exact in fp32: the mean is the value and nothing is left of the row."""
+    value = torch.arange(1.0, 51.0)
+    x = value[:, None].expand(50, D).to(DT[dtype]).contiguous().cuda()
+    b = torch.randn(D, device="cuda")
+    y, mean, rstd = ttm.layer_norm_fwd(x, None, b)
+    assert torch.equal(mean.cpu(), value)
+    assert torch.equal(y, b.to(DT[dtype]).expand(50, D))
