@@ -594,7 +594,7 @@ unsigned long long ttm_launch_count(void);
 /* Failure-detection hooks for tests (no counterpart on the pages: they exist
  * so that the error paths can be exercised without faulting a GPU).
  *   TTM_DBG_WAIT_CYCLES, n >= 0: every bounded device wait of the tensor-core
- *     kernels gives up after n SM clock cycles (0 restores the default, about
+ *     kernels and of the operators around the memory gives up after n SM clock cycles (0 restores the default, about
  *     2 s).  Applies to calls made from now on.
  *   TTM_DBG_STALL_CHUNK, c >= 0: the next call that runs the tensor-core
  *     linear / Titans scan announces 16 bytes more for chunk c's input tiles
@@ -603,7 +603,11 @@ unsigned long long ttm_launch_count(void);
  *     drains its copies and MMAs, frees its tensor memory and returns (its
  *     outputs are then invalid).  A ttm_titans_bwd / ttm_linear_bwd call on
  *     the tensor-core path takes the setting for its chain pass instead, with
- *     c counted in the chain's order (c = 0 is the last chunk).  The setting
+ *     c counted in the chain's order (c = 0 is the last chunk).  A
+ *     ttm_orthogonalize call takes it too: its kernel that keeps a matrix on
+ *     chip and the one that takes the steps on A alone leave their product c
+ *     (three a step) unannounced, the first product from global memory
+ *     announces 16 bytes more for its copy c.  The setting
  *     is used up by that one call; -1 clears it.  Nothing faults, traps or
  *     hangs.
  *   TTM_DBG_FAIL_CALLS, n >= 0: the next n calls of ttm_linear_fwd,

@@ -102,11 +102,13 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* a
                                           long long limit) {
     return __all_sync(0xffffffffu, wait_one(bar, parity, abort, status, limit));
 }
-// After an abort: give copies and products in flight a last bounded chance to land.
+// After an abort: give copies and products in flight a last bounded chance to land, however short the
+// waits themselves are.
+constexpr long long kDrainCycles = 20000000LL;    // ~10 ms
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, long long limit) {
     const long long t0 = clock64();
     while (!mbar_try_wait(bar, parity))
-        if (clock64() - t0 > limit) return;
+        if (clock64() - t0 > max(limit, kDrainCycles)) return;
 }
 
 // ------------------------------------------------------------------- clusters (PTX)
@@ -262,28 +264,38 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
     const uint32_t xb = smem_u32(sx), ab = smem_u32(sa);
     const uint32_t acc = tmem_addr(tmem, (warp & 3) * 32, half * 64);
     uint32_t phase = 0;
-    // Every epilogue ends here: operands written, accumulators read, next product issued.
+    bool lost = false;                                  // a wait of this warp ran out (S.abort is set)
+    bool gone = false;                                  // one of this block did: no products any more
+    // Every epilogue ends here: operands written, accumulators read, next product issued, unless a
+    // wait of any warp has run out.  One verdict for the block, as all its warps meet at the barriers
+    // that follow.
     auto ready = [&]() {
         fence_proxy_async_smem();
         tc_fence_before();
-        __syncthreads();
+        const bool any = __syncthreads_or(lost);
         tc_fence_after();
+        return !any;
     };
     auto wait_product = [&]() {
-        const bool ok = wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles);
+        if (!wait_warp(&S.done, phase, &S.abort, a.status, a.wait_cycles)) lost = true;
         phase ^= 1;
         tc_fence_after();
-        return ok;
+    };
+    auto announce = [&](int product) {                  // or not, for a test of the waits
+        if (product + 1 != a.debug_stall || rank + 1 != ranks) mma_commit(&S.done);
     };
     for (int step = 0; step < a.steps; ++step) {
         const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
+        if (!gone) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            *operand_at(sx, row, half * 8 + q) =
-                make_uint4(half2_bits(X[8 * q], X[8 * q + 1]), half2_bits(X[8 * q + 2], X[8 * q + 3]),
-                           half2_bits(X[8 * q + 4], X[8 * q + 5]), half2_bits(X[8 * q + 6], X[8 * q + 7]));
-        ready();
-        if (warp == 0) {                                // A = X X^T
+            for (int q = 0; q < 8; ++q)
+                *operand_at(sx, row, half * 8 + q) =
+                    make_uint4(half2_bits(X[8 * q], X[8 * q + 1]), half2_bits(X[8 * q + 2], X[8 * q + 3]),
+                               half2_bits(X[8 * q + 4], X[8 * q + 5]), half2_bits(X[8 * q + 6], X[8 * q + 7]));
+            gone = !ready();
+        }
+        if (gone && !kCluster) break;
+        if (warp == 0 && !gone) {                       // A = X X^T
             if (elect_one()) {
                 const uint32_t id = idesc_f16(128, rp, 0, 0);
                 const uint64_t d0 = sdesc(xb, 16, 1024, 2);
@@ -292,11 +304,11 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
                     const uint64_t d = d0 + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4);
                     if (k * 16 < lp) mma_bf16(tmem, d, d, id, k > 0);
                 }
-                mma_commit(&S.done);
+                announce(3 * step);
             }
             __syncwarp();
         }
-        if (!wait_product()) break;
+        if (!gone) wait_product();
         const bool mine = half * 64 < rp;               // columns of A and B that exist
         if (kCluster) {
             // rows of 512 bytes, 16-byte groups permuted by row
@@ -316,6 +328,10 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
             tc_fence_before();
             cluster_sync();                             // every block's share is written
             tc_fence_after();
+            // Whether a wait of any block has run out: all see the same flags, which do not change
+            // before the next product, so all leave in the same step, and none while another one
+            // still reads its shared memory (they meet once more at the end).
+            const float flag = lane < ranks ? peer_load(peer_addr(&S.abort, lane)) : 0.f;
             const int rows = (rp + ranks - 1) / ranks, groups = rp / 4;
 #pragma unroll 2
             for (int i = tid; i < rows * groups; i += kSmallThreads) {
@@ -333,6 +349,7 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
                 const unsigned char* at = reinterpret_cast<unsigned char*>(operand_at(sa, y, g >> 1)) + (g & 1) * 8;
                 for (int k = 0; k < ranks; ++k) peer_store2(peer_addr(at, k), lo, hi);
             }
+            if (__any_sync(0xffffffffu, __float_as_int(flag) != 0)) break;
             asm volatile("fence.proxy.async;" ::: "memory");
             cluster_sync();                             // A is whole in every block
         } else if (mine) {
@@ -352,7 +369,7 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
                 }
             }
         }
-        ready();
+        if (!ready()) break;                            // kCluster: not since all looked at the flags
         if (warp == 0) {                                // A A (A is symmetric)
             if (elect_one()) {
                 const uint32_t id = idesc_f16(128, rp, 0, 0);
@@ -362,11 +379,11 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
                     const uint64_t d = d0 + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4);
                     if (k * 16 < rp) mma_bf16(tmem, d, d, id, k > 0);
                 }
-                mma_commit(&S.done);
+                announce(3 * step + 1);
             }
             __syncwarp();
         }
-        if (!wait_product()) break;
+        wait_product();
         float diag = 0.f;                               // of B, this row's
         if (mine) {                                     // B = b A + c A A over A, without its diagonal
             const float c2 = cc * kUnscale;
@@ -400,7 +417,10 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
             }
         }
         if (mine && row < rp && (row >> 6) == half) S.diag[row] = diag;
-        ready();
+        if (!ready()) {                                 // kCluster: tells the others in the next step
+            gone = true;
+            continue;
+        }
         const float beside = row < rp ? S.diag[row] * kUnscale : 0.f;
         const float keep = step < a.late ? 1.f : ca + beside;
         if (warp == 0) {                                // B X, X as [k][n]
@@ -412,7 +432,7 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
                     if (k * 16 < rp)
                         mma_bf16(tmem, d0 + (((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4),
                                  e0 + (k * 2048 >> 4), id, k > 0);
-                mma_commit(&S.done);
+                announce(3 * step + 2);
             }
             __syncwarp();
         }
@@ -424,7 +444,7 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
                 X[c + 1] = fmaf(ca, X[c + 1], beside * h.y);
             }
         }
-        if (!wait_product()) break;
+        wait_product();
         if (half * 64 < lp) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -461,7 +481,7 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
     }
     tc_fence_before();
     __syncthreads();
-    if (S.abort && tid == 0) drain(&S.done, phase, a.wait_cycles);
+    if (S.abort && tid == 0) drain(&S.done, phase ^ 1, a.wait_cycles);   // the product issued last
     __syncthreads();
     if (kCluster) cluster_sync();                       // no access to a block that has left
     tc_fence_after();
@@ -912,6 +932,9 @@ __global__ void __launch_bounds__(kGramThreads<RP>, RP == 64 ? 2 : 1)
         mma_split(tmem_addr(tmem, 0, column), Operand{u, u + ob, half, false}, Operand{v, v + ob, half, false}, RP,
                   steps, false);
     };
+    auto announce = [&](int product) {                  // or not, for a test of the waits
+        if (product + 1 != a.debug_stall) mma_commit(&S.done);
+    };
     bool ok = true;
     for (int k = 0; k < a.steps; ++k) {
         const float ca = a.coeffs[3 * k], cb = a.coeffs[3 * k + 1], cc = a.coeffs[3 * k + 2];
@@ -920,7 +943,7 @@ __global__ void __launch_bounds__(kGramThreads<RP>, RP == 64 ? 2 : 1)
         if (warp == 0) {
             if (elect_one()) {
                 product(0, sa, sa);
-                mma_commit(&S.done);
+                announce(3 * k);
             }
             __syncwarp();
         }
@@ -955,7 +978,7 @@ __global__ void __launch_bounds__(kGramThreads<RP>, RP == 64 ? 2 : 1)
             if (elect_one()) {
                 if (!last) product(0, sp, sa);
                 if (k > 0) product(RP, sp, sq);
-                mma_commit(&S.done);
+                announce(3 * k + 1);
             }
             __syncwarp();
         }
@@ -977,7 +1000,7 @@ __global__ void __launch_bounds__(kGramThreads<RP>, RP == 64 ? 2 : 1)
             if (warp == 0) {
                 if (elect_one()) {
                     product(0, sa, sp);
-                    mma_commit(&S.done);
+                    announce(3 * k + 2);
                 }
                 __syncwarp();
             }
@@ -1157,6 +1180,7 @@ struct GemmParams {
     __nv_bfloat16* last;            // kUpdate, last step: the result instead, [batch][M][N]
     int* status;
     long long limit;
+    int debug_stall;                // block of K (of a thread block) + 1 that never arrives; 0: none
 };
 
 struct GemmShared {
@@ -1261,7 +1285,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 ok = wait_one(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort, p.status, p.limit);
                 if (!ok) break;
                 unsigned char *da = base + s * kStage, *db = da + kBM * 128;
-                if (rank == 0) mbar_expect_tx(&S.full[s], CG * stage);
+                // (a test of the waits has more announced than comes)
+                if (rank == 0) mbar_expect_tx(&S.full[s], CG * stage + (it + 1 == p.debug_stall ? 16u : 0u));
                 const uint32_t bar = CG == 2 ? peer_addr(&S.full[s], 0) : 0;
                 auto load = [&](unsigned char* dst, const CUtensorMap* m, int x, int y) {
                     if (CG == 2) tma_load_3d_pair(dst, m, bar, x, y, at.mat);
@@ -1881,6 +1906,7 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         p.batch = a.batch;
         p.status = a.status;
         p.limit = a.wait_cycles;
+        p.debug_stall = i == 0 ? a.debug_stall : 0;
         p.M = p.N = r;
         p.K = l;
         p.alpha = kUnscale;                              // (2^10 X)(2^10 X)^T -> 2^10 A
@@ -1906,6 +1932,7 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         p.out_hi = B.p;
         p.diag = reinterpret_cast<float*>(ws + w.diag);
         p.diag_n = r;
+        p.debug_stall = 0;
         e = gemm<false, false, kSquare>(A, A, p, s);
         if (e != cudaSuccess) return e;
         p.M = a.m;

@@ -271,6 +271,7 @@ int ttm_orthogonalize(int batch, int m, int n, int dtype, const void* G, const f
     a.status = ttm::api_status_ptr();
     if (!a.status) return TTM_ERR_CUDA;
     a.wait_cycles = ttm::api_wait_cycles();
+    a.debug_stall = ttm::api_take_stall();
     int launches = 0;
     if (ttm::ortho_launch(a, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
         return TTM_ERR_CUDA;

@@ -69,6 +69,7 @@ struct OrthoArgs {
     void* workspace;
     int* status;
     long long wait_cycles;
+    int debug_stall;                // test hook: product or copy + 1 that is never announced; 0: none
 };
 
 size_t ortho_workspace_bytes(int batch, int m, int n);
@@ -85,6 +86,7 @@ bool make_tma_map(void* map, TmaType type, const void* ptr, const unsigned long 
 // Process-wide state of the API layer (ttm_api.cu).
 int* api_status_ptr();              // device status word of the current device; NULL on failure
 long long api_wait_cycles();        // bounded-wait limit in SM cycles (0: default)
+int api_take_stall();               // test hook: the setting + 1, used up; 0: none
 void api_note_launches(int kernels);
 
 }  // namespace ttm

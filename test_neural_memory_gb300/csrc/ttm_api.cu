@@ -265,6 +265,7 @@ ttm::LinearArgs lmm_scan_args(const ttm::LmmArgs& a) {
 namespace ttm {
 int* api_status_ptr() { return status_ptr(); }
 long long api_wait_cycles() { return g_wait_cycles.load(); }
+int api_take_stall() { return g_stall_chunk.exchange(-1) + 1; }
 void api_note_launches(int kernels) {
     __atomic_add_fetch(&g_launches, (unsigned long long)kernels, __ATOMIC_RELAXED);
 }
