@@ -54,6 +54,7 @@ constexpr int kMaxLog = 4;                        // at most 16 threads over the
 constexpr int kChans = V << kMaxLog;          // channels of a full strip
 constexpr int kNear = 4, kBatch = 8;              // tiles a look-back takes with the hints; maps then
 constexpr long long kWaitCycles = 4000000000LL;   // default limit, ~2 s at 2 GHz
+constexpr long long kDrainCycles = 20000000LL;    // ~10 ms, for copies in flight
 
 // R, the tokens of one thread in a tile: its two tensors (three in the gradient with a gate per
 // channel, which gets half the tokens) take 64 (48) registers.
@@ -392,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
         const unsigned strip = ticket % strips;
         const int j = ticket / strips, n = strip / p.ncols, c0 = (strip % p.ncols) * chans;
         const int t0 = (kBack ? p.ntiles - 1 - j : j) * p.tokens;
-        tc::mbar_expect_tx(arrived, kIns * kBytes);
+        // (a test of the waits has more announced than comes)
+        tc::mbar_expect_tx(arrived, kIns * kBytes + (ticket + 1 == a.debug_stall ? 16u : 0u));
         const int box = min(p.tokens, 256);
         for (int r = 0; r < p.tokens; r += box) {
             tc::tma_load_3d(sx + r * srow, &mx, arrived, c0, t0 + r, n);
@@ -443,12 +445,13 @@ __global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
         unsigned next = 0;
         if (tid == 0) next = p.counter ? atomicAdd(p.counter, 1u) + 1u : ticket + gridDim.x;
 
+        bool late = false;                            // the copies did not come
         if (p.tma) {
             const long long since = clock64();
-            while (!tc::mbar_try_wait(arrived, phase))
+            while (!late && !tc::mbar_try_wait(arrived, phase))
                 if (clock64() - since > a.wait_cycles) {
                     atomicExch(a.status, TTM_ERR_TIMEOUT);
-                    break;
+                    late = true;
                 }
         } else {
             load_rows(sx, p.tokens, srow,
@@ -540,7 +543,17 @@ __global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
 #pragma unroll
             for (int v = 0; v < V; ++v) { A[v] = 1.f; H[v] = 0.f; }
         }
-        __syncthreads();                              // maps written, the tile is in registers
+        // Maps written, the tile is in registers.  If a thread's wait ran out the block hands out no
+        // result and asks for no copy any more: it leaves once the last ones have had time to land.
+        if (__syncthreads_or(late)) {
+            if (tid == 0) {
+                const long long since = clock64();
+                while (!tc::mbar_try_wait(arrived, phase) &&
+                       clock64() - since < max(a.wait_cycles, kDrainCycles)) {
+                }
+            }
+            break;
+        }
 
         if (tid == 0) {
             J.ticket = next;

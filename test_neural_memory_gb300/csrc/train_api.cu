@@ -87,6 +87,7 @@ int glr_run(ttm::GlrArgs& a, int backward, void* workspace, size_t workspace_byt
     a.status = ttm::api_status_ptr();
     if (!a.status) return TTM_ERR_CUDA;
     a.wait_cycles = ttm::api_wait_cycles();
+    a.debug_stall = (unsigned)ttm::api_take_stall();
     int launches = 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = backward ? ttm::glr_bwd_launch(a, s, &launches)

@@ -27,6 +27,7 @@ struct GlrArgs {
     void* workspace;
     int* status;
     long long wait_cycles;
+    unsigned debug_stall;           // test hook: tile + 1 whose copies never complete; 0: none
 };
 
 size_t glr_workspace_bytes(const GlrArgs& a, int backward);

@@ -49,3 +49,17 @@ def stalls(call, at):
 def test_orthogonalize(batch, m, n, at):
     G = torch.randn((batch, m, n), generator=torch.Generator().manual_seed(m)).cuda()
     stalls(lambda: (ttm.orthogonalize(G),), at)
+
+
+@pytest.mark.parametrize("token", [False, True])
+@pytest.mark.parametrize("N,T,D,dtype,at", [(2, 777, 768, "bf16", 3), (2, 5000, 128, "bf16", 0), (1, 40000, 64, "f32", 7),
+                                            (3, 1500, 40, "bf16", 2), (30, 9000, 64, "bf16", 40)])
+def test_recurrence(N, T, D, dtype, at, token):
+    """One of the tiles never arrives: its block leaves, and the blocks that wait for its state give up too."""
+    r = torch.Generator().manual_seed(T)
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    x = torch.randn((N, T, D), generator=r).to(dt).cuda()
+    g = (-0.1 * torch.rand((N, T) if token else (N, T, D), generator=r)).to(torch.float32 if token else dt).cuda()
+    h, _ = ttm.glr_fwd(x, g)
+    stalls(lambda: ttm.glr_fwd(x, g), at)
+    stalls(lambda: tuple(ttm.glr_bwd(g, h, x).values()), at)
