@@ -550,8 +550,11 @@ int ttm_layer_norm_bwd(int N, int D, int dtype, const void* dy, long long dy_row
  *   workspace: ttm_orthogonalize_workspace_size() bytes of device scratch.
  * |G|_F is summed in fp32 (it must stay below 1e19).  A zero matrix gives zero.
  * The products take fp16 operands and add in fp32, X itself is kept to about fp32's
- * accuracy: with the usual coefficients the result is 2e-3 of its norm off (bf16
- * rounding alone: 1.7e-3).  Device waits are bounded: see ttm_device_status.
+ * accuracy: with the usual coefficients the result is 1.7e-3 to 2.1e-3 of its norm off
+ * (bf16 rounding alone: 1.7e-3), whatever the rank; up to 2.5e-3 for a short side
+ * below 64.  The operands' scales follow from the coefficients, which may be of any size as
+ * long as the polynomials stay within fp32's range.  Device waits are bounded: see
+ * ttm_device_status.
  * Shapes: batch, m, n >= 1, 0 <= steps <= 32, eps > 0; batch <= 65535 and
  * m, n <= TTM_ORTHO_MAX_DIM (else TTM_ERR_UNSUPPORTED).  All device pointers are
  * 16-byte aligned; no overlap.  Asynchronous on `stream`; TTM_ERR_INVALID_ARG

@@ -17,7 +17,9 @@
 // diagonal's share by itself is not, and grows with the steps to come (rank 1: 2.6e-2 off at 16 x 24,
 // 4e-3 at 128 x 128).  Near the end that growth is small (kLateGrowth) and a matrix of full rank gains
 // (512 x 512: 1.86e-3 off, 2.06e-3 with hi in every step).  Operands are stored times 2^10, so
-// that entries of 1e-4 stay clear of fp16's subnormal range.
+// that entries of 1e-4 stay clear of fp16's subnormal range, and by other powers of two where the
+// coefficients let the singular values leave the neighbourhood of one (operand_scales): a fixed 2^10 gave
+// infinities for an entry of bA + cA^2 beyond 64.
 //
 // Three ways, by size.  128 x 128 at most, or 64 x 1024: one block, or a cluster, keeps a matrix on chip through all
 // steps (ns_small_kernel: 192 x 128 x 128 in 26 us on the device).  A longer long side: the steps run on A alone, and
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
         if (product + 1 != a.debug_stall || rank + 1 != ranks) mma_commit(&S.done);
     };
     for (int step = 0; step < a.steps; ++step) {
-        const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
+        const NsStep& c = a.step[step];
         if (!gone) {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
@@ -344,8 +346,8 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
 #pragma unroll
                 for (int k = 0; k < kMaxCluster; ++k)
                     if (k < ranks) { t.x += q[k].x; t.y += q[k].y; t.z += q[k].z; t.w += q[k].w; }
-                const uint32_t lo = half2_bits(t.x * kUnscale, t.y * kUnscale);
-                const uint32_t hi = half2_bits(t.z * kUnscale, t.w * kUnscale);
+                const uint32_t lo = half2_bits(t.x * c.a, t.y * c.a);
+                const uint32_t hi = half2_bits(t.z * c.a, t.w * c.a);
                 const unsigned char* at = reinterpret_cast<unsigned char*>(operand_at(sa, y, g >> 1)) + (g & 1) * 8;
                 for (int k = 0; k < ranks; ++k) peer_store2(peer_addr(at, k), lo, hi);
             }
@@ -362,10 +364,8 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
                 for (int h = 0; h < 2; ++h) {
                     const float* f = v + 8 * h;
                     *operand_at(sa, row, half * 8 + 2 * q + h) =
-                        make_uint4(half2_bits(f[0] * kUnscale, f[1] * kUnscale),
-                                   half2_bits(f[2] * kUnscale, f[3] * kUnscale),
-                                   half2_bits(f[4] * kUnscale, f[5] * kUnscale),
-                                   half2_bits(f[6] * kUnscale, f[7] * kUnscale));
+                        make_uint4(half2_bits(f[0] * c.a, f[1] * c.a), half2_bits(f[2] * c.a, f[3] * c.a),
+                                   half2_bits(f[4] * c.a, f[5] * c.a), half2_bits(f[6] * c.a, f[7] * c.a));
                 }
             }
         }
@@ -386,7 +386,6 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
         wait_product();
         float diag = 0.f;                               // of B, this row's
         if (mine) {                                     // B = b A + c A A over A, without its diagonal
-            const float c2 = cc * kUnscale;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float v[16];
@@ -399,8 +398,8 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 old = half2_floats(w[i]);
-                        v[8 * h + 2 * i] = fmaf(c2, v[8 * h + 2 * i], cb * old.x);
-                        v[8 * h + 2 * i + 1] = fmaf(c2, v[8 * h + 2 * i + 1], cb * old.y);
+                        v[8 * h + 2 * i] = fmaf(c.c2, v[8 * h + 2 * i], c.b1 * old.x);
+                        v[8 * h + 2 * i + 1] = fmaf(c.c2, v[8 * h + 2 * i + 1], c.b1 * old.y);
                     }
                     if (half * 8 + 2 * q + h == row >> 3) {
 #pragma unroll
@@ -421,8 +420,8 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
             gone = true;
             continue;
         }
-        const float beside = row < rp ? S.diag[row] * kUnscale : 0.f;
-        const float keep = step < a.late ? 1.f : ca + beside;
+        const float beside = row < rp ? S.diag[row] * c.b : 0.f;
+        const float keep = step < a.late ? 1.f : c.keep + beside;
         if (warp == 0) {                                // B X, X as [k][n]
             if (elect_one()) {
                 const uint32_t id = idesc_f16(128, lp, 0, 1);
@@ -438,10 +437,10 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
         }
         if (step < a.late) {                            // the diagonal times hi, the rest of a step a X
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-                const float2 h = half2_floats(half2_bits(X[c], X[c + 1]));
-                X[c] = fmaf(ca, X[c], beside * h.x);
-                X[c + 1] = fmaf(ca, X[c + 1], beside * h.y);
+            for (int i = 0; i < 64; i += 2) {
+                const float2 h = half2_floats(half2_bits(X[i], X[i + 1]));
+                X[i] = fmaf(c.keep, X[i], beside * h.x);
+                X[i + 1] = fmaf(c.keep, X[i + 1], beside * h.y);
             }
         }
         wait_product();
@@ -453,7 +452,7 @@ __global__ void __launch_bounds__(kSmallThreads, kCluster ? 1 : 2)
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    X[16 * q + i] = fmaf(keep, X[16 * q + i], v[i] * kUnscale);
+                    X[16 * q + i] = fmaf(keep, X[16 * q + i], v[i] * c.b);
             }
         }
     }
@@ -1652,6 +1651,35 @@ Reach reach(const float* c, float top) {
     return r;
 }
 
+// The steps with the powers of two that their operands are stored times, from bounds on the singular
+// values: X (at most `top`) times sx and A (at most top^2) times sa so that the bounds come to between 2^10 and
+// 2^11, and B (an entry is at most its largest eigenvalue, the polynomial less a) times sb so that its
+// bound does to between 2^11 and 2^12.  With the default coefficients all three are 2^10 in every step.  The
+// last X is in fp32 and times 2^10.
+void operand_scales(const float* coeffs, int steps, NsStep* out) {
+    auto power = [](double bound, int to) {            // 2^(to - floor(log2 bound)), 2^to for 0 and infinity
+        int e = 0;
+        if (bound > 0. && std::isfinite(bound)) std::frexp(bound, &e), --e;
+        return std::ldexp(1., to - (e < -100 ? -100 : (e > 100 ? 100 : e)));
+    };
+    double top = 1., sx = kScale;
+    for (int k = 0; k < steps; ++k) {
+        const double a = coeffs[3 * k], b = coeffs[3 * k + 1], c = coeffs[3 * k + 2];
+        double next = 0., most = 0.;                    // of X', of B
+        for (int i = 0; i <= 64; ++i) {
+            const double x = top * i / 64, y = x * x, p = b * y + c * y * y;
+            most = std::fmax(most, std::fabs(p));
+            next = std::fmax(next, x * std::fabs(a + p));
+        }
+        const double sa = power(top * top, 10), sb = power(most, 11);
+        top = std::fmin(1.01 * next, 1e60);
+        const double sy = k + 1 == steps ? kScale : power(top, 10);
+        out[k] = {(float)(sa / (sx * sx)), (float)(b * sb / sa), (float)(c * sb / (sa * sa)), (float)(a * sy / sx),
+                  (float)(sy / (sx * sb))};
+        sx = sy;
+    }
+}
+
 // The first step after which the steps to come multiply a singular value by less than this.
 constexpr float kLateGrowth = 8.f;
 int late_step(const float* coeffs, int steps) {
@@ -1666,14 +1694,16 @@ int late_step(const float* coeffs, int steps) {
     return k;
 }
 
-// Whether the steps may run on A alone: bounds on the operands (fp16, scaled) and on the growth of
-// a rounding, from the polynomials' values over the range of the singular values.
+// Whether the steps may run on A alone: bounds on the operands (fp16, scaled; from above against
+// overflow, from below against what lo cannot hold) and on the growth of a rounding, from the
+// polynomials' values over the range of the singular values.
 bool tame(const float* coeffs, int steps) {
     float top = 1.f, grown = 1.f;                       // of the singular values, of Q
     for (int k = 0; k < steps; ++k) {
         const Reach r = reach(coeffs + 3 * k, top);
         grown *= r.most;
-        if (!(r.most <= 48.f && r.most * top * top <= 48.f && grown <= 1024.f)) return false;
+        if (!(top >= 0.0625f && top * top <= 48.f && r.most <= 48.f && r.most * top * top <= 48.f)) return false;
+        if (!(grown >= 0.25f && grown <= 1024.f)) return false;
         top = 1.01f * r.next;
     }
     return steps > 0;
@@ -1835,6 +1865,7 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
     OrthoArgs a = in;
     if (a.wait_cycles <= 0) a.wait_cycles = kWaitCycles;
     a.late = late_step(a.coeffs, a.steps);
+    operand_scales(a.coeffs, a.steps, a.step);
     if (small(a.batch, a.m, a.n)) {
         constexpr int smem = 1024 + 2 * kOperandBytes + sizeof(SmallShared), shares = kSide * kSide * 4;
         const int ranks = ((a.m > a.n ? a.m : a.n) + kSide - 1) / kSide;
@@ -1897,11 +1928,8 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         return cudaGetLastError();
     }
     for (int i = 0; i < a.steps; ++i) {
-        const float *c = a.coeffs + 3 * i;
+        const NsStep& c = a.step[i];
         const Mat &x = hi[i & 1], &y = hi[(i & 1) ^ 1];
-        // B is stored times 2^10, less where its coefficients are large
-        float sb = kScale;
-        while (sb > 1.f && (std::fabs(c[1]) + std::fabs(c[2])) * sb > 8.f * kScale) sb *= 0.5f;
         GemmParams p{};
         p.batch = a.batch;
         p.status = a.status;
@@ -1909,7 +1937,7 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         p.debug_stall = i == 0 ? a.debug_stall : 0;
         p.M = p.N = r;
         p.K = l;
-        p.alpha = kUnscale;                              // (2^10 X)(2^10 X)^T -> 2^10 A
+        p.alpha = c.a;
         p.pitch = ap;
         p.out_hi = A.p;
         p.splits = splits;
@@ -1926,8 +1954,8 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
             ++*launches;
         }
         p.K = r;
-        p.alpha = c[2] * sb * kUnscale * kUnscale;       // -> sb (b A + c A A)
-        p.beta = c[1] * sb * kUnscale;
+        p.alpha = c.c2;
+        p.beta = c.b1;
         p.in_hi = A.p;
         p.out_hi = B.p;
         p.diag = reinterpret_cast<float*>(ws + w.diag);
@@ -1937,10 +1965,10 @@ cudaError_t ortho_launch(const OrthoArgs& in, cudaStream_t s, int* launches) {
         if (e != cudaSuccess) return e;
         p.M = a.m;
         p.N = a.n;
-        p.alpha = p.diag_scale = 1.f / sb;               // -> 2^10 X'
+        p.alpha = p.diag_scale = c.b;
         p.diag_lo = i < a.late ? 0.f : p.diag_scale;
         p.by_column = !wide;
-        p.beta = c[0];
+        p.beta = c.keep;
         p.pitch = xp;
         p.in_hi = x.p;
         p.lo = lo;

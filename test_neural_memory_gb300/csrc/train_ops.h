@@ -58,6 +58,12 @@ cudaError_t layer_norm_bwd_launch(const LayerNormArgs& a, cudaStream_t s, int* l
 
 // Orthogonalised update (orthogonalize.cu).
 constexpr int kNsMaxSteps = 32;
+// One step with its operands as they are stored: X, A and B times a power of two each.
+struct NsStep {
+    float a;                        // A = a X X^T
+    float b1, c2;                   // B = b1 A + c2 A A
+    float keep, b;                  // X' = (keep + b diag B) X + b (B without its diagonal) X
+};
 struct OrthoArgs {
     int batch, m, n;
     int bf16;                       // type of G; 0: fp32
@@ -65,6 +71,7 @@ struct OrthoArgs {
     int steps;
     float coeffs[3 * kNsMaxSteps];
     int late;                       // first step whose B takes its diagonal times all of X
+    NsStep step[kNsMaxSteps];       // set by ortho_launch
     float eps;
     void* out;                      // [batch][m][n] bf16
     void* workspace;

@@ -259,3 +259,39 @@ def test_few_directions_and_short_sides(batch, m, n, kind):
     """The same bound where B's diagonal is a large part of it although X is far from orthogonal."""
     G = (matrices if kind in ("normal", "low rank") else spectrum)(batch, m, n, kind, seed=m + n)
     check(G, ttm.train.NS_COEFFS)
+
+
+def steps_in_11_bits(G, coeffs):
+    """steps64, and the same with every operand rounded to 11 significant bits whatever its size."""
+    def half(t):
+        f, e = torch.frexp(t)
+        return torch.ldexp(torch.round(torch.ldexp(f, torch.tensor(11))), e - 11)
+
+    out = []
+    for rounded in (lambda t: t, half):
+        X = G.double()
+        tall = X.shape[-2] > X.shape[-1]
+        X = X.mT if tall else X
+        X = X / X.flatten(1).norm(dim=1)[:, None, None]
+        for a, b, c in coeffs:
+            Y = rounded(X)
+            A = rounded(Y @ Y.mT)
+            X = a * X + rounded(b * A + c * (A @ A)) @ Y
+        out.append(X.mT if tall else X)
+    return out
+
+
+@pytest.mark.parametrize("m,n", [(2, 40), (64, 64), (128, 100), (60, 700), (100, 300), (900, 40), (300, 200)])
+@pytest.mark.parametrize("coeffs", [[(1.0, -200.0, 0.0)], [(0.0, 0.0, 3e4)], [(0.0, 1e-7, 0.0)],
+                                    [(40.0, 0.0, 0.0), (0.01, 0.0, 0.0)], [(100.0, 0.0, 0.0), (1.0, -1e-4, 3e-9)],
+                                    [(1e6, 0.0, 0.0), (1e-6, 1e-18, 0.0)], [(1e-3, 0.0, 0.0)] * 3,
+                                    [(1e-4, 0.0, 0.0), (0.0, 1e8, 0.0)]])
+@pytest.mark.parametrize("kind", ["normal", "rank 1"])
+def test_coefficients_of_any_size(m, n, coeffs, kind):
+    """Finite coefficients whose polynomials are finite: the operands' scales follow them.  The bound is
+    check()'s, with operands of 11 bits and no limit to their exponent."""
+    G = matrices(2, m, n, "normal", seed=3) if kind == "normal" else spectrum(2, m, n, kind, seed=3)
+    O = ttm.orthogonalize(G.cuda(), coeffs=coeffs).double().cpu()
+    ref, rough = steps_in_11_bits(G, coeffs)
+    err, moved, size = ((t - ref).flatten(1).norm(dim=1) for t in (O, rough, 0 * ref))
+    assert bool((err <= 2 * moved + (2.0 ** -9 + 2e-4) * size).all()), (err / size, moved / size)
