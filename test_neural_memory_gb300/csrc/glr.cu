@@ -106,20 +106,34 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, const float (&f)[V]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(bf16_of_pair(pair(f[0], f[1])), bf16_of_pair(pair(f[2], f[3])));
 }
 
-// exp through the base-2 unit (2 units in the last place); -infinity gives 0.
+// exp of gates of type G; -infinity gives 0.  An fp32 gate takes expf (2 units in the last place).  A bf16
+// gate takes the base-2 unit on the rounded product with log2 e, which adds |g| 2^-24 of the
+// result, 2^-15 of what half a unit of the gate itself is worth.
+template <typename G>
 __device__ __forceinline__ float retention(float g) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(g * 1.44269504088896341f));
-    return r;
+    if constexpr (sizeof(G) == 4) {
+        return expf(g);
+    } else {
+        float r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(g * 1.44269504088896341f));
+        return r;
+    }
 }
 
+template <typename G>
 __device__ __forceinline__ void retention(const f2 (&g)[2], f2 (&r)[2]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         float lo, hi;
-        split(mul(g[i], splat<f2>(1.44269504088896341f)), lo, hi);
-        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(lo));
-        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(hi));
+        if constexpr (sizeof(G) == 4) {
+            split(g[i], lo, hi);
+            lo = expf(lo);
+            hi = expf(hi);
+        } else {
+            split(mul(g[i], splat<f2>(1.44269504088896341f)), lo, hi);
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(lo));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(hi));
+        }
         r[i] = pair(lo, hi);
     }
 }
@@ -374,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
     unsigned char* so = smem + kIns * kBytes;                        // h or dx
     unsigned char* sog = so + kBytes;                                // gradient: dg (gate per channel)
     Joints& J = *reinterpret_cast<Joints*>(so + (kBack && !kToken ? 2 : 1) * kBytes);
-    float* sgt = reinterpret_cast<float*>(&J + 1);    // token gate: a tile's, two in turn
+    float* sgt = reinterpret_cast<float*>(&J + 1);    // token gate: a tile's retentions, two in turn
     uint64_t* arrived = reinterpret_cast<uint64_t*>(&J.arrived);
 
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -416,6 +430,15 @@ __global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
                          : "memory");
         }
     };
+    // waits for this thread's and leaves their retentions in their place, once a token for all channels
+    auto gates_arrived = [&](bool any, unsigned turn) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (any)
+            for (int i = tid; i < p.tokens; i += kThreads) {
+                float& g = sgt[turn * p.tokens + i];
+                g = retention<float>(g);
+            }
+    };
     if (tid == 0) {
         J.ticket = p.counter ? atomicAdd(p.counter, 1u) + 1u : blockIdx.x;
         if (p.tma) {
@@ -427,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
     __syncthreads();
     if (kToken) {
         if (J.ticket < p.tiles) request_gates(J.ticket, 0);
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        gates_arrived(J.ticket < p.tiles, 0);
         __syncthreads();
     }
 
@@ -480,11 +503,11 @@ __global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
         const float* gt = sgt + phase * p.tokens + r0;
         auto retain = [&](int q, f2 (&r)[2]) {        // of token r0 + q
             if constexpr (kToken) {
-                r[0] = r[1] = splat<f2>(retention(gt[q]));
+                r[0] = r[1] = splat<f2>(gt[q]);
             } else {
                 f2 g[2];
                 hg[q].get(g);
-                retention(g, r);
+                retention<E>(g, r);
             }
         };
 
@@ -693,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
                 if (c0 + ch + v < a.D) end[n * a.D + c0 + ch + v] = f[v];
         }
         if (p.tma_out) tc::fence_proxy_async_smem();
-        if (kToken) asm volatile("cp.async.wait_all;" ::: "memory");
+        if (kToken) gates_arrived(J.ticket < p.tiles, phase ^ 1);
         __syncthreads();
         if (p.tma_out) {
             if (tid == 0) {
@@ -789,9 +812,9 @@ __global__ void glr_serial_kernel(GlrArgs a, const float* start) {
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             if (t0 + b >= a.T) break;
-            const float rt = kToken ? retention(gv[b][0]) : 0.f;
+            const float rt = kToken ? retention<float>(gv[b][0]) : 0.f;
 #pragma unroll
-            for (int v = 0; v < W; ++v) s[v] = fmaf(kToken ? rt : retention(gv[b][v]), s[v], xv[b][v]);
+            for (int v = 0; v < W; ++v) s[v] = fmaf(kToken ? rt : retention<E>(gv[b][v]), s[v], xv[b][v]);
             put_wide(h + (size_t)(t0 + b) * a.D, s);
         }
     }
@@ -833,7 +856,7 @@ __global__ void glr_serial_back_kernel(GlrArgs a) {
 #pragma unroll
             for (int v = 0; v < W; ++v) {
                 G[b][v] += c[v];
-                c[v] = retention(gv[b][v]) * G[b][v];
+                c[v] = retention<E>(gv[b][v]) * G[b][v];
                 before[b][v] = c[v] * (t > 0 ? before[b][v] : first[v]);
             }
             put_wide(dx + (size_t)t * a.D, G[b]);

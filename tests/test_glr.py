@@ -327,3 +327,29 @@ def test_short_sequences_and_many_channels(N, T, D, dtype, token, pad):
     close(out["dx"], dx, tx, x.dtype)
     close(out["dg"], dg, tg, g.dtype)
     close(out["dh0"], c, tc, torch.float32)
+
+
+@pytest.mark.parametrize("token", [False, True])
+@pytest.mark.parametrize("T,D", [(6, 64), (40, 64), (300, 64), (2500, 8)])
+def test_gates_far_from_zero(token, T, D):
+    """The bound holds however far a gate is from 0: states decay from 1e37 through gates of -30 to -1
+    and are brought back by a value of 1e30 now and then.  The retention over a stretch of tokens is a product
+    that goes to 0 below 2^-126, so a state errs by that share of the largest one before it too."""
+    r = torch.Generator().manual_seed(T)
+    shape = (40, T) if token else (40, T, D)
+    x = torch.zeros((40, T, D))
+    x[:, ::9] = 1e30 * torch.randn((40, (T + 8) // 9, D), generator=r)
+    g = -torch.exp(math.log(30.0) * torch.rand(shape, generator=r))
+    h0 = 1e37 * torch.randn((40, D), generator=r)
+    h, last = ttm.glr_fwd(on(x), on(g), h0=on(h0))
+    rh, th, rl, tl = reference(x, g, h0)
+    lost = 2.0 ** -126 * max(float(h0.abs().max()), float(rh.abs().max()))
+    close(h, rh, th + lost, torch.float32)
+    close(last, rl, tl + lost, torch.float32)
+    rh = rh.float()
+    out = ttm.glr_bwd(on(g), on(rh), on(x), h0=on(h0 * 1e-30), dh_last=on(h0))
+    dx, _, dg, _, c, _ = grad_reference(g, rh, h0 * 1e-30, x, h0)
+    assert all(bool(torch.isfinite(t).all()) for t in (out["dx"], out["dh0"]))
+    _, tx, _, _, _, tc = grad_reference(g, rh, h0 * 1e-30, x, h0)
+    close(out["dx"], dx, tx + lost, torch.float32)
+    close(out["dh0"], c, tc + lost, torch.float32)
