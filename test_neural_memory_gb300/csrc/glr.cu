@@ -138,10 +138,18 @@ __device__ __forceinline__ void retention(const f2 (&g)[2], f2 (&r)[2]) {
     }
 }
 
-// A c + H for the map (A, H).  A state of exactly zero stays out of the product: a
-// growing gate may have taken A to infinity, which must not turn it into NaN.
-__device__ __forceinline__ float apply(float A, float H, float c) {
-    return c == 0.f ? H : fmaf(A, c, H);
+// R^2 c + H for the map (A, H) with R the root of A.  Growing gates may take A past fp32's range
+// while A c is well inside it (gates of 0.05 over 2000 tokens, a state of 1e-30); the root has
+// twice the range, which is that of A c for any state but zero, which stays out of the product.
+__device__ __forceinline__ float apply(float R, float H, float c) {
+    return c == 0.f ? H : fmaf(c * R, R, H);
+}
+// The root of a run's A (to 2^-23, once for the 4 to 16 retentions that A is the product of); an A of
+// infinity times 0 is one that a forgetting gate (-infinity) has cut off.
+__device__ __forceinline__ float root(float A) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(A));
+    return A == A ? r : 0.f;
 }
 
 // ------------------------------------------------------------ global <-> shared
@@ -225,7 +233,7 @@ struct TilePlan {
     int tokens;            // of a tile
     int ntiles, ncols;     // tiles of a sequence, strips of channels
     unsigned* counter;     // hands out tiles in order; NULL when ntiles == 1
-    unsigned long long* maps;   // [strip][tile][channel] in processing order: A low, H high word
+    unsigned long long* maps;   // [strip][tile][channel] in processing order: root of A low, H high word
     unsigned* ends;        // [strip][tile][channel]: state after the tile
     unsigned* hints;       // [strip][32 channels][tile]: kMapThere, kEndThere
     size_t words_bytes;    // of the counter, maps, ends and hints, all set to kEmpty before
@@ -270,7 +278,7 @@ __device__ __forceinline__ float apply_map(unsigned long long w, float s) {
 
 // Shared memory behind the input tiles.
 struct Joints {
-    float a[kWarps][kChans], h[kWarps][kChans];   // map of each warp's tokens, by channel
+    float a[kWarps][kChans], h[kWarps][kChans];   // map of each warp's tokens, by channel (roots)
     float carry[kChans];                          // state before the tile
     unsigned ticket;
     unsigned long long arrived;                   // mbarrier of the tensor copies
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
             }
         };
 
-        // This run's map
+        // This run's map; from here on A is its root
         float A[V], H[V];
         {
             f2 mA[2] = {splat<f2>(1.f), splat<f2>(1.f)}, mH[2] = {splat<f2>(0.f), splat<f2>(0.f)};
@@ -531,6 +539,9 @@ __global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
             split(mA[1], A[2], A[3]);
             split(mH[0], H[0], H[1]);
             split(mH[1], H[2], H[3]);
+            A[0] = root(A[0]);
+#pragma unroll
+            for (int v = 1; v < V; ++v) A[v] = kToken ? A[0] : root(A[v]);
         }
 #pragma unroll
         for (int q = 0; q < R; ++q) {

@@ -353,3 +353,32 @@ def test_gates_far_from_zero(token, T, D):
     _, tx, _, _, _, tc = grad_reference(g, rh, h0 * 1e-30, x, h0)
     close(out["dx"], dx, tx + lost, torch.float32)
     close(out["dh0"], c, tc + lost, torch.float32)
+
+
+@pytest.mark.parametrize("token", [False, True])
+@pytest.mark.parametrize("T,D,dtype", [(100, 8, "f32"), (2000, 4, "f32"), (3900, 4, "bf16"), (5000, 64, "f32"),
+                                       (3000, 131, "bf16")])
+def test_growing_gates(token, T, D, dtype):
+    """A state of 1e-30 that grows by e^130 in all, one more than fp32 holds, before a reset and after it:
+    every state is finite although the retention over such a stretch is not."""
+    r = torch.Generator().manual_seed(T)
+    shape = (3, T) if token else (3, T, D)
+    g = (240.0 / T) * (1 + 0.1 * torch.rand(shape, generator=r))
+    g[:, T // 2] = -math.inf
+    g = g.to(torch.float32 if token else DT[dtype])
+    x = torch.zeros((3, T, D), dtype=DT[dtype])
+    x[:, T // 2] = 1e-30
+    x[:, T // 2 + 1] = 1e-30 * torch.randn((3, D), generator=r)
+    h0 = 1e-30 * torch.randn((3, D), generator=r)
+    h, last = ttm.glr_fwd(on(x), on(g), h0=on(h0))
+    rh, th, rl, tl = reference(x, g, h0)
+    assert float(rh.abs().max()) > 1e20
+    close(h, rh, th, x.dtype)
+    close(last, rl, tl, torch.float32)
+    dh, dl = torch.zeros_like(x), 1e-30 * torch.randn((3, D), generator=r)
+    rh = torch.ones_like(x)
+    out = ttm.glr_bwd(on(g), on(rh), on(dh), h0=on(h0), dh_last=on(dl))
+    dx, tx, dg, tg, c, tc = grad_reference(g, rh, h0, dh, dl)
+    close(out["dx"], dx, tx, x.dtype)
+    close(out["dg"], dg, tg, g.dtype)
+    close(out["dh0"], c, tc, torch.float32)
