@@ -967,8 +967,11 @@ cudaError_t tile_launch(const GlrArgs& a, TilePlan p, cudaStream_t s) {
     constexpr int tiles = 1 + (kToken ? 0 : 1) + (kBack ? 1 : 0) + (kBack && !kToken ? 2 : 1);
     const int smem = tiles * kTileBytes<E, kToken, kBack> + (int)sizeof(Joints) +
                      (kToken ? 2 * p.tokens * (int)sizeof(float) : 0);
+    // The most any call needs, so that calls of two host threads set the same limit
+    constexpr int most = tiles * kTileBytes<E, kToken, kBack> + (int)sizeof(Joints) +
+                         (kToken ? 2 * kThreads * kRun<E, kToken, kBack> * (int)sizeof(float) : 0);
     auto kernel = glr_tile_kernel<E, kToken, kBack>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     if (p.ntiles > 1) {
         e = cudaMemsetAsync(a.workspace, kEmpty & 0xff, p.words_bytes, s);

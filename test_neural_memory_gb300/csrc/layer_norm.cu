@@ -551,10 +551,13 @@ cudaError_t run(const LayerNormArgs& a, bool back, int blocks, cudaStream_t s) {
     } else if constexpr (kShift ? shift_pays<E>(TPR * K * W) : W > 2 || TPR > 32 || K * W < 32) {
         constexpr int rows = bytes > (kShift ? 16 : 32) || K * W > 8 ? 1 : 2;
         constexpr int resident = K * W <= (kShift ? 8 : 16) ? kResident : 1;
-        const size_t shared = TPR == kThreads || !a.partial ? 0 : (size_t)kWarps * 2 * TPR * K * W * 4;
+        // The limit is what a call with dw or db needs, also for one without: calls of two host threads
+        // set the same
+        constexpr int most = TPR == kThreads ? 0 : kWarps * 2 * TPR * K * W * 4;
+        const size_t shared = a.partial ? most : 0;
         auto kernel = ln_bwd_kernel<E, W, kShift, TPR, K, rows, resident>;
         const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
         kernel<<<blocks, kThreads, shared, s>>>(a);
     }
