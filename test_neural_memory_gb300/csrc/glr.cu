@@ -239,6 +239,7 @@ struct TilePlan {
     size_t words_bytes;    // of the counter, maps, ends and hints, all set to kEmpty before
     unsigned tiles;        // of all strips
     int tma, tma_out;      // inputs, outputs by tensor copies
+    int x_first, g_first;  // x, g have their tokens further apart than their sequences
     int width_o;           // else: access width of the outputs' rows
     float* dg_part;        // token gate over several strips: [ncols][N T] partial sums
 };
@@ -419,8 +420,9 @@ __global__ void __launch_bounds__(kThreads, kResident<kToken, kBack>)
         tc::mbar_expect_tx(arrived, kIns * kBytes + (ticket + 1 == a.debug_stall ? 16u : 0u));
         const int box = min(p.tokens, 256);
         for (int r = 0; r < p.tokens; r += box) {
-            tc::tma_load_3d(sx + r * srow, &mx, arrived, c0, t0 + r, n);
-            if (!kToken) tc::tma_load_3d(sg + r * srow, &mg, arrived, c0, t0 + r, n);
+            tc::tma_load_3d(sx + r * srow, &mx, arrived, c0, p.x_first ? n : t0 + r, p.x_first ? t0 + r : n);
+            if (!kToken)
+                tc::tma_load_3d(sg + r * srow, &mg, arrived, c0, p.g_first ? n : t0 + r, p.g_first ? t0 + r : n);
             // row r of sh holds h of token t0 + r - 1; token -1 is h0, taken below
             if (kBack) tc::tma_load_3d(sh + r * srow, &mh, arrived, c0, t0 + r - 1, n);
         }
@@ -949,17 +951,24 @@ TilePlan make_plan(const GlrArgs& a, int backward, size_t* bytes) {
     return p;
 }
 
-// Tensor maps of the inputs where they allow it: 16-byte rows and strides below 2^40.
+// Tensor maps where the strides allow it: 16-byte rows and strides below 2^40, the outer one the
+// larger and a multiple of the inner one.  Of the tokens and the sequences those come first (`first`: the
+// sequences do) that lie closer together.
 template <typename E>
 bool tile_map(CUtensorMap* m, const TilePlan& p, const GlrArgs& a, const void* ptr, long long seq,
-              long long tok) {
-    const unsigned long long es = sizeof(E), D = a.D;
-    unsigned long long ts = a.T > 1 ? tok * es : (D * es + 15) / 16 * 16;
-    unsigned long long ss = a.N > 1 ? seq * es : ts * a.T;
-    if (reinterpret_cast<uintptr_t>(ptr) % 16 || ts % 16 || ss % 16 || ss >= 1ull << 40) return false;
-    return make_tma_map(m, sizeof(E) == 2 ? TmaType::bf16 : TmaType::f32, ptr,
-                        {D, (unsigned long long)a.T, (unsigned long long)a.N}, {ts, ss},
-                        {(unsigned)V << p.cw_log, (unsigned)min(p.tokens, 256), 1u}, false);
+              long long tok, int* first = nullptr) {
+    const unsigned long long es = sizeof(E), D = a.D, T = a.T, N = a.N;
+    unsigned long long ts = tok * es, ss = seq * es;
+    if (a.T == 1) ts = a.N > 1 ? ss : (D * es + 15) / 16 * 16;   // any will do
+    if (a.N == 1) ss = ts * T;
+    const bool swap = ss < ts;
+    const unsigned long long inner = swap ? ss : ts, outer = swap ? ts : ss;
+    if (reinterpret_cast<uintptr_t>(ptr) % 16 || inner % 16 || outer % inner || outer >= 1ull << 40) return false;
+    if (first) *first = swap;
+    const unsigned tokens = (unsigned)min(p.tokens, 256);
+    const TmaType type = sizeof(E) == 2 ? TmaType::bf16 : TmaType::f32;
+    if (swap) return make_tma_map(m, type, ptr, {D, N, T}, {ss, ts}, {(unsigned)V << p.cw_log, 1u, tokens}, false);
+    return make_tma_map(m, type, ptr, {D, T, N}, {ts, ss}, {(unsigned)V << p.cw_log, tokens, 1u}, false);
 }
 
 template <typename E, bool kToken, bool kBack>
@@ -979,8 +988,8 @@ cudaError_t tile_launch(const GlrArgs& a, TilePlan p, cudaStream_t s) {
     }
     CUtensorMap mx{}, mg{}, mh{}, mo{}, mog{};
     p.tma = ((size_t)V << p.cw_log) * sizeof(E) >= 16 &&
-            tile_map<E>(&mx, p, a, a.x, a.x_seq, a.x_tok) &&
-            (kToken || tile_map<E>(&mg, p, a, a.g, a.g_seq, a.g_tok)) &&
+            tile_map<E>(&mx, p, a, a.x, a.x_seq, a.x_tok, &p.x_first) &&
+            (kToken || tile_map<E>(&mg, p, a, a.g, a.g_seq, a.g_tok, &p.g_first)) &&
             (!kBack || tile_map<E>(&mh, p, a, a.h, (long long)a.T * a.D, a.D));
     p.tma_out = ((size_t)V << p.cw_log) * sizeof(E) >= 16 &&
                 tile_map<E>(&mo, p, a, kBack ? a.dx : a.h, (long long)a.T * a.D, a.D) &&

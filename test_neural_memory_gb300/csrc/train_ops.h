@@ -84,8 +84,8 @@ size_t ortho_workspace_bytes(int batch, int m, int n);
 cudaError_t ortho_launch(const OrthoArgs& a, cudaStream_t s, int* launches);
 
 // Tensor map (a CUtensorMap) of a 3-D view: dims from the innermost on, byte strides of
-// the outer two (multiples of 16, below 2^40), a box of at most 256 values a side whose
-// inner extent is a multiple of 16 bytes.  Values outside the view load as zero.
+// the outer two (multiples of 16, below 2^40, the second a multiple of the first), a box of at most
+// 256 values a side whose inner extent is a multiple of 16 bytes.  Values outside the view load as zero.
 // tma_map.cu; false when the driver refuses it.
 enum class TmaType { f32, bf16, f16 };
 bool make_tma_map(void* map, TmaType type, const void* ptr, const unsigned long long (&dims)[3],

@@ -382,3 +382,48 @@ def test_growing_gates(token, T, D, dtype):
     close(out["dx"], dx, tx, x.dtype)
     close(out["dg"], dg, tg, g.dtype)
     close(out["dh0"], c, tc, torch.float32)
+
+
+@pytest.mark.parametrize("N,T,D", [(3, 700, 64), (16, 40, 136), (5, 1025, 16), (2, 3000, 131), (1, 600, 64), (300, 9, 8)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("order", ["time first", "padded sequences", "windows", "mixed"])
+@pytest.mark.parametrize("token", [False, True])
+def test_other_orders(N, T, D, dtype, order, token):
+    """Tokens further apart than sequences, sequences a stride apart that no number of tokens makes, windows that
+    share their rows, and x and g of two orders: the results are those of contiguous tensors, bit for bit."""
+    x, g, h0 = (on(t) for t in make(N, T, D, dtype, token, seed=N + T, resets=True))
+    if token and dtype == "bf16":
+        g = g.float()
+
+    def lay(t, how):
+        if how == "time first":
+            return t.transpose(0, 1).contiguous().transpose(0, 1)
+        inner = t[0].numel()
+        if how == "padded sequences":                 # 24 or 8 elements: rows stay on 16 bytes, or do not
+            buf = torch.full((N, inner + (24 if D % 8 == 0 else 8)), math.nan, dtype=t.dtype, device="cuda")
+            v = buf[:, :inner].view(N, *t.shape[1:]) if N == 1 else buf.as_strided(
+                t.shape, (buf.stride(0), *t[0].stride()))
+        else:                                         # windows: sequence n starts at token n of the first
+            row = t[0, 0].numel()
+            buf = torch.cat((t[0].reshape(T, row), t[:N, -1].reshape(N, row)))
+            return buf.as_strided(t.shape, (row, *t[0].stride()))
+        v.copy_(t)
+        return v
+
+    xo = lay(x, "time first" if order == "mixed" else order)
+    go = lay(g, "padded sequences" if order == "mixed" else order)
+    h, last = ttm.glr_fwd(xo, go, h0=h0)
+    xc, gc = xo.contiguous(), go.contiguous()
+    rh, th, rl, tl = reference(xc.cpu(), gc.cpu(), h0.cpu())
+    close(h, rh, th, x.dtype)
+    close(last, rl, tl, torch.float32)
+    out, same = ttm.glr_bwd(go, h, xo, h0=h0), ttm.glr_bwd(gc, h, xc, h0=h0)
+    assert torch.equal(ttm.glr_fwd(xc, gc, h0=h0)[0], h)
+    dx, tx, dg, tg, c, tc = grad_reference(gc.cpu(), h.cpu(), h0.cpu(), xc.cpu(), None)
+    close(out["dx"], dx, tx, x.dtype)
+    close(out["dg"], dg, tg, g.dtype)
+    close(out["dh0"], c, tc, torch.float32)
+    assert all(torch.equal(out[k], same[k]) for k in out)
+    if T < 50:
+        state = h0.clone()
+        assert torch.equal(ttm.glr_step(xo, go, state), ttm.glr_step(xc, gc, h0.clone()))
