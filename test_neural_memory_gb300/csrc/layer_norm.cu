@@ -435,7 +435,8 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) ln_bwd_kernel(const __grid_c
     }
 }
 
-// Rows longer than the registers: one block per row, values read again from the cache.
+// Rows longer than the registers: one block per row, values read again from the cache.  Columns count in
+// 64 bits: 2 D passes 31 of them, and the last stride past D 32.
 template <typename E>
 __device__ __forceinline__ float block_sum(float s, float* buf) {
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -453,15 +454,15 @@ __global__ void __launch_bounds__(kLongThreads) ln_fwd_long_kernel(LayerNormArgs
     for (long long r = blockIdx.x; r < a.N; r += gridDim.x) {
         const E* x = static_cast<const E*>(a.x) + r * a.x_row;
         float s = 0.f;
-        for (int d = threadIdx.x; d < a.D; d += kLongThreads) s += to_f(x[d]);
+        for (long long d = threadIdx.x; d < a.D; d += kLongThreads) s += to_f(x[d]);
         const float mean = block_sum<E>(s, buf) / a.D;
         s = 0.f;
-        for (int d = threadIdx.x; d < a.D; d += kLongThreads) {
+        for (long long d = threadIdx.x; d < a.D; d += kLongThreads) {
             const float c = to_f(x[d]) - mean;
             s = fmaf(c, c, s);
         }
         const float rstd = 1.f / sqrtf(block_sum<E>(s, buf) / a.D + a.eps);
-        for (int d = threadIdx.x; d < a.D; d += kLongThreads)
+        for (long long d = threadIdx.x; d < a.D; d += kLongThreads)
             put(static_cast<E*>(a.y)[r * a.D + d],
                 fmaf((to_f(x[d]) - mean) * rstd, a.w ? a.w[d] : 1.f, a.b ? a.b[d] : 0.f));
         if (threadIdx.x == 0) {
@@ -476,14 +477,14 @@ __global__ void __launch_bounds__(kLongThreads) ln_bwd_long_kernel(LayerNormArgs
     __shared__ float buf[kLongThreads / 32];
     float* part = a.partial ? a.partial + (size_t)blockIdx.x * 2 * a.D : nullptr;
     if (part)
-        for (int d = threadIdx.x; d < 2 * a.D; d += kLongThreads) part[d] = 0.f;
+        for (long long d = threadIdx.x; d < 2ll * a.D; d += kLongThreads) part[d] = 0.f;
     __syncthreads();
     for (long long r = blockIdx.x; r < a.N; r += gridDim.x) {
         const E* x = static_cast<const E*>(a.x) + r * a.x_row;
         const E* dy = static_cast<const E*>(a.dy) + r * a.dy_row;
         const float mean = a.mean[r], rstd = a.rstd[r];
         float su = 0.f, sn = 0.f;
-        for (int d = threadIdx.x; d < a.D; d += kLongThreads) {
+        for (long long d = threadIdx.x; d < a.D; d += kLongThreads) {
             const float g = to_f(dy[d]), n = (to_f(x[d]) - mean) * rstd;
             const float u = g * (a.w ? a.w[d] : 1.f);
             su += u;
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kLongThreads) ln_bwd_long_kernel(LayerNormArgs
         }
         su = block_sum<E>(su, buf) / a.D;
         sn = block_sum<E>(sn, buf) / a.D;
-        for (int d = threadIdx.x; d < a.D; d += kLongThreads) {
+        for (long long d = threadIdx.x; d < a.D; d += kLongThreads) {
             const float n = (to_f(x[d]) - mean) * rstd;
             put(static_cast<E*>(a.dx)[r * a.D + d],
                 rstd * (fmaf(to_f(dy[d]), a.w ? a.w[d] : 1.f, -su) - n * sn));
@@ -507,13 +508,13 @@ __global__ void __launch_bounds__(kLongThreads) ln_bwd_long_kernel(LayerNormArgs
 __global__ void __launch_bounds__(512) ln_join_kernel(const float* part, int blocks, int D,
                                                       float* dw, float* db) {
     __shared__ float buf[16][33];
-    const int c = blockIdx.x * 32 + threadIdx.x;
+    const long long c = blockIdx.x * 32ll + threadIdx.x;
     float s = 0.f;
-    if (c < 2 * D)
-        for (int p = threadIdx.y; p < blocks; p += 16) s += part[(size_t)p * 2 * D + c];
+    if (c < 2ll * D)
+        for (int p = threadIdx.y; p < blocks; p += 16) s += part[p * 2ll * D + c];
     buf[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y || c >= 2 * D) return;
+    if (threadIdx.y || c >= 2ll * D) return;
     s = 0.f;
 #pragma unroll
     for (int y = 0; y < 16; ++y) s += buf[y][threadIdx.x];
@@ -665,7 +666,7 @@ cudaError_t layer_norm_bwd_launch(const LayerNormArgs& in, cudaStream_t s, int* 
     const cudaError_t e =
         a.bf16 ? by_width<__nv_bfloat16>(a, true, blocks, s) : by_width<float>(a, true, blocks, s);
     if (e != cudaSuccess || !a.partial) return e;
-    ln_join_kernel<<<(2 * a.D + 31) / 32, dim3(32, 16), 0, s>>>(a.partial, blocks, a.D, a.dw, a.db);
+    ln_join_kernel<<<(unsigned)((2ll * a.D + 31) / 32), dim3(32, 16), 0, s>>>(a.partial, blocks, a.D, a.dw, a.db);
     *launches = 2;
     return cudaGetLastError();
 }

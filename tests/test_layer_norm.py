@@ -241,3 +241,18 @@ def test_constant_rows_have_their_value_as_mean(D, dtype):
     y, mean, rstd = ttm.layer_norm_fwd(x, None, b)
     assert torch.equal(mean.cpu(), value)
     assert torch.equal(y, b.to(DT[dtype]).expand(50, D))
+
+
+def test_a_row_of_2_to_the_30():
+    """One row whose two sums take 2^31 words: the last columns count, and those of dw and db beyond 2^31."""
+    D = 2 ** 30 + 3
+    x = torch.ones(1, D, dtype=torch.bfloat16, device="cuda")
+    x[:, 1::2] = -1                                   # n = x for mean 0 and rstd 1; sum x = 1
+    y, mean, rstd = ttm.layer_norm_fwd(x)
+    # a thread's 2^21 values have one sign, so its sums are exact; the mean is 1 / D, rstd off by 1e-5 / 2
+    assert abs(float(mean)) < 2.0 ** -20 and abs(float(rstd) - 1) < 1e-5
+    assert torch.equal(y, x)
+    del y
+    out = ttm.layer_norm_bwd(x, x, torch.zeros(1, device="cuda"), torch.ones(1, device="cuda"))
+    assert bool((out["dw"] == 1).all()) and torch.equal(out["db"], x[0].float())
+    assert float(out["dx"].abs().max()) < 2.0 ** -20   # x - 1 / D - x (1 - 3 2^-30), sums to 2^-24
