@@ -463,8 +463,8 @@ int ttm_lmm_layer_fwd(int B, int T, int H, int d, int chunk, int conv_k,
  *     them.
  *   workspace: ttm_glr_workspace_size(..., 0) bytes of device scratch (NULL when
  *     that is 0); its contents on entry are ignored.
- * Shapes: N, D >= 1, T >= 0, N D < 2^31 (else TTM_ERR_UNSUPPORTED); T = 0 gives
- * h_last = h0.  No output may overlap an input, another output or the workspace.
+ * Shapes: N, D >= 1, T >= 0, N D < 2^31, T < 2^31 - 8192 (else TTM_ERR_UNSUPPORTED);
+ * T = 0 gives h_last = h0.  No output may overlap an input, another output or the workspace.
  * Long sequences are split over blocks that hand the state on with bounded waits:
  * ttm_device_status reports TTM_ERR_TIMEOUT, and the outputs are invalid, if one
  * ran out.  Equal inputs give equal bits.  Asynchronous on `stream`;

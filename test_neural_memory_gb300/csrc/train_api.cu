@@ -57,6 +57,9 @@ size_t view_bytes(long long N, long long T, long long D, long long seq, long lon
     return ok ? (size_t)((N - 1) * seq + (T - 1) * tok + D) * es : 0;
 }
 
+// A tile, 4096 tokens at most, may start at any token and is counted in 31 bits.
+constexpr int kMostTokens = 0x7fffffff - 8192;
+
 // What the three recurrence calls share.  `x` is the strided input (the forward's x or
 // the gradient's dh).
 int glr_common(ttm::GlrArgs& a, int N, int T, int D, int dtype, int gate, const void* x,
@@ -71,7 +74,7 @@ int glr_common(ttm::GlrArgs& a, int N, int T, int D, int dtype, int gate, const 
     sx = {x, view_bytes(N, T, D, x_seq, x_tok, es, ok)};
     sg = {g, view_bytes(N, T, gate == TTM_GATE_TOKEN ? 1 : D, g_seq, g_tok, gs, ok)};
     if (!ok) return TTM_ERR_INVALID_ARG;
-    if ((long long)N * D > (1LL << 31) - 1) return TTM_ERR_UNSUPPORTED;
+    if ((long long)N * D > (1LL << 31) - 1 || T > kMostTokens) return TTM_ERR_UNSUPPORTED;
     a.N = N; a.T = T; a.D = D;
     a.bf16 = dtype == TTM_BF16;
     a.gate_token = gate == TTM_GATE_TOKEN;
@@ -106,7 +109,7 @@ size_t ttm_glr_workspace_size(int N, int T, int D, int dtype, int gate, int back
     Span sx, sg;
     if (N < 1 || T < 0 || D < 1 || !dtype_ok(dtype) ||
         (gate != TTM_GATE_CHANNEL && gate != TTM_GATE_TOKEN) ||
-        (long long)N * D > (1LL << 31) - 1)
+        (long long)N * D > (1LL << 31) - 1 || T > kMostTokens)
         return 0;
     a.N = N; a.T = T; a.D = D;
     a.bf16 = dtype == TTM_BF16;

@@ -92,3 +92,14 @@ def test_orthogonalize_rejects_malformed(L):
     need = L.ttm_orthogonalize_workspace_size(1, 300, 400)
     assert need > 0 and call(m=300, n=400, wsb=need - 1) == INVALID
     assert L.ttm_orthogonalize_workspace_size(1, 0, 4) == 0
+
+
+@host_only
+def test_recurrence_refuses_lengths_its_tiles_cannot_count(L):
+    for T in (2 ** 31 - 1, 2 ** 31 - 8192):
+        assert glr(L, N=1, T=T, D=1, xt=1, gt=1) == UNSUPPORTED
+        assert L.ttm_glr_workspace_size(1, T, 1, 0, 0, 0) == 0
+        assert L.ttm_glr_step(1, T, 1, 0, 0, P(0), 0, 1, P(1), 0, 1, P(2), P(3), None) == UNSUPPORTED
+        assert L.ttm_glr_bwd(1, T, 1, 0, 0, P(0), 0, 1, P(1), None, P(2), 0, 1, None, P(3), P(4), None,
+                             P(5), 1 << 18, None) == UNSUPPORTED
+    assert L.ttm_glr_workspace_size(1, 2 ** 31 - 8193, 1, 0, 0, 0) > 0
