@@ -106,10 +106,11 @@ def orthogonalize(G, *, coeffs=NS_COEFFS, eps=1e-7, out=None, workspace=None, st
     """Orthogonalised update of the matrices G ([..., m, n], fp32 or bf16, contiguous): one
     Newton-Schulz step X <- a X + (b A + c A^2) X, A = X X^T, per (a, b, c) of `coeffs`, from
     G / max(|G|_F, eps).  Returns bf16 [..., m, n]."""
-    flat = [v for step in coeffs for v in step]
-    if len(flat) != 3 * len(coeffs):
-        raise TTMError(ERR_INVALID_ARG, "orthogonalize: coeffs is a sequence of (a, b, c)")
-    return _call("orthogonalize", stream, G, struct.pack(f"{len(flat)}f", *flat), eps, out, workspace)
+    try:
+        packed = b"".join(struct.pack("=3f", *step) for step in coeffs)
+    except (TypeError, OverflowError, struct.error):
+        raise TTMError(ERR_INVALID_ARG, "orthogonalize: coeffs is a sequence of (a, b, c) in fp32's range") from None
+    return _call("orthogonalize", stream, G, packed, eps, out, workspace)
 
 
 def _nothing(_key):

@@ -103,3 +103,11 @@ def test_recurrence_refuses_lengths_its_tiles_cannot_count(L):
         assert L.ttm_glr_bwd(1, T, 1, 0, 0, P(0), 0, 1, P(1), None, P(2), 0, 1, None, P(3), P(4), None,
                              P(5), 1 << 18, None) == UNSUPPORTED
     assert L.ttm_glr_workspace_size(1, 2 ** 31 - 8193, 1, 0, 0, 0) > 0
+
+
+@pytest.mark.parametrize("coeffs", [[(1.0, 2.0), (3.0, 4.0, 5.0, 6.0)], [1.0, 2.0, 3.0], [(1.0, 2.0, "3")], 7.0,
+                                    [(1.0, 2.0, 1e300)]])
+def test_coefficients_come_in_threes(coeffs):
+    with pytest.raises(ttm.TTMError, match="coeffs") as e:
+        ttm.orthogonalize(None, coeffs=coeffs)
+    assert e.value.code == INVALID
