@@ -452,8 +452,9 @@ int ttm_lmm_layer_fwd(int B, int T, int H, int d, int chunk, int conv_k,
  *     state rounded; the recurrence itself runs in fp32).
  *   g: the logarithm of the retention.  gate TTM_GATE_CHANNEL: [N][T][D] in
  *     dtype; TTM_GATE_TOKEN: [N][T] fp32, one value for all channels.  0 keeps
- *     the state, -infinity forgets it (a document boundary); values above 0
- *     grow it and are taken as given.
+ *     the state, -infinity forgets it (a document boundary; a state that is not
+ *     finite stays, as 0 times it is NaN); values above 0 grow it and are taken
+ *     as given.
  *   h0: [N][D] fp32 or NULL (zero).  h_last: [N][D] fp32, written.
  *   x_seq, x_tok (g_seq, g_tok): elements between sequences and between tokens,
  *     at least D (1 for a token gate) where there is more than one, so that x
@@ -548,7 +549,8 @@ int ttm_layer_norm_bwd(int N, int D, int dtype, const void* dy, long long dy_row
  *   G: [batch][m][n] in dtype, contiguous.  out: [batch][m][n] bf16, written.
  *   coeffs: HOST array of steps x (a, b, c), finite; read during the call.
  *   workspace: ttm_orthogonalize_workspace_size() bytes of device scratch.
- * |G|_F is summed in fp32 (it must stay below 1e19).  A zero matrix gives zero.
+ * |G|_F is summed in fp32: it has to stay below 1e19 and counts as 0 below 1e-22; an eps below
+ * 1e-30 counts as that.  A zero matrix gives zero.
  * The products take fp16 operands and add in fp32, X itself is kept to about fp32's
  * accuracy: with the usual coefficients the result is 1.7e-3 to 2.1e-3 of its norm off
  * (bf16 rounding alone: 1.7e-3), whatever the rank; up to 2.5e-3 for a short side

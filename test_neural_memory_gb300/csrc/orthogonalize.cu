@@ -64,10 +64,11 @@ __device__ __forceinline__ uint32_t bf162_bits(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 1 / max(norm, eps); NaN stays NaN.
+// 1 / max(norm, eps); NaN stays NaN.  A sum of squares is 0 or above 1e-45, so a norm 0 or above 1e-23;
+// below 1e-30 eps counts as that, or 1 / eps times 2^10 were infinite and a zero matrix NaN.
 __device__ __forceinline__ float inverse_norm(float sum_of_squares, float eps) {
     const float norm = sqrtf(sum_of_squares);
-    return norm <= eps ? 1.f / eps : 1.f / norm;
+    return norm <= eps ? 1.f / fmaxf(eps, 1e-30f) : 1.f / norm;
 }
 
 __device__ __forceinline__ float4 load4(const OrthoArgs& a, size_t i) {

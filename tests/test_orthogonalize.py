@@ -295,3 +295,13 @@ def test_coefficients_of_any_size(m, n, coeffs, kind):
     ref, rough = steps_in_11_bits(G, coeffs)
     err, moved, size = ((t - ref).flatten(1).norm(dim=1) for t in (O, rough, 0 * ref))
     assert bool((err <= 2 * moved + (2.0 ** -9 + 2e-4) * size).all()), (err / size, moved / size)
+
+
+@pytest.mark.parametrize("m,n", [(64, 64), (40, 700), (100, 900), (300, 200)])
+@pytest.mark.parametrize("eps", [1e-20, 1e-30, 1e-38])
+def test_zero_with_a_tiny_eps(m, n, eps):
+    G = torch.zeros(2, m, n)
+    G[1] = matrices(1, m, n, "normal")[0]
+    O = ttm.orthogonalize(G.cuda(), eps=eps)
+    assert not O[0].any()
+    assert torch.equal(O[1], ttm.orthogonalize(G.cuda())[1])
