@@ -553,8 +553,8 @@ int ttm_layer_norm_bwd(int N, int D, int dtype, const void* dy, long long dy_row
  * 1e-30 counts as that.  A zero matrix gives zero.
  * The products take fp16 operands and add in fp32, X itself is kept to about fp32's
  * accuracy: with the usual coefficients the result is 1.7e-3 to 2.1e-3 of its norm off
- * (bf16 rounding alone: 1.7e-3), whatever the rank; up to 2.5e-3 for a short side
- * below 64.  The operands' scales follow from the coefficients, which may be of any size as
+ * (bf16 rounding alone: 1.7e-3) at any rank; up to 3e-3 for a short side below 64, or of up
+ * to 128 with a long side beyond 128 for a matrix next to rank one.  The operands' scales follow from the coefficients, which may be of any size as
  * long as the polynomials stay within fp32's range.  Device waits are bounded: see
  * ttm_device_status.
  * Shapes: batch, m, n >= 1, 0 <= steps <= 32, eps > 0; batch <= 65535 and

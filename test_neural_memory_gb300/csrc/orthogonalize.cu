@@ -598,7 +598,9 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
 // twice a step.  What that costs is accuracy: a rounding of A_0 is not put right by the next step's
 // A.  Every operand here is therefore a sum hi + lo of two fp16 values, and a product takes hi hi +
 // hi lo + lo hi: 1e-4 off for a matrix of low rank plus noise, 1e-5 for a normal one, before
-// the result is rounded to bf16 (1.66e-3).  Roundings grow as small singular values do, so coefficients that grow these by
+// the result is rounded to bf16 (1.66e-3).  Next to rank one that is 6e-4 (short side 50) to 2e-3 (128),
+// 1.8e-3 to 2.6e-3 in all: the tensor cores cut their sums off at 24 bits, and Q's large part, 485 times
+// what has no direction of X in it, cancels.  Roundings grow as small singular values do, so coefficients that grow these by
 // more than 1024 in all take the other path (tame).
 //
 //   ns_gram_kernel:  A_0 by parts of the long side, 128 of it at a time (fp32 sums)
@@ -927,9 +929,11 @@ __global__ void __launch_bounds__(kGramThreads<RP>, RP == 64 ? 2 : 1)
     if (mine) put_A();
     uint32_t phase = 0;
     const int steps = (r + 15) / 16;
+    // x y.  All are symmetric but for their roundings; with y's transpose in its place those of one step came
+    // back on the side where the next one multiplies them by up to 3.4 (rank 1 at 128 x 2000: 3.4e-3 off).
     auto product = [&](uint32_t column, const unsigned char* x, const unsigned char* y) {
         const uint32_t u = smem_u32(x), v = smem_u32(y);
-        mma_split(tmem_addr(tmem, 0, column), Operand{u, u + ob, half, false}, Operand{v, v + ob, half, false}, RP,
+        mma_split(tmem_addr(tmem, 0, column), Operand{u, u + ob, half, false}, Operand{v, v + ob, half, true}, RP,
                   steps, false);
     };
     auto announce = [&](int product) {                  // or not, for a test of the waits
