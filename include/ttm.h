@@ -612,7 +612,7 @@ unsigned long long ttm_launch_count(void);
  *     ttm_orthogonalize call takes it too: its kernel that keeps a matrix on
  *     chip and the one that takes the steps on A alone leave their product c
  *     (three a step) unannounced, the first product from global memory
- *     announces 16 bytes more for its copy c.  So does ttm_glr_fwd /
+ *     leaves stage c of its copies (modulo their number) unfilled.  So does ttm_glr_fwd /
  *     ttm_glr_bwd, with 16 bytes more for its tile c.  The setting
  *     is used up by that one call; -1 clears it.  Nothing faults, traps or
  *     hangs.

@@ -1184,7 +1184,7 @@ struct GemmParams {
     __nv_bfloat16* last;            // kUpdate, last step: the result instead, [batch][M][N]
     int* status;
     long long limit;
-    int debug_stall;                // block of K (of a thread block) + 1 that never arrives; 0: none
+    int debug_stall;                // stage (modulo their number) + 1 that never fills; 0: none
 };
 
 struct GemmShared {
@@ -1257,7 +1257,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const bool by_tile = p.tiles > stride && p.K <= 8 * kBK;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&S.full[i], 1);
+            // (in a test of the waits one stage expects an arrival that does not come; a condition in the
+            // loader's loop took 1 % of the projection)
+            mbar_init(&S.full[i], p.debug_stall && (p.debug_stall - 1) % kStages == i ? 2 : 1);
             mbar_init(&S.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -1289,8 +1291,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 ok = wait_one(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort, p.status, p.limit);
                 if (!ok) break;
                 unsigned char *da = base + s * kStage, *db = da + kBM * 128;
-                // (a test of the waits has more announced than comes)
-                if (rank == 0) mbar_expect_tx(&S.full[s], CG * stage + (it + 1 == p.debug_stall ? 16u : 0u));
+                if (rank == 0) mbar_expect_tx(&S.full[s], CG * stage);
                 const uint32_t bar = CG == 2 ? peer_addr(&S.full[s], 0) : 0;
                 auto load = [&](unsigned char* dst, const CUtensorMap* m, int x, int y) {
                     if (CG == 2) tma_load_3d_pair(dst, m, bar, x, y, at.mat);
