@@ -19,9 +19,12 @@
 // side over a strip of channels and 256 / CW over the tokens (make_plan chooses CW).
 // The runs of a warp are joined by shuffles, the eight warps' through shared memory.
 //
-// Measured, bf16, a gate per channel: forward 16 x 131072 x 128 256 us (6.3 TB/s, 93 % of what a copy
-// reaches), 256 x 8192 x 128 241 us (6.7 TB/s); gradient 96 x 8192 x 64 83 us (6.1 TB/s); one tile,
-// 2 x 777 x 768, 6.0 us.
+// Measured, a gate per channel: bf16 forward 16 x 131072 x 128 258 us (6.3 TB/s, 92 % of what a copy
+// reaches), 256 x 8192 x 128 238 us (6.8 TB/s); gradient 96 x 8192 x 64 83 us (6.1 TB/s); one tile,
+// 2 x 777 x 768, 6.3 us; fp32 forward 16 x 65536 x 128 242 us (6.7 TB/s), gradient 96 x 8192 x 64 150 us (6.7
+// TB/s).  A gate per token: forward 16 x 131072 x 128 bf16 238 us and 16 x 65536 x 128 fp32 206 us (4.6 and
+// 5.2 TB/s: a token's arithmetic is the same for a third less of traffic), gradient 96 x 8192 x 64 bf16 83,
+// fp32 108 us (3.7 and 5.7 TB/s: each token's sum over the channels besides).
 //
 // Between tiles (look-back), a lane per channel: a warp publishes its channels' map of
 // the tile as soon as it has it, finds the nearest tile before whose end state is known,
@@ -914,9 +917,10 @@ TilePlan make_plan(const GlrArgs& a, int backward, size_t* bytes) {
     // Strips of 64 channels (or D).  With few of them the blocks at work on one are many, and each
     // waits longer for the state before its tile, so they are halved, and their tiles twice as
     // long, down to rows of 64 bytes, until there are 128 of them (128 channels, bf16: 1 x 131072
-    // tokens 155 us with one strip of 128 channels, 86 with two, 54 with four; 64 x 32768 tokens
+    // tokens 155 us with one strip of 128 channels, 86 with two, 54 with four when they were
+    // compared, 39 with four now; 64 x 32768 tokens
     // 245 us with two strips a row, 258 with four).  Down to rows of 32 bytes where all of a
-    // sequence then is one tile and nobody waits (2 x 777 x 768: 6.0 us against 7.7).
+    // sequence then is one tile and nobody waits (2 x 777 x 768: 6.3 us against 7.7).
     auto strips_at = [&](int log) { return (long long)a.N * ((a.D + (V << log) - 1) / (V << log)); };
     auto tokens_at = [&](int log) { return (kThreads >> log) * run; };
     while (p.cw_log < kMaxLog && (V << p.cw_log) < a.D) ++p.cw_log;

@@ -19,15 +19,16 @@
 // in flight and one reduction serves several rows.  TPR is the rows' packs up to a warp
 // (shuffles), or the whole block of 256 (shuffles, then shared memory) for long rows; a warp
 // takes rows of up to 1024 single values, in which a block of 256 would mostly wait at barriers
-// (697568 x 169 bf16, gradient: 679 us with a row a block, 236 with a row a warp) once there are many.  Rows longer
+// (697568 x 169 bf16, gradient: 679 us with a row a block, 250 with a row a warp) once there are many.  Rows longer
 // than the registers hold are read again from the cache instead.  W is the widest pack that the
 // rows' alignment and D allow; rows of x and dy that do not start on 16 bytes are read in 16-byte
 // words all the same and shifted into place (238817 x 768 bf16 from rows of 771, forward: 318 us
 // value by value, 137 so).
 //
-// Measured, bf16, forward and gradient: 131072 x 2048 199 and 264 us (5.4 and 6.1 TB/s of 6.8 that a
-// copy reaches), 786432 x 64 40 and 50 us, 100000 x 512 41 and 54 us, 8000 x 8192 60 and 105 us (its
-// sums of dw and db take the registers of one of the two blocks an SM).
+// Measured, forward and gradient: bf16 131072 x 2048 200 and 285 us (5.4 and 5.6 TB/s of 6.8 that a
+// copy reaches), 786432 x 64 39 and 61 us, 100000 x 512 40 and 62 us, 8000 x 8192 60 and 112 us (its
+// sums of dw and db take the registers of one of the two blocks an SM); fp32 65536 x 2048 151 and 243 us,
+// 100000 x 512 65 and 102 us.  The figures further down compare variants with x as dy, one read less.
 //
 // The gradient's blocks leave their dw, db sums in the workspace and a second kernel adds
 // them in a fixed order: no atomics, so equal inputs give equal bits.

@@ -8,7 +8,7 @@
 // rounding with them (1 % off for a normal matrix, 6 % for one of low rank plus noise).  With
 // fp16 operands, X itself kept to fp32's accuracy (in registers, or as the sum of two fp16
 // values, hi + lo, in every step) and the diagonal of B, its largest entries once X is near
-// orthogonal, in fp32 beside the product, the result is 1.7e-3 to 2.1e-3 off (2.4e-3 at 16 x 24), of
+// orthogonal, in fp32 beside the product, the result is 1.7e-3 to 2.1e-3 off (2.8e-3 at 16 x 24), of
 // which rounding it to bf16 is 1.7e-3; with B's diagonal in fp16 it would be up to
 // 2.6e-3.  lo is kept to the end because a matrix of few directions has nothing that puts a
 // rounding of X right: with lo dropped from the last three of five states one of rank 1
@@ -22,8 +22,8 @@
 // infinities for an entry of bA + cA^2 beyond 64.
 //
 // Three ways, by size.  128 x 128 at most, or 64 x 1024: one block, or a cluster, keeps a matrix on chip through all
-// steps (ns_small_kernel: 192 x 128 x 128 in 26 us on the device).  A longer long side: the steps run on A alone, and
-// G is read three times in all (ns_gram_kernel and those after it: 158 x 39 x 3516 in 137 us, 630 as products of every
+// steps (ns_small_kernel: 192 x 128 x 128 in 28 us on the device).  A longer long side: the steps run on A alone, and
+// G is read three times in all (ns_gram_kernel and those after it: 158 x 39 x 3516 in 131 us, 630 as products of every
 // step).  A longer short side: three products a step (ns_gemm_kernel).  A and
 // B = b A + c A^2 are symmetric, so only their tiles on and below the diagonal are
 // computed and each is written twice, once transposed.
@@ -163,7 +163,7 @@ __device__ __forceinline__ void peer_store2(uint32_t addr, uint32_t a, uint32_t 
 // columns each.
 // A is then a sum over the blocks: each leaves its share in shared memory (fp32), adds a
 // range of rows over all blocks in their order and hands the result to all of them;
-// everything else stays a block's own.  (2 x 709 x 37: 28 us, 88 as products from global
+// everything else stays a block's own.  (2 x 709 x 37: 27 us, 88 as products from global
 // memory.)
 constexpr int kSide = 128, kSmallThreads = 256, kMaxCluster = 8;
 constexpr uint32_t kHalfBytes = kSide * 128;            // 64 columns of an operand
@@ -1137,8 +1137,8 @@ __device__ __forceinline__ void free_columns(uint32_t t, uint32_t n) {
 // That halves what a block reads of B, and the copies are what bounds a tile: they reach about 50
 // bytes a cycle and SM, so that a block of K takes 490 cycles for the 24 KB of a tile of 256 x 128 and
 // 650 for the 32 KB of 256 x 256, whose products take 256 and 512.  At 2048 x 8240 A takes 36 us
-// (129 blocks of K in one round of tiles), B 16 and the update 52, 58 with lo (37 without its
-// epilogue, whose 100 MB pass through the same L2): 530 us for five steps with norm and start, 1.06
+// (129 blocks of K in one round of tiles), B 16 and the update 58 (37 without its
+// epilogue, whose 134 MB pass through the same L2): 550 us for five steps with norm and start, 1.02
 // PFLOP/s with the symmetric products counted half.
 //   kGram:   out = alpha acc                (A; on and below the diagonal, mirrored; or, with few
 //            tiles and a long K, fp32 sums over parts of K, which ns_join_kernel adds)
@@ -1752,7 +1752,7 @@ GramPlan gram_plan(int batch, int m, int n, size_t* bytes) {
 }
 
 // Whether a call stays on chip: one block a matrix, or, with a short side of up to 64, a cluster of
-// blocks of 128 of the long side, up to two blocks for each SM (2 x 709 x 37: 28 us so, 40 by its
+// blocks of 128 of the long side, up to two blocks for each SM (2 x 709 x 37: 27 us so, 40 by its
 // A alone; 1 x 64 x 256: 25 and 32; but 20 x 128 x 1024: 79 and 65).
 bool small(int batch, int m, int n) {
     const int r = m < n ? m : n, ranks = ((m < n ? n : m) + kSide - 1) / kSide;
