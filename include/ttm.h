@@ -568,6 +568,133 @@ int ttm_orthogonalize(int batch, int m, int n, int dtype, const void* G,
                       const float* coeffs, int steps, float eps, void* out,
                       void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Short causal convolution, depthwise, per sequence and channel, with an optional SiLU:
+ *     pre_t = b + sum_{i < K} w[i] x_{t-K+1+i},   y_t = pre_t,  or pre_t / (1 + exp(-pre_t))
+ * (the convolution after the q, k and v projections of "论文速览 | Titans" §7.3 with the SiLU of §7.1,
+ * as an operator of its own: ttm_lmm_layer_fwd has it fused with what follows).
+ *   x: [N][T][C] in dtype, channels contiguous, x_seq and x_tok elements between sequences and tokens (at
+ *     least C where there is more than one).  w: [C][K] fp32, w[c][K-1] the current token's.  b: [C] fp32 or
+ *     NULL (0).  silu: 0 or 1.
+ *   state0: [N][K-1][C] in dtype, the K - 1 inputs before the first token, or NULL (zero).
+ *   doc: [N][T] int32, doc_seq apart, or NULL: a tap whose row has another number than the token is left
+ *     out.  The rows of state0 have the number of the first token.
+ *   y: [N][T][C] in dtype, contiguous.  state: [N][K-1][C] in dtype or NULL: the last K - 1 inputs
+ *     (state0's rows among them where T < K - 1), zero where they are of another document than the last
+ *     token; state0 of the call that continues the sequences.
+ * Sums are fp32.  x, w, b and doc need the alignment of their type only, every other pointer 16 bytes.
+ * Shapes: N, C >= 1, T >= 0, 1 <= K <= 8 (TTM_CONV_MAX_TAPS), T < 2^31 - 8192, N C < 2^31 (else
+ * TTM_ERR_UNSUPPORTED); T = 0 gives state = state0.  No output may overlap an input or another output.
+ * Asynchronous on `stream`; TTM_ERR_INVALID_ARG for malformed arguments, TTM_ERR_CUDA if a launch fails.
+ */
+#define TTM_CONV_MAX_TAPS 8
+int ttm_causal_conv_fwd(int N, int T, int C, int K, int dtype, int silu,
+                        const void* x, long long x_seq, long long x_tok,
+                        const float* w, const float* b, const void* state0,
+                        const int* doc, long long doc_seq,
+                        void* y, void* state, void* stream);
+
+/* Gradient of ttm_causal_conv_fwd for the adjoints dy of y ([N][T][C] in dtype, strides as x) and dstate of
+ * state ([N][K-1][C] in dtype or NULL, zero): with d_t = dy_t act'(pre_t), the taps left out as above,
+ *     dx_s = sum_i w[i] d_{s+K-1-i}  (+ dstate),  dw[i] = sum d_t x_{t-K+1+i},  db = sum d_t
+ * (dw and db over sequences and tokens).
+ *   dx: [N][T][C] in dtype.  dw: [C][K] fp32, db: [C] fp32, dstate0: [N][K-1][C] in dtype, each or NULL.
+ *   workspace: ttm_causal_conv_bwd_workspace_size(C, K) bytes of device scratch (may be NULL when dw and
+ *     db are).
+ * The sums run in a fixed order (equal inputs give equal bits).  Otherwise as ttm_causal_conv_fwd. */
+size_t ttm_causal_conv_bwd_workspace_size(int C, int K);
+int ttm_causal_conv_bwd(int N, int T, int C, int K, int dtype, int silu,
+                        const void* dy, long long dy_seq, long long dy_tok,
+                        const void* x, long long x_seq, long long x_tok,
+                        const float* w, const float* b, const void* state0,
+                        const int* doc, long long doc_seq, const void* dstate,
+                        void* dx, float* dw, float* db, void* dstate0,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Decode step of the convolution: continues every sequence by n >= 1 tokens from `state` ([N][K-1][C] in
+ * dtype, updated in place).  Otherwise as ttm_causal_conv_fwd, without documents. */
+int ttm_causal_conv_step(int N, int n, int C, int K, int dtype, int silu,
+                         const void* x, long long x_seq, long long x_tok,
+                         const float* w, const float* b, void* state, void* y, void* stream);
+
+/*
+ * Gated feed-forward block on N rows:
+ *     g | u = x W_in,   h = act(g) u,   y = h W_out (+ residual)
+ * (the position-wise half of a residual block, beside the memory layer of "论文速览 | Titans" §6.4).
+ *   x: N rows of D, x_row elements apart.  W_in: [D][2F], the gate's F columns first.  W_out: [F][D].
+ *   residual: N rows of D, residual_row apart, or NULL.  y: [N][D].  gu: [N][2F] or NULL: g and u, which the
+ *     gradient takes.  act: TTM_ACT_SILU, g / (1 + exp(-g)), or TTM_ACT_GELU, g Phi(g) (erf).
+ *   workspace: ttm_gated_ffn_workspace_size(N, D, F, 0) bytes of device scratch (h among it).
+ * All tensors are bf16; products add in fp32, g and u enter the activation in fp32, h is rounded to bf16 for
+ * its product (half a step, 2^-9 of its norm, as the result's own rounding is).
+ * Shapes: N >= 0, D and F >= 8 and multiples of 8 (tensor copies take 16 bytes), as x_row and residual_row
+ * are; D, 2F < 2^24, N < 2^31 - 8192 (else TTM_ERR_UNSUPPORTED).  Every pointer is 16-byte aligned.  No output may overlap an
+ * input, another output or the workspace.  Equal inputs give equal bits.  Device waits are bounded: see
+ * ttm_device_status.  Asynchronous on `stream`; TTM_ERR_INVALID_ARG for malformed arguments, TTM_ERR_CUDA
+ * if a launch fails.
+ */
+typedef enum { TTM_ACT_SILU = 0, TTM_ACT_GELU = 1 } ttm_act;
+size_t ttm_gated_ffn_workspace_size(int N, int D, int F, int backward);
+int ttm_gated_ffn_fwd(int N, int D, int F, int act, const void* x, long long x_row,
+                      const void* W_in, const void* W_out,
+                      const void* residual, long long residual_row,
+                      void* y, void* gu, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of ttm_gated_ffn_fwd for the adjoint dy of y (N rows, dy_row elements apart; the residual's
+ * adjoint is dy itself):
+ *     dh = dy W_out^T,  dg = dh u act'(g),  du = dh act(g),
+ *     dx = [dg | du] W_in^T,  dW_in = x^T [dg | du],  dW_out = h^T dy
+ *   gu: what the forward call wrote (h is taken from it again).  dx: [N][D], dW_in: [D][2F], dW_out: [F][D],
+ *   each or NULL; all bf16, written (the weights' are zero for N = 0).
+ *   workspace: ttm_gated_ffn_workspace_size(N, D, F, 1) bytes ([dg | du] and h, rounded to bf16).
+ * Otherwise as ttm_gated_ffn_fwd; dy_row a multiple of 8. */
+int ttm_gated_ffn_bwd(int N, int D, int F, int act, const void* dy, long long dy_row,
+                      const void* x, long long x_row, const void* gu,
+                      const void* W_in, const void* W_out,
+                      void* dx, void* dW_in, void* dW_out,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * AdamW step over `count` tensors, the update of the outer loop for what ttm_orthogonalize does not take:
+ * with s = grad_scale, t the number of this step (from 1),
+ *     m <- b1 m + (1 - b1) s g,   v <- b2 v + (1 - b2) (s g)^2,
+ *     p <- p (1 - lr weight_decay) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+ *   tensors: HOST array, read during the call: param (in param_dtype, updated), grad (in grad_dtype; NULL
+ *     leaves the tensor and its moments as they are), copy (bf16, written with the new values, or NULL), n
+ *     values each, contiguous, aligned to their type (16 bytes are faster).
+ *   m, v: the moments of all tensors, tensor i from value 256 * sum_{j < i} ceil(n_j / 256) on; 16-byte
+ *     aligned, the values behind a tensor's last up to the next multiple of 256 are not touched.
+ *     bits 32: fp32.  bits 8: e4m3 bytes; m and sqrt(v) divided by a power of two per 256 values, m_scale and
+ *     v_scale (fp32, one per 256 values; NULL for bits 32), the smallest that leaves none over 448.  A value
+ *     goes to one of its two neighbours in e4m3, up where its distance from the lower one (in steps) and a
+ *     dither reach 1: with place i (in m) and all arithmetic modulo 2^32, h = hash(i + t 0x9e3779b9 +
+ *     (i >> 32) 0x85ebca6b), hash: x ^= x >> 16, x *= 0x7feb352d, x ^= x >> 15, x *= 0x846ca68b,
+ *     x ^= x >> 16; m takes h mod 2^16, sqrt(v) h >> 16, in units of 2^-16.  Values that are not finite become NaN.
+ *   step: int[2] on the device: the steps done so far, read and increased by the call (also when count is 0),
+ *     and a counter that is 0 between calls.  A captured call so counts its own replays.
+ *   lr_at, grad_scale: fp32 on the device, or NULL (lr; 1).
+ * Arithmetic is fp32; a bf16 param or copy is rounded to nearest.  Equal inputs give equal bits.
+ * bits 8 or 32; 0 <= beta < 1, eps > 0.  No two written tensors, and no written and read one, may overlap
+ * (TTM_ERR_INVALID_ARG; one gradient may serve several tensors).  Calls that share m, v or step run one after the
+ * other on one stream.  Asynchronous on `stream`; TTM_ERR_CUDA if a launch fails.
+ */
+typedef struct {
+    void* param;
+    const void* grad;
+    void* copy;
+    long long n;
+    int param_dtype, grad_dtype;
+} ttm_adamw_tensor;
+int ttm_adamw_step(int count, const ttm_adamw_tensor* tensors, int bits,
+                   void* m, void* v, float* m_scale, float* v_scale, int* step,
+                   double lr, const float* lr_at, double beta1, double beta2, double eps,
+                   double weight_decay, const float* grad_scale, void* stream);
+
+/* The moments of bits 8 as fp32: m_out = m m_scale, v_out = (v v_scale)^2 for `blocks` blocks of 256 values. */
+int ttm_adamw_moments(long long blocks, const void* m, const void* v,
+                      const float* m_scale, const float* v_scale,
+                      float* m_out, float* v_out, void* stream);
+
 /* The activation of the 2-layer memory and its derivative, evaluated on the
  * device exactly as the tensor-core 2-layer kernel evaluates them: for the n
  * values x[i], y[i] = GELU(x) = x Phi(x) and, if dy is not NULL,

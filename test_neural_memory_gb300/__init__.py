@@ -9,12 +9,15 @@ fallback: if the library is missing the calls raise.
     z, W, S = titans_fwd(q, k, v, theta, W0, chunk, eta=eta, alpha=alpha)
     z, W1, W2, S1, S2 = mlp_fwd(q, k, v, theta, W1_0, W2_0, chunk, eta=eta, alpha=alpha)
 
-The operators around the scan (gated linear recurrence, layer norm, orthogonalised
-update) are in train.py and re-exported here:
+The operators around the scan (gated linear recurrence, layer norm, short convolution, gated
+feed-forward block, orthogonalised update, AdamW) are in train.py and re-exported here:
 
     h, h_last = glr_fwd(x, g, h0=h0)
     y, mean, rstd = layer_norm_fwd(x, w, b)
+    y, state = causal_conv_fwd(x, w, b)
+    y, gu = gated_ffn_fwd(x, W_in, W_out)
     O = orthogonalize(G)
+    adamw_step(params, grads, state, lr=1e-3)
 """
 from __future__ import annotations
 
@@ -87,8 +90,20 @@ def lib() -> ctypes.CDLL:
         L.ttm_layer_norm_bwd.argtypes = [i] * 3 + [p, ll] * 2 + [p] * 7 + [sz, p]
         L.ttm_orthogonalize_workspace_size.argtypes = [i] * 3
         L.ttm_orthogonalize.argtypes = [i] * 4 + [p, p, i, fl, p, p, sz, p]
+        db = ctypes.c_double
+        L.ttm_causal_conv_fwd.argtypes = [i] * 6 + [p, ll, ll] + [p] * 4 + [ll, p, p, p]
+        L.ttm_causal_conv_bwd_workspace_size.argtypes = [i] * 2
+        L.ttm_causal_conv_bwd.argtypes = ([i] * 6 + [p, ll, ll] * 2 + [p] * 4 + [ll] + [p] * 6 +
+                                          [sz, p])
+        L.ttm_causal_conv_step.argtypes = [i] * 6 + [p, ll, ll] + [p] * 5
+        L.ttm_gated_ffn_workspace_size.argtypes = [i] * 4
+        L.ttm_gated_ffn_fwd.argtypes = [i] * 4 + [p, ll, p, p, p, ll, p, p, p, sz, p]
+        L.ttm_gated_ffn_bwd.argtypes = [i] * 4 + [p, ll] * 2 + [p] * 7 + [sz, p]
+        L.ttm_adamw_step.argtypes = [i, p, i] + [p] * 5 + [db, p] + [db] * 4 + [p, p]
+        L.ttm_adamw_moments.argtypes = [ll] + [p] * 7
         for f in (L.ttm_glr_workspace_size, L.ttm_layer_norm_bwd_workspace_size,
-                  L.ttm_orthogonalize_workspace_size):
+                  L.ttm_orthogonalize_workspace_size, L.ttm_causal_conv_bwd_workspace_size,
+                  L.ttm_gated_ffn_workspace_size):
             f.restype = sz
         for f in (L.ttm_linear_fwd, L.ttm_titans_fwd, L.ttm_mlp_fwd):
             f.restype = i
@@ -473,5 +488,6 @@ def mlp_gelu(x, *, want_grad=True, stream=None):
     return y, dy
 
 
-from .train import (glr_bwd, glr_fwd, glr_step, layer_norm_bwd, layer_norm_fwd,  # noqa: E402,F401
-                    orthogonalize)
+from .train import (adamw_moments, adamw_state, adamw_step, causal_conv_bwd,  # noqa: E402,F401
+                    causal_conv_fwd, causal_conv_step, gated_ffn_bwd, gated_ffn_fwd, glr_bwd, glr_fwd,
+                    glr_step, layer_norm_bwd, layer_norm_fwd, orthogonalize)

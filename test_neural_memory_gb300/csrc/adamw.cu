@@ -1,0 +1,355 @@
+// AdamW step over many tensors in one launch:
+//   m <- b1 m + (1 - b1) g,  v <- b2 v + (1 - b2) g^2,
+//   p <- p (1 - lr decay) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps),
+// g scaled by a number on the device, p in fp32 or bf16, fp32 weights with a bf16 copy on request, m and v in
+// fp32 or in 8 bits.
+//
+// 8 bits.  m and sqrt(v) are e4m3 values times a power of two per 256 of them, the smallest that leaves none over
+// 448.  Rounding to nearest would stand still: a step changes v by (1 - b2) (g^2 - v), a thousandth of it, and
+// half a step of e4m3 is a sixteenth.  So a value goes up or down as its distance to the two neighbours and a
+// dither say, a fixed hash of the value's place and the step: the moments move by the right amount on average, and
+// equal calls give equal bits.  The moments' own arithmetic rounds after every operation (no fused
+// multiply-add): whether a value is past the dither then does not depend on how a compiler contracts it.
+//
+// Bound by HBM: 28 bytes a value with fp32 moments and gradients, 14 in 8 bits with bf16 gradients.  A warp
+// takes blocks of 256 values, 8 a lane in two runs of 4, so that every access of a warp is one piece of
+// memory; tensors that do not start on 16 bytes, and their last blocks, go value by value.  The table of
+// tensors travels as a kernel argument (a copy to the device would be a call of its own, and not the
+// captured graph's), and a block finds its tensor by bisection.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "train_ops.h"
+
+namespace ttm {
+namespace {
+
+constexpr int kSms = 152, kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBlock = 256;             // values that share a scale
+constexpr int kChunk = kWarps * kBlock; // values a block of threads takes at a time
+
+template <int CAP>
+struct Table {
+    AdamwEntry e[CAP];
+    int count, chunks;
+    int last;                           // the launch that ends the step
+};
+
+struct Consts {
+    float lr, keep, b1, b2, c1, c2, lr1, root2, eps, scale;   // lr1: lr / (1 - b1^t); root2: 1 / sqrt(1 - b2^t)
+    uint32_t key;                       // of the dither
+};
+
+// lowbias32 of C. Wellons' search for integer hashes ("Prospecting for Hash Functions", 2018).
+__device__ __forceinline__ uint32_t hash32(uint32_t x) {
+    x ^= x >> 16;
+    x *= 0x7feb352du;
+    x ^= x >> 15;
+    x *= 0x846ca68bu;
+    return x ^ (x >> 16);
+}
+
+// The power of two, as an exponent, that a block's largest size is divided by.
+__device__ __forceinline__ int scale_of(float most) {
+    const uint32_t u = __float_as_uint(most);
+    const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u);
+    return max(e, -126);
+}
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// x / 2^e on e4m3's grid: down, or up where the missing part of a step and `frac` make one.  What is not a
+// number or infinite becomes NaN (e4m3 has no infinity).
+__device__ __forceinline__ float to_grid(float x, float inverse, float frac) {
+    const float y = fabsf(x) * inverse;
+    const int b = max((int)(__float_as_uint(y) >> 23) - 127, -6);
+    const float q = floorf(__fadd_rn(y * power(3 - b), frac)) * power(b - 3);
+    return isfinite(x) ? copysignf(q, x) : __uint_as_float(0x7fc00000u);
+}
+
+__device__ __forceinline__ float4 decode4(uint32_t code) {
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(code & 0xffffu), __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(code >> 16), __NV_E4M3);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ float decode1(unsigned char code) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(code, __NV_E4M3);
+    return __half2float(*reinterpret_cast<const __half*>(&h));
+}
+__device__ __forceinline__ uint32_t encode4(const float* f) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+}
+
+__device__ __forceinline__ float warp_most(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+__device__ __forceinline__ Consts constants(const AdamwScalars& a) {
+    Consts k;
+    const int t = *reinterpret_cast<const volatile int*>(a.step) + 1;
+    k.lr = a.lr_at ? *a.lr_at : a.lr;
+    k.keep = fmaf(-k.lr, a.decay, 1.f);
+    k.b1 = a.b1; k.b2 = a.b2; k.c1 = a.c1; k.c2 = a.c2;
+    k.lr1 = k.lr / -expm1f((float)t * a.log_b1);
+    k.root2 = 1.f / sqrtf(-expm1f((float)t * a.log_b2));
+    k.eps = a.eps;
+    k.scale = a.grad_scale ? *a.grad_scale : 1.f;
+    k.key = (uint32_t)t * 0x9e3779b9u;
+    return k;
+}
+
+// m, v and p of one value.
+__device__ __forceinline__ void moments(const Consts& k, float g, float& m, float& v) {
+    g = __fmul_rn(g, k.scale);
+    m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.c1));
+    v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.c2));
+}
+__device__ __forceinline__ float update(const Consts& k, float p, float m, float root) {
+    return fmaf(p, k.keep, -__fdividef(k.lr1 * m, fmaf(root, k.root2, k.eps)));
+}
+
+__device__ __forceinline__ float finite_size(float x) { return isfinite(x) ? fabsf(x) : 0.f; }
+
+// One block of up to 256 values by a warp.  VEC: 256 of them, in runs of 4 a lane; otherwise lane l takes the
+// values l, l + 32, ..
+template <bool EIGHT, bool VEC>
+__device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScalars& a, const Consts& k, long long block,
+                                           int lane) {
+    const long long i0 = block * kBlock;                            // of the tensor
+    const long long s0 = (e.first + block) * kBlock;                // of the moments
+    const int n = (int)min((long long)kBlock, e.n - i0);
+    auto index = [&](int j) { return VEC ? (j >> 2) * 128 + lane * 4 + (j & 3) : lane + 32 * j; };
+    float p[8], g[8], m[8], v[8];
+    if constexpr (VEC) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = h * 128 + lane * 4;
+            if (e.p_bf16) {
+                const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.p) + i0 + i);
+                p[4 * h] = __uint_as_float(u.x << 16); p[4 * h + 1] = __uint_as_float(u.x & 0xffff0000u);
+                p[4 * h + 2] = __uint_as_float(u.y << 16); p[4 * h + 3] = __uint_as_float(u.y & 0xffff0000u);
+            } else {
+                *reinterpret_cast<float4*>(p + 4 * h) = *reinterpret_cast<const float4*>(static_cast<const float*>(e.p) + i0 + i);
+            }
+            if (e.g_bf16) {
+                const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.g) + i0 + i);
+                g[4 * h] = __uint_as_float(u.x << 16); g[4 * h + 1] = __uint_as_float(u.x & 0xffff0000u);
+                g[4 * h + 2] = __uint_as_float(u.y << 16); g[4 * h + 3] = __uint_as_float(u.y & 0xffff0000u);
+            } else {
+                *reinterpret_cast<float4*>(g + 4 * h) = *reinterpret_cast<const float4*>(static_cast<const float*>(e.g) + i0 + i);
+            }
+            if constexpr (EIGHT) {
+                *reinterpret_cast<float4*>(m + 4 * h) = decode4(*reinterpret_cast<const uint32_t*>(static_cast<const unsigned char*>(a.m) + s0 + i));
+                *reinterpret_cast<float4*>(v + 4 * h) = decode4(*reinterpret_cast<const uint32_t*>(static_cast<const unsigned char*>(a.v) + s0 + i));
+            } else {
+                *reinterpret_cast<float4*>(m + 4 * h) = *reinterpret_cast<const float4*>(static_cast<const float*>(a.m) + s0 + i);
+                *reinterpret_cast<float4*>(v + 4 * h) = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v) + s0 + i);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = lane + 32 * j;
+            p[j] = g[j] = m[j] = v[j] = 0.f;
+            if (i >= n) continue;
+            p[j] = e.p_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.p)[i0 + i]) : static_cast<const float*>(e.p)[i0 + i];
+            g[j] = e.g_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.g)[i0 + i]) : static_cast<const float*>(e.g)[i0 + i];
+            if constexpr (EIGHT) {
+                m[j] = decode1(static_cast<const unsigned char*>(a.m)[s0 + i]);
+                v[j] = decode1(static_cast<const unsigned char*>(a.v)[s0 + i]);
+            } else {
+                m[j] = static_cast<const float*>(a.m)[s0 + i];
+                v[j] = static_cast<const float*>(a.v)[s0 + i];
+            }
+        }
+    }
+    float ms = 0.f, vs = 0.f;
+    if constexpr (EIGHT) {
+        ms = a.m_scale[e.first + block];
+        vs = a.v_scale[e.first + block];
+    }
+    float most_m = 0.f, most_r = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (EIGHT) {
+            m[j] = __fmul_rn(m[j], ms);
+            v[j] = __fmul_rn(v[j], vs);
+            v[j] = __fmul_rn(v[j], v[j]);
+        }
+        moments(k, g[j], m[j], v[j]);
+        const float root = sqrtf(v[j]);
+        p[j] = update(k, p[j], m[j], root);
+        if constexpr (EIGHT) {
+            v[j] = root;
+            if (VEC || index(j) < n) {
+                most_m = fmaxf(most_m, finite_size(m[j]));
+                most_r = fmaxf(most_r, finite_size(root));
+            }
+        }
+    }
+    if constexpr (EIGHT) {
+        const int em = scale_of(warp_most(most_m)), er = scale_of(warp_most(most_r));
+        const float im = power(-em), ir = power(-er);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const unsigned long long at = (unsigned long long)s0 + index(j);
+            const uint32_t h = hash32((uint32_t)at + k.key + (uint32_t)(at >> 32) * 0x85ebca6bu);
+            m[j] = to_grid(m[j], im, (float)(h & 0xffffu) * (1.f / 65536.f));
+            v[j] = to_grid(v[j], ir, (float)(h >> 16) * (1.f / 65536.f));
+        }
+        if (lane == 0) {
+            a.m_scale[e.first + block] = power(em);
+            a.v_scale[e.first + block] = power(er);
+        }
+    }
+    if constexpr (VEC) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = h * 128 + lane * 4;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(p[4 * h], p[4 * h + 1]);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(p[4 * h + 2], p[4 * h + 3]);
+            const uint2 half = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            if (e.p_bf16) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(e.p) + i0 + i) = half;
+            else *reinterpret_cast<float4*>(static_cast<float*>(e.p) + i0 + i) = *reinterpret_cast<float4*>(p + 4 * h);
+            if (e.copy) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(e.copy) + i0 + i) = half;
+            if constexpr (EIGHT) {
+                *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.m) + s0 + i) = encode4(m + 4 * h);
+                *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.v) + s0 + i) = encode4(v + 4 * h);
+            } else {
+                *reinterpret_cast<float4*>(static_cast<float*>(a.m) + s0 + i) = *reinterpret_cast<float4*>(m + 4 * h);
+                *reinterpret_cast<float4*>(static_cast<float*>(a.v) + s0 + i) = *reinterpret_cast<float4*>(v + 4 * h);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = lane + 32 * j;
+            if (i >= n) continue;
+            if (e.p_bf16) static_cast<__nv_bfloat16*>(e.p)[i0 + i] = __float2bfloat16_rn(p[j]);
+            else static_cast<float*>(e.p)[i0 + i] = p[j];
+            if (e.copy) static_cast<__nv_bfloat16*>(e.copy)[i0 + i] = __float2bfloat16_rn(p[j]);
+            if constexpr (EIGHT) {
+                static_cast<unsigned char*>(a.m)[s0 + i] = __nv_cvt_float_to_fp8(m[j], __NV_SATFINITE, __NV_E4M3);
+                static_cast<unsigned char*>(a.v)[s0 + i] = __nv_cvt_float_to_fp8(v[j], __NV_SATFINITE, __NV_E4M3);
+            } else {
+                static_cast<float*>(a.m)[s0 + i] = m[j];
+                static_cast<float*>(a.v)[s0 + i] = v[j];
+            }
+        }
+    }
+}
+
+template <bool EIGHT, int CAP>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> t,
+                                                          const __grid_constant__ AdamwScalars a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Consts k = constants(a);
+    for (int chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
+        int lo = 0, hi = t.count - 1;   // the last tensor that starts at or before the chunk
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (t.e[mid].chunk <= chunk) lo = mid;
+            else hi = mid - 1;
+        }
+        const AdamwEntry& e = t.e[lo];
+        const long long block = (long long)(chunk - e.chunk) * kWarps + warp;
+        if (block * kBlock >= e.n) continue;
+        const uint64_t at = reinterpret_cast<uintptr_t>(e.p) << e.p_bf16 | reinterpret_cast<uintptr_t>(e.g) << e.g_bf16 |
+                            reinterpret_cast<uintptr_t>(e.copy) << 1;    // 4 bf16 values are 8 bytes
+        if (at % 16 == 0 && (block + 1) * kBlock <= e.n) step_block<EIGHT, true>(e, a, k, block, lane);
+        else step_block<EIGHT, false>(e, a, k, block, lane);
+    }
+    // The last block to finish counts the step: every block has read the count by then.
+    if (t.last) {
+        __syncthreads();
+        if (threadIdx.x == 0 && atomicAdd(a.step + 1, 1) == (int)gridDim.x - 1) {
+            a.step[1] = 0;
+            a.step[0] += 1;
+        }
+    }
+}
+
+// m and v in fp32 from 8 bits: a warp a block of 256 values.
+__global__ void __launch_bounds__(kThreads) adamw_moments_kernel(long long blocks, const __grid_constant__ AdamwScalars a,
+                                                                  float* m, float* v) {
+    const int lane = threadIdx.x & 31;
+    for (long long b = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); b < blocks; b += (long long)gridDim.x * kWarps) {
+        const float ms = a.m_scale[b], vs = a.v_scale[b];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const long long i = b * kBlock + h * 128 + lane * 4;
+            float4 x = decode4(*reinterpret_cast<const uint32_t*>(static_cast<const unsigned char*>(a.m) + i));
+            float4 r = decode4(*reinterpret_cast<const uint32_t*>(static_cast<const unsigned char*>(a.v) + i));
+            x.x *= ms; x.y *= ms; x.z *= ms; x.w *= ms;
+            r.x *= vs; r.y *= vs; r.z *= vs; r.w *= vs;
+            *reinterpret_cast<float4*>(m + i) = x;
+            *reinterpret_cast<float4*>(v + i) = make_float4(r.x * r.x, r.y * r.y, r.z * r.z, r.w * r.w);
+        }
+    }
+}
+
+template <bool EIGHT, int CAP>
+cudaError_t launch(const AdamwEntry* tensors, int count, int chunks, int last, const AdamwScalars& a, cudaStream_t s) {
+    Table<CAP> t;
+    for (int i = 0; i < count; ++i) t.e[i] = tensors[i];
+    t.count = count;
+    t.chunks = chunks;
+    t.last = last;
+    const int most = kSms * 4, grid = chunks < 1 ? 1 : chunks < most ? chunks : most;
+    adamw_kernel<EIGHT, CAP><<<grid, kThreads, 0, s>>>(t, a);
+    return cudaGetLastError();
+}
+
+// Kernel arguments take 32764 bytes at most; short lists go with a short table.
+constexpr int kMost = 500, kFew = 48;
+
+template <bool EIGHT>
+cudaError_t run(const AdamwEntry* tensors, int count, const AdamwScalars& a, cudaStream_t s, int* launches) {
+    static_assert(sizeof(Table<kMost>) + sizeof(AdamwScalars) <= 32764, "kernel arguments");
+    AdamwEntry part[kMost];
+    int at = 0;
+    *launches = 0;
+    do {
+        int n = 0;
+        long long chunks = 0;
+        while (at < count && n < kMost) {
+            const long long more = (tensors[at].n + kChunk - 1) / kChunk;
+            if (chunks + more > INT_MAX) break;
+            part[n] = tensors[at++];
+            part[n++].chunk = (int)chunks;
+            chunks += more;
+        }
+        const cudaError_t e = n <= kFew ? launch<EIGHT, kFew>(part, n, (int)chunks, at == count, a, s)
+                                        : launch<EIGHT, kMost>(part, n, (int)chunks, at == count, a, s);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    } while (at < count);
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t adamw_step_launch(const AdamwEntry* tensors, int count, const AdamwScalars& a, cudaStream_t s,
+                              int* launches) {
+    return a.m_scale ? run<true>(tensors, count, a, s, launches) : run<false>(tensors, count, a, s, launches);
+}
+
+cudaError_t adamw_moments_launch(long long blocks, const AdamwScalars& a, float* m, float* v, cudaStream_t s) {
+    if (blocks == 0) return cudaSuccess;
+    const long long need = (blocks + kWarps - 1) / kWarps;
+    const int grid = need < kSms * 8 ? (int)need : kSms * 8;
+    adamw_moments_kernel<<<grid, kThreads, 0, s>>>(blocks, a, m, v);
+    return cudaGetLastError();
+}
+
+}  // namespace ttm

@@ -317,6 +317,310 @@ PyObject* orthogonalize(PyObject* const* a) {
     return wrap(out);
 }
 
+// x [..., T, C] with taps w [C, K]: sizes, strides and the shape of its state.
+struct Conv {
+    int N, T, C, K, dtype;
+    long long xs, xt;
+    std::vector<int64_t> state;
+};
+
+Conv conv_shapes(const at::Tensor& x, const at::Tensor& w, const Maybe& b, const char* what) {
+    Conv r;
+    const int64_t lead = x.dim() - 2;
+    if (lead < 0) bad(std::string(what) + ": expected [..., T, C]");
+    const int64_t C = x.size(lead + 1);
+    r.dtype = dtype_code(x, what);
+    if ((C > 1 && x.stride(lead + 1) != 1) || !x.is_cuda())
+        bad(std::string(what) + ": expected a CUDA tensor with contiguous channels");
+    if (w.dim() != 2) bad(std::string(what) + ": w must be [C, K]");
+    const int64_t K = w.size(1);
+    check(w, {C, K}, at::kFloat, x.device(), "w");
+    check(b, {C}, x.device(), "b");
+    int64_t N = 1;
+    for (int64_t k = 0; k < lead; ++k) N *= x.size(k);
+    r.N = narrow(N, what);
+    r.T = narrow(x.size(lead), what);
+    r.C = narrow(C, what);
+    r.K = narrow(K, what);
+    strides(x, lead, C, what, r.xs, r.xt);
+    r.state.assign(x.sizes().begin(), x.sizes().begin() + lead);
+    r.state.push_back(K - 1);
+    r.state.push_back(C);
+    return r;
+}
+
+void check_state(const Maybe& t, const Conv& c, const at::Tensor& x, const char* what) {
+    if (t) check(*t, c.state, x.scalar_type(), x.device(), what);
+}
+
+// Document numbers [..., T] and the elements between sequences.
+const int* documents(const Maybe& doc, const at::Tensor& x, long long& seq) {
+    seq = 0;
+    if (!doc) return nullptr;
+    const int64_t lead = x.dim() - 2;
+    if (doc->scalar_type() != at::kInt || doc->sizes() != x.sizes().slice(0, lead + 1) || doc->device() != x.device() ||
+        (x.size(lead) > 1 && doc->stride(lead) != 1))
+        bad("doc must be int32, of the shape of x without its last axis, tokens contiguous, on the call's device");
+    seq = one_stride(*doc, lead, "doc").value_or(x.size(lead));
+    return static_cast<const int*>(doc->data_ptr());
+}
+
+// (x, w, b, state0, doc, silu, want_state, y, state) -> (y, state)
+PyObject* causal_conv_fwd(PyObject* const* a) {
+    const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w");
+    const Maybe b = maybe(a[2], "b"), s0 = maybe(a[3], "state0"), doc = maybe(a[4], "doc");
+    const Conv c = conv_shapes(x, w, b, "causal_conv_fwd");
+    const at::Device dev = x.device();
+    const c10::cuda::CUDAGuard guard(dev);
+    check_state(s0, c, x, "state0");
+    long long doc_seq;
+    const int* ids = documents(doc, x, doc_seq);
+    at::Tensor y = output(maybe(a[7], "y"), x.sizes(), x.scalar_type(), dev, "y");
+    Maybe state;
+    if (a[6] == Py_True) state = output(maybe(a[8], "state"), c.state, x.scalar_type(), dev, "state");
+    done(ttm_causal_conv_fwd(c.N, c.T, c.C, c.K, c.dtype, a[5] == Py_True, x.data_ptr(), c.xs, c.xt,
+                             static_cast<float*>(w.data_ptr()), fptr(b), ptr(s0), ids, doc_seq, y.data_ptr(), ptr(state),
+                             current_stream(dev)),
+         "ttm_causal_conv_fwd");
+    return tuple({y, state});
+}
+
+// (dy, x, w, b, state0, doc, silu, dstate, want_dw, dx, dw, db, dstate0, workspace) -> (dx, dw, db, dstate0)
+PyObject* causal_conv_bwd(PyObject* const* a) {
+    const at::Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x"), &w = tensor(a[2], "w");
+    const Maybe b = maybe(a[3], "b"), s0 = maybe(a[4], "state0"), doc = maybe(a[5], "doc"), ds = maybe(a[7], "dstate");
+    const Conv c = conv_shapes(x, w, b, "causal_conv_bwd");
+    const at::Device dev = x.device();
+    const c10::cuda::CUDAGuard guard(dev);
+    check_state(s0, c, x, "state0");
+    check_state(ds, c, x, "dstate");
+    if (dy.sizes() != x.sizes() || dy.scalar_type() != x.scalar_type() || dy.device() != dev ||
+        (c.C > 1 && dy.stride(-1) != 1))
+        bad("causal_conv_bwd: dy must have the shape, dtype and channel order of x");
+    long long doc_seq, ys, yt;
+    const int* ids = documents(doc, x, doc_seq);
+    strides(dy, x.dim() - 2, c.C, "causal_conv_bwd", ys, yt);
+    const bool want = a[8] == Py_True;
+    at::Tensor dx = output(maybe(a[9], "dx"), x.sizes(), x.scalar_type(), dev, "dx");
+    Maybe dw, db, d0;
+    if (want) dw = output(maybe(a[10], "dw"), w.sizes(), at::kFloat, dev, "dw");
+    if (want && b) db = output(maybe(a[11], "db"), b->sizes(), at::kFloat, dev, "db");
+    if (s0) d0 = output(maybe(a[12], "dstate0"), c.state, x.scalar_type(), dev, "dstate0");
+    const Maybe ws = scratch(maybe(a[13], "workspace"), want ? ttm_causal_conv_bwd_workspace_size(c.C, c.K) : 0, dev);
+    done(ttm_causal_conv_bwd(c.N, c.T, c.C, c.K, c.dtype, a[6] == Py_True, dy.data_ptr(), ys, yt, x.data_ptr(), c.xs,
+                             c.xt, static_cast<float*>(w.data_ptr()), fptr(b), ptr(s0), ids, doc_seq, ptr(ds),
+                             dx.data_ptr(), fptr(dw), fptr(db), ptr(d0), ptr(ws), bytes(ws), current_stream(dev)),
+         "ttm_causal_conv_bwd");
+    return tuple({dx, dw, db, d0});
+}
+
+// (x, w, state, b, silu, y) -> y
+PyObject* causal_conv_step(PyObject* const* a) {
+    const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w"), &state = tensor(a[2], "state");
+    const Maybe b = maybe(a[3], "b");
+    const Conv c = conv_shapes(x, w, b, "causal_conv_step");
+    const at::Device dev = x.device();
+    const c10::cuda::CUDAGuard guard(dev);
+    check(state, c.state, x.scalar_type(), dev, "state");
+    at::Tensor y = output(maybe(a[5], "y"), x.sizes(), x.scalar_type(), dev, "y");
+    done(ttm_causal_conv_step(c.N, c.T, c.C, c.K, c.dtype, a[4] == Py_True, x.data_ptr(), c.xs, c.xt,
+                              static_cast<float*>(w.data_ptr()), fptr(b), state.data_ptr(), y.data_ptr(),
+                              current_stream(dev)),
+         "ttm_causal_conv_step");
+    return wrap(y);
+}
+
+// x [..., D], W_in [D, 2F], W_out [F, D], all bf16 on one device.
+struct Ffn {
+    int N, D, F, act;
+    long long step;
+    std::vector<int64_t> wide;          // [..., 2F]
+};
+
+Ffn ffn_shapes(const at::Tensor& x, const at::Tensor& W_in, const at::Tensor& W_out, PyObject* act, const char* what) {
+    Ffn r;
+    if (x.scalar_type() != at::kBFloat16) throw WrongType{std::string(what) + ": tensors must be bfloat16"};
+    rows(x, what, r.N, r.D, r.step);
+    if (W_in.dim() != 2 || W_in.size(1) % 2) bad(std::string(what) + ": W_in must be [D, 2F]");
+    const int64_t F = W_in.size(1) / 2;
+    r.F = narrow(F, what);
+    check(W_in, {r.D, 2 * F}, at::kBFloat16, x.device(), "W_in");
+    check(W_out, {F, r.D}, at::kBFloat16, x.device(), "W_out");
+    r.act = (int)PyLong_AsLong(act);
+    if (PyErr_Occurred()) throw PythonError{};
+    r.wide.assign(x.sizes().begin(), x.sizes().end() - 1);
+    r.wide.push_back(2 * F);
+    return r;
+}
+
+// Elements between the rows of a tensor that has the shape of x.
+long long rows_like(const at::Tensor& t, const at::Tensor& x, const char* what) {
+    if (t.sizes() != x.sizes() || t.scalar_type() != x.scalar_type() || t.device() != x.device())
+        bad(std::string(what) + " must have the shape and dtype of x and be on its device");
+    int n, d;
+    long long step;
+    rows(t, what, n, d, step);
+    return step;
+}
+
+// (x, W_in, W_out, act, residual, want_gu, y, gu, workspace) -> (y, gu)
+PyObject* gated_ffn_fwd(PyObject* const* a) {
+    const at::Tensor &x = tensor(a[0], "x"), &W_in = tensor(a[1], "W_in"), &W_out = tensor(a[2], "W_out");
+    const Ffn f = ffn_shapes(x, W_in, W_out, a[3], "gated_ffn_fwd");
+    const Maybe res = maybe(a[4], "residual");
+    const long long res_step = res ? rows_like(*res, x, "residual") : 0;
+    const at::Device dev = x.device();
+    const c10::cuda::CUDAGuard guard(dev);
+    at::Tensor y = output(maybe(a[6], "y"), x.sizes(), at::kBFloat16, dev, "y");
+    Maybe gu;
+    if (a[5] == Py_True) gu = output(maybe(a[7], "gu"), f.wide, at::kBFloat16, dev, "gu");
+    const Maybe ws = scratch(maybe(a[8], "workspace"), ttm_gated_ffn_workspace_size(f.N, f.D, f.F, 0), dev);
+    done(ttm_gated_ffn_fwd(f.N, f.D, f.F, f.act, x.data_ptr(), f.step, W_in.data_ptr(), W_out.data_ptr(), ptr(res),
+                           res_step, y.data_ptr(), ptr(gu), ptr(ws), bytes(ws), current_stream(dev)),
+         "ttm_gated_ffn_fwd");
+    return tuple({y, gu});
+}
+
+// (dy, x, gu, W_in, W_out, act, want_dx, want_dw, dx, dW_in, dW_out, workspace) -> (dx, dW_in, dW_out)
+PyObject* gated_ffn_bwd(PyObject* const* a) {
+    const at::Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x"), &gu = tensor(a[2], "gu"),
+                     &W_in = tensor(a[3], "W_in"), &W_out = tensor(a[4], "W_out");
+    const Ffn f = ffn_shapes(x, W_in, W_out, a[5], "gated_ffn_bwd");
+    const long long dy_step = rows_like(dy, x, "dy");
+    const at::Device dev = x.device();
+    const c10::cuda::CUDAGuard guard(dev);
+    check(gu, f.wide, at::kBFloat16, dev, "gu");
+    Maybe dx, dW_in, dW_out;
+    if (a[6] == Py_True) dx = output(maybe(a[8], "dx"), x.sizes(), at::kBFloat16, dev, "dx");
+    if (a[7] == Py_True) {
+        dW_in = output(maybe(a[9], "dW_in"), W_in.sizes(), at::kBFloat16, dev, "dW_in");
+        dW_out = output(maybe(a[10], "dW_out"), W_out.sizes(), at::kBFloat16, dev, "dW_out");
+    }
+    const Maybe ws = scratch(maybe(a[11], "workspace"), ttm_gated_ffn_workspace_size(f.N, f.D, f.F, 1), dev);
+    done(ttm_gated_ffn_bwd(f.N, f.D, f.F, f.act, dy.data_ptr(), dy_step, x.data_ptr(), f.step, gu.data_ptr(),
+                           W_in.data_ptr(), W_out.data_ptr(), ptr(dx), ptr(dW_in), ptr(dW_out), ptr(ws), bytes(ws),
+                           current_stream(dev)),
+         "ttm_gated_ffn_bwd");
+    return tuple({dx, dW_in, dW_out});
+}
+
+// A list or tuple, held while it is read.
+struct Items {
+    PyObject* seq;
+    Items(PyObject* o, const char* what) : seq(PySequence_Fast(o, "")) {
+        if (!seq) {
+            PyErr_Clear();
+            bad(std::string(what) + " must be a list of tensors");
+        }
+    }
+    ~Items() { Py_XDECREF(seq); }
+    Items(const Items&) = delete;
+    Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(seq); }
+    PyObject* at(Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(seq, i); }
+};
+
+double number(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw PythonError{};
+    return v;
+}
+
+const float* scalar(const Maybe& t, const at::Device& dev, const char* what) {
+    if (!t) return nullptr;
+    if (t->numel() != 1 || t->scalar_type() != at::kFloat || t->device() != dev)
+        bad(std::string(what) + " must be a float32 tensor of one value on the call's device");
+    return static_cast<const float*>(t->data_ptr());
+}
+
+// Whole blocks of 256 moments; 8 bits when there are scales.
+int64_t moments_of(const at::Tensor& m, const at::Tensor& v, const Maybe& ms, const Maybe& vs, const at::Device& dev) {
+    const at::ScalarType type = ms ? at::kFloat8_e4m3fn : at::kFloat;
+    const int64_t n = m.numel();
+    if (ms.has_value() != vs.has_value() || n % 256) bad("state: not one of adamw_state");
+    check(m, {n}, type, dev, "state m");
+    check(v, {n}, type, dev, "state v");
+    check(ms, {n / 256}, dev, "state m_scale");
+    check(vs, {n / 256}, dev, "state v_scale");
+    return n / 256;
+}
+
+// (params, grads, copies, m, v, m_scale, v_scale, step, lr, b1, b2, eps, weight_decay, grad_scale) -> None
+PyObject* adamw_step(PyObject* const* a) {
+    const Items params(a[0], "params"), grads(a[1], "grads");
+    std::optional<Items> copies;
+    if (a[2] != Py_None) copies.emplace(a[2], "copies");
+    const Py_ssize_t n = params.size();
+    if (grads.size() != n || (copies && copies->size() != n)) bad("adamw_step: as many grads and copies as params");
+    const at::Tensor &m = tensor(a[3], "m"), &v = tensor(a[4], "v"), &step = tensor(a[7], "step");
+    const Maybe ms = maybe(a[5], "m_scale"), vs = maybe(a[6], "v_scale"), gs = maybe(a[13], "grad_scale");
+    if (!m.is_cuda()) bad("adamw_step: expected CUDA tensors");
+    const at::Device dev = m.device();
+    const int64_t blocks = moments_of(m, v, ms, vs, dev);
+    check(step, {2}, at::kInt, dev, "state step");
+    const float* scale = scalar(gs, dev, "grad_scale");
+    Maybe lr_tensor;
+    double lr = 0;
+    if (THPVariable_Check(a[8]) && THPVariable_Unpack(a[8]).is_cuda()) lr_tensor = THPVariable_Unpack(a[8]);
+    else lr = number(a[8]);
+    const float* lr_at = scalar(lr_tensor, dev, "lr");
+    std::vector<ttm_adamw_tensor> list((size_t)n);
+    int64_t need = 0;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        const at::Tensor& p = tensor(params.at(i), "param");
+        ttm_adamw_tensor& t = list[(size_t)i];
+        t.n = p.numel();
+        t.param_dtype = t.grad_dtype = dtype_code(p, "param");
+        need += (t.n + 255) / 256;
+        if (!p.is_contiguous() || p.device() != dev) bad("params must be contiguous and on the device of the state");
+        t.param = p.data_ptr();
+        t.grad = nullptr;
+        t.copy = nullptr;
+        if (grads.at(i) == Py_None) continue;
+        const at::Tensor& g = tensor(grads.at(i), "grad");
+        if (g.sizes() != p.sizes() || !g.is_contiguous() || g.device() != dev)
+            bad("grads must be contiguous, of their parameter's shape and on its device");
+        t.grad = g.data_ptr();
+        t.grad_dtype = dtype_code(g, "grad");
+        if (copies && copies->at(i) != Py_None) {
+            const at::Tensor& c = tensor(copies->at(i), "copy");
+            check(c, p.sizes(), at::kBFloat16, dev, "copies");
+            t.copy = c.data_ptr();
+        }
+    }
+    if (need != blocks) bad("adamw_step: the state is of other parameters");
+    const c10::cuda::CUDAGuard guard(dev);
+    done(ttm_adamw_step((int)n, list.data(), ms ? 8 : 32, m.data_ptr(), v.data_ptr(), fptr(ms), fptr(vs),
+                        static_cast<int*>(step.data_ptr()), lr, lr_at, number(a[9]), number(a[10]), number(a[11]),
+                        number(a[12]), scale, current_stream(dev)),
+         "ttm_adamw_step");
+    // autograd sees the parameters written in place
+    auto written = [](PyObject* o) {
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    };
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (!list[(size_t)i].grad) continue;
+        written(params.at(i));
+        if (list[(size_t)i].copy) written(copies->at(i));
+    }
+    Py_RETURN_NONE;
+}
+
+// (m, v, m_scale, v_scale) -> (m, v) in fp32
+PyObject* adamw_moments(PyObject* const* a) {
+    const at::Tensor &m = tensor(a[0], "m"), &v = tensor(a[1], "v");
+    const Maybe ms = maybe(a[2], "m_scale"), vs = maybe(a[3], "v_scale");
+    if (!m.is_cuda() || !ms) bad("adamw_moments: expected CUDA tensors in 8 bits with their scales");
+    const at::Device dev = m.device();
+    const c10::cuda::CUDAGuard guard(dev);
+    const int64_t blocks = moments_of(m, v, ms, vs, dev);
+    at::Tensor mo = make({blocks * 256}, at::kFloat, dev), vo = make({blocks * 256}, at::kFloat, dev);
+    done(ttm_adamw_moments(blocks, m.data_ptr(), v.data_ptr(), fptr(ms), fptr(vs), static_cast<float*>(mo.data_ptr()),
+                           static_cast<float*>(vo.data_ptr()), current_stream(dev)),
+         "ttm_adamw_moments");
+    return tuple({mo, vo});
+}
+
 // No C++ exception leaves the module.
 template <PyObject* (*F)(PyObject* const*), int kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -368,6 +672,13 @@ PyMethodDef g_methods[] = {method<glr_fwd, 6>("glr_fwd"),
                            method<layer_norm_fwd, 8>("layer_norm_fwd"),
                            method<layer_norm_bwd, 11>("layer_norm_bwd"),
                            method<orthogonalize, 5>("orthogonalize"),
+                           method<causal_conv_fwd, 9>("causal_conv_fwd"),
+                           method<causal_conv_bwd, 14>("causal_conv_bwd"),
+                           method<causal_conv_step, 6>("causal_conv_step"),
+                           method<gated_ffn_fwd, 9>("gated_ffn_fwd"),
+                           method<gated_ffn_bwd, 12>("gated_ffn_bwd"),
+                           method<adamw_step, 14>("adamw_step"),
+                           method<adamw_moments, 4>("adamw_moments"),
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 

@@ -1,0 +1,490 @@
+// Short causal convolution, depthwise, with an optional SiLU, per sequence and channel:
+//   pre_t = b + sum_i w[i] x_{t-K+1+i},   y_t = pre_t or pre_t / (1 + exp(-pre_t)),
+// rows before the first from a state (the last K - 1 inputs) or zero, taps whose row is of another
+// document than the token left out; its gradient
+//   d_t = dy_t act'(pre_t),  dx_s = sum_i w[i] d_{s+K-1-i},  dw[i] = sum_t d_t x_{t-K+1+i},  db = sum_t d_t;
+// and its form for a few tokens on a resident state.
+//
+// Bound by HBM: two tensors forward, three in the gradient, K products and one exponential a value.  So
+// every value is read once (but for the K - 1 rows between strips) and the window stays in registers: a
+// thread takes V neighbouring channels, as wide as the rows' alignment allows, and walks a strip of
+// tokens, the loads of kBatch rows ahead of their use.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "train_ops.h"
+
+namespace ttm {
+namespace {
+
+constexpr int kSms = 152;
+constexpr int kBatch = 4;               // rows whose loads are in flight together
+constexpr int kFwdThreads = 128;
+constexpr int kBwdThreads = 256;
+
+// V values of a row as they are stored, and as fp32.
+template <int BYTES> struct Word;
+template <> struct Word<2> { using type = unsigned short; };
+template <> struct Word<4> { using type = uint32_t; };
+template <> struct Word<8> { using type = uint2; };
+template <> struct Word<16> { using type = uint4; };
+template <typename T, int V> using Raw = typename Word<sizeof(T) * V>::type;
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load(const T* p) {
+    return *reinterpret_cast<const Raw<T, V>*>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V>& raw, float (&f)[V]) {
+    if constexpr (sizeof(T) == 4) {
+        const float* s = reinterpret_cast<const float*>(&raw);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = s[i];
+    } else if constexpr (V == 1) {
+        f[0] = __uint_as_float((uint32_t)raw << 16);
+    } else {
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(&raw);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            f[2 * i] = __uint_as_float(s[i] << 16);
+            f[2 * i + 1] = __uint_as_float(s[i] & 0xffff0000u);
+        }
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T* p, const float (&f)[V]) {
+    Raw<T, V> raw;
+    if constexpr (sizeof(T) == 4) {
+        float* d = reinterpret_cast<float*>(&raw);
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = f[i];
+    } else if constexpr (V == 1) {
+        raw = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+    } else {
+        uint32_t* d = reinterpret_cast<uint32_t*>(&raw);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            d[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+    }
+    *reinterpret_cast<Raw<T, V>*>(p) = raw;
+}
+
+// 1 / (1 + exp(-x)).  bf16 results take the fast exponential and division (a few 2^-22 off, |x| 2^-24 more).
+template <typename T>
+__device__ __forceinline__ float sigmoid(float x) {
+    if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-x));
+    else return __fdividef(1.f, 1.f + __expf(-x));
+}
+
+// What a thread walks: rows of one sequence, its V channels from c on.
+template <typename T>
+struct Rows {
+    const T* x;                         // row 0, first channel
+    long long tok;
+    const T* state;                     // [K-1][C] of this sequence, first channel, or NULL
+    int C, K;
+    template <int V>
+    __device__ __forceinline__ Raw<T, V> at(int t) const {           // rows before 0 from the state
+        if (t >= 0) return load<T, V>(x + (long long)t * tok);
+        const int s = t + K - 1;
+        if (state && s >= 0) return load<T, V>(state + (long long)s * C);
+        return Raw<T, V>{};
+    }
+};
+
+// KW: the window, K at most; tap i of K sits in slot i + KW - K, slots before it have weight 0.
+// A strip of tokens a thread; the thread of a sequence's last strip writes the state.  `strips` = 1
+// lets the state be updated in place.
+template <typename T, int V, int KW, bool DOC>
+__global__ void __launch_bounds__(kFwdThreads) conv_fwd_kernel(const __grid_constant__ ConvArgs a, int groups,
+                                                                int strips, int strip) {
+    const long long id = (long long)blockIdx.x * kFwdThreads + threadIdx.x;
+    const int c = (int)(id % groups) * V;
+    const long long rest = id / groups;
+    const int part = (int)(rest % strips);
+    const long long n = rest / strips;
+    if (n >= a.N) return;
+    const int K = a.K, C = a.C, before = KW - K;
+    const int t0 = part * strip, t1 = min(a.T, t0 + strip);
+    Rows<T> rows{static_cast<const T*>(a.x) + n * a.x_seq + c, a.x_tok,
+                 a.state0 ? static_cast<const T*>(a.state0) + n * (K - 1) * C + c : nullptr, C, K};
+    const int* doc = DOC ? a.doc + n * a.doc_seq : nullptr;
+    float w[KW][V], bias[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        bias[v] = a.b ? a.b[c + v] : 0.f;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) w[i][v] = i >= before ? a.w[(long long)(c + v) * K + i - before] : 0.f;
+    }
+    float win[KW][V];                   // slots KW - 1 .. : the rows before the token, the token in the last
+    int id_win[KW];
+#pragma unroll
+    for (int i = 1; i < KW; ++i) {
+        const int t = t0 - KW + i;
+        Raw<T, V> raw{};
+        if (i > before) raw = rows.template at<V>(t);
+        unpack<T, V>(raw, win[i]);
+        if (DOC) id_win[i] = doc[max(t, 0)];
+    }
+    T* y = static_cast<T*>(a.y) + n * a.T * (long long)C + c;
+    for (int t = t0; t < t1; t += kBatch) {
+        Raw<T, V> raw[kBatch];
+        int ids[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (t + j < t1) {
+                raw[j] = load<T, V>(rows.x + (long long)(t + j) * rows.tok);
+                if (DOC) ids[j] = doc[t + j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (t + j >= t1) break;
+#pragma unroll
+            for (int i = 0; i + 1 < KW; ++i) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) win[i][v] = win[i + 1][v];
+                if (DOC) id_win[i] = id_win[i + 1];
+            }
+            unpack<T, V>(raw[j], win[KW - 1]);
+            if (DOC) id_win[KW - 1] = ids[j];
+            float out[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) out[v] = bias[v];
+#pragma unroll
+            for (int i = 0; i < KW; ++i) {
+                const bool in = i >= before && (!DOC || id_win[i] == id_win[KW - 1]);
+#pragma unroll
+                for (int v = 0; v < V; ++v) out[v] = in ? fmaf(w[i][v], win[i][v], out[v]) : out[v];
+            }
+            if (a.silu) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) out[v] *= sigmoid<T>(out[v]);
+            }
+            store<T, V>(y + (long long)(t + j) * C, out);
+        }
+    }
+    if (a.state && part == strips - 1 && K > 1) {
+        T* s = static_cast<T*>(a.state) + n * (K - 1) * C + c;
+#pragma unroll
+        for (int i = 1; i < KW; ++i) {
+            if (i <= before) continue;
+            float f[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = !DOC || id_win[i] == id_win[KW - 1] ? win[i][v] : 0.f;
+            store<T, V>(s + (long long)(i - before - 1) * C, f);
+        }
+    }
+}
+
+// T = 0: the state passes on as it came.
+template <typename T>
+__global__ void conv_pass_kernel(const T* from, T* to, long long n) {
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < n) to[i] = from ? from[i] : T(0.f);
+}
+
+// A thread walks strips of V channels, KW - 1 tokens past each strip's end, and row t - KW + 1 leaves once d_t
+// is known (the d of those tokens are computed twice, their share of dw only by the strip that they are in).  A
+// block is bx threads of neighbouring channels by as many strips as it has threads left.  dw and db are added up
+// in registers over a thread's strips, over the block's threads in shared memory in their order, and leave as
+// one part of the block's row of the grid, joined by conv_join_kernel in the rows' order: equal inputs give
+// equal bits.
+template <typename T, int V, int KW, bool DOC>
+__global__ void __launch_bounds__(kBwdThreads) conv_bwd_kernel(const __grid_constant__ ConvArgs a, int groups,
+                                                                int strips, int strip) {
+    __shared__ float sums[kBwdThreads * V];
+    const int K = a.K, C = a.C, before = KW - K;
+    const int group = blockIdx.x * blockDim.x + threadIdx.x;
+    const bool live = group < groups;
+    const int c = live ? group * V : 0;
+    float w[KW][V], bias[V], dw[KW][V], db[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        bias[v] = a.b ? a.b[c + v] : 0.f;
+        db[v] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+            w[i][v] = i >= before ? a.w[(long long)(c + v) * K + i - before] : 0.f;
+            dw[i][v] = 0.f;
+        }
+    }
+    const long long total = live ? (long long)a.N * strips : 0;
+    for (long long s = (long long)blockIdx.y * blockDim.y + threadIdx.y; s < total;
+         s += (long long)gridDim.y * blockDim.y) {
+        const long long n = s / strips;
+        const int t0 = (int)(s % strips) * strip, t1 = min(a.T, t0 + strip), end = min(a.T, t1 + KW - 1);
+        Rows<T> rows{static_cast<const T*>(a.x) + n * a.x_seq + c, a.x_tok,
+                     a.state0 ? static_cast<const T*>(a.state0) + n * (K - 1) * C + c : nullptr, C, K};
+        const T* dy = static_cast<const T*>(a.dy) + n * a.dy_seq + c;
+        const int* doc = DOC ? a.doc + n * a.doc_seq : nullptr;
+        const int id_last = DOC ? doc[a.T - 1] : 0;
+        T* dx = static_cast<T*>(a.dx) + n * a.T * (long long)C + c;
+        T* ds0 = a.dstate0 ? static_cast<T*>(a.dstate0) + n * (K - 1) * C + c : nullptr;
+        const T* ds = a.dstate ? static_cast<const T*>(a.dstate) + n * (K - 1) * C + c : nullptr;
+        const int first_row = t0 == 0 && ds0 ? -(K - 1) : t0;
+        float win[KW][V], d[KW][V];     // rows t - KW + 1 .. t and their d
+        int id_win[KW];
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+            const int t = t0 - KW + i;
+            Raw<T, V> raw{};
+            if (i > before) raw = rows.template at<V>(t);
+            unpack<T, V>(raw, win[i]);
+            if (DOC) id_win[i] = doc[max(t, 0)];
+#pragma unroll
+            for (int v = 0; v < V; ++v) d[i][v] = 0.f;
+        }
+        for (int t = t0; t < t1 + KW - 1; t += kBatch) {
+            Raw<T, V> raw[kBatch], draw[kBatch];
+            int ids[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (t + j < end) {
+                    raw[j] = load<T, V>(rows.x + (long long)(t + j) * rows.tok);
+                    draw[j] = load<T, V>(dy + (long long)(t + j) * a.dy_tok);
+                    if (DOC) ids[j] = doc[t + j];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int now = t + j, row = now - (KW - 1);
+#pragma unroll
+                for (int i = 0; i + 1 < KW; ++i) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        win[i][v] = win[i + 1][v];
+                        d[i][v] = d[i + 1][v];
+                    }
+                    if (DOC) id_win[i] = id_win[i + 1];
+                }
+                if (now < end) {
+                    unpack<T, V>(raw[j], win[KW - 1]);
+                    unpack<T, V>(draw[j], d[KW - 1]);
+                    if (DOC) id_win[KW - 1] = ids[j];
+                    if (a.silu) {
+                        float pre[V];
+#pragma unroll
+                        for (int v = 0; v < V; ++v) pre[v] = bias[v];
+#pragma unroll
+                        for (int i = 0; i < KW; ++i) {
+                            const bool in = i >= before && (!DOC || id_win[i] == id_win[KW - 1]);
+#pragma unroll
+                            for (int v = 0; v < V; ++v) pre[v] = in ? fmaf(w[i][v], win[i][v], pre[v]) : pre[v];
+                        }
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            const float g = sigmoid<T>(pre[v]);
+                            d[KW - 1][v] *= g * fmaf(pre[v], 1.f - g, 1.f);
+                        }
+                    }
+                    if (now < t1) {
+#pragma unroll
+                        for (int i = 0; i < KW; ++i) {
+                            const bool in = i >= before && (!DOC || id_win[i] == id_win[KW - 1]);
+#pragma unroll
+                            for (int v = 0; v < V; ++v)
+                                dw[i][v] = in ? fmaf(d[KW - 1][v], win[i][v], dw[i][v]) : dw[i][v];
+                        }
+#pragma unroll
+                        for (int v = 0; v < V; ++v) db[v] += d[KW - 1][v];
+                    }
+                } else {                // past the sequence, or past what the strip's rows need
+#pragma unroll
+                    for (int v = 0; v < V; ++v) d[KW - 1][v] = 0.f;
+                    if (DOC) id_win[KW - 1] = id_last;
+                }
+                if (row < first_row || row >= t1) continue;
+                // row + m met row in its tap K - 1 - m, slot KW - 1 - m
+                float out[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) out[v] = 0.f;
+#pragma unroll
+                for (int m = 0; m < KW; ++m) {
+                    const bool in = m < K && (!DOC || id_win[m] == id_win[0]);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) out[v] = in ? fmaf(w[KW - 1 - m][v], d[m][v], out[v]) : out[v];
+                }
+                const int tail = row - (a.T - (K - 1));
+                if (ds && tail >= 0 && (!DOC || id_win[0] == id_last)) {
+                    float f[V];
+                    unpack<T, V>(load<T, V>(ds + (long long)tail * C), f);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) out[v] += f[v];
+                }
+                if (row >= 0) store<T, V>(dx + (long long)row * C, out);
+                else store<T, V>(ds0 + (long long)(row + K - 1) * C, out);
+            }
+        }
+    }
+    if (!a.partial) return;
+    const int bx = blockDim.x, tid = threadIdx.y * bx + threadIdx.x;
+    float* to = a.partial + (size_t)blockIdx.y * (K + 1) * C;
+#pragma unroll
+    for (int q = 0; q <= KW; ++q) {     // tap slots, then db
+        if (q < before) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) sums[tid * V + v] = q < KW ? dw[q < KW ? q : 0][v] : db[v];
+        __syncthreads();
+        for (int i = tid; i < bx * V; i += kBwdThreads) {
+            float total = 0.f;
+            for (int y = 0; y < (int)blockDim.y; ++y) total += sums[y * bx * V + i];
+            const int channel = blockIdx.x * bx * V + i;
+            if (channel < C) to[(size_t)(q - before) * C + channel] = total;
+        }
+        __syncthreads();
+    }
+}
+
+// dw [C][K] and db [C] from the parts [rows][K + 1][C].  32 channels by 8 shares of the rows a block.
+__global__ void __launch_bounds__(256) conv_join_kernel(const float* parts, int rows, int C, int K, float* dw,
+                                                         float* db) {
+    __shared__ float sums[8][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x * 32 + threadIdx.x, q = blockIdx.y;
+    float total = 0.f;
+    if (c < C)
+        for (int r = threadIdx.y; r < rows; r += 8) total += parts[((size_t)r * (K + 1) + q) * C + c];
+    sums[threadIdx.y][threadIdx.x] = total;
+    __syncthreads();
+    if (threadIdx.y != 0 || c >= C) return;
+#pragma unroll
+    for (int y = 1; y < 8; ++y) total += sums[y][threadIdx.x];
+    if (q < K) { if (dw) dw[(size_t)c * K + q] = total; }
+    else if (db) db[c] = total;
+}
+
+// ----------------------------------------------------------------------------- host
+
+// Bytes that V neighbouring values may span: what every row of every tensor starts on.
+int widest(const ConvArgs& a, bool back) {
+    const int es = a.bf16 ? 2 : 4;
+    uint64_t bits = (uint64_t)a.C * es | 16;
+    auto at = [&](const void* p) { bits |= reinterpret_cast<uintptr_t>(p); };
+    auto step = [&](long long elements, bool used) { if (used) bits |= (uint64_t)elements * es; };
+    at(a.x);
+    step(a.x_tok, a.T > 1);
+    step(a.x_seq, a.N > 1);
+    if (back) {
+        at(a.dy);
+        step(a.dy_tok, a.T > 1);
+        step(a.dy_seq, a.N > 1);
+    }
+    return (int)(bits & (~bits + 1));   // every other pointer is 16-byte aligned, its rows C values apart
+}
+
+template <typename T, int V, int KW>
+cudaError_t fwd(const ConvArgs& a, bool one_strip, cudaStream_t s) {
+    const int groups = a.C / V;
+    // Strips as long as leave two waves of threads, 8 to 128 tokens: the rows between strips are read twice.
+    int strip = one_strip ? a.T : 128;
+    while (!one_strip && strip > 8 && (long long)a.N * groups * ((a.T + strip - 1) / strip) < kSms * 2048LL) strip /= 2;
+    const int strips = (a.T + strip - 1) / strip;
+    const long long blocks = ((long long)a.N * groups * strips + kFwdThreads - 1) / kFwdThreads;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (a.doc) conv_fwd_kernel<T, V, KW, true><<<(unsigned)blocks, kFwdThreads, 0, s>>>(a, groups, strips, strip);
+    else conv_fwd_kernel<T, V, KW, false><<<(unsigned)blocks, kFwdThreads, 0, s>>>(a, groups, strips, strip);
+    return cudaGetLastError();
+}
+
+// Rows of the gradient's grid at most, by the widest channel groups that a call may take; the workspace holds
+// a part for each.
+int most_rows(int C) {
+    const int across = ((C + 3) / 4 + 31) / 32;
+    const int rows = kSms * 4 / across;
+    return rows < 1 ? 1 : rows;
+}
+
+template <typename T, int V, int KW>
+cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
+    const int groups = a.C / V;
+    int bx = 1;
+    while (bx < groups && bx < 32) bx *= 2;
+    const int by = kBwdThreads / bx, across = (groups + bx - 1) / bx;
+    int strip = 128;
+    while (strip > 16 && (long long)a.N * ((a.T + strip - 1) / strip) < (long long)by * most_rows(a.C)) strip /= 2;
+    const int strips = (a.T + strip - 1) / strip;
+    const long long wanted = ((long long)a.N * strips + by - 1) / by;
+    const int rows = (int)(wanted < most_rows(a.C) ? wanted : most_rows(a.C));
+    const dim3 grid(across, rows), block(bx, by);
+    if (a.doc) conv_bwd_kernel<T, V, KW, true><<<grid, block, 0, s>>>(a, groups, strips, strip);
+    else conv_bwd_kernel<T, V, KW, false><<<grid, block, 0, s>>>(a, groups, strips, strip);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.partial) return e;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((a.C + 31) / 32, a.K + 1);
+    c.blockDim = dim3(32, 8);
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, conv_join_kernel, (const float*)a.partial, rows, a.C, a.K, a.dw, a.db);
+}
+
+// F<T, V, KW>: as many channels a thread as the rows' alignment and the registers allow.
+#define CONV_BY_WIDTH(F, MOST, KW, bytes, ...)                                             \
+    do {                                                                                   \
+        if (a.bf16) {                                                                      \
+            if constexpr (MOST >= 8) if (bytes >= 16) return F<__nv_bfloat16, 8, KW>(a, ##__VA_ARGS__); \
+            if constexpr (MOST >= 4) if (bytes >= 8) return F<__nv_bfloat16, 4, KW>(a, ##__VA_ARGS__);  \
+            if (bytes >= 4) return F<__nv_bfloat16, 2, KW>(a, ##__VA_ARGS__);              \
+            return F<__nv_bfloat16, 1, KW>(a, ##__VA_ARGS__);                              \
+        }                                                                                  \
+        if constexpr (MOST >= 4) if (bytes >= 16) return F<float, 4, KW>(a, ##__VA_ARGS__); \
+        if (bytes >= 8) return F<float, 2, KW>(a, ##__VA_ARGS__);                          \
+        return F<float, 1, KW>(a, ##__VA_ARGS__);                                          \
+    } while (0)
+
+cudaError_t fwd_any(const ConvArgs& a, bool one_strip, cudaStream_t s) {
+    const int bytes = widest(a, false);
+    if (a.K <= 4) CONV_BY_WIDTH(fwd, 8, 4, bytes, one_strip, s);
+    CONV_BY_WIDTH(fwd, 4, 8, bytes, one_strip, s);
+}
+
+cudaError_t bwd_any(const ConvArgs& a, cudaStream_t s) {
+    const int bytes = widest(a, true);
+    if (a.K <= 4) CONV_BY_WIDTH(bwd, 4, 4, bytes, s);
+    CONV_BY_WIDTH(bwd, 2, 8, bytes, s);
+}
+
+cudaError_t pass_state(const ConvArgs& a, const void* from, void* to, cudaStream_t s) {
+    const long long n = (long long)a.N * (a.K - 1) * a.C;
+    if (!to || n == 0) return cudaSuccess;
+    const unsigned blocks = (unsigned)((n + 255) / 256);
+    if (a.bf16)
+        conv_pass_kernel<<<blocks, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(from), static_cast<__nv_bfloat16*>(to), n);
+    else
+        conv_pass_kernel<<<blocks, 256, 0, s>>>(static_cast<const float*>(from), static_cast<float*>(to), n);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t conv_bwd_workspace_bytes(const ConvArgs& a) {
+    return (size_t)most_rows(a.C) * (a.K + 1) * a.C * 4;
+}
+
+cudaError_t conv_fwd_launch(const ConvArgs& a, cudaStream_t s) {
+    if (a.T == 0) return pass_state(a, a.state0, a.state, s);
+    return fwd_any(a, false, s);
+}
+
+cudaError_t conv_step_launch(const ConvArgs& a, cudaStream_t s) { return fwd_any(a, true, s); }
+
+cudaError_t conv_bwd_launch(const ConvArgs& a, cudaStream_t s, int* launches) {
+    *launches = a.partial ? 2 : 1;
+    if (a.T > 0) return bwd_any(a, s);
+    // no tokens: the state passed on, the sums are empty
+    cudaError_t e = pass_state(a, a.dstate, a.dstate0, s);
+    if (e == cudaSuccess && a.dw) e = cudaMemsetAsync(a.dw, 0, (size_t)a.C * a.K * 4, s);
+    if (e == cudaSuccess && a.db) e = cudaMemsetAsync(a.db, 0, (size_t)a.C * 4, s);
+    return e;
+}
+
+}  // namespace ttm

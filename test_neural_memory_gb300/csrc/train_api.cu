@@ -2,8 +2,11 @@
 // validation and launch.  Declarations and contract are in include/ttm.h.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <new>
+#include <vector>
 
 #include "../../include/ttm.h"
 #include "train_ops.h"
@@ -81,6 +84,84 @@ int glr_common(ttm::GlrArgs& a, int N, int T, int D, int dtype, int gate, const 
     a.x = x; a.x_seq = x_seq; a.x_tok = x_tok;
     a.g = g; a.g_seq = g_seq; a.g_tok = g_tok;
     return TTM_OK;
+}
+
+// What the three convolution calls share, but for the outputs.
+int conv_common(ttm::ConvArgs& a, int N, int T, int C, int K, int dtype, int silu, const void* x, long long x_seq,
+                long long x_tok, const float* w, const float* b, Span& sx) {
+    if (N < 1 || T < 0 || C < 1 || K < 1 || !dtype_ok(dtype) || (silu != 0 && silu != 1)) return TTM_ERR_INVALID_ARG;
+    if (!w || (T > 0 && !x)) return TTM_ERR_INVALID_ARG;
+    const size_t es = dtype == TTM_BF16 ? 2 : 4;
+    if (!aligned(x, es) || !aligned(w, 4) || !aligned(b, 4)) return TTM_ERR_INVALID_ARG;
+    bool ok = true;
+    sx = {x, view_bytes(N, T, C, x_seq, x_tok, es, ok)};
+    if (!ok) return TTM_ERR_INVALID_ARG;
+    if ((long long)N * C > (1LL << 31) - 1 || T > kMostTokens || K > TTM_CONV_MAX_TAPS) return TTM_ERR_UNSUPPORTED;
+    a.N = N; a.T = T; a.C = C; a.K = K;
+    a.bf16 = dtype == TTM_BF16;
+    a.silu = silu;
+    a.x = x; a.x_seq = x_seq; a.x_tok = x_tok;
+    a.w = w; a.b = b;
+    return TTM_OK;
+}
+
+bool doc_ok(const ttm::ConvArgs& a, const int* doc, long long doc_seq, Span& sd) {
+    bool ok = aligned(doc, 4);
+    sd = {doc, doc ? view_bytes(a.N, a.T, 1, doc_seq, 1, 4, ok) : 0};
+    return ok;
+}
+
+// Widths whose products count in 32 bits.
+constexpr int kMostWidth = 1 << 24;
+
+int ffn_common(ttm::FfnArgs& a, int N, int D, int F, int act, const void* x, long long x_row, const void* W_in,
+               const void* W_out, Span& sx) {
+    if (N < 0 || D < 8 || F < 8 || D % 8 || F % 8 || (act != TTM_ACT_SILU && act != TTM_ACT_GELU))
+        return TTM_ERR_INVALID_ARG;
+    if (!W_in || !W_out || (N > 0 && !x) || x_row % 8) return TTM_ERR_INVALID_ARG;
+    if (!all_aligned16<3>({x, W_in, W_out})) return TTM_ERR_INVALID_ARG;
+    bool ok = true;
+    sx = {x, view_bytes(1, N, D, 0, x_row, 2, ok)};
+    if (!ok) return TTM_ERR_INVALID_ARG;
+    if (D >= kMostWidth || F >= kMostWidth / 2 || N > kMostTokens) return TTM_ERR_UNSUPPORTED;
+    a.N = N; a.D = D; a.F = F;
+    a.gelu = act == TTM_ACT_GELU;
+    a.x = x; a.x_row = x_row;
+    a.W_in = W_in; a.W_out = W_out;
+    return TTM_OK;
+}
+
+int ffn_run(ttm::FfnArgs& a, int backward, void* workspace, size_t workspace_bytes, void* stream) {
+    const size_t need = ttm::ffn_workspace_bytes(a.N, a.D, a.F, backward);
+    if (need && (!workspace || workspace_bytes < need)) return TTM_ERR_INVALID_ARG;
+    a.workspace = workspace;
+    a.status = ttm::api_status_ptr();
+    if (!a.status) return TTM_ERR_CUDA;
+    a.wait_cycles = ttm::api_wait_cycles();
+    a.debug_stall = ttm::api_take_stall();
+    int launches = 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = backward ? ttm::ffn_bwd_launch(a, s, &launches) : ttm::ffn_fwd_launch(a, s, &launches);
+    if (e != cudaSuccess) return TTM_ERR_CUDA;
+    ttm::api_note_launches(launches);
+    return TTM_OK;
+}
+
+struct Range {
+    uintptr_t from, to;
+    bool written;
+};
+
+// Whether a written range meets another one.
+bool ranges_clash(std::vector<Range>& r) {
+    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+    uintptr_t any = 0, written = 0;         // ends of the ranges so far
+    for (const Range& x : r) {
+        if (x.from < written || (x.written && x.from < any)) return true;
+        any = std::max(any, x.to);
+        if (x.written) written = std::max(written, x.to);
+    }
+    return false;
 }
 
 int glr_run(ttm::GlrArgs& a, int backward, void* workspace, size_t workspace_bytes, void* stream) {
@@ -280,6 +361,224 @@ int ttm_orthogonalize(int batch, int m, int n, int dtype, const void* G, const f
     if (ttm::ortho_launch(a, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
         return TTM_ERR_CUDA;
     ttm::api_note_launches(launches);
+    return TTM_OK;
+}
+
+
+int ttm_causal_conv_fwd(int N, int T, int C, int K, int dtype, int silu, const void* x, long long x_seq,
+                        long long x_tok, const float* w, const float* b, const void* state0, const int* doc,
+                        long long doc_seq, void* y, void* state, void* stream) {
+    ttm::ConvArgs a{};
+    Span sx, sd;
+    const int r = conv_common(a, N, T, C, K, dtype, silu, x, x_seq, x_tok, w, b, sx);
+    if (r != TTM_OK) return r;
+    if (T > 0 && !y) return TTM_ERR_INVALID_ARG;
+    if (!doc_ok(a, doc, doc_seq, sd) || !all_aligned16<3>({state0, y, state})) return TTM_ERR_INVALID_ARG;
+    const size_t es = a.bf16 ? 2 : 4, nc = (size_t)N * C, st = nc * (K - 1) * es;
+    const Span ins[] = {sx, sd, {w, (size_t)C * K * 4}, {b, (size_t)C * 4}, {state0, st}};
+    const Span outs[] = {{y, nc * T * es}, {state, st}};
+    if (!outputs_clear(ins, outs)) return TTM_ERR_INVALID_ARG;
+    a.state0 = state0; a.doc = T > 0 ? doc : nullptr; a.doc_seq = doc_seq; a.y = y; a.state = state;
+    if (ttm::conv_fwd_launch(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return TTM_ERR_CUDA;
+    ttm::api_note_launches(1);
+    return TTM_OK;
+}
+
+size_t ttm_causal_conv_bwd_workspace_size(int C, int K) {
+    if (C < 1 || K < 1 || K > TTM_CONV_MAX_TAPS) return 0;
+    ttm::ConvArgs a{};
+    a.C = C; a.K = K;
+    return ttm::conv_bwd_workspace_bytes(a);
+}
+
+int ttm_causal_conv_bwd(int N, int T, int C, int K, int dtype, int silu, const void* dy, long long dy_seq,
+                        long long dy_tok, const void* x, long long x_seq, long long x_tok, const float* w,
+                        const float* b, const void* state0, const int* doc, long long doc_seq, const void* dstate,
+                        void* dx, float* dw, float* db, void* dstate0, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    ttm::ConvArgs a{};
+    Span sx, sd;
+    const int r = conv_common(a, N, T, C, K, dtype, silu, x, x_seq, x_tok, w, b, sx);
+    if (r != TTM_OK) return r;
+    const size_t es = a.bf16 ? 2 : 4, nc = (size_t)N * C, st = nc * (K - 1) * es;
+    if ((T > 0 && (!dy || !dx)) || !aligned(dy, es)) return TTM_ERR_INVALID_ARG;
+    if (!doc_ok(a, doc, doc_seq, sd) || !all_aligned16<7>({state0, dstate, dx, dw, db, dstate0, workspace}))
+        return TTM_ERR_INVALID_ARG;
+    bool ok = true;
+    const Span sdy{dy, view_bytes(N, T, C, dy_seq, dy_tok, es, ok)};
+    if (!ok) return TTM_ERR_INVALID_ARG;
+    const bool sums = dw || db;
+    if (sums && (!workspace || workspace_bytes < ttm::conv_bwd_workspace_bytes(a))) return TTM_ERR_INVALID_ARG;
+    const Span ins[] = {sx, sd, sdy, {w, (size_t)C * K * 4}, {b, (size_t)C * 4}, {state0, st}, {dstate, st}};
+    const Span outs[] = {{dx, nc * T * es},
+                         {dw, (size_t)C * K * 4},
+                         {db, (size_t)C * 4},
+                         {dstate0, st},
+                         {workspace, workspace ? workspace_bytes : 0}};
+    if (!outputs_clear(ins, outs)) return TTM_ERR_INVALID_ARG;
+    a.state0 = state0; a.doc = T > 0 ? doc : nullptr; a.doc_seq = doc_seq;
+    a.dy = dy; a.dy_seq = dy_seq; a.dy_tok = dy_tok;
+    a.dstate = dstate; a.dx = dx; a.dw = dw; a.db = db; a.dstate0 = dstate0;
+    a.partial = sums ? static_cast<float*>(workspace) : nullptr;
+    int launches = 0;
+    if (ttm::conv_bwd_launch(a, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess) return TTM_ERR_CUDA;
+    ttm::api_note_launches(launches);
+    return TTM_OK;
+}
+
+int ttm_causal_conv_step(int N, int n, int C, int K, int dtype, int silu, const void* x, long long x_seq,
+                         long long x_tok, const float* w, const float* b, void* state, void* y, void* stream) {
+    ttm::ConvArgs a{};
+    Span sx;
+    if (n < 1) return TTM_ERR_INVALID_ARG;
+    const int r = conv_common(a, N, n, C, K, dtype, silu, x, x_seq, x_tok, w, b, sx);
+    if (r != TTM_OK) return r;
+    if ((K > 1 && !state) || !y || !all_aligned16<2>({state, y})) return TTM_ERR_INVALID_ARG;
+    const size_t es = a.bf16 ? 2 : 4, nc = (size_t)N * C;
+    const Span ins[] = {sx, {w, (size_t)C * K * 4}, {b, (size_t)C * 4}};
+    const Span outs[] = {{state, nc * (K - 1) * es}, {y, nc * n * es}};
+    if (!outputs_clear(ins, outs)) return TTM_ERR_INVALID_ARG;
+    a.state0 = a.state = state;
+    a.y = y;
+    if (ttm::conv_step_launch(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return TTM_ERR_CUDA;
+    ttm::api_note_launches(1);
+    return TTM_OK;
+}
+
+size_t ttm_gated_ffn_workspace_size(int N, int D, int F, int backward) {
+    if (N < 1 || D < 8 || F < 8 || D % 8 || F % 8 || D >= kMostWidth || F >= kMostWidth / 2 || N > kMostTokens) return 0;
+    return ttm::ffn_workspace_bytes(N, D, F, backward != 0);
+}
+
+int ttm_gated_ffn_fwd(int N, int D, int F, int act, const void* x, long long x_row, const void* W_in,
+                      const void* W_out, const void* residual, long long residual_row, void* y, void* gu,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    ttm::FfnArgs a{};
+    Span sx;
+    const int r = ffn_common(a, N, D, F, act, x, x_row, W_in, W_out, sx);
+    if (r != TTM_OK) return r;
+    if ((N > 0 && !y) || !all_aligned16<4>({residual, y, gu, workspace})) return TTM_ERR_INVALID_ARG;
+    bool ok = !residual || residual_row % 8 == 0;
+    const Span sr{residual, residual ? view_bytes(1, N, D, 0, residual_row, 2, ok) : 0};
+    if (!ok) return TTM_ERR_INVALID_ARG;
+    const size_t df = (size_t)D * F, n = N;
+    const Span ins[] = {sx, sr, {W_in, df * 4}, {W_out, df * 2}};
+    const Span outs[] = {{y, n * D * 2}, {gu, n * F * 4}, {workspace, workspace ? workspace_bytes : 0}};
+    if (!outputs_clear(ins, outs)) return TTM_ERR_INVALID_ARG;
+    if (N == 0) return TTM_OK;
+    a.residual = residual; a.residual_row = residual_row;
+    a.y = y; a.gu = gu;
+    return ffn_run(a, 0, workspace, workspace_bytes, stream);
+}
+
+int ttm_gated_ffn_bwd(int N, int D, int F, int act, const void* dy, long long dy_row, const void* x, long long x_row,
+                      const void* gu, const void* W_in, const void* W_out, void* dx, void* dW_in, void* dW_out,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    ttm::FfnArgs a{};
+    Span sx;
+    const int r = ffn_common(a, N, D, F, act, x, x_row, W_in, W_out, sx);
+    if (r != TTM_OK) return r;
+    if ((N > 0 && (!dy || !gu)) || dy_row % 8) return TTM_ERR_INVALID_ARG;
+    if (!all_aligned16<6>({dy, gu, dx, dW_in, dW_out, workspace})) return TTM_ERR_INVALID_ARG;
+    bool ok = true;
+    const Span sdy{dy, view_bytes(1, N, D, 0, dy_row, 2, ok)};
+    if (!ok) return TTM_ERR_INVALID_ARG;
+    const size_t df = (size_t)D * F, n = N;
+    const Span ins[] = {sx, sdy, {gu, n * F * 4}, {W_in, df * 4}, {W_out, df * 2}};
+    const Span outs[] = {{dx, n * D * 2}, {dW_in, df * 4}, {dW_out, df * 2}, {workspace, workspace ? workspace_bytes : 0}};
+    if (!outputs_clear(ins, outs)) return TTM_ERR_INVALID_ARG;
+    if (N == 0) {
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        if (dW_in && cudaMemsetAsync(dW_in, 0, df * 4, s) != cudaSuccess) return TTM_ERR_CUDA;
+        if (dW_out && cudaMemsetAsync(dW_out, 0, df * 2, s) != cudaSuccess) return TTM_ERR_CUDA;
+        return TTM_OK;
+    }
+    a.dy = dy; a.dy_row = dy_row;
+    a.gu = const_cast<void*>(gu);
+    a.dx = dx; a.dW_in = dW_in; a.dW_out = dW_out;
+    return ffn_run(a, 1, workspace, workspace_bytes, stream);
+}
+
+int ttm_adamw_step(int count, const ttm_adamw_tensor* tensors, int bits, void* m, void* v, float* m_scale,
+                   float* v_scale, int* step, double lr, const float* lr_at, double beta1, double beta2, double eps,
+                   double weight_decay, const float* grad_scale, void* stream) {
+    if (count < 0 || (count > 0 && !tensors) || (bits != 8 && bits != 32) || !step) return TTM_ERR_INVALID_ARG;
+    if (!(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0) || !((float)eps > 0.f) || !std::isfinite(eps) ||
+        !std::isfinite(lr) || !std::isfinite(weight_decay))
+        return TTM_ERR_INVALID_ARG;
+    if ((bits == 8) != (m_scale != nullptr) || (bits == 8) != (v_scale != nullptr)) return TTM_ERR_INVALID_ARG;
+    if (!all_aligned16<4>({m, v, m_scale, v_scale}) || !aligned(step, 4) || !aligned(lr_at, 4) || !aligned(grad_scale, 4))
+        return TTM_ERR_INVALID_ARG;
+    try {
+        std::vector<ttm::AdamwEntry> list;
+        std::vector<Range> ranges;
+        list.reserve(count);
+        ranges.reserve(3 * (size_t)count + 7);
+        auto range = [&](const void* p, size_t bytes, bool written) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+            if (p && bytes) ranges.push_back({at, at + bytes, written});
+        };
+        long long blocks = 0;
+        for (int i = 0; i < count; ++i) {
+            const ttm_adamw_tensor& t = tensors[i];
+            if (t.n < 0 || t.n > (1LL << 48) || !dtype_ok(t.param_dtype)) return TTM_ERR_INVALID_ARG;
+            const long long first = blocks;
+            blocks += (t.n + 255) / 256;
+            if (blocks > (1LL << 48)) return TTM_ERR_INVALID_ARG;
+            if (!t.grad || t.n == 0) continue;
+            const int pb = t.param_dtype == TTM_BF16, gb = t.grad_dtype == TTM_BF16;
+            if (!t.param || !dtype_ok(t.grad_dtype) || !aligned(t.param, pb ? 2 : 4) || !aligned(t.grad, gb ? 2 : 4) ||
+                !aligned(t.copy, 2))
+                return TTM_ERR_INVALID_ARG;
+            range(t.param, (size_t)t.n * (pb ? 2 : 4), true);
+            range(t.grad, (size_t)t.n * (gb ? 2 : 4), false);
+            range(t.copy, (size_t)t.n * 2, true);
+            list.push_back({t.param, t.grad, t.copy, t.n, first, 0, pb, gb});
+        }
+        if (blocks && (!m || !v)) return TTM_ERR_INVALID_ARG;
+        const size_t held = (size_t)blocks * 256 * (bits / 8);
+        range(m, held, true);
+        range(v, held, true);
+        range(m_scale, (size_t)blocks * 4, true);
+        range(v_scale, (size_t)blocks * 4, true);
+        range(step, 8, true);
+        range(lr_at, 4, false);
+        range(grad_scale, 4, false);
+        if (ranges_clash(ranges)) return TTM_ERR_INVALID_ARG;
+        ttm::AdamwScalars a{};
+        a.m = m; a.v = v; a.m_scale = m_scale; a.v_scale = v_scale; a.step = step;
+        a.lr = (float)lr; a.lr_at = lr_at;
+        a.b1 = (float)beta1; a.b2 = (float)beta2;
+        a.c1 = (float)(1.0 - beta1); a.c2 = (float)(1.0 - beta2);
+        a.log_b1 = (float)std::log(beta1); a.log_b2 = (float)std::log(beta2);
+        a.eps = (float)eps; a.decay = (float)weight_decay;
+        a.grad_scale = grad_scale;
+        int launches = 0;
+        if (ttm::adamw_step_launch(list.data(), (int)list.size(), a, static_cast<cudaStream_t>(stream), &launches) !=
+            cudaSuccess)
+            return TTM_ERR_CUDA;
+        ttm::api_note_launches(launches);
+    } catch (const std::bad_alloc&) {
+        return TTM_ERR_CUDA;
+    }
+    return TTM_OK;
+}
+
+int ttm_adamw_moments(long long blocks, const void* m, const void* v, const float* m_scale, const float* v_scale,
+                      float* m_out, float* v_out, void* stream) {
+    if (blocks < 0 || blocks > (1LL << 48)) return TTM_ERR_INVALID_ARG;
+    if (blocks && (!m || !v || !m_scale || !v_scale || !m_out || !v_out)) return TTM_ERR_INVALID_ARG;
+    if (!all_aligned16<6>({m, v, m_scale, v_scale, m_out, v_out})) return TTM_ERR_INVALID_ARG;
+    const size_t n = (size_t)blocks * 256;
+    const Span ins[] = {{m, n}, {v, n}, {m_scale, (size_t)blocks * 4}, {v_scale, (size_t)blocks * 4}};
+    const Span outs[] = {{m_out, n * 4}, {v_out, n * 4}};
+    if (!outputs_clear(ins, outs)) return TTM_ERR_INVALID_ARG;
+    ttm::AdamwScalars a{};
+    a.m = const_cast<void*>(m); a.v = const_cast<void*>(v);
+    a.m_scale = const_cast<float*>(m_scale); a.v_scale = const_cast<float*>(v_scale);
+    if (ttm::adamw_moments_launch(blocks, a, m_out, v_out, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return TTM_ERR_CUDA;
+    ttm::api_note_launches(blocks > 0);
     return TTM_OK;
 }
 

@@ -1,5 +1,6 @@
 // Internal interface of the operators around the memory scan (gated linear
-// recurrence, layer norm, orthogonalised update): argument blocks that
+// recurrence, layer norm, orthogonalised update, short convolution, gated feed-forward block,
+// AdamW): argument blocks that
 // train_api.cu has validated, and the launchers of their translation units.
 #pragma once
 
@@ -82,6 +83,81 @@ struct OrthoArgs {
 
 size_t ortho_workspace_bytes(int batch, int m, int n);
 cudaError_t ortho_launch(const OrthoArgs& a, cudaStream_t s, int* launches);
+
+// Short causal convolution (causal_conv.cu), depthwise, with an optional SiLU.  Strides in elements;
+// channels are contiguous.
+struct ConvArgs {
+    int N, T, C, K;
+    int bf16;                       // type of x, y, dy, dx and the states
+    int silu;
+    const void* x;                  // [N][T][C]
+    long long x_seq, x_tok;
+    const float *w, *b;             // [C][K], [C] or NULL (0)
+    const void* state0;             // [N][K-1][C] or NULL (0)
+    const int* doc;                 // [N][T], doc_seq apart, or NULL
+    long long doc_seq;
+    void* y;                        // forward, step: [N][T][C]
+    void* state;                    // forward, step: [N][K-1][C] or NULL; may be state0 in a step
+    const void* dy;                 // gradient
+    long long dy_seq, dy_tok;
+    const void* dstate;             // [N][K-1][C] or NULL (0)
+    void *dx, *dstate0;             // [N][T][C]; [N][K-1][C] or NULL
+    float *dw, *db;                 // [C][K], [C] or NULL
+    float* partial;                 // workspace, NULL when neither dw nor db is wanted
+};
+
+size_t conv_bwd_workspace_bytes(const ConvArgs& a);
+cudaError_t conv_fwd_launch(const ConvArgs& a, cudaStream_t s);
+cudaError_t conv_step_launch(const ConvArgs& a, cudaStream_t s);
+cudaError_t conv_bwd_launch(const ConvArgs& a, cudaStream_t s, int* launches);
+
+// AdamW step over many tensors (adamw.cu).  The moments of tensor i lie from value 256 first on.
+struct AdamwEntry {
+    void* p;
+    const void* g;
+    void* copy;                     // bf16, or NULL
+    long long n;
+    long long first;                // block of 256 values
+    int chunk;                      // chunks of the tensors before it in the same launch
+    int p_bf16, g_bf16;
+};
+struct AdamwScalars {
+    void *m, *v;
+    float *m_scale, *v_scale;       // 8 bits, else NULL
+    int* step;                      // steps done, blocks done
+    float lr;
+    const float* lr_at;             // or NULL
+    float b1, b2, c1, c2;           // betas and one minus each
+    float log_b1, log_b2;
+    float eps, decay;
+    const float* grad_scale;        // or NULL
+};
+cudaError_t adamw_step_launch(const AdamwEntry* tensors, int count, const AdamwScalars& a, cudaStream_t s,
+                              int* launches);
+cudaError_t adamw_moments_launch(long long blocks, const AdamwScalars& a, float* m, float* v, cudaStream_t s);
+
+// Gated feed-forward block (gated_ffn.cu).  bf16; row strides in elements.
+struct FfnArgs {
+    int N, D, F;
+    int gelu;                       // 0: SiLU
+    const void* x;                  // [N][D]
+    long long x_row;
+    const void *W_in, *W_out;       // [D][2F], [F][D]
+    const void* residual;           // [N][D] or NULL
+    long long residual_row;
+    void* y;                        // forward: [N][D]
+    void* gu;                       // [N][2F]: written (forward, NULL to skip), read (gradient)
+    const void* dy;                 // gradient: [N][D]
+    long long dy_row;
+    void *dx, *dW_in, *dW_out;      // gradient; each may be NULL
+    void* workspace;
+    int* status;
+    long long wait_cycles;
+    int debug_stall;                // test hook: stage + 1 that never fills; 0: none
+};
+size_t ffn_workspace_bytes(int N, int D, int F, int backward);
+cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches);
+cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches);
 
 // Tensor map (a CUtensorMap) of a 3-D view: dims from the innermost on, byte strides of
 // the outer two (multiples of 16, below 2^40, the second a multiple of the first), a box of at most
