@@ -1,99 +1,436 @@
-// Gated feed-forward block: g | u = x W_in, h = act(g) u, y = h W_out (+ residual), and its gradient.
-// Plain tiles on the CUDA cores: 64 x 64 results a block, 4 x 4 a thread, 16 of K at a time.
+// Gated feed-forward block: g | u = x W_in, h = act(g) u, y = h W_out (+ residual), and its gradient
+//   dh = dy W_out^T,  dg = dh u act'(g),  du = dh act(g),  dx = [dg | du] W_in^T,
+//   dW_in = x^T [dg | du],  dW_out = h^T dy.
+// Bound by the tensor cores: 6 N D F operations forward, 12 N D F in the gradient, on bf16 operands with fp32 sums.
+//
+// Products (ffn_gemm_kernel): tiles of 256 x 256 by two blocks (a cluster), M = 256 on tcgen05, K in blocks of
+// 64.  Each block copies in 128 rows of A and 128 of B, one issues products over both, each keeps its rows' sums
+// in tensor memory, in two sets, so that one tile's epilogue runs beside the next one's products.  Every operand is
+// read as it lies in memory (rows of K, or K as rows: the transposes of the formulas cost nothing).
+//   kGated:     B is 128 columns of W_g beside the same 128 of W_u, one from each block, so that a thread of the
+//               epilogue has g and u of the same place; out go h and, if wanted, g and u
+//   kStore:     y (+ residual), dx, dW_in, dW_out
+//   kGatedBack: dh stays in tensor memory; g and u come in by tensor copies, dg, du and h leave
+// The epilogue takes 32 rows by 32 columns a warp at a time through shared memory (rows of 64 bytes, 64-byte
+// swizzle: free of conflicts), in and out by tensor copies, which also cut what lies outside the matrices.
+//
+// Roundings: g and u enter the activation in fp32; h, dg and du are rounded to bf16 once, as operands of the next
+// product (half a step, 2^-8 of a value at most: the same as rounding the result, and what the tensor cores
+// take); sums are fp32 throughout.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
+#include "../../include/ttm.h"
+#include "tc_pair.cuh"
+#include "tc_ptx.cuh"
 #include "train_ops.h"
 
 namespace ttm {
 namespace {
 
+using namespace tc;
 using bf16 = __nv_bfloat16;
 
-// Element (row, k) of A at row * rs + k * ks.
-struct Operand {
-    const bf16* p;
-    long long rs, ks;
-};
+constexpr long long kWaitCycles = 4000000000LL;   // default limit, ~2 s at 2 GHz
+constexpr int kPairs = 76;                        // pairs of the 152 SMs
 
-__device__ __forceinline__ float act_of(float g, int gelu, float& slope) {
+__device__ __forceinline__ uint32_t bf162_bits(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(bf162_bits(f[0], f[1]), bf162_bits(f[2], f[3]), bf162_bits(f[4], f[5]), bf162_bits(f[6], f[7]));
+}
+
+// ------------------------------------------------------------------------ activation
+
+// The normal distribution's upper tail: erfc(z) for z >= 0 by the Chebyshev fit in "Numerical Recipes" (erfcc),
+// 1.2e-7 of itself anywhere; bf16 results, so the fast exponential and division do.
+__device__ __forceinline__ float erfc_tail(float z) {
+    const float t = __fdividef(1.f, fmaf(0.5f, z, 1.f));
+    float p = 0.17087277f;
+    p = fmaf(p, t, -0.82215223f);
+    p = fmaf(p, t, 1.48851587f);
+    p = fmaf(p, t, -1.13520398f);
+    p = fmaf(p, t, 0.27886807f);
+    p = fmaf(p, t, -0.18628806f);
+    p = fmaf(p, t, 0.09678418f);
+    p = fmaf(p, t, 0.37409196f);
+    p = fmaf(p, t, 1.00002368f);
+    return t * __expf(fmaf(p, t, fmaf(-z, z, -1.26551223f)));
+}
+
+// act(g) and, where kSlope, its derivative.
+template <bool kSlope>
+__device__ __forceinline__ float act(float g, int gelu, float& slope) {
     if (gelu) {
-        const float c = 0.5f * erfcf(-0.70710678f * g);
-        slope = c + g * 0.39894228f * expf(-0.5f * g * g);
+        const float z = fminf(fabsf(g) * 0.70710678f, 16.f);         // erfc(16) is below the smallest number
+        const float tail = 0.5f * erfc_tail(z), c = g < 0.f ? tail : 1.f - tail;
+        if (kSlope) slope = fmaf(g * 0.39894228f, __expf(-z * z), c);
         return g * c;
     }
-    const float s = 1.f / (1.f + expf(-g));
-    slope = s * fmaf(g, 1.f - s, 1.f);
+    const float s = __fdividef(1.f, 1.f + __expf(-g));
+    if (kSlope) slope = s * fmaf(g, 1.f - s, 1.f);
     return g * s;
 }
 
-enum { kStore, kGated, kGatedBack };
+// -------------------------------------------------------------------------- products
 
-struct Epilogue {
-    bf16* out;                          // [M][N]
-    const bf16* add;
-    long long add_row;
-    bf16 *h, *gu;                       // kGated: results [M][F], [M][2F]; kGatedBack: gu read, out = dgu
-    int F, gelu;
+enum { kStore, kGated, kGatedBack };
+constexpr int kBM = 128, kBK = 64, kTile = 256, kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
+constexpr uint32_t kOperand = kBM * kBK * 2, kStageBytes = 2 * kOperand;      // of a block: 128 rows of A, 128 of B
+constexpr uint32_t kPiece = 32 * 32 * 2;                                      // 32 rows x 32 columns
+// Pieces of a warp: results (kStore: two turns), kGated h, g, u; kGatedBack dg over g, du over u, h, two turns.
+template <int MODE> constexpr int kPieces = MODE == kStore ? 2 : MODE == kGated ? 3 : 6;
+template <int MODE> constexpr int kStages = MODE == kGatedBack ? 4 : 5;
+template <int MODE> constexpr uint32_t kEpiBytes = kEpiWarps * kPieces<MODE> * kPiece;
+constexpr int kRowGroup = 8;            // row tiles that share their way through the columns
+
+struct Problem {                        // one product
+    int M, N, K;                        // kGated: N = F
+    int tiles_m, tiles;
+    int add;                            // kStore: a residual is added
+};
+struct Maps {
+    CUtensorMap a, b, out, aux, h;      // aux: the residual, or gu; kGated: out is h
+};
+struct GemmParams {
+    Problem q[2];
+    int tiles;
+    int gelu, save;                     // save: kGated writes g and u
+    int* status;
+    long long limit;
+    int debug_stall;                    // stage (modulo their number) + 1 that never fills; 0: none
+};
+struct GemmShared {
+    uint64_t full[5], empty[5], acc_full[2], acc_empty[2], landed[kEpiWarps][2];
+    uint32_t tmem;
+    int abort;
+};
+template <int MODE> constexpr int kSmem = 1024 + kStages<MODE> * kStageBytes + kEpiBytes<MODE> + sizeof(GemmShared);
+
+struct TileAt {
+    int row, col, which;
 };
 
+// Tiles go through kRowGroup row tiles at a time, column by column, so that the tiles at work share rows of A and
+// the columns of B come round while they are in the L2 cache.
 template <int MODE>
-__global__ void __launch_bounds__(256) gemm_kernel(Operand A, Operand B, int M, int N, int K, Epilogue e) {
-    __shared__ float sa[16][65], sb[2][16][65];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int row0 = blockIdx.y * 64, col0 = blockIdx.x * 64;
-    constexpr int kTwo = MODE == kGated ? 2 : 1;
-    float acc[kTwo][4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += 16) {
-        for (int i = threadIdx.x; i < 1024; i += 256) {
-            const int r = i >> 4, k = i & 15;
-            sa[k][r] = row0 + r < M && k0 + k < K ? __bfloat162float(A.p[(row0 + r) * A.rs + (k0 + k) * A.ks]) : 0.f;
-            for (int t = 0; t < kTwo; ++t)
-                sb[t][k][r] = col0 + r < N && k0 + k < K
-                                  ? __bfloat162float(B.p[(col0 + r + (long long)t * e.F) * B.rs + (k0 + k) * B.ks])
-                                  : 0.f;
-        }
-        __syncthreads();
-        for (int k = 0; k < 16; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j)
-                    for (int t = 0; t < kTwo; ++t)
-                        acc[t][i][j] = fmaf(sa[k][ty + 16 * i], sb[t][k][tx + 16 * j], acc[t][i][j]);
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const long long r = row0 + ty + 16 * i;
-            const int c = col0 + tx + 16 * j;
-            if (r >= M || c >= N) continue;
-            float slope;
-            if (MODE == kStore) {
-                float v = acc[0][i][j];
-                if (e.add) v += __bfloat162float(e.add[r * e.add_row + c]);
-                e.out[r * N + c] = __float2bfloat16_rn(v);
-            } else if (MODE == kGated) {
-                const float g = acc[0][i][j], u = acc[kTwo - 1][i][j];
-                e.h[r * e.F + c] = __float2bfloat16_rn(act_of(g, e.gelu, slope) * u);
-                if (e.gu) {
-                    e.gu[r * 2 * e.F + c] = __float2bfloat16_rn(g);
-                    e.gu[r * 2 * e.F + e.F + c] = __float2bfloat16_rn(u);
-                }
-            } else {
-                const float dh = acc[0][i][j], g = __bfloat162float(e.gu[r * 2 * e.F + c]),
-                            u = __bfloat162float(e.gu[r * 2 * e.F + e.F + c]), a = act_of(g, e.gelu, slope);
-                e.h[r * e.F + c] = __float2bfloat16_rn(a * u);
-                e.out[r * 2 * e.F + c] = __float2bfloat16_rn(dh * u * slope);
-                e.out[r * 2 * e.F + e.F + c] = __float2bfloat16_rn(dh * a);
-            }
-        }
+__device__ __forceinline__ TileAt tile_at(const GemmParams& p, int t) {
+    TileAt at;
+    at.which = t >= p.q[0].tiles;
+    if (at.which) t -= p.q[0].tiles;
+    const Problem& q = p.q[at.which];
+    const int tiles_n = q.tiles / q.tiles_m, group = t / (kRowGroup * tiles_n), first = group * kRowGroup;
+    const int rows = min(kRowGroup, q.tiles_m - first), r = t - group * kRowGroup * tiles_n;
+    at.row = (first + r % rows) * kTile;
+    at.col = r / rows * (MODE == kGated ? kTile / 2 : kTile);
+    return at;
 }
 
-template <int MODE>
-cudaError_t gemm(Operand A, Operand B, int M, int N, int K, const Epilogue& e, cudaStream_t s) {
-    gemm_kernel<MODE><<<dim3((N + 63) / 64, (M + 63) / 64), 256, 0, s>>>(A, B, M, N, K, e);
-    return cudaGetLastError();
+// 16 bytes j of row r of a piece.
+__device__ __forceinline__ uint4* piece_at(unsigned char* piece, int r, int j) {
+    return reinterpret_cast<uint4*>(piece + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ void load_sums(uint32_t at, float (&v)[32]) {
+    tmem_ld16(at, *reinterpret_cast<float(*)[16]>(v));
+    tmem_ld16(at + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+}
+
+template <bool AMN, bool BMN, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    ffn_gemm_kernel(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
+                    const __grid_constant__ GemmParams p) {
+    constexpr int kS = kStages<MODE>;
+    extern __shared__ unsigned char raw[];
+    unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    unsigned char* epi = base + kS * kStageBytes;
+    GemmShared& S = *reinterpret_cast<GemmShared*>(epi + kEpiBytes<MODE>);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int first = blockIdx.x / 2, stride = gridDim.x / 2;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kS; ++i) {
+            // (in a test of the waits one stage expects an arrival that does not come)
+            mbar_init(&S.full[i], p.debug_stall && (p.debug_stall - 1) % kS == i ? 2 : 1);
+            mbar_init(&S.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.acc_full[i], 1);
+            mbar_init(&S.acc_empty[i], 2 * kEpiWarps);
+        }
+        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&S.landed[i / 2][i % 2], 1);
+        fence_mbar_init();
+        S.abort = 0;
+    }
+    if (warp == 1) alloc_columns<2>(&S.tmem, 2 * kTile);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                     // both blocks' barriers are set up
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    after_previous();
+
+    if (warp == 0 && lane == 0) {
+        int it = 0;
+        bool ok = true;
+        for (int t = first; t < p.tiles && ok; t += stride) {
+            const TileAt at = tile_at<MODE>(p, t);
+            const CUtensorMap *ma = at.which ? &m1.a : &m0.a, *mb = at.which ? &m1.b : &m0.b;
+            const int kblocks = (p.q[at.which].K + kBK - 1) / kBK;
+            const int row = at.row + rank * kBM, col = MODE == kGated ? at.col : at.col + rank * (kTile / 2);
+            for (int k = 0; k < kblocks; ++k, ++it) {
+                const int s = it % kS;
+                ok = wait_one(&S.empty[s], ((it / kS) & 1) ^ 1, &S.abort, p.status, p.limit);
+                if (!ok) break;
+                unsigned char *da = base + s * kStageBytes, *db = da + kOperand;
+                if (rank == 0) mbar_expect_tx(&S.full[s], 2 * kStageBytes);
+                const uint32_t bar = peer_addr(&S.full[s], 0);
+                if (AMN) {
+                    for (int i = 0; i < 2; ++i) tma_load_3d_pair(da + i * 8192, ma, bar, row + 64 * i, k * kBK, 0);
+                } else {
+                    tma_load_3d_pair(da, ma, bar, k * kBK, row, 0);
+                }
+                if (MODE == kGated) {                   // W_in as [D][2][F]: one block W_g, the other W_u
+                    for (int i = 0; i < 2; ++i) tma_load_3d_pair(db + i * 8192, mb, bar, col + 64 * i, rank, k * kBK);
+                } else if (BMN) {
+                    for (int i = 0; i < 2; ++i) tma_load_3d_pair(db + i * 8192, mb, bar, col + 64 * i, k * kBK, 0);
+                } else {
+                    tma_load_3d_pair(db, mb, bar, k * kBK, col, 0);
+                }
+            }
+        }
+        if (*(volatile int*)&S.abort && rank == 0)      // copies still in flight
+            for (int i = max(0, it - kS); i < it; ++i) drain(&S.full[i % kS], (i / kS) & 1, p.limit);
+    } else if (warp == 1 && rank == 0) {
+        // The whole warp walks the loop, so that descriptors stay in uniform registers, and one elected lane issues.
+        constexpr uint32_t step_a = (AMN ? 2048 : 32) >> 4, step_b = (BMN ? 2048 : 32) >> 4;
+        constexpr uint32_t id = idesc_bf16_f32(kTile, kTile, AMN, BMN);
+        const uint32_t base_u = __shfl_sync(0xffffffffu, smem_u32(base), 0);
+        const uint64_t a0 = AMN ? sdesc(base_u, 8192, 1024, 2) : sdesc(base_u, 16, 1024, 2);
+        const uint64_t b0 = BMN ? sdesc(base_u + kOperand, 8192, 1024, 2) : sdesc(base_u + kOperand, 16, 1024, 2);
+        int s = 0, n = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = first; t < p.tiles && ok; t += stride, ++n) {
+            const int acc = n & 1;
+            ok = wait_warp(&S.acc_empty[acc], ((n >> 1) & 1) ^ 1, &S.abort, p.status, p.limit);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem + acc * kTile;
+            const int kblocks = (p.q[t >= p.q[0].tiles].K + kBK - 1) / kBK;
+            for (int k = 0; k < kblocks; ++k) {
+                ok = wait_warp(&S.full[s], phase, &S.abort, p.status, p.limit);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t da = a0 + s * (kStageBytes >> 4), db = b0 + s * (kStageBytes >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        mma_pair(d, da + kk * step_a, db + kk * step_b, id, k > 0 || kk > 0);
+                    commit_pair(&S.empty[s]);
+                    if (k + 1 == kblocks) commit_pair(&S.acc_full[acc]);
+                }
+                __syncwarp();
+                if (++s == kS) { s = 0; phase ^= 1; }
+            }
+        }
+        // after an abort: products still in flight (the commit of the stage before s)
+        if (*(volatile int*)&S.abort && lane == 0 && (s > 0 || phase))
+            drain(&S.empty[s ? s - 1 : kS - 1], s ? phase : phase ^ 1, p.limit);
+    } else if (warp >= 2) {
+        const int part = warp & 3;                      // this warp's lanes of tensor memory
+        const int team = (warp - 2) >> 2;               // takes every other piece
+        unsigned char* mine = epi + (warp - 2) * kPieces<MODE> * kPiece;
+        uint64_t* landed = S.landed[warp - 2];
+        int n = 0, turn = 0;
+        uint32_t asked = 0, seen = 0;                   // copies into this warp's pieces, on one barrier and the other
+        bool ok = true;
+        for (int t = first; t < p.tiles && ok; t += stride, ++n) {
+            const TileAt at = tile_at<MODE>(p, t);
+            const Problem& q = p.q[at.which];
+            const Maps& m = at.which ? m1 : m0;
+            const int acc = n & 1, row0 = at.row + rank * kBM + part * 32;
+            const int width = MODE == kGated ? kTile / 2 : kTile;
+            const int pieces = row0 < q.M ? min(width, q.N - at.col + 31) / 32 : 0;     // that hold a result
+            const bool loads = MODE == kGatedBack || (MODE == kStore && q.add);
+            auto fetch = [&](int c) {                   // what piece c takes, into one place and the other
+                if (lane == 0) {
+                    bulk_wait_read<0>();                // the results that lay there have left
+                    unsigned char* to = mine + (asked & 1) * (MODE == kGatedBack ? 3 : 1) * kPiece;
+                    uint64_t* bar = &landed[asked & 1];
+                    const int x = at.col + 32 * c;
+                    mbar_expect_tx(bar, MODE == kGatedBack ? 2 * kPiece : kPiece);
+                    tma_load_3d(to, &m.aux, bar, x, MODE == kGatedBack ? 0 : row0, MODE == kGatedBack ? row0 : 0);
+                    if (MODE == kGatedBack) tma_load_3d(to + kPiece, &m.aux, bar, x, 1, row0);
+                }
+                ++asked;
+            };
+            if (loads && team < pieces) fetch(team);
+            ok = wait_warp(&S.acc_full[acc], (n >> 1) & 1, &S.abort, p.status, p.limit);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sums = tmem_addr(tmem, part * 32, acc * kTile);
+            for (int c = team; c < pieces; c += 2, ++turn) {
+                const int x = at.col + 32 * c;
+                unsigned char* to = mine + (MODE == kGated ? 0 : (turn & 1) * (MODE == kGatedBack ? 3 : 1)) * kPiece;
+                float v[32];
+                load_sums(sums + 32 * c, v);
+                float up[MODE == kGated ? 32 : 1];
+                if constexpr (MODE == kGated) load_sums(sums + kTile / 2 + 32 * c, up);
+                tmem_wait_ld();
+                if (loads) {
+                    if (c + 2 < pieces) fetch(c + 2);
+                    ok = wait_warp(&landed[seen & 1], (seen >> 1) & 1, &S.abort, p.status, p.limit);
+                    if (!ok) break;
+                    ++seen;
+                } else {
+                    if (lane == 0) {
+                        if (MODE == kStore) bulk_wait_read<1>();
+                        else bulk_wait_read<0>();
+                    }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float (&f)[8] = *reinterpret_cast<float(*)[8]>(v + 8 * j);
+                    uint4* a0 = piece_at(to, lane, j);
+                    if constexpr (MODE == kStore) {
+                        if (loads) {
+                            float r[8];
+                            unpack8(*a0, r);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) f[i] += r[i];
+                        }
+                        *a0 = pack8(f);
+                    } else if constexpr (MODE == kGated) {
+                        float (&u)[8] = *reinterpret_cast<float(*)[8]>(up + 8 * j);
+                        if (p.save) {
+                            *piece_at(to + kPiece, lane, j) = pack8(f);
+                            *piece_at(to + 2 * kPiece, lane, j) = pack8(u);
+                        }
+                        float unused;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = act<false>(f[i], p.gelu, unused) * u[i];
+                        *a0 = pack8(f);
+                    } else {
+                        uint4 *a1 = piece_at(to + kPiece, lane, j), *a2 = piece_at(to + 2 * kPiece, lane, j);
+                        float g[8], u[8], h[8];
+                        unpack8(*a0, g);
+                        unpack8(*a1, u);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float slope;
+                            const float a = act<true>(g[i], p.gelu, slope);
+                            h[i] = a * u[i];
+                            g[i] = f[i] * u[i] * slope;
+                            u[i] = f[i] * a;
+                        }
+                        *a0 = pack8(g);
+                        *a1 = pack8(u);
+                        *a2 = pack8(h);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (MODE == kStore) {
+                        tma_store_3d(&m.out, to, x, row0, 0);
+                    } else if constexpr (MODE == kGated) {
+                        tma_store_3d(&m.out, to, x, row0, 0);
+                        if (p.save) {
+                            tma_store_3d(&m.aux, to + kPiece, x, 0, row0);
+                            tma_store_3d(&m.aux, to + 2 * kPiece, x, 1, row0);
+                        }
+                    } else {
+                        tma_store_3d(&m.out, to, x, 0, row0);
+                        tma_store_3d(&m.out, to + kPiece, x, 1, row0);
+                        tma_store_3d(&m.h, to + 2 * kPiece, x, row0, 0);
+                    }
+                    bulk_commit();
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(peer_addr(&S.acc_empty[acc], 0));
+        }
+        if (lane == 0) {
+            for (; seen != asked; ++seen) drain(&landed[seen & 1], (seen >> 1) & 1, p.limit);     // after an abort
+            bulk_wait_read<0>();
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                     // no arrival at a block that has left
+    tc_fence_after();
+    if (warp == 1) free_columns<2>(tmem, 2 * kTile);
+}
+
+// ----------------------------------------------------------------------------- host
+
+// A matrix in memory: rows of `cols` values, `pitch` apart.
+struct Matrix {
+    const void* p;
+    long long rows, cols, pitch;
+    // box: values across by rows down.
+    bool map(CUtensorMap* m, int across, int down, TmaSwizzle sw) const {
+        const unsigned long long dims[3] = {(unsigned long long)cols, (unsigned long long)rows, 1};
+        const unsigned long long row = (unsigned long long)pitch * 2, strides[2] = {row, row * (unsigned long long)rows};
+        const unsigned box[3] = {(unsigned)across, (unsigned)down, 1};
+        return make_tma_map(m, TmaType::bf16, p, dims, strides, box, sw);
+    }
+    // [rows][2][F] of rows of 2F.
+    bool halves(CUtensorMap* m, int across, int down, TmaSwizzle sw) const {
+        const unsigned long long dims[3] = {(unsigned long long)cols / 2, 2, (unsigned long long)rows};
+        const unsigned long long strides[2] = {(unsigned long long)cols, (unsigned long long)cols * 2};
+        const unsigned box[3] = {(unsigned)across, 1, (unsigned)down};
+        return make_tma_map(m, TmaType::bf16, p, dims, strides, box, sw);
+    }
+    // As an operand: rows of K, or (mn) K as rows.
+    bool operand(CUtensorMap* m, bool mn) const { return map(m, 64, mn ? 64 : kBM, TmaSwizzle::b128); }
+    bool piece(CUtensorMap* m) const { return map(m, 32, 32, TmaSwizzle::b64); }
+};
+
+bool problem(Problem& q, int M, int N, int K, int mode) {
+    q.M = M; q.N = N; q.K = K;
+    q.tiles_m = (M + kTile - 1) / kTile;
+    const int wide = mode == kGated ? kTile / 2 : kTile;
+    const long long tiles = (long long)q.tiles_m * ((N + wide - 1) / wide);
+    q.tiles = (int)tiles;
+    return tiles < (1LL << 30);
+}
+
+template <bool AMN, bool BMN, int MODE>
+cudaError_t gemm(const Maps& m0, const Maps& m1, GemmParams p, bool overlap, cudaStream_t s) {
+    p.tiles = p.q[0].tiles + p.q[1].tiles;
+    static_assert(kSmem<MODE> <= 232448, "shared memory of a block");
+    auto kernel = ffn_gemm_kernel<AMN, BMN, MODE>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<MODE>);
+    if (e != cudaSuccess) return e;
+    const int pairs = p.tiles < kPairs ? p.tiles : kPairs;
+    return launch_in_clusters(kernel, dim3(2 * pairs), dim3(kThreads), kSmem<MODE>, s, 2, overlap, m0, m1, p);
+}
+
+GemmParams params(const FfnArgs& a) {
+    GemmParams p{};
+    p.gelu = a.gelu;
+    p.status = a.status;
+    p.limit = a.wait_cycles > 0 ? a.wait_cycles : kWaitCycles;
+    return p;
 }
 
 }  // namespace
@@ -103,52 +440,71 @@ size_t ffn_workspace_bytes(int N, int D, int F, int backward) {
 }
 
 cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
-    const bf16 *x = static_cast<const bf16*>(a.x), *wi = static_cast<const bf16*>(a.W_in),
-               *wo = static_cast<const bf16*>(a.W_out);
-    Epilogue e{};
-    e.h = static_cast<bf16*>(a.workspace);
-    e.gu = static_cast<bf16*>(a.gu);
-    e.F = a.F;
-    e.gelu = a.gelu;
+    const long long N = a.N, D = a.D, F = a.F;
+    const Matrix x{a.x, N, D, a.x_row}, wi{a.W_in, D, 2 * F, 2 * F}, wo{a.W_out, F, D, D}, h{a.workspace, N, F, F},
+        y{a.y, N, D, D}, gu{a.gu, N, 2 * F, 2 * F}, res{a.residual, N, D, a.residual_row};
     *launches = 2;
-    const cudaError_t r = gemm<kGated>({x, a.x_row, 1}, {wi, 1, 2LL * a.F}, a.N, a.F, a.D, e, s);
-    if (r != cudaSuccess) return r;
-    e.out = static_cast<bf16*>(a.y);
-    e.add = static_cast<const bf16*>(a.residual);
-    e.add_row = a.residual_row;
-    return gemm<kStore>({e.h, a.F, 1}, {wo, 1, a.D}, a.N, a.D, a.F, e, s);
+    Maps m{};
+    GemmParams p = params(a);
+    p.save = a.gu != nullptr;
+    p.debug_stall = a.debug_stall;
+    if (!x.operand(&m.a, false) || !wi.halves(&m.b, 64, 64, TmaSwizzle::b128) || !h.piece(&m.out) ||
+        (a.gu && !gu.halves(&m.aux, 32, 32, TmaSwizzle::b64)) || !problem(p.q[0], a.N, a.F, a.D, kGated))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = gemm<false, true, kGated>(m, m, p, false, s);
+    if (e != cudaSuccess) return e;
+    GemmParams o = params(a);
+    Maps n{};
+    if (!h.operand(&n.a, false) || !wo.operand(&n.b, true) || !y.piece(&n.out) || (a.residual && !res.piece(&n.aux)) ||
+        !problem(o.q[0], a.N, a.D, a.F, kStore))
+        return cudaErrorInvalidValue;
+    o.q[0].add = a.residual != nullptr;
+    return gemm<false, true, kStore>(n, n, o, true, s);
 }
 
 cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
-    const bf16 *x = static_cast<const bf16*>(a.x), *wi = static_cast<const bf16*>(a.W_in),
-               *wo = static_cast<const bf16*>(a.W_out), *dy = static_cast<const bf16*>(a.dy);
-    bf16* dgu = static_cast<bf16*>(a.workspace);
-    bf16* h = dgu + (size_t)a.N * 2 * a.F;
-    Epilogue e{};
-    e.F = a.F;
-    e.gelu = a.gelu;
-    e.out = dgu;
-    e.h = h;
-    e.gu = static_cast<bf16*>(a.gu);
+    const long long N = a.N, D = a.D, F = a.F;
+    char* ws = static_cast<char*>(a.workspace);
+    const Matrix x{a.x, N, D, a.x_row}, wi{a.W_in, D, 2 * F, 2 * F}, wo{a.W_out, F, D, D}, dy{a.dy, N, D, a.dy_row},
+        gu{a.gu, N, 2 * F, 2 * F}, dgu{ws, N, 2 * F, 2 * F}, h{ws + (size_t)N * F * 4, N, F, F}, dx{a.dx, N, D, D},
+        dwi{a.dW_in, D, 2 * F, 2 * F}, dwo{a.dW_out, F, D, D};
     *launches = 1;
-    cudaError_t r = gemm<kGatedBack>({dy, a.dy_row, 1}, {wo, a.D, 1}, a.N, a.F, a.D, e, s);
-    Epilogue o{};
-    if (r == cudaSuccess && a.dx) {
-        o.out = static_cast<bf16*>(a.dx);
-        r = gemm<kStore>({dgu, 2LL * a.F, 1}, {wi, 2LL * a.F, 1}, a.N, a.D, 2 * a.F, o, s);
+    Maps m{};
+    GemmParams p = params(a);
+    p.debug_stall = a.debug_stall;
+    if (!dy.operand(&m.a, false) || !wo.operand(&m.b, false) || !dgu.halves(&m.out, 32, 32, TmaSwizzle::b64) ||
+        !gu.halves(&m.aux, 32, 32, TmaSwizzle::b64) || !h.piece(&m.h) || !problem(p.q[0], a.N, a.F, a.D, kGatedBack))
+        return cudaErrorInvalidValue;
+    cudaError_t e = gemm<false, false, kGatedBack>(m, m, p, false, s);
+    if (e != cudaSuccess) return e;
+    if (a.dx) {
+        GemmParams o = params(a);
+        Maps n{};
+        if (!dgu.operand(&n.a, false) || !wi.operand(&n.b, false) || !dx.piece(&n.out) ||
+            !problem(o.q[0], a.N, a.D, 2 * a.F, kStore))
+            return cudaErrorInvalidValue;
+        e = gemm<false, false, kStore>(n, n, o, true, s);
+        if (e != cudaSuccess) return e;
         ++*launches;
     }
-    if (r == cudaSuccess && a.dW_in) {
-        o.out = static_cast<bf16*>(a.dW_in);
-        r = gemm<kStore>({x, 1, a.x_row}, {dgu, 1, 2LL * a.F}, a.D, 2 * a.F, a.N, o, s);
-        ++*launches;
+    if (!a.dW_in && !a.dW_out) return cudaSuccess;
+    // both weights' products in one launch: few tiles each, so that one's last round fills up with the other's
+    GemmParams o = params(a);
+    Maps n[2] = {};
+    int k = 0;
+    if (a.dW_in) {
+        if (!x.operand(&n[k].a, true) || !dgu.operand(&n[k].b, true) || !dwi.piece(&n[k].out) ||
+            !problem(o.q[k], a.D, 2 * a.F, a.N, kStore))
+            return cudaErrorInvalidValue;
+        ++k;
     }
-    if (r == cudaSuccess && a.dW_out) {
-        o.out = static_cast<bf16*>(a.dW_out);
-        r = gemm<kStore>({h, 1, a.F}, {dy, 1, a.dy_row}, a.F, a.D, a.N, o, s);
-        ++*launches;
+    if (a.dW_out) {
+        if (!h.operand(&n[k].a, true) || !dy.operand(&n[k].b, true) || !dwo.piece(&n[k].out) ||
+            !problem(o.q[k], a.F, a.D, a.N, kStore))
+            return cudaErrorInvalidValue;
     }
-    return r;
+    ++*launches;
+    return gemm<true, true, kStore>(n[0], n[1], o, true, s);
 }
 
 }  // namespace ttm
