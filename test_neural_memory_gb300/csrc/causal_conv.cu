@@ -14,6 +14,7 @@
 
 #include <cstdint>
 
+#include "pairs.cuh"
 #include "train_ops.h"
 
 namespace ttm {
@@ -24,54 +25,66 @@ constexpr int kBatch = 4;               // rows whose loads are in flight togeth
 constexpr int kFwdThreads = 128;
 constexpr int kBwdThreads = 256;
 
-// V values of a row as they are stored, and as fp32.
+// V values of a row as they are stored, and as fp32: pairs of values (two results an instruction), or one.
 template <int BYTES> struct Word;
 template <> struct Word<2> { using type = unsigned short; };
 template <> struct Word<4> { using type = uint32_t; };
 template <> struct Word<8> { using type = uint2; };
 template <> struct Word<16> { using type = uint4; };
 template <typename T, int V> using Raw = typename Word<sizeof(T) * V>::type;
+template <int V> struct Lanes { static constexpr int n = V / 2; using type = f2; };
+template <> struct Lanes<1> { static constexpr int n = 1; using type = float; };
+template <int V> using Val = typename Lanes<V>::type;
+template <int V> constexpr int kVals = Lanes<V>::n;
 
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> load(const T* p) {
     return *reinterpret_cast<const Raw<T, V>*>(p);
 }
 template <typename T, int V>
-__device__ __forceinline__ void unpack(const Raw<T, V>& raw, float (&f)[V]) {
+__device__ __forceinline__ void unpack(const Raw<T, V>& raw, Val<V> (&f)[kVals<V>]) {
     if constexpr (sizeof(T) == 4) {
         const float* s = reinterpret_cast<const float*>(&raw);
+        if constexpr (V == 1) {
+            f[0] = s[0];
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = s[i];
+            for (int i = 0; i < V / 2; ++i) f[i] = pair(s[2 * i], s[2 * i + 1]);
+        }
     } else if constexpr (V == 1) {
         f[0] = __uint_as_float((uint32_t)raw << 16);
     } else {
         const uint32_t* s = reinterpret_cast<const uint32_t*>(&raw);
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            f[2 * i] = __uint_as_float(s[i] << 16);
-            f[2 * i + 1] = __uint_as_float(s[i] & 0xffff0000u);
-        }
+        for (int i = 0; i < V / 2; ++i) f[i] = pair_of_bf16(s[i]);
     }
 }
 template <typename T, int V>
-__device__ __forceinline__ void store(T* p, const float (&f)[V]) {
+__device__ __forceinline__ void store(T* p, const Val<V> (&f)[kVals<V>]) {
     Raw<T, V> raw;
     if constexpr (sizeof(T) == 4) {
         float* d = reinterpret_cast<float*>(&raw);
+        if constexpr (V == 1) {
+            d[0] = f[0];
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = f[i];
+            for (int i = 0; i < V / 2; ++i) split(f[i], d[2 * i], d[2 * i + 1]);
+        }
     } else if constexpr (V == 1) {
         raw = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
     } else {
         uint32_t* d = reinterpret_cast<uint32_t*>(&raw);
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            d[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
+        for (int i = 0; i < V / 2; ++i) d[i] = bf16_of_pair(f[i]);
     }
     *reinterpret_cast<Raw<T, V>*>(p) = raw;
 }
+template <int V>
+__device__ __forceinline__ Val<V> gather(const float* p, long long step) {     // the values of neighbouring channels
+    if constexpr (V == 1) return p[0];
+    else return pair(p[0], p[step]);
+}
+template <typename E> __device__ __forceinline__ E zero() { return splat<E>(0.f); }
 
 // 1 / (1 + exp(-x)).  bf16 results take the fast exponential and division (a few 2^-22 off, |x| 2^-24 more).
 template <typename T>
@@ -79,8 +92,14 @@ __device__ __forceinline__ float sigmoid(float x) {
     if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-x));
     else return __fdividef(1.f, 1.f + __expf(-x));
 }
+template <typename T>
+__device__ __forceinline__ f2 sigmoid(f2 x) {
+    float a, b;
+    split(x, a, b);
+    return pair(sigmoid<T>(a), sigmoid<T>(b));
+}
 
-// What a thread walks: rows of one sequence, its V channels from c on.
+// What a thread walks: rows of one sequence, its V channels.
 template <typename T>
 struct Rows {
     const T* x;                         // row 0, first channel
@@ -96,86 +115,131 @@ struct Rows {
     }
 };
 
-// KW: the window, K at most; tap i of K sits in slot i + KW - K, slots before it have weight 0.
+// KW: the window, K at most (kAll: K itself); tap i of K sits in slot i + KW - K, slots before it take no part.
+template <int V, int KW, bool kAll, bool DOC>
+__device__ __forceinline__ void taps(Val<V> (&out)[kVals<V>], const Val<V> (&w)[KW][kVals<V>],
+                                     const Val<V> (&win)[KW][kVals<V>], const int (&id)[KW], int before) {
+    bool same = true;
+    if (DOC) {
+#pragma unroll
+        for (int i = 0; i + 1 < KW; ++i) same &= i < before || id[i] == id[KW - 1];
+    }
+    if (!DOC || same) {
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+            if (!kAll && i < before) continue;
+#pragma unroll
+            for (int v = 0; v < kVals<V>; ++v) out[v] = fma(w[i][v], win[i][v], out[v]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+            if (i < before || id[i] != id[KW - 1]) continue;
+#pragma unroll
+            for (int v = 0; v < kVals<V>; ++v) out[v] = fma(w[i][v], win[i][v], out[v]);
+        }
+    }
+}
+
 // A strip of tokens a thread; the thread of a sequence's last strip writes the state.  `strips` = 1
 // lets the state be updated in place.
-template <typename T, int V, int KW, bool DOC>
-__global__ void __launch_bounds__(kFwdThreads) conv_fwd_kernel(const __grid_constant__ ConvArgs a, int groups,
-                                                                int strips, int strip) {
-    const long long id = (long long)blockIdx.x * kFwdThreads + threadIdx.x;
-    const int c = (int)(id % groups) * V;
-    const long long rest = id / groups;
-    const int part = (int)(rest % strips);
-    const long long n = rest / strips;
-    if (n >= a.N) return;
-    const int K = a.K, C = a.C, before = KW - K;
-    const int t0 = part * strip, t1 = min(a.T, t0 + strip);
-    Rows<T> rows{static_cast<const T*>(a.x) + n * a.x_seq + c, a.x_tok,
-                 a.state0 ? static_cast<const T*>(a.state0) + n * (K - 1) * C + c : nullptr, C, K};
-    const int* doc = DOC ? a.doc + n * a.doc_seq : nullptr;
-    float w[KW][V], bias[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        bias[v] = a.b ? a.b[c + v] : 0.f;
-#pragma unroll
-        for (int i = 0; i < KW; ++i) w[i][v] = i >= before ? a.w[(long long)(c + v) * K + i - before] : 0.f;
+template <typename T, int V, int KW, bool kAll, bool DOC>
+__global__ void __launch_bounds__(kFwdThreads) conv_fwd_kernel(const __grid_constant__ ConvArgs a, unsigned groups,
+                                                                unsigned strips, int strip) {
+    constexpr int NV = kVals<V>;
+    const unsigned long long id = (unsigned long long)blockIdx.x * kFwdThreads + threadIdx.x;
+    unsigned group, part, n;
+    if (id >> 32) {
+        const unsigned long long rest = id / groups;
+        group = (unsigned)(id - rest * groups);
+        n = (unsigned)(rest / strips);
+        part = (unsigned)(rest - (unsigned long long)n * strips);
+    } else {
+        const unsigned rest = (unsigned)id / groups;
+        group = (unsigned)id - rest * groups;
+        n = rest / strips;
+        part = rest - n * strips;
     }
-    float win[KW][V];                   // slots KW - 1 .. : the rows before the token, the token in the last
-    int id_win[KW];
+    if (n >= (unsigned)a.N) return;
+    const int c = (int)group * V, K = a.K, C = a.C, before = kAll ? 0 : KW - K;
+    const int t0 = (int)part * strip, t1 = min(a.T, t0 + strip);
+    const Rows<T> rows{static_cast<const T*>(a.x) + n * a.x_seq + c, a.x_tok,
+                       a.state0 ? static_cast<const T*>(a.state0) + (long long)n * (K - 1) * C + c : nullptr, C, K};
+    const int* doc = DOC ? a.doc + n * a.doc_seq : nullptr;
+    Raw<T, V> next[kBatch];
+    int next_id[kBatch];
+    const T* from = rows.x + (long long)t0 * rows.tok;
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (t + j < t1) {
+                next[j] = load<T, V>(from);
+                if (DOC) next_id[j] = doc[t + j];
+            }
+            from += rows.tok;
+        }
+    };
+    fetch(t0);
+    Val<V> w[KW][NV], bias[NV], win[KW][NV];            // win: slots up to KW - 2 the rows before the token
+    int ids[KW];
 #pragma unroll
     for (int i = 1; i < KW; ++i) {
         const int t = t0 - KW + i;
         Raw<T, V> raw{};
         if (i > before) raw = rows.template at<V>(t);
         unpack<T, V>(raw, win[i]);
-        if (DOC) id_win[i] = doc[max(t, 0)];
+        if (DOC) ids[i] = doc[max(t, 0)];
     }
-    T* y = static_cast<T*>(a.y) + n * a.T * (long long)C + c;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int ch = c + v * (V / NV);
+        bias[v] = a.b ? gather<V>(a.b + ch, 1) : zero<Val<V>>();
+#pragma unroll
+        for (int i = 0; i < KW; ++i)
+            w[i][v] = i >= before ? gather<V>(a.w + (long long)ch * K + i - before, K) : zero<Val<V>>();
+    }
+    T* y = static_cast<T*>(a.y) + ((long long)n * a.T + t0) * C + c;
     for (int t = t0; t < t1; t += kBatch) {
         Raw<T, V> raw[kBatch];
-        int ids[kBatch];
+        int raw_id[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            raw[j] = next[j];
+            if (DOC) raw_id[j] = next_id[j];
+        }
+        fetch(t + kBatch);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (t + j < t1) {
-                raw[j] = load<T, V>(rows.x + (long long)(t + j) * rows.tok);
-                if (DOC) ids[j] = doc[t + j];
+#pragma unroll
+                for (int i = 0; i + 1 < KW; ++i) {
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) win[i][v] = win[i + 1][v];
+                    if (DOC) ids[i] = ids[i + 1];
+                }
+                unpack<T, V>(raw[j], win[KW - 1]);
+                if (DOC) ids[KW - 1] = raw_id[j];
+                Val<V> out[NV];
+#pragma unroll
+                for (int v = 0; v < NV; ++v) out[v] = bias[v];
+                taps<V, KW, kAll, DOC>(out, w, win, ids, before);
+                if (a.silu) {
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) out[v] = mul(out[v], sigmoid<T>(out[v]));
+                }
+                store<T, V>(y, out);
+                y += C;
             }
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            if (t + j >= t1) break;
-#pragma unroll
-            for (int i = 0; i + 1 < KW; ++i) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) win[i][v] = win[i + 1][v];
-                if (DOC) id_win[i] = id_win[i + 1];
-            }
-            unpack<T, V>(raw[j], win[KW - 1]);
-            if (DOC) id_win[KW - 1] = ids[j];
-            float out[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) out[v] = bias[v];
-#pragma unroll
-            for (int i = 0; i < KW; ++i) {
-                const bool in = i >= before && (!DOC || id_win[i] == id_win[KW - 1]);
-#pragma unroll
-                for (int v = 0; v < V; ++v) out[v] = in ? fmaf(w[i][v], win[i][v], out[v]) : out[v];
-            }
-            if (a.silu) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) out[v] *= sigmoid<T>(out[v]);
-            }
-            store<T, V>(y + (long long)(t + j) * C, out);
         }
     }
-    if (a.state && part == strips - 1 && K > 1) {
-        T* s = static_cast<T*>(a.state) + n * (K - 1) * C + c;
+    if (a.state && part + 1 == strips) {
+        T* s = static_cast<T*>(a.state) + (long long)n * (K - 1) * C + c;
 #pragma unroll
         for (int i = 1; i < KW; ++i) {
             if (i <= before) continue;
-            float f[V];
+            Val<V> f[NV];
 #pragma unroll
-            for (int v = 0; v < V; ++v) f[v] = !DOC || id_win[i] == id_win[KW - 1] ? win[i][v] : 0.f;
+            for (int v = 0; v < NV; ++v) f[v] = !DOC || ids[i] == ids[KW - 1] ? win[i][v] : zero<Val<V>>();
             store<T, V>(s + (long long)(i - before - 1) * C, f);
         }
     }
@@ -194,23 +258,26 @@ __global__ void conv_pass_kernel(const T* from, T* to, long long n) {
 // in registers over a thread's strips, over the block's threads in shared memory in their order, and leave as
 // one part of the block's row of the grid, joined by conv_join_kernel in the rows' order: equal inputs give
 // equal bits.
-template <typename T, int V, int KW, bool DOC>
-__global__ void __launch_bounds__(kBwdThreads) conv_bwd_kernel(const __grid_constant__ ConvArgs a, int groups,
+template <typename T, int V, int KW, bool kAll, bool DOC>
+__global__ void __launch_bounds__(kBwdThreads, 2) conv_bwd_kernel(const __grid_constant__ ConvArgs a, int groups,
                                                                 int strips, int strip) {
+    constexpr int NV = kVals<V>;
+    using E = Val<V>;
     __shared__ float sums[kBwdThreads * V];
-    const int K = a.K, C = a.C, before = KW - K;
+    const int K = a.K, C = a.C, before = kAll ? 0 : KW - K;
     const int group = blockIdx.x * blockDim.x + threadIdx.x;
     const bool live = group < groups;
     const int c = live ? group * V : 0;
-    float w[KW][V], bias[V], dw[KW][V], db[V];
+    E w[KW][NV], bias[NV], dw[KW][NV], db[NV];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        bias[v] = a.b ? a.b[c + v] : 0.f;
-        db[v] = 0.f;
+    for (int v = 0; v < NV; ++v) {
+        const int ch = c + v * (V / NV);
+        bias[v] = a.b ? gather<V>(a.b + ch, 1) : zero<E>();
+        db[v] = zero<E>();
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
-            w[i][v] = i >= before ? a.w[(long long)(c + v) * K + i - before] : 0.f;
-            dw[i][v] = 0.f;
+            w[i][v] = i >= before ? gather<V>(a.w + (long long)ch * K + i - before, K) : zero<E>();
+            dw[i][v] = zero<E>();
         }
     }
     const long long total = live ? (long long)a.N * strips : 0;
@@ -218,106 +285,116 @@ __global__ void __launch_bounds__(kBwdThreads) conv_bwd_kernel(const __grid_cons
          s += (long long)gridDim.y * blockDim.y) {
         const long long n = s / strips;
         const int t0 = (int)(s % strips) * strip, t1 = min(a.T, t0 + strip), end = min(a.T, t1 + KW - 1);
-        Rows<T> rows{static_cast<const T*>(a.x) + n * a.x_seq + c, a.x_tok,
-                     a.state0 ? static_cast<const T*>(a.state0) + n * (K - 1) * C + c : nullptr, C, K};
-        const T* dy = static_cast<const T*>(a.dy) + n * a.dy_seq + c;
+        const Rows<T> rows{static_cast<const T*>(a.x) + n * a.x_seq + c, a.x_tok,
+                           a.state0 ? static_cast<const T*>(a.state0) + n * (K - 1) * C + c : nullptr, C, K};
         const int* doc = DOC ? a.doc + n * a.doc_seq : nullptr;
         const int id_last = DOC ? doc[a.T - 1] : 0;
         T* dx = static_cast<T*>(a.dx) + n * a.T * (long long)C + c;
         T* ds0 = a.dstate0 ? static_cast<T*>(a.dstate0) + n * (K - 1) * C + c : nullptr;
         const T* ds = a.dstate ? static_cast<const T*>(a.dstate) + n * (K - 1) * C + c : nullptr;
         const int first_row = t0 == 0 && ds0 ? -(K - 1) : t0;
-        float win[KW][V], d[KW][V];     // rows t - KW + 1 .. t and their d
-        int id_win[KW];
+        Raw<T, V> next[kBatch], dnext[kBatch];
+        int next_id[kBatch];
+        const T *from = rows.x + (long long)t0 * rows.tok, *dfrom = static_cast<const T*>(a.dy) + n * a.dy_seq + (long long)t0 * a.dy_tok + c;
+        auto fetch = [&](int t) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (t + j < end) {
+                    next[j] = load<T, V>(from);
+                    dnext[j] = load<T, V>(dfrom);
+                    if (DOC) next_id[j] = doc[t + j];
+                }
+                from += rows.tok;
+                dfrom += a.dy_tok;
+            }
+        };
+        fetch(t0);
+        E win[KW][NV], d[KW][NV];       // rows t - KW + 1 .. t and their d
+        int ids[KW];
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
             const int t = t0 - KW + i;
             Raw<T, V> raw{};
             if (i > before) raw = rows.template at<V>(t);
             unpack<T, V>(raw, win[i]);
-            if (DOC) id_win[i] = doc[max(t, 0)];
+            if (DOC) ids[i] = doc[max(t, 0)];
 #pragma unroll
-            for (int v = 0; v < V; ++v) d[i][v] = 0.f;
+            for (int v = 0; v < NV; ++v) d[i][v] = zero<E>();
         }
         for (int t = t0; t < t1 + KW - 1; t += kBatch) {
             Raw<T, V> raw[kBatch], draw[kBatch];
-            int ids[kBatch];
+            int raw_id[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-                if (t + j < end) {
-                    raw[j] = load<T, V>(rows.x + (long long)(t + j) * rows.tok);
-                    draw[j] = load<T, V>(dy + (long long)(t + j) * a.dy_tok);
-                    if (DOC) ids[j] = doc[t + j];
-                }
+                raw[j] = next[j];
+                draw[j] = dnext[j];
+                if (DOC) raw_id[j] = next_id[j];
             }
+            fetch(t + kBatch);
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 const int now = t + j, row = now - (KW - 1);
 #pragma unroll
                 for (int i = 0; i + 1 < KW; ++i) {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) {
+                    for (int v = 0; v < NV; ++v) {
                         win[i][v] = win[i + 1][v];
                         d[i][v] = d[i + 1][v];
                     }
-                    if (DOC) id_win[i] = id_win[i + 1];
+                    if (DOC) ids[i] = ids[i + 1];
                 }
                 if (now < end) {
                     unpack<T, V>(raw[j], win[KW - 1]);
                     unpack<T, V>(draw[j], d[KW - 1]);
-                    if (DOC) id_win[KW - 1] = ids[j];
+                    if (DOC) ids[KW - 1] = raw_id[j];
                     if (a.silu) {
-                        float pre[V];
+                        E pre[NV];
 #pragma unroll
-                        for (int v = 0; v < V; ++v) pre[v] = bias[v];
+                        for (int v = 0; v < NV; ++v) pre[v] = bias[v];
+                        taps<V, KW, kAll, DOC>(pre, w, win, ids, before);
 #pragma unroll
-                        for (int i = 0; i < KW; ++i) {
-                            const bool in = i >= before && (!DOC || id_win[i] == id_win[KW - 1]);
-#pragma unroll
-                            for (int v = 0; v < V; ++v) pre[v] = in ? fmaf(w[i][v], win[i][v], pre[v]) : pre[v];
-                        }
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            const float g = sigmoid<T>(pre[v]);
-                            d[KW - 1][v] *= g * fmaf(pre[v], 1.f - g, 1.f);
+                        for (int v = 0; v < NV; ++v) {
+                            const E g = sigmoid<T>(pre[v]);
+                            // 1 + pre (1 - g)
+                            const E up = fma(pre[v], fma(g, splat<E>(-1.f), splat<E>(1.f)), splat<E>(1.f));
+                            d[KW - 1][v] = mul(d[KW - 1][v], mul(g, up));
                         }
                     }
                     if (now < t1) {
 #pragma unroll
                         for (int i = 0; i < KW; ++i) {
-                            const bool in = i >= before && (!DOC || id_win[i] == id_win[KW - 1]);
+                            if ((!kAll && i < before) || (DOC && ids[i] != ids[KW - 1])) continue;
 #pragma unroll
-                            for (int v = 0; v < V; ++v)
-                                dw[i][v] = in ? fmaf(d[KW - 1][v], win[i][v], dw[i][v]) : dw[i][v];
+                            for (int v = 0; v < NV; ++v) dw[i][v] = fma(d[KW - 1][v], win[i][v], dw[i][v]);
                         }
 #pragma unroll
-                        for (int v = 0; v < V; ++v) db[v] += d[KW - 1][v];
+                        for (int v = 0; v < NV; ++v) db[v] = add(db[v], d[KW - 1][v]);
                     }
                 } else {                // past the sequence, or past what the strip's rows need
 #pragma unroll
-                    for (int v = 0; v < V; ++v) d[KW - 1][v] = 0.f;
-                    if (DOC) id_win[KW - 1] = id_last;
+                    for (int v = 0; v < NV; ++v) d[KW - 1][v] = zero<E>();
+                    if (DOC) ids[KW - 1] = id_last;
                 }
-                if (row < first_row || row >= t1) continue;
-                // row + m met row in its tap K - 1 - m, slot KW - 1 - m
-                float out[V];
+                if (row >= first_row && row < t1) {
+                    // row + m met row in its tap K - 1 - m, slot KW - 1 - m
+                    E out[NV];
 #pragma unroll
-                for (int v = 0; v < V; ++v) out[v] = 0.f;
+                    for (int v = 0; v < NV; ++v) out[v] = zero<E>();
 #pragma unroll
-                for (int m = 0; m < KW; ++m) {
-                    const bool in = m < K && (!DOC || id_win[m] == id_win[0]);
+                    for (int m = 0; m < KW; ++m) {
+                        if ((!kAll && m >= K) || (DOC && ids[m] != ids[0])) continue;
 #pragma unroll
-                    for (int v = 0; v < V; ++v) out[v] = in ? fmaf(w[KW - 1 - m][v], d[m][v], out[v]) : out[v];
+                        for (int v = 0; v < NV; ++v) out[v] = fma(w[KW - 1 - m][v], d[m][v], out[v]);
+                    }
+                    const int tail = row - (a.T - (K - 1));
+                    if (ds && tail >= 0 && (!DOC || ids[0] == id_last)) {
+                        E f[NV];
+                        unpack<T, V>(load<T, V>(ds + (long long)tail * C), f);
+#pragma unroll
+                        for (int v = 0; v < NV; ++v) out[v] = add(out[v], f[v]);
+                    }
+                    store<T, V>(row >= 0 ? dx + (long long)row * C : ds0 + (long long)(row + K - 1) * C, out);
                 }
-                const int tail = row - (a.T - (K - 1));
-                if (ds && tail >= 0 && (!DOC || id_win[0] == id_last)) {
-                    float f[V];
-                    unpack<T, V>(load<T, V>(ds + (long long)tail * C), f);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) out[v] += f[v];
-                }
-                if (row >= 0) store<T, V>(dx + (long long)row * C, out);
-                else store<T, V>(ds0 + (long long)(row + K - 1) * C, out);
             }
         }
     }
@@ -328,7 +405,11 @@ __global__ void __launch_bounds__(kBwdThreads) conv_bwd_kernel(const __grid_cons
     for (int q = 0; q <= KW; ++q) {     // tap slots, then db
         if (q < before) continue;
 #pragma unroll
-        for (int v = 0; v < V; ++v) sums[tid * V + v] = q < KW ? dw[q < KW ? q : 0][v] : db[v];
+        for (int v = 0; v < NV; ++v) {
+            const E x = q < KW ? dw[q < KW ? q : 0][v] : db[v];
+            if constexpr (V == 1) sums[tid] = x;
+            else split(x, sums[tid * V + 2 * v], sums[tid * V + 2 * v + 1]);
+        }
         __syncthreads();
         for (int i = tid; i < bx * V; i += kBwdThreads) {
             float total = 0.f;
@@ -377,17 +458,17 @@ int widest(const ConvArgs& a, bool back) {
     return (int)(bits & (~bits + 1));   // every other pointer is 16-byte aligned, its rows C values apart
 }
 
-template <typename T, int V, int KW>
+template <typename T, int V, int KW, bool kAll>
 cudaError_t fwd(const ConvArgs& a, bool one_strip, cudaStream_t s) {
-    const int groups = a.C / V;
+    const unsigned groups = a.C / V;
     // Strips as long as leave two waves of threads, 8 to 128 tokens: the rows between strips are read twice.
     int strip = one_strip ? a.T : 128;
     while (!one_strip && strip > 8 && (long long)a.N * groups * ((a.T + strip - 1) / strip) < kSms * 2048LL) strip /= 2;
-    const int strips = (a.T + strip - 1) / strip;
+    const unsigned strips = (a.T + strip - 1) / strip;
     const long long blocks = ((long long)a.N * groups * strips + kFwdThreads - 1) / kFwdThreads;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (a.doc) conv_fwd_kernel<T, V, KW, true><<<(unsigned)blocks, kFwdThreads, 0, s>>>(a, groups, strips, strip);
-    else conv_fwd_kernel<T, V, KW, false><<<(unsigned)blocks, kFwdThreads, 0, s>>>(a, groups, strips, strip);
+    if (a.doc) conv_fwd_kernel<T, V, KW, kAll, true><<<(unsigned)blocks, kFwdThreads, 0, s>>>(a, groups, strips, strip);
+    else conv_fwd_kernel<T, V, KW, kAll, false><<<(unsigned)blocks, kFwdThreads, 0, s>>>(a, groups, strips, strip);
     return cudaGetLastError();
 }
 
@@ -399,7 +480,7 @@ int most_rows(int C) {
     return rows < 1 ? 1 : rows;
 }
 
-template <typename T, int V, int KW>
+template <typename T, int V, int KW, bool kAll>
 cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
     const int groups = a.C / V;
     int bx = 1;
@@ -411,8 +492,8 @@ cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
     const long long wanted = ((long long)a.N * strips + by - 1) / by;
     const int rows = (int)(wanted < most_rows(a.C) ? wanted : most_rows(a.C));
     const dim3 grid(across, rows), block(bx, by);
-    if (a.doc) conv_bwd_kernel<T, V, KW, true><<<grid, block, 0, s>>>(a, groups, strips, strip);
-    else conv_bwd_kernel<T, V, KW, false><<<grid, block, 0, s>>>(a, groups, strips, strip);
+    if (a.doc) conv_bwd_kernel<T, V, KW, kAll, true><<<grid, block, 0, s>>>(a, groups, strips, strip);
+    else conv_bwd_kernel<T, V, KW, kAll, false><<<grid, block, 0, s>>>(a, groups, strips, strip);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.partial) return e;
     cudaLaunchAttribute at[1];
@@ -427,31 +508,40 @@ cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&c, conv_join_kernel, (const float*)a.partial, rows, a.C, a.K, a.dw, a.db);
 }
 
-// F<T, V, KW>: as many channels a thread as the rows' alignment and the registers allow.
-#define CONV_BY_WIDTH(F, MOST, KW, bytes, ...)                                             \
-    do {                                                                                   \
-        if (a.bf16) {                                                                      \
-            if constexpr (MOST >= 8) if (bytes >= 16) return F<__nv_bfloat16, 8, KW>(a, ##__VA_ARGS__); \
-            if constexpr (MOST >= 4) if (bytes >= 8) return F<__nv_bfloat16, 4, KW>(a, ##__VA_ARGS__);  \
-            if (bytes >= 4) return F<__nv_bfloat16, 2, KW>(a, ##__VA_ARGS__);              \
-            return F<__nv_bfloat16, 1, KW>(a, ##__VA_ARGS__);                              \
-        }                                                                                  \
-        if constexpr (MOST >= 4) if (bytes >= 16) return F<float, 4, KW>(a, ##__VA_ARGS__); \
-        if (bytes >= 8) return F<float, 2, KW>(a, ##__VA_ARGS__);                          \
-        return F<float, 1, KW>(a, ##__VA_ARGS__);                                          \
+// The window: 4 taps exactly (the usual case), up to 4, up to 8.
+#define CONV_BY_TAPS(F, T, V, V8, ...)                              \
+    do {                                                            \
+        if (a.K == 4) return F<T, V, 4, true>(a, ##__VA_ARGS__);    \
+        if (a.K < 4) return F<T, V, 4, false>(a, ##__VA_ARGS__);    \
+        return F<T, V8, 8, false>(a, ##__VA_ARGS__);                \
     } while (0)
 
+// As many channels a thread as the rows' alignment and the registers allow.
 cudaError_t fwd_any(const ConvArgs& a, bool one_strip, cudaStream_t s) {
     const int bytes = widest(a, false);
-    if (a.K <= 4) CONV_BY_WIDTH(fwd, 8, 4, bytes, one_strip, s);
-    CONV_BY_WIDTH(fwd, 4, 8, bytes, one_strip, s);
+    if (a.bf16) {
+        if (bytes >= 16) CONV_BY_TAPS(fwd, __nv_bfloat16, 8, 4, one_strip, s);
+        if (bytes >= 8) CONV_BY_TAPS(fwd, __nv_bfloat16, 4, 4, one_strip, s);
+        if (bytes >= 4) CONV_BY_TAPS(fwd, __nv_bfloat16, 2, 2, one_strip, s);
+        CONV_BY_TAPS(fwd, __nv_bfloat16, 1, 1, one_strip, s);
+    }
+    if (bytes >= 16) CONV_BY_TAPS(fwd, float, 4, 4, one_strip, s);
+    if (bytes >= 8) CONV_BY_TAPS(fwd, float, 2, 2, one_strip, s);
+    CONV_BY_TAPS(fwd, float, 1, 1, one_strip, s);
 }
 
 cudaError_t bwd_any(const ConvArgs& a, cudaStream_t s) {
     const int bytes = widest(a, true);
-    if (a.K <= 4) CONV_BY_WIDTH(bwd, 4, 4, bytes, s);
-    CONV_BY_WIDTH(bwd, 2, 8, bytes, s);
+    if (a.bf16) {
+        if (bytes >= 8) CONV_BY_TAPS(bwd, __nv_bfloat16, 4, 2, s);
+        if (bytes >= 4) CONV_BY_TAPS(bwd, __nv_bfloat16, 2, 2, s);
+        CONV_BY_TAPS(bwd, __nv_bfloat16, 1, 1, s);
+    }
+    if (bytes >= 16) CONV_BY_TAPS(bwd, float, 4, 2, s);
+    if (bytes >= 8) CONV_BY_TAPS(bwd, float, 2, 2, s);
+    CONV_BY_TAPS(bwd, float, 1, 1, s);
 }
+#undef CONV_BY_TAPS
 
 cudaError_t pass_state(const ConvArgs& a, const void* from, void* to, cudaStream_t s) {
     const long long n = (long long)a.N * (a.K - 1) * a.C;

@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/ttm.h"
@@ -108,6 +109,7 @@ struct Maps {
 struct GemmParams {
     Problem q[2];
     int tiles;
+    int splits;                         // SPLIT: pairs of a cluster that share a tile's K
     int gelu, save;                     // save: kGated writes g and u
     int* status;
     long long limit;
@@ -149,7 +151,28 @@ __device__ __forceinline__ void load_sums(uint32_t at, float (&v)[32]) {
     tmem_ld16(at + 16, *reinterpret_cast<float(*)[16]>(v + 16));
 }
 
-template <bool AMN, bool BMN, int MODE>
+// Blocks of K [from, to) of a pair of the cluster.
+struct Share {
+    int from, to;
+};
+template <bool SPLIT>
+__device__ __forceinline__ Share share_of(const GemmParams& p, int which, int pair) {
+    const int kblocks = (p.q[which].K + kBK - 1) / kBK;
+    if (!SPLIT) return {0, kblocks};
+    const int each = (kblocks + p.splits - 1) / p.splits;
+    return {min(kblocks, pair * each), min(kblocks, (pair + 1) * each)};
+}
+
+__device__ __forceinline__ float peer_load1(uint32_t addr) {
+    float f;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(addr));
+    return f;
+}
+
+// SPLIT: a cluster of 2 to 4 pairs has one tile, each pair a share of its K.  The pairs leave their sums where the
+// operands lay, and each takes its share of the pieces through the epilogue, summed over the pairs in their
+// order.
+template <bool AMN, bool BMN, int MODE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
                     const __grid_constant__ GemmParams p) {
@@ -159,8 +182,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* epi = base + kS * kStageBytes;
     GemmShared& S = *reinterpret_cast<GemmShared*>(epi + kEpiBytes<MODE>);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank();
-    const int first = blockIdx.x / 2, stride = gridDim.x / 2;
+    const int member = SPLIT ? (int)cluster_rank() : 0, pair_of = member >> 1;
+    const int rank = SPLIT ? member & 1 : (int)cluster_rank(), lead = member & ~1;
+    const uint16_t both = (uint16_t)(3 << lead);
+    const int width = SPLIT ? 2 * p.splits : 2, first = blockIdx.x / width, stride = gridDim.x / width;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kS; ++i) {
             // (in a test of the waits one stage expects an arrival that does not come)
@@ -189,15 +214,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = first; t < p.tiles && ok; t += stride) {
             const TileAt at = tile_at<MODE>(p, t);
             const CUtensorMap *ma = at.which ? &m1.a : &m0.a, *mb = at.which ? &m1.b : &m0.b;
-            const int kblocks = (p.q[at.which].K + kBK - 1) / kBK;
+            const Share own = share_of<SPLIT>(p, at.which, pair_of);
             const int row = at.row + rank * kBM, col = MODE == kGated ? at.col : at.col + rank * (kTile / 2);
-            for (int k = 0; k < kblocks; ++k, ++it) {
+            for (int k = own.from; k < own.to; ++k, ++it) {
                 const int s = it % kS;
                 ok = wait_one(&S.empty[s], ((it / kS) & 1) ^ 1, &S.abort, p.status, p.limit);
                 if (!ok) break;
                 unsigned char *da = base + s * kStageBytes, *db = da + kOperand;
                 if (rank == 0) mbar_expect_tx(&S.full[s], 2 * kStageBytes);
-                const uint32_t bar = peer_addr(&S.full[s], 0);
+                const uint32_t bar = peer_addr(&S.full[s], lead);
                 if (AMN) {
                     for (int i = 0; i < 2; ++i) tma_load_3d_pair(da + i * 8192, ma, bar, row + 64 * i, k * kBK, 0);
                 } else {
@@ -230,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + acc * kTile;
-            const int kblocks = (p.q[t >= p.q[0].tiles].K + kBK - 1) / kBK;
-            for (int k = 0; k < kblocks; ++k) {
+            const Share own = share_of<SPLIT>(p, t >= p.q[0].tiles, pair_of);
+            for (int k = own.from; k < own.to; ++k) {
                 ok = wait_warp(&S.full[s], phase, &S.abort, p.status, p.limit);
                 if (!ok) break;
                 tc_fence_after();
@@ -239,9 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
-                        mma_pair(d, da + kk * step_a, db + kk * step_b, id, k > 0 || kk > 0);
-                    commit_pair(&S.empty[s]);
-                    if (k + 1 == kblocks) commit_pair(&S.acc_full[acc]);
+                        mma_pair(d, da + kk * step_a, db + kk * step_b, id, k > own.from || kk > 0);
+                    commit_pair(&S.empty[s], both);
+                    if (k + 1 == own.to) commit_pair(&S.acc_full[acc], both);
                 }
                 __syncwarp();
                 if (++s == kS) { s = 0; phase ^= 1; }
@@ -250,127 +275,179 @@ __global__ void __launch_bounds__(kThreads, 1)
         // after an abort: products still in flight (the commit of the stage before s)
         if (*(volatile int*)&S.abort && lane == 0 && (s > 0 || phase))
             drain(&S.empty[s ? s - 1 : kS - 1], s ? phase : phase ^ 1, p.limit);
-    } else if (warp >= 2) {
-        const int part = warp & 3;                      // this warp's lanes of tensor memory
-        const int team = (warp - 2) >> 2;               // takes every other piece
-        unsigned char* mine = epi + (warp - 2) * kPieces<MODE> * kPiece;
-        uint64_t* landed = S.landed[warp - 2];
-        int n = 0, turn = 0;
-        uint32_t asked = 0, seen = 0;                   // copies into this warp's pieces, on one barrier and the other
-        bool ok = true;
-        for (int t = first; t < p.tiles && ok; t += stride, ++n) {
-            const TileAt at = tile_at<MODE>(p, t);
-            const Problem& q = p.q[at.which];
-            const Maps& m = at.which ? m1 : m0;
-            const int acc = n & 1, row0 = at.row + rank * kBM + part * 32;
-            const int width = MODE == kGated ? kTile / 2 : kTile;
-            const int pieces = row0 < q.M ? min(width, q.N - at.col + 31) / 32 : 0;     // that hold a result
-            const bool loads = MODE == kGatedBack || (MODE == kStore && q.add);
-            auto fetch = [&](int c) {                   // what piece c takes, into one place and the other
-                if (lane == 0) {
-                    bulk_wait_read<0>();                // the results that lay there have left
-                    unsigned char* to = mine + (asked & 1) * (MODE == kGatedBack ? 3 : 1) * kPiece;
-                    uint64_t* bar = &landed[asked & 1];
-                    const int x = at.col + 32 * c;
-                    mbar_expect_tx(bar, MODE == kGatedBack ? 2 * kPiece : kPiece);
-                    tma_load_3d(to, &m.aux, bar, x, MODE == kGatedBack ? 0 : row0, MODE == kGatedBack ? row0 : 0);
-                    if (MODE == kGatedBack) tma_load_3d(to + kPiece, &m.aux, bar, x, 1, row0);
-                }
-                ++asked;
-            };
-            if (loads && team < pieces) fetch(team);
-            ok = wait_warp(&S.acc_full[acc], (n >> 1) & 1, &S.abort, p.status, p.limit);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t sums = tmem_addr(tmem, part * 32, acc * kTile);
-            for (int c = team; c < pieces; c += 2, ++turn) {
-                const int x = at.col + 32 * c;
-                unsigned char* to = mine + (MODE == kGated ? 0 : (turn & 1) * (MODE == kGatedBack ? 3 : 1)) * kPiece;
-                float v[32];
-                load_sums(sums + 32 * c, v);
-                float up[MODE == kGated ? 32 : 1];
-                if constexpr (MODE == kGated) load_sums(sums + kTile / 2 + 32 * c, up);
-                tmem_wait_ld();
+    }
+
+    // ------ epilogue: warps 2 .. 9
+    const int part = warp & 3;                          // this warp's lanes of tensor memory
+    const int team = (warp - 2) >> 2;                   // takes every other piece
+    unsigned char* mine = epi + (warp - 2) * kPieces<MODE> * kPiece;
+    uint64_t* landed = S.landed[(warp - 2) & 7];
+    uint32_t asked = 0, seen = 0;                       // copies into this warp's pieces, on one barrier and the other
+    int turn = 0;
+    bool ok = true;
+    auto loads_of = [&](const Problem& q) { return MODE == kGatedBack || (MODE == kStore && q.add); };
+    auto row_of = [&](const TileAt& at) { return at.row + rank * kBM + part * 32; };
+    auto pieces_of = [&](const TileAt& at) {            // that hold a result
+        const Problem& q = p.q[at.which];
+        const int all = MODE == kGated ? kTile / 2 : kTile;
+        return row_of(at) < q.M ? min(all, q.N - at.col + 31) / 32 : 0;
+    };
+    auto fetch = [&](const TileAt& at, int c) {         // what piece c takes, into one place and the other
+        if (lane == 0) {
+            const CUtensorMap* aux = at.which ? &m1.aux : &m0.aux;
+            bulk_wait_read<0>();                        // the results that lay there have left
+            unsigned char* to = mine + (asked & 1) * (MODE == kGatedBack ? 3 : 1) * kPiece;
+            uint64_t* bar = &landed[asked & 1];
+            const int x = at.col + 32 * c, row = row_of(at);
+            mbar_expect_tx(bar, MODE == kGatedBack ? 2 * kPiece : kPiece);
+            tma_load_3d(to, aux, bar, x, MODE == kGatedBack ? 0 : row, MODE == kGatedBack ? row : 0);
+            if (MODE == kGatedBack) tma_load_3d(to + kPiece, aux, bar, x, 1, row);
+        }
+        ++asked;
+    };
+    // Piece c from its sums v (kGated: of g, and up of u); `after`: the next piece of this warp.
+    auto piece = [&](const TileAt& at, int c, int after, int pieces, float (&v)[32], float (&up)[MODE == kGated ? 32 : 1]) {
+        const Maps& m = at.which ? m1 : m0;
+        const bool loads = loads_of(p.q[at.which]);
+        const int x = at.col + 32 * c, row0 = row_of(at);
+        unsigned char* to = mine + (MODE == kGated ? 0 : (turn & 1) * (MODE == kGatedBack ? 3 : 1)) * kPiece;
+        if (loads) {
+            if (after < pieces) fetch(at, after);
+            ok = wait_warp(&landed[seen & 1], (seen >> 1) & 1, &S.abort, p.status, p.limit);
+            if (!ok) return;
+            ++seen;
+        } else {
+            if (lane == 0) {
+                if (MODE == kStore) bulk_wait_read<1>();
+                else bulk_wait_read<0>();
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float (&f)[8] = *reinterpret_cast<float(*)[8]>(v + 8 * j);
+            uint4* a0 = piece_at(to, lane, j);
+            if constexpr (MODE == kStore) {
                 if (loads) {
-                    if (c + 2 < pieces) fetch(c + 2);
-                    ok = wait_warp(&landed[seen & 1], (seen >> 1) & 1, &S.abort, p.status, p.limit);
-                    if (!ok) break;
-                    ++seen;
-                } else {
-                    if (lane == 0) {
-                        if (MODE == kStore) bulk_wait_read<1>();
-                        else bulk_wait_read<0>();
-                    }
-                    __syncwarp();
+                    float r[8];
+                    unpack8(*a0, r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] += r[i];
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float (&f)[8] = *reinterpret_cast<float(*)[8]>(v + 8 * j);
-                    uint4* a0 = piece_at(to, lane, j);
-                    if constexpr (MODE == kStore) {
-                        if (loads) {
-                            float r[8];
-                            unpack8(*a0, r);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) f[i] += r[i];
-                        }
-                        *a0 = pack8(f);
-                    } else if constexpr (MODE == kGated) {
-                        float (&u)[8] = *reinterpret_cast<float(*)[8]>(up + 8 * j);
-                        if (p.save) {
-                            *piece_at(to + kPiece, lane, j) = pack8(f);
-                            *piece_at(to + 2 * kPiece, lane, j) = pack8(u);
-                        }
-                        float unused;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = act<false>(f[i], p.gelu, unused) * u[i];
-                        *a0 = pack8(f);
-                    } else {
-                        uint4 *a1 = piece_at(to + kPiece, lane, j), *a2 = piece_at(to + 2 * kPiece, lane, j);
-                        float g[8], u[8], h[8];
-                        unpack8(*a0, g);
-                        unpack8(*a1, u);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float slope;
-                            const float a = act<true>(g[i], p.gelu, slope);
-                            h[i] = a * u[i];
-                            g[i] = f[i] * u[i] * slope;
-                            u[i] = f[i] * a;
-                        }
-                        *a0 = pack8(g);
-                        *a1 = pack8(u);
-                        *a2 = pack8(h);
-                    }
+                *a0 = pack8(f);
+            } else if constexpr (MODE == kGated) {
+                float (&u)[8] = *reinterpret_cast<float(*)[8]>(up + 8 * j);
+                if (p.save) {
+                    *piece_at(to + kPiece, lane, j) = pack8(f);
+                    *piece_at(to + 2 * kPiece, lane, j) = pack8(u);
                 }
-                fence_proxy_async_smem();
+                float unused;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = act<false>(f[i], p.gelu, unused) * u[i];
+                *a0 = pack8(f);
+            } else {
+                uint4 *a1 = piece_at(to + kPiece, lane, j), *a2 = piece_at(to + 2 * kPiece, lane, j);
+                float g[8], u[8], h[8];
+                unpack8(*a0, g);
+                unpack8(*a1, u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float slope;
+                    const float a = act<true>(g[i], p.gelu, slope);
+                    h[i] = a * u[i];
+                    g[i] = f[i] * u[i] * slope;
+                    u[i] = f[i] * a;
+                }
+                *a0 = pack8(g);
+                *a1 = pack8(u);
+                *a2 = pack8(h);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if constexpr (MODE == kStore) {
+                tma_store_3d(&m.out, to, x, row0, 0);
+            } else if constexpr (MODE == kGated) {
+                tma_store_3d(&m.out, to, x, row0, 0);
+                if (p.save) {
+                    tma_store_3d(&m.aux, to + kPiece, x, 0, row0);
+                    tma_store_3d(&m.aux, to + 2 * kPiece, x, 1, row0);
+                }
+            } else {
+                tma_store_3d(&m.out, to, x, 0, row0);
+                tma_store_3d(&m.out, to + kPiece, x, 1, row0);
+                tma_store_3d(&m.h, to + 2 * kPiece, x, row0, 0);
+            }
+            bulk_commit();
+        }
+        __syncwarp();
+        ++turn;
+    };
+    if constexpr (!SPLIT) {
+        if (warp >= 2) {
+            int n = 0;
+            for (int t = first; t < p.tiles && ok; t += stride, ++n) {
+                const TileAt at = tile_at<MODE>(p, t);
+                const int acc = n & 1, pieces = pieces_of(at);
+                if (loads_of(p.q[at.which]) && team < pieces) fetch(at, team);
+                ok = wait_warp(&S.acc_full[acc], (n >> 1) & 1, &S.abort, p.status, p.limit);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sums = tmem_addr(tmem, part * 32, acc * kTile);
+                for (int c = team; c < pieces && ok; c += 2) {
+                    float v[32], up[MODE == kGated ? 32 : 1];
+                    load_sums(sums + 32 * c, v);
+                    if constexpr (MODE == kGated) load_sums(sums + kTile / 2 + 32 * c, up);
+                    tmem_wait_ld();
+                    piece(at, c, c + 2, pieces, v, up);
+                }
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if constexpr (MODE == kStore) {
-                        tma_store_3d(&m.out, to, x, row0, 0);
-                    } else if constexpr (MODE == kGated) {
-                        tma_store_3d(&m.out, to, x, row0, 0);
-                        if (p.save) {
-                            tma_store_3d(&m.aux, to + kPiece, x, 0, row0);
-                            tma_store_3d(&m.aux, to + 2 * kPiece, x, 1, row0);
-                        }
-                    } else {
-                        tma_store_3d(&m.out, to, x, 0, row0);
-                        tma_store_3d(&m.out, to + kPiece, x, 1, row0);
-                        tma_store_3d(&m.h, to + 2 * kPiece, x, row0, 0);
-                    }
-                    bulk_commit();
+                if (lane == 0) mbar_arrive_at(peer_addr(&S.acc_empty[acc], 0));
+            }
+        }
+    } else {
+        // one tile: its sums as [column][128 rows] over the stages, which nothing reads any more
+        float* sums = reinterpret_cast<float*>(base);
+        if (warp >= 2) {
+            ok = wait_warp(&S.acc_full[0], 0, &S.abort, p.status, p.limit);
+            if (ok) {
+                tc_fence_after();
+                for (int c = team; c < kTile / 32; c += 2) {
+                    float v[32];
+                    load_sums(tmem_addr(tmem, part * 32, 32 * c), v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sums[(32 * c + i) * kBM + part * 32 + lane] = v[i];
                 }
-                __syncwarp();
             }
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_at(peer_addr(&S.acc_empty[acc], 0));
         }
-        if (lane == 0) {
-            for (; seen != asked; ++seen) drain(&landed[seen & 1], (seen >> 1) & 1, p.limit);     // after an abort
-            bulk_wait_read<0>();
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 2 && ok) {
+            const TileAt at = tile_at<MODE>(p, first);
+            const int pieces = pieces_of(at), step = 2 * p.splits, begin = 2 * pair_of + team;
+            if (loads_of(p.q[at.which]) && begin < pieces) fetch(at, begin);
+            for (int c = begin; c < pieces && ok; c += step) {
+                float v[32] = {}, up[MODE == kGated ? 32 : 1] = {};
+                for (int q = 0; q < p.splits; ++q) {
+                    const uint32_t from = peer_addr(sums + (32 * c) * kBM + part * 32 + lane, 2 * q + rank);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] += peer_load1(from + i * kBM * 4);
+                    if constexpr (MODE == kGated) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) up[i] += peer_load1(from + (kTile / 2 + i) * kBM * 4);
+                    }
+                }
+                piece(at, c, c + step, pieces, v, up);
+            }
         }
+    }
+    if (warp >= 2 && lane == 0) {
+        for (; seen != asked; ++seen) drain(&landed[seen & 1], (seen >> 1) & 1, p.limit);     // after an abort
+        bulk_wait_read<0>();
     }
     __syncwarp();
     tc_fence_before();
@@ -378,6 +455,199 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();                                     // no arrival at a block that has left
     tc_fence_after();
     if (warp == 1) free_columns<2>(tmem, 2 * kTile);
+}
+
+// ------------------------------------------------------------------- products of few rows
+
+// Up to 128 rows: the weights are what is read, and the rows too few for a tile's first side.  So the product is
+// turned: 128 of the weights' columns are the 128 rows of the first operand, the rows of x the second operand's,
+// 16 to 128 of them.  A cluster of up to 8 blocks shares a tile's K, so that all SMs read weights however few the
+// tiles are; each leaves its sums in shared memory, and a share of the results is added up over the blocks
+// in their order, put through the epilogue and written by each.  The second kernel of a call starts on its weights
+// while the first one finishes.
+constexpr int kNarrow = 128, kNarrowThreads = 256, kNarrowStages = 6, kNarrowSmem = 110 * 1024;
+
+struct NarrowParams {
+    int N, wide, K;                     // rows; columns of the result (kGated: F); K
+    int F, kblocks;                     // kGated, kGatedBack: F; blocks of K of a block of the cluster
+    int bn, stages;                     // rows, padded to 16
+    int gelu;
+    bf16 *out, *gu, *h;                 // kStore: result; kGated: h and gu (or NULL); kGatedBack: dgu, gu read, h
+    const bf16* add;                    // kStore: residual or NULL
+    long long add_row;
+    int* status;
+    long long limit;
+    int debug_stall;
+};
+struct NarrowShared {
+    uint64_t full[kNarrowStages], empty[kNarrowStages], done;
+    uint32_t tmem;
+    int abort;
+};
+
+template <bool WMN, int MODE>
+__global__ void __launch_bounds__(kNarrowThreads, 2)
+    ffn_narrow_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
+                      const __grid_constant__ NarrowParams p) {
+    __shared__ NarrowShared S;
+    extern __shared__ unsigned char raw[];
+    unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
+    const int tile = blockIdx.x / ranks;
+    const int first = MODE == kGated ? tile * 64 : tile * 128;       // column of the result (kGated: f)
+    const int k0 = rank * p.kblocks, k1 = min((p.K + kBK - 1) / kBK, k0 + p.kblocks);
+    const uint32_t stage = kOperand + p.bn * 128;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&S.full[i], p.debug_stall && (p.debug_stall - 1) % p.stages == i ? 2 : 1);
+            mbar_init(&S.empty[i], 1);
+        }
+        mbar_init(&S.done, 1);
+        fence_mbar_init();
+        S.abort = 0;
+    }
+    if (warp == 1) tmem_alloc(&S.tmem, kNarrow);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    if (warp == 0 && lane == 0) {
+        auto weights = [&](int k, int s) {
+            unsigned char* to = base + s * stage;
+            mbar_expect_tx(&S.full[s], stage);
+            for (int i = 0; i < (WMN ? 2 : 1); ++i) {
+                if (MODE == kGated) tma_load_3d(to + i * 8192, &mw, &S.full[s], first, i, k * kBK);
+                else if (WMN) tma_load_3d(to + i * 8192, &mw, &S.full[s], first + 64 * i, k * kBK, 0);
+                else tma_load_3d(to, &mw, &S.full[s], k * kBK, first, 0);
+            }
+        };
+        // weights need no earlier kernel of the call: the first stages' are on their way before its end
+        const int ahead = max(0, min(p.stages, k1 - k0));
+        for (int i = 0; i < ahead; ++i) weights(k0 + i, i);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        int it = 0;
+        bool ok = true;
+        for (int k = k0; k < k1; ++k, ++it) {
+            const int s = it % p.stages;
+            if (it >= p.stages) {
+                ok = wait_one(&S.empty[s], ((it / p.stages) & 1) ^ 1, &S.abort, p.status, p.limit);
+                if (!ok) break;
+                weights(k, s);
+            }
+            tma_load_3d(base + s * stage + kOperand, &mx, &S.full[s], k * kBK, 0, 0);
+        }
+        if (*(volatile int*)&S.abort)                   // copies still in flight
+            for (int i = max(0, it - p.stages); i < it; ++i) drain(&S.full[i % p.stages], (i / p.stages) & 1, p.limit);
+    } else if (warp == 1) {
+        constexpr uint32_t step = (WMN ? 2048 : 32) >> 4;
+        const uint32_t id = idesc_bf16_f32(128, p.bn, WMN, 0);
+        const uint32_t base_u = __shfl_sync(0xffffffffu, smem_u32(base), 0);
+        const uint64_t a0 = WMN ? sdesc(base_u, 8192, 1024, 2) : sdesc(base_u, 16, 1024, 2);
+        const uint64_t b0 = sdesc(base_u + kOperand, 16, 1024, 2);
+        int s = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int k = k0; k < k1; ++k) {
+            ok = wait_warp(&S.full[s], phase, &S.abort, p.status, p.limit);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t da = a0 + s * (stage >> 4), db = b0 + s * (stage >> 4);
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk) mma_bf16(tmem, da + kk * step, db + kk * 2, id, k > k0 || kk > 0);
+                mma_commit(&S.empty[s]);
+                if (k + 1 == k1) mma_commit(&S.done);
+            }
+            __syncwarp();
+            if (++s == p.stages) { s = 0; phase ^= 1; }
+        }
+        if (ok && k1 > k0) ok = wait_warp(&S.done, 0, &S.abort, p.status, p.limit);
+        if (!ok && lane == 0 && (s > 0 || phase)) drain(&S.empty[s ? s - 1 : p.stages - 1], s ? phase : phase ^ 1, p.limit);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // sums as [row of x][128 columns], over the stages that nothing reads any more
+    float* sums = reinterpret_cast<float*>(base);
+    const bool good = *(volatile int*)&S.abort == 0;
+    if (good) {
+        const int part = warp & 3, half = p.bn / 2;
+        for (int c = (warp >> 2) * half; c < ((warp >> 2) + 1) * half; c += 8) {
+            float v[8];
+            tmem_ld8(tmem_addr(tmem, part * 32, c), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sums[(c + i) * 128 + part * 32 + lane] = k1 > k0 ? v[i] : 0.f;
+        }
+    }
+    tc_fence_before();
+    cluster_sync();
+    if (good) {
+        constexpr int kGroups = MODE == kGated ? 8 : 16;             // of 8 columns
+        const int items = p.N * kGroups, share = (items + ranks - 1) / ranks;
+        const int last = min(items, (rank + 1) * share);
+        for (int i = rank * share + (int)threadIdx.x; i < last; i += kNarrowThreads) {
+            const int t = i / kGroups, g8 = i % kGroups * 8, col = first + g8;
+            if (col >= p.wide) continue;
+            float v[8] = {}, u[8] = {};
+            for (int q = 0; q < ranks; ++q) {
+                const uint32_t at = peer_addr(sums + t * 128 + g8, q);
+                const float4 a = peer_load4(at), b = peer_load4(at + 16);
+                v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+                v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+                if constexpr (MODE == kGated) {
+                    const float4 c = peer_load4(at + 256), d = peer_load4(at + 272);
+                    u[0] += c.x; u[1] += c.y; u[2] += c.z; u[3] += c.w;
+                    u[4] += d.x; u[5] += d.y; u[6] += d.z; u[7] += d.w;
+                }
+            }
+            if constexpr (MODE == kStore) {
+                if (p.add) {
+                    float r[8];
+                    unpack8(*reinterpret_cast<const uint4*>(p.add + t * p.add_row + col), r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += r[j];
+                }
+                *reinterpret_cast<uint4*>(p.out + (long long)t * p.wide + col) = pack8(v);
+            } else {
+                bf16* gu = p.gu + (long long)t * 2 * p.F + col;
+                uint4* h = reinterpret_cast<uint4*>(p.h + (long long)t * p.F + col);
+                if constexpr (MODE == kGated) {
+                    if (p.gu) {
+                        *reinterpret_cast<uint4*>(gu) = pack8(v);
+                        *reinterpret_cast<uint4*>(gu + p.F) = pack8(u);
+                    }
+                    float unused;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = act<false>(v[j], p.gelu, unused) * u[j];
+                    *h = pack8(v);
+                } else {
+                    float g[8], hh[8];
+                    unpack8(*reinterpret_cast<const uint4*>(gu), g);
+                    unpack8(*reinterpret_cast<const uint4*>(gu + p.F), u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float slope;
+                        const float a = act<true>(g[j], p.gelu, slope);
+                        hh[j] = a * u[j];
+                        g[j] = v[j] * u[j] * slope;
+                        u[j] = v[j] * a;
+                    }
+                    bf16* dgu = p.out + (long long)t * 2 * p.F + col;
+                    *reinterpret_cast<uint4*>(dgu) = pack8(g);
+                    *reinterpret_cast<uint4*>(dgu + p.F) = pack8(u);
+                    *h = pack8(hh);
+                }
+            }
+        }
+    }
+    cluster_sync();                                     // no block leaves while its sums are read
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, kNarrow);
 }
 
 // ----------------------------------------------------------------------------- host
@@ -414,15 +684,105 @@ bool problem(Problem& q, int M, int N, int K, int mode) {
     return tiles < (1LL << 30);
 }
 
+// Clusters of `width` blocks that run at once (a cluster stays within a group of SMs).
+template <bool AMN, bool BMN, int MODE>
+int clusters_at_once(int width) {
+    static std::atomic<int> known[9];
+    const int k = known[width].load(std::memory_order_relaxed);
+    if (k > 0) return k;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = width;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(width);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = kSmem<MODE>;
+    c.attrs = at;
+    c.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, ffn_gemm_kernel<AMN, BMN, MODE, true>, &c) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    if (n < 1) n = 1;
+    known[width].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Pairs that share a tile, by what the rounds of tiles take in blocks of K (650 cycles each): a tile alone in its round
+// also waits for its own epilogue (about 6 blocks), and for the sums to pass between the pairs (4 more).
+template <bool AMN, bool BMN, int MODE>
+int splits_for(const GemmParams& p) {
+    const int K = p.q[0].K > p.q[1].K ? p.q[0].K : p.q[1].K, kblocks = (K + kBK - 1) / kBK;
+    if (p.tiles > 2 * kPairs) return 1;
+    int best = 1;
+    double least = (double)((p.tiles + kPairs - 1) / kPairs) * kblocks + 6;
+    for (int n = 2; n <= 4; ++n) {
+        const int each = (kblocks + n - 1) / n;
+        if (each < 4 || (kblocks + each - 1) / each != n) continue;
+        const int at_once = clusters_at_once<AMN, BMN, MODE>(2 * n);
+        const double rounds = (p.tiles + at_once - 1) / at_once, blocks = rounds * (each + 10);
+        if (blocks < least) {
+            least = blocks;
+            best = n;
+        }
+    }
+    return best;
+}
+
+template <bool AMN, bool BMN, int MODE, bool SPLIT>
+cudaError_t launch(const Maps& m0, const Maps& m1, const GemmParams& p, int blocks, bool overlap, cudaStream_t s) {
+    static_assert(kSmem<MODE> <= 232448, "shared memory of a block");
+    static_assert(!SPLIT || kStages<MODE> * kStageBytes >= kTile * kBM * 4, "the sums of a block");
+    auto kernel = ffn_gemm_kernel<AMN, BMN, MODE, SPLIT>;
+    return launch_in_clusters(kernel, dim3(blocks), dim3(kThreads), kSmem<MODE>, s, SPLIT ? 2 * p.splits : 2, overlap, m0, m1,
+                              p);
+}
+
 template <bool AMN, bool BMN, int MODE>
 cudaError_t gemm(const Maps& m0, const Maps& m1, GemmParams p, bool overlap, cudaStream_t s) {
     p.tiles = p.q[0].tiles + p.q[1].tiles;
-    static_assert(kSmem<MODE> <= 232448, "shared memory of a block");
-    auto kernel = ffn_gemm_kernel<AMN, BMN, MODE>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<MODE>);
+    cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<AMN, BMN, MODE, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmem<MODE>);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(ffn_gemm_kernel<AMN, BMN, MODE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<MODE>);
     if (e != cudaSuccess) return e;
-    const int pairs = p.tiles < kPairs ? p.tiles : kPairs;
-    return launch_in_clusters(kernel, dim3(2 * pairs), dim3(kThreads), kSmem<MODE>, s, 2, overlap, m0, m1, p);
+    p.splits = splits_for<AMN, BMN, MODE>(p);
+    if (p.splits > 1) return launch<AMN, BMN, MODE, true>(m0, m1, p, 2 * p.splits * p.tiles, overlap, s);
+    return launch<AMN, BMN, MODE, false>(m0, m1, p, 2 * (p.tiles < kPairs ? p.tiles : kPairs), overlap, s);
+}
+
+// Splits of K: as many as fill two blocks an SM, of two blocks of K at least.
+template <bool WMN, int MODE>
+cudaError_t narrow(const CUtensorMap& mw, const Matrix& x, NarrowParams p, bool overlap, cudaStream_t s) {
+    const int columns = MODE == kGated ? 64 : 128, tiles = (p.wide + columns - 1) / columns;
+    const int kblocks = (p.K + kBK - 1) / kBK;
+    int splits = 2 * 2 * kPairs / tiles;
+    splits = splits > 8 ? 8 : splits;
+    if (splits > kblocks / 2) splits = kblocks / 2;
+    if (splits < 1) splits = 1;
+    p.kblocks = (kblocks + splits - 1) / splits;
+    splits = (kblocks + p.kblocks - 1) / p.kblocks;
+    p.bn = (p.N + 15) / 16 * 16;
+    const int stage = kOperand + p.bn * 128, room = kNarrowSmem - 1024;
+    p.stages = room / stage < kNarrowStages ? room / stage : kNarrowStages;
+    CUtensorMap mx;
+    if (!x.map(&mx, 64, p.bn, TmaSwizzle::b128)) return cudaErrorInvalidValue;
+    auto kernel = ffn_narrow_kernel<WMN, MODE>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
+    if (e != cudaSuccess) return e;
+    return launch_in_clusters(kernel, dim3(tiles * splits), dim3(kNarrowThreads), kNarrowSmem, s, splits, overlap, mw, mx, p);
+}
+
+NarrowParams narrow_params(const FfnArgs& a) {
+    NarrowParams p{};
+    p.N = a.N;
+    p.F = a.F;
+    p.gelu = a.gelu;
+    p.status = a.status;
+    p.limit = a.wait_cycles > 0 ? a.wait_cycles : kWaitCycles;
+    return p;
 }
 
 GemmParams params(const FfnArgs& a) {
@@ -444,6 +804,26 @@ cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     const Matrix x{a.x, N, D, a.x_row}, wi{a.W_in, D, 2 * F, 2 * F}, wo{a.W_out, F, D, D}, h{a.workspace, N, F, F},
         y{a.y, N, D, D}, gu{a.gu, N, 2 * F, 2 * F}, res{a.residual, N, D, a.residual_row};
     *launches = 2;
+    if (a.N <= kNarrow) {
+        NarrowParams p = narrow_params(a);
+        CUtensorMap w;
+        p.wide = a.F;
+        p.K = a.D;
+        p.h = static_cast<bf16*>(a.workspace);
+        p.gu = static_cast<bf16*>(a.gu);
+        p.debug_stall = a.debug_stall;
+        if (!wi.halves(&w, 64, 64, TmaSwizzle::b128)) return cudaErrorInvalidValue;
+        const cudaError_t e = narrow<true, kGated>(w, x, p, false, s);
+        if (e != cudaSuccess) return e;
+        NarrowParams o = narrow_params(a);
+        o.wide = a.D;
+        o.K = a.F;
+        o.out = static_cast<bf16*>(a.y);
+        o.add = static_cast<const bf16*>(a.residual);
+        o.add_row = a.residual_row;
+        if (!wo.operand(&w, true)) return cudaErrorInvalidValue;
+        return narrow<true, kStore>(w, h, o, true, s);
+    }
     Maps m{};
     GemmParams p = params(a);
     p.save = a.gu != nullptr;
@@ -469,15 +849,39 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         gu{a.gu, N, 2 * F, 2 * F}, dgu{ws, N, 2 * F, 2 * F}, h{ws + (size_t)N * F * 4, N, F, F}, dx{a.dx, N, D, D},
         dwi{a.dW_in, D, 2 * F, 2 * F}, dwo{a.dW_out, F, D, D};
     *launches = 1;
-    Maps m{};
-    GemmParams p = params(a);
-    p.debug_stall = a.debug_stall;
-    if (!dy.operand(&m.a, false) || !wo.operand(&m.b, false) || !dgu.halves(&m.out, 32, 32, TmaSwizzle::b64) ||
-        !gu.halves(&m.aux, 32, 32, TmaSwizzle::b64) || !h.piece(&m.h) || !problem(p.q[0], a.N, a.F, a.D, kGatedBack))
-        return cudaErrorInvalidValue;
-    cudaError_t e = gemm<false, false, kGatedBack>(m, m, p, false, s);
+    cudaError_t e;
+    if (a.N <= kNarrow) {
+        NarrowParams p = narrow_params(a);
+        CUtensorMap w;
+        p.wide = a.F;
+        p.K = a.D;
+        p.out = static_cast<bf16*>(const_cast<void*>(dgu.p));
+        p.h = static_cast<bf16*>(const_cast<void*>(h.p));
+        p.gu = static_cast<bf16*>(a.gu);
+        p.debug_stall = a.debug_stall;
+        if (!wo.operand(&w, false)) return cudaErrorInvalidValue;
+        e = narrow<false, kGatedBack>(w, dy, p, false, s);
+    } else {
+        Maps m{};
+        GemmParams p = params(a);
+        p.debug_stall = a.debug_stall;
+        if (!dy.operand(&m.a, false) || !wo.operand(&m.b, false) || !dgu.halves(&m.out, 32, 32, TmaSwizzle::b64) ||
+            !gu.halves(&m.aux, 32, 32, TmaSwizzle::b64) || !h.piece(&m.h) || !problem(p.q[0], a.N, a.F, a.D, kGatedBack))
+            return cudaErrorInvalidValue;
+        e = gemm<false, false, kGatedBack>(m, m, p, false, s);
+    }
     if (e != cudaSuccess) return e;
-    if (a.dx) {
+    if (a.dx && a.N <= kNarrow) {
+        NarrowParams o = narrow_params(a);
+        CUtensorMap w;
+        o.wide = a.D;
+        o.K = 2 * a.F;
+        o.out = static_cast<bf16*>(a.dx);
+        if (!wi.operand(&w, false)) return cudaErrorInvalidValue;
+        e = narrow<false, kStore>(w, dgu, o, true, s);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    } else if (a.dx) {
         GemmParams o = params(a);
         Maps n{};
         if (!dgu.operand(&n.a, false) || !wi.operand(&n.b, false) || !dx.piece(&n.out) ||
