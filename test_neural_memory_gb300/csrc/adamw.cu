@@ -54,21 +54,22 @@ __device__ __forceinline__ uint32_t hash32(uint32_t x) {
     return x ^ (x >> 16);
 }
 
-// The power of two, as an exponent, that a block's largest size is divided by.
-__device__ __forceinline__ int scale_of(float most) {
-    const uint32_t u = __float_as_uint(most);
-    const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u);
+// The power of two, as an exponent, that a block's largest size (its bits) is divided by.
+__device__ __forceinline__ int scale_of(uint32_t most) {
+    const int e = (int)(most >> 23) - 127 - 8 + ((most & 0x7fffffu) > 0x600000u);
     return max(e, -126);
 }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// x / 2^e on e4m3's grid: down, or up where the missing part of a step and `frac` make one.  What is not a
-// number or infinite becomes NaN (e4m3 has no infinity).
-__device__ __forceinline__ float to_grid(float x, float inverse, float frac) {
+// The e4m3 code of the finite |x| / 2^e (times `inverse`, exact): its lower neighbour on the grid, or the upper one where
+// the missing part of a step and `frac` (in 2^-16) make one.  Above 2^-6 adding frac below the three bits that stay
+// carries by itself; below, steps are 2^-9 and the sum of both parts is rounded to 24 bits before the floor.
+__device__ __forceinline__ uint32_t to_code(float x, float inverse, uint32_t frac) {
     const float y = fabsf(x) * inverse;
-    const int b = max((int)(__float_as_uint(y) >> 23) - 127, -6);
-    const float q = floorf(__fadd_rn(y * power(3 - b), frac)) * power(b - 3);
-    return isfinite(x) ? copysignf(q, x) : __uint_as_float(0x7fc00000u);
+    const uint32_t u = __float_as_uint(y);
+    uint32_t code = ((u + (frac << 4)) >> 20) - (120u << 3);
+    if (u < 0x3c800000u) code = (uint32_t)__fadd_rn(y * 512.f, (float)frac * (1.f / 65536.f));
+    return code | (__float_as_uint(x) >> 24 & 0x80u);
 }
 
 __device__ __forceinline__ float4 decode4(uint32_t code) {
@@ -82,17 +83,9 @@ __device__ __forceinline__ float decode1(unsigned char code) {
     const __half_raw h = __nv_cvt_fp8_to_halfraw(code, __NV_E4M3);
     return __half2float(*reinterpret_cast<const __half*>(&h));
 }
-__device__ __forceinline__ uint32_t encode4(const float* f) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
-    return lo | hi << 16;
-}
-
-__device__ __forceinline__ float warp_most(float x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
-}
+// Sizes compare as their bits do.
+__device__ __forceinline__ uint32_t size_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+constexpr uint32_t kInf = 0x7f800000u;
 
 __device__ __forceinline__ Consts constants(const AdamwScalars& a) {
     Consts k;
@@ -115,10 +108,10 @@ __device__ __forceinline__ void moments(const Consts& k, float g, float& m, floa
     v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.c2));
 }
 __device__ __forceinline__ float update(const Consts& k, float p, float m, float root) {
-    return fmaf(p, k.keep, -__fdividef(k.lr1 * m, fmaf(root, k.root2, k.eps)));
+    float r;                            // 1 unit off
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(root, k.root2, k.eps)));
+    return fmaf(-(k.lr1 * m), r, p * k.keep);
 }
-
-__device__ __forceinline__ float finite_size(float x) { return isfinite(x) ? fabsf(x) : 0.f; }
 
 // One block of up to 256 values by a warp.  VEC: 256 of them, in runs of 4 a lane; otherwise lane l takes the
 // values l, l + 32, ..
@@ -178,7 +171,7 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
         ms = a.m_scale[e.first + block];
         vs = a.v_scale[e.first + block];
     }
-    float most_m = 0.f, most_r = 0.f;
+    uint32_t most_m = 0, most_r = 0, mc[8], vc[8];      // largest sizes; codes
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         if constexpr (EIGHT) {
@@ -192,20 +185,60 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
         if constexpr (EIGHT) {
             v[j] = root;
             if (VEC || index(j) < n) {
-                most_m = fmaxf(most_m, finite_size(m[j]));
-                most_r = fmaxf(most_r, finite_size(root));
+                most_m = max(most_m, size_bits(m[j]));
+                most_r = max(most_r, size_bits(root));
             }
         }
     }
-    if constexpr (EIGHT) {
-        const int em = scale_of(warp_most(most_m)), er = scale_of(warp_most(most_r));
-        const float im = power(-em), ir = power(-er);
+    if constexpr (VEC) {                // the weights leave first: the codes take registers
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = h * 128 + lane * 4;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(p[4 * h], p[4 * h + 1]);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(p[4 * h + 2], p[4 * h + 3]);
+            const uint2 half = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            if (e.p_bf16) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(e.p) + i0 + i) = half;
+            else *reinterpret_cast<float4*>(static_cast<float*>(e.p) + i0 + i) = *reinterpret_cast<float4*>(p + 4 * h);
+            if (e.copy) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(e.copy) + i0 + i) = half;
+        }
+    } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const unsigned long long at = (unsigned long long)s0 + index(j);
-            const uint32_t h = hash32((uint32_t)at + k.key + (uint32_t)(at >> 32) * 0x85ebca6bu);
-            m[j] = to_grid(m[j], im, (float)(h & 0xffffu) * (1.f / 65536.f));
-            v[j] = to_grid(v[j], ir, (float)(h >> 16) * (1.f / 65536.f));
+            const int i = lane + 32 * j;
+            if (i >= n) continue;
+            if (e.p_bf16) static_cast<__nv_bfloat16*>(e.p)[i0 + i] = __float2bfloat16_rn(p[j]);
+            else static_cast<float*>(e.p)[i0 + i] = p[j];
+            if (e.copy) static_cast<__nv_bfloat16*>(e.copy)[i0 + i] = __float2bfloat16_rn(p[j]);
+        }
+    }
+    if constexpr (EIGHT) {
+        most_m = __reduce_max_sync(0xffffffffu, most_m);
+        most_r = __reduce_max_sync(0xffffffffu, most_r);
+        const bool odd = max(most_m, most_r) >= kInf;   // a value that is not finite: the scale goes by the others
+        if (odd) {
+            most_m = most_r = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (!VEC && index(j) >= n) continue;
+                if (size_bits(m[j]) < kInf) most_m = max(most_m, size_bits(m[j]));
+                if (size_bits(v[j]) < kInf) most_r = max(most_r, size_bits(v[j]));
+            }
+            most_m = __reduce_max_sync(0xffffffffu, most_m);
+            most_r = __reduce_max_sync(0xffffffffu, most_r);
+        }
+        const int em = scale_of(most_m), er = scale_of(most_r);
+        const float im = power(-em), ir = power(-er);
+        // a block's places differ in their low 8 bits
+        const uint32_t key = (uint32_t)s0 + k.key + (uint32_t)((unsigned long long)s0 >> 32) * 0x85ebca6bu;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t h = hash32(key + index(j));
+            mc[j] = to_code(m[j], im, h & 0xffffu);
+            vc[j] = to_code(v[j], ir, h >> 16);
+            if (odd) {                                  // e4m3 has no infinity
+                if (size_bits(m[j]) >= kInf) mc[j] = 0x7f;
+                if (size_bits(v[j]) >= kInf) vc[j] = 0x7f;
+            }
         }
         if (lane == 0) {
             a.m_scale[e.first + block] = power(em);
@@ -216,15 +249,11 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int i = h * 128 + lane * 4;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(p[4 * h], p[4 * h + 1]);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(p[4 * h + 2], p[4 * h + 3]);
-            const uint2 half = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-            if (e.p_bf16) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(e.p) + i0 + i) = half;
-            else *reinterpret_cast<float4*>(static_cast<float*>(e.p) + i0 + i) = *reinterpret_cast<float4*>(p + 4 * h);
-            if (e.copy) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(e.copy) + i0 + i) = half;
             if constexpr (EIGHT) {
-                *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.m) + s0 + i) = encode4(m + 4 * h);
-                *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.v) + s0 + i) = encode4(v + 4 * h);
+                const uint32_t* x = mc + 4 * h;
+                const uint32_t* r = vc + 4 * h;
+                *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.m) + s0 + i) = x[0] | x[1] << 8 | x[2] << 16 | x[3] << 24;
+                *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.v) + s0 + i) = r[0] | r[1] << 8 | r[2] << 16 | r[3] << 24;
             } else {
                 *reinterpret_cast<float4*>(static_cast<float*>(a.m) + s0 + i) = *reinterpret_cast<float4*>(m + 4 * h);
                 *reinterpret_cast<float4*>(static_cast<float*>(a.v) + s0 + i) = *reinterpret_cast<float4*>(v + 4 * h);
@@ -235,12 +264,9 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
         for (int j = 0; j < 8; ++j) {
             const int i = lane + 32 * j;
             if (i >= n) continue;
-            if (e.p_bf16) static_cast<__nv_bfloat16*>(e.p)[i0 + i] = __float2bfloat16_rn(p[j]);
-            else static_cast<float*>(e.p)[i0 + i] = p[j];
-            if (e.copy) static_cast<__nv_bfloat16*>(e.copy)[i0 + i] = __float2bfloat16_rn(p[j]);
             if constexpr (EIGHT) {
-                static_cast<unsigned char*>(a.m)[s0 + i] = __nv_cvt_float_to_fp8(m[j], __NV_SATFINITE, __NV_E4M3);
-                static_cast<unsigned char*>(a.v)[s0 + i] = __nv_cvt_float_to_fp8(v[j], __NV_SATFINITE, __NV_E4M3);
+                static_cast<unsigned char*>(a.m)[s0 + i] = (unsigned char)mc[j];
+                static_cast<unsigned char*>(a.v)[s0 + i] = (unsigned char)vc[j];
             } else {
                 static_cast<float*>(a.m)[s0 + i] = m[j];
                 static_cast<float*>(a.v)[s0 + i] = v[j];
@@ -250,7 +276,7 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
 }
 
 template <bool EIGHT, int CAP>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> t,
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Table<CAP> t,
                                                           const __grid_constant__ AdamwScalars a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Consts k = constants(a);

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "pairs.cuh"
 #include "train_ops.h"
@@ -23,7 +24,7 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kBatch = 4;               // rows whose loads are in flight together
 constexpr int kFwdThreads = 128;
-constexpr int kBwdThreads = 256;
+constexpr int kBwdThreads = 128, kBwdBlocks = 3;       // blocks an SM
 
 // V values of a row as they are stored, and as fp32: pairs of values (two results an instruction), or one.
 template <int BYTES> struct Word;
@@ -84,13 +85,34 @@ __device__ __forceinline__ Val<V> gather(const float* p, long long step) {     /
     if constexpr (V == 1) return p[0];
     else return pair(p[0], p[step]);
 }
+// The K taps of V channels from c on, tap i in slot i + KW - K.  kAll: four taps on 16 bytes.
+template <int V, int KW, bool kAll>
+__device__ __forceinline__ void load_taps(Val<V> (&w)[KW][kVals<V>], const float* p, int c, int K) {
+    constexpr int step = V / kVals<V>;
+#pragma unroll
+    for (int v = 0; v < kVals<V>; ++v) {
+        if constexpr (kAll) {
+            const float4 a = reinterpret_cast<const float4*>(p)[c + step * v];
+            if constexpr (V == 1) {
+                w[0][v] = a.x; w[1][v] = a.y; w[2][v] = a.z; w[3][v] = a.w;
+            } else {
+                const float4 b = reinterpret_cast<const float4*>(p)[c + step * v + 1];
+                w[0][v] = pair(a.x, b.x); w[1][v] = pair(a.y, b.y); w[2][v] = pair(a.z, b.z); w[3][v] = pair(a.w, b.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < KW; ++i)
+                w[i][v] = i >= KW - K ? gather<V>(p + (long long)(c + step * v) * K + i - (KW - K), K) : splat<Val<V>>(0.f);
+        }
+    }
+}
 template <typename E> __device__ __forceinline__ E zero() { return splat<E>(0.f); }
 
-// 1 / (1 + exp(-x)).  bf16 results take the fast exponential and division (a few 2^-22 off, |x| 2^-24 more).
+// 1 / (1 + exp(-x)); the fast one for bf16 results.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float x) {
     if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-x));
-    else return __fdividef(1.f, 1.f + __expf(-x));
+    else return fast_logistic(x);
 }
 template <typename T>
 __device__ __forceinline__ f2 sigmoid(f2 x) {
@@ -190,48 +212,46 @@ __global__ void __launch_bounds__(kFwdThreads) conv_fwd_kernel(const __grid_cons
         unpack<T, V>(raw, win[i]);
         if (DOC) ids[i] = doc[max(t, 0)];
     }
+    load_taps<V, KW, kAll>(w, a.w, c, K);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int ch = c + v * (V / NV);
-        bias[v] = a.b ? gather<V>(a.b + ch, 1) : zero<Val<V>>();
-#pragma unroll
-        for (int i = 0; i < KW; ++i)
-            w[i][v] = i >= before ? gather<V>(a.w + (long long)ch * K + i - before, K) : zero<Val<V>>();
-    }
+    for (int v = 0; v < NV; ++v) bias[v] = a.b ? gather<V>(a.b + c + v * (V / NV), 1) : zero<Val<V>>();
     T* y = static_cast<T*>(a.y) + ((long long)n * a.T + t0) * C + c;
-    for (int t = t0; t < t1; t += kBatch) {
+    auto token = [&](const Raw<T, V>& raw, int raw_id) {
+#pragma unroll
+        for (int i = 0; i + 1 < KW; ++i) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) win[i][v] = win[i + 1][v];
+            if (DOC) ids[i] = ids[i + 1];
+        }
+        unpack<T, V>(raw, win[KW - 1]);
+        if (DOC) ids[KW - 1] = raw_id;
+        Val<V> out[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) out[v] = bias[v];
+        taps<V, KW, kAll, DOC>(out, w, win, ids, before);
+        if (a.silu) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) out[v] = mul(out[v], sigmoid<T>(out[v]));
+        }
+        store<T, V>(y, out);
+        y += C;
+    };
+    int t = t0;
+    for (; t + kBatch <= t1; t += kBatch) {             // whole batches: the window stays in place
         Raw<T, V> raw[kBatch];
         int raw_id[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             raw[j] = next[j];
-            if (DOC) raw_id[j] = next_id[j];
+            raw_id[j] = DOC ? next_id[j] : 0;
         }
         fetch(t + kBatch);
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            if (t + j < t1) {
-#pragma unroll
-                for (int i = 0; i + 1 < KW; ++i) {
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) win[i][v] = win[i + 1][v];
-                    if (DOC) ids[i] = ids[i + 1];
-                }
-                unpack<T, V>(raw[j], win[KW - 1]);
-                if (DOC) ids[KW - 1] = raw_id[j];
-                Val<V> out[NV];
-#pragma unroll
-                for (int v = 0; v < NV; ++v) out[v] = bias[v];
-                taps<V, KW, kAll, DOC>(out, w, win, ids, before);
-                if (a.silu) {
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) out[v] = mul(out[v], sigmoid<T>(out[v]));
-                }
-                store<T, V>(y, out);
-                y += C;
-            }
-        }
+        for (int j = 0; j < kBatch; ++j) token(raw[j], raw_id[j]);
     }
+#pragma unroll
+    for (int j = 0; j + 1 < kBatch; ++j)
+        if (t + j < t1) token(next[j], DOC ? next_id[j] : 0);
     if (a.state && part + 1 == strips) {
         T* s = static_cast<T*>(a.state) + (long long)n * (K - 1) * C + c;
 #pragma unroll
@@ -259,7 +279,7 @@ __global__ void conv_pass_kernel(const T* from, T* to, long long n) {
 // one part of the block's row of the grid, joined by conv_join_kernel in the rows' order: equal inputs give
 // equal bits.
 template <typename T, int V, int KW, bool kAll, bool DOC>
-__global__ void __launch_bounds__(kBwdThreads, 2) conv_bwd_kernel(const __grid_constant__ ConvArgs a, int groups,
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const __grid_constant__ ConvArgs a, int groups,
                                                                 int strips, int strip) {
     constexpr int NV = kVals<V>;
     using E = Val<V>;
@@ -269,16 +289,13 @@ __global__ void __launch_bounds__(kBwdThreads, 2) conv_bwd_kernel(const __grid_c
     const bool live = group < groups;
     const int c = live ? group * V : 0;
     E w[KW][NV], bias[NV], dw[KW][NV], db[NV];
+    load_taps<V, KW, kAll>(w, a.w, c, K);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int ch = c + v * (V / NV);
-        bias[v] = a.b ? gather<V>(a.b + ch, 1) : zero<E>();
+        bias[v] = a.b ? gather<V>(a.b + c + v * (V / NV), 1) : zero<E>();
         db[v] = zero<E>();
 #pragma unroll
-        for (int i = 0; i < KW; ++i) {
-            w[i][v] = i >= before ? gather<V>(a.w + (long long)ch * K + i - before, K) : zero<E>();
-            dw[i][v] = zero<E>();
-        }
+        for (int i = 0; i < KW; ++i) dw[i][v] = zero<E>();
     }
     const long long total = live ? (long long)a.N * strips : 0;
     for (long long s = (long long)blockIdx.y * blockDim.y + threadIdx.y; s < total;
@@ -321,71 +338,63 @@ __global__ void __launch_bounds__(kBwdThreads, 2) conv_bwd_kernel(const __grid_c
 #pragma unroll
             for (int v = 0; v < NV; ++v) d[i][v] = zero<E>();
         }
-        for (int t = t0; t < t1 + KW - 1; t += kBatch) {
-            Raw<T, V> raw[kBatch], draw[kBatch];
-            int raw_id[kBatch];
+        // One token: kInner where it is of the strip, its row to leave too, and neither is next to an end.
+        auto token = [&](auto inner, int now, const Raw<T, V>& raw, const Raw<T, V>& draw, int raw_id) {
+            constexpr bool kInner = decltype(inner)::value;
+            const int row = now - (KW - 1);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                raw[j] = next[j];
-                draw[j] = dnext[j];
-                if (DOC) raw_id[j] = next_id[j];
+            for (int i = 0; i + 1 < KW; ++i) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    win[i][v] = win[i + 1][v];
+                    d[i][v] = d[i + 1][v];
+                }
+                if (DOC) ids[i] = ids[i + 1];
             }
-            fetch(t + kBatch);
+            if (kInner || now < end) {
+                unpack<T, V>(raw, win[KW - 1]);
+                unpack<T, V>(draw, d[KW - 1]);
+                if (DOC) ids[KW - 1] = raw_id;
+                if (a.silu) {
+                    E pre[NV];
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int now = t + j, row = now - (KW - 1);
-#pragma unroll
-                for (int i = 0; i + 1 < KW; ++i) {
+                    for (int v = 0; v < NV; ++v) pre[v] = bias[v];
+                    taps<V, KW, kAll, DOC>(pre, w, win, ids, before);
 #pragma unroll
                     for (int v = 0; v < NV; ++v) {
-                        win[i][v] = win[i + 1][v];
-                        d[i][v] = d[i + 1][v];
+                        const E g = sigmoid<T>(pre[v]);
+                        // 1 + pre (1 - g)
+                        const E up = fma(pre[v], fma(g, splat<E>(-1.f), splat<E>(1.f)), splat<E>(1.f));
+                        d[KW - 1][v] = mul(d[KW - 1][v], mul(g, up));
                     }
-                    if (DOC) ids[i] = ids[i + 1];
                 }
-                if (now < end) {
-                    unpack<T, V>(raw[j], win[KW - 1]);
-                    unpack<T, V>(draw[j], d[KW - 1]);
-                    if (DOC) ids[KW - 1] = raw_id[j];
-                    if (a.silu) {
-                        E pre[NV];
+                if (kInner || now < t1) {
 #pragma unroll
-                        for (int v = 0; v < NV; ++v) pre[v] = bias[v];
-                        taps<V, KW, kAll, DOC>(pre, w, win, ids, before);
+                    for (int i = 0; i < KW; ++i) {
+                        if ((!kAll && i < before) || (DOC && ids[i] != ids[KW - 1])) continue;
 #pragma unroll
-                        for (int v = 0; v < NV; ++v) {
-                            const E g = sigmoid<T>(pre[v]);
-                            // 1 + pre (1 - g)
-                            const E up = fma(pre[v], fma(g, splat<E>(-1.f), splat<E>(1.f)), splat<E>(1.f));
-                            d[KW - 1][v] = mul(d[KW - 1][v], mul(g, up));
-                        }
+                        for (int v = 0; v < NV; ++v) dw[i][v] = fma(d[KW - 1][v], win[i][v], dw[i][v]);
                     }
-                    if (now < t1) {
 #pragma unroll
-                        for (int i = 0; i < KW; ++i) {
-                            if ((!kAll && i < before) || (DOC && ids[i] != ids[KW - 1])) continue;
-#pragma unroll
-                            for (int v = 0; v < NV; ++v) dw[i][v] = fma(d[KW - 1][v], win[i][v], dw[i][v]);
-                        }
-#pragma unroll
-                        for (int v = 0; v < NV; ++v) db[v] = add(db[v], d[KW - 1][v]);
-                    }
-                } else {                // past the sequence, or past what the strip's rows need
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) d[KW - 1][v] = zero<E>();
-                    if (DOC) ids[KW - 1] = id_last;
+                    for (int v = 0; v < NV; ++v) db[v] = add(db[v], d[KW - 1][v]);
                 }
-                if (row >= first_row && row < t1) {
-                    // row + m met row in its tap K - 1 - m, slot KW - 1 - m
-                    E out[NV];
+            } else {                    // past the sequence, or past what the strip's rows need
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) out[v] = zero<E>();
+                for (int v = 0; v < NV; ++v) d[KW - 1][v] = zero<E>();
+                if (DOC) ids[KW - 1] = id_last;
+            }
+            if (kInner || (row >= first_row && row < t1)) {
+                // row + m met row in its tap K - 1 - m, slot KW - 1 - m
+                E out[NV];
 #pragma unroll
-                    for (int m = 0; m < KW; ++m) {
-                        if ((!kAll && m >= K) || (DOC && ids[m] != ids[0])) continue;
+                for (int v = 0; v < NV; ++v) out[v] = zero<E>();
 #pragma unroll
-                        for (int v = 0; v < NV; ++v) out[v] = fma(w[KW - 1 - m][v], d[m][v], out[v]);
-                    }
+                for (int m = 0; m < KW; ++m) {
+                    if ((!kAll && m >= K) || (DOC && ids[m] != ids[0])) continue;
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) out[v] = fma(w[KW - 1 - m][v], d[m][v], out[v]);
+                }
+                if constexpr (!kInner) {
                     const int tail = row - (a.T - (K - 1));
                     if (ds && tail >= 0 && (!DOC || ids[0] == id_last)) {
                         E f[NV];
@@ -393,7 +402,33 @@ __global__ void __launch_bounds__(kBwdThreads, 2) conv_bwd_kernel(const __grid_c
 #pragma unroll
                         for (int v = 0; v < NV; ++v) out[v] = add(out[v], f[v]);
                     }
-                    store<T, V>(row >= 0 ? dx + (long long)row * C : ds0 + (long long)(row + K - 1) * C, out);
+                }
+                store<T, V>(kInner || row >= 0 ? dx + (long long)row * C : ds0 + (long long)(row + K - 1) * C, out);
+            }
+        };
+        // rows up to t1 - KW leave within the strip: before T - K + 1, where dstate begins
+        for (int t = t0; t < t1 + KW - 1; t += kBatch) {
+            Raw<T, V> raw[kBatch], draw[kBatch];
+            int raw_id[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                raw[j] = next[j];
+                draw[j] = dnext[j];
+                raw_id[j] = DOC ? next_id[j] : 0;
+            }
+            fetch(t + kBatch);
+            if (t - (KW - 1) >= t0 && t + kBatch <= t1) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) token(std::true_type{}, t + j, raw[j], draw[j], raw_id[j]);
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < kBatch; ++j) {      // (one copy of the code for the few tokens at the ends)
+                    Raw<T, V> r = raw[0], q = draw[0];
+                    int id = raw_id[0];
+#pragma unroll
+                    for (int i = 1; i < kBatch; ++i)
+                        if (j == i) { r = raw[i]; q = draw[i]; id = raw_id[i]; }
+                    token(std::false_type{}, t + j, r, q, id);
                 }
             }
         }
@@ -472,11 +507,11 @@ cudaError_t fwd(const ConvArgs& a, bool one_strip, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// Rows of the gradient's grid at most, by the widest channel groups that a call may take; the workspace holds
-// a part for each.
+// Rows of the gradient's grid at most, one wave by the widest channel groups that a call may take; the workspace
+// holds a part for each.
 int most_rows(int C) {
     const int across = ((C + 3) / 4 + 31) / 32;
-    const int rows = kSms * 4 / across;
+    const int rows = kSms * kBwdBlocks / across;
     return rows < 1 ? 1 : rows;
 }
 
@@ -486,11 +521,16 @@ cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
     int bx = 1;
     while (bx < groups && bx < 32) bx *= 2;
     const int by = kBwdThreads / bx, across = (groups + bx - 1) / bx;
-    int strip = 128;
-    while (strip > 16 && (long long)a.N * ((a.T + strip - 1) / strip) < (long long)by * most_rows(a.C)) strip /= 2;
+    // One strip a thread where the sequences are fewer than the threads of a column of the grid, of 16 tokens at least.
+    int rows = kSms * kBwdBlocks / across;
+    if (rows > most_rows(a.C)) rows = most_rows(a.C);
+    if (rows < 1) rows = 1;
+    const long long places = (long long)rows * by, each = places / a.N;
+    int strip = each <= 1 ? a.T : (int)((a.T + each - 1) / each);
+    strip = strip < 16 ? 16 : (strip + kBatch - 1) / kBatch * kBatch;
     const int strips = (a.T + strip - 1) / strip;
     const long long wanted = ((long long)a.N * strips + by - 1) / by;
-    const int rows = (int)(wanted < most_rows(a.C) ? wanted : most_rows(a.C));
+    if (wanted < rows) rows = (int)wanted;
     const dim3 grid(across, rows), block(bx, by);
     if (a.doc) conv_bwd_kernel<T, V, KW, kAll, true><<<grid, block, 0, s>>>(a, groups, strips, strip);
     else conv_bwd_kernel<T, V, KW, kAll, false><<<grid, block, 0, s>>>(a, groups, strips, strip);
@@ -508,11 +548,13 @@ cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&c, conv_join_kernel, (const float*)a.partial, rows, a.C, a.K, a.dw, a.db);
 }
 
+bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
 // The window: 4 taps exactly (the usual case), up to 4, up to 8.
 #define CONV_BY_TAPS(F, T, V, V8, ...)                              \
     do {                                                            \
-        if (a.K == 4) return F<T, V, 4, true>(a, ##__VA_ARGS__);    \
-        if (a.K < 4) return F<T, V, 4, false>(a, ##__VA_ARGS__);    \
+        if (a.K == 4 && on16(a.w)) return F<T, V, 4, true>(a, ##__VA_ARGS__); \
+        if (a.K <= 4) return F<T, V, 4, false>(a, ##__VA_ARGS__);   \
         return F<T, V8, 8, false>(a, ##__VA_ARGS__);                \
     } while (0)
 
@@ -537,7 +579,6 @@ cudaError_t bwd_any(const ConvArgs& a, cudaStream_t s) {
         if (bytes >= 4) CONV_BY_TAPS(bwd, __nv_bfloat16, 2, 2, s);
         CONV_BY_TAPS(bwd, __nv_bfloat16, 1, 1, s);
     }
-    if (bytes >= 16) CONV_BY_TAPS(bwd, float, 4, 2, s);
     if (bytes >= 8) CONV_BY_TAPS(bwd, float, 2, 2, s);
     CONV_BY_TAPS(bwd, float, 1, 1, s);
 }

@@ -10,7 +10,8 @@
 //   kGated:     B is 128 columns of W_g beside the same 128 of W_u, one from each block, so that a thread of the
 //               epilogue has g and u of the same place; out go h and, if wanted, g and u
 //   kStore:     y (+ residual), dx, dW_in, dW_out
-//   kGatedBack: dh stays in tensor memory; g and u come in by tensor copies, dg, du and h leave
+//   kGatedBack: dh stays in tensor memory; g and u come into registers a piece ahead (by tensor copies they would
+//               queue behind the operands: 29 600 cycles a tile at K = 2048, whose products take 20 000), dg, du and h leave
 // The epilogue takes 32 rows by 32 columns a warp at a time through shared memory (rows of 64 bytes, 64-byte
 // swizzle: free of conflicts), in and out by tensor copies, which also cut what lies outside the matrices.
 //
@@ -25,6 +26,7 @@
 #include <cstdint>
 
 #include "../../include/ttm.h"
+#include "pairs.cuh"
 #include "tc_pair.cuh"
 #include "tc_ptx.cuh"
 #include "train_ops.h"
@@ -54,6 +56,12 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(bf162_bits(f[0], f[1]), bf162_bits(f[2], f[3]), bf162_bits(f[4], f[5]), bf162_bits(f[6], f[7]));
 }
 
+__device__ __forceinline__ void unpack4(const uint2& u, float (&f)[4]) {
+    f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xffff0000u);
+    f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ uint2 pack4(const float (&f)[4]) { return make_uint2(bf162_bits(f[0], f[1]), bf162_bits(f[2], f[3])); }
+
 // ------------------------------------------------------------------------ activation
 
 // The normal distribution's upper tail: erfc(z) for z >= 0 by the Chebyshev fit in "Numerical Recipes" (erfcc),
@@ -81,7 +89,7 @@ __device__ __forceinline__ float act(float g, int gelu, float& slope) {
         if (kSlope) slope = fmaf(g * 0.39894228f, __expf(-z * z), c);
         return g * c;
     }
-    const float s = __fdividef(1.f, 1.f + __expf(-g));
+    const float s = fast_logistic(g);
     if (kSlope) slope = s * fmaf(g, 1.f - s, 1.f);
     return g * s;
 }
@@ -92,7 +100,7 @@ enum { kStore, kGated, kGatedBack };
 constexpr int kBM = 128, kBK = 64, kTile = 256, kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kOperand = kBM * kBK * 2, kStageBytes = 2 * kOperand;      // of a block: 128 rows of A, 128 of B
 constexpr uint32_t kPiece = 32 * 32 * 2;                                      // 32 rows x 32 columns
-// Pieces of a warp: results (kStore: two turns), kGated h, g, u; kGatedBack dg over g, du over u, h, two turns.
+// Pieces of a warp: kStore the result, two turns; kGated h, g, u; kGatedBack dg, du, h, two turns.
 template <int MODE> constexpr int kPieces = MODE == kStore ? 2 : MODE == kGated ? 3 : 6;
 template <int MODE> constexpr int kStages = MODE == kGatedBack ? 4 : 5;
 template <int MODE> constexpr uint32_t kEpiBytes = kEpiWarps * kPieces<MODE> * kPiece;
@@ -104,13 +112,14 @@ struct Problem {                        // one product
     int add;                            // kStore: a residual is added
 };
 struct Maps {
-    CUtensorMap a, b, out, aux, h;      // aux: the residual, or gu; kGated: out is h
+    CUtensorMap a, b, out, aux, h;      // aux: the residual; kGated: out is h, aux gu
 };
 struct GemmParams {
     Problem q[2];
     int tiles;
     int splits;                         // SPLIT: pairs of a cluster that share a tile's K
     int gelu, save;                     // save: kGated writes g and u
+    const bf16* gu;                     // kGatedBack: [M][2N]
     int* status;
     long long limit;
     int debug_stall;                    // stage (modulo their number) + 1 that never fills; 0: none
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t asked = 0, seen = 0;                       // copies into this warp's pieces, on one barrier and the other
     int turn = 0;
     bool ok = true;
-    auto loads_of = [&](const Problem& q) { return MODE == kGatedBack || (MODE == kStore && q.add); };
+    auto loads_of = [&](const Problem& q) { return MODE == kStore && q.add; };
     auto row_of = [&](const TileAt& at) { return at.row + rank * kBM + part * 32; };
     auto pieces_of = [&](const TileAt& at) {            // that hold a result
         const Problem& q = p.q[at.which];
@@ -296,14 +305,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             const CUtensorMap* aux = at.which ? &m1.aux : &m0.aux;
             bulk_wait_read<0>();                        // the results that lay there have left
-            unsigned char* to = mine + (asked & 1) * (MODE == kGatedBack ? 3 : 1) * kPiece;
             uint64_t* bar = &landed[asked & 1];
-            const int x = at.col + 32 * c, row = row_of(at);
-            mbar_expect_tx(bar, MODE == kGatedBack ? 2 * kPiece : kPiece);
-            tma_load_3d(to, aux, bar, x, MODE == kGatedBack ? 0 : row, MODE == kGatedBack ? row : 0);
-            if (MODE == kGatedBack) tma_load_3d(to + kPiece, aux, bar, x, 1, row);
+            mbar_expect_tx(bar, kPiece);
+            tma_load_3d(mine + (asked & 1) * kPiece, aux, bar, at.col + 32 * c, row_of(at), 0);
         }
         ++asked;
+    };
+    // kGatedBack: g and u of this lane's row in piece c; `pieces`: those there are.
+    uint4 g_next[MODE == kGatedBack ? 4 : 1] = {}, u_next[MODE == kGatedBack ? 4 : 1] = {};
+    auto read = [&](const TileAt& at, int c, int pieces) {
+        if constexpr (MODE == kGatedBack) {
+            const int row = row_of(at) + lane, x = at.col + 32 * c;
+            const bf16* from = p.gu + (long long)row * 2 * p.q[0].N + x;
+            const bool in = c < pieces && row < p.q[0].M;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (in && x + 8 * j < p.q[0].N) {
+                    g_next[j] = *reinterpret_cast<const uint4*>(from + 8 * j);
+                    u_next[j] = *reinterpret_cast<const uint4*>(from + p.q[0].N + 8 * j);
+                }
+            }
+        }
     };
     // Piece c from its sums v (kGated: of g, and up of u); `after`: the next piece of this warp.
     auto piece = [&](const TileAt& at, int c, int after, int pieces, float (&v)[32], float (&up)[MODE == kGated ? 32 : 1]) {
@@ -318,10 +340,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++seen;
         } else {
             if (lane == 0) {
-                if (MODE == kStore) bulk_wait_read<1>();
-                else bulk_wait_read<0>();
+                if (MODE == kGated) bulk_wait_read<0>();
+                else bulk_wait_read<1>();
             }
             __syncwarp();
+        }
+        uint4 g_now[MODE == kGatedBack ? 4 : 1], u_now[MODE == kGatedBack ? 4 : 1];
+        if constexpr (MODE == kGatedBack) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                g_now[j] = g_next[j];
+                u_now[j] = u_next[j];
+            }
+            read(at, after, pieces);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -348,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 uint4 *a1 = piece_at(to + kPiece, lane, j), *a2 = piece_at(to + 2 * kPiece, lane, j);
                 float g[8], u[8], h[8];
-                unpack8(*a0, g);
-                unpack8(*a1, u);
+                unpack8(g_now[j], g);
+                unpack8(u_now[j], u);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     float slope;
@@ -391,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const TileAt at = tile_at<MODE>(p, t);
                 const int acc = n & 1, pieces = pieces_of(at);
                 if (loads_of(p.q[at.which]) && team < pieces) fetch(at, team);
+                read(at, team, pieces);
                 ok = wait_warp(&S.acc_full[acc], (n >> 1) & 1, &S.abort, p.status, p.limit);
                 if (!ok) break;
                 tc_fence_after();
@@ -430,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const TileAt at = tile_at<MODE>(p, first);
             const int pieces = pieces_of(at), step = 2 * p.splits, begin = 2 * pair_of + team;
             if (loads_of(p.q[at.which]) && begin < pieces) fetch(at, begin);
+            read(at, begin, pieces);
             for (int c = begin; c < pieces && ok; c += step) {
                 float v[32] = {}, up[MODE == kGated ? 32 : 1] = {};
                 for (int q = 0; q < p.splits; ++q) {
@@ -465,13 +498,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // tiles are; each leaves its sums in shared memory, and a share of the results is added up over the blocks
 // in their order, put through the epilogue and written by each.  The second kernel of a call starts on its weights
 // while the first one finishes.
+constexpr int kNarrowBlocks = 176;               // blocks of a launch at most, of 304 places
 constexpr int kNarrow = 128, kNarrowThreads = 256, kNarrowStages = 6, kNarrowSmem = 110 * 1024;
 
 struct NarrowParams {
     int N, wide, K;                     // rows; columns of the result (kGated: F); K
     int F, kblocks;                     // kGated, kGatedBack: F; blocks of K of a block of the cluster
     int bn, stages;                     // rows, padded to 16
-    int gelu;
+    int gelu, second;                   // second: of a call's kernels
     bf16 *out, *gu, *h;                 // kStore: result; kGated: h and gu (or NULL); kGatedBack: dgu, gu read, h
     const bf16* add;                    // kStore: residual or NULL
     long long add_row;
@@ -508,11 +542,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
         S.abort = 0;
     }
     if (warp == 1) tmem_alloc(&S.tmem, kNarrow);
+    if (warp == 2 && lane == 0) {
+        tma_prefetch_desc(&mw);
+        tma_prefetch_desc(&mx);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    asm volatile("griddepcontrol.launch_dependents;");
 
     if (warp == 0 && lane == 0) {
         auto weights = [&](int k, int s) {
@@ -524,10 +561,24 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                 else tma_load_3d(to, &mw, &S.full[s], k * kBK, first, 0);
             }
         };
-        // weights need no earlier kernel of the call: the first stages' are on their way before its end
+        // A call's second kernel needs its first one's results, but not for the weights, whose first stages are on
+        // their way before its end.  The first kernel lets the second one start only when all before it has ended,
+        // whatever wrote the weights among it.
+        // What does not fit, and the first kernel's weights, are asked into the L2 cache meanwhile: that is where later
+        // writes would meet them.
         const int ahead = max(0, min(p.stages, k1 - k0));
-        for (int i = 0; i < ahead; ++i) weights(k0 + i, i);
+        if (p.second)
+            for (int i = 0; i < ahead; ++i) weights(k0 + i, i);
+        for (int k = p.second ? k0 + ahead : k0; k < k1; ++k)
+            for (int i = 0; i < (WMN ? 2 : 1); ++i) {
+                if (MODE == kGated) tma_prefetch_l2_3d(&mw, first, i, k * kBK);
+                else if (WMN) tma_prefetch_l2_3d(&mw, first + 64 * i, k * kBK, 0);
+                else tma_prefetch_l2_3d(&mw, k * kBK, first, 0);
+            }
         asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;");
+        if (!p.second)
+            for (int i = 0; i < ahead; ++i) weights(k0 + i, i);
         int it = 0;
         bool ok = true;
         for (int k = k0; k < k1; ++k, ++it) {
@@ -587,50 +638,55 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     tc_fence_before();
     cluster_sync();
     if (good) {
-        constexpr int kGroups = MODE == kGated ? 8 : 16;             // of 8 columns
+        constexpr int kGroups = MODE == kGated ? 16 : 32;            // of 4 columns
         const int items = p.N * kGroups, share = (items + ranks - 1) / ranks;
         const int last = min(items, (rank + 1) * share);
         for (int i = rank * share + (int)threadIdx.x; i < last; i += kNarrowThreads) {
-            const int t = i / kGroups, g8 = i % kGroups * 8, col = first + g8;
+            const int t = i / kGroups, g4 = i % kGroups * 4, col = first + g4;
             if (col >= p.wide) continue;
-            float v[8] = {}, u[8] = {};
-            for (int q = 0; q < ranks; ++q) {
-                const uint32_t at = peer_addr(sums + t * 128 + g8, q);
-                const float4 a = peer_load4(at), b = peer_load4(at + 16);
-                v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-                v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-                if constexpr (MODE == kGated) {
-                    const float4 c = peer_load4(at + 256), d = peer_load4(at + 272);
-                    u[0] += c.x; u[1] += c.y; u[2] += c.z; u[3] += c.w;
-                    u[4] += d.x; u[5] += d.y; u[6] += d.z; u[7] += d.w;
+            float v[4] = {}, u[4] = {};
+            for (int q0 = 0; q0 < ranks; q0 += 4) {                  // four blocks' sums on their way together
+                float4 a[4], b[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    a[q] = b[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (q0 + q >= ranks) continue;
+                    const uint32_t at = peer_addr(sums + t * 128 + g4, q0 + q);
+                    a[q] = peer_load4(at);
+                    if constexpr (MODE == kGated) b[q] = peer_load4(at + 256);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    v[0] += a[q].x; v[1] += a[q].y; v[2] += a[q].z; v[3] += a[q].w;
+                    if constexpr (MODE == kGated) { u[0] += b[q].x; u[1] += b[q].y; u[2] += b[q].z; u[3] += b[q].w; }
                 }
             }
             if constexpr (MODE == kStore) {
                 if (p.add) {
-                    float r[8];
-                    unpack8(*reinterpret_cast<const uint4*>(p.add + t * p.add_row + col), r);
+                    float r[4];
+                    unpack4(*reinterpret_cast<const uint2*>(p.add + t * p.add_row + col), r);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += r[j];
+                    for (int j = 0; j < 4; ++j) v[j] += r[j];
                 }
-                *reinterpret_cast<uint4*>(p.out + (long long)t * p.wide + col) = pack8(v);
+                *reinterpret_cast<uint2*>(p.out + (long long)t * p.wide + col) = pack4(v);
             } else {
                 bf16* gu = p.gu + (long long)t * 2 * p.F + col;
-                uint4* h = reinterpret_cast<uint4*>(p.h + (long long)t * p.F + col);
+                uint2* h = reinterpret_cast<uint2*>(p.h + (long long)t * p.F + col);
                 if constexpr (MODE == kGated) {
                     if (p.gu) {
-                        *reinterpret_cast<uint4*>(gu) = pack8(v);
-                        *reinterpret_cast<uint4*>(gu + p.F) = pack8(u);
+                        *reinterpret_cast<uint2*>(gu) = pack4(v);
+                        *reinterpret_cast<uint2*>(gu + p.F) = pack4(u);
                     }
                     float unused;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = act<false>(v[j], p.gelu, unused) * u[j];
-                    *h = pack8(v);
+                    for (int j = 0; j < 4; ++j) v[j] = act<false>(v[j], p.gelu, unused) * u[j];
+                    *h = pack4(v);
                 } else {
-                    float g[8], hh[8];
-                    unpack8(*reinterpret_cast<const uint4*>(gu), g);
-                    unpack8(*reinterpret_cast<const uint4*>(gu + p.F), u);
+                    float g[4], hh[4];
+                    unpack4(*reinterpret_cast<const uint2*>(gu), g);
+                    unpack4(*reinterpret_cast<const uint2*>(gu + p.F), u);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 4; ++j) {
                         float slope;
                         const float a = act<true>(g[j], p.gelu, slope);
                         hh[j] = a * u[j];
@@ -638,9 +694,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                         u[j] = v[j] * a;
                     }
                     bf16* dgu = p.out + (long long)t * 2 * p.F + col;
-                    *reinterpret_cast<uint4*>(dgu) = pack8(g);
-                    *reinterpret_cast<uint4*>(dgu + p.F) = pack8(u);
-                    *h = pack8(hh);
+                    *reinterpret_cast<uint2*>(dgu) = pack4(g);
+                    *reinterpret_cast<uint2*>(dgu + p.F) = pack4(u);
+                    *h = pack4(hh);
                 }
             }
         }
@@ -753,18 +809,20 @@ cudaError_t gemm(const Maps& m0, const Maps& m1, GemmParams p, bool overlap, cud
     return launch<AMN, BMN, MODE, false>(m0, m1, p, 2 * (p.tiles < kPairs ? p.tiles : kPairs), overlap, s);
 }
 
-// Splits of K: as many as fill two blocks an SM, of two blocks of K at least.
+// Splits of K, of two blocks of K at least: about a block an SM, so that the blocks of a call's second kernel fit beside
+// the first one's and have their weights on the way.
 template <bool WMN, int MODE>
-cudaError_t narrow(const CUtensorMap& mw, const Matrix& x, NarrowParams p, bool overlap, cudaStream_t s) {
+cudaError_t narrow(const CUtensorMap& mw, const Matrix& x, NarrowParams p, bool second, cudaStream_t s) {
     const int columns = MODE == kGated ? 64 : 128, tiles = (p.wide + columns - 1) / columns;
     const int kblocks = (p.K + kBK - 1) / kBK;
-    int splits = 2 * 2 * kPairs / tiles;
+    int splits = kNarrowBlocks / tiles;
     splits = splits > 8 ? 8 : splits;
     if (splits > kblocks / 2) splits = kblocks / 2;
     if (splits < 1) splits = 1;
     p.kblocks = (kblocks + splits - 1) / splits;
     splits = (kblocks + p.kblocks - 1) / p.kblocks;
     p.bn = (p.N + 15) / 16 * 16;
+    p.second = second;
     const int stage = kOperand + p.bn * 128, room = kNarrowSmem - 1024;
     p.stages = room / stage < kNarrowStages ? room / stage : kNarrowStages;
     CUtensorMap mx;
@@ -772,7 +830,7 @@ cudaError_t narrow(const CUtensorMap& mw, const Matrix& x, NarrowParams p, bool 
     auto kernel = ffn_narrow_kernel<WMN, MODE>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
     if (e != cudaSuccess) return e;
-    return launch_in_clusters(kernel, dim3(tiles * splits), dim3(kNarrowThreads), kNarrowSmem, s, splits, overlap, mw, mx, p);
+    return launch_in_clusters(kernel, dim3(tiles * splits), dim3(kNarrowThreads), kNarrowSmem, s, splits, true, mw, mx, p);
 }
 
 NarrowParams narrow_params(const FfnArgs& a) {
@@ -831,7 +889,7 @@ cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     if (!x.operand(&m.a, false) || !wi.halves(&m.b, 64, 64, TmaSwizzle::b128) || !h.piece(&m.out) ||
         (a.gu && !gu.halves(&m.aux, 32, 32, TmaSwizzle::b64)) || !problem(p.q[0], a.N, a.F, a.D, kGated))
         return cudaErrorInvalidValue;
-    const cudaError_t e = gemm<false, true, kGated>(m, m, p, false, s);
+    const cudaError_t e = gemm<false, true, kGated>(m, m, p, true, s);
     if (e != cudaSuccess) return e;
     GemmParams o = params(a);
     Maps n{};
@@ -846,7 +904,7 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     const long long N = a.N, D = a.D, F = a.F;
     char* ws = static_cast<char*>(a.workspace);
     const Matrix x{a.x, N, D, a.x_row}, wi{a.W_in, D, 2 * F, 2 * F}, wo{a.W_out, F, D, D}, dy{a.dy, N, D, a.dy_row},
-        gu{a.gu, N, 2 * F, 2 * F}, dgu{ws, N, 2 * F, 2 * F}, h{ws + (size_t)N * F * 4, N, F, F}, dx{a.dx, N, D, D},
+        dgu{ws, N, 2 * F, 2 * F}, h{ws + (size_t)N * F * 4, N, F, F}, dx{a.dx, N, D, D},
         dwi{a.dW_in, D, 2 * F, 2 * F}, dwo{a.dW_out, F, D, D};
     *launches = 1;
     cudaError_t e;
@@ -866,9 +924,10 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         GemmParams p = params(a);
         p.debug_stall = a.debug_stall;
         if (!dy.operand(&m.a, false) || !wo.operand(&m.b, false) || !dgu.halves(&m.out, 32, 32, TmaSwizzle::b64) ||
-            !gu.halves(&m.aux, 32, 32, TmaSwizzle::b64) || !h.piece(&m.h) || !problem(p.q[0], a.N, a.F, a.D, kGatedBack))
+            !h.piece(&m.h) || !problem(p.q[0], a.N, a.F, a.D, kGatedBack))
             return cudaErrorInvalidValue;
-        e = gemm<false, false, kGatedBack>(m, m, p, false, s);
+        p.gu = static_cast<const bf16*>(a.gu);
+        e = gemm<false, false, kGatedBack>(m, m, p, true, s);
     }
     if (e != cudaSuccess) return e;
     if (a.dx && a.N <= kNarrow) {

@@ -61,4 +61,13 @@ __device__ __forceinline__ uint32_t bf16_of_pair(f2 a) {
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// 1 / (1 + exp(-x)) by the base-2 and reciprocal units: (4 + 0.7 |x|) 2^-23 of itself off at most, 0 where it is
+// below the smallest normal number.
+__device__ __forceinline__ float fast_logistic(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
+    return r;
+}
+
 }  // namespace ttm
