@@ -116,8 +116,9 @@ struct Maps {
 };
 struct GemmParams {
     Problem q[2];
-    int tiles;
+    int tile0, tiles;                   // this launch's tiles: from .. to
     int splits;                         // SPLIT: pairs of a cluster that share a tile's K
+    int beside;                         // the second of two launches of one product, which runs beside the first
     int gelu, save;                     // save: kGated writes g and u
     const bf16* gu;                     // kGatedBack: [M][2N]
     int* status;
@@ -191,10 +192,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* epi = base + kS * kStageBytes;
     GemmShared& S = *reinterpret_cast<GemmShared*>(epi + kEpiBytes<MODE>);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int member = SPLIT ? (int)cluster_rank() : 0, pair_of = member >> 1;
-    const int rank = SPLIT ? member & 1 : (int)cluster_rank(), lead = member & ~1;
+    const int member = (int)cluster_rank(), pair_of = SPLIT ? member >> 1 : 0;
+    const int rank = member & 1, lead = SPLIT ? member & ~1 : 0;
     const uint16_t both = (uint16_t)(3 << lead);
-    const int width = SPLIT ? 2 * p.splits : 2, first = blockIdx.x / width, stride = gridDim.x / width;
+    const int width = SPLIT ? 2 * p.splits : 2, first = p.tile0 + (int)blockIdx.x / width, stride = (int)gridDim.x / width;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kS; ++i) {
             // (in a test of the waits one stage expects an arrival that does not come)
@@ -215,7 +216,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();                                     // both blocks' barriers are set up
     tc_fence_after();
     const uint32_t tmem = S.tmem;
-    after_previous();
+    // A launch starts its successor's set-up only when all before it has ended, so that one that runs beside it finds
+    // the operands written, and needs to wait for it only before its own end, which the next launch goes by.
+    if (!p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
 
     if (warp == 0 && lane == 0) {
         int it = 0;
@@ -436,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_at(peer_addr(&S.acc_empty[acc], 0));
+                if (lane == 0) mbar_arrive_at(peer_addr(&S.acc_empty[acc], lead));
             }
         }
     } else {
@@ -488,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();                                     // no arrival at a block that has left
     tc_fence_after();
     if (warp == 1) free_columns<2>(tmem, 2 * kTile);
+    if (p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------- products of few rows
@@ -766,47 +771,64 @@ int clusters_at_once(int width) {
     return n;
 }
 
-// Pairs that share a tile, by what the rounds of tiles take in blocks of K (650 cycles each): a tile alone in its round
-// also waits for its own epilogue (about 6 blocks), and for the sums to pass between the pairs (4 more).
+// How a product's tiles are gone through: whole rounds by the pairs, the rest in one more round or with K shared by
+// clusters of 2 to 4 pairs (20 tiles of a last round leave 56 pairs idle).
+struct Plan {
+    int whole, splits;                  // tiles of the first launch; pairs on a tile in the second, 1 for none
+};
+
+// Counted in blocks of K of a pair: a round takes its blocks of K and the epilogue of the last tile (6), tiles that share K
+// the passing on of their sums too (4 more).
 template <bool AMN, bool BMN, int MODE>
-int splits_for(const GemmParams& p) {
+Plan plan_of(const GemmParams& p) {
     const int K = p.q[0].K > p.q[1].K ? p.q[0].K : p.q[1].K, kblocks = (K + kBK - 1) / kBK;
-    if (p.tiles > 2 * kPairs) return 1;
-    int best = 1;
-    double least = (double)((p.tiles + kPairs - 1) / kPairs) * kblocks + 6;
+    const int whole = p.tiles / kPairs * kPairs, rest = p.tiles - whole;
+    Plan plan{p.tiles, 1};
+    if (rest == 0) return plan;
+    int least = kblocks + (whole ? 0 : 6);
     for (int n = 2; n <= 4; ++n) {
-        const int each = (kblocks + n - 1) / n;
+        const int each = (kblocks + n - 1) / n, at_once = clusters_at_once<AMN, BMN, MODE>(2 * n);
         if (each < 4 || (kblocks + each - 1) / each != n) continue;
-        const int at_once = clusters_at_once<AMN, BMN, MODE>(2 * n);
-        const double rounds = (p.tiles + at_once - 1) / at_once, blocks = rounds * (each + 10);
-        if (blocks < least) {
-            least = blocks;
-            best = n;
+        const int cost = (rest + at_once - 1) / at_once * (each + 10);
+        if (cost < least) {
+            least = cost;
+            plan = {whole, n};
         }
     }
-    return best;
+    return plan;
 }
 
 template <bool AMN, bool BMN, int MODE, bool SPLIT>
-cudaError_t launch(const Maps& m0, const Maps& m1, const GemmParams& p, int blocks, bool overlap, cudaStream_t s) {
+cudaError_t launch(const Maps& m0, const Maps& m1, const GemmParams& p, int blocks, cudaStream_t s) {
     static_assert(kSmem<MODE> <= 232448, "shared memory of a block");
     static_assert(!SPLIT || kStages<MODE> * kStageBytes >= kTile * kBM * 4, "the sums of a block");
-    auto kernel = ffn_gemm_kernel<AMN, BMN, MODE, SPLIT>;
-    return launch_in_clusters(kernel, dim3(blocks), dim3(kThreads), kSmem<MODE>, s, SPLIT ? 2 * p.splits : 2, overlap, m0, m1,
-                              p);
+    return launch_in_clusters(ffn_gemm_kernel<AMN, BMN, MODE, SPLIT>, dim3(blocks), dim3(kThreads), kSmem<MODE>, s,
+                              SPLIT ? 2 * p.splits : 2, true, m0, m1, p);
 }
 
 template <bool AMN, bool BMN, int MODE>
-cudaError_t gemm(const Maps& m0, const Maps& m1, GemmParams p, bool overlap, cudaStream_t s) {
-    p.tiles = p.q[0].tiles + p.q[1].tiles;
+cudaError_t gemm(const Maps& m0, const Maps& m1, GemmParams p, cudaStream_t s, int* launches) {
     cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<AMN, BMN, MODE, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmem<MODE>);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(ffn_gemm_kernel<AMN, BMN, MODE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<MODE>);
     if (e != cudaSuccess) return e;
-    p.splits = splits_for<AMN, BMN, MODE>(p);
-    if (p.splits > 1) return launch<AMN, BMN, MODE, true>(m0, m1, p, 2 * p.splits * p.tiles, overlap, s);
-    return launch<AMN, BMN, MODE, false>(m0, m1, p, 2 * (p.tiles < kPairs ? p.tiles : kPairs), overlap, s);
+    const int all = p.tiles = p.q[0].tiles + p.q[1].tiles;
+    const Plan plan = plan_of<AMN, BMN, MODE>(p);
+    if (plan.whole) {
+        p.tiles = plan.whole;
+        e = launch<AMN, BMN, MODE, false>(m0, m1, p, 2 * (plan.whole < kPairs ? plan.whole : kPairs), s);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
+    if (plan.whole == all) return cudaSuccess;
+    p.beside = plan.whole > 0;
+    p.tile0 = plan.whole;
+    p.tiles = all;
+    p.splits = plan.splits;
+    if (plan.whole) p.debug_stall = 0;
+    ++*launches;
+    return launch<AMN, BMN, MODE, true>(m0, m1, p, 2 * p.splits * (all - p.tile0), s);
 }
 
 // Splits of K, of two blocks of K at least: about a block an SM, so that the blocks of a call's second kernel fit beside
@@ -861,8 +883,9 @@ cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     const long long N = a.N, D = a.D, F = a.F;
     const Matrix x{a.x, N, D, a.x_row}, wi{a.W_in, D, 2 * F, 2 * F}, wo{a.W_out, F, D, D}, h{a.workspace, N, F, F},
         y{a.y, N, D, D}, gu{a.gu, N, 2 * F, 2 * F}, res{a.residual, N, D, a.residual_row};
-    *launches = 2;
+    *launches = 0;
     if (a.N <= kNarrow) {
+        *launches = 2;
         NarrowParams p = narrow_params(a);
         CUtensorMap w;
         p.wide = a.F;
@@ -889,7 +912,7 @@ cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     if (!x.operand(&m.a, false) || !wi.halves(&m.b, 64, 64, TmaSwizzle::b128) || !h.piece(&m.out) ||
         (a.gu && !gu.halves(&m.aux, 32, 32, TmaSwizzle::b64)) || !problem(p.q[0], a.N, a.F, a.D, kGated))
         return cudaErrorInvalidValue;
-    const cudaError_t e = gemm<false, true, kGated>(m, m, p, true, s);
+    const cudaError_t e = gemm<false, true, kGated>(m, m, p, s, launches);
     if (e != cudaSuccess) return e;
     GemmParams o = params(a);
     Maps n{};
@@ -897,7 +920,7 @@ cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         !problem(o.q[0], a.N, a.D, a.F, kStore))
         return cudaErrorInvalidValue;
     o.q[0].add = a.residual != nullptr;
-    return gemm<false, true, kStore>(n, n, o, true, s);
+    return gemm<false, true, kStore>(n, n, o, s, launches);
 }
 
 cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
@@ -906,7 +929,7 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     const Matrix x{a.x, N, D, a.x_row}, wi{a.W_in, D, 2 * F, 2 * F}, wo{a.W_out, F, D, D}, dy{a.dy, N, D, a.dy_row},
         dgu{ws, N, 2 * F, 2 * F}, h{ws + (size_t)N * F * 4, N, F, F}, dx{a.dx, N, D, D},
         dwi{a.dW_in, D, 2 * F, 2 * F}, dwo{a.dW_out, F, D, D};
-    *launches = 1;
+    *launches = 0;
     cudaError_t e;
     if (a.N <= kNarrow) {
         NarrowParams p = narrow_params(a);
@@ -919,15 +942,16 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         p.debug_stall = a.debug_stall;
         if (!wo.operand(&w, false)) return cudaErrorInvalidValue;
         e = narrow<false, kGatedBack>(w, dy, p, false, s);
+        ++*launches;
     } else {
         Maps m{};
         GemmParams p = params(a);
         p.debug_stall = a.debug_stall;
-        if (!dy.operand(&m.a, false) || !wo.operand(&m.b, false) || !dgu.halves(&m.out, 32, 32, TmaSwizzle::b64) ||
-            !h.piece(&m.h) || !problem(p.q[0], a.N, a.F, a.D, kGatedBack))
+        if (!dy.operand(&m.a, false) || !wo.operand(&m.b, false) ||
+            !dgu.halves(&m.out, 32, 32, TmaSwizzle::b64) || !h.piece(&m.h) || !problem(p.q[0], a.N, a.F, a.D, kGatedBack))
             return cudaErrorInvalidValue;
         p.gu = static_cast<const bf16*>(a.gu);
-        e = gemm<false, false, kGatedBack>(m, m, p, true, s);
+        e = gemm<false, false, kGatedBack>(m, m, p, s, launches);
     }
     if (e != cudaSuccess) return e;
     if (a.dx && a.N <= kNarrow) {
@@ -946,9 +970,8 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         if (!dgu.operand(&n.a, false) || !wi.operand(&n.b, false) || !dx.piece(&n.out) ||
             !problem(o.q[0], a.N, a.D, 2 * a.F, kStore))
             return cudaErrorInvalidValue;
-        e = gemm<false, false, kStore>(n, n, o, true, s);
+        e = gemm<false, false, kStore>(n, n, o, s, launches);
         if (e != cudaSuccess) return e;
-        ++*launches;
     }
     if (!a.dW_in && !a.dW_out) return cudaSuccess;
     // both weights' products in one launch: few tiles each, so that one's last round fills up with the other's
@@ -966,8 +989,7 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
             !problem(o.q[k], a.F, a.D, a.N, kStore))
             return cudaErrorInvalidValue;
     }
-    ++*launches;
-    return gemm<true, true, kStore>(n[0], n[1], o, true, s);
+    return gemm<true, true, kStore>(n[0], n[1], o, s, launches);
 }
 
 }  // namespace ttm

@@ -102,7 +102,7 @@ def test_sizes(N, D, F):
 
 @pytest.mark.parametrize("N,D,F", [(1, 2048, 5504), (16, 2048, 5504), (48, 768, 2048), (300, 2048, 512), (1537, 768, 2056),
                                    (777, 1000, 3000), (2048, 512, 1024), (4097, 136, 72), (1000, 24, 4096), (130, 4096, 40),
-                                   (5000, 1032, 776)])
+                                   (5000, 1032, 776), (9001, 264, 2008), (20011, 520, 136), (2300, 2048, 2816)])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_larger(N, D, F, act):
     check(N, D, F, act)
