@@ -10,10 +10,12 @@
 //   kGated:     B is 128 columns of W_g beside the same 128 of W_u, one from each block, so that a thread of the
 //               epilogue has g and u of the same place; out go h and, if wanted, g and u
 //   kStore:     y (+ residual), dx, dW_in, dW_out
-//   kGatedBack: dh stays in tensor memory; g and u come into registers a piece ahead (by tensor copies they would
-//               queue behind the operands: 29 600 cycles a tile at K = 2048, whose products take 20 000), dg, du and h leave
-// The epilogue takes 32 rows by 32 columns a warp at a time through shared memory (rows of 64 bytes, 64-byte
-// swizzle: free of conflicts), in and out by tensor copies, which also cut what lies outside the matrices.
+//   kGatedBack: dh stays in tensor memory; g and u come in a piece ahead, dg, du and h leave
+// What bounds a tile is how far ahead the copies run: 32 KB a block of K and 2000 cycles until they land; with four
+// stages a block of K took 900 cycles, with five 680, with six 560, where the tensor cores need 512.  So the epilogue has
+// little shared memory: 32 rows by 32 columns a warp at a time, one result after the other through two places (rows of 64
+// bytes, swizzled: free of conflicts), out by tensor copies, which also cut what lies outside the matrices; what it
+// reads goes to registers.
 //
 // Roundings: g and u enter the activation in fp32; h, dg and du are rounded to bf16 once, as operands of the next
 // product (half a step, 2^-8 of a value at most: the same as rounding the result, and what the tensor cores
@@ -100,19 +102,18 @@ enum { kStore, kGated, kGatedBack };
 constexpr int kBM = 128, kBK = 64, kTile = 256, kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kOperand = kBM * kBK * 2, kStageBytes = 2 * kOperand;      // of a block: 128 rows of A, 128 of B
 constexpr uint32_t kPiece = 32 * 32 * 2;                                      // 32 rows x 32 columns
-// Pieces of a warp: kStore the result, two turns; kGated h, g, u; kGatedBack dg, du, h, two turns.
-template <int MODE> constexpr int kPieces = MODE == kStore ? 2 : MODE == kGated ? 3 : 6;
-template <int MODE> constexpr int kStages = MODE == kGatedBack ? 4 : 5;
-template <int MODE> constexpr uint32_t kEpiBytes = kEpiWarps * kPieces<MODE> * kPiece;
+constexpr uint32_t kEpiBytes = kEpiWarps * 2 * kPiece;
+constexpr int kStages = 6;
 constexpr int kRowGroup = 8;            // row tiles that share their way through the columns
 
 struct Problem {                        // one product
     int M, N, K;                        // kGated: N = F
     int tiles_m, tiles;
-    int add;                            // kStore: a residual is added
+    const bf16* add;                    // kStore: residual or NULL
+    long long add_row;
 };
 struct Maps {
-    CUtensorMap a, b, out, aux, h;      // aux: the residual; kGated: out is h, aux gu
+    CUtensorMap a, b, out, aux;         // kGated: out is gu, aux h; kGatedBack: out is dgu, aux h
 };
 struct GemmParams {
     Problem q[2];
@@ -126,11 +127,11 @@ struct GemmParams {
     int debug_stall;                    // stage (modulo their number) + 1 that never fills; 0: none
 };
 struct GemmShared {
-    uint64_t full[5], empty[5], acc_full[2], acc_empty[2], landed[kEpiWarps][2];
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int abort;
 };
-template <int MODE> constexpr int kSmem = 1024 + kStages<MODE> * kStageBytes + kEpiBytes<MODE> + sizeof(GemmShared);
+constexpr int kSmem = 1024 + kStages * kStageBytes + kEpiBytes + sizeof(GemmShared);
 
 struct TileAt {
     int row, col, which;
@@ -186,11 +187,11 @@ template <bool AMN, bool BMN, int MODE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ Maps m0, const __grid_constant__ Maps m1,
                     const __grid_constant__ GemmParams p) {
-    constexpr int kS = kStages<MODE>;
+    constexpr int kS = kStages;
     extern __shared__ unsigned char raw[];
     unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     unsigned char* epi = base + kS * kStageBytes;
-    GemmShared& S = *reinterpret_cast<GemmShared*>(epi + kEpiBytes<MODE>);
+    GemmShared& S = *reinterpret_cast<GemmShared*>(epi + kEpiBytes);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int member = (int)cluster_rank(), pair_of = SPLIT ? member >> 1 : 0;
     const int rank = member & 1, lead = SPLIT ? member & ~1 : 0;
@@ -206,7 +207,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&S.acc_full[i], 1);
             mbar_init(&S.acc_empty[i], 2 * kEpiWarps);
         }
-        for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&S.landed[i / 2][i % 2], 1);
         fence_mbar_init();
         S.abort = 0;
     }
@@ -291,100 +291,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // ------ epilogue: warps 2 .. 9
+    constexpr int kIn = MODE == kGatedBack ? 8 : MODE == kStore ? 4 : 1;     // 16 bytes that a piece takes in, a lane
     const int part = warp & 3;                          // this warp's lanes of tensor memory
     const int team = (warp - 2) >> 2;                   // takes every other piece
-    unsigned char* mine = epi + (warp - 2) * kPieces<MODE> * kPiece;
-    uint64_t* landed = S.landed[(warp - 2) & 7];
-    uint32_t asked = 0, seen = 0;                       // copies into this warp's pieces, on one barrier and the other
+    unsigned char* mine = epi + (warp - 2) * 2 * kPiece;
     int turn = 0;
     bool ok = true;
-    auto loads_of = [&](const Problem& q) { return MODE == kStore && q.add; };
+    uint4 next[kIn] = {};                               // of the next piece, this lane's row: the residual, or g and u
     auto row_of = [&](const TileAt& at) { return at.row + rank * kBM + part * 32; };
     auto pieces_of = [&](const TileAt& at) {            // that hold a result
         const Problem& q = p.q[at.which];
         const int all = MODE == kGated ? kTile / 2 : kTile;
-        return row_of(at) < q.M ? min(all, q.N - at.col + 31) / 32 : 0;
+        return row_of(at) < q.M ? (min(all, q.N - at.col) + 31) / 32 : 0;
     };
-    auto fetch = [&](const TileAt& at, int c) {         // what piece c takes, into one place and the other
-        if (lane == 0) {
-            const CUtensorMap* aux = at.which ? &m1.aux : &m0.aux;
-            bulk_wait_read<0>();                        // the results that lay there have left
-            uint64_t* bar = &landed[asked & 1];
-            mbar_expect_tx(bar, kPiece);
-            tma_load_3d(mine + (asked & 1) * kPiece, aux, bar, at.col + 32 * c, row_of(at), 0);
-        }
-        ++asked;
-    };
-    // kGatedBack: g and u of this lane's row in piece c; `pieces`: those there are.
-    uint4 g_next[MODE == kGatedBack ? 4 : 1] = {}, u_next[MODE == kGatedBack ? 4 : 1] = {};
     auto read = [&](const TileAt& at, int c, int pieces) {
+        const Problem& q = p.q[at.which];
+        const int row = row_of(at) + lane, x = at.col + 32 * c;
+        const bool in = c < pieces && row < q.M;
         if constexpr (MODE == kGatedBack) {
-            const int row = row_of(at) + lane, x = at.col + 32 * c;
-            const bf16* from = p.gu + (long long)row * 2 * p.q[0].N + x;
-            const bool in = c < pieces && row < p.q[0].M;
+            const bf16* from = p.gu + (long long)row * 2 * q.N + x;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (in && x + 8 * j < p.q[0].N) {
-                    g_next[j] = *reinterpret_cast<const uint4*>(from + 8 * j);
-                    u_next[j] = *reinterpret_cast<const uint4*>(from + p.q[0].N + 8 * j);
+            for (int j = 0; j < 4; ++j)
+                if (in && x + 8 * j < q.N) {
+                    next[j] = *reinterpret_cast<const uint4*>(from + 8 * j);
+                    next[4 + j] = *reinterpret_cast<const uint4*>(from + q.N + 8 * j);
                 }
-            }
+        } else if (MODE == kStore && q.add) {
+            const bf16* from = q.add + row * q.add_row + x;
+#pragma unroll
+            for (int j = 0; j < kIn; ++j)
+                if (in && x + 8 * j < q.N) next[j] = *reinterpret_cast<const uint4*>(from + 8 * j);
         }
     };
-    // Piece c from its sums v (kGated: of g, and up of u); `after`: the next piece of this warp.
+    // 32 columns of results of this warp's 32 rows: to (x, y, z) of a map, by way of one place or the other.
+    auto emit = [&](const uint4 (&r)[4], const CUtensorMap* m, int x, int y, int z) {
+        unsigned char* place = mine + (turn & 1) * kPiece;
+        ++turn;
+        if (lane == 0) bulk_wait_read<1>();             // what lay there has left
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *piece_at(place, lane, j) = r[j];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(m, place, x, y, z);
+            bulk_commit();
+        }
+    };
+    // Piece c with its sums (kGated: of g in v, of u in up); `after`: the next piece of this warp.
     auto piece = [&](const TileAt& at, int c, int after, int pieces, float (&v)[32], float (&up)[MODE == kGated ? 32 : 1]) {
         const Maps& m = at.which ? m1 : m0;
-        const bool loads = loads_of(p.q[at.which]);
         const int x = at.col + 32 * c, row0 = row_of(at);
-        unsigned char* to = mine + (MODE == kGated ? 0 : (turn & 1) * (MODE == kGatedBack ? 3 : 1)) * kPiece;
-        if (loads) {
-            if (after < pieces) fetch(at, after);
-            ok = wait_warp(&landed[seen & 1], (seen >> 1) & 1, &S.abort, p.status, p.limit);
-            if (!ok) return;
-            ++seen;
-        } else {
-            if (lane == 0) {
-                if (MODE == kGated) bulk_wait_read<0>();
-                else bulk_wait_read<1>();
-            }
-            __syncwarp();
-        }
-        uint4 g_now[MODE == kGatedBack ? 4 : 1], u_now[MODE == kGatedBack ? 4 : 1];
-        if constexpr (MODE == kGatedBack) {
+        uint4 now[kIn], r0[4], r1[4], r2[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                g_now[j] = g_next[j];
-                u_now[j] = u_next[j];
-            }
-            read(at, after, pieces);
-        }
+        for (int j = 0; j < kIn; ++j) now[j] = next[j];
+        read(at, after, pieces);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float (&f)[8] = *reinterpret_cast<float(*)[8]>(v + 8 * j);
-            uint4* a0 = piece_at(to, lane, j);
             if constexpr (MODE == kStore) {
-                if (loads) {
+                if (p.q[at.which].add) {
                     float r[8];
-                    unpack8(*a0, r);
+                    unpack8(now[j], r);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) f[i] += r[i];
                 }
-                *a0 = pack8(f);
+                r0[j] = pack8(f);
             } else if constexpr (MODE == kGated) {
                 float (&u)[8] = *reinterpret_cast<float(*)[8]>(up + 8 * j);
-                if (p.save) {
-                    *piece_at(to + kPiece, lane, j) = pack8(f);
-                    *piece_at(to + 2 * kPiece, lane, j) = pack8(u);
-                }
+                r0[j] = pack8(f);
+                r1[j] = pack8(u);
                 float unused;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = act<false>(f[i], p.gelu, unused) * u[i];
-                *a0 = pack8(f);
+                r2[j] = pack8(f);
             } else {
-                uint4 *a1 = piece_at(to + kPiece, lane, j), *a2 = piece_at(to + 2 * kPiece, lane, j);
                 float g[8], u[8], h[8];
-                unpack8(g_now[j], g);
-                unpack8(u_now[j], u);
+                unpack8(now[j], g);
+                unpack8(now[4 + j], u);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     float slope;
@@ -393,31 +377,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     g[i] = f[i] * u[i] * slope;
                     u[i] = f[i] * a;
                 }
-                *a0 = pack8(g);
-                *a1 = pack8(u);
-                *a2 = pack8(h);
+                r0[j] = pack8(g);
+                r1[j] = pack8(u);
+                r2[j] = pack8(h);
             }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            if constexpr (MODE == kStore) {
-                tma_store_3d(&m.out, to, x, row0, 0);
-            } else if constexpr (MODE == kGated) {
-                tma_store_3d(&m.out, to, x, row0, 0);
-                if (p.save) {
-                    tma_store_3d(&m.aux, to + kPiece, x, 0, row0);
-                    tma_store_3d(&m.aux, to + 2 * kPiece, x, 1, row0);
-                }
-            } else {
-                tma_store_3d(&m.out, to, x, 0, row0);
-                tma_store_3d(&m.out, to + kPiece, x, 1, row0);
-                tma_store_3d(&m.h, to + 2 * kPiece, x, row0, 0);
+        if constexpr (MODE == kStore) {
+            emit(r0, &m.out, x, row0, 0);
+        } else {
+            if (MODE == kGatedBack || p.save) {
+                emit(r0, &m.out, x, 0, row0);
+                emit(r1, &m.out, x, 1, row0);
             }
-            bulk_commit();
+            emit(r2, &m.aux, x, row0, 0);
         }
-        __syncwarp();
-        ++turn;
     };
     if constexpr (!SPLIT) {
         if (warp >= 2) {
@@ -425,13 +398,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = first; t < p.tiles && ok; t += stride, ++n) {
                 const TileAt at = tile_at<MODE>(p, t);
                 const int acc = n & 1, pieces = pieces_of(at);
-                if (loads_of(p.q[at.which]) && team < pieces) fetch(at, team);
                 read(at, team, pieces);
                 ok = wait_warp(&S.acc_full[acc], (n >> 1) & 1, &S.abort, p.status, p.limit);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t sums = tmem_addr(tmem, part * 32, acc * kTile);
-                for (int c = team; c < pieces && ok; c += 2) {
+                for (int c = team; c < pieces; c += 2) {
                     float v[32], up[MODE == kGated ? 32 : 1];
                     load_sums(sums + 32 * c, v);
                     if constexpr (MODE == kGated) load_sums(sums + kTile / 2 + 32 * c, up);
@@ -440,13 +412,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_at(peer_addr(&S.acc_empty[acc], lead));
+                if (lane == 0) mbar_arrive_at(peer_addr(&S.acc_empty[acc], 0));
             }
         }
     } else {
         // one tile: its sums as [column][128 rows] over the stages, which nothing reads any more
         float* sums = reinterpret_cast<float*>(base);
+        const TileAt at = tile_at<MODE>(p, first);
+        const int pieces = pieces_of(at), step = 2 * p.splits, begin = 2 * pair_of + team;
         if (warp >= 2) {
+            read(at, begin, pieces);
             ok = wait_warp(&S.acc_full[0], 0, &S.abort, p.status, p.limit);
             if (ok) {
                 tc_fence_after();
@@ -463,14 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         cluster_sync();
         if (warp >= 2 && ok) {
-            const TileAt at = tile_at<MODE>(p, first);
-            const int pieces = pieces_of(at), step = 2 * p.splits, begin = 2 * pair_of + team;
-            if (loads_of(p.q[at.which]) && begin < pieces) fetch(at, begin);
-            read(at, begin, pieces);
-            for (int c = begin; c < pieces && ok; c += step) {
+            for (int c = begin; c < pieces; c += step) {
                 float v[32] = {}, up[MODE == kGated ? 32 : 1] = {};
                 for (int q = 0; q < p.splits; ++q) {
-                    const uint32_t from = peer_addr(sums + (32 * c) * kBM + part * 32 + lane, 2 * q + rank);
+                    const uint32_t from = peer_addr(sums + 32 * c * kBM + part * 32 + lane, 2 * q + rank);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] += peer_load1(from + i * kBM * 4);
                     if constexpr (MODE == kGated) {
@@ -482,10 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    if (warp >= 2 && lane == 0) {
-        for (; seen != asked; ++seen) drain(&landed[seen & 1], (seen >> 1) & 1, p.limit);     // after an abort
-        bulk_wait_read<0>();
-    }
+    if (warp >= 2 && lane == 0) bulk_wait_read<0>();
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -734,6 +702,7 @@ struct Matrix {
     // As an operand: rows of K, or (mn) K as rows.
     bool operand(CUtensorMap* m, bool mn) const { return map(m, 64, mn ? 64 : kBM, TmaSwizzle::b128); }
     bool piece(CUtensorMap* m) const { return map(m, 32, 32, TmaSwizzle::b64); }
+    bool half_piece(CUtensorMap* m) const { return halves(m, 32, 32, TmaSwizzle::b64); }
 };
 
 bool problem(Problem& q, int M, int N, int K, int mode) {
@@ -758,7 +727,7 @@ int clusters_at_once(int width) {
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(width);
     c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = kSmem<MODE>;
+    c.dynamicSmemBytes = kSmem;
     c.attrs = at;
     c.numAttrs = 1;
     int n = 0;
@@ -800,18 +769,18 @@ Plan plan_of(const GemmParams& p) {
 
 template <bool AMN, bool BMN, int MODE, bool SPLIT>
 cudaError_t launch(const Maps& m0, const Maps& m1, const GemmParams& p, int blocks, cudaStream_t s) {
-    static_assert(kSmem<MODE> <= 232448, "shared memory of a block");
-    static_assert(!SPLIT || kStages<MODE> * kStageBytes >= kTile * kBM * 4, "the sums of a block");
-    return launch_in_clusters(ffn_gemm_kernel<AMN, BMN, MODE, SPLIT>, dim3(blocks), dim3(kThreads), kSmem<MODE>, s,
+    static_assert(kSmem <= 232448, "shared memory of a block");
+    static_assert(!SPLIT || kStages * kStageBytes >= kTile * kBM * 4, "the sums of a block");
+    return launch_in_clusters(ffn_gemm_kernel<AMN, BMN, MODE, SPLIT>, dim3(blocks), dim3(kThreads), kSmem, s,
                               SPLIT ? 2 * p.splits : 2, true, m0, m1, p);
 }
 
 template <bool AMN, bool BMN, int MODE>
 cudaError_t gemm(const Maps& m0, const Maps& m1, GemmParams p, cudaStream_t s, int* launches) {
     cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<AMN, BMN, MODE, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSmem<MODE>);
+                                         kSmem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(ffn_gemm_kernel<AMN, BMN, MODE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<MODE>);
+        e = cudaFuncSetAttribute(ffn_gemm_kernel<AMN, BMN, MODE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int all = p.tiles = p.q[0].tiles + p.q[1].tiles;
     const Plan plan = plan_of<AMN, BMN, MODE>(p);
@@ -882,7 +851,7 @@ size_t ffn_workspace_bytes(int N, int D, int F, int backward) {
 cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     const long long N = a.N, D = a.D, F = a.F;
     const Matrix x{a.x, N, D, a.x_row}, wi{a.W_in, D, 2 * F, 2 * F}, wo{a.W_out, F, D, D}, h{a.workspace, N, F, F},
-        y{a.y, N, D, D}, gu{a.gu, N, 2 * F, 2 * F}, res{a.residual, N, D, a.residual_row};
+        y{a.y, N, D, D}, gu{a.gu, N, 2 * F, 2 * F};
     *launches = 0;
     if (a.N <= kNarrow) {
         *launches = 2;
@@ -905,21 +874,21 @@ cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         if (!wo.operand(&w, true)) return cudaErrorInvalidValue;
         return narrow<true, kStore>(w, h, o, true, s);
     }
-    Maps m{};
     GemmParams p = params(a);
     p.save = a.gu != nullptr;
     p.debug_stall = a.debug_stall;
-    if (!x.operand(&m.a, false) || !wi.halves(&m.b, 64, 64, TmaSwizzle::b128) || !h.piece(&m.out) ||
-        (a.gu && !gu.halves(&m.aux, 32, 32, TmaSwizzle::b64)) || !problem(p.q[0], a.N, a.F, a.D, kGated))
+    Maps m{};
+    if (!x.operand(&m.a, false) || !wi.halves(&m.b, 64, 64, TmaSwizzle::b128) || !h.piece(&m.aux) ||
+        (a.gu && !gu.half_piece(&m.out)) || !problem(p.q[0], a.N, a.F, a.D, kGated))
         return cudaErrorInvalidValue;
     const cudaError_t e = gemm<false, true, kGated>(m, m, p, s, launches);
     if (e != cudaSuccess) return e;
     GemmParams o = params(a);
     Maps n{};
-    if (!h.operand(&n.a, false) || !wo.operand(&n.b, true) || !y.piece(&n.out) || (a.residual && !res.piece(&n.aux)) ||
-        !problem(o.q[0], a.N, a.D, a.F, kStore))
+    if (!h.operand(&n.a, false) || !wo.operand(&n.b, true) || !y.piece(&n.out) || !problem(o.q[0], a.N, a.D, a.F, kStore))
         return cudaErrorInvalidValue;
-    o.q[0].add = a.residual != nullptr;
+    o.q[0].add = static_cast<const bf16*>(a.residual);
+    o.q[0].add_row = a.residual_row;
     return gemm<false, true, kStore>(n, n, o, s, launches);
 }
 
@@ -944,13 +913,13 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         e = narrow<false, kGatedBack>(w, dy, p, false, s);
         ++*launches;
     } else {
-        Maps m{};
         GemmParams p = params(a);
         p.debug_stall = a.debug_stall;
-        if (!dy.operand(&m.a, false) || !wo.operand(&m.b, false) ||
-            !dgu.halves(&m.out, 32, 32, TmaSwizzle::b64) || !h.piece(&m.h) || !problem(p.q[0], a.N, a.F, a.D, kGatedBack))
-            return cudaErrorInvalidValue;
         p.gu = static_cast<const bf16*>(a.gu);
+        Maps m{};
+        if (!dy.operand(&m.a, false) || !wo.operand(&m.b, false) || !dgu.half_piece(&m.out) || !h.piece(&m.aux) ||
+            !problem(p.q[0], a.N, a.F, a.D, kGatedBack))
+            return cudaErrorInvalidValue;
         e = gemm<false, false, kGatedBack>(m, m, p, s, launches);
     }
     if (e != cudaSuccess) return e;
@@ -974,7 +943,7 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         if (e != cudaSuccess) return e;
     }
     if (!a.dW_in && !a.dW_out) return cudaSuccess;
-    // both weights' products in one launch: few tiles each, so that one's last round fills up with the other's
+    // both weights' products together: few tiles each, so that one's last round fills up with the other's
     GemmParams o = params(a);
     Maps n[2] = {};
     int k = 0;
@@ -984,11 +953,9 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
             return cudaErrorInvalidValue;
         ++k;
     }
-    if (a.dW_out) {
-        if (!h.operand(&n[k].a, true) || !dy.operand(&n[k].b, true) || !dwo.piece(&n[k].out) ||
-            !problem(o.q[k], a.F, a.D, a.N, kStore))
-            return cudaErrorInvalidValue;
-    }
+    if (a.dW_out && (!h.operand(&n[k].a, true) || !dy.operand(&n[k].b, true) || !dwo.piece(&n[k].out) ||
+                     !problem(o.q[k], a.F, a.D, a.N, kStore)))
+        return cudaErrorInvalidValue;
     return gemm<true, true, kStore>(n[0], n[1], o, s, launches);
 }
 
