@@ -24,6 +24,7 @@
 #include <climits>
 #include <cstdint>
 
+#include "overlap.cuh"
 #include "train_ops.h"
 
 namespace ttm {
@@ -279,6 +280,7 @@ template <bool EIGHT, int CAP>
 __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Table<CAP> t,
                                                           const __grid_constant__ AdamwScalars a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    after_all_before();
     const Consts k = constants(a);
     for (int chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
         int lo = 0, hi = t.count - 1;   // the last tensor that starts at or before the chunk
@@ -309,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
 __global__ void __launch_bounds__(kThreads) adamw_moments_kernel(long long blocks, const __grid_constant__ AdamwScalars a,
                                                                   float* m, float* v) {
     const int lane = threadIdx.x & 31;
+    after_all_before();
     for (long long b = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); b < blocks; b += (long long)gridDim.x * kWarps) {
         const float ms = a.m_scale[b], vs = a.v_scale[b];
 #pragma unroll
@@ -332,12 +335,11 @@ cudaError_t launch(const AdamwEntry* tensors, int count, int chunks, int last, c
     t.chunks = chunks;
     t.last = last;
     const int most = kSms * 4, grid = chunks < 1 ? 1 : chunks < most ? chunks : most;
-    adamw_kernel<EIGHT, CAP><<<grid, kThreads, 0, s>>>(t, a);
-    return cudaGetLastError();
+    return launch_overlapped(adamw_kernel<EIGHT, CAP>, dim3(grid), dim3(kThreads), s, t, a);
 }
 
 // Kernel arguments take 32764 bytes at most; short lists go with a short table.
-constexpr int kMost = 500, kFew = 48;
+constexpr int kMost = 500, kSome = 144, kFew = 32;
 
 template <bool EIGHT>
 cudaError_t run(const AdamwEntry* tensors, int count, const AdamwScalars& a, cudaStream_t s, int* launches) {
@@ -355,8 +357,9 @@ cudaError_t run(const AdamwEntry* tensors, int count, const AdamwScalars& a, cud
             part[n++].chunk = (int)chunks;
             chunks += more;
         }
-        const cudaError_t e = n <= kFew ? launch<EIGHT, kFew>(part, n, (int)chunks, at == count, a, s)
-                                        : launch<EIGHT, kMost>(part, n, (int)chunks, at == count, a, s);
+        const cudaError_t e = n <= kFew    ? launch<EIGHT, kFew>(part, n, (int)chunks, at == count, a, s)
+                              : n <= kSome ? launch<EIGHT, kSome>(part, n, (int)chunks, at == count, a, s)
+                                           : launch<EIGHT, kMost>(part, n, (int)chunks, at == count, a, s);
         if (e != cudaSuccess) return e;
         ++*launches;
     } while (at < count);
@@ -374,8 +377,7 @@ cudaError_t adamw_moments_launch(long long blocks, const AdamwScalars& a, float*
     if (blocks == 0) return cudaSuccess;
     const long long need = (blocks + kWarps - 1) / kWarps;
     const int grid = need < kSms * 8 ? (int)need : kSms * 8;
-    adamw_moments_kernel<<<grid, kThreads, 0, s>>>(blocks, a, m, v);
-    return cudaGetLastError();
+    return launch_overlapped(adamw_moments_kernel, dim3(grid), dim3(kThreads), s, blocks, a, m, v);
 }
 
 }  // namespace ttm

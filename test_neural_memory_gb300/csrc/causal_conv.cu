@@ -15,6 +15,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "overlap.cuh"
 #include "pairs.cuh"
 #include "train_ops.h"
 
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(kFwdThreads) conv_fwd_kernel(const __grid_cons
         n = rest / strips;
         part = rest - n * strips;
     }
+    after_all_before();
     if (n >= (unsigned)a.N) return;
     const int c = (int)group * V, K = a.K, C = a.C, before = kAll ? 0 : KW - K;
     const int t0 = (int)part * strip, t1 = min(a.T, t0 + strip);
@@ -288,6 +290,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const
     const int group = blockIdx.x * blockDim.x + threadIdx.x;
     const bool live = group < groups;
     const int c = live ? group * V : 0;
+    after_all_before();
     E w[KW][NV], bias[NV], dw[KW][NV], db[NV];
     load_taps<V, KW, kAll>(w, a.w, c, K);
 #pragma unroll
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const
 __global__ void __launch_bounds__(256) conv_join_kernel(const float* parts, int rows, int C, int K, float* dw,
                                                          float* db) {
     __shared__ float sums[8][32];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_all_before();
     const int c = blockIdx.x * 32 + threadIdx.x, q = blockIdx.y;
     float total = 0.f;
     if (c < C)
@@ -502,9 +505,8 @@ cudaError_t fwd(const ConvArgs& a, bool one_strip, cudaStream_t s) {
     const unsigned strips = (a.T + strip - 1) / strip;
     const long long blocks = ((long long)a.N * groups * strips + kFwdThreads - 1) / kFwdThreads;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    if (a.doc) conv_fwd_kernel<T, V, KW, kAll, true><<<(unsigned)blocks, kFwdThreads, 0, s>>>(a, groups, strips, strip);
-    else conv_fwd_kernel<T, V, KW, kAll, false><<<(unsigned)blocks, kFwdThreads, 0, s>>>(a, groups, strips, strip);
-    return cudaGetLastError();
+    return launch_overlapped(a.doc ? conv_fwd_kernel<T, V, KW, kAll, true> : conv_fwd_kernel<T, V, KW, kAll, false>,
+                             dim3((unsigned)blocks), dim3(kFwdThreads), s, a, groups, strips, strip);
 }
 
 // Rows of the gradient's grid at most, one wave by the widest channel groups that a call may take; the workspace
@@ -532,20 +534,11 @@ cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
     const long long wanted = ((long long)a.N * strips + by - 1) / by;
     if (wanted < rows) rows = (int)wanted;
     const dim3 grid(across, rows), block(bx, by);
-    if (a.doc) conv_bwd_kernel<T, V, KW, kAll, true><<<grid, block, 0, s>>>(a, groups, strips, strip);
-    else conv_bwd_kernel<T, V, KW, kAll, false><<<grid, block, 0, s>>>(a, groups, strips, strip);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_overlapped(a.doc ? conv_bwd_kernel<T, V, KW, kAll, true> : conv_bwd_kernel<T, V, KW, kAll, false>,
+                                            grid, block, s, a, groups, strips, strip);
     if (e != cudaSuccess || !a.partial) return e;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((a.C + 31) / 32, a.K + 1);
-    c.blockDim = dim3(32, 8);
-    c.stream = s;
-    c.attrs = at;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, conv_join_kernel, (const float*)a.partial, rows, a.C, a.K, a.dw, a.db);
+    return launch_overlapped(conv_join_kernel, dim3((a.C + 31) / 32, a.K + 1), dim3(32, 8), s, (const float*)a.partial, rows,
+                             a.C, a.K, a.dw, a.db);
 }
 
 bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
