@@ -15,7 +15,7 @@
 // takes blocks of 256 values, 8 a lane in two runs of 4, so that every access of a warp is one piece of
 // memory; tensors that do not start on 16 bytes, and their last blocks, go value by value.  The table of
 // tensors travels as a kernel argument (a copy to the device would be a call of its own, and not the
-// captured graph's), and a block finds its tensor by bisection.
+// captured graph's), and a block finds its first tensor by bisection.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -62,15 +62,17 @@ __device__ __forceinline__ int scale_of(uint32_t most) {
 }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// The e4m3 code of the finite |x| / 2^e (times `inverse`, exact): its lower neighbour on the grid, or the upper one where
-// the missing part of a step and `frac` (in 2^-16) make one.  Above 2^-6 adding frac below the three bits that stay
-// carries by itself; below, steps are 2^-9 and the sum of both parts is rounded to 24 bits before the floor.
-__device__ __forceinline__ uint32_t to_code(float x, float inverse, uint32_t frac) {
-    const float y = fabsf(x) * inverse;
-    const uint32_t u = __float_as_uint(y);
-    uint32_t code = ((u + (frac << 4)) >> 20) - (120u << 3);
-    if (u < 0x3c800000u) code = (uint32_t)__fadd_rn(y * 512.f, (float)frac * (1.f / 65536.f));
-    return code | (__float_as_uint(x) >> 24 & 0x80u);
+// The e4m3 code of a size y (bits u) from 2^-6 to 448: its lower neighbour on the grid, or the upper one where the missing part
+// of a step and `frac`, in 2^-16 of one and shifted by 4, make a step: added below the three bits that stay, it
+// carries by itself.
+constexpr uint32_t kSmallest = 0x3c800000u;             // 2^-6
+__device__ __forceinline__ uint32_t to_code(uint32_t u, uint32_t frac4) { return (u + frac4 - (120u << 23)) >> 20; }
+__device__ __forceinline__ uint32_t low_bytes(const uint32_t (&c)[4]) {
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+}
+// Below 2^-6, where steps are 2^-9 (the sum is rounded to 24 bits before the floor).
+__device__ __forceinline__ uint32_t to_small_code(float y, uint32_t frac4) {
+    return (uint32_t)__fadd_rn(y * 512.f, (float)frac4 * (1.f / 1048576.f));
 }
 
 __device__ __forceinline__ float4 decode4(uint32_t code) {
@@ -172,7 +174,7 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
         ms = a.m_scale[e.first + block];
         vs = a.v_scale[e.first + block];
     }
-    uint32_t most_m = 0, most_r = 0, mc[8], vc[8];      // largest sizes; codes
+    uint32_t most_m = 0, most_r = 0, mc[2], vc[2];  // largest sizes; codes, four to a word
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         if constexpr (EIGHT) {
@@ -231,14 +233,32 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
         const float im = power(-em), ir = power(-er);
         // a block's places differ in their low 8 bits
         const uint32_t key = (uint32_t)s0 + k.key + (uint32_t)((unsigned long long)s0 >> 32) * 0x85ebca6bu;
+        uint32_t least = kInf;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t h = hash32(key + index(j));
-            mc[j] = to_code(m[j], im, h & 0xffffu);
-            vc[j] = to_code(v[j], ir, h >> 16);
-            if (odd) {                                  // e4m3 has no infinity
-                if (size_bits(m[j]) >= kInf) mc[j] = 0x7f;
-                if (size_bits(v[j]) >= kInf) vc[j] = 0x7f;
+        for (int q = 0; q < 2; ++q) {
+            uint32_t cm[4], cr[4];                      // (garbage above the low byte for what is below 2^-6)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = 4 * q + i;
+                const uint32_t h = hash32(key + index(j)), um = __float_as_uint(fabsf(m[j]) * im), ur = __float_as_uint(v[j] * ir);
+                cm[i] = to_code(um, h << 4 & 0xffff0u) | (__float_as_uint(m[j]) >> 24 & 0x80u);
+                cr[i] = to_code(ur, h >> 12 & 0xffff0u);
+                least = min(least, min(um, ur));
+            }
+            mc[q] = low_bytes(cm);
+            vc[q] = low_bytes(cr);
+        }
+        if (least < kSmallest || odd) {                 // rare: values 2^-14 of their block's largest, zeros, no numbers
+            auto put = [](uint32_t& word, int at, uint32_t code) { word = (word & ~(0xffu << 8 * at)) | code << 8 * at; };
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t h = hash32(key + index(j));
+                const float ym = fabsf(m[j]) * im, yr = v[j] * ir;
+                if (__float_as_uint(ym) < kSmallest)
+                    put(mc[j / 4], j & 3, to_small_code(ym, h << 4 & 0xffff0u) | (__float_as_uint(m[j]) >> 24 & 0x80u));
+                if (__float_as_uint(yr) < kSmallest) put(vc[j / 4], j & 3, to_small_code(yr, h >> 12 & 0xffff0u));
+                if (size_bits(m[j]) >= kInf) put(mc[j / 4], j & 3, 0x7f);        // e4m3 has no infinity
+                if (size_bits(v[j]) >= kInf) put(vc[j / 4], j & 3, 0x7f);
             }
         }
         if (lane == 0) {
@@ -251,10 +271,8 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
         for (int h = 0; h < 2; ++h) {
             const int i = h * 128 + lane * 4;
             if constexpr (EIGHT) {
-                const uint32_t* x = mc + 4 * h;
-                const uint32_t* r = vc + 4 * h;
-                *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.m) + s0 + i) = x[0] | x[1] << 8 | x[2] << 16 | x[3] << 24;
-                *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.v) + s0 + i) = r[0] | r[1] << 8 | r[2] << 16 | r[3] << 24;
+                *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.m) + s0 + i) = mc[h];
+                *reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(a.v) + s0 + i) = vc[h];
             } else {
                 *reinterpret_cast<float4*>(static_cast<float*>(a.m) + s0 + i) = *reinterpret_cast<float4*>(m + 4 * h);
                 *reinterpret_cast<float4*>(static_cast<float*>(a.v) + s0 + i) = *reinterpret_cast<float4*>(v + 4 * h);
@@ -266,8 +284,8 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
             const int i = lane + 32 * j;
             if (i >= n) continue;
             if constexpr (EIGHT) {
-                static_cast<unsigned char*>(a.m)[s0 + i] = (unsigned char)mc[j];
-                static_cast<unsigned char*>(a.v)[s0 + i] = (unsigned char)vc[j];
+                static_cast<unsigned char*>(a.m)[s0 + i] = (unsigned char)(mc[j / 4] >> 8 * (j & 3));
+                static_cast<unsigned char*>(a.v)[s0 + i] = (unsigned char)(vc[j / 4] >> 8 * (j & 3));
             } else {
                 static_cast<float*>(a.m)[s0 + i] = m[j];
                 static_cast<float*>(a.v)[s0 + i] = v[j];
@@ -282,13 +300,14 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     after_all_before();
     const Consts k = constants(a);
+    int lo = 0, hi = t.count - 1;       // the last tensor that starts at or before the first chunk
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.e[mid].chunk <= (int)blockIdx.x) lo = mid;
+        else hi = mid - 1;
+    }
     for (int chunk = blockIdx.x; chunk < t.chunks; chunk += gridDim.x) {
-        int lo = 0, hi = t.count - 1;   // the last tensor that starts at or before the chunk
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (t.e[mid].chunk <= chunk) lo = mid;
-            else hi = mid - 1;
-        }
+        while (lo + 1 < t.count && t.e[lo + 1].chunk <= chunk) ++lo;
         const AdamwEntry& e = t.e[lo];
         const long long block = (long long)(chunk - e.chunk) * kWarps + warp;
         if (block * kBlock >= e.n) continue;

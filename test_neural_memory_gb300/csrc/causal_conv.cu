@@ -81,6 +81,14 @@ __device__ __forceinline__ void store(T* p, const Val<V> (&f)[kVals<V>]) {
     }
     *reinterpret_cast<Raw<T, V>*>(p) = raw;
 }
+// A value of 4, 8 or 16 bytes into shared memory, asynchronously.
+template <typename R, typename T>
+__device__ __forceinline__ void copy_async(R* to, const T* from) {
+    if constexpr (sizeof(R) >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                     "n"(sizeof(R))
+                     : "memory");
+}
 template <int V>
 __device__ __forceinline__ Val<V> gather(const float* p, long long step) {     // the values of neighbouring channels
     if constexpr (V == 1) return p[0];
@@ -285,7 +293,11 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const
                                                                 int strips, int strip) {
     constexpr int NV = kVals<V>;
     using E = Val<V>;
+    constexpr bool kRing = sizeof(Raw<T, V>) >= 4;      // (asynchronous copies take 4 bytes at least)
+    constexpr int kDeep = 4;                            // batches of rows on their way, or in the ring
+    __shared__ Raw<T, V> ring[kRing ? kDeep * kBatch * 2 : 1][kBwdThreads];
     __shared__ float sums[kBwdThreads * V];
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x;
     const int K = a.K, C = a.C, before = kAll ? 0 : KW - K;
     const int group = blockIdx.x * blockDim.x + threadIdx.x;
     const bool live = group < groups;
@@ -316,19 +328,32 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const
         Raw<T, V> next[kBatch], dnext[kBatch];
         int next_id[kBatch];
         const T *from = rows.x + (long long)t0 * rows.tok, *dfrom = static_cast<const T*>(a.dy) + n * a.dy_seq + (long long)t0 * a.dy_tok + c;
+        int slot = 0;
+        // Rows t .. t + kBatch - 1 on their way: into this thread's places of the ring, or registers.
         auto fetch = [&](int t) {
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 if (t + j < end) {
-                    next[j] = load<T, V>(from);
-                    dnext[j] = load<T, V>(dfrom);
-                    if (DOC) next_id[j] = doc[t + j];
+                    if constexpr (kRing) {
+                        copy_async(&ring[(slot * kBatch + j) * 2][tid], from);
+                        copy_async(&ring[(slot * kBatch + j) * 2 + 1][tid], dfrom);
+                    } else {
+                        next[j] = load<T, V>(from);
+                        dnext[j] = load<T, V>(dfrom);
+                        if (DOC) next_id[j] = doc[t + j];
+                    }
                 }
                 from += rows.tok;
                 dfrom += a.dy_tok;
             }
+            if constexpr (kRing) asm volatile("cp.async.commit_group;" ::: "memory");
+            slot = slot + 1 == kDeep ? 0 : slot + 1;
         };
         fetch(t0);
+        if constexpr (kRing) {
+#pragma unroll
+            for (int i = 1; i < kDeep; ++i) fetch(t0 + i * kBatch);
+        }
         E win[KW][NV], d[KW][NV];       // rows t - KW + 1 .. t and their d
         int ids[KW];
 #pragma unroll
@@ -413,13 +438,24 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const
         for (int t = t0; t < t1 + KW - 1; t += kBatch) {
             Raw<T, V> raw[kBatch], draw[kBatch];
             int raw_id[kBatch];
+            if constexpr (kRing) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                raw[j] = next[j];
-                draw[j] = dnext[j];
-                raw_id[j] = DOC ? next_id[j] : 0;
+                for (int j = 0; j < kBatch; ++j) {
+                    raw[j] = ring[(slot * kBatch + j) * 2][tid];
+                    draw[j] = ring[(slot * kBatch + j) * 2 + 1][tid];
+                    raw_id[j] = DOC && t + j < end ? doc[t + j] : 0;
+                }
+                fetch(t + kDeep * kBatch);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    raw[j] = next[j];
+                    draw[j] = dnext[j];
+                    raw_id[j] = DOC ? next_id[j] : 0;
+                }
+                fetch(t + kBatch);
             }
-            fetch(t + kBatch);
             if (t - (KW - 1) >= t0 && t + kBatch <= t1) {
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) token(std::true_type{}, t + j, raw[j], draw[j], raw_id[j]);
@@ -435,9 +471,10 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const
                 }
             }
         }
+        if constexpr (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
     }
     if (!a.partial) return;
-    const int bx = blockDim.x, tid = threadIdx.y * bx + threadIdx.x;
+    const int bx = blockDim.x;
     float* to = a.partial + (size_t)blockIdx.y * (K + 1) * C;
 #pragma unroll
     for (int q = 0; q <= KW; ++q) {     // tap slots, then db
