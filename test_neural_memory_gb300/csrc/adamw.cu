@@ -294,8 +294,12 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
     }
 }
 
+// Blocks an SM: 8 bits have 85 instructions and more to a value and want every warp; 32 bits are at HBM's rate either way
+// and go 3 % faster with fewer rows of memory open at a time (92 M values 396 us, 407 with four).
+template <bool EIGHT> constexpr int kBlocksPerSm = EIGHT ? 4 : 3;
+
 template <bool EIGHT, int CAP>
-__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Table<CAP> t,
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm<EIGHT>) adamw_kernel(const __grid_constant__ Table<CAP> t,
                                                           const __grid_constant__ AdamwScalars a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     after_all_before();
@@ -353,7 +357,7 @@ cudaError_t launch(const AdamwEntry* tensors, int count, int chunks, int last, c
     t.count = count;
     t.chunks = chunks;
     t.last = last;
-    const int most = kSms * 4, grid = chunks < 1 ? 1 : chunks < most ? chunks : most;
+    const int most = kSms * kBlocksPerSm<EIGHT>, grid = chunks < 1 ? 1 : chunks < most ? chunks : most;
     return launch_overlapped(adamw_kernel<EIGHT, CAP>, dim3(grid), dim3(kThreads), s, t, a);
 }
 

@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // tiles are; each leaves its sums in shared memory, and a share of the results is added up over the blocks
 // in their order, put through the epilogue and written by each.  The second kernel of a call starts on its weights
 // while the first one finishes.
-constexpr int kNarrowBlocks = 176;               // blocks of a launch at most, of 304 places
+constexpr int kNarrowBlocks = 304;               // blocks of a launch at most: two an SM
 constexpr int kNarrow = 128, kNarrowThreads = 256, kNarrowStages = 6, kNarrowSmem = 110 * 1024;
 
 struct NarrowParams {
@@ -532,17 +532,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
         // A call's second kernel needs its first one's results, but not for the weights, whose first stages are on
         // their way before its end.  The first kernel lets the second one start only when all before it has ended,
         // whatever wrote the weights among it.
-        // What does not fit, and the first kernel's weights, are asked into the L2 cache meanwhile: that is where later
-        // writes would meet them.
         const int ahead = max(0, min(p.stages, k1 - k0));
         if (p.second)
             for (int i = 0; i < ahead; ++i) weights(k0 + i, i);
-        for (int k = p.second ? k0 + ahead : k0; k < k1; ++k)
-            for (int i = 0; i < (WMN ? 2 : 1); ++i) {
-                if (MODE == kGated) tma_prefetch_l2_3d(&mw, first, i, k * kBK);
-                else if (WMN) tma_prefetch_l2_3d(&mw, first + 64 * i, k * kBK, 0);
-                else tma_prefetch_l2_3d(&mw, k * kBK, first, 0);
-            }
         asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;");
         if (!p.second)
@@ -605,6 +597,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     }
     tc_fence_before();
     cluster_sync();
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // (long over: for the residual, g and u, read by every thread)
     if (good) {
         constexpr int kGroups = MODE == kGated ? 16 : 32;            // of 4 columns
         const int items = p.N * kGroups, share = (items + ranks - 1) / ranks;
@@ -795,8 +788,8 @@ cudaError_t gemm(const Maps& m0, const Maps& m1, GemmParams p, cudaStream_t s, i
     return launch<AMN, BMN, MODE, true>(m0, m1, p, 2 * p.splits * (all - p.tile0), s);
 }
 
-// Splits of K, of two blocks of K at least: about a block an SM, so that the blocks of a call's second kernel fit beside
-// the first one's and have their weights on the way.
+// Splits of K, of two blocks of K at least, that fill the places of two blocks an SM (16 x 2048 x 5504: 19.4 us a call, 22.2
+// with three quarters of that, 25 with more blocks than places).
 template <bool WMN, int MODE>
 cudaError_t narrow(const CUtensorMap& mw, const Matrix& x, NarrowParams p, bool second, cudaStream_t s) {
     const int columns = MODE == kGated ? 64 : 128, tiles = (p.wide + columns - 1) / columns;
