@@ -147,28 +147,15 @@ struct Rows {
 };
 
 // KW: the window, K at most (kAll: K itself); tap i of K sits in slot i + KW - K, slots before it take no part.
-template <int V, int KW, bool kAll, bool DOC>
+// kOne: every row of the window is of the token's document.
+template <int V, int KW, bool kAll, bool kOne>
 __device__ __forceinline__ void taps(Val<V> (&out)[kVals<V>], const Val<V> (&w)[KW][kVals<V>],
                                      const Val<V> (&win)[KW][kVals<V>], const int (&id)[KW], int before) {
-    bool same = true;
-    if (DOC) {
 #pragma unroll
-        for (int i = 0; i + 1 < KW; ++i) same &= i < before || id[i] == id[KW - 1];
-    }
-    if (!DOC || same) {
+    for (int i = 0; i < KW; ++i) {
+        if ((!kAll && i < before) || (!kOne && id[i] != id[KW - 1])) continue;
 #pragma unroll
-        for (int i = 0; i < KW; ++i) {
-            if (!kAll && i < before) continue;
-#pragma unroll
-            for (int v = 0; v < kVals<V>; ++v) out[v] = fma(w[i][v], win[i][v], out[v]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < KW; ++i) {
-            if (i < before || id[i] != id[KW - 1]) continue;
-#pragma unroll
-            for (int v = 0; v < kVals<V>; ++v) out[v] = fma(w[i][v], win[i][v], out[v]);
-        }
+        for (int v = 0; v < kVals<V>; ++v) out[v] = fma(w[i][v], win[i][v], out[v]);
     }
 }
 
@@ -226,7 +213,7 @@ __global__ void __launch_bounds__(kFwdThreads) conv_fwd_kernel(const __grid_cons
 #pragma unroll
     for (int v = 0; v < NV; ++v) bias[v] = a.b ? gather<V>(a.b + c + v * (V / NV), 1) : zero<Val<V>>();
     T* y = static_cast<T*>(a.y) + ((long long)n * a.T + t0) * C + c;
-    auto token = [&](const Raw<T, V>& raw, int raw_id) {
+    auto token = [&](auto one, const Raw<T, V>& raw, int raw_id) {
 #pragma unroll
         for (int i = 0; i + 1 < KW; ++i) {
 #pragma unroll
@@ -238,7 +225,7 @@ __global__ void __launch_bounds__(kFwdThreads) conv_fwd_kernel(const __grid_cons
         Val<V> out[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) out[v] = bias[v];
-        taps<V, KW, kAll, DOC>(out, w, win, ids, before);
+        taps<V, KW, kAll, decltype(one)::value>(out, w, win, ids, before);
         if (a.silu) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) out[v] = mul(out[v], sigmoid<T>(out[v]));
@@ -256,12 +243,31 @@ __global__ void __launch_bounds__(kFwdThreads) conv_fwd_kernel(const __grid_cons
             raw_id[j] = DOC ? next_id[j] : 0;
         }
         fetch(t + kBatch);
+        bool one = true;                // the window and the batch are of one document
+        if (DOC) {
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) token(raw[j], raw_id[j]);
+            for (int i = 1; i + 1 < KW; ++i) one &= ids[i] == ids[KW - 1];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) one &= raw_id[j] == ids[KW - 1];
+        }
+        if (one) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) token(std::true_type{}, raw[j], raw_id[j]);
+        } else if constexpr (DOC) {
+#pragma unroll 1
+            for (int j = 0; j < kBatch; ++j) {          // (one copy of the code for the few batches with a border)
+                Raw<T, V> r = raw[0];
+                int id = raw_id[0];
+#pragma unroll
+                for (int i = 1; i < kBatch; ++i)
+                    if (j == i) { r = raw[i]; id = raw_id[i]; }
+                token(std::false_type{}, r, id);
+            }
+        }
     }
 #pragma unroll
     for (int j = 0; j + 1 < kBatch; ++j)
-        if (t + j < t1) token(next[j], DOC ? next_id[j] : 0);
+        if (t + j < t1) token(std::integral_constant<bool, !DOC>{}, next[j], DOC ? next_id[j] : 0);
     if (a.state && part + 1 == strips) {
         T* s = static_cast<T*>(a.state) + (long long)n * (K - 1) * C + c;
 #pragma unroll
@@ -366,7 +372,8 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const
 #pragma unroll
             for (int v = 0; v < NV; ++v) d[i][v] = zero<E>();
         }
-        // One token: kInner where it is of the strip, its row to leave too, and neither is next to an end.
+        // One token: kInner where it is of the strip, its row to leave too, neither is next to an end, and all of the
+        // window is of one document.
         auto token = [&](auto inner, int now, const Raw<T, V>& raw, const Raw<T, V>& draw, int raw_id) {
             constexpr bool kInner = decltype(inner)::value;
             const int row = now - (KW - 1);
@@ -387,7 +394,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const
                     E pre[NV];
 #pragma unroll
                     for (int v = 0; v < NV; ++v) pre[v] = bias[v];
-                    taps<V, KW, kAll, DOC>(pre, w, win, ids, before);
+                    taps<V, KW, kAll, kInner || !DOC>(pre, w, win, ids, before);
 #pragma unroll
                     for (int v = 0; v < NV; ++v) {
                         const E g = sigmoid<T>(pre[v]);
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const
                 if (kInner || now < t1) {
 #pragma unroll
                     for (int i = 0; i < KW; ++i) {
-                        if ((!kAll && i < before) || (DOC && ids[i] != ids[KW - 1])) continue;
+                        if ((!kAll && i < before) || (DOC && !kInner && ids[i] != ids[KW - 1])) continue;
 #pragma unroll
                         for (int v = 0; v < NV; ++v) dw[i][v] = fma(d[KW - 1][v], win[i][v], dw[i][v]);
                     }
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const
                 for (int v = 0; v < NV; ++v) out[v] = zero<E>();
 #pragma unroll
                 for (int m = 0; m < KW; ++m) {
-                    if ((!kAll && m >= K) || (DOC && ids[m] != ids[0])) continue;
+                    if ((!kAll && m >= K) || (DOC && !kInner && ids[m] != ids[0])) continue;
 #pragma unroll
                     for (int v = 0; v < NV; ++v) out[v] = fma(w[KW - 1 - m][v], d[m][v], out[v]);
                 }
@@ -456,7 +463,14 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const
                 }
                 fetch(t + kBatch);
             }
-            if (t - (KW - 1) >= t0 && t + kBatch <= t1) {
+            bool inner = t - (KW - 1) >= t0 && t + kBatch <= t1;
+            if (DOC) {
+#pragma unroll
+                for (int i = 1; i + 1 < KW; ++i) inner &= ids[i] == ids[KW - 1];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) inner &= raw_id[j] == ids[KW - 1];
+            }
+            if (inner) {
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) token(std::true_type{}, t + j, raw[j], draw[j], raw_id[j]);
             } else {

@@ -152,16 +152,30 @@ struct Range {
     bool written;
 };
 
-// Whether a written range meets another one.
-bool ranges_clash(std::vector<Range>& r) {
-    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+template <typename F>
+bool sorted_ranges_clash(size_t n, F range) {
     uintptr_t any = 0, written = 0;         // ends of the ranges so far
-    for (const Range& x : r) {
+    for (size_t i = 0; i < n; ++i) {
+        const Range x = range(i);
         if (x.from < written || (x.written && x.from < any)) return true;
         any = std::max(any, x.to);
         if (x.written) written = std::max(written, x.to);
     }
     return false;
+}
+
+// Whether a written range meets another one.  Sorted as one word each, the start (in 2 bytes, the least alignment) and the
+// place: a list of a few hundred is a good part of a short call's time.
+bool ranges_clash(const std::vector<Range>& r) {
+    if (r.size() >= 65536) {
+        std::vector<Range> by_start(r);
+        std::sort(by_start.begin(), by_start.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+        return sorted_ranges_clash(by_start.size(), [&](size_t i) { return by_start[i]; });
+    }
+    std::vector<uint64_t> key(r.size());
+    for (size_t i = 0; i < r.size(); ++i) key[i] = (uint64_t)(r[i].from >> 1) << 16 | i;
+    if (!std::is_sorted(key.begin(), key.end())) std::sort(key.begin(), key.end());
+    return sorted_ranges_clash(r.size(), [&](size_t i) { return r[key[i] & 0xffff]; });
 }
 
 int glr_run(ttm::GlrArgs& a, int backward, void* workspace, size_t workspace_bytes, void* stream) {
