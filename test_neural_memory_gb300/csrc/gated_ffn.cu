@@ -14,8 +14,9 @@
 // What bounds a tile is how far ahead the copies run: 32 KB a block of K and 2000 cycles until they land; with four
 // stages a block of K took 900 cycles, with five 680, with six 560, where the tensor cores need 512.  So the epilogue has
 // little shared memory: 32 rows by 32 columns a warp at a time, one result after the other through two places (rows of 64
-// bytes, swizzled: free of conflicts), out by tensor copies, which also cut what lies outside the matrices; what it
-// reads goes to registers.
+// bytes, swizzled: free of conflicts), from where rows of 64 bytes leave.  (By tensor copies every result waits for a
+// fence and for the copy before it: 4700 cycles for kGatedBack's three, of which 1700 are arithmetic.)  What it reads goes
+// to registers a piece ahead.
 //
 // Roundings: g and u enter the activation in fp32; h, dg and du are rounded to bf16 once, as operands of the next
 // product (half a step, 2^-8 of a value at most: the same as rounding the result, and what the tensor cores
@@ -42,53 +43,57 @@ using bf16 = __nv_bfloat16;
 constexpr long long kWaitCycles = 4000000000LL;   // default limit, ~2 s at 2 GHz
 constexpr int kPairs = 76;                        // pairs of the 152 SMs
 
-__device__ __forceinline__ uint32_t bf162_bits(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Values in pairs, as bf16 in words.
+template <int N>
+__device__ __forceinline__ void unpack(const uint32_t* w, f2 (&f)[N]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < N; ++i) f[i] = pair_of_bf16(w[i]);
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(bf162_bits(f[0], f[1]), bf162_bits(f[2], f[3]), bf162_bits(f[4], f[5]), bf162_bits(f[6], f[7]));
+__device__ __forceinline__ void unpack(const uint4& u, f2 (&f)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    unpack<4>(w, f);
 }
-
-__device__ __forceinline__ void unpack4(const uint2& u, float (&f)[4]) {
-    f[0] = __uint_as_float(u.x << 16); f[1] = __uint_as_float(u.x & 0xffff0000u);
-    f[2] = __uint_as_float(u.y << 16); f[3] = __uint_as_float(u.y & 0xffff0000u);
+__device__ __forceinline__ void unpack(const uint2& u, f2 (&f)[2]) {
+    const uint32_t w[2] = {u.x, u.y};
+    unpack<2>(w, f);
 }
-__device__ __forceinline__ uint2 pack4(const float (&f)[4]) { return make_uint2(bf162_bits(f[0], f[1]), bf162_bits(f[2], f[3])); }
+__device__ __forceinline__ uint4 pack(const f2 (&f)[4]) {
+    return make_uint4(bf16_of_pair(f[0]), bf16_of_pair(f[1]), bf16_of_pair(f[2]), bf16_of_pair(f[3]));
+}
+__device__ __forceinline__ uint2 pack(const f2 (&f)[2]) { return make_uint2(bf16_of_pair(f[0]), bf16_of_pair(f[1])); }
 
 // ------------------------------------------------------------------------ activation
 
-// act(g) and, where kSlope, its derivative.  GELU: with z = |g| / sqrt(2), the upper tail of the normal distribution is
-// erfc(z) / 2 = exp(-z^2) P(1 / (1 + 0.425 z)), P a polynomial fitted to exp(z^2) erfc(z) / 2 over the z that matter
-// (2e-6 of itself at most, by iterated least squares on the relative error); the density's exponential is the same one.
+// act(g) and, where kSlope, its derivative, of two values.  GELU: with z = |g| / sqrt(2), the upper tail of the normal
+// distribution is erfc(z) / 2 = exp(-z^2) P(1 / (1 + 0.425 z)), P a polynomial fitted to exp(z^2) erfc(z) / 2 over the z
+// that matter (2e-6 of itself at most, by iterated least squares on the relative error); the density's exponential is
+// the same one.
 template <bool kSlope>
-__device__ __forceinline__ float act(float g, int gelu, float& slope) {
+__device__ __forceinline__ f2 act(f2 g, int gelu, f2& slope) {
     if (gelu) {
-        float e, t;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * g * -0.72134752f));                 // exp(-g^2 / 2)
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(fabsf(g), 0.425f * 0.70710678f, 1.f)));
-        float p = -0.08400925f;
-        p = fmaf(p, t, 0.23711844f);
-        p = fmaf(p, t, -0.04467765f);
-        p = fmaf(p, t, 0.16266398f);
-        p = fmaf(p, t, 0.10760187f);
-        p = fmaf(p, t, 0.12137473f);
-        p = fmaf(p, t, -7.3115713e-5f);
-        const float tail = e * p, c = g < 0.f ? tail : 1.f - tail;
-        if (kSlope) slope = fmaf(g * 0.39894228f, e, c);
-        return g * c;
+        float a, b, ea, eb, ta, tb, pa, pb;
+        split(mul(mul(g, g), splat<f2>(-0.72134752f)), a, b);                                    // -g^2 / 2 in base 2
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ea) : "f"(a));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(eb) : "f"(b));
+        split(g, a, b);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ta) : "f"(fmaf(fabsf(a), 0.425f * 0.70710678f, 1.f)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(tb) : "f"(fmaf(fabsf(b), 0.425f * 0.70710678f, 1.f)));
+        const f2 t = pair(ta, tb), e = pair(ea, eb);
+        f2 p = splat<f2>(-0.08400925f);
+        p = fma(p, t, splat<f2>(0.23711844f));
+        p = fma(p, t, splat<f2>(-0.04467765f));
+        p = fma(p, t, splat<f2>(0.16266398f));
+        p = fma(p, t, splat<f2>(0.10760187f));
+        p = fma(p, t, splat<f2>(0.12137473f));
+        p = fma(p, t, splat<f2>(-7.3115713e-5f));
+        split(mul(e, p), pa, pb);                       // the tail
+        const f2 c = pair(a < 0.f ? pa : 1.f - pa, b < 0.f ? pb : 1.f - pb);
+        if (kSlope) slope = fma(mul(g, splat<f2>(0.39894228f)), e, c);
+        return mul(g, c);
     }
-    const float s = fast_logistic(g);
-    if (kSlope) slope = s * fmaf(g, 1.f - s, 1.f);
-    return g * s;
+    const f2 s = fast_logistic(g);
+    if (kSlope) slope = mul(s, fma(g, sub(splat<f2>(1.f), s), splat<f2>(1.f)));
+    return mul(g, s);
 }
 
 // -------------------------------------------------------------------------- products
@@ -102,21 +107,21 @@ constexpr int kStages = 6;
 constexpr int kRowGroup = 8;            // row tiles that share their way through the columns
 
 struct Problem {                        // one product
-    int M, N, K;                        // kGated: N = F
+    int M, N, K;                        // kGated, kGatedBack: N = F
     int tiles_m, tiles;
-    const bf16* add;                    // kStore: residual or NULL
+    bf16 *out, *h;                      // kStore: result; kGated: gu (or NULL) and h; kGatedBack: dgu and h
+    const bf16* add;                    // kStore: residual or NULL; kGatedBack: gu
     long long add_row;
 };
 struct Maps {
-    CUtensorMap a, b, out, aux;         // kGated: out is gu, aux h; kGatedBack: out is dgu, aux h
+    CUtensorMap a, b;
 };
 struct GemmParams {
     Problem q[2];
     int tile0, tiles;                   // this launch's tiles: from .. to
     int splits;                         // SPLIT: pairs of a cluster that share a tile's K
     int beside;                         // the second of two launches of one product, which runs beside the first
-    int gelu, save;                     // save: kGated writes g and u
-    const bf16* gu;                     // kGatedBack: [M][2N]
+    int gelu;
     int* status;
     long long limit;
     int debug_stall;                    // stage (modulo their number) + 1 that never fills; 0: none
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned char* mine = epi + (warp - 2) * 2 * kPiece;
     int turn = 0;
     bool ok = true;
-    uint4 next[kIn] = {};                               // of the next piece, this lane's row: the residual, or g and u
+    uint4 next[kIn] = {};                               // of the next piece: the residual, or g and u, four lanes to a row
     auto row_of = [&](const TileAt& at) { return at.row + rank * kBM + part * 32; };
     auto pieces_of = [&](const TileAt& at) {            // that hold a result
         const Problem& q = p.q[at.which];
@@ -301,90 +306,97 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto read = [&](const TileAt& at, int c, int pieces) {
         const Problem& q = p.q[at.which];
-        const int row = row_of(at) + lane, x = at.col + 32 * c;
-        const bool in = c < pieces && row < q.M;
-        if constexpr (MODE == kGatedBack) {
-            const bf16* from = p.gu + (long long)row * 2 * q.N + x;
+        if (MODE == kGated || !q.add || c >= pieces) return;
+        // places outside read the nearest ones inside: a load under a condition would be waited for at once
+        const int row0 = row_of(at) + (lane >> 2), x = min(at.col + 32 * c + 8 * (lane & 3), q.N - 8);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (in && x + 8 * j < q.N) {
-                    next[j] = *reinterpret_cast<const uint4*>(from + 8 * j);
-                    next[4 + j] = *reinterpret_cast<const uint4*>(from + q.N + 8 * j);
-                }
-        } else if (MODE == kStore && q.add) {
-            const bf16* from = q.add + row * q.add_row + x;
-#pragma unroll
-            for (int j = 0; j < kIn; ++j)
-                if (in && x + 8 * j < q.N) next[j] = *reinterpret_cast<const uint4*>(from + 8 * j);
+        for (int i = 0; i < kIn / (MODE == kGatedBack ? 2 : 1); ++i) {
+            const bf16* from = q.add + min(row0 + 8 * i, q.M - 1) * q.add_row + x;
+            next[i] = *reinterpret_cast<const uint4*>(from);
+            if constexpr (MODE == kGatedBack) next[4 + i] = *reinterpret_cast<const uint4*>(from + q.N);
         }
     };
-    // 32 columns of results of this warp's 32 rows: to (x, y, z) of a map, by way of one place or the other.
-    auto emit = [&](const uint4 (&r)[4], const CUtensorMap* m, int x, int y, int z) {
-        unsigned char* place = mine + (turn & 1) * kPiece;
-        ++turn;
-        if (lane == 0) bulk_wait_read<1>();             // what lay there has left
+    // What was read, a row a lane.
+    auto turned = [&](uint4 (&now)[kIn]) {
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *piece_at(place, lane, j) = r[j];
-        fence_proxy_async_smem();
+        for (int i = 0; i < kIn; ++i) *piece_at(mine + i / 4 * kPiece, 8 * (i & 3) + (lane >> 2), lane & 3) = next[i];
         __syncwarp();
-        if (lane == 0) {
-            tma_store_3d(m, place, x, y, z);
-            bulk_commit();
+#pragma unroll
+        for (int i = 0; i < kIn; ++i) now[i] = *piece_at(mine + i / 4 * kPiece, lane, i & 3);
+    };
+    // 32 columns of results of this warp's 32 rows, to `to` (rows `pitch` apart) where they are of the matrix, by way of one
+    // place or the other: lanes with a row each write them, four lanes to a row take them out.
+    auto emit = [&](const uint4 (&r)[4], bf16* to, long long pitch, int rows, int columns) {
+        unsigned char* place = mine + (turn & 1) * kPiece;
+        ++turn;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *piece_at(place, lane, j) = r[j];
+        __syncwarp();
+        const int j = lane & 3;
+        bf16* at = to + (lane >> 2) * pitch + 8 * j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + (lane >> 2);
+            if (row < rows && 8 * j < columns) *reinterpret_cast<uint4*>(at + 8 * i * pitch) = *piece_at(place, row, j);
         }
     };
     // Piece c with its sums (kGated: of g in v, of u in up); `after`: the next piece of this warp.
     auto piece = [&](const TileAt& at, int c, int after, int pieces, float (&v)[32], float (&up)[MODE == kGated ? 32 : 1]) {
-        const Maps& m = at.which ? m1 : m0;
-        const int x = at.col + 32 * c, row0 = row_of(at);
+        const Problem& q = p.q[at.which];
+        const int x = at.col + 32 * c, row0 = row_of(at), rows = q.M - row0, columns = q.N - x;
         uint4 now[kIn], r0[4], r1[4], r2[4];
-#pragma unroll
-        for (int j = 0; j < kIn; ++j) now[j] = next[j];
+        if (MODE != kGated && q.add) turned(now);
         read(at, after, pieces);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float (&f)[8] = *reinterpret_cast<float(*)[8]>(v + 8 * j);
+            f2 f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = pair(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
             if constexpr (MODE == kStore) {
-                if (p.q[at.which].add) {
-                    float r[8];
-                    unpack8(now[j], r);
+                if (q.add) {
+                    f2 r[4];
+                    unpack(now[j], r);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] += r[i];
+                    for (int i = 0; i < 4; ++i) f[i] = add(f[i], r[i]);
                 }
-                r0[j] = pack8(f);
+                r0[j] = pack(f);
             } else if constexpr (MODE == kGated) {
-                float (&u)[8] = *reinterpret_cast<float(*)[8]>(up + 8 * j);
-                r0[j] = pack8(f);
-                r1[j] = pack8(u);
-                float unused;
+                f2 u[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = act<false>(f[i], p.gelu, unused) * u[i];
-                r2[j] = pack8(f);
+                for (int i = 0; i < 4; ++i) u[i] = pair(up[8 * j + 2 * i], up[8 * j + 2 * i + 1]);
+                r0[j] = pack(f);
+                r1[j] = pack(u);
+                f2 unused;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = mul(act<false>(f[i], p.gelu, unused), u[i]);
+                r2[j] = pack(f);
             } else {
-                float g[8], u[8], h[8];
-                unpack8(now[j], g);
-                unpack8(now[4 + j], u);
+                f2 g[4], u[4], h[4];
+                unpack(now[j], g);
+                unpack(now[4 + j], u);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float slope;
-                    const float a = act<true>(g[i], p.gelu, slope);
-                    h[i] = a * u[i];
-                    g[i] = f[i] * u[i] * slope;
-                    u[i] = f[i] * a;
+                for (int i = 0; i < 4; ++i) {
+                    f2 slope;
+                    const f2 a = act<true>(g[i], p.gelu, slope);
+                    h[i] = mul(a, u[i]);
+                    g[i] = mul(mul(f[i], u[i]), slope);
+                    u[i] = mul(f[i], a);
                 }
-                r0[j] = pack8(g);
-                r1[j] = pack8(u);
-                r2[j] = pack8(h);
+                r0[j] = pack(g);
+                r1[j] = pack(u);
+                r2[j] = pack(h);
             }
         }
         if constexpr (MODE == kStore) {
-            emit(r0, &m.out, x, row0, 0);
+            emit(r0, q.out + (long long)row0 * q.N + x, q.N, rows, columns);
         } else {
-            if (MODE == kGatedBack || p.save) {
-                emit(r0, &m.out, x, 0, row0);
-                emit(r1, &m.out, x, 1, row0);
+            if (MODE == kGatedBack || q.out) {
+                bf16* to = q.out + (long long)row0 * 2 * q.N + x;
+                emit(r0, to, 2 * q.N, rows, columns);
+                emit(r1, to + q.N, 2 * q.N, rows, columns);
             }
-            emit(r2, &m.aux, x, row0, 0);
+            emit(r2, q.h + (long long)row0 * q.N + x, q.N, rows, columns);
         }
     };
     if constexpr (!SPLIT) {
@@ -398,16 +410,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t sums = tmem_addr(tmem, part * 32, acc * kTile);
+                auto give_back = [&] {                  // this warp has read its sums
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed_at(peer_addr(&S.acc_empty[acc], 0));
+                };
+                if (team >= pieces) give_back();
                 for (int c = team; c < pieces; c += 2) {
                     float v[32], up[MODE == kGated ? 32 : 1];
                     load_sums(sums + 32 * c, v);
                     if constexpr (MODE == kGated) load_sums(sums + kTile / 2 + 32 * c, up);
                     tmem_wait_ld();
+                    if (c + 2 >= pieces) give_back();
                     piece(at, c, c + 2, pieces, v, up);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_at(peer_addr(&S.acc_empty[acc], 0));
             }
         }
     } else {
@@ -448,7 +464,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    if (warp >= 2 && lane == 0) bulk_wait_read<0>();
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -605,7 +620,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
         for (int i = rank * share + (int)threadIdx.x; i < last; i += kNarrowThreads) {
             const int t = i / kGroups, g4 = i % kGroups * 4, col = first + g4;
             if (col >= p.wide) continue;
-            float v[4] = {}, u[4] = {};
+            f2 v[2] = {splat<f2>(0.f), splat<f2>(0.f)}, u[2] = {v[0], v[0]};
             for (int q0 = 0; q0 < ranks; q0 += 4) {                  // four blocks' sums on their way together
                 float4 a[4], b[4];
 #pragma unroll
@@ -618,46 +633,50 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    v[0] += a[q].x; v[1] += a[q].y; v[2] += a[q].z; v[3] += a[q].w;
-                    if constexpr (MODE == kGated) { u[0] += b[q].x; u[1] += b[q].y; u[2] += b[q].z; u[3] += b[q].w; }
+                    v[0] = add(v[0], pair(a[q].x, a[q].y));
+                    v[1] = add(v[1], pair(a[q].z, a[q].w));
+                    if constexpr (MODE == kGated) {
+                        u[0] = add(u[0], pair(b[q].x, b[q].y));
+                        u[1] = add(u[1], pair(b[q].z, b[q].w));
+                    }
                 }
             }
             if constexpr (MODE == kStore) {
                 if (p.add) {
-                    float r[4];
-                    unpack4(*reinterpret_cast<const uint2*>(p.add + t * p.add_row + col), r);
+                    f2 r[2];
+                    unpack(*reinterpret_cast<const uint2*>(p.add + t * p.add_row + col), r);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] += r[j];
+                    for (int j = 0; j < 2; ++j) v[j] = add(v[j], r[j]);
                 }
-                *reinterpret_cast<uint2*>(p.out + (long long)t * p.wide + col) = pack4(v);
+                *reinterpret_cast<uint2*>(p.out + (long long)t * p.wide + col) = pack(v);
             } else {
                 bf16* gu = p.gu + (long long)t * 2 * p.F + col;
                 uint2* h = reinterpret_cast<uint2*>(p.h + (long long)t * p.F + col);
                 if constexpr (MODE == kGated) {
                     if (p.gu) {
-                        *reinterpret_cast<uint2*>(gu) = pack4(v);
-                        *reinterpret_cast<uint2*>(gu + p.F) = pack4(u);
+                        *reinterpret_cast<uint2*>(gu) = pack(v);
+                        *reinterpret_cast<uint2*>(gu + p.F) = pack(u);
                     }
-                    float unused;
+                    f2 unused;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = act<false>(v[j], p.gelu, unused) * u[j];
-                    *h = pack4(v);
+                    for (int j = 0; j < 2; ++j) v[j] = mul(act<false>(v[j], p.gelu, unused), u[j]);
+                    *h = pack(v);
                 } else {
-                    float g[4], hh[4];
-                    unpack4(*reinterpret_cast<const uint2*>(gu), g);
-                    unpack4(*reinterpret_cast<const uint2*>(gu + p.F), u);
+                    f2 g[2], hh[2];
+                    unpack(*reinterpret_cast<const uint2*>(gu), g);
+                    unpack(*reinterpret_cast<const uint2*>(gu + p.F), u);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float slope;
-                        const float a = act<true>(g[j], p.gelu, slope);
-                        hh[j] = a * u[j];
-                        g[j] = v[j] * u[j] * slope;
-                        u[j] = v[j] * a;
+                    for (int j = 0; j < 2; ++j) {
+                        f2 slope;
+                        const f2 a = act<true>(g[j], p.gelu, slope);
+                        hh[j] = mul(a, u[j]);
+                        g[j] = mul(mul(v[j], u[j]), slope);
+                        u[j] = mul(v[j], a);
                     }
                     bf16* dgu = p.out + (long long)t * 2 * p.F + col;
-                    *reinterpret_cast<uint2*>(dgu) = pack4(g);
-                    *reinterpret_cast<uint2*>(dgu + p.F) = pack4(u);
-                    *h = pack4(hh);
+                    *reinterpret_cast<uint2*>(dgu) = pack(g);
+                    *reinterpret_cast<uint2*>(dgu + p.F) = pack(u);
+                    *h = pack(hh);
                 }
             }
         }
@@ -673,24 +692,22 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
 struct Matrix {
     const void* p;
     long long rows, cols, pitch;
-    // box: values across by rows down.
-    bool map(CUtensorMap* m, int across, int down, TmaSwizzle sw) const {
+    // Copies of 64 values by `down` rows.
+    bool map(CUtensorMap* m, int down) const {
         const unsigned long long dims[3] = {(unsigned long long)cols, (unsigned long long)rows, 1};
         const unsigned long long row = (unsigned long long)pitch * 2, strides[2] = {row, row * (unsigned long long)rows};
-        const unsigned box[3] = {(unsigned)across, (unsigned)down, 1};
-        return make_tma_map(m, TmaType::bf16, p, dims, strides, box, sw);
+        const unsigned box[3] = {64, (unsigned)down, 1};
+        return make_tma_map(m, TmaType::bf16, p, dims, strides, box, true);
     }
-    // [rows][2][F] of rows of 2F.
-    bool halves(CUtensorMap* m, int across, int down, TmaSwizzle sw) const {
+    // Rows of 2F as [rows][2][F].
+    bool halves(CUtensorMap* m, int down) const {
         const unsigned long long dims[3] = {(unsigned long long)cols / 2, 2, (unsigned long long)rows};
         const unsigned long long strides[2] = {(unsigned long long)cols, (unsigned long long)cols * 2};
-        const unsigned box[3] = {(unsigned)across, 1, (unsigned)down};
-        return make_tma_map(m, TmaType::bf16, p, dims, strides, box, sw);
+        const unsigned box[3] = {64, 1, (unsigned)down};
+        return make_tma_map(m, TmaType::bf16, p, dims, strides, box, true);
     }
     // As an operand: rows of K, or (mn) K as rows.
-    bool operand(CUtensorMap* m, bool mn) const { return map(m, 64, mn ? 64 : kBM, TmaSwizzle::b128); }
-    bool piece(CUtensorMap* m) const { return map(m, 32, 32, TmaSwizzle::b64); }
-    bool half_piece(CUtensorMap* m) const { return halves(m, 32, 32, TmaSwizzle::b64); }
+    bool operand(CUtensorMap* m, bool mn) const { return map(m, mn ? 64 : kBM); }
 };
 
 bool problem(Problem& q, int M, int N, int K, int mode) {
@@ -805,7 +822,7 @@ cudaError_t narrow(const CUtensorMap& mw, const Matrix& x, NarrowParams p, bool 
     const int stage = kOperand + p.bn * 128, room = kNarrowSmem - 1024;
     p.stages = room / stage < kNarrowStages ? room / stage : kNarrowStages;
     CUtensorMap mx;
-    if (!x.map(&mx, 64, p.bn, TmaSwizzle::b128)) return cudaErrorInvalidValue;
+    if (!x.map(&mx, p.bn)) return cudaErrorInvalidValue;
     auto kernel = ffn_narrow_kernel<WMN, MODE>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
     if (e != cudaSuccess) return e;
@@ -838,8 +855,7 @@ size_t ffn_workspace_bytes(int N, int D, int F, int backward) {
 
 cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     const long long N = a.N, D = a.D, F = a.F;
-    const Matrix x{a.x, N, D, a.x_row}, wi{a.W_in, D, 2 * F, 2 * F}, wo{a.W_out, F, D, D}, h{a.workspace, N, F, F},
-        y{a.y, N, D, D}, gu{a.gu, N, 2 * F, 2 * F};
+    const Matrix x{a.x, N, D, a.x_row}, wi{a.W_in, D, 2 * F, 2 * F}, wo{a.W_out, F, D, D}, h{a.workspace, N, F, F};
     *launches = 0;
     if (a.N <= kNarrow) {
         *launches = 2;
@@ -850,7 +866,7 @@ cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         p.h = static_cast<bf16*>(a.workspace);
         p.gu = static_cast<bf16*>(a.gu);
         p.debug_stall = a.debug_stall;
-        if (!wi.halves(&w, 64, 64, TmaSwizzle::b128)) return cudaErrorInvalidValue;
+        if (!wi.halves(&w, 64)) return cudaErrorInvalidValue;
         const cudaError_t e = narrow<true, kGated>(w, x, p, false, s);
         if (e != cudaSuccess) return e;
         NarrowParams o = narrow_params(a);
@@ -863,18 +879,19 @@ cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         return narrow<true, kStore>(w, h, o, true, s);
     }
     GemmParams p = params(a);
-    p.save = a.gu != nullptr;
     p.debug_stall = a.debug_stall;
+    p.q[0].out = static_cast<bf16*>(a.gu);
+    p.q[0].h = static_cast<bf16*>(a.workspace);
     Maps m{};
-    if (!x.operand(&m.a, false) || !wi.halves(&m.b, 64, 64, TmaSwizzle::b128) || !h.piece(&m.aux) ||
-        (a.gu && !gu.half_piece(&m.out)) || !problem(p.q[0], a.N, a.F, a.D, kGated))
+    if (!x.operand(&m.a, false) || !wi.halves(&m.b, 64) || !problem(p.q[0], a.N, a.F, a.D, kGated))
         return cudaErrorInvalidValue;
     const cudaError_t e = gemm<false, true, kGated>(m, m, p, s, launches);
     if (e != cudaSuccess) return e;
     GemmParams o = params(a);
     Maps n{};
-    if (!h.operand(&n.a, false) || !wo.operand(&n.b, true) || !y.piece(&n.out) || !problem(o.q[0], a.N, a.D, a.F, kStore))
+    if (!h.operand(&n.a, false) || !wo.operand(&n.b, true) || !problem(o.q[0], a.N, a.D, a.F, kStore))
         return cudaErrorInvalidValue;
+    o.q[0].out = static_cast<bf16*>(a.y);
     o.q[0].add = static_cast<const bf16*>(a.residual);
     o.q[0].add_row = a.residual_row;
     return gemm<false, true, kStore>(n, n, o, s, launches);
@@ -884,8 +901,7 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     const long long N = a.N, D = a.D, F = a.F;
     char* ws = static_cast<char*>(a.workspace);
     const Matrix x{a.x, N, D, a.x_row}, wi{a.W_in, D, 2 * F, 2 * F}, wo{a.W_out, F, D, D}, dy{a.dy, N, D, a.dy_row},
-        dgu{ws, N, 2 * F, 2 * F}, h{ws + (size_t)N * F * 4, N, F, F}, dx{a.dx, N, D, D},
-        dwi{a.dW_in, D, 2 * F, 2 * F}, dwo{a.dW_out, F, D, D};
+        dgu{ws, N, 2 * F, 2 * F}, h{ws + (size_t)N * F * 4, N, F, F};
     *launches = 0;
     cudaError_t e;
     if (a.N <= kNarrow) {
@@ -903,9 +919,12 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     } else {
         GemmParams p = params(a);
         p.debug_stall = a.debug_stall;
-        p.gu = static_cast<const bf16*>(a.gu);
+        p.q[0].add = static_cast<const bf16*>(a.gu);
+        p.q[0].add_row = 2LL * a.F;
+        p.q[0].out = static_cast<bf16*>(const_cast<void*>(dgu.p));
+        p.q[0].h = static_cast<bf16*>(const_cast<void*>(h.p));
         Maps m{};
-        if (!dy.operand(&m.a, false) || !wo.operand(&m.b, false) || !dgu.half_piece(&m.out) || !h.piece(&m.aux) ||
+        if (!dy.operand(&m.a, false) || !wo.operand(&m.b, false) ||
             !problem(p.q[0], a.N, a.F, a.D, kGatedBack))
             return cudaErrorInvalidValue;
         e = gemm<false, false, kGatedBack>(m, m, p, s, launches);
@@ -924,9 +943,9 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     } else if (a.dx) {
         GemmParams o = params(a);
         Maps n{};
-        if (!dgu.operand(&n.a, false) || !wi.operand(&n.b, false) || !dx.piece(&n.out) ||
-            !problem(o.q[0], a.N, a.D, 2 * a.F, kStore))
+        if (!dgu.operand(&n.a, false) || !wi.operand(&n.b, false) || !problem(o.q[0], a.N, a.D, 2 * a.F, kStore))
             return cudaErrorInvalidValue;
+        o.q[0].out = static_cast<bf16*>(a.dx);
         e = gemm<false, false, kStore>(n, n, o, s, launches);
         if (e != cudaSuccess) return e;
     }
@@ -936,14 +955,15 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     Maps n[2] = {};
     int k = 0;
     if (a.dW_in) {
-        if (!x.operand(&n[k].a, true) || !dgu.operand(&n[k].b, true) || !dwi.piece(&n[k].out) ||
-            !problem(o.q[k], a.D, 2 * a.F, a.N, kStore))
+        if (!x.operand(&n[k].a, true) || !dgu.operand(&n[k].b, true) || !problem(o.q[k], a.D, 2 * a.F, a.N, kStore))
             return cudaErrorInvalidValue;
-        ++k;
+        o.q[k++].out = static_cast<bf16*>(a.dW_in);
     }
-    if (a.dW_out && (!h.operand(&n[k].a, true) || !dy.operand(&n[k].b, true) || !dwo.piece(&n[k].out) ||
-                     !problem(o.q[k], a.F, a.D, a.N, kStore)))
-        return cudaErrorInvalidValue;
+    if (a.dW_out) {
+        if (!h.operand(&n[k].a, true) || !dy.operand(&n[k].b, true) || !problem(o.q[k], a.F, a.D, a.N, kStore))
+            return cudaErrorInvalidValue;
+        o.q[k].out = static_cast<bf16*>(a.dW_out);
+    }
     return gemm<true, true, kStore>(n[0], n[1], o, s, launches);
 }
 

@@ -61,6 +61,8 @@ __device__ __forceinline__ uint32_t bf16_of_pair(f2 a) {
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+__device__ __forceinline__ f2 sub(f2 a, f2 b) { return fma(b, splat<f2>(-1.f), a); }
+
 // 1 / (1 + exp(-x)) by the base-2 and reciprocal units: (4 + 0.7 |x|) 2^-23 of itself off at most, 0 where it is
 // below the smallest normal number.
 __device__ __forceinline__ float fast_logistic(float x) {
@@ -68,6 +70,12 @@ __device__ __forceinline__ float fast_logistic(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
     return r;
+}
+
+__device__ __forceinline__ f2 fast_logistic(f2 x) {
+    float a, b;
+    split(x, a, b);
+    return pair(fast_logistic(a), fast_logistic(b));
 }
 
 }  // namespace ttm

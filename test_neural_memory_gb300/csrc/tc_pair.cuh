@@ -93,6 +93,10 @@ __device__ __forceinline__ void after_previous() {
 __device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+// The same without the wait for this thread's own stores: for hand-offs that pass no memory on.
+__device__ __forceinline__ void mbar_arrive_relaxed_at(uint32_t addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
 // Tensor copy into this block's shared memory, counted on a barrier of either block.
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* tmap, uint32_t bar, int x, int y, int z) {
     asm volatile(

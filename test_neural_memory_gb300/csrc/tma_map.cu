@@ -10,7 +10,7 @@
 namespace ttm {
 
 bool make_tma_map(void* map, TmaType type, const void* ptr, const unsigned long long (&dims)[3],
-                  const unsigned long long (&strides)[2], const unsigned (&box)[3], TmaSwizzle swizzle) {
+                  const unsigned long long (&strides)[2], const unsigned (&box)[3], bool swizzle128) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -28,9 +28,7 @@ bool make_tma_map(void* map, TmaType type, const void* ptr, const unsigned long 
     const cuuint32_t b[3] = {box[0], box[1], box[2]}, e[3] = {1, 1, 1};
     return encode(static_cast<CUtensorMap*>(map), t, 3, const_cast<void*>(ptr), d, s, b, e,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle == TmaSwizzle::b128   ? CU_TENSOR_MAP_SWIZZLE_128B
-                  : swizzle == TmaSwizzle::b64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                               : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

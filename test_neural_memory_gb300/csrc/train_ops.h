@@ -164,13 +164,8 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches);
 // 256 values a side whose inner extent is a multiple of 16 bytes.  Values outside the view load as zero.
 // tma_map.cu; false when the driver refuses it.
 enum class TmaType { f32, bf16, f16 };
-enum class TmaSwizzle { none, b64, b128 };
 bool make_tma_map(void* map, TmaType type, const void* ptr, const unsigned long long (&dims)[3],
-                  const unsigned long long (&strides)[2], const unsigned (&box)[3], TmaSwizzle swizzle);
-inline bool make_tma_map(void* map, TmaType type, const void* ptr, const unsigned long long (&dims)[3],
-                         const unsigned long long (&strides)[2], const unsigned (&box)[3], bool swizzle128) {
-    return make_tma_map(map, type, ptr, dims, strides, box, swizzle128 ? TmaSwizzle::b128 : TmaSwizzle::none);
-}
+                  const unsigned long long (&strides)[2], const unsigned (&box)[3], bool swizzle128);
 
 // Process-wide state of the API layer (ttm_api.cu).
 int* api_status_ptr();              // device status word of the current device; NULL on failure
