@@ -26,11 +26,17 @@ bool make_tma_map(void* map, TmaType type, const void* ptr, const unsigned long 
                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, s[2] = {strides[0], strides[1]};
     const cuuint32_t b[3] = {box[0], box[1], box[2]}, e[3] = {1, 1, 1};
-    return encode(static_cast<CUtensorMap*>(map), t, 3, const_cast<void*>(ptr), d, s, b, e,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto ok = [&] {
+        return encode(static_cast<CUtensorMap*>(map), t, 3, const_cast<void*>(ptr), d, s, b, e,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (ok()) return true;
+    // a host thread's first call: the driver wants the context current, which the runtime makes it here
+    int device;
+    return cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess && ok();
 }
 
 }  // namespace ttm
