@@ -577,7 +577,7 @@ int ttm_orthogonalize(int batch, int m, int n, int dtype, const void* G,
  *     least C where there is more than one).  w: [C][K] fp32, w[c][K-1] the current token's.  b: [C] fp32 or
  *     NULL (0).  silu: 0 or 1.
  *   state0: [N][K-1][C] in dtype, the K - 1 inputs before the first token, or NULL (zero).
- *   doc: [N][T] int32, doc_seq apart, or NULL: a tap whose row has another number than the token is left
+ *   doc: [N][T] int32, doc_seq >= 0 apart (0: one row for every sequence), or NULL: a tap whose row has another number than the token is left
  *     out.  The rows of state0 have the number of the first token.
  *   y: [N][T][C] in dtype, contiguous.  state: [N][K-1][C] in dtype or NULL: the last K - 1 inputs
  *     (state0's rows among them where T < K - 1), zero where they are of another document than the last
@@ -674,7 +674,7 @@ int ttm_gated_ffn_bwd(int N, int D, int F, int act, const void* dy, long long dy
  *     and a counter that is 0 between calls.  A captured call so counts its own replays.
  *   lr_at, grad_scale: fp32 on the device, or NULL (lr; 1).
  * Arithmetic is fp32; a bf16 param or copy is rounded to nearest.  Equal inputs give equal bits.
- * bits 8 or 32; 0 <= beta < 1, eps > 0.  No two written tensors, and no written and read one, may overlap
+ * bits 8 or 32; 0 <= beta < 1, eps > 0, n <= 2^40 (else TTM_ERR_UNSUPPORTED).  No two written tensors, and no written and read one, may overlap
  * (TTM_ERR_INVALID_ARG; one gradient may serve several tensors).  Calls that share m, v or step run one after the
  * other on one stream.  Asynchronous on `stream`; TTM_ERR_CUDA if a launch fails.
  */

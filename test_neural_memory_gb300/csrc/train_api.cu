@@ -106,9 +106,12 @@ int conv_common(ttm::ConvArgs& a, int N, int T, int C, int K, int dtype, int sil
 }
 
 bool doc_ok(const ttm::ConvArgs& a, const int* doc, long long doc_seq, Span& sd) {
-    bool ok = aligned(doc, 4);
-    sd = {doc, doc ? view_bytes(a.N, a.T, 1, doc_seq, 1, 4, ok) : 0};
-    return ok;
+    // (only read: rows may overlap, as where one row serves every sequence)
+    sd = {doc, 0};
+    if (!doc) return true;
+    if (!aligned(doc, 4) || (a.N > 1 && (doc_seq < 0 || double(a.N - 1) * double(doc_seq) > 1e18))) return false;
+    sd.bytes = ((size_t)(a.N - 1) * (a.N > 1 ? doc_seq : 0) + a.T) * 4;
+    return true;
 }
 
 // Widths whose products count in 32 bits.
@@ -535,10 +538,10 @@ int ttm_adamw_step(int count, const ttm_adamw_tensor* tensors, int bits, void* m
         long long blocks = 0;
         for (int i = 0; i < count; ++i) {
             const ttm_adamw_tensor& t = tensors[i];
-            if (t.n < 0 || t.n > (1LL << 48) || !dtype_ok(t.param_dtype)) return TTM_ERR_INVALID_ARG;
+            if (t.n < 0 || !dtype_ok(t.param_dtype)) return TTM_ERR_INVALID_ARG;
+            if (t.n > (1LL << 40)) return TTM_ERR_UNSUPPORTED;
             const long long first = blocks;
             blocks += (t.n + 255) / 256;
-            if (blocks > (1LL << 48)) return TTM_ERR_INVALID_ARG;
             if (!t.grad || t.n == 0) continue;
             const int pb = t.param_dtype == TTM_BF16, gb = t.grad_dtype == TTM_BF16;
             if (!t.param || !dtype_ok(t.grad_dtype) || !aligned(t.param, pb ? 2 : 4) || !aligned(t.grad, gb ? 2 : 4) ||

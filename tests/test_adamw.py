@@ -251,6 +251,23 @@ def test_other_streams_and_long_runs():
     near(twin, *p)
 
 
+def test_offsets_past_32_bits():
+    """A tensor of 2.2e9 values beside a short one: its last values as a tensor of their own gives them."""
+    n = 2 ** 31 + 70001
+    p, g = torch.ones(n, device="cuda", dtype=torch.bfloat16), torch.full((n,), 0.5, device="cuda", dtype=torch.bfloat16)
+    g[-1000:] = torch.linspace(-1, 1, 1000, device="cuda").to(torch.bfloat16)
+    short, gs = torch.ones(300, device="cuda"), torch.ones(300, device="cuda")
+    state = ttm.adamw_state([p, short])
+    end, ge = torch.ones(1000, device="cuda", dtype=torch.bfloat16), g[-1000:].clone()
+    other = ttm.adamw_state([end])
+    for _ in range(2):
+        ttm.adamw_step([p, short], [g, gs], state, **HYPER)
+        ttm.adamw_step([end], [ge], other, **HYPER)
+    assert torch.equal(p[-1000:], end) and torch.equal(state["m"][n - 1000:n], other["m"][:1000])
+    assert torch.equal(state["v"][n - 1000:n], other["v"][:1000]) and not state["m"][n:(n + 255) // 256 * 256].any()
+    assert bool((short < 1).all()) and bool((state["m"][-512:-212] > 0).all())
+
+
 def test_refusals():
     p, g = [torch.zeros(300, device="cuda")], [torch.ones(300, device="cuda")]
     state = ttm.adamw_state(p)

@@ -84,6 +84,7 @@ def test_adamw_rejects_malformed(L):
     assert call(lr=float("inf")) == INVALID and call(wd=float("nan")) == INVALID
     assert call(bits=8) == INVALID and call(ms=P(20), vs=P(21)) == INVALID and call(bits=8, ms=P(20)) == INVALID
     assert call(m=P(10, 8)) == INVALID and call(step=P(12, 2)) == INVALID and call(gs=P(13, 1)) == INVALID
+    assert one(n=1 << 41) == UNSUPPORTED and one(n=1 << 62) == UNSUPPORTED
     assert one(p=None) == INVALID and one(n=-1) == INVALID and one(pd=3) == INVALID and one(gd=2) == INVALID
     assert one(p=P(0, 2)) == INVALID and one(g=P(1, 1)) == INVALID and one(c=P(2, 1)) == INVALID
     assert one(g=P(0)) == INVALID and one(c=P(0)) == INVALID and one(p=P(10)) == INVALID and one(g=P(11, 64)) == INVALID

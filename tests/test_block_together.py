@@ -170,3 +170,35 @@ def test_one_block_after_the_other_without_a_pause():
         torch.cuda.synchronize()
         return [t.view(torch.uint8) for t in outs]
     assert all(torch.equal(a, b) for a, b in zip(chain(False), chain(True)))
+
+
+def test_a_captured_step_of_many_rows():
+    """A pass, its gradient and the optimiser's step in one graph, at a size whose tiles take a launch for the whole rounds and one
+    beside it: replays give the bits of calls one by one, weights changing from replay to replay."""
+    N, D, F = 9001, 264, 2008
+
+    def made():
+        r = torch.Generator(device="cuda").manual_seed(5)
+        rand = lambda *s: torch.randn(s, generator=r, device="cuda")  # noqa: E731
+        x, dy = rand(N, D).to(BF), rand(N, D).to(BF)
+        master = [rand(D, 2 * F) / D ** 0.5, rand(F, D) / F ** 0.5]
+        return x, dy, master, [m.to(BF) for m in master], ttm.adamw_state(master)
+
+    def step(x, dy, master, w, state):
+        y, gu = ttm.gated_ffn_fwd(x, *w, residual=dy)
+        g = ttm.gated_ffn_bwd(dy, x, gu, *w)
+        ttm.adamw_step(master, [g["dW_in"], g["dW_out"]], state, lr=1e-2, copies=w)
+        return y, g["dx"]
+    one = made()
+    for _ in range(4):
+        want = step(*one)
+    two = made()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        got = step(*two)
+    for _ in range(4):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert all(torch.equal(a, b) for a, b in zip(one[2] + one[3], two[2] + two[3]))

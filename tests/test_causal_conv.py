@@ -196,6 +196,40 @@ def test_documents_are_independent():
     assert torch.equal(state, sp) and torch.isfinite(state).all()
 
 
+def test_one_row_of_documents_for_every_sequence():
+    x, dy, w, b, _, _, doc = (on(t) for t in make(3, 50, 24, 4, "bf16", docs=True))
+    row = doc[:1].expand(3, 50)
+    y, st = ttm.causal_conv_fwd(x, w, b, doc=row)
+    want, wst = ttm.causal_conv_fwd(x, w, b, doc=row.contiguous())
+    assert torch.equal(y, want) and torch.equal(st, wst)
+    g, r = (ttm.causal_conv_bwd(dy, x, w, b, doc=d) for d in (row, row.contiguous()))
+    assert torch.equal(g["dx"], r["dx"]) and torch.equal(g["dw"], r["dw"])
+
+
+def test_offsets_past_32_bits():
+    """2.3e9 values: the last tokens of a long row as short calls give them; as many sequences are refused (N C of 2^31
+    and more)."""
+    T, C = 140001, 16384
+    r = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((1, T, C), generator=r, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn((C, 4), generator=r, device="cuda")
+    y, st = ttm.causal_conv_fwd(x, w)
+    tail = x[:, -500:].contiguous()
+    part, pst = ttm.causal_conv_fwd(tail[:, 3:], w, state0=tail[:, :3].contiguous())
+    assert torch.equal(y[:, -497:], part) and torch.equal(st, pst)
+    del y
+    out = dict(dx=torch.empty_like(x))
+    g = ttm.causal_conv_bwd(x, x, w, want_dw=False, out=out)
+    gp = ttm.causal_conv_bwd(tail[:, 3:], tail[:, 3:], w, state0=tail[:, :3].contiguous(), want_dw=False)
+    assert torch.equal(g["dx"][:, -497:], gp["dx"])
+    many = x.view(T, 1, C)
+    with pytest.raises(ttm.TTMError) as e:
+        ttm.causal_conv_fwd(many, w)
+    assert e.value.code == ttm.ERR_UNSUPPORTED
+    y, _ = ttm.causal_conv_fwd(many[-131071:], w)
+    assert torch.equal(y[-9:], ttm.causal_conv_fwd(many[-9:].contiguous(), w)[0])
+
+
 def test_gradient_against_differences():
     """Central differences in float64 (step 1e-5, error about 1e-9) of <dy, y> + <ds, state>."""
     x, dy, w, b, s0, ds, doc = make(2, 6, 3, 3, "f32", docs=True, seed=5)

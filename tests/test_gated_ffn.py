@@ -182,6 +182,19 @@ def test_gradient_against_differences():
         assert abs(got - want) < 2.0 ** -7 * float(d[n].double().norm() * 3), (n, got, want)
 
 
+def test_offsets_past_32_bits():
+    """gu of 2.2e9 values: the last rows as a call on them alone gives them (other tiles, so within the roundings)."""
+    N, D, F = 200003, 64, 5504
+    x, dy, res, W_in, W_out = make(N, D, F)
+    y, gu = ttm.gated_ffn_fwd(x, W_in, W_out, residual=res)
+    d = ttm.gated_ffn_bwd(dy, x, gu, W_in, W_out, want_dw=False)
+    tail = [t[-300:].contiguous() for t in (x, dy, res)]
+    y2, gu2 = ttm.gated_ffn_fwd(tail[0], W_in, W_out, residual=tail[2])
+    d2 = ttm.gated_ffn_bwd(tail[1], tail[0], gu[-300:].contiguous(), W_in, W_out, want_dw=False)
+    for a, b in ((y[-300:], y2), (gu[-300:], gu2), (d["dx"][-300:], d2["dx"])):
+        assert float((a.double() - b.double()).norm()) <= HALF * float(b.double().norm())
+
+
 @pytest.mark.parametrize("N", [9, 400])
 def test_streams_graphs_and_given_outputs(N):
     x, dy, res, W_in, W_out = make(N, 256, 512)
