@@ -25,7 +25,9 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kBatch = 4;               // rows whose loads are in flight together
 constexpr int kFwdThreads = 128;
-constexpr int kBwdThreads = 128, kBwdBlocks = 3;       // blocks an SM
+constexpr int kBwdThreads = 128;
+// Blocks of the gradient an SM, by registers (8 x 8192 x 2304 bf16 in pairs of values: 212 us with 4, 278 with 3).
+template <int V, int KW> constexpr int kBwdBlocks = V <= 2 && KW <= 4 ? 4 : 3;
 
 // V values of a row as they are stored, and as fp32: pairs of values (two results an instruction), or one.
 template <int BYTES> struct Word;
@@ -295,7 +297,7 @@ __global__ void conv_pass_kernel(const T* from, T* to, long long n) {
 // one part of the block's row of the grid, joined by conv_join_kernel in the rows' order: equal inputs give
 // equal bits.
 template <typename T, int V, int KW, bool kAll, bool DOC>
-__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) conv_bwd_kernel(const __grid_constant__ ConvArgs a, int groups,
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks<V, KW>) conv_bwd_kernel(const __grid_constant__ ConvArgs a, int groups,
                                                                 int strips, int strip) {
     constexpr int NV = kVals<V>;
     using E = Val<V>;
@@ -564,7 +566,7 @@ cudaError_t fwd(const ConvArgs& a, bool one_strip, cudaStream_t s) {
 // holds a part for each.
 int most_rows(int C) {
     const int across = ((C + 3) / 4 + 31) / 32;
-    const int rows = kSms * kBwdBlocks / across;
+    const int rows = kSms * 4 / across;
     return rows < 1 ? 1 : rows;
 }
 
@@ -575,7 +577,7 @@ cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
     while (bx < groups && bx < 32) bx *= 2;
     const int by = kBwdThreads / bx, across = (groups + bx - 1) / bx;
     // One strip a thread where the sequences are fewer than the threads of a column of the grid, of 16 tokens at least.
-    int rows = kSms * kBwdBlocks / across;
+    int rows = kSms * kBwdBlocks<V, KW> / across;
     if (rows > most_rows(a.C)) rows = most_rows(a.C);
     if (rows < 1) rows = 1;
     const long long places = (long long)rows * by, each = places / a.N;
