@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <climits>
 #include <cstdint>
 
 #include "../../include/ttm.h"
@@ -475,17 +476,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- products of few rows
 
-// Up to 128 rows: the weights are what is read, and the rows too few for a tile's first side.  So the product is
-// turned: 128 of the weights' columns are the 128 rows of the first operand, the rows of x the second operand's,
-// 16 to 128 of them.  A cluster of up to 8 blocks shares a tile's K, so that all SMs read weights however few the
-// tiles are; each leaves its sums in shared memory, and a share of the results is added up over the blocks
-// in their order, put through the epilogue and written by each.  The second kernel of a call starts on its weights
-// while the first one finishes.
-constexpr int kNarrowBlocks = 304;               // blocks of a launch at most: two an SM
-constexpr int kNarrow = 128, kNarrowThreads = 256, kNarrowStages = 6, kNarrowSmem = 110 * 1024;
+// Few rows: the weights are what is read, and the rows too few for a tile's first side.  So the product is turned: 128
+// of the weights' columns are the 128 rows of the first operand, the rows of x the second operand's, 16 to 128 of
+// them (more take another block).  A cluster of up to 8 blocks shares a tile's K, so that all SMs read weights however
+// few the tiles are; each leaves its sums in shared memory, and a share of the results is added up over the blocks in
+// their order, put through the epilogue and written by each.  The second kernel of a call starts on its weights while
+// the first one finishes.  16 x 2048 x 5504: 16.9 us a call, 67.6 MB of weights at 4.0 TB/s with both launches.
+constexpr int kNarrow = 128, kNarrowThreads = 256, kNarrowStages = 6, kNarrowSmem = 110 * 1024;     // two blocks an SM
 
 struct NarrowParams {
     int N, wide, K;                     // rows; columns of the result (kGated: F); K
+    int parts;                          // of the rows, bn each
     int F, kblocks;                     // kGated, kGatedBack: F; blocks of K of a block of the cluster
     int bn, stages;                     // rows, padded to 16
     int gelu, second;                   // second: of a call's kernels
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
-    const int tile = blockIdx.x / ranks;
+    const int tile = blockIdx.x / ranks / p.parts, row0 = blockIdx.x / ranks % p.parts * p.bn;
     const int first = MODE == kGated ? tile * 64 : tile * 128;       // column of the result (kGated: f)
     const int k0 = rank * p.kblocks, k1 = min((p.K + kBK - 1) / kBK, k0 + p.kblocks);
     const uint32_t stage = kOperand + p.bn * 128;
@@ -563,7 +564,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                 if (!ok) break;
                 weights(k, s);
             }
-            tma_load_3d(base + s * stage + kOperand, &mx, &S.full[s], k * kBK, 0, 0);
+            tma_load_3d(base + s * stage + kOperand, &mx, &S.full[s], k * kBK, row0, 0);
         }
         if (*(volatile int*)&S.abort)                   // copies still in flight
             for (int i = max(0, it - p.stages); i < it; ++i) drain(&S.full[i % p.stages], (i / p.stages) & 1, p.limit);
@@ -615,10 +616,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     asm volatile("griddepcontrol.wait;" ::: "memory");     // (long over: for the residual, g and u, read by every thread)
     if (good) {
         constexpr int kGroups = MODE == kGated ? 16 : 32;            // of 4 columns
-        const int items = p.N * kGroups, share = (items + ranks - 1) / ranks;
+        const int items = min(p.bn, p.N - row0) * kGroups, share = (items + ranks - 1) / ranks;
         const int last = min(items, (rank + 1) * share);
         for (int i = rank * share + (int)threadIdx.x; i < last; i += kNarrowThreads) {
             const int t = i / kGroups, g4 = i % kGroups * 4, col = first + g4;
+            const long long row = row0 + t;
             if (col >= p.wide) continue;
             f2 v[2] = {splat<f2>(0.f), splat<f2>(0.f)}, u[2] = {v[0], v[0]};
             for (int q0 = 0; q0 < ranks; q0 += 4) {                  // four blocks' sums on their way together
@@ -644,14 +646,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
             if constexpr (MODE == kStore) {
                 if (p.add) {
                     f2 r[2];
-                    unpack(*reinterpret_cast<const uint2*>(p.add + t * p.add_row + col), r);
+                    unpack(*reinterpret_cast<const uint2*>(p.add + row * p.add_row + col), r);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) v[j] = add(v[j], r[j]);
                 }
-                *reinterpret_cast<uint2*>(p.out + (long long)t * p.wide + col) = pack(v);
+                *reinterpret_cast<uint2*>(p.out + row * p.wide + col) = pack(v);
             } else {
-                bf16* gu = p.gu + (long long)t * 2 * p.F + col;
-                uint2* h = reinterpret_cast<uint2*>(p.h + (long long)t * p.F + col);
+                bf16* gu = p.gu + row * 2 * p.F + col;
+                uint2* h = reinterpret_cast<uint2*>(p.h + row * p.F + col);
                 if constexpr (MODE == kGated) {
                     if (p.gu) {
                         *reinterpret_cast<uint2*>(gu) = pack(v);
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                         g[j] = mul(mul(v[j], u[j]), slope);
                         u[j] = mul(v[j], a);
                     }
-                    bf16* dgu = p.out + (long long)t * 2 * p.F + col;
+                    bf16* dgu = p.out + row * 2 * p.F + col;
                     *reinterpret_cast<uint2*>(dgu) = pack(g);
                     *reinterpret_cast<uint2*>(dgu + p.F) = pack(u);
                     *h = pack(hh);
@@ -719,10 +721,8 @@ bool problem(Problem& q, int M, int N, int K, int mode) {
     return tiles < (1LL << 30);
 }
 
-// Clusters of `width` blocks that run at once (a cluster stays within a group of SMs).
-template <bool AMN, bool BMN, int MODE>
-int clusters_at_once(int width) {
-    static std::atomic<int> known[9];
+// Clusters of `width` blocks that run at once (a cluster stays within a group of SMs), asked once for a kernel and width.
+int clusters_at_once(const void* kernel, std::atomic<int>* known, int width, int threads, int smem) {
     const int k = known[width].load(std::memory_order_relaxed);
     if (k > 0) return k;
     cudaLaunchAttribute at[1];
@@ -731,12 +731,12 @@ int clusters_at_once(int width) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3(width);
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = kSmem;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
     c.attrs = at;
     c.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, ffn_gemm_kernel<AMN, BMN, MODE, true>, &c) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess) {
         cudaGetLastError();
         n = 0;
     }
@@ -759,10 +759,13 @@ Plan plan_of(const GemmParams& p) {
     const int whole = p.tiles / kPairs * kPairs, rest = p.tiles - whole;
     Plan plan{p.tiles, 1};
     if (rest == 0) return plan;
+    static std::atomic<int> known[9];
+    const void* kernel = reinterpret_cast<const void*>(ffn_gemm_kernel<AMN, BMN, MODE, true>);
     int least = kblocks + (whole ? 0 : 6);
     for (int n = 2; n <= 4; ++n) {
-        const int each = (kblocks + n - 1) / n, at_once = clusters_at_once<AMN, BMN, MODE>(2 * n);
+        const int each = (kblocks + n - 1) / n;
         if (each < 4 || (kblocks + each - 1) / each != n) continue;
+        const int at_once = clusters_at_once(kernel, known, 2 * n, kThreads, kSmem);
         const int cost = (rest + at_once - 1) / at_once * (each + 10);
         if (cost < least) {
             least = cost;
@@ -805,28 +808,53 @@ cudaError_t gemm(const Maps& m0, const Maps& m1, GemmParams p, cudaStream_t s, i
     return launch<AMN, BMN, MODE, true>(m0, m1, p, 2 * p.splits * (all - p.tile0), s);
 }
 
-// Splits of K, of two blocks of K at least, that fill the places of two blocks an SM (16 x 2048 x 5504: 19.4 us a call, 22.2
-// with three quarters of that, 25 with more blocks than places).
+// Splits of K, of two blocks of K at least, by rounds of the clusters that run at once: a round takes its blocks of K and
+// the set-up, the passing on of the sums and the epilogue (6).  16 x 2048 x 5504: 16.9 us a call, 19.4 with as many
+// splits as fill two blocks an SM whether the clusters fit at once or not; 128 x 2048 x 1544 17.4 and 22.
 template <bool WMN, int MODE>
 cudaError_t narrow(const CUtensorMap& mw, const Matrix& x, NarrowParams p, bool second, cudaStream_t s) {
     const int columns = MODE == kGated ? 64 : 128, tiles = (p.wide + columns - 1) / columns;
     const int kblocks = (p.K + kBK - 1) / kBK;
-    int splits = kNarrowBlocks / tiles;
-    splits = splits > 8 ? 8 : splits;
-    if (splits > kblocks / 2) splits = kblocks / 2;
-    if (splits < 1) splits = 1;
+    p.parts = (p.N + kNarrow - 1) / kNarrow;
+    const int rows = (p.N + p.parts - 1) / p.parts;
+    p.bn = (rows + 15) / 16 * 16;
+    auto kernel = ffn_narrow_kernel<WMN, MODE>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
+    if (e != cudaSuccess) return e;
+    static std::atomic<int> known[9];
+    int splits = 1, least = INT_MAX;
+    for (int n = 1; n <= 8; ++n) {
+        const int each = (kblocks + n - 1) / n;
+        if (n > 1 && (each < 2 || (kblocks + each - 1) / each != n)) continue;
+        const int at_once = clusters_at_once(reinterpret_cast<const void*>(kernel), known, n, kNarrowThreads, kNarrowSmem);
+        const long long cost = ((long long)tiles * p.parts + at_once - 1) / at_once * (each + 6);
+        if (cost < least) {
+            least = (int)cost;
+            splits = n;
+        }
+    }
     p.kblocks = (kblocks + splits - 1) / splits;
-    splits = (kblocks + p.kblocks - 1) / p.kblocks;
-    p.bn = (p.N + 15) / 16 * 16;
     p.second = second;
     const int stage = kOperand + p.bn * 128, room = kNarrowSmem - 1024;
     p.stages = room / stage < kNarrowStages ? room / stage : kNarrowStages;
     CUtensorMap mx;
     if (!x.map(&mx, p.bn)) return cudaErrorInvalidValue;
-    auto kernel = ffn_narrow_kernel<WMN, MODE>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
-    if (e != cudaSuccess) return e;
-    return launch_in_clusters(kernel, dim3(tiles * splits), dim3(kNarrowThreads), kNarrowSmem, s, splits, true, mw, mx, p);
+    return launch_in_clusters(kernel, dim3(tiles * p.parts * splits), dim3(kNarrowThreads), kNarrowSmem, s, splits, true, mw, mx, p);
+}
+
+// Whether a product of N rows takes the narrow kernel: always up to 128.  Up to 768 rows, parts of 128 read the weights
+// again (from L2), which pays while the wide kernel's 256 x 256 tiles leave most pairs idle: with up to 48 parts of tiles
+// (330 x 2048 x 5504 forward 46.9 us, both products wide 50.8; 500 rows, 64 parts: 56.5 and 52.6), up to 152 where K is
+// short and the parts of rows are few (500 x 768 x 2048 forward 19.6 and 23.1, input gradient 21.1 and 28.0; 760 rows,
+// 192 parts: 22.2 and 20.2; 760 x 2048 x 1544, second product: 36.8 and 28.6 in all), or where the tiles are a little
+// more than a round of the pairs (330 x 2048 x 5504, first product also: 35.4 and 46.9).
+bool few(int N, int K, int wide, int columns) {
+    if (N <= kNarrow) return true;
+    if (N > 6 * kNarrow) return false;
+    const long long of_rows = (N + kNarrow - 1) / kNarrow, parts = (wide + columns - 1) / columns * of_rows;
+    const long long tiles = (long long)((wide + 2 * columns - 1) / (2 * columns)) * ((N + kTile - 1) / kTile);
+    return parts <= 48 || (parts <= 2 * kPairs && parts * of_rows * ((K + kBK - 1) / kBK) <= 6800) ||
+           (tiles > kPairs && parts <= 4 * kPairs);
 }
 
 NarrowParams narrow_params(const FfnArgs& a) {
@@ -857,8 +885,8 @@ cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
     const long long N = a.N, D = a.D, F = a.F;
     const Matrix x{a.x, N, D, a.x_row}, wi{a.W_in, D, 2 * F, 2 * F}, wo{a.W_out, F, D, D}, h{a.workspace, N, F, F};
     *launches = 0;
-    if (a.N <= kNarrow) {
-        *launches = 2;
+    cudaError_t e;
+    if (few(a.N, a.D, a.F, 64)) {
         NarrowParams p = narrow_params(a);
         CUtensorMap w;
         p.wide = a.F;
@@ -867,26 +895,31 @@ cudaError_t ffn_fwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         p.gu = static_cast<bf16*>(a.gu);
         p.debug_stall = a.debug_stall;
         if (!wi.halves(&w, 64)) return cudaErrorInvalidValue;
-        const cudaError_t e = narrow<true, kGated>(w, x, p, false, s);
-        if (e != cudaSuccess) return e;
+        e = narrow<true, kGated>(w, x, p, false, s);
+        ++*launches;
+    } else {
+        GemmParams p = params(a);
+        p.debug_stall = a.debug_stall;
+        p.q[0].out = static_cast<bf16*>(a.gu);
+        p.q[0].h = static_cast<bf16*>(a.workspace);
+        Maps m{};
+        if (!x.operand(&m.a, false) || !wi.halves(&m.b, 64) || !problem(p.q[0], a.N, a.F, a.D, kGated))
+            return cudaErrorInvalidValue;
+        e = gemm<false, true, kGated>(m, m, p, s, launches);
+    }
+    if (e != cudaSuccess) return e;
+    if (few(a.N, a.F, a.D, 128)) {
         NarrowParams o = narrow_params(a);
+        CUtensorMap w;
         o.wide = a.D;
         o.K = a.F;
         o.out = static_cast<bf16*>(a.y);
         o.add = static_cast<const bf16*>(a.residual);
         o.add_row = a.residual_row;
         if (!wo.operand(&w, true)) return cudaErrorInvalidValue;
+        ++*launches;
         return narrow<true, kStore>(w, h, o, true, s);
     }
-    GemmParams p = params(a);
-    p.debug_stall = a.debug_stall;
-    p.q[0].out = static_cast<bf16*>(a.gu);
-    p.q[0].h = static_cast<bf16*>(a.workspace);
-    Maps m{};
-    if (!x.operand(&m.a, false) || !wi.halves(&m.b, 64) || !problem(p.q[0], a.N, a.F, a.D, kGated))
-        return cudaErrorInvalidValue;
-    const cudaError_t e = gemm<false, true, kGated>(m, m, p, s, launches);
-    if (e != cudaSuccess) return e;
     GemmParams o = params(a);
     Maps n{};
     if (!h.operand(&n.a, false) || !wo.operand(&n.b, true) || !problem(o.q[0], a.N, a.D, a.F, kStore))
@@ -904,7 +937,7 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         dgu{ws, N, 2 * F, 2 * F}, h{ws + (size_t)N * F * 4, N, F, F};
     *launches = 0;
     cudaError_t e;
-    if (a.N <= kNarrow) {
+    if (few(a.N, a.D, a.F, 128)) {
         NarrowParams p = narrow_params(a);
         CUtensorMap w;
         p.wide = a.F;
@@ -930,7 +963,7 @@ cudaError_t ffn_bwd_launch(const FfnArgs& a, cudaStream_t s, int* launches) {
         e = gemm<false, false, kGatedBack>(m, m, p, s, launches);
     }
     if (e != cudaSuccess) return e;
-    if (a.dx && a.N <= kNarrow) {
+    if (a.dx && few(a.N, 2 * a.F, a.D, 128)) {
         NarrowParams o = narrow_params(a);
         CUtensorMap w;
         o.wide = a.D;

@@ -102,7 +102,9 @@ def test_sizes(N, D, F):
 
 @pytest.mark.parametrize("N,D,F", [(1, 2048, 5504), (16, 2048, 5504), (48, 768, 2048), (300, 2048, 512), (1537, 768, 2056),
                                    (777, 1000, 3000), (2048, 512, 1024), (4097, 136, 72), (1000, 24, 4096), (130, 4096, 40),
-                                   (5000, 1032, 776), (9001, 264, 2008), (20011, 520, 136), (2300, 2048, 2816)])
+                                   (5000, 1032, 776), (9001, 264, 2008), (20011, 520, 136), (2300, 2048, 2816),
+                                   (330, 2048, 5504), (250, 2048, 5504), (500, 768, 2048), (768, 136, 2048), (769, 136, 2048),
+                                   (640, 2048, 1544), (385, 520, 5504)])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_larger(N, D, F, act):
     check(N, D, F, act)
@@ -131,7 +133,7 @@ def test_no_rows():
     assert d["dx"].shape == (0, 64) and not d["dW_in"].any() and not d["dW_out"].any()
 
 
-@pytest.mark.parametrize("N", [5, 300])
+@pytest.mark.parametrize("N", [5, 300, 900])
 def test_values_that_are_not_finite_stay_in_their_row(N):
     x, dy, res, W_in, W_out = make(N, 128, 256)
     want, gu = ttm.gated_ffn_fwd(x, W_in, W_out, residual=res)
@@ -195,7 +197,7 @@ def test_offsets_past_32_bits():
         assert float((a.double() - b.double()).norm()) <= HALF * float(b.double().norm())
 
 
-@pytest.mark.parametrize("N", [9, 400])
+@pytest.mark.parametrize("N", [9, 400, 1100])
 def test_streams_graphs_and_given_outputs(N):
     x, dy, res, W_in, W_out = make(N, 256, 512)
     y, gu = ttm.gated_ffn_fwd(x, W_in, W_out, residual=res)
