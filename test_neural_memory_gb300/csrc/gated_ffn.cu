@@ -42,7 +42,7 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr long long kWaitCycles = 4000000000LL;   // default limit, ~2 s at 2 GHz
-constexpr int kPairs = 76;                        // pairs of the 152 SMs
+constexpr int kSms = 152, kPairs = kSms / 2;
 
 // Values in pairs, as bf16 in words.
 template <int N>
@@ -481,12 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // them (more take another block).  A cluster of up to 8 blocks shares a tile's K, so that all SMs read weights however
 // few the tiles are; each leaves its sums in shared memory, and a share of the results is added up over the blocks in
 // their order, put through the epilogue and written by each.  The second kernel of a call starts on its weights while
-// the first one finishes.  16 x 2048 x 5504: 16.9 us a call, 67.6 MB of weights at 4.0 TB/s with both launches.
+// the first one finishes.  16 x 2048 x 5504: 19.7 us a call, 67.6 MB of weights
+// at 3.4 TB/s with both launches.
 constexpr int kNarrow = 128, kNarrowThreads = 256, kNarrowStages = 6, kNarrowSmem = 110 * 1024;     // two blocks an SM
 
 struct NarrowParams {
     int N, wide, K;                     // rows; columns of the result (kGated: F); K
-    int parts;                          // of the rows, bn each
     int F, kblocks;                     // kGated, kGatedBack: F; blocks of K of a block of the cluster
     int bn, stages;                     // rows, padded to 16
     int gelu, second;                   // second: of a call's kernels
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     unsigned char* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
-    const int tile = blockIdx.x / ranks / p.parts, row0 = blockIdx.x / ranks % p.parts * p.bn;
+    const int tile = blockIdx.x / ranks, row0 = blockIdx.y * p.bn;
     const int first = MODE == kGated ? tile * 64 : tile * 128;       // column of the result (kGated: f)
     const int k0 = rank * p.kblocks, k1 = min((p.K + kBK - 1) / kBK, k0 + p.kblocks);
     const uint32_t stage = kOperand + p.bn * 128;
@@ -808,28 +808,32 @@ cudaError_t gemm(const Maps& m0, const Maps& m1, GemmParams p, cudaStream_t s, i
     return launch<AMN, BMN, MODE, true>(m0, m1, p, 2 * p.splits * (all - p.tile0), s);
 }
 
-// Splits of K, of two blocks of K at least, by rounds of the clusters that run at once: a round takes its blocks of K and
-// the set-up, the passing on of the sums and the epilogue (6).  16 x 2048 x 5504: 16.9 us a call, 19.4 with as many
-// splits as fill two blocks an SM whether the clusters fit at once or not; 128 x 2048 x 1544 17.4 and 22.
+// Splits of K, of two blocks of K at least, by rounds of the clusters that run at once: a round takes its blocks of K, the
+// set-up and epilogue (6) and the passing on of sums (2).  Two blocks share an SM (the query counts one where a kernel uses
+// tensor memory); a launch that needs the second places (4 more) leaves none to the launch after it, whose weights could
+// be on their way.  128 x 2048 x 1544 forward: 19 us with 125 blocks, 23.5 with 200; 16 x 2048 x 5504: 19.6 with 258, 22.2 with
+// two thirds of them.
 template <bool WMN, int MODE>
 cudaError_t narrow(const CUtensorMap& mw, const Matrix& x, NarrowParams p, bool second, cudaStream_t s) {
     const int columns = MODE == kGated ? 64 : 128, tiles = (p.wide + columns - 1) / columns;
     const int kblocks = (p.K + kBK - 1) / kBK;
-    p.parts = (p.N + kNarrow - 1) / kNarrow;
-    const int rows = (p.N + p.parts - 1) / p.parts;
+    const int parts = (p.N + kNarrow - 1) / kNarrow;
+    const int rows = (p.N + parts - 1) / parts;
     p.bn = (rows + 15) / 16 * 16;
     auto kernel = ffn_narrow_kernel<WMN, MODE>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
     if (e != cudaSuccess) return e;
     static std::atomic<int> known[9];
-    int splits = 1, least = INT_MAX;
+    int splits = 1;
+    long long least = LLONG_MAX;
     for (int n = 1; n <= 8; ++n) {
         const int each = (kblocks + n - 1) / n;
         if (n > 1 && (each < 2 || (kblocks + each - 1) / each != n)) continue;
-        const int at_once = clusters_at_once(reinterpret_cast<const void*>(kernel), known, n, kNarrowThreads, kNarrowSmem);
-        const long long cost = ((long long)tiles * p.parts + at_once - 1) / at_once * (each + 6);
-        if (cost < least) {
-            least = (int)cost;
+        const int places = clusters_at_once(reinterpret_cast<const void*>(kernel), known, n, kNarrowThreads, kNarrowSmem);
+        const long long all = (long long)tiles * parts, rounds = (all + 2 * places - 1) / (2 * places);
+        const long long cost = rounds * (each + (n > 1 ? 8 : 6)) + (all > places ? 4 : 0);
+        if (cost <= least) {
+            least = cost;
             splits = n;
         }
     }
@@ -839,15 +843,15 @@ cudaError_t narrow(const CUtensorMap& mw, const Matrix& x, NarrowParams p, bool 
     p.stages = room / stage < kNarrowStages ? room / stage : kNarrowStages;
     CUtensorMap mx;
     if (!x.map(&mx, p.bn)) return cudaErrorInvalidValue;
-    return launch_in_clusters(kernel, dim3(tiles * p.parts * splits), dim3(kNarrowThreads), kNarrowSmem, s, splits, true, mw, mx, p);
+    return launch_in_clusters(kernel, dim3(tiles * splits, parts), dim3(kNarrowThreads), kNarrowSmem, s, splits, true, mw, mx, p);
 }
 
 // Whether a product of N rows takes the narrow kernel: always up to 128.  Up to 768 rows, parts of 128 read the weights
 // again (from L2), which pays while the wide kernel's 256 x 256 tiles leave most pairs idle: with up to 48 parts of tiles
-// (330 x 2048 x 5504 forward 46.9 us, both products wide 50.8; 500 rows, 64 parts: 56.5 and 52.6), up to 152 where K is
-// short and the parts of rows are few (500 x 768 x 2048 forward 19.6 and 23.1, input gradient 21.1 and 28.0; 760 rows,
-// 192 parts: 22.2 and 20.2; 760 x 2048 x 1544, second product: 36.8 and 28.6 in all), or where the tiles are a little
-// more than a round of the pairs (330 x 2048 x 5504, first product also: 35.4 and 46.9).
+// (160 x 2048 x 5504 forward 29.2 us, wide 33.1; with the weights in L2 500 rows, 64 parts: 56.5 and 52.6), up to 152 where
+// K is short and the parts of rows are few (250 x 768 x 2048 forward 16.3 and 25.9, input gradient 18.7 and 26.5; with the
+// weights in L2 760 rows, 192 parts: 22.2 and 20.2; 760 x 2048 x 1544, second product: 36.8 and 28.6 in all), or where the
+// tiles are a little more than a round of the pairs (330 x 2048 x 5504: 36.8 and 51.2).
 bool few(int N, int K, int wide, int columns) {
     if (N <= kNarrow) return true;
     if (N > 6 * kNarrow) return false;
