@@ -740,7 +740,9 @@ unsigned long long ttm_launch_count(void);
  *     chip and the one that takes the steps on A alone leave their product c
  *     (three a step) unannounced, the first product from global memory
  *     leaves stage c of its copies (modulo their number) unfilled.  So does ttm_glr_fwd /
- *     ttm_glr_bwd, with 16 bytes more for its tile c.  The setting
+ *     ttm_glr_bwd, with 16 bytes more for its tile c, and ttm_gated_ffn_fwd /
+ *     ttm_gated_ffn_bwd, whose first product leaves stage c of its copies
+ *     (modulo their number) unfilled.  The setting
  *     is used up by that one call; -1 clears it.  Nothing faults, traps or
  *     hangs.
  *   TTM_DBG_FAIL_CALLS, n >= 0: the next n calls of ttm_linear_fwd,

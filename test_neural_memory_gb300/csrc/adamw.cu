@@ -15,7 +15,9 @@
 // takes blocks of 256 values, 8 a lane in two runs of 4, so that every access of a warp is one piece of
 // memory; tensors that do not start on 16 bytes, and their last blocks, go value by value.  The table of
 // tensors travels as a kernel argument (a copy to the device would be a call of its own, and not the
-// captured graph's), and a block finds its first tensor by bisection.
+// captured graph's), and a block finds its first tensor by bisection.  Measured: 92 M values of 12 layers, bf16 gradients and
+// copies, 396 us, 98 % of a copy's rate; 8 bits 55 M values cold 212 us, 3.9 TB/s, bound by 96 instructions a value (hash,
+// two roundings, scales), and 91 us for reading the moments out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -294,7 +296,7 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
     }
 }
 
-// Blocks an SM: 8 bits have 85 instructions and more to a value and want every warp; 32 bits are at HBM's rate either way
+// Blocks an SM: 8 bits have 96 instructions to a value and want every warp; 32 bits are at HBM's rate either way
 // and go 3 % faster with fewer rows of memory open at a time (92 M values 396 us, 407 with four).
 template <bool EIGHT> constexpr int kBlocksPerSm = EIGHT ? 4 : 3;
 

@@ -8,7 +8,9 @@
 // Bound by HBM: two tensors forward, three in the gradient, K products and one exponential a value.  So
 // every value is read once (but for the K - 1 rows between strips) and the window stays in registers: a
 // thread takes V neighbouring channels, as wide as the rows' alignment allows, and walks a strip of
-// tokens, the loads of kBatch rows ahead of their use.
+// tokens, the loads of kBatch rows ahead of their use.  Measured (K = 4, bf16, SiLU): forward 131072 x 6144 537 us, 6.0 TB/s,
+// 90 % of a copy; gradient 8 x 8192 x 2304 174 us, 5.2 TB/s, its 26 instructions a value and three blocks of registers
+// an SM as much the bound as the memory; a step of 64 x 6144 4.6 us, of which the GPU's part is a launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -297,8 +299,8 @@ __global__ void conv_pass_kernel(const T* from, T* to, long long n) {
 // one part of the block's row of the grid, joined by conv_join_kernel in the rows' order: equal inputs give
 // equal bits.
 template <typename T, int V, int KW, bool kAll, bool DOC>
-__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks<V, KW>) conv_bwd_kernel(const __grid_constant__ ConvArgs a, int groups,
-                                                                int strips, int strip) {
+__global__ void __launch_bounds__(kBwdThreads, kBwdBlocks<V, KW>)
+    conv_bwd_kernel(const __grid_constant__ ConvArgs a, int groups, int strips, int strip) {
     constexpr int NV = kVals<V>;
     using E = Val<V>;
     constexpr bool kRing = sizeof(Raw<T, V>) >= 4;      // (asynchronous copies take 4 bytes at least)
