@@ -16,7 +16,7 @@
 // memory; tensors that do not start on 16 bytes, and their last blocks, go value by value.  The table of
 // tensors travels as a kernel argument (a copy to the device would be a call of its own, and not the
 // captured graph's), and a block finds its first tensor by bisection.  Measured: 92 M values of 12 layers, bf16 gradients and
-// copies, 396 us, 98 % of a copy's rate; 8 bits 55 M values cold 201 us, 4.1 TB/s, bound by 89 instructions a value (hash,
+// copies, 396 us, 98 % of a copy's rate; 8 bits 55 M values cold 212 us, 3.9 TB/s, bound by 96 instructions a value (hash,
 // two roundings, scales), and 91 us for reading the moments out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -27,7 +27,6 @@
 #include <cstdint>
 
 #include "overlap.cuh"
-#include "pairs.cuh"
 #include "train_ops.h"
 
 namespace ttm {
@@ -107,19 +106,16 @@ __device__ __forceinline__ Consts constants(const AdamwScalars& a) {
     return k;
 }
 
-// m and v of two values (no fused multiply-add; packed operations round as single ones do, and are half as many: 55 M
-// values in 8 bits 186 -> 178 us), then p from v's root.
-__device__ __forceinline__ void moments(const Consts& k, f2 g, f2& m, f2& v) {
-    g = mul(g, splat<f2>(k.scale));
-    m = add(mul(m, splat<f2>(k.b1)), mul(g, splat<f2>(k.c1)));
-    v = add(mul(v, splat<f2>(k.b2)), mul(mul(g, g), splat<f2>(k.c2)));
+// m, v and p of one value.
+__device__ __forceinline__ void moments(const Consts& k, float g, float& m, float& v) {
+    g = __fmul_rn(g, k.scale);
+    m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.c1));
+    v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.c2));
 }
-__device__ __forceinline__ f2 update(const Consts& k, f2 p, f2 m, f2 root) {
-    float lo, hi;
-    split(fma(root, splat<f2>(k.root2), splat<f2>(k.eps)), lo, hi);
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(lo));       // 1 unit off
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(hi));
-    return fma(mul(m, splat<f2>(-k.lr1)), pair(lo, hi), mul(p, splat<f2>(k.keep)));
+__device__ __forceinline__ float update(const Consts& k, float p, float m, float root) {
+    float r;                            // 1 unit off
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(root, k.root2, k.eps)));
+    return fmaf(-(k.lr1 * m), r, p * k.keep);
 }
 
 // One block of up to 256 values by a warp.  VEC: 256 of them, in runs of 4 a lane; otherwise lane l takes the
@@ -182,28 +178,20 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
     }
     uint32_t most_m = 0, most_r = 0, mc[2], vc[2];  // largest sizes; codes, four to a word
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        f2 mj = pair(m[j], m[j + 1]), vj = pair(v[j], v[j + 1]);
+    for (int j = 0; j < 8; ++j) {
         if constexpr (EIGHT) {
-            mj = mul(mj, splat<f2>(ms));
-            vj = mul(vj, splat<f2>(vs));
-            vj = mul(vj, vj);
+            m[j] = __fmul_rn(m[j], ms);
+            v[j] = __fmul_rn(v[j], vs);
+            v[j] = __fmul_rn(v[j], v[j]);
         }
-        moments(k, pair(g[j], g[j + 1]), mj, vj);
-        float root[2];
-        split(mj, m[j], m[j + 1]);
-        split(vj, v[j], v[j + 1]);
-        root[0] = sqrtf(v[j]);
-        root[1] = sqrtf(v[j + 1]);
-        split(update(k, pair(p[j], p[j + 1]), mj, pair(root[0], root[1])), p[j], p[j + 1]);
+        moments(k, g[j], m[j], v[j]);
+        const float root = sqrtf(v[j]);
+        p[j] = update(k, p[j], m[j], root);
         if constexpr (EIGHT) {
-#pragma unroll
-            for (int i = j; i < j + 2; ++i) {
-                v[i] = root[i - j];
-                if (VEC || index(i) < n) {
-                    most_m = max(most_m, size_bits(m[i]));
-                    most_r = max(most_r, size_bits(v[i]));
-                }
+            v[j] = root;
+            if (VEC || index(j) < n) {
+                most_m = max(most_m, size_bits(m[j]));
+                most_r = max(most_r, size_bits(root));
             }
         }
     }
@@ -308,7 +296,7 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
     }
 }
 
-// Blocks an SM: 8 bits have 89 instructions to a value and want every warp; 32 bits are at HBM's rate either way
+// Blocks an SM: 8 bits have 96 instructions to a value and want every warp; 32 bits are at HBM's rate either way
 // and go 3 % faster with fewer rows of memory open at a time (92 M values 396 us, 407 with four).
 template <bool EIGHT> constexpr int kBlocksPerSm = EIGHT ? 4 : 3;
 
