@@ -94,6 +94,22 @@ def test_32_bits(sizes, param, grad, copies, packed):
     assert state["step"].tolist() == [3, 0]
 
 
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+def test_moments_round_after_every_operation(grad):
+    """m and v in 32 bits are those of single operations, bit for bit: none is fused with the next."""
+    p, g = make([5000, 257, 70001], "f32", grad, seed=6)
+    state = ttm.adamw_state(p)
+    b1, b2 = torch.tensor(0.9, device="cuda"), torch.tensor(0.95, device="cuda")
+    c1, c2 = torch.tensor(1 - 0.9, device="cuda"), torch.tensor(1 - 0.95, device="cuda")
+    want = [(torch.zeros_like(a), torch.zeros_like(a)) for a in p]
+    for _ in range(3):
+        ttm.adamw_step(p, g, state, **HYPER)
+        want = [(m * b1 + x.float() * c1, v * b2 + (x.float() * x.float()) * c2) for (m, v), x in zip(want, g)]
+    for (m, v), at in zip(want, starts([5000, 257, 70001])):
+        assert torch.equal(state["m"].flatten()[at:at + m.numel()], m)
+        assert torch.equal(state["v"].flatten()[at:at + v.numel()], v)
+
+
 def dither(first, n, t):
     at = first + torch.arange(n)
     h = (at + t * 0x9e3779b9) & 0xffffffff
