@@ -17,6 +17,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "conv_plan.h"
 #include "overlap.cuh"
 #include "pairs.cuh"
 #include "train_ops.h"
@@ -24,10 +25,7 @@
 namespace ttm {
 namespace {
 
-constexpr int kSms = 152;
-constexpr int kBatch = 4;               // rows whose loads are in flight together
-constexpr int kFwdThreads = 128;
-constexpr int kBwdThreads = 128;
+constexpr int kBatch = kConvBatch, kFwdThreads = kConvThreads, kBwdThreads = kConvThreads;
 // Blocks of the gradient an SM, by registers (8 x 8192 x 2304 bf16 in pairs of values: 212 us with 4, 278 with 3).
 template <int V, int KW> constexpr int kBwdBlocks = V <= 2 && KW <= 4 ? 4 : 3;
 
@@ -553,22 +551,18 @@ int widest(const ConvArgs& a, bool back) {
 
 template <typename T, int V, int KW, bool kAll>
 cudaError_t fwd(const ConvArgs& a, bool one_strip, cudaStream_t s) {
-    const unsigned groups = a.C / V;
-    // Strips as long as leave two waves of threads, 8 to 128 tokens: the rows between strips are read twice.
-    int strip = one_strip ? a.T : 128;
-    while (!one_strip && strip > 8 && (long long)a.N * groups * ((a.T + strip - 1) / strip) < kSms * 2048LL) strip /= 2;
-    const unsigned strips = (a.T + strip - 1) / strip;
-    const long long blocks = ((long long)a.N * groups * strips + kFwdThreads - 1) / kFwdThreads;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const int groups = a.C / V;
+    const ConvFwdPlan p = conv_fwd_plan(a.N, a.T, groups, one_strip);
+    if (p.blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_overlapped(a.doc ? conv_fwd_kernel<T, V, KW, kAll, true> : conv_fwd_kernel<T, V, KW, kAll, false>,
-                             dim3((unsigned)blocks), dim3(kFwdThreads), s, a, groups, strips, strip);
+                             dim3((unsigned)p.blocks), dim3(kFwdThreads), s, a, (unsigned)groups, (unsigned)p.strips, p.strip);
 }
 
 // Rows of the gradient's grid at most, one wave by the widest channel groups that a call may take; the workspace
 // holds a part for each.
 int most_rows(int C) {
     const int across = ((C + 3) / 4 + 31) / 32;
-    const int rows = kSms * 4 / across;
+    const int rows = kConvSms * 4 / across;
     return rows < 1 ? 1 : rows;
 }
 
@@ -579,7 +573,7 @@ cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
     while (bx < groups && bx < 32) bx *= 2;
     const int by = kBwdThreads / bx, across = (groups + bx - 1) / bx;
     // One strip a thread where the sequences are fewer than the threads of a column of the grid, of 16 tokens at least.
-    int rows = kSms * kBwdBlocks<V, KW> / across;
+    int rows = kConvSms * kBwdBlocks<V, KW> / across;
     if (rows > most_rows(a.C)) rows = most_rows(a.C);
     if (rows < 1) rows = 1;
     const long long places = (long long)rows * by, each = places / a.N;
