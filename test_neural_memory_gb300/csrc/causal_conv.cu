@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kFwdThreads) conv_fwd_kernel(const __grid_cons
     after_all_before();
     if (n >= (unsigned)a.N) return;
     const int c = (int)group * V, K = a.K, C = a.C, before = kAll ? 0 : KW - K;
-    const int t0 = (int)part * strip, t1 = min(a.T, t0 + strip);
+    const int t0 = (int)part * strip, t1 = conv_strip_end(a.T, t0, strip);
     const Rows<T> rows{static_cast<const T*>(a.x) + n * a.x_seq + c, a.x_tok,
                        a.state0 ? static_cast<const T*>(a.state0) + (long long)n * (K - 1) * C + c : nullptr, C, K};
     const int* doc = DOC ? a.doc + n * a.doc_seq : nullptr;
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks<V, KW>)
     for (long long s = (long long)blockIdx.y * blockDim.y + threadIdx.y; s < total;
          s += (long long)gridDim.y * blockDim.y) {
         const long long n = s / strips;
-        const int t0 = (int)(s % strips) * strip, t1 = min(a.T, t0 + strip), end = min(a.T, t1 + KW - 1);
+        const int t0 = (int)(s % strips) * strip, t1 = conv_strip_end(a.T, t0, strip), end = min(a.T, t1 + KW - 1);
         const Rows<T> rows{static_cast<const T*>(a.x) + n * a.x_seq + c, a.x_tok,
                            a.state0 ? static_cast<const T*>(a.state0) + n * (K - 1) * C + c : nullptr, C, K};
         const int* doc = DOC ? a.doc + n * a.doc_seq : nullptr;
@@ -558,35 +558,15 @@ cudaError_t fwd(const ConvArgs& a, bool one_strip, cudaStream_t s) {
                              dim3((unsigned)p.blocks), dim3(kFwdThreads), s, a, (unsigned)groups, (unsigned)p.strips, p.strip);
 }
 
-// Rows of the gradient's grid at most, one wave by the widest channel groups that a call may take; the workspace
-// holds a part for each.
-int most_rows(int C) {
-    const int across = ((C + 3) / 4 + 31) / 32;
-    const int rows = kConvSms * 4 / across;
-    return rows < 1 ? 1 : rows;
-}
-
 template <typename T, int V, int KW, bool kAll>
 cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
     const int groups = a.C / V;
-    int bx = 1;
-    while (bx < groups && bx < 32) bx *= 2;
-    const int by = kBwdThreads / bx, across = (groups + bx - 1) / bx;
-    // One strip a thread where the sequences are fewer than the threads of a column of the grid, of 16 tokens at least.
-    int rows = kConvSms * kBwdBlocks<V, KW> / across;
-    if (rows > most_rows(a.C)) rows = most_rows(a.C);
-    if (rows < 1) rows = 1;
-    const long long places = (long long)rows * by, each = places / a.N;
-    int strip = each <= 1 ? a.T : (int)((a.T + each - 1) / each);
-    strip = strip < 16 ? 16 : (strip + kBatch - 1) / kBatch * kBatch;
-    const int strips = (a.T + strip - 1) / strip;
-    const long long wanted = ((long long)a.N * strips + by - 1) / by;
-    if (wanted < rows) rows = (int)wanted;
-    const dim3 grid(across, rows), block(bx, by);
+    const ConvBwdPlan p = conv_bwd_plan(a.N, a.T, a.C, groups, kBwdBlocks<V, KW>);
+    const dim3 grid(p.across, p.rows), block(p.bx, p.by);
     const cudaError_t e = launch_overlapped(a.doc ? conv_bwd_kernel<T, V, KW, kAll, true> : conv_bwd_kernel<T, V, KW, kAll, false>,
-                                            grid, block, s, a, groups, strips, strip);
+                                            grid, block, s, a, groups, p.strips, p.strip);
     if (e != cudaSuccess || !a.partial) return e;
-    return launch_overlapped(conv_join_kernel, dim3((a.C + 31) / 32, a.K + 1), dim3(32, 8), s, (const float*)a.partial, rows,
+    return launch_overlapped(conv_join_kernel, dim3((a.C + 31) / 32, a.K + 1), dim3(32, 8), s, (const float*)a.partial, p.rows,
                              a.C, a.K, a.dw, a.db);
 }
 
@@ -640,7 +620,7 @@ cudaError_t pass_state(const ConvArgs& a, const void* from, void* to, cudaStream
 }  // namespace
 
 size_t conv_bwd_workspace_bytes(const ConvArgs& a) {
-    return (size_t)most_rows(a.C) * (a.K + 1) * a.C * 4;
+    return (size_t)conv_most_rows(a.C) * (a.K + 1) * a.C * 4;
 }
 
 cudaError_t conv_fwd_launch(const ConvArgs& a, cudaStream_t s) {
