@@ -307,9 +307,9 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks<V, KW>)
     __shared__ float sums[kBwdThreads * V];
     const int tid = threadIdx.y * blockDim.x + threadIdx.x;
     const int K = a.K, C = a.C, before = kAll ? 0 : KW - K;
-    const int group = blockIdx.x * blockDim.x + threadIdx.x;
-    const bool live = group < groups;
-    const int c = live ? group * V : 0;
+    const unsigned group = blockIdx.x * blockDim.x + threadIdx.x;     // (the last block's may pass 2^31)
+    const bool live = group < (unsigned)groups;
+    const int c = live ? (int)group * V : 0;
     after_all_before();
     E w[KW][NV], bias[NV], dw[KW][NV], db[NV];
     load_taps<V, KW, kAll>(w, a.w, c, K);
@@ -505,8 +505,8 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks<V, KW>)
         for (int i = tid; i < bx * V; i += kBwdThreads) {
             float total = 0.f;
             for (int y = 0; y < (int)blockDim.y; ++y) total += sums[y * bx * V + i];
-            const int channel = blockIdx.x * bx * V + i;
-            if (channel < C) to[(size_t)(q - before) * C + channel] = total;
+            const unsigned channel = blockIdx.x * bx * V + i;
+            if (channel < (unsigned)C) to[(size_t)(q - before) * C + channel] = total;
         }
         __syncthreads();
     }
@@ -517,16 +517,17 @@ __global__ void __launch_bounds__(256) conv_join_kernel(const float* parts, int 
                                                          float* db) {
     __shared__ float sums[8][32];
     after_all_before();
-    const int c = blockIdx.x * 32 + threadIdx.x, q = blockIdx.y;
+    const unsigned c = blockIdx.x * 32 + threadIdx.x, q = blockIdx.y;
+    const bool live = c < (unsigned)C;
     float total = 0.f;
-    if (c < C)
+    if (live)
         for (int r = threadIdx.y; r < rows; r += 8) total += parts[((size_t)r * (K + 1) + q) * C + c];
     sums[threadIdx.y][threadIdx.x] = total;
     __syncthreads();
-    if (threadIdx.y != 0 || c >= C) return;
+    if (threadIdx.y != 0 || !live) return;
 #pragma unroll
     for (int y = 1; y < 8; ++y) total += sums[y][threadIdx.x];
-    if (q < K) { if (dw) dw[(size_t)c * K + q] = total; }
+    if (q < (unsigned)K) { if (dw) dw[(size_t)c * K + q] = total; }
     else if (db) db[c] = total;
 }
 
@@ -566,7 +567,7 @@ cudaError_t bwd(const ConvArgs& a, cudaStream_t s) {
     const cudaError_t e = launch_overlapped(a.doc ? conv_bwd_kernel<T, V, KW, kAll, true> : conv_bwd_kernel<T, V, KW, kAll, false>,
                                             grid, block, s, a, groups, p.strips, p.strip);
     if (e != cudaSuccess || !a.partial) return e;
-    return launch_overlapped(conv_join_kernel, dim3((a.C + 31) / 32, a.K + 1), dim3(32, 8), s, (const float*)a.partial, p.rows,
+    return launch_overlapped(conv_join_kernel, dim3(((unsigned)a.C + 31) / 32, a.K + 1), dim3(32, 8), s, (const float*)a.partial, p.rows,
                              a.C, a.K, a.dw, a.db);
 }
 

@@ -1,6 +1,6 @@
 // How the launches of the short convolution (causal_conv.cu) cut up sequences and channels.  Plain C++, so that
-// the counts are checked without a GPU up to the largest sizes that a call may have: tokens within 8192 of 2^31,
-// where the sum of two sizes passes 31 bits.
+// the counts are checked without a GPU up to the largest sizes that a call may have: tokens within 8192 of 2^31, channels
+// and sequences up to 2^31 - 1 between them, whose sums pass 31 bits.
 #pragma once
 
 #ifdef __CUDACC__
@@ -38,8 +38,8 @@ inline ConvFwdPlan conv_fwd_plan(int N, int T, int groups, bool one_strip) {
 // Rows of the gradient's grid at most, one wave by the widest channel groups that a call may take; the workspace
 // holds a part for each.
 inline int conv_most_rows(int C) {
-    const int across = ((C + 3) / 4 + 31) / 32;
-    const int rows = kConvSms * 4 / across;
+    const long long across = (((long long)C + 3) / 4 + 31) / 32;
+    const int rows = (int)(kConvSms * 4 / across);
     return rows < 1 ? 1 : rows;
 }
 
@@ -55,7 +55,7 @@ inline ConvBwdPlan conv_bwd_plan(int N, int T, int C, int groups, int blocks_per
     p.bx = 1;
     while (p.bx < groups && p.bx < 32) p.bx *= 2;
     p.by = kConvThreads / p.bx;
-    p.across = (groups + p.bx - 1) / p.bx;
+    p.across = (int)(((long long)groups + p.bx - 1) / p.bx);
     p.rows = kConvSms * blocks_per_sm / p.across;
     if (p.rows > conv_most_rows(C)) p.rows = conv_most_rows(C);
     if (p.rows < 1) p.rows = 1;

@@ -51,11 +51,11 @@ def sizes():
     spread = lambda most: int(round(2 ** rng.uniform(0, 31))) % most + 1  # noqa: E731
     edges = [1, 2, 2 ** 30 - 1, 2 ** 30, 2 ** 30 + 1, 1_431_655_765, 1_500_000_000, MOST_T - 300_000, MOST_T - 20_000, MOST_T]
     out = [(1, t, c) for t in edges for c in (1, 7, 8, 768)]
-    out += [(n, 5, c) for n, c in ((MOST, 1), (2 ** 15, 2 ** 15), (3, MOST // 3))]
+    out += [(n, 5, c) for n, c in ((1, MOST), (1, MOST - 1), (1, MOST - 31), (1, MOST - 7), (MOST, 1), (2 ** 15, 2 ** 15), (3, MOST // 3))]
     out += [(77824, t, 1) for t in edges] + [(4, t, 40000) for t in edges]
     while len(out) < 3000:
         n, t, c = spread(MOST), spread(MOST_T), spread(MOST)
-        if n * c <= MOST and c < MOST - 63:
+        if n * c <= MOST:
             out.append((n, t, c))
     return out
 
