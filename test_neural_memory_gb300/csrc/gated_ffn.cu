@@ -577,6 +577,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
         const uint32_t base_u = __shfl_sync(0xffffffffu, smem_u32(base), 0);
         const uint64_t a0 = WMN ? sdesc(base_u, 8192, 1024, 2) : sdesc(base_u, 16, 1024, 2);
         const uint64_t b0 = sdesc(base_u + kOperand, 16, 1024, 2);
+        // (x comes after this too: the limit of a wait counts from the end of the kernel before, however long that runs)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         int s = 0;
         uint32_t phase = 0;
         bool ok = true;
