@@ -114,6 +114,9 @@ bool doc_ok(const ttm::ConvArgs& a, const int* doc, long long doc_seq, Span& sd)
     return true;
 }
 
+// The distance to a next row says nothing where there is one row, but a tensor map takes it all the same.
+long long row_step(int N, int D, long long step) { return N > 1 ? step : D; }
+
 // Widths whose products count in 32 bits.
 constexpr int kMostWidth = 1 << 24;
 
@@ -129,7 +132,7 @@ int ffn_common(ttm::FfnArgs& a, int N, int D, int F, int act, const void* x, lon
     if (D >= kMostWidth || F >= kMostWidth / 2 || N > kMostTokens) return TTM_ERR_UNSUPPORTED;
     a.N = N; a.D = D; a.F = F;
     a.gelu = act == TTM_ACT_GELU;
-    a.x = x; a.x_row = x_row;
+    a.x = x; a.x_row = row_step(N, D, x_row);
     a.W_in = W_in; a.W_out = W_out;
     return TTM_OK;
 }
@@ -510,7 +513,7 @@ int ttm_gated_ffn_bwd(int N, int D, int F, int act, const void* dy, long long dy
         if (dW_out && cudaMemsetAsync(dW_out, 0, df * 2, s) != cudaSuccess) return TTM_ERR_CUDA;
         return TTM_OK;
     }
-    a.dy = dy; a.dy_row = dy_row;
+    a.dy = dy; a.dy_row = row_step(N, D, dy_row);
     a.gu = const_cast<void*>(gu);
     a.dx = dx; a.dW_in = dW_in; a.dW_out = dW_out;
     return ffn_run(a, 1, workspace, workspace_bytes, stream);
