@@ -669,7 +669,9 @@ int ttm_gated_ffn_bwd(int N, int D, int F, int act, const void* dy, long long dy
  *     goes to one of its two neighbours in e4m3, up where its distance from the lower one (in steps) and a
  *     dither reach 1: with place i (in m) and all arithmetic modulo 2^32, h = hash(i + t 0x9e3779b9 +
  *     (i >> 32) 0x85ebca6b), hash: x ^= x >> 16, x *= 0x7feb352d, x ^= x >> 15, x *= 0x846ca68b,
- *     x ^= x >> 16; m takes h mod 2^16, sqrt(v) h >> 16, in units of 2^-16.  Values that are not finite become NaN.
+ *     x ^= x >> 16; m takes h mod 2^16, sqrt(v) h >> 16, in units of 2^-16.  Where the code
+ *     of m is not zero, that of sqrt(v) is 2^-9 at least (m over a root coded as zero would be a step of any size).  Values that
+ *     are not finite become NaN.
  *   step: int[2] on the device: the steps done so far, read and increased by the call (also when count is 0),
  *     and a counter that is 0 between calls.  A captured call so counts its own replays.
  *   lr_at, grad_scale: fp32 on the device, or NULL (lr; 1).

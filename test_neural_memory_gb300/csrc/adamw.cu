@@ -8,8 +8,11 @@
 // 448.  Rounding to nearest would stand still: a step changes v by (1 - b2) (g^2 - v), a thousandth of it, and
 // half a step of e4m3 is a sixteenth.  So a value goes up or down as its distance to the two neighbours and a
 // dither say, a fixed hash of the value's place and the step: the moments move by the right amount on average, and
-// equal calls give equal bits.  The moments' own arithmetic rounds after every operation (no fused
-// multiply-add): whether a value is past the dither then does not depend on how a compiler contracts it.
+// equal calls give equal bits.  One exception: beside an m that is not coded as zero a root is not either, but as the
+// smallest size.  Values of 2^-15 of their block's largest would else see m / (almost nothing) in the next step: with
+// gradients of sizes exp(3 normal) the largest of 250 steps of 16384 values was 1e5 times the rate, and is 3 times.
+// The moments' own arithmetic rounds after every operation (no fused multiply-add): whether a value is past the dither
+// then does not depend on how a compiler contracts it.
 //
 // Bound by HBM: 28 bytes a value with fp32 moments and gradients, 14 in 8 bits with bf16 gradients.  A warp
 // takes blocks of 256 values, 8 a lane in two runs of 4, so that every access of a warp is one piece of
@@ -262,6 +265,9 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
                 if (size_bits(m[j]) >= kInf) put(mc[j / 4], j & 3, 0x7f);        // e4m3 has no infinity
                 if (size_bits(v[j]) >= kInf) put(vc[j / 4], j & 3, 0x7f);
             }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)                 // roots of zero beside an m that is not: the smallest size
+                vc[q] |= __vcmpeq4(vc[q], 0) & __vcmpne4(mc[q] & 0x7f7f7f7fu, 0) & 0x01010101u;
         }
         if (lane == 0) {
             a.m_scale[e.first + block] = power(em);
