@@ -676,7 +676,7 @@ int ttm_gated_ffn_bwd(int N, int D, int F, int act, const void* dy, long long dy
  *     and a counter that is 0 between calls.  A captured call so counts its own replays.
  *   lr_at, grad_scale: fp32 on the device, or NULL (lr; 1).
  * Arithmetic is fp32; a bf16 param or copy is rounded to nearest.  Equal inputs give equal bits.
- * bits 8 or 32; 0 <= beta < 1, eps > 0, n <= 2^40 (else TTM_ERR_UNSUPPORTED).  No two written tensors, and no written and read one, may overlap
+ * bits 8 or 32; 0 <= beta < 1, eps > 0 (below 2^-126 it counts as 2^-126), n <= 2^40 (else TTM_ERR_UNSUPPORTED).  No two written tensors, and no written and read one, may overlap
  * (TTM_ERR_INVALID_ARG; one gradient may serve several tensors).  Calls that share m, v or step run one after the
  * other on one stream.  Asynchronous on `stream`; TTM_ERR_CUDA if a launch fails.
  */

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -571,7 +572,9 @@ int ttm_adamw_step(int count, const ttm_adamw_tensor* tensors, int bits, void* m
         a.b1 = (float)beta1; a.b2 = (float)beta2;
         a.c1 = (float)(1.0 - beta1); a.c2 = (float)(1.0 - beta2);
         a.log_b1 = (float)std::log(beta1); a.log_b2 = (float)std::log(beta2);
-        a.eps = (float)eps; a.decay = (float)weight_decay;
+        // (the kernel's reciprocal takes a denominator below the smallest normal number as zero; a root above zero is 2^-75 at
+        // least and takes no notice)
+        a.eps = std::max((float)eps, FLT_MIN); a.decay = (float)weight_decay;
         a.grad_scale = grad_scale;
         int launches = 0;
         if (ttm::adamw_step_launch(list.data(), (int)list.size(), a, static_cast<cudaStream_t>(stream), &launches) !=
