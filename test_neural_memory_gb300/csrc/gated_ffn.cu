@@ -28,11 +28,11 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <climits>
 #include <cstdint>
 
 #include "../../include/ttm.h"
+#include "known_clusters.h"
 #include "pairs.cuh"
 #include "tc_pair.cuh"
 #include "tc_ptx.cuh"
@@ -726,28 +726,25 @@ bool problem(Problem& q, int M, int N, int K, int mode) {
     return tiles < (1LL << 30);
 }
 
-// Clusters of `width` blocks that run at once (a cluster stays within a group of SMs), asked once for a kernel and width.
-int clusters_at_once(const void* kernel, std::atomic<int>* known, int width, int threads, int smem) {
-    const int k = known[width].load(std::memory_order_relaxed);
-    if (k > 0) return k;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = width;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3(width);
-    c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = smem;
-    c.attrs = at;
-    c.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess) {
-        cudaGetLastError();
-        n = 0;
-    }
-    if (n < 1) n = 1;
-    known[width].store(n, std::memory_order_relaxed);
-    return n;
+// Clusters of `width` blocks that run at once (a cluster stays within a group of SMs), asked once for a kernel, device and
+// width.
+cudaError_t clusters_at_once(const void* kernel, KnownClusters& known, int width, int threads, int smem, int& n) {
+    int device;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    return known.get(device, width, n, [&](int* out) {
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = width;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t c{};
+        c.gridDim = dim3(width);
+        c.blockDim = dim3(threads);
+        c.dynamicSmemBytes = smem;
+        c.attrs = at;
+        c.numAttrs = 1;
+        return cudaOccupancyMaxActiveClusters(out, kernel, &c);
+    });
 }
 
 // How a product's tiles are gone through: whole rounds by the pairs, the rest in one more round or with K shared by
@@ -759,25 +756,28 @@ struct Plan {
 // Counted in blocks of K of a pair: a round takes its blocks of K and the epilogue of the last tile (6), tiles that share K
 // the passing on of their sums too (4 more).
 template <bool AMN, bool BMN, int MODE>
-Plan plan_of(const GemmParams& p) {
+cudaError_t plan_of(const GemmParams& p, Plan& plan) {
     const int K = p.q[0].K > p.q[1].K ? p.q[0].K : p.q[1].K, kblocks = (K + kBK - 1) / kBK;
     const int whole = p.tiles / kPairs * kPairs, rest = p.tiles - whole;
-    Plan plan{p.tiles, 1};
-    if (rest == 0) return plan;
-    static std::atomic<int> known[9];
+    plan = {p.tiles, 1};
+    if (rest == 0) return cudaSuccess;
+    static KnownClusters known;
     const void* kernel = reinterpret_cast<const void*>(ffn_gemm_kernel<AMN, BMN, MODE, true>);
     int least = kblocks + (whole ? 0 : 6);
     for (int n = 2; n <= 4; ++n) {
         const int each = (kblocks + n - 1) / n;
         if (each < 4 || (kblocks + each - 1) / each != n) continue;
-        const int at_once = clusters_at_once(kernel, known, 2 * n, kThreads, kSmem);
+        int at_once;
+        const cudaError_t e = clusters_at_once(kernel, known, 2 * n, kThreads, kSmem, at_once);
+        if (e != cudaSuccess) return e;
+        if (at_once < 1) continue;
         const int cost = (rest + at_once - 1) / at_once * (each + 10);
         if (cost < least) {
             least = cost;
             plan = {whole, n};
         }
     }
-    return plan;
+    return cudaSuccess;
 }
 
 template <bool AMN, bool BMN, int MODE, bool SPLIT>
@@ -796,7 +796,9 @@ cudaError_t gemm(const Maps& m0, const Maps& m1, GemmParams p, cudaStream_t s, i
         e = cudaFuncSetAttribute(ffn_gemm_kernel<AMN, BMN, MODE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const int all = p.tiles = p.q[0].tiles + p.q[1].tiles;
-    const Plan plan = plan_of<AMN, BMN, MODE>(p);
+    Plan plan;
+    e = plan_of<AMN, BMN, MODE>(p, plan);
+    if (e != cudaSuccess) return e;
     if (plan.whole) {
         p.tiles = plan.whole;
         e = launch<AMN, BMN, MODE, false>(m0, m1, p, 2 * (plan.whole < kPairs ? plan.whole : kPairs), s);
@@ -826,15 +828,18 @@ cudaError_t narrow(const CUtensorMap& mw, const Matrix& x, NarrowParams p, bool 
     const int rows = (p.N + parts - 1) / parts;
     p.bn = (rows + 15) / 16 * 16;
     auto kernel = ffn_narrow_kernel<WMN, MODE>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
     if (e != cudaSuccess) return e;
-    static std::atomic<int> known[9];
+    static KnownClusters known;
     int splits = 1;
     long long least = LLONG_MAX;
     for (int n = 1; n <= 8; ++n) {
         const int each = (kblocks + n - 1) / n;
         if (n > 1 && (each < 2 || (kblocks + each - 1) / each != n)) continue;
-        const int places = clusters_at_once(reinterpret_cast<const void*>(kernel), known, n, kNarrowThreads, kNarrowSmem);
+        int places;
+        e = clusters_at_once(reinterpret_cast<const void*>(kernel), known, n, kNarrowThreads, kNarrowSmem, places);
+        if (e != cudaSuccess) return e;
+        if (places < 1) continue;
         const long long all = (long long)tiles * parts, rounds = (all + 2 * places - 1) / (2 * places);
         const long long cost = rounds * (each + (n > 1 ? 8 : 6)) + (all > places ? 4 : 0);
         if (cost <= least) {
