@@ -261,13 +261,11 @@ __device__ __forceinline__ void step_block(const AdamwEntry& e, const AdamwScala
                 const float ym = fabsf(m[j]) * im, yr = v[j] * ir;
                 if (__float_as_uint(ym) < kSmallest)
                     put(mc[j / 4], j & 3, to_small_code(ym, h << 4 & 0xffff0u) | (__float_as_uint(m[j]) >> 24 & 0x80u));
-                if (__float_as_uint(yr) < kSmallest) put(vc[j / 4], j & 3, to_small_code(yr, h >> 12 & 0xffff0u));
+                if (__float_as_uint(yr) < kSmallest)    // (beside an m that is not zero: the smallest size at least)
+                    put(vc[j / 4], j & 3, max(to_small_code(yr, h >> 12 & 0xffff0u), (uint32_t)((mc[j / 4] >> 8 * (j & 3) & 0x7fu) != 0)));
                 if (size_bits(m[j]) >= kInf) put(mc[j / 4], j & 3, 0x7f);        // e4m3 has no infinity
                 if (size_bits(v[j]) >= kInf) put(vc[j / 4], j & 3, 0x7f);
             }
-#pragma unroll
-            for (int q = 0; q < 2; ++q)                 // roots of zero beside an m that is not: the smallest size
-                vc[q] |= __vcmpeq4(vc[q], 0) & __vcmpne4(mc[q] & 0x7f7f7f7fu, 0) & 0x01010101u;
         }
         if (lane == 0) {
             a.m_scale[e.first + block] = power(em);
