@@ -178,12 +178,6 @@ __device__ __forceinline__ Share share_of(const GemmParams& p, int which, int pa
     return {min(kblocks, pair * each), min(kblocks, (pair + 1) * each)};
 }
 
-__device__ __forceinline__ float peer_load1(uint32_t addr) {
-    float f;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(addr));
-    return f;
-}
-
 // SPLIT: a cluster of 2 to 4 pairs has one tile, each pair a share of its K.  The pairs leave their sums where the
 // operands lay, and each takes its share of the pieces through the epilogue, summed over the pairs in their
 // order.
@@ -458,10 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int q = 0; q < p.splits; ++q) {
                     const uint32_t from = peer_addr(sums + 32 * c * kBM + part * 32 + lane, 2 * q + rank);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += peer_load1(from + i * kBM * 4);
+                    for (int i = 0; i < 32; ++i) v[i] += peer_load(from + i * kBM * 4);
                     if constexpr (MODE == kGated) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) up[i] += peer_load1(from + (kTile / 2 + i) * kBM * 4);
+                        for (int i = 0; i < 32; ++i) up[i] += peer_load(from + (kTile / 2 + i) * kBM * 4);
                     }
                 }
                 piece(at, c, c + step, pieces, v, up);
