@@ -607,9 +607,10 @@ cudaError_t bwd_any(const ConvArgs& a, cudaStream_t s) {
 }
 #undef CONV_BY_TAPS
 
-cudaError_t pass_state(const ConvArgs& a, const void* from, void* to, cudaStream_t s) {
+cudaError_t pass_state(const ConvArgs& a, const void* from, void* to, cudaStream_t s, int* launches) {
     const long long n = (long long)a.N * (a.K - 1) * a.C;
-    if (!to || n == 0) return cudaSuccess;
+    *launches = to && n > 0;
+    if (!*launches) return cudaSuccess;
     const unsigned blocks = (unsigned)((n + 255) / 256);
     if (a.bf16)
         conv_pass_kernel<<<blocks, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(from), static_cast<__nv_bfloat16*>(to), n);
@@ -624,9 +625,9 @@ size_t conv_bwd_workspace_bytes(const ConvArgs& a) {
     return (size_t)conv_most_rows(a.C) * (a.K + 1) * a.C * 4;
 }
 
-cudaError_t conv_fwd_launch(const ConvArgs& a, cudaStream_t s) {
-    if (a.T == 0) return pass_state(a, a.state0, a.state, s);
-    return fwd_any(a, false, s);
+cudaError_t conv_fwd_launch(const ConvArgs& a, cudaStream_t s, int* launches) {
+    *launches = 1;
+    return a.T > 0 ? fwd_any(a, false, s) : pass_state(a, a.state0, a.state, s, launches);
 }
 
 cudaError_t conv_step_launch(const ConvArgs& a, cudaStream_t s) { return fwd_any(a, true, s); }
@@ -635,7 +636,7 @@ cudaError_t conv_bwd_launch(const ConvArgs& a, cudaStream_t s, int* launches) {
     *launches = a.partial ? 2 : 1;
     if (a.T > 0) return bwd_any(a, s);
     // no tokens: the state passed on, the sums are empty
-    cudaError_t e = pass_state(a, a.dstate, a.dstate0, s);
+    cudaError_t e = pass_state(a, a.dstate, a.dstate0, s, launches);
     if (e == cudaSuccess && a.dw) e = cudaMemsetAsync(a.dw, 0, (size_t)a.C * a.K * 4, s);
     if (e == cudaSuccess && a.db) e = cudaMemsetAsync(a.db, 0, (size_t)a.C * 4, s);
     return e;

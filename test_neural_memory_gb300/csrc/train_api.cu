@@ -400,8 +400,9 @@ int ttm_causal_conv_fwd(int N, int T, int C, int K, int dtype, int silu, const v
     const Span outs[] = {{y, nc * T * es}, {state, st}};
     if (!outputs_clear(ins, outs)) return TTM_ERR_INVALID_ARG;
     a.state0 = state0; a.doc = T > 0 ? doc : nullptr; a.doc_seq = doc_seq; a.y = y; a.state = state;
-    if (ttm::conv_fwd_launch(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return TTM_ERR_CUDA;
-    ttm::api_note_launches(1);
+    int launches = 0;
+    if (ttm::conv_fwd_launch(a, static_cast<cudaStream_t>(stream), &launches) != cudaSuccess) return TTM_ERR_CUDA;
+    ttm::api_note_launches(launches);
     return TTM_OK;
 }
 

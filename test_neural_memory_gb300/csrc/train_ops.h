@@ -107,7 +107,7 @@ struct ConvArgs {
 };
 
 size_t conv_bwd_workspace_bytes(const ConvArgs& a);
-cudaError_t conv_fwd_launch(const ConvArgs& a, cudaStream_t s);
+cudaError_t conv_fwd_launch(const ConvArgs& a, cudaStream_t s, int* launches);
 cudaError_t conv_step_launch(const ConvArgs& a, cudaStream_t s);
 cudaError_t conv_bwd_launch(const ConvArgs& a, cudaStream_t s, int* launches);
 
