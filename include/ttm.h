@@ -612,7 +612,9 @@ int ttm_causal_conv_bwd(int N, int T, int C, int K, int dtype, int silu,
                         void* workspace, size_t workspace_bytes, void* stream);
 
 /* Decode step of the convolution: continues every sequence by n >= 1 tokens from `state` ([N][K-1][C] in
- * dtype, updated in place).  Otherwise as ttm_causal_conv_fwd, without documents. */
+ * dtype, updated in place).  Otherwise as ttm_causal_conv_fwd, without documents.  For few tokens: a thread walks all
+ * tokens of its channels, as the state in place asks for; a continuation by hundreds of them is faster by
+ * ttm_causal_conv_fwd from the state into another one. */
 int ttm_causal_conv_step(int N, int n, int C, int K, int dtype, int silu,
                          const void* x, long long x_seq, long long x_tok,
                          const float* w, const float* b, void* state, void* y, void* stream);
@@ -644,8 +646,9 @@ int ttm_gated_ffn_fwd(int N, int D, int F, int act, const void* x, long long x_r
  * adjoint is dy itself):
  *     dh = dy W_out^T,  dg = dh u act'(g),  du = dh act(g),
  *     dx = [dg | du] W_in^T,  dW_in = x^T [dg | du],  dW_out = h^T dy
- *   gu: what the forward call wrote (h is taken from it again).  dx: [N][D], dW_in: [D][2F], dW_out: [F][D],
- *   each or NULL; all bf16, written (the weights' are zero for N = 0).
+ *   gu: what the forward call wrote.  h is taken from it again: from g and u in bf16, half a step of it off their fp32 sums,
+ *     which the forward call's h came from.
+ *   dx: [N][D], dW_in: [D][2F], dW_out: [F][D], each or NULL; all bf16, written (the weights' are zero for N = 0).
  *   workspace: ttm_gated_ffn_workspace_size(N, D, F, 1) bytes ([dg | du] and h, rounded to bf16).
  * Otherwise as ttm_gated_ffn_fwd; dy_row a multiple of 8. */
 int ttm_gated_ffn_bwd(int N, int D, int F, int act, const void* dy, long long dy_row,
@@ -675,9 +678,10 @@ int ttm_gated_ffn_bwd(int N, int D, int F, int act, const void* dy, long long dy
  *   step: int[2] on the device: the steps done so far, read and increased by the call (also when count is 0),
  *     and a counter that is 0 between calls.  A captured call so counts its own replays.
  *   lr_at, grad_scale: fp32 on the device, or NULL (lr; 1).
- * Arithmetic is fp32; a bf16 param or copy is rounded to nearest.  Equal inputs give equal bits.
- * bits 8 or 32; 0 <= beta < 1, eps > 0 (below 2^-126 it counts as 2^-126), n <= 2^40 (else TTM_ERR_UNSUPPORTED).  No two written tensors, and no written and read one, may overlap
- * (TTM_ERR_INVALID_ARG; one gradient may serve several tensors).  Calls that share m, v or step run one after the
+ * Arithmetic is fp32; a bf16 param or copy is rounded to nearest, so a bf16 param stays where it is under steps below 2^-9 of
+ * it (a rate of 3e-4 does not move weights near one): fp32 params with bf16 copies keep such steps.  Equal inputs give equal bits.
+ * bits 8 or 32; 0 <= beta < 1, eps > 0 (below 2^-126 it counts as 2^-126), n <= 2^40 (else TTM_ERR_UNSUPPORTED).  No two
+ * written tensors, and no written and read one, may overlap (TTM_ERR_INVALID_ARG; one gradient may serve several tensors).  Calls that share m, v or step run one after the
  * other on one stream.  Asynchronous on `stream`; TTM_ERR_CUDA if a launch fails.
  */
 typedef struct {

@@ -19,7 +19,7 @@
 // memory; tensors that do not start on 16 bytes, and their last blocks, go value by value.  The table of
 // tensors travels as a kernel argument (a copy to the device would be a call of its own, and not the
 // captured graph's), and a block finds its first tensor by bisection.  Measured: 92 M values of 12 layers, bf16 gradients and
-// copies, 396 us, 98 % of a copy's rate; 8 bits 55 M values cold 212 us, 3.9 TB/s, bound by 96 instructions a value (hash,
+// copies, 396 us, 98 % of a copy's rate; 8 bits 55 M values cold 211 us, 3.9 TB/s, bound by 96 instructions a value (hash,
 // two roundings, scales), and 91 us for reading the moments out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

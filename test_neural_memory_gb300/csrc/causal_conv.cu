@@ -8,9 +8,9 @@
 // Bound by HBM: two tensors forward, three in the gradient, K products and one exponential a value.  So
 // every value is read once (but for the K - 1 rows between strips) and the window stays in registers: a
 // thread takes V neighbouring channels, as wide as the rows' alignment allows, and walks a strip of
-// tokens, the loads of kBatch rows ahead of their use.  Measured (K = 4, bf16, SiLU): forward 131072 x 6144 537 us, 6.0 TB/s,
-// 90 % of a copy; gradient 8 x 8192 x 2304 174 us, 5.2 TB/s, its 26 instructions a value and three blocks of registers
-// an SM as much the bound as the memory; a step of 64 x 6144 4.6 us, of which the GPU's part is a launch.
+// tokens, the loads of kBatch rows ahead of their use.  Measured (K = 4, bf16, SiLU): forward 131072 x 6144 540 us, 6.0 TB/s,
+// 89 % of a copy; gradient 8 x 8192 x 2304 174 us, 5.2 TB/s, its 26 instructions a value and three blocks of registers
+// an SM as much the bound as the memory; a step of 64 x 6144 4.6 to 5.0 us, of which the GPU's part is a launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -17,13 +17,13 @@
 // bytes, swizzled: free of conflicts), from where rows of 64 bytes leave.  (By tensor copies every result waits for a
 // fence and for the copy before it: 4700 cycles for kGatedBack's three, of which 1700 are arithmetic.)  What it reads goes
 // to registers a piece ahead.
-// Measured, 2048 x 5504: forward of 32768 rows 1380 us, 1.61 PFLOP/s, gradient of 16384 rows 1436 us, 1.54 PFLOP/s, both
-// under the power limit (1.44 to 1.6 GHz); the tensor pipe is busy 87 to 95 % of a kernel, 62 % of kGatedBack's, whose
+// Measured, 2048 x 5504: forward of 32768 rows 1330 to 1413 us, 1.57 to 1.67 PFLOP/s, gradient of 16384 rows 1393 to 1464
+// us, 1.51 to 1.59 PFLOP/s, by the card, both under the power limit (1.44 to 1.6 GHz); the tensor pipe is busy 87 to 95 % of a kernel, 62 % of kGatedBack's, whose
 // epilogue (two results and h out, g and u in) is as long as the products.
 //
 // Roundings: g and u enter the activation in fp32; h, dg and du are rounded to bf16 once, as operands of the next
 // product (half a step, 2^-8 of a value at most: the same as rounding the result, and what the tensor cores
-// take); sums are fp32 throughout.
+// take); sums are fp32 throughout.  The gradient's h comes from the saved bf16 g and u, another half step each.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

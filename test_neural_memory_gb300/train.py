@@ -137,7 +137,8 @@ def causal_conv_bwd(dy, x, w, b=None, *, state0=None, doc=None, silu=True, dstat
 
 def causal_conv_step(x, w, state, b=None, *, silu=True, y=None, stream=None):
     """Decode step of the convolution: continues every sequence by the n tokens of x ([..., n, C]) from
-    `state` ([..., K-1, C] in the dtype of x, updated in place).  Returns y like x."""
+    `state` ([..., K-1, C] in the dtype of x, updated in place).  For few tokens (they are walked one after the
+    other): a long continuation is causal_conv_fwd's with state0.  Returns y like x."""
     return _call("causal_conv_step", stream, x, w, state, b, bool(silu), y)
 
 
@@ -183,7 +184,8 @@ def adamw_state(params, *, bits=32):
 def adamw_step(params, grads, state, *, lr, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, grad_scale=None,
                copies=None, stream=None):
     """AdamW step over many tensors in one pass, params (fp32 or bf16, contiguous) and `state` (from
-    adamw_state for the same tensors in the same order) updated in place.  grads: fp32 or bf16, None leaves its
+    adamw_state for the same tensors in the same order) updated in place.  bf16 params are rounded to nearest and stand still
+    under steps below 2^-9 of them; fp32 params with copies do not.  grads: fp32 or bf16, None leaves its
     parameter and moments as they are.  copies: None, or bf16 tensors (or None) written with the new
     values.  lr: a number, or a 0-dim fp32 tensor on the device; grad_scale: a 0-dim fp32 tensor that
     multiplies the gradients, or None.  The steps are counted on the device, so that a captured
