@@ -10,7 +10,7 @@
 // dither say, a fixed hash of the value's place and the step: the moments move by the right amount on average, and
 // equal calls give equal bits.  One exception: beside an m that is not coded as zero a root is not either, but as the
 // smallest size.  Values of 2^-15 of their block's largest would else see m / (almost nothing) in the next step: with
-// gradients of sizes exp(3 normal) the largest of 250 steps of 16384 values was 1e5 times the rate, and is 3 times.
+// gradients of sizes exp(3 normal) the largest of 250 steps of 16384 values was 1e4 to 1e5 times the rate, and is 2.4 times.
 // The moments' own arithmetic rounds after every operation (no fused multiply-add): whether a value is past the dither
 // then does not depend on how a compiler contracts it.
 //
